@@ -326,10 +326,10 @@ def _own(s, c):
             out["d_rows"], out["d_gates"] = moe.unpermute_backward(s["dy"], s["y_rows"], s["slot_pos"], s["gates"], out=s["rows"])
         return out
     if c["kind"] == "norm":
-        h, u = moe.block_norm(s["x"], s["y"], w_post=s["w_post"], w_pre=s["w_pre"], gate=s["gate"], res_scale=RES_SCALE, eps=EPS)
+        h, u = moe.block_norm(s["x"], s["y"], w_post=s["w_post"], w_pre=s["w_pre"], gate=s["gate"], gate_per=c["gate"], res_scale=RES_SCALE, eps=EPS)
         return dict(h=h, u=u)
     if c["kind"] == "norm_backward":
-        got = moe.block_norm_backward(s["dh"], s["du"], s["x"], s["y"], w_post=s["w_post"], w_pre=s["w_pre"], gate=s["gate"], res_scale=RES_SCALE, eps=EPS)
+        got = moe.block_norm_backward(s["dh"], s["du"], s["x"], s["y"], w_post=s["w_post"], w_pre=s["w_pre"], gate=s["gate"], gate_per=c["gate"], res_scale=RES_SCALE, eps=EPS)
         return {k: v for k, v in got.items() if v is not None}
     codes, scales = moe.mxfp4_quantize(s["x"])
     if c["kind"] == "quantise":
