@@ -341,6 +341,188 @@ MOE_API moe_status moe_mx_gemm_noalloc(const uint8_t *a_codes, const uint8_t *a_
                                        const uint8_t *b_codes, const uint8_t *b_scales, int32_t N, int32_t K,
                                        float *out, int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators round the layer.  They stand alone (no plan), run on the current
+ * device, are asynchronous on `stream`, allocate nothing, and can be captured
+ * in a CUDA graph.  Matrices are row-major with their row stride given in
+ * elements (moe_permute: in bytes); a row's elements are contiguous.  Element
+ * types are moe_dtype values; every sum, norm and gradient is accumulated in
+ * fp32 and rounded once (to nearest even) when it is stored.  Sums run in a
+ * fixed order, so that results do not change from call to call.  Rows whose
+ * address and stride are multiples of 16 bytes and whose length is a multiple
+ * of 8 elements go by in 16-byte words, others element by element.  Outputs
+ * must not overlap inputs except where a call says so. */
+typedef enum {
+    MOE_DTYPE_F32 = 0,
+    MOE_DTYPE_BF16 = 1,
+    MOE_DTYPE_F16 = 2
+} moe_dtype;
+
+/* Sort the (token, slot) pairs by expert: the layer's dispatch order, as an
+ * operator of its own.  idx int32 [T][k] holds the expert of each slot; a slot
+ * whose entry is outside [0, E) (a padded token, a dropped slot) is routed
+ * nowhere.  A token may name the same expert twice.  Writes
+ *   offsets     int32 [E + 1]   kept slots of the experts below e
+ *   sorted_slot int32 [T * k]   flat slot t k + j at each sorted place, equal
+ *                               experts in slot order; -1 behind offsets[E]
+ *   slot_pos    int32 [T][k]    place of each slot, -1 for a dropped one
+ * T >= 0, 1 <= k <= 32, T k < 2^31, 1 <= E <= 1024. */
+MOE_API moe_status moe_sort(const int32_t *idx, int32_t T, int32_t k, int32_t E, int32_t *offsets,
+                            int32_t *sorted_slot, int32_t *slot_pos, void *stream);
+
+/* rows[slot_pos[t][j]] = x[t] for every slot: rows of row_bytes bytes of any
+ * type (activations, MXFP4 or MXFP8 codes, scales).  Strides in bytes, at
+ * least row_bytes.  Places that no slot names are left as they were; a place
+ * outside [0, n_rows) counts as dropped. */
+MOE_API moe_status moe_permute(const void *x, int64_t x_stride, int64_t row_bytes, int32_t T, int32_t k,
+                               const int32_t *slot_pos, int64_t n_rows, void *rows, int64_t rows_stride,
+                               void *stream);
+
+/* y[t] = sum_j w[t][j] rows[slot_pos[t][j]], an fp32 FMA chain in slot order:
+ * the layer's combine.  w fp32 [T][k]; with w = NULL every weight is one,
+ * which is the gradient of moe_permute.  Dropped slots (a place outside
+ * [0, n_rows)) add nothing and their rows are not read; a token without kept
+ * slots gets zeros.  D >= 1. */
+MOE_API moe_status moe_unpermute(const void *rows, int64_t ld_rows, int32_t dtype, int64_t n_rows,
+                                 const int32_t *slot_pos, const float *w, int32_t T, int32_t k, int32_t D, void *y,
+                                 int64_t ld_y, int32_t y_dtype, void *stream);
+
+/* Gradients of moe_unpermute from dy [T][D]:
+ *   d_rows[slot_pos[t][j]] = w[t][j] dy[t]   (type of rows; places that no
+ *                                             slot names are left as they were)
+ *   d_w[t][j] = <dy[t], rows[slot_pos[t][j]]>   fp32, 0 for a dropped slot
+ * Either output may be NULL (rows is read only for d_w). */
+MOE_API moe_status moe_unpermute_backward(const void *dy, int64_t ld_dy, int32_t dy_dtype, const void *rows,
+                                          int64_t ld_rows, int32_t dtype, int64_t n_rows, const int32_t *slot_pos,
+                                          const float *w, int32_t T, int32_t k, int32_t D, void *d_rows,
+                                          int64_t ld_d_rows, float *d_w, void *stream);
+
+/* The norms behind and before a block, with its gate and the residual scale,
+ * in one pass:
+ *   h = res_scale x + g w_post y / rms(y)      rms(v) = sqrt(mean(v^2) + eps)
+ *   u = w_pre h / rms(h)                        of h as it is stored
+ * x is the residual stream, y the block's output, u the next block's input.
+ * y = NULL: no block behind it yet, h = x and is not written (res_scale and
+ * the gate are not used).  u = NULL: only h.  w_post / w_pre = NULL: ones.
+ * The gate is a value a channel ([D]), a value a token ([T]), or absent.
+ * Weights and gate share one type.  h has x's type and may be x itself (same
+ * address and stride).  T >= 0, 1 <= D <= 16384, eps >= 0. */
+typedef enum {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_CHANNEL = 1,
+    MOE_GATE_TOKEN = 2
+} moe_gate_kind;
+
+typedef struct {
+    const void *x;
+    int64_t ld_x;
+    const void *y;
+    int64_t ld_y;
+    const void *w_post;   /* [D] */
+    const void *w_pre;    /* [D] */
+    const void *gate;     /* [D] or [T] */
+    void *h;
+    int64_t ld_h;
+    void *u;
+    int64_t ld_u;
+    int32_t T, D;
+    int32_t x_dtype;      /* moe_dtype of x and h */
+    int32_t y_dtype;
+    int32_t u_dtype;
+    int32_t w_dtype;      /* of w_post, w_pre and gate */
+    int32_t gate_kind;    /* moe_gate_kind */
+    float res_scale, eps;
+} moe_block_norm_args;
+MOE_API moe_status moe_block_norm(const moe_block_norm_args *args, void *stream);
+
+/* Its gradients, from dh (gradient of h, NULL: zero) and du (gradient of u,
+ * NULL: there was no u), with h and y as the forward pass stored them:
+ *   total = dh + (a - h^ mean(a h^)) / rms(h)   a = du w_pre, h^ = h / rms(h)
+ *   dx = res_scale total (total itself without y)
+ *   dy = (p - y^ mean(p y^)) / rms(y)           p = total g w_post, y^ = y / rms(y)
+ *   dw_pre = sum_t du h^, dw_post = sum_t total g y^,
+ *   d_gate = sum total w_post y^ over the tokens (channel gate) or the row
+ * Any output may be NULL.  Weight and gate gradients are fp32.  `workspace`
+ * (16-byte aligned, moe_block_norm_workspace_bytes(T, D) bytes) is needed for
+ * dw_pre, dw_post and a channel gate's d_gate; calls that overlap need one
+ * each.  y = NULL: no norm behind a block (dy, dw_post and d_gate are NULL).
+ * dx may be dh itself, dy may be y itself, and dx may be du itself if they
+ * have one type (same address and stride). */
+typedef struct {
+    const void *dh;
+    int64_t ld_dh;
+    const void *du;
+    int64_t ld_du;
+    const void *h;        /* may be NULL if du is */
+    int64_t ld_h;
+    const void *y;
+    int64_t ld_y;
+    const void *w_post, *w_pre, *gate;
+    void *dx;             /* x_dtype */
+    int64_t ld_dx;
+    void *dy;             /* y_dtype */
+    int64_t ld_dy;
+    float *dw_post, *dw_pre, *d_gate;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t T, D;
+    int32_t x_dtype;      /* of h, dh and dx */
+    int32_t y_dtype;
+    int32_t u_dtype;      /* of du */
+    int32_t w_dtype;
+    int32_t gate_kind;
+    float res_scale, eps;
+} moe_block_norm_backward_args;
+MOE_API size_t moe_block_norm_workspace_bytes(int32_t T, int32_t D);
+MOE_API moe_status moe_block_norm_backward(const moe_block_norm_backward_args *args, void *stream);
+
+/* MXFP4 of activations: x [rows][K] of any moe_dtype into codes [rows][K/2]
+ * (4-byte aligned) and scales [rows][K/32], by moe_mxfp4_encode's rule.  A
+ * block that holds an infinity or a NaN gets scale code 255 (not a number)
+ * and codes 0.  K a multiple of 32, rows >= 0. */
+MOE_API moe_status moe_mxfp4_quantize(const void *x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t K,
+                                      uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values that MXFP4 codes and scales stand for, rounded to the nearest of
+ * `dtype` (scale code 255: NaN).  codes 4-byte aligned, K a multiple of 32. */
+MOE_API moe_status moe_mxfp4_decode(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, void *x,
+                                    int64_t ld_x, int32_t dtype, void *stream);
+
+/* Product of four-bit operands, for one matrix or one for each group of rows
+ * (the experts' products on rows sorted by expert):
+ *   out[n][m] = sum_k dq(B[n][k]) dq(A[g][m][k])   for offsets[g] <= n < offsets[g + 1]
+ * A MXFP4 [G][M][K] and B MXFP4 [N][K], codes 16-byte and scales 4-byte
+ * aligned, row-major as moe_mxfp4_encode and moe_mxfp4_quantize write them;
+ * out [N][M] of out_dtype with row stride ld_out.  offsets: device int32
+ * [G + 1], ascending, as moe_sort writes them (values are kept inside [0, N]);
+ * NULL with G = 1: all rows.  Rows outside [offsets[0], offsets[G]) are left
+ * as they were.  M >= 1, N >= 0, K a multiple of 128, 1 <= G <= 1024,
+ * G M < 2^31.  dev_status (device int32, optional) receives a non-zero code if
+ * a bounded wait inside the kernel ran out, as with moe_mx_gemm.  A device of
+ * compute capability 10.3 is needed. */
+MOE_API moe_status moe_mx4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, int32_t G, int32_t M,
+                                const uint8_t *b_codes, const uint8_t *b_scales, int32_t N, int32_t K,
+                                const int32_t *offsets, void *out, int64_t ld_out, int32_t out_dtype,
+                                int32_t *dev_status, void *stream);
+
+/* One block of a model round the layer: the norm before it, the layer, and
+ * the norm behind it with gate and residual scale (and, with next_w_pre or
+ * next_u, the norm before the next block):
+ *   u = w_pre x / rms(x);  y = layer(u);  h = res_scale x + g w_post y / rms(y)
+ * x and h [T][D] of x_dtype (h may be x); u bf16 [T][D] is written by this
+ * call, or, with u_ready != 0, read (the previous block's next_u).  y [T][D]
+ * in the plan's output type is the layer's output.  All matrices contiguous.
+ * next_u (bf16 [T][D], may be u itself): w_pre of the next block is next_w_pre
+ * (NULL: ones).  Enqueued on `stream` like moe_forward. */
+typedef struct {
+    const void *x;
+    void *u, *y, *h, *next_u;
+    const void *w_pre, *w_post, *gate, *next_w_pre;
+    int32_t x_dtype, w_dtype, gate_kind, u_ready;
+    float res_scale, eps;
+} moe_block_args;
+MOE_API moe_status moe_forward_block(void *plan, const moe_block_args *args, int32_t T, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,9 @@ PRECISION_MX, PRECISION_MIXED = 0, 1
 ENTRY_POINTS = ("moe_plan", "moe_forward", "moe_forward_host", "moe_get_device_status", "moe_workspace_bytes",
                 "moe_free", "moe_status_str", "moe_mxfp4_encode", "moe_mx_gemm", "moe_mma_probe",
                 "moe_ep_row_bytes", "moe_ep_dispatch", "moe_ep_combine", "moe_quantile_balance", "moe_set_bias",
-                "moe_mx_gemm_noalloc")
+                "moe_mx_gemm_noalloc", "moe_sort", "moe_permute", "moe_unpermute", "moe_unpermute_backward",
+                "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward", "moe_mxfp4_quantize",
+                "moe_mxfp4_decode", "moe_mx4_gemm", "moe_forward_block")
 
 
 class MoeError(RuntimeError):
@@ -79,6 +81,8 @@ def library_path() -> str:
 def lib(build_if_missing: bool = False):
     """Load libmoe.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -120,6 +124,8 @@ def lib(build_if_missing: bool = False):
             L.moe_mma_probe.argtypes = [i32, i32, i32, P, C.POINTER(C.c_double), P]
             L.moe_mx_gemm_noalloc.restype = C.c_int
             L.moe_mx_gemm_noalloc.argtypes = [P, P, i32, P, P, i32, i32, P, P, P]
+            from . import block
+            block.declare(L)
             _lib = L
     return _lib
 
@@ -270,6 +276,46 @@ class Plan:
                                  C.byref(dbg) if dbg is not None else None), "moe_forward")
         return out
 
+    def forward_block(self, x: torch.Tensor, *, w_pre: Optional[torch.Tensor] = None,
+                      w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      gate_per: Optional[str] = None, res_scale: float = 1.0, eps: float = 1e-6,
+                      u: Optional[torch.Tensor] = None, next_w_pre: Optional[torch.Tensor] = None,
+                      need_next_u: bool = False, stream=None):
+        """The layer inside its block (see moe_forward_block): u = w_pre x /
+        rms(x), y = layer(u), h = res_scale x + gate w_post y / rms(y), for x
+        [T][D] (the residual stream).  Returns (h, next_u): with need_next_u,
+        next_u = next_w_pre h / rms(h) is the next block's input, to be given to
+        its call as `u`, which then computes no norm of its own."""
+        what = "forward_block"
+        block._require(x.is_cuda and x.device == self.device and x.dim() == 2 and x.shape[1] == self.cfg.d_model
+                       and x.dtype in block.DTYPES, "forward_block: x is [T][D] on the plan's device")
+        x = x.contiguous()
+        T, D = x.shape
+        a = block._BlockArgs()
+        gate, a.gate_kind = block._gate(gate, gate_per, T, D, x.device, what)
+        a.w_dtype = block._norm_weights(what, x.device, D, w_post, w_pre, gate)
+        if next_w_pre is not None:
+            block._require(need_next_u and block.DTYPES.get(next_w_pre.dtype) == a.w_dtype
+                           or (need_next_u and w_post is None and w_pre is None and gate is None),
+                           "forward_block: next_w_pre goes with need_next_u and has the other weights' type")
+            a.w_dtype = block._norm_weights(what, x.device, D, next_w_pre, None, None)
+        if u is not None:
+            block._require(u.dtype == torch.bfloat16 and u.shape == x.shape and u.device == x.device and u.is_contiguous(),
+                           "forward_block: u is the previous call's next_u")
+        a.u_ready = int(u is not None)
+        with torch.cuda.device(self.device):
+            if u is None:
+                u = torch.empty(T, D, dtype=torch.bfloat16, device=x.device)
+            y = torch.empty(T, D, dtype=self.out_dtype, device=x.device)
+            h = torch.empty_like(x)
+            next_u = torch.empty_like(u) if need_next_u else None
+            for n, t in (("x", x), ("u", u), ("y", y), ("h", h), ("next_u", next_u), ("w_pre", w_pre), ("w_post", w_post),
+                         ("gate", gate), ("next_w_pre", next_w_pre)):
+                setattr(a, n, None if t is None else t.data_ptr())
+            a.x_dtype, a.res_scale, a.eps = block.DTYPES[x.dtype], res_scale, eps
+            _check(lib().moe_forward_block(self._h, C.byref(a), T, _stream_ptr(stream)), "moe_forward_block")
+        return h, next_u
+
     def forward_host(self, x_host: torch.Tensor, y_host: torch.Tensor, stream=None):
         """End-to-end call with host buffers (bf16 [T][D] in, [T][D] out in the plan's output dtype)."""
         assert x_host.dtype == torch.bfloat16 and not x_host.is_cuda and y_host.dtype == self.out_dtype
@@ -343,3 +389,8 @@ def debug_buffers(cfg, T: int, device, fields=DEBUG_FIELDS) -> dict:
         "hqs": ((T * k, I // 32), u8), "o": ((T * k, L), f32), "cq": ((T, L), u8), "cs": ((T, L // 32), u8),
     }
     return {f: torch.zeros(*spec[f][0], dtype=spec[f][1], device=device) for f in fields}
+
+
+from . import block  # noqa: E402
+from .block import (block_norm, block_norm_backward, mx4_gemm, mxfp4_decode, mxfp4_quantize, permute,  # noqa: E402,F401
+                    permute_backward, sort_by_expert, unpermute, unpermute_backward)

@@ -28,6 +28,7 @@
 
 #include "../../include/moe.h"
 #include "internal.h"
+#include "vec.cuh"
 
 using namespace moe;
 
@@ -1453,6 +1454,298 @@ moe_status moe_mma_probe(int32_t kind, int32_t n, int32_t iters, int32_t* dev_st
     if (err != cudaSuccess) return cuda_status(err);
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
     return cuda_status(launch_mma_probe(kind, n, iters, sms, dev_status, flops_out, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Operators round the layer: argument checks, then one launch or two.
+namespace {
+
+bool known_dtype(int dt) { return dt == MOE_DTYPE_F32 || dt == MOE_DTYPE_BF16 || dt == MOE_DTYPE_F16; }
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool aligned_elem(const void* p, int dt) { return aligned(p, elem_bytes(dt)); }
+
+// A matrix of T rows of D elements: present, aligned to its elements, rows
+// that do not overlap.
+bool matrix_ok(const void* p, int64_t ld, int dt, int D) { return p && aligned_elem(p, dt) && ld >= D; }
+
+bool slots_ok(int32_t T, int32_t k) {
+    return T >= 0 && k >= 1 && k <= 32 && static_cast<int64_t>(T) * k <= 0x7fffffff;
+}
+
+// MXFP4 codes [rows][K / 2] as bytes, boxes of 128 bytes (256 elements) x box_rows.
+bool map_fp4(CUtensorMap* m, const void* codes, int64_t rows, int64_t K, int box_rows) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+    cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t es[2] = {1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_sort(const int32_t* idx, int32_t T, int32_t k, int32_t E, int32_t* offsets, int32_t* sorted_slot,
+                    int32_t* slot_pos, void* stream) {
+    if (!slots_ok(T, k) || E < 1 || E > 1024 || !offsets) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!idx || !sorted_slot || !slot_pos)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(idx, 4) || !aligned(offsets, 4) || !aligned(sorted_slot, 4) || !aligned(slot_pos, 4))
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_sort(idx, static_cast<int64_t>(T) * k, E, offsets, sorted_slot, slot_pos,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_permute(const void* x, int64_t x_stride, int64_t row_bytes, int32_t T, int32_t k,
+                       const int32_t* slot_pos, int64_t n_rows, void* rows, int64_t rows_stride, void* stream) {
+    if (!slots_ok(T, k) || n_rows < 0 || row_bytes < 1 || x_stride < row_bytes || rows_stride < row_bytes)
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0 || n_rows == 0) return MOE_OK;
+    if (!x || !slot_pos || !rows || !aligned(slot_pos, 4)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_permute(static_cast<const uint8_t*>(x), x_stride, row_bytes, T, k, slot_pos, n_rows,
+                                      static_cast<uint8_t*>(rows), rows_stride, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_unpermute(const void* rows, int64_t ld_rows, int32_t dtype, int64_t n_rows, const int32_t* slot_pos,
+                         const float* w, int32_t T, int32_t k, int32_t D, void* y, int64_t ld_y, int32_t y_dtype,
+                         void* stream) {
+    if (!slots_ok(T, k) || n_rows < 0 || D < 1 || !known_dtype(dtype) || !known_dtype(y_dtype))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if ((n_rows > 0 && !matrix_ok(rows, ld_rows, dtype, D)) || !matrix_ok(y, ld_y, y_dtype, D) || !slot_pos ||
+        !aligned(slot_pos, 4) || !aligned(w, 4))
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_unpermute(rows, ld_rows, dtype, n_rows, slot_pos, w, T, k, D, y, ld_y, y_dtype,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_unpermute_backward(const void* dy, int64_t ld_dy, int32_t dy_dtype, const void* rows, int64_t ld_rows,
+                                  int32_t dtype, int64_t n_rows, const int32_t* slot_pos, const float* w, int32_t T,
+                                  int32_t k, int32_t D, void* d_rows, int64_t ld_d_rows, float* d_w, void* stream) {
+    if (!slots_ok(T, k) || n_rows < 0 || D < 1 || !known_dtype(dtype) || !known_dtype(dy_dtype))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0 || (!d_rows && !d_w)) return MOE_OK;
+    if (!matrix_ok(dy, ld_dy, dy_dtype, D) || !slot_pos || !aligned(slot_pos, 4) || !aligned(w, 4) || !aligned(d_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (d_w && n_rows > 0 && !matrix_ok(rows, ld_rows, dtype, D)) return MOE_ERR_INVALID_ARG;
+    if (d_rows && !matrix_ok(d_rows, ld_d_rows, dtype, D)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_unpermute_backward(dy, ld_dy, dy_dtype, rows, ld_rows, dtype, n_rows, slot_pos, w, T, k,
+                                                 D, d_rows, ld_d_rows, d_w, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_block_norm(const moe_block_norm_args* p, void* stream) {
+    if (!p || p->T < 0 || p->D < 1 || p->D > kNormMaxWidth || !known_dtype(p->x_dtype) || !(p->eps >= 0.0f))
+        return MOE_ERR_INVALID_ARG;
+    if ((!p->y && !p->u) || (p->y && !p->h)) return MOE_ERR_INVALID_ARG;
+    if (p->gate_kind != MOE_GATE_NONE && p->gate_kind != MOE_GATE_CHANNEL && p->gate_kind != MOE_GATE_TOKEN)
+        return MOE_ERR_INVALID_ARG;
+    const bool gated = p->y && p->gate_kind != MOE_GATE_NONE;
+    if (gated && !p->gate) return MOE_ERR_INVALID_ARG;
+    if ((p->y && p->w_post) || (p->u && p->w_pre) || gated) {
+        if (!known_dtype(p->w_dtype) || !aligned_elem(p->w_post, p->w_dtype) || !aligned_elem(p->w_pre, p->w_dtype) ||
+            !aligned_elem(p->gate, p->w_dtype))
+            return MOE_ERR_INVALID_ARG;
+    }
+    if (p->T == 0) return MOE_OK;
+    if (!matrix_ok(p->x, p->ld_x, p->x_dtype, p->D)) return MOE_ERR_INVALID_ARG;
+    if (p->y && (!known_dtype(p->y_dtype) || !matrix_ok(p->y, p->ld_y, p->y_dtype, p->D) ||
+                 !matrix_ok(p->h, p->ld_h, p->x_dtype, p->D)))
+        return MOE_ERR_INVALID_ARG;
+    if (p->u && (!known_dtype(p->u_dtype) || !matrix_ok(p->u, p->ld_u, p->u_dtype, p->D))) return MOE_ERR_INVALID_ARG;
+    NormArgs a = {};
+    a.x = p->x;
+    a.ld_x = p->ld_x;
+    a.u = p->u;
+    a.ld_u = p->ld_u;
+    a.w_pre = p->u ? p->w_pre : nullptr;
+    if (p->y) {
+        a.y = p->y;
+        a.ld_y = p->ld_y;
+        a.h = p->h;
+        a.ld_h = p->ld_h;
+        a.w_post = p->w_post;
+        a.gate = gated ? p->gate : nullptr;
+        a.gate_kind = p->gate_kind;
+    }
+    a.T = p->T;
+    a.D = p->D;
+    a.dt_x = p->x_dtype;
+    a.dt_y = p->y_dtype;
+    a.dt_u = p->u_dtype;
+    a.dt_w = p->w_dtype;
+    a.res_scale = p->res_scale;
+    a.eps = p->eps;
+    return cuda_status(launch_block_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_block_norm_workspace_bytes(int32_t T, int32_t D) {
+    if (T < 0 || D < 1) return 0;
+    return sizeof(float) * 2 * static_cast<size_t>(D) * static_cast<size_t>(std::min<int32_t>(std::max<int32_t>(T, 1), kNormParts));
+}
+
+moe_status moe_block_norm_backward(const moe_block_norm_backward_args* p, void* stream) {
+    if (!p || p->T < 0 || p->D < 1 || p->D > kNormMaxWidth || !known_dtype(p->x_dtype) || !(p->eps >= 0.0f))
+        return MOE_ERR_INVALID_ARG;
+    if (p->gate_kind != MOE_GATE_NONE && p->gate_kind != MOE_GATE_CHANNEL && p->gate_kind != MOE_GATE_TOKEN)
+        return MOE_ERR_INVALID_ARG;
+    const bool gated = p->y && p->gate_kind != MOE_GATE_NONE;
+    if (p->T > 0) {
+        if (!p->dh && !p->du) return MOE_ERR_INVALID_ARG;
+        if (p->du && !p->h) return MOE_ERR_INVALID_ARG;
+    }
+    if (gated && !p->gate) return MOE_ERR_INVALID_ARG;
+    if (!p->y && (p->dy || p->dw_post || p->d_gate) && p->T > 0) return MOE_ERR_INVALID_ARG;
+    if (p->d_gate && p->gate_kind == MOE_GATE_NONE) return MOE_ERR_INVALID_ARG;
+    if (p->dw_pre && !p->du && p->T > 0) return MOE_ERR_INVALID_ARG;
+    if (p->w_post || p->w_pre || gated) {
+        if (!known_dtype(p->w_dtype) || !aligned_elem(p->w_post, p->w_dtype) || !aligned_elem(p->w_pre, p->w_dtype) ||
+            !aligned_elem(p->gate, p->w_dtype))
+            return MOE_ERR_INVALID_ARG;
+    }
+    if (!aligned(p->dw_post, 4) || !aligned(p->dw_pre, 4) || !aligned(p->d_gate, 4)) return MOE_ERR_INVALID_ARG;
+    const bool columns = p->dw_pre || p->dw_post || (p->d_gate && p->gate_kind == MOE_GATE_CHANNEL);
+    NormBackArgs a = {};
+    if (p->T > 0) {
+        if (p->dh && !matrix_ok(p->dh, p->ld_dh, p->x_dtype, p->D)) return MOE_ERR_INVALID_ARG;
+        if (p->du && (!known_dtype(p->u_dtype) || !matrix_ok(p->du, p->ld_du, p->u_dtype, p->D) ||
+                      !matrix_ok(p->h, p->ld_h, p->x_dtype, p->D)))
+            return MOE_ERR_INVALID_ARG;
+        if (p->y && (!known_dtype(p->y_dtype) || !matrix_ok(p->y, p->ld_y, p->y_dtype, p->D))) return MOE_ERR_INVALID_ARG;
+        if (p->dx && !matrix_ok(p->dx, p->ld_dx, p->x_dtype, p->D)) return MOE_ERR_INVALID_ARG;
+        if (p->dy && !matrix_ok(p->dy, p->ld_dy, p->y_dtype, p->D)) return MOE_ERR_INVALID_ARG;
+        if (columns && (!p->workspace || !aligned(p->workspace, 16) ||
+                        p->workspace_bytes < moe_block_norm_workspace_bytes(p->T, p->D)))
+            return MOE_ERR_INVALID_ARG;
+        a.part = columns ? static_cast<float*>(p->workspace) : nullptr;
+    }
+    a.dh = p->dh;
+    a.ld_dh = p->ld_dh;
+    a.du = p->du;
+    a.ld_du = p->ld_du;
+    a.h = p->du ? p->h : nullptr;
+    a.ld_h = p->ld_h;
+    a.y = p->y;
+    a.ld_y = p->ld_y;
+    a.w_post = p->w_post;
+    a.w_pre = p->w_pre;
+    a.gate = gated ? p->gate : nullptr;
+    a.gate_kind = p->y ? p->gate_kind : MOE_GATE_NONE;
+    a.dx = p->dx;
+    a.ld_dx = p->ld_dx;
+    a.dy = p->dy;
+    a.ld_dy = p->ld_dy;
+    a.dw_post = p->dw_post;
+    a.dw_pre = p->dw_pre;
+    a.d_gate_channel = p->gate_kind == MOE_GATE_CHANNEL ? p->d_gate : nullptr;
+    a.d_gate_token = p->gate_kind == MOE_GATE_TOKEN ? p->d_gate : nullptr;
+    a.T = p->T;
+    a.D = p->D;
+    a.dt_x = p->x_dtype;
+    a.dt_y = p->y_dtype;
+    a.dt_u = p->u_dtype;
+    a.dt_w = p->w_dtype;
+    a.res_scale = p->res_scale;
+    a.eps = p->eps;
+    return cuda_status(launch_block_norm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_mxfp4_quantize(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t K, uint8_t* codes,
+                              uint8_t* scales, void* stream) {
+    if (rows < 0 || K <= 0 || K % 32 || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !aligned_elem(x, dtype) || ld_x < K || !codes || !scales || !aligned(codes, 4)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_mxfp4_quantize(x, ld_x, dtype, rows, K, codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x, int64_t ld_x,
+                            int32_t dtype, void* stream) {
+    if (rows < 0 || K <= 0 || K % 32 || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !aligned_elem(x, dtype) || ld_x < K || !codes || !scales || !aligned(codes, 4)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_mxfp4_decode(codes, scales, rows, K, x, ld_x, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t G, int32_t M, const uint8_t* b_codes,
+                        const uint8_t* b_scales, int32_t N, int32_t K, const int32_t* offsets, void* out,
+                        int64_t ld_out, int32_t out_dtype, int32_t* dev_status, void* stream) {
+    if (G < 1 || G > 1024 || M < 1 || N < 0 || K < 128 || K % 128 || static_cast<int64_t>(G) * M > 0x7fffffff ||
+        !known_dtype(out_dtype) || (!offsets && G != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (N == 0) return MOE_OK;
+    if (!a_codes || !a_scales || !b_codes || !b_scales || !out || ld_out < M) return MOE_ERR_INVALID_ARG;
+    if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
+        !aligned(offsets, 4) || !aligned(dev_status, 4) || !aligned_elem(out, out_dtype))
+        return MOE_ERR_INVALID_ARG;
+    if (!encode_fn()) return MOE_ERR_UNSUPPORTED;
+    int dev = 0, major = 0, minor = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (err != cudaSuccess) return cuda_status(err);
+    if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
+    Mx4Params p;
+    mx4_tiles(M, N, G, &p.nt, &p.b_box);
+    if (!map_fp4(&p.tmA, a_codes, static_cast<int64_t>(G) * M, K, 128) || !map_fp4(&p.tmB, b_codes, N, K, p.b_box))
+        return MOE_ERR_INVALID_ARG;
+    p.sfa = a_scales;
+    p.sfb = b_scales;
+    p.offsets = offsets;
+    p.out = out;
+    p.ld_out = ld_out;
+    p.status = dev_status;
+    p.G = G;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.dt_out = out_dtype;
+    return cuda_status(launch_mx4_gemm(p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_forward_block(void* plan, const moe_block_args* b, int32_t T, void* stream) {
+    Plan* p = static_cast<Plan*>(plan);
+    if (!p || !b || T < 1 || T > p->T_max || p->D > kNormMaxWidth || !b->x || !b->u || !b->y || !b->h)
+        return MOE_ERR_INVALID_ARG;
+    DevGuard guard(p->device);
+    moe_block_norm_args in = {}, out = {};
+    in.T = out.T = T;
+    in.D = out.D = p->D;
+    in.ld_x = in.ld_u = out.ld_x = out.ld_y = out.ld_h = out.ld_u = p->D;
+    in.x = out.x = b->x;
+    in.x_dtype = out.x_dtype = b->x_dtype;
+    in.w_dtype = out.w_dtype = b->w_dtype;
+    in.u_dtype = out.u_dtype = MOE_DTYPE_BF16;
+    in.eps = out.eps = b->eps;
+    in.w_pre = b->w_pre;
+    in.u = b->u;
+    out.y = b->y;
+    out.y_dtype = p->out_bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
+    out.w_post = b->w_post;
+    out.gate = b->gate;
+    out.gate_kind = b->gate_kind;
+    out.res_scale = b->res_scale;
+    out.h = b->h;
+    out.u = b->next_u;
+    out.w_pre = b->next_u ? b->next_w_pre : nullptr;
+    // the last step's arguments are checked before the first is enqueued
+    moe_block_norm_args probe = out;
+    probe.T = 0;
+    moe_status st = moe_block_norm(&probe, stream);
+    if (st != MOE_OK) return st;
+    if (!known_dtype(b->x_dtype) || !matrix_ok(b->x, p->D, b->x_dtype, p->D) || !matrix_ok(b->h, p->D, b->x_dtype, p->D) ||
+        !aligned(b->y, 16) || !aligned(b->u, 16) || !aligned(b->next_u, 2))
+        return MOE_ERR_INVALID_ARG;
+    if (!b->u_ready) {
+        st = moe_block_norm(&in, stream);
+        if (st != MOE_OK) return st;
+    }
+    st = moe_forward(plan, b->u, T, b->y, stream, nullptr);
+    if (st != MOE_OK) return st;
+    return moe_block_norm(&out, stream);
 }
 
 }  // extern "C"

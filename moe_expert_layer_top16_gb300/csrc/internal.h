@@ -305,6 +305,67 @@ cudaError_t launch_ep_combine(const uint8_t* wire, const float* out, int T, int 
 cudaError_t launch_quantile_balance(const float* logits, const float* bias, int T, int E, int k, int target,
                                     double alpha, double* marg, float* bias_out, cudaStream_t s);
 
+// ------------------------------------------------------------------ tokens by expert and back (route.cu)
+// Strides in elements of their matrix (permute: in bytes); element types are
+// ElemType values (vec.cuh).
+cudaError_t launch_sort(const int32_t* idx, int64_t n, int E, int32_t* offsets, int32_t* sorted_slot,
+                        int32_t* slot_pos, cudaStream_t s);
+cudaError_t launch_permute(const uint8_t* x, int64_t x_stride, int64_t row_bytes, int64_t T, int k,
+                           const int32_t* slot_pos, int64_t n_rows, uint8_t* rows, int64_t rows_stride,
+                           cudaStream_t s);
+cudaError_t launch_unpermute(const void* rows, int64_t ld_rows, int dt, int64_t n_rows, const int32_t* slot_pos,
+                             const float* w, int64_t T, int k, int D, void* y, int64_t ld_y, int dty, cudaStream_t s);
+cudaError_t launch_unpermute_backward(const void* dy, int64_t ld_dy, int dty, const void* rows, int64_t ld_rows, int dt,
+                                      int64_t n_rows, const int32_t* slot_pos, const float* w, int64_t T, int k, int D,
+                                      void* d_rows, int64_t ld_d, float* d_w, cudaStream_t s);
+
+// ------------------------------------------------------------------ norms round a block (norm.cu)
+enum NormGate : int { NORM_GATE_NONE = 0, NORM_GATE_CHANNEL = 1, NORM_GATE_TOKEN = 2 };
+constexpr int kNormMaxWidth = 16384;
+constexpr int kNormParts = 304;          // partial column sums of a backward pass at most
+struct NormArgs {
+    const void *x, *y, *w_post, *w_pre, *gate;
+    void *h, *u;
+    int64_t ld_x, ld_y, ld_h, ld_u, T;
+    int D, dt_x, dt_y, dt_u, dt_w, gate_kind;
+    float res_scale, eps;
+};
+struct NormBackArgs {
+    const void *dh, *du, *h, *y, *w_post, *w_pre, *gate;
+    void *dx, *dy;
+    float *dw_post, *dw_pre, *d_gate_channel, *d_gate_token;
+    float* part;                         // [grid][2][D], or null: no column sums wanted
+    int64_t ld_dh, ld_du, ld_h, ld_y, ld_dx, ld_dy, T;
+    int D, dt_x, dt_y, dt_u, dt_w, gate_kind;
+    float res_scale, eps;
+};
+cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------------ four-bit activations and products (mx4.cu)
+cudaError_t launch_mxfp4_quantize(const void* x, int64_t ld, int dt, int64_t rows, int64_t K, uint8_t* codes,
+                                  uint8_t* scales, cudaStream_t s);
+cudaError_t launch_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x,
+                                int64_t ld, int dt, cudaStream_t s);
+struct Mx4Params {
+    CUtensorMap tmA;            // [G * M][K / 2] bytes, boxes of 128 bytes x 128 rows, 128-byte swizzle
+    CUtensorMap tmB;            // [N][K / 2] bytes, boxes of 128 bytes x b_box rows
+    const uint8_t* sfa;         // [G * M][K / 32]
+    const uint8_t* sfb;         // [N][K / 32]
+    const int32_t* offsets;     // [G + 1], or null (G == 1): all N rows
+    void* out;
+    int64_t ld_out;
+    int* status;
+    int G, M, N, K;
+    int dt_out;
+    int nt;                     // tokens of a work item at most
+    int b_box;
+    int stages, stage_bytes;
+};
+// Token rows of a work item and of a TMA box of B, for `N` rows in G groups.
+void mx4_tiles(int M, int N, int G, int* nt, int* b_box);
+cudaError_t launch_mx4_gemm(const Mx4Params& p, cudaStream_t s);
+
 // ------------------------------------------------------------------ tensor-core rate probe (peak.cu)
 enum ProbeKind : int { PROBE_MX_E2M1_E4M3 = 0, PROBE_MX_E4M3_E4M3 = 1, PROBE_BF16 = 2 };
 // grid CTAs each issue iters x 4 MMAs of M = 128 x n; *flops = their FLOPs

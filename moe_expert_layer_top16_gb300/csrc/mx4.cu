@@ -1,0 +1,587 @@
+// Four-bit activations and four-bit products.
+//
+//   quantise   MXFP4 codes and scales of fp32, bf16 or fp16 rows, by the rule
+//              of the weight encoder: per 32 elements the scale 2^e with
+//              e = floor(log2 amax) - 2, each magnitude to the nearest E2M1
+//              level, a tie to the smaller one
+//   decode     the values that codes and scales stand for
+//   product    out[n][m] = sum_k dq(B[n][k]) dq(A[g(n)][m][k]), A and B both
+//              MXFP4, on tcgen05 kind::mxf4 (K = 64 an instruction, twice the
+//              rate of the MXFP8 kind), fp32 accumulation
+#include "internal.h"
+#include "mx.cuh"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace moe {
+
+namespace {
+
+// ------------------------------------------------------------------ codec
+// Two E2M1 codes (nearest even, saturating) as a byte, `lo` in the low nibble.
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+        "cvt.u32.u8 %0, t;\n\t}"
+        : "=r"(r)
+        : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^-14 below one: a 16-bit input on a midpoint of the E2M1 levels, times
+// this, lies below it, and the next larger 16-bit value (at least 2^-11 above)
+// still lies above, so that rounding to nearest sends ties to the smaller
+// level.
+constexpr float kTieDown = 1.0f - 0x1p-14f;
+
+// The same for any fp32 value: the low 12 bits become one sticky bit and the
+// magnitude goes down by a quarter of the remaining unit, which moves a
+// midpoint (few significant bits) below itself and no other value across one.
+__device__ __forceinline__ float tie_down(float v) {
+    const uint32_t b = __float_as_uint(v), m = b & 0x7FFFFFFFu;
+    uint32_t s = (m & 0x7FFFF000u) | ((m & 0xFFFu) ? 0x800u : 0u);
+    s = s >= 0x01000000u ? s - 0x400u : 0u;          // below 2^-125: zero in any case
+    return __uint_as_float(s | (b & 0x80000000u));
+}
+
+// Scale code of a block whose largest magnitude has the bits `top`: 255 (not
+// a number) if that is an infinity or a NaN, 0 for a block of zeros.
+__device__ __forceinline__ uint32_t mx4_scale_code(uint32_t top) {
+    if (top >= 0x7F800000u) return 255u;
+    const int biased = static_cast<int>(top >> 23);
+    return biased > 2 ? static_cast<uint32_t>(biased - 2) : 0u;      // e = -127 at least
+}
+
+// Factor 2^-e for scale code c <= 252.
+__device__ __forceinline__ float mx4_inverse(uint32_t c) { return __uint_as_float((254u - c) << 23); }
+
+// V = 8: four lanes hold a block, 16-byte loads; V = 1: a warp holds a block.
+template <int V>
+__global__ void __launch_bounds__(256) mxfp4_quantize_kernel(const void* __restrict__ x, int64_t ld, int dt,
+                                                             int64_t rows, int64_t K, uint8_t* __restrict__ codes,
+                                                             uint8_t* __restrict__ scales) {
+    const int64_t per_row = K / V;
+    const int64_t n = rows * per_row;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    // whole warps iterate together: n is a multiple of a block's lanes
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31); i0 < n; i0 += stride) {
+        const int64_t i = i0 + (threadIdx.x & 31);
+        const bool in = i < n;
+        const int64_t r = in ? i / per_row : 0;
+        const int64_t c = in ? (i - r * per_row) * V : 0;
+        float v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = 0.0f;
+        if (in) raw_to_f32(load_raw<V>(x, r * ld + c, dt), dt, v);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 1; o < 32 / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t sc = mx4_scale_code(top);
+        const bool none = top == 0 || sc == 255u;
+        if (V == 8) {
+            const float f = none ? 0.0f : mx4_inverse(sc) * (dt == ELEM_F32 ? 1.0f : kTieDown);
+            uint32_t word = 0;
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                float lo = v[(2 * j) % V] * f, hi = v[(2 * j + 1) % V] * f;
+                if (dt == ELEM_F32) {
+                    lo = tie_down(lo);
+                    hi = tie_down(hi);
+                }
+                word |= e2m1_pair(lo, hi) << (8 * j);
+            }
+            if (in) {
+                *reinterpret_cast<uint32_t*>(codes + r * (K / 2) + c / 2) = none ? 0u : word;
+                if ((threadIdx.x & 3) == 0) scales[r * (K / 32) + c / 32] = static_cast<uint8_t>(sc);
+            }
+        } else {
+            const float f = tie_down(v[0] * (none ? 0.0f : mx4_inverse(sc)));
+            const float g = __shfl_down_sync(0xffffffffu, f, 1);
+            if (in) {
+                if (!(threadIdx.x & 1)) codes[r * (K / 2) + c / 2] = none ? 0 : static_cast<uint8_t>(e2m1_pair(f, g));
+                if ((threadIdx.x & 31) == 0) scales[r * (K / 32) + c / 32] = static_cast<uint8_t>(sc);
+            }
+        }
+    }
+}
+
+// One thread per 8 codes.
+template <int V>
+__global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __restrict__ codes,
+                                                           const uint8_t* __restrict__ scales, int64_t rows, int64_t K,
+                                                           void* __restrict__ x, int64_t ld, int dt) {
+    const int64_t per_row = K / 8;
+    const int64_t n = rows * per_row;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * 8;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + r * (K / 2) + c / 2);
+        const uint32_t sc = scales[r * (K / 32) + c / 32];
+        // 2^e in two factors, each a normal number
+        const int e = static_cast<int>(sc) - 127;
+        const float f1 = exp2i(e / 2), f2 = exp2i(e - e / 2);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t q = (w >> (4 * j)) & 15u, m = q & 7u;
+            // 0, 1/2, then (1 + low bit / 2) 2^(m / 2 - 1)
+            const float a = m < 2 ? 0.5f * static_cast<float>(m)
+                                  : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
+            const float s = a * f1 * f2;
+            v[j] = sc == 255u ? __uint_as_float(0x7FFFFFFFu) : (q & 8u ? -s : s);
+        }
+        if (V == 8) {
+            store_vec(x, r * ld + c, dt, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float o[1] = {v[j]};
+                store_vec(x, r * ld + c + j, dt, o);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ product
+// A persistent CTA on each SM takes work items (group g, 128 rows of A, up to
+// nt rows of B of that group): A is the MMA's M operand, so that a short group
+// pads B's rows to 16 only.  A stage is 256 elements of K: 128 bytes a row of
+// A and of B, in the 128-byte swizzle.  Roles:
+//   warp 0      TMA producer of both operands
+//   warp 1      MMA issuer: scale copies shared memory -> TMEM, four MMAs of
+//               K = 64, commit
+//   warps 2-5   scales: warp q takes every fourth stage; it reads the row-major
+//               scales of the stage's rows and arranges them as the copy wants
+//               them (row r of 128 in 16-byte slot r % 32, word r / 32)
+//   warps 6-9   epilogue
+// The scale warps read ahead of the free stage, so that the caller's row-major
+// scales need no launch that rearranges them.
+constexpr int kMx4BlockM = 128;
+constexpr int kMx4BlockK = 256;
+constexpr int kMx4NtMax = 224;                    // two accumulators and two sets of scale columns in 512
+constexpr int kMx4ABytes = kMx4BlockM * 128;
+constexpr int kMx4ScaleWarps = 4;
+constexpr int kMx4Threads = (2 + kMx4ScaleWarps + 4) * 32;
+constexpr int kMx4MaxStages = 16;
+constexpr int kMx4TmemCols = 512;
+constexpr int kMx4MaxGroups = 1024;
+constexpr int kMx4BarBytes = (3 * kMx4MaxStages + 5) * 8 + 24;
+
+struct Mx4Item {
+    int a_row, m0, b_row, n;
+};
+
+struct Mx4Geometry {
+    int M, m_tiles, nt, G;
+    const int* tile_off;     // [G + 1] first token tile of each group
+    const int* first;        // [G + 1] first row; first[G]: unused
+    const int* count;        // [G]
+};
+
+__device__ __forceinline__ Mx4Item mx4_item(const Mx4Geometry& g, int64_t it) {
+    const int tile = static_cast<int>(it / g.m_tiles);
+    const int mt = static_cast<int>(it - static_cast<int64_t>(tile) * g.m_tiles);
+    int lo = 0, hi = g.G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (g.tile_off[mid] <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    const int j = tile - g.tile_off[lo];
+    Mx4Item w;
+    w.m0 = mt * kMx4BlockM;
+    w.a_row = lo * g.M + w.m0;
+    w.b_row = g.first[lo] + j * g.nt;
+    w.n = min(g.nt, g.count[lo] - j * g.nt);
+    return w;
+}
+
+// Eight scale codes of a row, as two words.  Rows are K / 32 bytes apart: a
+// multiple of 8 bytes when `wide`, else of 4 (and the last stage may hold one
+// word only).
+__device__ __forceinline__ uint2 load_scales(const uint8_t* p, bool wide, bool second) {
+    if (wide) return __ldg(reinterpret_cast<const uint2*>(p));
+    uint2 r;
+    r.x = __ldg(reinterpret_cast<const uint32_t*>(p));
+    r.y = second ? __ldg(reinterpret_cast<const uint32_t*>(p + 4)) : 0u;
+    return r;
+}
+
+__device__ __forceinline__ bool mx4_drain(uint64_t* bar, uint32_t parity, int* status) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (status) atomicCAS(status, 0, DEV_TIMEOUT_TEARDOWN);
+            return false;
+        }
+    }
+    return true;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_out(void* out, int64_t off, float v) {
+    if (DT == ELEM_F32) static_cast<float*>(out)[off] = v;
+    else if (DT == ELEM_BF16) static_cast<__nv_bfloat16*>(out)[off] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(out)[off] = __float2half_rn(v);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int S = pin(p.stages), stage_bytes = pin(p.stage_bytes);
+    const int M = pin(p.M), K = pin(p.K), nt = pin(p.nt), G = pin(p.G), b_box = pin(p.b_box);
+    const int atoms_max = (nt + 127) / 128;
+    const int off_b = kMx4ABytes, off_sfa = off_b + nt * 128, off_sfb = off_sfa + 1024;
+    uint8_t* tail = base + S * stage_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(tail);      // operands of a stage have landed
+    uint64_t* sfull = full + kMx4MaxStages;                  // its scales are arranged
+    uint64_t* empty = sfull + kMx4MaxStages;
+    uint64_t* tfull = empty + kMx4MaxStages;                 // [2]
+    uint64_t* tempty = tfull + 2;                            // [2]
+    uint64_t* tdown = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdown + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* tile_off = reinterpret_cast<int*>(tail + kMx4BarBytes);
+    int* first = tile_off + G + 1;
+    int* count = first + G + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* status = pin(p.status);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&sfull[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 4);
+        }
+        mbar_init(tdown, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&p.tmA);
+        prefetch_tmap(&p.tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, kMx4TmemCols);
+        tmem_relinquish();
+    }
+    if (warp == 2) {
+        // token tiles of each group, from the offsets (kept inside [0, N])
+        const int per = (G + 31) / 32;
+        int sum = 0;
+        for (int u = 0; u < per; ++u) {
+            const int g = lane * per + u;
+            if (g >= G) break;
+            int lo = 0, hi = p.N;
+            if (p.offsets) {
+                lo = min(max(p.offsets[g], 0), p.N);
+                hi = min(max(p.offsets[g + 1], lo), p.N);
+            }
+            first[g] = lo;
+            count[g] = hi - lo;
+            tile_off[g] = sum;
+            sum += (hi - lo + nt - 1) / nt;
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        for (int u = 0; u < per; ++u) {
+            const int g = lane * per + u;
+            if (g < G) tile_off[g] += incl - sum;
+        }
+        if (lane == 31) tile_off[G] = incl;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int m_tiles = (M + kMx4BlockM - 1) / kMx4BlockM;
+    const Mx4Geometry geo{M, m_tiles, nt, G, tile_off, first, count};
+    const int64_t items = static_cast<int64_t>(tile_off[G]) * m_tiles;
+    const int KT = (K + kMx4BlockK - 1) / kMx4BlockK;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
+        bool ok = true;
+        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+            const Mx4Item w = mx4_item(geo, it);
+            const int nm = (w.n + 15) & ~15;
+            const int nbox = (nm + b_box - 1) / b_box;
+            const uint32_t tx = static_cast<uint32_t>(kMx4ABytes + nbox * b_box * 128);
+            for (int kt = 0; kt < KT; ++kt) {
+                ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag, status, DEV_TIMEOUT_PRODUCER);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    uint8_t* sb = base + stage * stage_bytes;
+                    mbar_arrive_expect_tx(&full[stage], tx);
+                    tma_load_2d(sb, &p.tmA, &full[stage], kt * 128, w.a_row);
+                    for (int c = 0; c < nbox; ++c)
+                        tma_load_2d(sb + off_b + c * b_box * 128, &p.tmB, &full[stage], kt * 128, w.b_row + c * b_box);
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == static_cast<uint32_t>(S)) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (*abort_flag && lane == 0) {
+            // every copy in flight lands before the CTA leaves
+            for (int s = 0; s < S; ++s)
+                if (issued & (1u << s)) mx4_drain(&full[s], (issued_parity >> s) & 1u, status);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, used = 0;
+        bool any = false;
+        for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+            const Mx4Item w = mx4_item(geo, it);
+            const int nm = (w.n + 15) & ~15;
+            const int atoms = (nm + 127) / 128;
+            bool ok = mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, status, DEV_TIMEOUT_MMA);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + acc * static_cast<uint32_t>(nt);
+            const uint32_t idesc0 = idesc_mxf4(kMx4BlockM, nm);
+            for (int kt = 0; kt < KT; ++kt) {
+                ok = mbar_wait(&full[stage], phase, abort_flag, status, DEV_TIMEOUT_MMA) &&
+                     mbar_wait(&sfull[stage], phase, abort_flag, status, DEV_TIMEOUT_MMA);
+                if (!__all_sync(0xffffffffu, ok)) goto mma_done;
+                tc_fence_after();
+                // consecutive stages use different scale columns
+                const uint32_t sfa = tmem + 2u * static_cast<uint32_t>(nt) + (used++ & 1u) * 24u;
+                const uint32_t sfb = sfa + 8u;
+                if (elect_one()) {
+                    uint8_t* sb = base + stage * stage_bytes;
+                    const uint64_t ad = sdesc_sw128(smem_u32(sb)), bd = sdesc_sw128(smem_u32(sb + off_b));
+                    const int halves = (K - kt * kMx4BlockK > 128) ? 2 : 1;
+                    for (int h = 0; h < halves; ++h) {
+                        tc_cp_32x128b_x4(sfa + 4u * h, sdesc_rows16(smem_u32(sb + off_sfa + h * 512)));
+                        for (int a = 0; a < atoms; ++a)
+                            tc_cp_32x128b_x4(sfb + 8u * h + 4u * a,
+                                             sdesc_rows16(smem_u32(sb + off_sfb + (h * atoms_max + a) * 512)));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            // scale ids 0 and 2: the low and high half of each scale word
+                            const uint32_t idesc = idesc0 | (2u * i) << 4 | (2u * i) << 29;
+                            mma_mxf4(d, ad + 4 * h + 2 * i, bd + 4 * h + 2 * i, idesc, sfa + 4u * h, sfb + 8u * h,
+                                     (kt | h | i) != 0 ? 1u : 0u);
+                        }
+                    }
+                    tc_commit(&empty[stage]);
+                }
+                any = true;
+                __syncwarp();
+                if (++stage == static_cast<uint32_t>(S)) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (elect_one()) tc_commit(&tfull[acc]);
+            __syncwarp();
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+        }
+    mma_done:
+        // every tcgen05 operation finishes before TMEM is freed
+        if (any) {
+            if (elect_one()) {
+                tc_commit(tdown);
+                mx4_drain(tdown, 0, status);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 2 + kMx4ScaleWarps) {
+        // ------------------------------------------------------------ scales
+        const int q = warp - 2;
+        const int64_t pitch = K / 32;
+        const bool wide_a = (K % 256 == 0) && (reinterpret_cast<uintptr_t>(p.sfa) & 7) == 0;
+        const bool wide_b = (K % 256 == 0) && (reinterpret_cast<uintptr_t>(p.sfb) & 7) == 0;
+        int64_t c0 = 0;                       // stages of earlier items
+        bool ok = true;
+        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, c0 += KT) {
+            const Mx4Item w = mx4_item(geo, it);
+            const int atoms = (w.n + 127) / 128;
+            for (int kt = static_cast<int>((q - c0) & (kMx4ScaleWarps - 1)); kt < KT; kt += kMx4ScaleWarps) {
+                const bool second = K - kt * kMx4BlockK > 128;
+                uint2 va[4], vb[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 32 * i + lane;
+                    va[i] = make_uint2(0, 0);
+                    if (w.m0 + r < M) va[i] = load_scales(p.sfa + (w.a_row + r) * pitch + kt * 8, wide_a, second);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 32 * i + lane;
+                    vb[i] = make_uint2(0, 0);
+                    if (r < w.n) vb[i] = load_scales(p.sfb + static_cast<int64_t>(w.b_row + r) * pitch + kt * 8, wide_b, second);
+                }
+                const int64_t c = c0 + kt;
+                const uint32_t stage = static_cast<uint32_t>(c % S), phase = static_cast<uint32_t>((c / S) & 1);
+                ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag, status, DEV_TIMEOUT_PRODUCER);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* sb = base + stage * stage_bytes;
+                uint4* sa = reinterpret_cast<uint4*>(sb + off_sfa);
+                sa[lane] = make_uint4(va[0].x, va[1].x, va[2].x, va[3].x);
+                sa[32 + lane] = make_uint4(va[0].y, va[1].y, va[2].y, va[3].y);
+                uint4* sfb = reinterpret_cast<uint4*>(sb + off_sfb);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    if (a < atoms) {
+                        sfb[a * 32 + lane] = make_uint4(vb[4 * a].x, vb[4 * a + 1].x, vb[4 * a + 2].x, vb[4 * a + 3].x);
+                        sfb[(atoms_max + a) * 32 + lane] =
+                            make_uint4(vb[4 * a].y, vb[4 * a + 1].y, vb[4 * a + 2].y, vb[4 * a + 3].y);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfull[stage]);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3;         // TMEM lanes this warp may read
+        const uint32_t t_lane = static_cast<uint32_t>(32 * quarter) << 16;
+        uint32_t acc = 0, acc_phase = 0;
+        for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+            const Mx4Item w = mx4_item(geo, it);
+            const bool ok = mbar_wait(&tfull[acc], acc_phase, abort_flag, status, DEV_TIMEOUT_EPILOGUE);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t a0 = tmem + t_lane + acc * static_cast<uint32_t>(nt);
+            const int col = w.m0 + 32 * quarter + lane;
+            const bool in = col < M;
+            const int nm = (w.n + 15) & ~15;
+            uint32_t cur[16], nxt[16];
+            tmem_ld16_async(a0, cur);
+            tmem_wait16(cur);
+            for (int n0 = 0; n0 < nm; n0 += 16) {
+                const bool more = n0 + 16 < nm;
+                if (more) tmem_ld16_async(a0 + static_cast<uint32_t>(n0 + 16), nxt);
+                const int nv = min(16, w.n - n0);
+                int64_t o = static_cast<int64_t>(w.b_row + n0) * p.ld_out + col;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (i >= nv) break;
+                    if (in) store_out<DT>(p.out, o, __uint_as_float(cur[i]));
+                    o += p.ld_out;
+                }
+                if (more) {
+                    tmem_wait16(nxt);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) cur[i] = nxt[i];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[acc]);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kMx4TmemCols);
+    }
+}
+
+int mx4_stage_bytes(int nt) {
+    const int bytes = kMx4ABytes + nt * 128 + 1024 + ((nt + 127) / 128) * 1024;
+    return (bytes + 1023) & ~1023;
+}
+
+int mx4_table_bytes(int G) { return (3 * (G + 1) * 4 + 15) & ~15; }
+
+}  // namespace
+
+void mx4_tiles(int M, int N, int G, int* nt, int* b_box) {
+    // one group: equal tiles; several: room for about twice the mean
+    int n;
+    if (G == 1) {
+        const int tiles = (N + kMx4NtMax - 1) / kMx4NtMax;
+        n = (N + tiles - 1) / tiles;
+    } else {
+        n = static_cast<int>((2 * static_cast<int64_t>(N) + G - 1) / G);
+    }
+    n = n > kMx4NtMax ? kMx4NtMax : (n < 16 ? 16 : n);
+    *b_box = n > 64 ? 32 : 16;
+    *nt = (n + *b_box - 1) / *b_box * *b_box;
+    (void)M;
+}
+
+cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
+    Mx4Params p = in;
+    if (p.M < 1 || p.N < 1 || p.K < 128 || p.K % 128 || p.G < 1 || p.G > kMx4MaxGroups) return cudaErrorInvalidValue;
+    if (p.nt < 16 || p.nt > kMx4NtMax || p.nt % p.b_box) return cudaErrorInvalidValue;
+    p.stage_bytes = mx4_stage_bytes(p.nt);
+    const int fixed = 1024 + kMx4BarBytes + mx4_table_bytes(p.G);
+    p.stages = (kSmemLimit - fixed) / p.stage_bytes;
+    if (p.stages > kMx4MaxStages) p.stages = kMx4MaxStages;
+    if (p.stages < 2) return cudaErrorInvalidValue;
+    const size_t smem = fixed + static_cast<size_t>(p.stages) * p.stage_bytes;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    const int64_t m_tiles = (p.M + kMx4BlockM - 1) / kMx4BlockM;
+    const int64_t most = m_tiles * ((p.N + p.nt - 1) / p.nt + p.G - 1);
+    const int grid = static_cast<int>(most < sms ? most : sms);
+    auto run = [&](void (*kern)(Mx4Params)) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+        if (e != cudaSuccess) return e;
+        kern<<<grid, kMx4Threads, smem, s>>>(p);
+        return cudaGetLastError();
+    };
+    if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32>);
+    if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16>);
+    return run(mx4_gemm_kernel<ELEM_F16>);
+}
+
+cudaError_t launch_mxfp4_quantize(const void* x, int64_t ld, int dt, int64_t rows, int64_t K, uint8_t* codes,
+                                  uint8_t* scales, cudaStream_t s) {
+    if (rows < 0 || K <= 0 || K % 32) return cudaErrorInvalidValue;
+    if (rows == 0) return cudaSuccess;
+    const bool v8 = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
+    const int64_t n = rows * (K / (v8 ? 8 : 1));
+    const int64_t blocks = (n + 255) / 256;
+    const unsigned grid = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
+    if (v8) mxfp4_quantize_kernel<8><<<grid, 256, 0, s>>>(x, ld, dt, rows, K, codes, scales);
+    else mxfp4_quantize_kernel<1><<<grid, 256, 0, s>>>(x, ld, dt, rows, K, codes, scales);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x,
+                                int64_t ld, int dt, cudaStream_t s) {
+    if (rows < 0 || K <= 0 || K % 32) return cudaErrorInvalidValue;
+    if (rows == 0) return cudaSuccess;
+    const bool v8 = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
+    const int64_t blocks = (rows * (K / 8) + 255) / 256;
+    const unsigned grid = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
+    if (v8) mxfp4_decode_kernel<8><<<grid, 256, 0, s>>>(codes, scales, rows, K, x, ld, dt);
+    else mxfp4_decode_kernel<1><<<grid, 256, 0, s>>>(codes, scales, rows, K, x, ld, dt);
+    return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -170,6 +170,18 @@ __device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t adesc, uint64
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// D[tmem] (+)= A[smem] * B[smem]^T, both E2M1 (two a byte), per-32 E8M0 scales
+// from TMEM: K = 64 an instruction.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
 // Copy a 32-row x 128-bit block from shared memory into 4 TMEM columns of
 // all four 32-lane quarters.
 __device__ __forceinline__ void tc_cp_32x128b_x4(uint32_t taddr, uint64_t sdesc) {
@@ -246,6 +258,18 @@ __host__ __device__ __forceinline__ uint32_t idesc_mxf8f6f4(int M, int N, int a_
     d |= 1u << 23;                                          // scale type E8M0
     d |= static_cast<uint32_t>((M >> 4) & 31) << 24;
     d |= static_cast<uint32_t>(sfa_id & 3) << 29;
+    return d;
+}
+
+// Instruction descriptor for kind::mxf4 with E8M0 block scales: A and B E2M1,
+// K-major; the scale ids (0 or 2) select the 16-bit half of each scale word.
+__host__ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N) {
+    uint32_t d = 0;
+    d |= 1u << 7;                                           // A: E2M1
+    d |= 1u << 10;                                          // B: E2M1
+    d |= static_cast<uint32_t>((N >> 3) & 63) << 17;
+    d |= 1u << 23;                                          // scale type E8M0
+    d |= static_cast<uint32_t>((M >> 4) & 31) << 24;
     return d;
 }
 
