@@ -292,13 +292,15 @@ class Plan:
         x = x.contiguous()
         T, D = x.shape
         a = block._BlockArgs()
-        gate, a.gate_kind = block._gate(gate, gate_per, T, D, x.device, what)
-        a.w_dtype = block._norm_weights(what, x.device, D, w_post, w_pre, gate)
+        dev = x.get_device()
+        gate, a.gate_kind = block._gate(gate, gate_per, T, D, dev, what)
+        a.w_dtype = block._norm_weights(what, dev, D, w_post, w_pre, gate)
         if next_w_pre is not None:
-            block._require(need_next_u and block.DTYPES.get(next_w_pre.dtype) == a.w_dtype
-                           or (need_next_u and w_post is None and w_pre is None and gate is None),
-                           "forward_block: next_w_pre goes with need_next_u and has the other weights' type")
-            a.w_dtype = block._norm_weights(what, x.device, D, next_w_pre, None, None)
+            block._require(need_next_u, "forward_block: next_w_pre goes with need_next_u")
+            kind = block._norm_weights(what, dev, D, next_w_pre, None, None)
+            block._require(kind == a.w_dtype or (w_post is None and w_pre is None and gate is None),
+                           "forward_block: next_w_pre has the other weights' type")
+            a.w_dtype = kind
         if u is not None:
             block._require(u.dtype == torch.bfloat16 and u.shape == x.shape and u.device == x.device and u.is_contiguous(),
                            "forward_block: u is the previous call's next_u")

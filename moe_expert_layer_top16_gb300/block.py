@@ -12,7 +12,6 @@ Gradients are calls of their own; nothing is recorded for autograd.
 from __future__ import annotations
 
 import ctypes as C
-import functools
 from typing import Optional
 
 import torch
@@ -70,74 +69,91 @@ def declare(L):
     L.moe_block_norm_workspace_bytes.argtypes = [i32, i32]
 
 
+def _bad(what):
+    raise MoeError(MOE_ERR_INVALID_ARG, what)
+
+
 def _require(ok, what):
     if not ok:
-        raise MoeError(MOE_ERR_INVALID_ARG, what)
+        _bad(what)
 
 
-def _on_device(f):
-    """Run with the device of the first tensor among the positional arguments current."""
-    @functools.wraps(f)
-    def call(*args, **kwargs):
-        first = next((t for t in args if isinstance(t, torch.Tensor)), None)
-        _require(first is not None and first.is_cuda, f"{f.__name__}: CUDA tensors are needed")
-        if first.device.index == torch.cuda.current_device():
-            return f(*args, **kwargs)
-        with torch.cuda.device(first.device):
-            return f(*args, **kwargs)
-    return call
+# The current stream's handle without building a Stream object (2.8 us a call
+# on the host of a GB300), where this PyTorch has that shortcut.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = torch.cuda.current_device
 
 
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _device(t, what):
+    """Index of the CUDA device that tensor `t` is on."""
+    if not isinstance(t, torch.Tensor):
+        _bad(what + ": CUDA tensors are needed")
+    dev = t.get_device()
+    if dev < 0:
+        _bad(what + ": CUDA tensors are needed")
+    return dev
 
 
-def _same_device(dev, what, *tensors):
-    for t in tensors:
-        if t is not None:
-            _require(t.device == dev, f"{what}: all tensors on one device")
+def _call(entry, name, dev, stream, *args):
+    """The entry point with `args` and the stream, on device `dev`."""
+    if dev == _current_device():
+        code = entry(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = entry(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code != 0:
+        _check(code, name)
 
 
-def _rows(t, what, dtypes=DTYPES):
-    """t [..., D] as rows: (2-D tensor whose rows are contiguous, row stride in elements)."""
-    _require(t.dim() >= 1 and t.dtype in dtypes, f"{what}: bad shape or type")
-    D = t.shape[-1]
-    if t.dim() != 2:
+def _rows(t, what):
+    """t [..., D] of a known type as rows: (2-D tensor whose rows are contiguous, row stride in elements)."""
+    if t.dtype not in DTYPES:
+        _bad(what + ": float32, bfloat16 or float16 is needed")
+    return _strided(t, what)
+
+
+def _strided(t, what):
+    if t.dim() == 2:
+        (T, D), (ld, unit) = t.shape, t.stride()
+        if unit == 1 and ld >= D and T > 1:
+            return t, ld
+    else:
+        _require(t.dim() >= 1, what + ": a matrix is needed")
+        D = t.shape[-1]
         t = t.reshape(-1, D) if D else t.reshape(0, 0)
-    T = t.shape[0]
+        T, (ld, unit) = t.shape[0], t.stride()
     if T <= 1 or D <= 1:
-        if not t.is_contiguous():
-            t = t.contiguous()
-        return t, D
-    if t.stride(1) != 1 or t.stride(0) < D:
-        t = t.contiguous()
-    return t, t.stride(0)
+        return t.contiguous(), D              # strides of single rows and columns say nothing
+    if unit != 1 or ld < D:
+        return t.contiguous(), D
+    return t, ld
 
 
-def _out_rows(out, shape, dtype, dev, what):
-    """An output matrix: `out` (2-D, contiguous rows), or a new one."""
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev), shape[1]
-    _require(tuple(out.shape) == tuple(shape) and out.dtype == dtype and out.device == dev, f"{what}: bad output")
-    if out.numel() == 0 or shape[0] == 1:
-        _require(out.numel() == 0 or shape[1] == 1 or out.stride(1) == 1, f"{what}: output rows must be contiguous")
-        return out, shape[1]
-    _require((shape[1] == 1 or out.stride(1) == 1) and out.stride(0) >= shape[1],
-             f"{what}: output rows must be contiguous and apart")
-    return out, out.stride(0)
+def _out_rows(out, T, D, dtype, dev, what):
+    """Row stride of the output matrix `out`, which has to be [T][D] with contiguous rows."""
+    if out.dim() != 2 or out.shape[0] != T or out.shape[1] != D or out.dtype != dtype or out.get_device() != dev:
+        _bad(what + ": the output's shape, type or device")
+    ld, unit = out.stride()
+    if out.numel() == 0 or T == 1:
+        ld = D
+    elif ld < D:
+        _bad(what + ": output rows must lie apart")
+    if unit != 1 and D > 1 and out.numel():
+        _bad(what + ": output rows must be contiguous")
+    return ld
 
 
 def _slots(slot_pos, dev, what):
-    _require(slot_pos.dtype == torch.int32 and slot_pos.dim() == 2 and slot_pos.is_contiguous() and slot_pos.device == dev,
-             f"{what}: slot_pos is a contiguous int32 [T][k] on the same device")
+    if slot_pos.dtype != torch.int32 or slot_pos.dim() != 2 or not slot_pos.is_contiguous() or slot_pos.get_device() != dev:
+        _bad(what + ": slot_pos is a contiguous int32 [T][k] on the same device")
     return slot_pos.shape
 
 
 def _weights_of(weights, slot_pos, what):
     if weights is None:
         return None
-    _require(weights.dtype == torch.float32 and weights.shape == slot_pos.shape and weights.device == slot_pos.device,
-             f"{what}: weights are float32 [T][k] on the same device")
+    if weights.dtype != torch.float32 or weights.shape != slot_pos.shape or weights.get_device() != slot_pos.get_device():
+        _bad(what + ": weights are float32 [T][k] on the same device")
     return weights.contiguous()
 
 
@@ -146,52 +162,68 @@ def _p(t):
 
 
 # ------------------------------------------------------------------ tokens by expert and back
-@_on_device
 def sort_by_expert(idx: torch.Tensor, n_experts: int, stream=None):
     """Sort the (token, slot) pairs of idx int32 [T][k] by expert (see
     moe_sort): (offsets int32 [E + 1], sorted_slot int32 [T * k], slot_pos
     int32 [T][k]).  Entries outside [0, n_experts) are dropped (-1)."""
-    _require(idx.dtype == torch.int32 and idx.dim() == 2, "sort_by_expert: idx is int32 [T][k]")
+    dev = _device(idx, "sort_by_expert")
+    if idx.dtype != torch.int32 or idx.dim() != 2:
+        _bad("sort_by_expert: idx is int32 [T][k]")
+    E = int(n_experts)
+    if not 1 <= E <= 1024:
+        _bad("sort_by_expert: 1 <= n_experts <= 1024")
     idx = idx.contiguous()
     T, k = idx.shape
-    _require(1 <= int(n_experts) <= 1024, "sort_by_expert: 1 <= n_experts <= 1024")
-    tables = torch.empty(2 * T * k + int(n_experts) + 1, dtype=torch.int32, device=idx.device)
-    slot_pos, sorted_slot, offsets = tables[:T * k].view(T, k), tables[T * k:2 * T * k], tables[2 * T * k:]
-    _check(lib().moe_sort(_p(idx), T, k, int(n_experts), _p(offsets), _p(sorted_slot), _p(slot_pos), _stream(stream)),
-           "moe_sort")
+    where = idx.device
+    slot_pos = torch.empty((T, k), dtype=torch.int32, device=where)
+    sorted_slot = torch.empty(T * k, dtype=torch.int32, device=where)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=where)
+    _call(lib().moe_sort, "moe_sort", dev, stream, idx.data_ptr(), T, k, E, offsets.data_ptr(), sorted_slot.data_ptr(),
+          slot_pos.data_ptr())
     return offsets, sorted_slot, slot_pos
 
 
-@_on_device
 def permute(x: torch.Tensor, slot_pos: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rows[slot_pos[t, j]] = x[t] (see moe_permute).  x [T][D] of any type
     (codes and scales too); out [n][D], by default T * k new rows, whose places
     that no slot names are not initialised."""
-    T, k = _slots(slot_pos, x.device, "permute")
-    _require(x.dim() == 2 and x.shape[0] == T and x.shape[1] >= 1, "permute: x is [T][D]")
-    x, ld = _rows(x, "permute", (x.dtype,))
+    dev = _device(x, "permute")
+    T, k = _slots(slot_pos, dev, "permute")
+    if x.dim() != 2 or x.shape[0] != T or x.shape[1] < 1:
+        _bad("permute: x is [T][D]")
+    x, ld = _strided(x, "permute")
     D, size = x.shape[1], x.element_size()
-    rows, ld_rows = _out_rows(out, (T * k if out is None else out.shape[0], D), x.dtype, x.device, "permute")
-    _check(lib().moe_permute(_p(x), ld * size, D * size, T, k, _p(slot_pos), rows.shape[0], _p(rows), ld_rows * size,
-                             _stream(stream)), "moe_permute")
-    return rows
+    if out is None:
+        n, ld_rows = T * k, D
+        out = torch.empty((n, D), dtype=x.dtype, device=x.device)
+    else:
+        n = out.shape[0] if out.dim() == 2 else -1
+        ld_rows = _out_rows(out, n, D, x.dtype, dev, "permute")
+    _call(lib().moe_permute, "moe_permute", dev, stream, x.data_ptr(), ld * size, D * size, T, k, slot_pos.data_ptr(), n,
+          out.data_ptr(), ld_rows * size)
+    return out
 
 
-@_on_device
 def unpermute(rows: torch.Tensor, slot_pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
               out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] rows[slot_pos[t, j]] (see moe_unpermute); y [T][D] of out_dtype (default: rows')."""
-    T, k = _slots(slot_pos, rows.device, "unpermute")
-    _require(rows.dim() == 2 and rows.shape[1] >= 1, "unpermute: rows is [n][D]")
+    dev = _device(rows, "unpermute")
+    T, k = _slots(slot_pos, dev, "unpermute")
+    if rows.dim() != 2 or rows.shape[1] < 1:
+        _bad("unpermute: rows is [n][D]")
     rows, ld = _rows(rows, "unpermute")
-    D = rows.shape[1]
+    n, D = rows.shape
     w = _weights_of(weights, slot_pos, "unpermute")
     dtype = out_dtype or (rows.dtype if out is None else out.dtype)
-    _require(dtype in DTYPES, "unpermute: output type")
-    y, ld_y = _out_rows(out, (T, D), dtype, rows.device, "unpermute")
-    _check(lib().moe_unpermute(_p(rows), ld, DTYPES[rows.dtype], rows.shape[0], _p(slot_pos), _p(w), T, k, D, _p(y), ld_y,
-                               DTYPES[dtype], _stream(stream)), "moe_unpermute")
-    return y
+    if dtype not in DTYPES:
+        _bad("unpermute: output type")
+    if out is None:
+        out, ld_y = torch.empty((T, D), dtype=dtype, device=rows.device), D
+    else:
+        ld_y = _out_rows(out, T, D, dtype, dev, "unpermute")
+    _call(lib().moe_unpermute, "moe_unpermute", dev, stream, rows.data_ptr(), ld, DTYPES[rows.dtype], n,
+          slot_pos.data_ptr(), _p(w), T, k, D, out.data_ptr(), ld_y, DTYPES[dtype])
+    return out
 
 
 def permute_backward(d_rows: torch.Tensor, slot_pos: torch.Tensor, out_dtype: Optional[torch.dtype] = None,
@@ -200,58 +232,87 @@ def permute_backward(d_rows: torch.Tensor, slot_pos: torch.Tensor, out_dtype: Op
     return unpermute(d_rows, slot_pos, None, out_dtype, out, stream)
 
 
-@_on_device
 def unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, slot_pos: torch.Tensor,
                        weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                        need_rows: bool = True, need_weights: bool = True, stream=None):
     """Gradients of unpermute (see moe_unpermute_backward): (d_rows like rows,
     or None; d_weights float32 [T][k], or None).  out: where d_rows goes; a new
     one's places that no slot names are not initialised."""
-    T, k = _slots(slot_pos, dy.device, "unpermute_backward")
-    _require(dy.dim() == 2 and dy.shape[0] == T and dy.shape[1] >= 1 and rows.dim() == 2 and rows.shape[1] == dy.shape[1],
-             "unpermute_backward: dy is [T][D], rows is [n][D]")
-    _same_device(dy.device, "unpermute_backward", rows)
+    dev = _device(dy, "unpermute_backward")
+    T, k = _slots(slot_pos, dev, "unpermute_backward")
+    if dy.dim() != 2 or dy.shape[0] != T or dy.shape[1] < 1 or rows.dim() != 2 or rows.shape[1] != dy.shape[1] \
+            or rows.get_device() != dev:
+        _bad("unpermute_backward: dy is [T][D], rows is [n][D] on the same device")
     dy, ld_dy = _rows(dy, "unpermute_backward")
     rows, ld = _rows(rows, "unpermute_backward")
-    D = dy.shape[1]
+    n, D = rows.shape
     w = _weights_of(weights, slot_pos, "unpermute_backward")
-    d_rows, ld_d = (_out_rows(out, tuple(rows.shape), rows.dtype, rows.device, "unpermute_backward")
-                    if need_rows else (None, 0))
-    d_w = torch.empty(T, k, dtype=torch.float32, device=dy.device) if need_weights else None
-    _check(lib().moe_unpermute_backward(_p(dy), ld_dy, DTYPES[dy.dtype], _p(rows), ld, DTYPES[rows.dtype], rows.shape[0],
-                                        _p(slot_pos), _p(w), T, k, D, _p(d_rows), ld_d, _p(d_w), _stream(stream)),
-           "moe_unpermute_backward")
-    return d_rows, d_w
+    ld_d = D
+    if not need_rows:
+        out = None
+    elif out is None:
+        out = torch.empty((n, D), dtype=rows.dtype, device=rows.device)
+    else:
+        ld_d = _out_rows(out, n, D, rows.dtype, dev, "unpermute_backward")
+    d_w = torch.empty((T, k), dtype=torch.float32, device=rows.device) if need_weights else None
+    _call(lib().moe_unpermute_backward, "moe_unpermute_backward", dev, stream, dy.data_ptr(), ld_dy, DTYPES[dy.dtype],
+          rows.data_ptr(), ld, DTYPES[rows.dtype], n, slot_pos.data_ptr(), _p(w), T, k, D, _p(out), ld_d, _p(d_w))
+    return out, d_w
 
 
 # ------------------------------------------------------------------ norms round a block
 def _gate(gate, gate_per, T, D, dev, what):
     """(contiguous gate, kind): gate [D] or [T], told apart by gate_per or, where T != D, by its length."""
     if gate is None:
-        _require(gate_per in (None, "none"), f"{what}: gate_per without a gate")
+        if gate_per not in (None, "none"):
+            _bad(what + ": gate_per without a gate")
         return None, GATE_NONE
-    _require(gate_per in (None, "channel", "token") and gate.device == dev, f"{what}: gate_per is 'channel' or 'token'")
     n = gate.numel()
     if gate_per is None:
-        _require(T != D and n in (T, D), f"{what}: the gate is [D] or [T]; gate_per says which where both fit")
+        if T == D or n not in (T, D):
+            _bad(what + ": the gate is [D] or [T]; gate_per says which where both fit")
         gate_per = "channel" if n == D else "token"
-    _require(n == (D if gate_per == "channel" else T), f"{what}: the gate's length")
-    return gate.reshape(-1).contiguous(), GATES[gate_per]
+    if gate_per not in ("channel", "token") or gate.get_device() != dev or n != (D if gate_per == "channel" else T):
+        _bad(what + ": gate_per is 'channel' ([D]) or 'token' ([T]), on the same device")
+    if gate.dim() != 1:
+        gate = gate.reshape(-1)
+    return gate.contiguous(), GATES[gate_per]
 
 
 def _norm_weights(what, dev, D, w_post, w_pre, gate):
-    """The weights' common type code; each weight contiguous [D]."""
-    given = [w for w in (w_post, w_pre, gate) if w is not None]
-    if not given:
+    """The code of the weights' common type; each norm weight is a contiguous [D]."""
+    kind = None
+    for w in (w_post, w_pre):
+        if w is not None:
+            if w.dim() != 1 or w.shape[0] != D or not w.is_contiguous():
+                _bad(what + ": norm weights are contiguous [D]")
+            if w.get_device() != dev or (kind is not None and w.dtype != kind):
+                _bad(what + ": weights and gate of one type on the same device")
+            kind = w.dtype
+    if gate is not None:
+        if gate.get_device() != dev or (kind is not None and gate.dtype != kind):
+            _bad(what + ": weights and gate of one type on the same device")
+        kind = gate.dtype
+    if kind is None:
         return 0
-    _require(all(w.dtype == given[0].dtype and w.device == dev for w in given) and given[0].dtype in DTYPES,
-             f"{what}: weights and gate of one type on the same device")
-    _require(all(w is None or (w.dim() == 1 and w.shape[0] == D and w.is_contiguous()) for w in (w_post, w_pre)),
-             f"{what}: norm weights are contiguous [D]")
-    return DTYPES[given[0].dtype]
+    if kind not in DTYPES:
+        _bad(what + ": float32, bfloat16 or float16 weights are needed")
+    return DTYPES[kind]
 
 
-@_on_device
+def _out_like(out, shape, T, dtype, dev, what):
+    """Row stride of `out`, which has to be of `shape` with evenly spaced, contiguous rows, and its rows."""
+    if out.shape != shape:
+        _bad(what + ": the output's shape, type or device")
+    r = out
+    if out.dim() != 2:
+        try:
+            r = out.view(T, shape[-1])
+        except RuntimeError:
+            _bad(what + ": output rows must be evenly spaced")
+    return _out_rows(r, T, shape[-1], dtype, dev, what)
+
+
 def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Optional[torch.Tensor] = None,
                w_pre: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, gate_per: Optional[str] = None,
                res_scale: float = 1.0, eps: float = 1e-6, u_dtype: Optional[torch.dtype] = None, need_u: bool = True,
@@ -262,56 +323,50 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Opt
     out_h (which may be x) and out_u take the results; they are [..., D] with
     contiguous rows."""
     what = "block_norm"
-    _require(x.dim() >= 1 and x.shape[-1] >= 1, "block_norm: x is [..., D]")
-    _same_device(x.device, what, y, out_h, out_u)
-    shape, D = x.shape, x.shape[-1]
-    _require(y is None or y.shape == shape, "block_norm: y has x's shape")
-    _require(y is not None or need_u, "block_norm: nothing to compute")
+    dev = _device(x, what)
+    shape = x.shape
+    if not shape or shape[-1] < 1:
+        _bad("block_norm: x is [..., D]")
+    D = shape[-1]
     xr, ld_x = _rows(x, what)
     T = xr.shape[0]
-    a = _BlockNormArgs()
-    a.T, a.D, a.res_scale, a.eps = T, D, res_scale, eps
-    a.x, a.ld_x, a.x_dtype = _p(xr), ld_x, DTYPES[xr.dtype]
-    h = x
+    h, u = x, None
+    y_p = h_p = u_p = gate_p = None
+    ld_y = ld_h = ld_u = D
+    y_type = u_type = kind = 0
     if y is not None:
-        yr, a.ld_y = _rows(y, what)
-        a.y, a.y_dtype = _p(yr), DTYPES[yr.dtype]
-        h, hr, a.ld_h = _out_like(out_h, shape, T, x.dtype, x.device, what)
-        a.h = _p(hr)
-        gate, a.gate_kind = _gate(gate, gate_per, T, D, x.device, what)
-        a.w_post, a.gate = _p(w_post), _p(gate)
-    else:
-        _require(gate is None and w_post is None and out_h is None, "block_norm: gate, w_post and out_h go with y")
-    u = None
+        if y.shape != shape or y.get_device() != dev:
+            _bad("block_norm: y has x's shape and device")
+        yr, ld_y = _rows(y, what)
+        y_p, y_type = yr.data_ptr(), DTYPES[yr.dtype]
+        if out_h is None:
+            h = torch.empty(shape, dtype=x.dtype, device=x.device)
+        else:
+            h, ld_h = out_h, _out_like(out_h, shape, T, x.dtype, dev, what)
+        h_p = h.data_ptr()
+        gate, kind = _gate(gate, gate_per, T, D, dev, what)
+        gate_p = _p(gate)
+    elif gate is not None or w_post is not None or out_h is not None or not need_u:
+        _bad("block_norm: gate, w_post and out_h go with y")
     if need_u:
         dt = u_dtype or (x.dtype if out_u is None else out_u.dtype)
-        _require(dt in DTYPES, "block_norm: u_dtype")
-        u, ur, a.ld_u = _out_like(out_u, shape, T, dt, x.device, what)
-        a.u, a.u_dtype, a.w_pre = _p(ur), DTYPES[dt], _p(w_pre)
-    a.w_dtype = _norm_weights(what, x.device, D, w_post, w_pre if need_u else None, gate)
+        if dt not in DTYPES:
+            _bad("block_norm: u_dtype")
+        if out_u is None:
+            u = torch.empty(shape, dtype=dt, device=x.device)
+        else:
+            u, ld_u = out_u, _out_like(out_u, shape, T, dt, dev, what)
+        u_p, u_type = u.data_ptr(), DTYPES[dt]
+    else:
+        w_pre = None
+    w_type = _norm_weights(what, dev, D, w_post, w_pre, gate)
     if T:
-        _check(lib().moe_block_norm(C.byref(a), _stream(stream)), "moe_block_norm")
+        a = _BlockNormArgs(xr.data_ptr(), ld_x, y_p, ld_y, _p(w_post), _p(w_pre), gate_p, h_p, ld_h, u_p, ld_u, T, D,
+                           DTYPES[xr.dtype], y_type, u_type, w_type, kind, res_scale, eps)
+        _call(lib().moe_block_norm, "moe_block_norm", dev, stream, a)
     return h, u
 
 
-def _out_like(out, shape, T, dtype, dev, what):
-    """(tensor of `shape`, the same as rows, row stride)."""
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-        return out, out, shape[-1]
-    _require(out.shape == shape and out.dtype == dtype and out.device == dev, f"{what}: bad output")
-    if out.dim() == 2:
-        r = out
-    else:
-        try:
-            r = out.view(T, shape[-1])
-        except RuntimeError:
-            raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: output rows must be evenly spaced") from None
-    r, ld = _out_rows(r, (T, shape[-1]), dtype, dev, what)
-    return out, r, ld
-
-
-@_on_device
 def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], h: torch.Tensor,
                         y: Optional[torch.Tensor] = None, *, w_post: Optional[torch.Tensor] = None,
                         w_pre: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
@@ -323,95 +378,101 @@ def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], 
     float32; None for what the call does not have).  need_weights=False leaves
     the weights' and the gate's out."""
     what = "block_norm_backward"
-    shape, D, dev = h.shape, h.shape[-1] if h.dim() else 0, h.device
-    _require(D >= 1 and (dh is not None or du is not None), "block_norm_backward: dh or du, and h [..., D]")
+    dev = _device(h, what)
+    shape, where = h.shape, h.device
+    if not shape or shape[-1] < 1 or (dh is None and du is None):
+        _bad("block_norm_backward: dh or du, and h [..., D]")
+    D = shape[-1]
     for t in (dh, du, y):
-        _require(t is None or (t.shape == shape and t.device == dev), "block_norm_backward: dh, du and y have h's shape and device")
-    _require(dh is None or dh.dtype == h.dtype, "block_norm_backward: dh has h's type")
-    a = _BlockNormBackwardArgs()
-    hr, a.ld_h = _rows(h, what)
+        if t is not None and (t.shape != shape or t.get_device() != dev):
+            _bad("block_norm_backward: dh, du and y have h's shape and device")
+    if dh is not None and dh.dtype != h.dtype:
+        _bad("block_norm_backward: dh has h's type")
+    hr, ld_h = _rows(h, what)
     T = hr.shape[0]
-    a.h, a.x_dtype = _p(hr), DTYPES[hr.dtype]
-    a.T, a.D, a.res_scale, a.eps = T, D, res_scale, eps
+    dh_p = du_p = y_p = dy_p = gate_p = work_p = None
+    ld_dh = ld_du = ld_y = D
+    u_type = y_type = kind = size = 0
     if dh is not None:
-        dhr, a.ld_dh = _rows(dh, what)
-        a.dh = _p(dhr)
+        dhr, ld_dh = _rows(dh, what)
+        dh_p = dhr.data_ptr()
     if du is not None:
-        dur, a.ld_du = _rows(du, what)
-        a.du, a.u_dtype = _p(dur), DTYPES[dur.dtype]
-    got = dict.fromkeys(("dx", "dy", "dw_post", "dw_pre", "d_gate"))
-    got["dx"] = torch.empty(shape, dtype=h.dtype, device=dev)
-    a.dx, a.ld_dx = _p(got["dx"]), D
-    columns = 0
-    if y is not None:
-        yr, a.ld_y = _rows(y, what)
-        a.y, a.y_dtype = _p(yr), DTYPES[yr.dtype]
-        got["dy"] = torch.empty(shape, dtype=y.dtype, device=dev)
-        a.dy, a.ld_dy = _p(got["dy"]), D
-        gate, a.gate_kind = _gate(gate, gate_per, T, D, dev, what)
-        a.w_post, a.gate = _p(w_post), _p(gate)
+        dur, ld_du = _rows(du, what)
+        du_p, u_type = dur.data_ptr(), DTYPES[dur.dtype]
     else:
-        _require(gate is None and w_post is None, "block_norm_backward: gate and w_post go with y")
-    if du is None:
         w_pre = None
-    a.w_pre = _p(w_pre)
-    a.w_dtype = _norm_weights(what, dev, D, w_post, w_pre, gate)
+    dx = torch.empty(shape, dtype=h.dtype, device=where)
+    dy = None
+    if y is not None:
+        yr, ld_y = _rows(y, what)
+        y_p, y_type = yr.data_ptr(), DTYPES[yr.dtype]
+        dy = torch.empty(shape, dtype=y.dtype, device=where)
+        dy_p = dy.data_ptr()
+        gate, kind = _gate(gate, gate_per, T, D, dev, what)
+        gate_p = _p(gate)
+    elif gate is not None or w_post is not None:
+        _bad("block_norm_backward: gate and w_post go with y")
+    w_type = _norm_weights(what, dev, D, w_post, w_pre, gate)
+    dw_post = dw_pre = d_gate = None
     if need_weights:
-        # the column sums: weights' gradients exist for norms without weights
-        # too (of the ones that they stand for), but only given ones are asked for
-        names = [n for n, t in (("dw_post", w_post), ("dw_pre", w_pre),
-                                ("d_gate", gate if a.gate_kind == GATE_CHANNEL else None)) if t is not None]
-        columns = len(names)
-        out = torch.empty(columns, D, dtype=torch.float32, device=dev)
-        for n, t in zip(names, out):
-            got[n] = t
-            setattr(a, n, _p(t))
-        if a.gate_kind == GATE_TOKEN:
-            got["d_gate"] = torch.empty(T, dtype=torch.float32, device=dev)
-            a.d_gate = _p(got["d_gate"])
-    if columns and T:
-        size = lib().moe_block_norm_workspace_bytes(T, D)
-        work = torch.empty(size, dtype=torch.uint8, device=dev)
-        a.workspace, a.workspace_bytes = _p(work), size
-    _check(lib().moe_block_norm_backward(C.byref(a), _stream(stream)), "moe_block_norm_backward")
-    return got
+        columns = 0
+        if w_post is not None:
+            dw_post, columns = torch.empty(D, dtype=torch.float32, device=where), 1
+        if w_pre is not None:
+            dw_pre, columns = torch.empty(D, dtype=torch.float32, device=where), 1
+        if kind == GATE_CHANNEL:
+            d_gate, columns = torch.empty(D, dtype=torch.float32, device=where), 1
+        elif kind == GATE_TOKEN:
+            d_gate = torch.empty(T, dtype=torch.float32, device=where)
+        if columns and T:
+            size = lib().moe_block_norm_workspace_bytes(T, D)
+            work = torch.empty(size, dtype=torch.uint8, device=where)
+            work_p = work.data_ptr()
+    a = _BlockNormBackwardArgs(dh_p, ld_dh, du_p, ld_du, hr.data_ptr(), ld_h, y_p, ld_y, _p(w_post), _p(w_pre), gate_p,
+                               dx.data_ptr(), D, dy_p, D, _p(dw_post), _p(dw_pre), _p(d_gate), work_p, size, T, D,
+                               DTYPES[hr.dtype], y_type, u_type, w_type, kind, res_scale, eps)
+    _call(lib().moe_block_norm_backward, "moe_block_norm_backward", dev, stream, a)
+    return dict(dx=dx, dy=dy, dw_post=dw_post, dw_pre=dw_pre, d_gate=d_gate)
 
 
 # ------------------------------------------------------------------ four bits
-@_on_device
 def mxfp4_quantize(x: torch.Tensor, stream=None):
     """MXFP4 of x [..., K] (float32, bfloat16 or float16; K a multiple of 32):
     (codes uint8 [..., K/2], scales uint8 [..., K/32]); see moe_mxfp4_quantize."""
-    _require(x.dim() >= 1 and x.shape[-1] >= 32 and x.shape[-1] % 32 == 0, "mxfp4_quantize: K is a multiple of 32")
+    dev = _device(x, "mxfp4_quantize")
+    shape = x.shape
+    if not shape or shape[-1] < 32 or shape[-1] % 32:
+        _bad("mxfp4_quantize: K is a multiple of 32")
+    K = shape[-1]
     xr, ld = _rows(x, "mxfp4_quantize")
-    K = x.shape[-1]
-    codes = torch.empty(*x.shape[:-1], K // 2, dtype=torch.uint8, device=x.device)
-    scales = torch.empty(*x.shape[:-1], K // 32, dtype=torch.uint8, device=x.device)
-    _check(lib().moe_mxfp4_quantize(_p(xr), ld, DTYPES[xr.dtype], xr.shape[0], K, _p(codes), _p(scales), _stream(stream)),
-           "moe_mxfp4_quantize")
+    codes = torch.empty(shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(shape[:-1] + (K // 32,), dtype=torch.uint8, device=x.device)
+    _call(lib().moe_mxfp4_quantize, "moe_mxfp4_quantize", dev, stream, xr.data_ptr(), ld, DTYPES[xr.dtype], xr.shape[0], K,
+          codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
 def _mx4(codes, scales, what):
-    _require(codes.dtype == torch.uint8 and scales.dtype == torch.uint8 and codes.dim() == scales.dim() >= 1
-             and codes.shape[:-1] == scales.shape[:-1] and codes.shape[-1] == 16 * scales.shape[-1] >= 16
-             and codes.device == scales.device, f"{what}: codes uint8 [..., K/2] and scales uint8 [..., K/32]")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.shape or not scales.shape \
+            or codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != 16 * scales.shape[-1] \
+            or codes.shape[-1] < 16 or codes.get_device() != scales.get_device():
+        _bad(what + ": codes uint8 [..., K/2] and scales uint8 [..., K/32] of one device")
     return codes.contiguous(), scales.contiguous()
 
 
-@_on_device
 def mxfp4_decode(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """The values [..., K] that MXFP4 codes and scales stand for, rounded to `dtype`."""
+    dev = _device(codes, "mxfp4_decode")
     codes, scales = _mx4(codes, scales, "mxfp4_decode")
-    _require(dtype in DTYPES, "mxfp4_decode: output type")
+    if dtype not in DTYPES:
+        _bad("mxfp4_decode: output type")
     K = codes.shape[-1] * 2
-    x = torch.empty(*codes.shape[:-1], K, dtype=dtype, device=codes.device)
-    _check(lib().moe_mxfp4_decode(_p(codes), _p(scales), x.numel() // K, K, _p(x), K, DTYPES[dtype], _stream(stream)),
-           "moe_mxfp4_decode")
+    x = torch.empty(codes.shape[:-1] + (K,), dtype=dtype, device=codes.device)
+    _call(lib().moe_mxfp4_decode, "moe_mxfp4_decode", dev, stream, codes.data_ptr(), scales.data_ptr(), x.numel() // K, K,
+          x.data_ptr(), K, DTYPES[dtype])
     return x
 
 
-@_on_device
 def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tensor, b_scales: torch.Tensor,
              offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
              out_dtype: Optional[torch.dtype] = None, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -420,22 +481,30 @@ def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tenso
     int32 [G + 1] on the device, rows offsets[g] to offsets[g + 1] of B times
     A[g].  Rows that belong to no group are left as they were."""
     what = "mx4_gemm"
+    dev = _device(a_codes, what)
     a_codes, a_scales = _mx4(a_codes, a_scales, what)
     b_codes, b_scales = _mx4(b_codes, b_scales, what)
-    _same_device(a_codes.device, what, b_codes, offsets, out, status)
-    _require(b_codes.dim() == 2 and b_codes.shape[1] == a_codes.shape[-1], "mx4_gemm: B is [N][K] of A's K")
+    if b_codes.dim() != 2 or b_codes.shape[1] != a_codes.shape[-1] or b_codes.get_device() != dev:
+        _bad("mx4_gemm: B is [N][K] of A's K, on A's device")
     if offsets is None:
-        _require(a_codes.dim() == 2, "mx4_gemm: one matrix [M][K] without offsets")
+        if a_codes.dim() != 2:
+            _bad("mx4_gemm: one matrix [M][K] without offsets")
         G, M = 1, a_codes.shape[0]
     else:
-        _require(a_codes.dim() == 3 and offsets.dtype == torch.int32 and offsets.is_contiguous()
-                 and offsets.numel() == a_codes.shape[0] + 1, "mx4_gemm: A is [G][M][K], offsets int32 [G + 1]")
-        G, M = a_codes.shape[:2]
-    _require(status is None or (status.dtype == torch.int32 and status.numel() >= 1), "mx4_gemm: status is int32")
+        if a_codes.dim() != 3 or offsets.dtype != torch.int32 or not offsets.is_contiguous() \
+                or offsets.numel() != a_codes.shape[0] + 1 or offsets.get_device() != dev:
+            _bad("mx4_gemm: A is [G][M][K], offsets int32 [G + 1] on its device")
+        G, M, _ = a_codes.shape
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev):
+        _bad("mx4_gemm: status is int32 on A's device")
     N, K = b_codes.shape[0], 2 * b_codes.shape[1]
     dtype = out_dtype or (torch.float32 if out is None else out.dtype)
-    _require(dtype in DTYPES, "mx4_gemm: output type")
-    out, ld = _out_rows(out, (N, M), dtype, a_codes.device, what)
-    _check(lib().moe_mx4_gemm(_p(a_codes), _p(a_scales), G, M, _p(b_codes), _p(b_scales), N, K, _p(offsets), _p(out), ld,
-                              DTYPES[dtype], _p(status), _stream(stream)), "moe_mx4_gemm")
+    if dtype not in DTYPES:
+        _bad("mx4_gemm: output type")
+    if out is None:
+        out, ld = torch.empty((N, M), dtype=dtype, device=a_codes.device), M
+    else:
+        ld = _out_rows(out, N, M, dtype, dev, what)
+    _call(lib().moe_mx4_gemm, "moe_mx4_gemm", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), G, M,
+          b_codes.data_ptr(), b_scales.data_ptr(), N, K, _p(offsets), out.data_ptr(), ld, DTYPES[dtype], _p(status))
     return out

@@ -315,9 +315,11 @@ cudaError_t launch_sort(const int32_t* idx, int64_t n, int E, int32_t* offsets, 
     while (W < kSortMaxWarps && static_cast<int64_t>(W) * C < steps) W *= 2;
     const size_t smem = sizeof(int32_t) * (static_cast<size_t>(W) + 2) * E;
     static_assert(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE <= kSmemLimit, "sort tables");
-    cudaError_t err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE));
-    if (err != cudaSuccess) return err;
+    if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE));
+        if (err != cudaSuccess) return err;
+    }
     return launch_ex_cluster(sort_kernel, dim3(C), dim3(W * 32), smem, s, false, C, idx, n, E, offsets, sorted_slot,
                              slot_pos, C);
 }

@@ -137,7 +137,7 @@ def test_binding_refuses_what_it_can_see():
         with pytest.raises(moe.MoeError) as e:
             f()
         assert e.value.code == BAD
-    d = x.device
+    d = -1                                  # the device index of CPU tensors
     for gate, per, T, D in ((torch.zeros(4), None, 4, 4), (torch.zeros(5), None, 4, 6), (torch.zeros(4), "row", 4, 6),
                             (torch.zeros(4), "channel", 4, 6), (None, "token", 4, 6)):
         with pytest.raises(moe.MoeError):
@@ -149,4 +149,4 @@ def test_binding_refuses_what_it_can_see():
     with pytest.raises(moe.MoeError):
         block._mx4(c, s[:, :1], "x")
     with pytest.raises(moe.MoeError):
-        block._out_rows(torch.zeros(1, 8).expand(4, 8), (4, 8), torch.float32, d, "x")
+        block._out_rows(torch.zeros(1, 8).expand(4, 8), 4, 8, torch.float32, d, "x")
