@@ -322,7 +322,8 @@ cudaError_t launch_unpermute_backward(const void* dy, int64_t ld_dy, int dty, co
 // ------------------------------------------------------------------ norms round a block (norm.cu)
 enum NormGate : int { NORM_GATE_NONE = 0, NORM_GATE_CHANNEL = 1, NORM_GATE_TOKEN = 2 };
 constexpr int kNormMaxWidth = 16384;
-constexpr int kNormParts = 304;          // partial column sums of a backward pass at most
+constexpr int kNormParts = 304;
+int norm_parts(int64_t T, int D);        // blocks of a backward pass (rows of partial column sums) at most
 struct NormArgs {
     const void *x, *y, *w_post, *w_pre, *gate;
     void *h, *u;

@@ -56,90 +56,153 @@ __device__ __forceinline__ uint32_t mx4_scale_code(uint32_t top) {
 // Factor 2^-e for scale code c <= 252.
 __device__ __forceinline__ float mx4_inverse(uint32_t c) { return __uint_as_float((254u - c) << 23); }
 
-// V = 8: four lanes hold a block, 16-byte loads; V = 1: a warp holds a block.
-template <int V>
-__global__ void __launch_bounds__(256) mxfp4_quantize_kernel(const void* __restrict__ x, int64_t ld, int dt,
-                                                             int64_t rows, int64_t K, uint8_t* __restrict__ codes,
+// Where vector i of a matrix with per_row vectors a row starts: row and vector
+// in the row.  Contiguous rows are one long row.
+template <bool FLAT>
+__device__ __forceinline__ void row_of(int64_t i, int64_t per_row, bool small, int64_t& r, int64_t& c) {
+    if (FLAT) {
+        r = 0;
+        c = i;
+    } else if (small) {
+        const uint32_t q = static_cast<uint32_t>(i) / static_cast<uint32_t>(per_row);
+        r = q;
+        c = static_cast<uint32_t>(i) - q * static_cast<uint32_t>(per_row);
+    } else {
+        r = i / per_row;
+        c = i - r * per_row;
+    }
+}
+
+// Four lanes hold a block of 32, a lane 8 elements; kQuantBatch vectors of a
+// thread are loaded before the first is used.  Bound by HBM: 2.53 bytes move
+// for a 16-bit element.
+constexpr int kQuantBatch = 4;
+
+template <int DT, bool FLAT>
+__global__ void __launch_bounds__(256) mxfp4_quantize_kernel(const void* __restrict__ x, int64_t ld, int64_t n,
+                                                             int64_t per_row, uint8_t* __restrict__ codes,
                                                              uint8_t* __restrict__ scales) {
-    const int64_t per_row = K / V;
-    const int64_t n = rows * per_row;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    // whole warps iterate together: n is a multiple of a block's lanes
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31); i0 < n; i0 += stride) {
-        const int64_t i = i0 + (threadIdx.x & 31);
-        const bool in = i < n;
-        const int64_t r = in ? i / per_row : 0;
-        const int64_t c = in ? (i - r * per_row) * V : 0;
-        float v[V];
+    const bool small = n <= 0xffffffffll;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kQuantBatch) + threadIdx.x;
+    RawVec<8> raw[kQuantBatch];
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = 0.0f;
-        if (in) raw_to_f32(load_raw<V>(x, r * ld + c, dt), dt, v);
+    for (int u = 0; u < kQuantBatch; ++u) {
+        const int64_t i = i0 + 256 * u;
+        raw[u].a = raw[u].b = make_uint4(0, 0, 0, 0);
+        if (i < n) {
+            int64_t r, c;
+            row_of<FLAT>(i, per_row, small, r, c);
+            raw[u] = load_stream<8, DT>(x, r * ld + c * 8);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantBatch; ++u) {
+        const int64_t i = i0 + 256 * u;
+        float v[8];
+        raw_to_f32(raw[u], DT, v);
         uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = 1; o < 32 / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+        // n is a multiple of 4: a block's four lanes are all inside or all outside
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t sc = mx4_scale_code(top);
         const bool none = top == 0 || sc == 255u;
-        if (V == 8) {
-            const float f = none ? 0.0f : mx4_inverse(sc) * (dt == ELEM_F32 ? 1.0f : kTieDown);
-            uint32_t word = 0;
+        const float f = none ? 0.0f : mx4_inverse(sc) * (DT == ELEM_F32 ? 1.0f : kTieDown);
+        uint32_t word = 0;
 #pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                float lo = v[(2 * j) % V] * f, hi = v[(2 * j + 1) % V] * f;
-                if (dt == ELEM_F32) {
-                    lo = tie_down(lo);
-                    hi = tie_down(hi);
-                }
-                word |= e2m1_pair(lo, hi) << (8 * j);
+        for (int j = 0; j < 4; ++j) {
+            float lo = v[2 * j] * f, hi = v[2 * j + 1] * f;
+            if (DT == ELEM_F32) {
+                lo = tie_down(lo);
+                hi = tie_down(hi);
             }
-            if (in) {
-                *reinterpret_cast<uint32_t*>(codes + r * (K / 2) + c / 2) = none ? 0u : word;
-                if ((threadIdx.x & 3) == 0) scales[r * (K / 32) + c / 32] = static_cast<uint8_t>(sc);
-            }
-        } else {
-            const float f = tie_down(v[0] * (none ? 0.0f : mx4_inverse(sc)));
-            const float g = __shfl_down_sync(0xffffffffu, f, 1);
-            if (in) {
-                if (!(threadIdx.x & 1)) codes[r * (K / 2) + c / 2] = none ? 0 : static_cast<uint8_t>(e2m1_pair(f, g));
-                if ((threadIdx.x & 31) == 0) scales[r * (K / 32) + c / 32] = static_cast<uint8_t>(sc);
-            }
+            word |= e2m1_pair(lo, hi) << (8 * j);
+        }
+        if (i < n) {
+            // codes and scales are contiguous: vector i's follow from i alone
+            reinterpret_cast<uint32_t*>(codes)[i] = none ? 0u : word;
+            if ((threadIdx.x & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(sc);
         }
     }
 }
 
-// One thread per 8 codes.
-template <int V>
+// Rows off 16 bytes: a warp holds a block, a lane an element.
+__global__ void __launch_bounds__(256) mxfp4_quantize_plain_kernel(const void* __restrict__ x, int64_t ld, int dt,
+                                                                   int64_t n, int64_t K, uint8_t* __restrict__ codes,
+                                                                   uint8_t* __restrict__ scales) {
+    const bool small = n <= 0xffffffffll;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if ((i & ~31ll) >= n) return;              // whole warps: n is a multiple of 32
+    int64_t r, c;
+    row_of<false>(i, K, small, r, c);
+    float v[1];
+    raw_to_f32(load_raw<1>(x, r * ld + c, dt), dt, v);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[0]) & 0x7FFFFFFFu);
+    const uint32_t sc = mx4_scale_code(top);
+    const bool none = top == 0 || sc == 255u;
+    const float f = tie_down(v[0] * (none ? 0.0f : mx4_inverse(sc)));
+    const float g = __shfl_down_sync(0xffffffffu, f, 1);
+    if (!(threadIdx.x & 1)) codes[i >> 1] = none ? 0 : static_cast<uint8_t>(e2m1_pair(f, g));
+    if ((threadIdx.x & 31) == 0) scales[i >> 5] = static_cast<uint8_t>(sc);
+}
+
+// 2^e of a scale code: subnormal for code 0, NaN for 255.
+__device__ __forceinline__ float mx4_scale(uint32_t c) {
+    return __uint_as_float(c == 0 ? 0x00400000u : (c == 255u ? 0x7FC00000u : c << 23));
+}
+
+// Two codes of a byte as fp32 (the low nibble first).
+__device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 t;\n\t.reg .b16 w;\n\t"
+        "cvt.u16.u32 w, %1;\n\t"
+        "mov.b16 {t, _}, w;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+        : "=r"(h)
+        : "r"(byte));
+    __half2 v;
+    memcpy(&v, &h, 4);
+    return __half22float2(v);
+}
+
+// One thread per 8 codes, kQuantBatch of them in flight.
+template <int DT, bool FLAT, int V>
 __global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __restrict__ codes,
-                                                           const uint8_t* __restrict__ scales, int64_t rows, int64_t K,
-                                                           void* __restrict__ x, int64_t ld, int dt) {
-    const int64_t per_row = K / 8;
-    const int64_t n = rows * per_row;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * 8;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + r * (K / 2) + c / 2);
-        const uint32_t sc = scales[r * (K / 32) + c / 32];
-        // 2^e in two factors, each a normal number
-        const int e = static_cast<int>(sc) - 127;
-        const float f1 = exp2i(e / 2), f2 = exp2i(e - e / 2);
+                                                           const uint8_t* __restrict__ scales, int64_t n,
+                                                           int64_t per_row, void* __restrict__ x, int64_t ld) {
+    const bool small = n <= 0xffffffffll;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kQuantBatch) + threadIdx.x;
+    uint32_t w[kQuantBatch], sc[kQuantBatch];
+#pragma unroll
+    for (int u = 0; u < kQuantBatch; ++u) {
+        const int64_t i = i0 + 256 * u;
+        if (i < n) {
+            w[u] = __ldcs(reinterpret_cast<const uint32_t*>(codes) + i);
+            sc[u] = scales[i >> 2];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantBatch; ++u) {
+        const int64_t i = i0 + 256 * u;
+        if (i >= n) break;
+        const float f = mx4_scale(sc[u]);
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t q = (w >> (4 * j)) & 15u, m = q & 7u;
-            // 0, 1/2, then (1 + low bit / 2) 2^(m / 2 - 1)
-            const float a = m < 2 ? 0.5f * static_cast<float>(m)
-                                  : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-            const float s = a * f1 * f2;
-            v[j] = sc == 255u ? __uint_as_float(0x7FFFFFFFu) : (q & 8u ? -s : s);
+        for (int j = 0; j < 4; ++j) {
+            const float2 p = e2m1_values((w[u] >> (8 * j)) & 0xFFu);
+            v[2 * j] = p.x * f;
+            v[2 * j + 1] = p.y * f;
         }
+        int64_t r, c;
+        row_of<FLAT>(i, per_row, small, r, c);
         if (V == 8) {
-            store_vec(x, r * ld + c, dt, v);
+            store_stream<8, DT>(x, r * ld + c * 8, v);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float o[1] = {v[j]};
-                store_vec(x, r * ld + c + j, dt, o);
+                store_vec(x, r * ld + c * 8 + j, DT, o);
             }
         }
     }
@@ -559,16 +622,40 @@ cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
     return run(mx4_gemm_kernel<ELEM_F16>);
 }
 
+namespace {
+
+template <int DT>
+void quantize_as(const void* x, int64_t ld, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales, unsigned grid,
+                 cudaStream_t s) {
+    const int64_t n = rows * (K / 8);
+    if (ld == K || rows == 1) mxfp4_quantize_kernel<DT, true><<<grid, 256, 0, s>>>(x, ld, n, K / 8, codes, scales);
+    else mxfp4_quantize_kernel<DT, false><<<grid, 256, 0, s>>>(x, ld, n, K / 8, codes, scales);
+}
+
+template <int DT>
+void decode_as(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x, int64_t ld, bool v8,
+               unsigned grid, cudaStream_t s) {
+    const int64_t n = rows * (K / 8);
+    if (!v8) mxfp4_decode_kernel<DT, false, 1><<<grid, 256, 0, s>>>(codes, scales, n, K / 8, x, ld);
+    else if (ld == K || rows == 1) mxfp4_decode_kernel<DT, true, 8><<<grid, 256, 0, s>>>(codes, scales, n, K / 8, x, ld);
+    else mxfp4_decode_kernel<DT, false, 8><<<grid, 256, 0, s>>>(codes, scales, n, K / 8, x, ld);
+}
+
+}  // namespace
+
 cudaError_t launch_mxfp4_quantize(const void* x, int64_t ld, int dt, int64_t rows, int64_t K, uint8_t* codes,
                                   uint8_t* scales, cudaStream_t s) {
     if (rows < 0 || K <= 0 || K % 32) return cudaErrorInvalidValue;
     if (rows == 0) return cudaSuccess;
-    const bool v8 = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
-    const int64_t n = rows * (K / (v8 ? 8 : 1));
-    const int64_t blocks = (n + 255) / 256;
-    const unsigned grid = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
-    if (v8) mxfp4_quantize_kernel<8><<<grid, 256, 0, s>>>(x, ld, dt, rows, K, codes, scales);
-    else mxfp4_quantize_kernel<1><<<grid, 256, 0, s>>>(x, ld, dt, rows, K, codes, scales);
+    const bool v8 = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rows == 1 || (ld * elem_bytes(dt)) % 16 == 0);
+    const int64_t per_block = v8 ? 256 * kQuantBatch : 256;
+    const int64_t blocks = (rows * (K / (v8 ? 8 : 1)) + per_block - 1) / per_block;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (!v8) mxfp4_quantize_plain_kernel<<<grid, 256, 0, s>>>(x, ld, dt, rows * K, K, codes, scales);
+    else if (dt == ELEM_F32) quantize_as<ELEM_F32>(x, ld, rows, K, codes, scales, grid, s);
+    else if (dt == ELEM_BF16) quantize_as<ELEM_BF16>(x, ld, rows, K, codes, scales, grid, s);
+    else quantize_as<ELEM_F16>(x, ld, rows, K, codes, scales, grid, s);
     return cudaGetLastError();
 }
 
@@ -576,11 +663,13 @@ cudaError_t launch_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int
                                 int64_t ld, int dt, cudaStream_t s) {
     if (rows < 0 || K <= 0 || K % 32) return cudaErrorInvalidValue;
     if (rows == 0) return cudaSuccess;
-    const bool v8 = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
-    const int64_t blocks = (rows * (K / 8) + 255) / 256;
-    const unsigned grid = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
-    if (v8) mxfp4_decode_kernel<8><<<grid, 256, 0, s>>>(codes, scales, rows, K, x, ld, dt);
-    else mxfp4_decode_kernel<1><<<grid, 256, 0, s>>>(codes, scales, rows, K, x, ld, dt);
+    const bool v8 = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (rows == 1 || (ld * elem_bytes(dt)) % 16 == 0);
+    const int64_t blocks = (rows * (K / 8) + 256 * kQuantBatch - 1) / (256 * kQuantBatch);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (dt == ELEM_F32) decode_as<ELEM_F32>(codes, scales, rows, K, x, ld, v8, grid, s);
+    else if (dt == ELEM_BF16) decode_as<ELEM_BF16>(codes, scales, rows, K, x, ld, v8, grid, s);
+    else decode_as<ELEM_F16>(codes, scales, rows, K, x, ld, v8, grid, s);
     return cudaGetLastError();
 }
 

@@ -13,10 +13,11 @@
 //   dw_pre = sum_t du h^,  dw_post = sum_t total g y^,
 //   dg = sum total w_post y^  over t (channel) or over the row (token)
 //
-// Bound by HBM: every row of every matrix goes by once.  A CTA holds whole
-// rows in registers, so the two block-wide sums (of y^2, then of h^2) need no
-// second read.  All sums are fp32.
-#include <atomic>
+// Bound by HBM: every row of every matrix goes by once.  A row's windows wait
+// in shared memory (a ring that cp.async fills some rows ahead), so that the
+// sums over the row (of y^2, then of h^2) need no second read.  All sums are
+// fp32.
+#include <algorithm>
 
 #include "internal.h"
 #include "vec.cuh"
@@ -26,272 +27,610 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxWarps = 32;
+constexpr int kNormVec = 8;                  // elements of a window
+constexpr int kNormMaxStages = 8;
 
-// Block-wide sums of N values in a fixed order: lanes by butterfly, then the
-// warps' sums in warp order (every thread adds them itself).  `buf` alternates
-// between calls, so that one barrier a call is enough.
+// ------------------------------------------------------------------ rows by windows of 8 elements
+// A row is cut at the 8-element windows of its matrix (16 bytes of a 16-bit
+// type, 32 of fp32), not at its own start: for rows of any length the windows
+// inside a row are whole 16-byte words, and only its first and last window
+// may be partial.  All matrices of a launch have 16-byte aligned bases and row
+// strides that are equal modulo 8, so a row lies alike in all of them; a group
+// of threads takes every (8 m)-th row, so that its rows all start at the same
+// place in their first window and thread i owns the same columns in each.
+//
+// A row is owned by TPR threads; a block holds blockDim / TPR such groups.
+struct Rows {
+    int tpr, lane_in_group, group, groups;
+    int64_t first, step;        // rows first, first + step, ...
+    int shift;                  // elements of the first window that belong to the row before
+};
+
+__device__ __forceinline__ Rows rows_of(int tpr, int64_t ld) {
+    Rows r;
+    r.tpr = tpr;
+    r.groups = blockDim.x / tpr;
+    r.group = threadIdx.x / tpr;
+    r.lane_in_group = threadIdx.x - r.group * tpr;
+    r.first = static_cast<int64_t>(blockIdx.x) * r.groups + r.group;
+    r.step = static_cast<int64_t>(gridDim.x) * r.groups;
+    r.shift = static_cast<int>((r.first * ld) & (kNormVec - 1));
+    return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most n of this thread's copy groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    }
+}
+
+// One window of a row into this thread's own slots (a 16-byte slot, two for
+// fp32, `pitch` bytes apart): what a thread copies it alone reads, so that the
+// ring needs no barriers.  off: the window's first element in the matrix; c:
+// its column, negative in a first window that starts in the row before.
+__device__ __forceinline__ void fetch(uint8_t* slot, int pitch, const void* base, int64_t off, int c, int D, int dt) {
+    const uint8_t* src = static_cast<const uint8_t*>(base) + off * elem_bytes(dt);
+    if (c >= 0 && c + kNormVec <= D) {
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
+        cp_async16(dst, src);
+        if (dt == ELEM_F32) cp_async16(dst + pitch, src + 16);
+        return;
+    }
+#pragma unroll 1
+    for (int j = 0; j < kNormVec; ++j) {
+        if (c + j < 0 || c + j >= D) continue;       // left as they are: never used
+        if (dt == ELEM_F32)
+            reinterpret_cast<uint32_t*>(slot + (j >> 2) * pitch)[j & 3] = reinterpret_cast<const uint32_t*>(src)[j];
+        else
+            reinterpret_cast<uint16_t*>(slot)[j] = reinterpret_cast<const uint16_t*>(src)[j];
+    }
+}
+
+// The window's values, zero outside the row.
+__device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, int c, int D, float (&v)[8]) {
+    RawVec<8> r;
+    r.a = *reinterpret_cast<const uint4*>(slot);
+    r.b = dt == ELEM_F32 ? *reinterpret_cast<const uint4*>(slot + pitch) : make_uint4(0, 0, 0, 0);
+    raw_to_f32(r, dt, v);
+    if (c < 0 || c + kNormVec > D) {
+#pragma unroll
+        for (int j = 0; j < kNormVec; ++j) v[j] = (c + j >= 0 && c + j < D) ? v[j] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void put(void* base, int64_t off, int c, int D, int dt, const float (&v)[8]) {
+    if (c >= 0 && c + kNormVec <= D) {
+        store_vec(base, off, dt, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kNormVec; ++j) {
+        const float o[1] = {v[j]};
+        if (c + j >= 0 && c + j < D) store_vec(base, off + j, dt, o);
+    }
+}
+
+// A thread's weights wait in its own slots of shared memory, as fp32.
+__device__ __forceinline__ void keep(uint8_t* slot, int pitch, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(slot) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(slot + pitch) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void kept(const uint8_t* slot, int pitch, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(slot), b = *reinterpret_cast<const float4*>(slot + pitch);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// v *= the vector's columns c .. c + 7 (those inside the row).
+__device__ __forceinline__ void times_columns(float (&v)[8], const void* w, int c, int D, int dt) {
+#pragma unroll
+    for (int j = 0; j < kNormVec; ++j) {
+        float f[1] = {1.0f};
+        if (c + j >= 0 && c + j < D) raw_to_f32(load_raw<1>(w, c + j, dt), dt, f);
+        v[j] *= f[0];
+    }
+}
+
+// Sums of N values over a group's threads in a fixed order (butterflies in the
+// warps, then over the warps' sums).  `buf` alternates between calls, so that
+// one barrier a call is enough; a group of one warp needs none.
 template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float (*red)[N][kNormMaxWarps], int& buf) {
+__device__ __forceinline__ void group_sums(float (&v)[N], const Rows& g, float (*red)[N][kNormMaxWarps], int& buf) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0)
+    if (g.tpr == 32) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = g.tpr >> 5, warp0 = g.group * warps;
+    if (lane == 0)
 #pragma unroll
-        for (int i = 0; i < N; ++i) red[buf][i][threadIdx.x >> 5] = v[i];
-    __syncthreads();
+        for (int i = 0; i < N; ++i) red[buf][i][warp] = v[i];
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float s = 0.0f;
-        for (int w = 0; w < warps; ++w) s += red[buf][i][w];
-        v[i] = s;
-    }
+    for (int i = 0; i < N; ++i) v[i] = lane < warps ? red[buf][i][warp0 + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     buf ^= 1;
 }
 
-template <int V, int NV>
-__global__ void __launch_bounds__(V == 8 ? 512 : 1024) block_norm_kernel(const NormArgs a) {
-    __shared__ float red[2][1][kNormMaxWarps];
+__device__ __forceinline__ float token_gate(const void* gate, int64_t t, int dt) {
+    float g[1];
+    raw_to_f32(load_raw<1>(gate, t, dt), dt, g);
+    return g[0];
+}
+
+// Slots a thread has for one window of type dt (none: no such matrix).
+__host__ __device__ __forceinline__ int window_slots(bool there, int dt) { return there ? (dt == ELEM_F32 ? 2 : 1) : 0; }
+
+// Forward.  A thread keeps `stages` batches of RB rows in flight by cp.async;
+// the rows of a batch share the barriers of the sums.  X, Y, U: element types
+// fixed at compile time (-1: as the arguments say).
+template <int NV, int RB, int MAXT, int X, int Y, int U>
+__global__ void __launch_bounds__(MAXT) block_norm_kernel(const NormArgs a, int tpr, int stages) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float red[2][RB][kNormMaxWarps];
     int buf = 0;
-    const int step = blockDim.x * V;
-    const int c0 = threadIdx.x * V;
+    const int dx = X >= 0 ? X : a.dt_x, dy = Y >= 0 ? Y : a.dt_y, du = U >= 0 ? U : a.dt_u;
+    const Rows g = rows_of(tpr, a.ld_x);
     const bool post = a.y != nullptr, pre = a.u != nullptr;
-    float wp[NV][V], wn[NV][V];
+    const int D = a.D;
+    const int T = static_cast<int>(a.T), row_step = static_cast<int>(g.step);
+    const int pitch = blockDim.x * 16;
+    const int xw = window_slots(true, dx), yw = window_slots(post, dy), slots = xw + yw;
+    uint8_t* weights = ring + threadIdx.x * 16;                   // [NV][post 2, pre 2] slots
+    uint8_t* mine = weights + NV * 4 * pitch;                     // [stages][RB][NV][slots]
+    const int c0 = g.lane_in_group * kNormVec - g.shift, step = tpr * kNormVec;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < V; ++j) wp[i][j] = wn[i][j] = 1.0f;
-        const int c = c0 + i * step;
-        if (c >= a.D) continue;
-        if (post && a.w_post) raw_to_f32(load_raw<V>(a.w_post, c, a.dt_w), a.dt_w, wp[i]);
-        if (post && a.gate_kind == NORM_GATE_CHANNEL) {
-            float g[V];
-            raw_to_f32(load_raw<V>(a.gate, c, a.dt_w), a.dt_w, g);
+        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+        if (post && a.w_post) times_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
+        if (post && a.gate_kind == NORM_GATE_CHANNEL) times_columns(w, a.gate, c0 + i * step, D, a.dt_w);
+        keep(weights + i * 4 * pitch, pitch, w);
 #pragma unroll
-            for (int j = 0; j < V; ++j) wp[i][j] *= g[j];
-        }
-        if (pre && a.w_pre) raw_to_f32(load_raw<V>(a.w_pre, c, a.dt_w), a.dt_w, wn[i]);
+        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+        if (pre && a.w_pre) times_columns(w, a.w_pre, c0 + i * step, D, a.dt_w);
+        keep(weights + (i * 4 + 2) * pitch, pitch, w);
     }
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        RawVec<V> rx[NV], ry[NV];
+    auto issue = [&](int64_t t, int stage) {
+        uint8_t* s = mine + stage * (RB * NV * slots * pitch);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * step;
-            if (c < a.D) {
-                if (post) ry[i] = load_raw<V>(a.y, t * a.ld_y + c, a.dt_y);
-                rx[i] = load_raw<V>(a.x, t * a.ld_x + c, a.dt_x);
-            }
-        }
-        float h[NV][V];
-        if (post) {
-            float y[NV][V];
-            float s[1] = {0.0f};
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (c0 + i * step >= a.D) continue;
-                raw_to_f32(ry[i], a.dt_y, y[i]);
-#pragma unroll
-                for (int j = 0; j < V; ++j) s[0] = fmaf(y[i][j], y[i][j], s[0]);
-            }
-            block_sums<1>(s, red, buf);
-            float q = 1.0f / sqrtf(s[0] / static_cast<float>(a.D) + a.eps);
-            if (a.gate_kind == NORM_GATE_TOKEN) {
-                float g[1];
-                raw_to_f32(load_raw<1>(a.gate, t, a.dt_w), a.dt_w, g);
-                q *= g[0];
-            }
+        for (int b = 0; b < RB; ++b, t += row_step) {
+            if (t >= T) break;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
-                if (c >= a.D) continue;
-                float x[V];
-                raw_to_f32(rx[i], a.dt_x, x);
-#pragma unroll
-                for (int j = 0; j < V; ++j) h[i][j] = fmaf(a.res_scale, x[j], q * wp[i][j] * y[i][j]);
-                store_vec(a.h, t * a.ld_h + c, a.dt_x, h[i]);
-#pragma unroll
-                for (int j = 0; j < V; ++j) h[i][j] = round_to(h[i][j], a.dt_x);
+                if (c >= D) break;
+                uint8_t* p = s + (b * NV + i) * slots * pitch;
+                if (post) fetch(p, pitch, a.y, t * a.ld_y + c, c, D, dy);
+                fetch(p + yw * pitch, pitch, a.x, t * a.ld_x + c, c, D, dx);
             }
-        } else {
+        }
+        cp_async_commit();
+    };
+    for (int k = 0; k + 1 < stages; ++k) issue(g.first + static_cast<int64_t>(k) * RB * row_step, k);
+    int stage = 0, ahead = stages - 1;
+    const float inv_d = 1.0f / static_cast<float>(D);
+    for (int64_t t = g.first; t < T; t += static_cast<int64_t>(RB) * row_step) {
+        issue(t + static_cast<int64_t>(stages - 1) * RB * row_step, ahead);
+        if (++ahead == stages) ahead = 0;
+        cp_async_wait(stages - 1);
+        const uint8_t* s = mine + stage * (RB * NV * slots * pitch);
+        if (++stage == stages) stage = 0;
+        float v[RB][NV][8];
+        float ss[RB];
+        if (post) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (c0 + i * step < a.D) raw_to_f32(rx[i], a.dt_x, h[i]);
+            for (int b = 0; b < RB; ++b) {
+                ss[b] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int c = c0 + i * step;
+                    if (c >= D || t + b * row_step >= T) break;
+                    unpack(s + (b * NV + i) * slots * pitch, pitch, dy, c, D, v[b][i]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) ss[b] = fmaf(v[b][i][j], v[b][i][j], ss[b]);
+                }
+            }
+            group_sums<RB>(ss, g, red, buf);
+        }
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            const int64_t tb = t + b * row_step;
+            float q = 0.0f;
+            if (post) {
+                q = rsqrtf(ss[b] * inv_d + a.eps);
+                if (a.gate_kind == NORM_GATE_TOKEN && tb < T) q *= token_gate(a.gate, tb, a.dt_w);
+            }
+            ss[b] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = c0 + i * step;
+                if (c >= D || tb >= T) break;
+                const uint8_t* p = s + ((b * NV + i) * slots + yw) * pitch;
+                if (post) {
+                    float x[8], w[8];
+                    unpack(p, pitch, dx, c, D, x);
+                    kept(weights + i * 4 * pitch, pitch, w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[b][i][j] = fmaf(a.res_scale, x[j], q * w[j] * v[b][i][j]);
+                    put(a.h, tb * a.ld_h + c, c, D, dx, v[b][i]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[b][i][j] = round_to(v[b][i][j], dx);
+                } else {
+                    unpack(p, pitch, dx, c, D, v[b][i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss[b] = fmaf(v[b][i][j], v[b][i][j], ss[b]);
+            }
         }
         if (pre) {
-            float s[1] = {0.0f};
+            group_sums<RB>(ss, g, red, buf);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (c0 + i * step >= a.D) continue;
+            for (int b = 0; b < RB; ++b) {
+                const int64_t tb = t + b * row_step;
+                const float r = rsqrtf(ss[b] * inv_d + a.eps);
 #pragma unroll
-                for (int j = 0; j < V; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);
-            }
-            block_sums<1>(s, red, buf);
-            const float r = 1.0f / sqrtf(s[0] / static_cast<float>(a.D) + a.eps);
+                for (int i = 0; i < NV; ++i) {
+                    const int c = c0 + i * step;
+                    if (c >= D || tb >= T) break;
+                    float w[8];
+                    kept(weights + (i * 4 + 2) * pitch, pitch, w);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = c0 + i * step;
-                if (c >= a.D) continue;
-#pragma unroll
-                for (int j = 0; j < V; ++j) h[i][j] = h[i][j] * r * wn[i][j];
-                store_vec(a.u, t * a.ld_u + c, a.dt_u, h[i]);
+                    for (int j = 0; j < 8; ++j) v[b][i][j] = v[b][i][j] * r * w[j];
+                    put(a.u, tb * a.ld_u + c, c, D, du, v[b][i]);
+                }
             }
         }
     }
 }
 
-// Gradients.  The column sums of a CTA's rows stay in registers and go to
-// part[blockIdx.x][2][D] at the end: sum du h^ and sum total y^ (times the
-// token's gate).
-template <int V, int NV>
-__global__ void __launch_bounds__(V == 8 ? 512 : 1024) block_norm_backward_kernel(const NormBackArgs a) {
+// Gradients, with the same ring, a row at a time.  The column sums of a
+// thread's rows stay in registers (sum du h^ and sum total y^, times the
+// token's gate), are added over the block's groups through shared memory and
+// go to part[block][2][D].
+template <int NV, int MAXT, int X, int Y, int U>
+__global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages) {
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][3][kNormMaxWarps];
     __shared__ float red1[2][1][kNormMaxWarps];
     int buf = 0, buf1 = 0;
-    const int step = blockDim.x * V;
-    const int c0 = threadIdx.x * V;
-    const bool post = a.y != nullptr, pre = a.du != nullptr;
-    const float inv_d = 1.0f / static_cast<float>(a.D);
-    float s_pre[NV][V], s_post[NV][V];
+    const int tx = X >= 0 ? X : a.dt_x, ty = Y >= 0 ? Y : a.dt_y, tu = U >= 0 ? U : a.dt_u;
+    const bool post = a.y != nullptr, pre = a.du != nullptr, has_dh = a.dh != nullptr;
+    const Rows g = rows_of(tpr, pre ? a.ld_h : a.ld_dh);
+    const int D = a.D;
+    const int T = static_cast<int>(a.T), row_step = static_cast<int>(g.step);
+    const int pitch = blockDim.x * 16;
+    const int off_u = window_slots(pre, tx), off_d = off_u + window_slots(pre, tu), off_y = off_d + window_slots(has_dh, tx);
+    const int slots = off_y + window_slots(post, ty);             // a window's
+    uint8_t* weights = ring + threadIdx.x * 16;                   // [NV][post 2, pre 2] slots
+    uint8_t* mine = weights + NV * 4 * pitch;                     // [stages][NV][slots]
+    const int c0 = g.lane_in_group * kNormVec - g.shift, step = tpr * kNormVec;
+    float s_pre[NV][8], s_post[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < V; ++j) s_pre[i][j] = s_post[i][j] = 0.0f;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        RawVec<V> rh[NV], rdu[NV], rdh[NV], ry[NV];
+        for (int j = 0; j < 8; ++j) {
+            s_pre[i][j] = s_post[i][j] = 0.0f;
+            w[j] = 1.0f;
+        }
+        if (post && a.w_post) times_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
+        if (post && a.gate_kind == NORM_GATE_CHANNEL) times_columns(w, a.gate, c0 + i * step, D, a.dt_w);
+        keep(weights + i * 4 * pitch, pitch, w);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = c0 + i * step;
-            if (c < a.D) {
+        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+        if (pre && a.w_pre) times_columns(w, a.w_pre, c0 + i * step, D, a.dt_w);
+        keep(weights + (i * 4 + 2) * pitch, pitch, w);
+    }
+    auto issue = [&](int64_t t, int stage) {
+        if (t < T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = c0 + i * step;
+                if (c >= D) break;
+                uint8_t* s = mine + (stage * NV + i) * slots * pitch;
                 if (pre) {
-                    rh[i] = load_raw<V>(a.h, t * a.ld_h + c, a.dt_x);
-                    rdu[i] = load_raw<V>(a.du, t * a.ld_du + c, a.dt_u);
+                    fetch(s, pitch, a.h, t * a.ld_h + c, c, D, tx);
+                    fetch(s + off_u * pitch, pitch, a.du, t * a.ld_du + c, c, D, tu);
                 }
-                if (post) ry[i] = load_raw<V>(a.y, t * a.ld_y + c, a.dt_y);
-                if (a.dh) rdh[i] = load_raw<V>(a.dh, t * a.ld_dh + c, a.dt_x);
+                if (has_dh) fetch(s + off_d * pitch, pitch, a.dh, t * a.ld_dh + c, c, D, tx);
+                if (post) fetch(s + off_y * pitch, pitch, a.y, t * a.ld_y + c, c, D, ty);
             }
         }
-        float total[NV][V];
-        float s[3] = {0.0f, 0.0f, 0.0f};     // h^2, a h, y^2
+        cp_async_commit();
+    };
+    for (int k = 0; k + 1 < stages; ++k) issue(g.first + static_cast<int64_t>(k) * row_step, k);
+    int stage = 0, ahead = stages - 1;
+    const float inv_d = 1.0f / static_cast<float>(D);
+    for (int64_t t = g.first; t < T; t += row_step) {
+        issue(t + static_cast<int64_t>(stages - 1) * row_step, ahead);
+        if (++ahead == stages) ahead = 0;
+        cp_async_wait(stages - 1);
+        const uint8_t* s = mine + stage * (NV * slots * pitch);
+        if (++stage == stages) stage = 0;
+        float sums[3] = {0.0f, 0.0f, 0.0f};     // h^2, a h, y^2
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
-            if (c >= a.D) continue;
+            if (c >= D) break;
+            const uint8_t* p = s + i * slots * pitch;
             if (pre) {
-                float h[V], g[V];
-                raw_to_f32(rh[i], a.dt_x, h);
-                raw_to_f32(rdu[i], a.dt_u, g);
-                if (a.w_pre) {
-                    float w[V];
-                    raw_to_f32(load_raw<V>(a.w_pre, c, a.dt_w), a.dt_w, w);
+                float h[8], u[8], w[8];
+                unpack(p, pitch, tx, c, D, h);
+                unpack(p + off_u * pitch, pitch, tu, c, D, u);
+                kept(weights + (i * 4 + 2) * pitch, pitch, w);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) g[j] *= w[j];
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    s[0] = fmaf(h[j], h[j], s[0]);
-                    s[1] = fmaf(g[j], h[j], s[1]);
-                    total[i][j] = g[j];
+                for (int j = 0; j < 8; ++j) {
+                    sums[0] = fmaf(h[j], h[j], sums[0]);
+                    sums[1] = fmaf(u[j] * w[j], h[j], sums[1]);
                 }
             }
             if (post) {
-                float y[V];
-                raw_to_f32(ry[i], a.dt_y, y);
+                float y[8];
+                unpack(p + off_y * pitch, pitch, ty, c, D, y);
 #pragma unroll
-                for (int j = 0; j < V; ++j) s[2] = fmaf(y[j], y[j], s[2]);
+                for (int j = 0; j < 8; ++j) sums[2] = fmaf(y[j], y[j], sums[2]);
             }
         }
-        block_sums<3>(s, red, buf);
-        const float r = 1.0f / sqrtf(s[0] * inv_d + a.eps);
-        const float m = r * r * s[1] * inv_d;          // mean(a h^) / rms(h)
-        const float q = 1.0f / sqrtf(s[2] * inv_d + a.eps);
-        float gt = 1.0f;
-        if (post && a.gate_kind == NORM_GATE_TOKEN) {
-            float g[1];
-            raw_to_f32(load_raw<1>(a.gate, t, a.dt_w), a.dt_w, g);
-            gt = g[0];
-        }
+        group_sums<3>(sums, g, red, buf);
+        const float r = rsqrtf(sums[0] * inv_d + a.eps);
+        const float m = r * r * sums[1] * inv_d;       // mean(a h^) / rms(h)
+        const float q = rsqrtf(sums[2] * inv_d + a.eps);
+        const float gt = (post && a.gate_kind == NORM_GATE_TOKEN) ? token_gate(a.gate, t, a.dt_w) : 1.0f;
+        float total[NV][8];
         float d[1] = {0.0f};                           // sum total w_post (channel gate) y
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
-            if (c >= a.D) continue;
-            float dh[V];
+            if (c >= D) break;
+            const uint8_t* p = s + i * slots * pitch;
 #pragma unroll
-            for (int j = 0; j < V; ++j) dh[j] = 0.0f;
-            if (a.dh) raw_to_f32(rdh[i], a.dt_x, dh);
+            for (int j = 0; j < 8; ++j) total[i][j] = 0.0f;
+            if (has_dh) unpack(p + off_d * pitch, pitch, tx, c, D, total[i]);
             if (pre) {
-                float h[V], g[V];
-                raw_to_f32(rh[i], a.dt_x, h);
-                raw_to_f32(rdu[i], a.dt_u, g);
+                float h[8], u[8], w[8];
+                unpack(p, pitch, tx, c, D, h);
+                unpack(p + off_u * pitch, pitch, tu, c, D, u);
+                kept(weights + (i * 4 + 2) * pitch, pitch, w);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    s_pre[i][j] = fmaf(g[j], h[j] * r, s_pre[i][j]);
-                    total[i][j] = dh[j] + r * (total[i][j] - h[j] * m);
+                for (int j = 0; j < 8; ++j) {
+                    s_pre[i][j] = fmaf(u[j], h[j] * r, s_pre[i][j]);
+                    total[i][j] += r * (u[j] * w[j] - h[j] * m);
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) total[i][j] = dh[j];
             }
             if (a.dx) {
-                float o[V];
+                float o[8];
 #pragma unroll
-                for (int j = 0; j < V; ++j) o[j] = post ? a.res_scale * total[i][j] : total[i][j];
-                store_vec(a.dx, t * a.ld_dx + c, a.dt_x, o);
+                for (int j = 0; j < 8; ++j) o[j] = post ? a.res_scale * total[i][j] : total[i][j];
+                put(a.dx, t * a.ld_dx + c, c, D, tx, o);
             }
             if (post) {
-                float y[V], w[V];
-                raw_to_f32(ry[i], a.dt_y, y);
+                float y[8], w[8];
+                unpack(p + off_y * pitch, pitch, ty, c, D, y);
+                kept(weights + i * 4 * pitch, pitch, w);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     s_post[i][j] = fmaf(total[i][j] * gt, y[j] * q, s_post[i][j]);
-                    w[j] = 1.0f;
-                }
-                if (a.w_post) raw_to_f32(load_raw<V>(a.w_post, c, a.dt_w), a.dt_w, w);
-                if (a.gate_kind == NORM_GATE_CHANNEL) {
-                    float g[V];
-                    raw_to_f32(load_raw<V>(a.gate, c, a.dt_w), a.dt_w, g);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) w[j] *= g[j];
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
                     total[i][j] *= w[j];
                     d[0] = fmaf(total[i][j], y[j], d[0]);
                 }
             }
         }
         if (post) {
-            block_sums<1>(d, red1, buf1);
-            if (a.d_gate_token && threadIdx.x == 0) a.d_gate_token[t] = d[0] * q;
+            group_sums<1>(d, g, red1, buf1);
+            if (a.d_gate_token && g.lane_in_group == 0) a.d_gate_token[t] = d[0] * q;
             if (a.dy) {
                 const float n = q * q * d[0] * inv_d;      // mean(p y^) / (g rms(y))
                 const float f = q * gt;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = c0 + i * step;
-                    if (c >= a.D) continue;
-                    float y[V], o[V];
-                    raw_to_f32(ry[i], a.dt_y, y);
+                    if (c >= D) break;
+                    float y[8], o[8];
+                    unpack(s + (i * slots + off_y) * pitch, pitch, ty, c, D, y);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) o[j] = f * (total[i][j] - y[j] * n);
-                    store_vec(a.dy, t * a.ld_dy + c, a.dt_y, o);
+                    for (int j = 0; j < 8; ++j) o[j] = f * (total[i][j] - y[j] * n);
+                    put(a.dy, t * a.ld_dy + c, c, D, ty, o);
                 }
+            }
+        }
+    }
+    if (!a.part) return;
+    float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * D;
+    if (g.groups == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = c0 + i * step + j;
+                if (c >= 0 && c < D) {
+                    out[c] = s_pre[i][j];
+                    out[D + c] = s_post[i][j];
+                }
+            }
+        return;
+    }
+    // groups in turn add their columns (their windows may start at different
+    // columns) to the block's, in the ring's memory
+    cp_async_wait(0);
+    float* acc = reinterpret_cast<float*>(ring);
+    __syncthreads();
+    for (int k = 0; k < g.groups; ++k) {
+        if (g.group == k)
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = c0 + i * step + j;
+                    if (c >= 0 && c < D) {
+                        acc[c] = (k ? acc[c] : 0.0f) + s_pre[i][j];
+                        acc[D + c] = (k ? acc[D + c] : 0.0f) + s_post[i][j];
+                    }
+                }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) out[c] = acc[c];
+}
+
+// ------------------------------------------------------------------ rows element by element
+// For matrices whose rows do not lie alike in their windows (bases off 16
+// bytes, strides that differ modulo 8).
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*red)[N][kNormMaxWarps], int& buf) {
+    Rows g;
+    g.tpr = blockDim.x;
+    g.group = 0;
+    group_sums<N>(v, g, red, buf);
+}
+
+__global__ void __launch_bounds__(1024) block_norm_plain_kernel(const NormArgs a) {
+    __shared__ float red[2][1][kNormMaxWarps];
+    int buf = 0;
+    const bool post = a.y != nullptr, pre = a.u != nullptr;
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    auto at = [](const void* p, int64_t i, int dt) {
+        float f[1];
+        raw_to_f32(load_raw<1>(p, i, dt), dt, f);
+        return f[0];
+    };
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        float q = 0.0f;
+        if (post) {
+            float ss[1] = {0.0f};
+            for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+                const float y = at(a.y, t * a.ld_y + c, a.dt_y);
+                ss[0] = fmaf(y, y, ss[0]);
+            }
+            block_sums<1>(ss, red, buf);
+            q = rsqrtf(ss[0] * inv_d + a.eps);
+            if (a.gate_kind == NORM_GATE_TOKEN) q *= token_gate(a.gate, t, a.dt_w);
+        }
+        // h as it is stored: computed once, then read back by the same thread
+        float ss[1] = {0.0f};
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            float h[1] = {at(a.x, t * a.ld_x + c, a.dt_x)};
+            if (post) {
+                float w = a.w_post ? at(a.w_post, c, a.dt_w) : 1.0f;
+                if (a.gate_kind == NORM_GATE_CHANNEL) w *= at(a.gate, c, a.dt_w);
+                h[0] = fmaf(a.res_scale, h[0], q * w * at(a.y, t * a.ld_y + c, a.dt_y));
+                store_vec(a.h, t * a.ld_h + c, a.dt_x, h);
+                h[0] = round_to(h[0], a.dt_x);
+            }
+            ss[0] = fmaf(h[0], h[0], ss[0]);
+        }
+        if (!pre) continue;
+        block_sums<1>(ss, red, buf);
+        const float r = rsqrtf(ss[0] * inv_d + a.eps);
+        const void* hp = post ? a.h : a.x;
+        const int64_t ld = post ? a.ld_h : a.ld_x;
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            const float o[1] = {at(hp, t * ld + c, a.dt_x) * r * (a.w_pre ? at(a.w_pre, c, a.dt_w) : 1.0f)};
+            store_vec(a.u, t * a.ld_u + c, a.dt_u, o);
+        }
+    }
+}
+
+constexpr int kPlainColumns = 16;       // columns a thread: widths up to 16 * 1024
+
+__global__ void __launch_bounds__(1024) block_norm_backward_plain_kernel(const NormBackArgs a) {
+    __shared__ float red[2][3][kNormMaxWarps];
+    __shared__ float red1[2][1][kNormMaxWarps];
+    int buf = 0, buf1 = 0;
+    const bool post = a.y != nullptr, pre = a.du != nullptr;
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    auto at = [](const void* p, int64_t i, int dt) {
+        float f[1];
+        raw_to_f32(load_raw<1>(p, i, dt), dt, f);
+        return f[0];
+    };
+    float s_pre[kPlainColumns], s_post[kPlainColumns];
+#pragma unroll
+    for (int i = 0; i < kPlainColumns; ++i) s_pre[i] = s_post[i] = 0.0f;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        float sums[3] = {0.0f, 0.0f, 0.0f};
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            if (pre) {
+                const float h = at(a.h, t * a.ld_h + c, a.dt_x);
+                const float u = at(a.du, t * a.ld_du + c, a.dt_u) * (a.w_pre ? at(a.w_pre, c, a.dt_w) : 1.0f);
+                sums[0] = fmaf(h, h, sums[0]);
+                sums[1] = fmaf(u, h, sums[1]);
+            }
+            if (post) {
+                const float y = at(a.y, t * a.ld_y + c, a.dt_y);
+                sums[2] = fmaf(y, y, sums[2]);
+            }
+        }
+        block_sums<3>(sums, red, buf);
+        const float r = rsqrtf(sums[0] * inv_d + a.eps);
+        const float m = r * r * sums[1] * inv_d;
+        const float q = rsqrtf(sums[2] * inv_d + a.eps);
+        const float gt = (post && a.gate_kind == NORM_GATE_TOKEN) ? token_gate(a.gate, t, a.dt_w) : 1.0f;
+        float total[kPlainColumns], yv[kPlainColumns];
+        float d[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < kPlainColumns; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c >= a.D) break;
+            total[i] = a.dh ? at(a.dh, t * a.ld_dh + c, a.dt_x) : 0.0f;
+            if (pre) {
+                const float h = at(a.h, t * a.ld_h + c, a.dt_x);
+                const float u = at(a.du, t * a.ld_du + c, a.dt_u);
+                s_pre[i] = fmaf(u, h * r, s_pre[i]);
+                total[i] += r * (u * (a.w_pre ? at(a.w_pre, c, a.dt_w) : 1.0f) - h * m);
+            }
+            if (post) {
+                yv[i] = at(a.y, t * a.ld_y + c, a.dt_y);
+                s_post[i] = fmaf(total[i] * gt, yv[i] * q, s_post[i]);
+            }
+            if (a.dx) {
+                const float o[1] = {post ? a.res_scale * total[i] : total[i]};
+                store_vec(a.dx, t * a.ld_dx + c, a.dt_x, o);
+            }
+            if (post) {
+                float w = a.w_post ? at(a.w_post, c, a.dt_w) : 1.0f;
+                if (a.gate_kind == NORM_GATE_CHANNEL) w *= at(a.gate, c, a.dt_w);
+                total[i] *= w;
+                d[0] = fmaf(total[i], yv[i], d[0]);
+            }
+        }
+        if (!post) continue;
+        block_sums<1>(d, red1, buf1);
+        if (a.d_gate_token && threadIdx.x == 0) a.d_gate_token[t] = d[0] * q;
+        if (a.dy) {
+            const float n = q * q * d[0] * inv_d, f = q * gt;
+#pragma unroll
+            for (int i = 0; i < kPlainColumns; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                if (c >= a.D) break;
+                const float o[1] = {f * (total[i] - yv[i] * n)};
+                store_vec(a.dy, t * a.ld_dy + c, a.dt_y, o);
             }
         }
     }
     if (a.part) {
         float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = c0 + i * step + j;
-                if (c < a.D) {
-                    out[c] = s_pre[i][j];
-                    out[a.D + c] = s_post[i][j];
-                }
-            }
+        for (int i = 0; i < kPlainColumns; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            if (c >= a.D) break;
+            out[c] = s_pre[i];
+            out[a.D + c] = s_post[i];
+        }
     }
 }
 
@@ -331,49 +670,6 @@ __global__ void norm_zero_kernel(const NormBackArgs a) {
     if (a.d_gate_channel) a.d_gate_channel[c] = 0.0f;
 }
 
-bool vec8(const void* p, int64_t ld, int dt) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0);
-}
-
-// Threads of a CTA and register vectors a thread for rows of D elements.
-void norm_shape(int D, bool v8, int& threads, int& nv) {
-    const int n = v8 ? D / 8 : D;
-    if (v8) nv = n <= 512 ? 1 : (n <= 1024 ? 2 : 4);
-    else nv = n <= 4096 ? 4 : 16;
-    threads = ((n + nv - 1) / nv + 31) / 32 * 32;
-}
-
-// Blocks of `threads` threads of this kernel instance that fit on an SM.
-template <auto Kern>
-int resident(int threads) {
-    static std::atomic<int> cache[kNormMaxWarps + 1];
-    int n = cache[threads / 32].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kern, threads, 0) != cudaSuccess || n < 1) n = 1;
-        cache[threads / 32].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
-template <int V, int NV>
-cudaError_t forward_as(const NormArgs& a, int threads, int sms, cudaStream_t s) {
-    const int64_t most = static_cast<int64_t>(sms) * resident<block_norm_kernel<V, NV>>(threads);
-    block_norm_kernel<V, NV><<<static_cast<unsigned>(a.T < most ? a.T : most), threads, 0, s>>>(a);
-    return cudaGetLastError();
-}
-
-template <int V, int NV>
-cudaError_t backward_as(const NormBackArgs& a, int threads, int sms, cudaStream_t s) {
-    int64_t grid = static_cast<int64_t>(sms) * resident<block_norm_backward_kernel<V, NV>>(threads);
-    if (grid > kNormParts) grid = kNormParts;
-    if (grid > a.T) grid = a.T;
-    block_norm_backward_kernel<V, NV><<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess || !a.part) return err;
-    norm_columns_kernel<<<dim3((a.D + 31) / 32, 2), 32 * kColGroups, 0, s>>>(a, static_cast<int>(grid));
-    return cudaGetLastError();
-}
-
 cudaError_t sm_count(int* sms) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
@@ -381,7 +677,100 @@ cudaError_t sm_count(int* sms) {
     return err;
 }
 
+// Collects whether a launch's matrices lie alike in their windows.
+struct Alike {
+    bool ok = true;
+    int64_t ld = -1;
+    bool odd = false;           // rows start at different places in their windows
+    void add(const void* p, int64_t l) {
+        if (!p) return;
+        if (reinterpret_cast<uintptr_t>(p) % 16) ok = false;
+        if (ld >= 0 && ((ld ^ l) & (kNormVec - 1))) ok = false;
+        ld = l;
+        odd = odd || (l & (kNormVec - 1));
+    }
+};
+
+// How a launch covers T rows of D elements.  Threads own one window each up to
+// max_threads windows a row, two beyond; rows of few windows share a block of
+// about 256 threads.  The ring takes what an SM's shared memory gives to the
+// blocks that its registers hold, up to eight batches of rows.
+struct Shape {
+    int nv, tpr, threads, stages, grid;
+    size_t smem;
+};
+constexpr int kNormSmem = kSmemLimit - 2048;     // without the sums' static part
+
+bool shape_of(int64_t T, int D, const Alike& al, int slots, int batch, int max_threads, int max_nv, int regs, int sms,
+              int most, Shape* s) {
+    if (!al.ok) return false;
+    const int windows = (D + (al.odd ? kNormVec - 1 : 0) + kNormVec - 1) / kNormVec;
+    if (windows > max_nv * max_threads) return false;
+    s->nv = 1;
+    while (s->nv * max_threads < windows) s->nv *= 2;
+    if (s->nv > 1) batch = 1;
+    s->tpr = ((windows + s->nv - 1) / s->nv + 31) / 32 * 32;
+    int groups = s->tpr >= 256 ? 1 : 256 / s->tpr;
+    while (groups > 1 && static_cast<int64_t>(groups) * sms > T) groups /= 2;      // few rows: over the SMs first
+    s->threads = s->tpr * groups;
+    int per_sm = 65536 / (regs * s->threads);
+    per_sm = std::max(1, std::min(per_sm, 2048 / s->threads));
+    const int stage = s->nv * batch * slots * s->threads * 16, fixed = s->nv * 4 * s->threads * 16;
+    // at least two batches in flight a block
+    while (per_sm > 1 && per_sm * (2 * stage + fixed + 1024) > kNormSmem) --per_sm;
+    int64_t grid = std::min<int64_t>((T + groups - 1) / groups, static_cast<int64_t>(sms) * per_sm);
+    if (grid > most) grid = most;
+    if (al.odd && grid * groups < T) {
+        // a row's place in its windows has to be the same in all rows of a
+        // group: blocks x groups is a multiple of 8
+        const int64_t unit = groups >= 8 ? 1 : 8 / groups;
+        if (grid < unit) return false;
+        grid = grid / unit * unit;
+    }
+    s->grid = static_cast<int>(grid);
+    const int per_block = std::min<int>(per_sm, static_cast<int>((grid + sms - 1) / sms));
+    const int64_t batches = (T + grid * groups * batch - 1) / (grid * groups * batch);  // of a group at most
+    int st = (kNormSmem / per_block - 1024 - fixed) / stage;
+    st = std::max(1, std::min<int>(st, kNormMaxStages));
+    s->stages = static_cast<int>(std::min<int64_t>(st, batches));
+    s->smem = static_cast<size_t>(s->stages) * stage + fixed;
+    return s->smem <= static_cast<size_t>(kNormSmem);
+}
+
+template <typename Args>
+cudaError_t run_rows(void (*kern)(Args, int, int), const Args& a, const Shape& sh, size_t smem, cudaStream_t s) {
+    if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
+        if (err != cudaSuccess) return err;
+    }
+    kern<<<sh.grid, sh.threads, smem, s>>>(a, sh.tpr, sh.stages);
+    return cudaGetLastError();
+}
+
+// Threads at most, by windows a thread: the forward kernel holds a batch of
+// two rows at one window; the backward kernel's column sums take more
+// registers, 896 threads leave it 72.
+template <int X, int Y, int U>
+cudaError_t forward_as(const NormArgs& a, const Shape& sh, cudaStream_t s) {
+    if (sh.nv == 2) return run_rows(block_norm_kernel<2, 1, 1024, X, Y, U>, a, sh, sh.smem, s);
+    return run_rows(block_norm_kernel<1, 2, 1024, X, Y, U>, a, sh, sh.smem, s);
+}
+template <int X, int Y, int U>
+cudaError_t backward_as(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
+    if (sh.nv == 2) return run_rows(block_norm_backward_kernel<2, 1024, X, Y, U>, a, sh, smem, s);
+    if (sh.threads > 896) return run_rows(block_norm_backward_kernel<1, 1024, X, Y, U>, a, sh, smem, s);
+    return run_rows(block_norm_backward_kernel<1, 896, X, Y, U>, a, sh, smem, s);
+}
+
+int plain_threads(int D) { return std::min(1024, std::max(32, (D + kPlainColumns / 4 - 1) / (kPlainColumns / 4) + 31) / 32 * 32); }
+
 }  // namespace
+
+int norm_parts(int64_t T, int D) {
+    // narrow rows: more blocks, each with a short part
+    const int64_t most = std::max<int64_t>(kNormParts, (1 << 19) / D);
+    return static_cast<int>(std::max<int64_t>(1, std::min(T, most)));
+}
 
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     if (a.D < 1 || a.D > kNormMaxWidth || a.T < 0) return cudaErrorInvalidValue;
@@ -389,18 +778,23 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
-    const bool v8 = a.D % 8 == 0 && vec8(a.x, a.ld_x, a.dt_x) && vec8(a.y, a.ld_y, a.dt_y) && vec8(a.h, a.ld_h, a.dt_x) &&
-                    vec8(a.u, a.ld_u, a.dt_u) && vec8(a.w_post, 0, a.dt_w) && vec8(a.w_pre, 0, a.dt_w) &&
-                    (a.gate_kind != NORM_GATE_CHANNEL || vec8(a.gate, 0, a.dt_w));
-    int threads, nv;
-    norm_shape(a.D, v8, threads, nv);
-    if (v8) {
-        if (nv == 1) return forward_as<8, 1>(a, threads, sms, s);
-        if (nv == 2) return forward_as<8, 2>(a, threads, sms, s);
-        return forward_as<8, 4>(a, threads, sms, s);
+    Alike al;
+    al.add(a.x, a.ld_x);
+    al.add(a.y, a.ld_y);
+    al.add(a.h, a.ld_h);
+    al.add(a.u, a.ld_u);
+    Shape sh;
+    const int slots = window_slots(true, a.dt_x) + window_slots(a.y, a.dt_y);
+    if (shape_of(a.T, a.D, al, slots, 2, 1024, 2, 64, sms, 1 << 30, &sh)) {
+        const bool b = a.dt_x == ELEM_BF16 && (!a.u || a.dt_u == ELEM_BF16);
+        if (b && (!a.y || a.dt_y == ELEM_BF16)) return forward_as<ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, s);
+        if (b && a.dt_y == ELEM_F32) return forward_as<ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, s);
+        return forward_as<-1, -1, -1>(a, sh, s);
     }
-    if (nv == 4) return forward_as<1, 4>(a, threads, sms, s);
-    return forward_as<1, 16>(a, threads, sms, s);
+    const int threads = plain_threads(a.D);
+    block_norm_plain_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.T, static_cast<int64_t>(sms) * (2048 / threads))),
+                              threads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
@@ -413,19 +807,36 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
-    const bool v8 = a.D % 8 == 0 && vec8(a.h, a.ld_h, a.dt_x) && vec8(a.y, a.ld_y, a.dt_y) && vec8(a.dh, a.ld_dh, a.dt_x) &&
-                    vec8(a.du, a.ld_du, a.dt_u) && vec8(a.dx, a.ld_dx, a.dt_x) && vec8(a.dy, a.ld_dy, a.dt_y) &&
-                    vec8(a.w_post, 0, a.dt_w) && vec8(a.w_pre, 0, a.dt_w) &&
-                    (a.gate_kind != NORM_GATE_CHANNEL || vec8(a.gate, 0, a.dt_w));
-    int threads, nv;
-    norm_shape(a.D, v8, threads, nv);
-    if (v8) {
-        if (nv == 1) return backward_as<8, 1>(a, threads, sms, s);
-        if (nv == 2) return backward_as<8, 2>(a, threads, sms, s);
-        return backward_as<8, 4>(a, threads, sms, s);
+    Alike al;
+    al.add(a.h, a.ld_h);
+    al.add(a.du, a.ld_du);
+    al.add(a.dh, a.ld_dh);
+    al.add(a.y, a.ld_y);
+    al.add(a.dx, a.ld_dx);
+    al.add(a.dy, a.ld_dy);
+    const int slots = window_slots(a.du, a.dt_x) + window_slots(a.du, a.dt_u) + window_slots(a.dh, a.dt_x) +
+                      window_slots(a.y, a.dt_y);
+    const int most = norm_parts(a.T, a.D);
+    Shape sh;
+    int parts;
+    if (shape_of(a.T, a.D, al, slots, 1, 1024, 2, 72, sms, most, &sh)) {
+        // the end of the kernel adds the groups' columns in the ring's memory
+        size_t smem = sh.smem;
+        if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.D));
+        parts = sh.grid;
+        const bool b = (!(a.h || a.dh || a.dx) || a.dt_x == ELEM_BF16) && (!a.du || a.dt_u == ELEM_BF16);
+        if (b && (!a.y || a.dt_y == ELEM_BF16)) err = backward_as<ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, smem, s);
+        else if (b && a.dt_y == ELEM_F32) err = backward_as<ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, smem, s);
+        else err = backward_as<-1, -1, -1>(a, sh, smem, s);
+    } else {
+        parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.T, most), 2 * sms));
+        const int threads = std::min(1024, (a.D + 31) / 32 * 32);
+        block_norm_backward_plain_kernel<<<parts, threads, 0, s>>>(a);
+        err = cudaGetLastError();
     }
-    if (nv == 4) return backward_as<1, 4>(a, threads, sms, s);
-    return backward_as<1, 16>(a, threads, sms, s);
+    if (err != cudaSuccess || !a.part) return err;
+    norm_columns_kernel<<<dim3((a.D + 31) / 32, 2), 32 * kColGroups, 0, s>>>(a, parts);
+    return cudaGetLastError();
 }
 
 }  // namespace moe

@@ -28,47 +28,66 @@ namespace {
 // ------------------------------------------------------------------ sort
 // A counting sort in one launch of one cluster.  Warp w of the cluster owns a
 // contiguous strip of slots and counts its experts in a row of its own
-// (cnt[w][E], shared memory): the 32 slots of a step find their equals with
-// match.any, and the lowest lane of each set adds the set's size.  A scan over
-// the CTA's warps, then over the cluster's CTAs (distributed shared memory),
-// then over experts turns the counts into each strip's first place of every
-// expert, and a second pass over the strip hands the places out.
+// (cnt[w][E], shared memory; integer atomics, whose order does not matter).  A
+// scan over the CTA's warps, then over the cluster's CTAs (distributed shared
+// memory), then over experts turns the counts into each strip's first place of
+// every expert.  A second pass over the strip hands the places out, 32 slots a
+// step: match.any finds a slot's equals, the lanes below it are its rank, and
+// the lowest lane of each set moves the strip's next place on.  The loads of
+// kSortBatch steps are in flight together: a strip's steps are short, and one
+// at a time each would pay a round trip to memory.
 constexpr int kSortMaxE = 1024;
 constexpr int kSortMaxWarps = 32;
+constexpr int kSortBatch = 8;
+constexpr int kSortMaxCluster = 8;
 
-__global__ void sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int32_t* __restrict__ offsets,
-                            int32_t* __restrict__ sorted_slot, int32_t* __restrict__ slot_pos, int C) {
-    extern __shared__ int32_t sm[];
+__global__ void __launch_bounds__(kSortMaxWarps * 32)
+    sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int32_t* __restrict__ offsets,
+                int32_t* __restrict__ sorted_slot, int32_t* __restrict__ slot_pos, int C) {
+    extern __shared__ __align__(16) int32_t sm[];
     __shared__ int32_t warp_sum[32];
     const int W = blockDim.x >> 5;
-    int32_t* cnt = sm;                 // [W][E]
-    int32_t* tot = sm + W * E;         // [E] this CTA's counts
-    int32_t* start = tot + E;          // [E] this CTA's first place of each expert
+    const int Ep = (E + 3) & ~3;       // rows of whole 16-byte words
+    int32_t* cnt = sm;                 // [W][Ep]
+    int32_t* tot = sm + W * Ep;        // [Ep] this CTA's counts
+    int32_t* start = tot + Ep;         // [Ep] this CTA's first place of each expert
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x);
-    for (int i = threadIdx.x; i < W * E; i += blockDim.x) cnt[i] = 0;
-    __syncthreads();
     // strips of whole 32-slot steps
     const int64_t steps = (n + 31) / 32;
     const int64_t per = (steps + static_cast<int64_t>(C) * W - 1) / (static_cast<int64_t>(C) * W);
     const int64_t s0 = (static_cast<int64_t>(rank) * W + warp) * per;
     const int64_t s1 = s0 + per < steps ? s0 + per : steps;
-    int32_t* mine = cnt + warp * E;
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t i = s * 32 + lane;
-        int e = (i < n) ? idx[i] : -1;
-        if (e < 0 || e >= E) e = E;
-        const uint32_t peers = __match_any_sync(0xffffffffu, e);
-        if (e < E && (peers & ((1u << lane) - 1)) == 0) mine[e] += __popc(peers);
-        __syncwarp();
+    int32_t ex[kSortBatch];
+    auto load = [&](int64_t s) {
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) {
+            const int64_t i = (s + u) * 32 + lane;
+            ex[u] = (s + u < s1 && i < n) ? idx[i] : -1;
+        }
+    };
+    load(s0);
+    for (int i = threadIdx.x; i < W * Ep / 4; i += blockDim.x) reinterpret_cast<int4*>(cnt)[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    int32_t* mine = cnt + warp * Ep;
+    for (int64_t s = s0; s < s1; s += kSortBatch) {
+        if (s != s0) load(s);
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u)
+            if (ex[u] >= 0 && ex[u] < E) atomicAdd(&mine[ex[u]], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         int32_t run = 0;
-        for (int w = 0; w < W; ++w) {
-            const int32_t c = cnt[w * E + e];
-            cnt[w * E + e] = run;
-            run += c;
+        for (int w0 = 0; w0 < W; w0 += 8) {
+            int32_t c[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) c[u] = w0 + u < W ? cnt[(w0 + u) * Ep + e] : 0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (w0 + u < W) cnt[(w0 + u) * Ep + e] = run;
+                run += c[u];
+            }
         }
         tot[e] = run;
     }
@@ -84,10 +103,13 @@ __global__ void sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, i
         if (e >= E) break;
         int32_t before = 0, all = 0;
         if (C > 1) {
-            for (int c = 0; c < C; ++c) {
-                const int32_t v = cg::this_cluster().map_shared_rank(tot, c)[e];
-                before += (c < rank) ? v : 0;
-                all += v;
+            int32_t v[kSortMaxCluster];
+#pragma unroll
+            for (int c = 0; c < kSortMaxCluster; ++c) v[c] = c < C ? cg::this_cluster().map_shared_rank(tot, c)[e] : 0;
+#pragma unroll
+            for (int c = 0; c < kSortMaxCluster; ++c) {
+                before += (c < rank) ? v[c] : 0;
+                all += v[c];
             }
         } else {
             all = tot[e];
@@ -103,39 +125,50 @@ __global__ void sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, i
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int32_t base = incl - sum, total = 0;
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) base += warp_sum[w];
-        total += warp_sum[w];
+    // every warp scans the warps' sums for itself
+    const int32_t ws = lane < W ? warp_sum[lane] : 0;
+    int32_t winc = ws;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, winc, o);
+        if (lane >= o) winc += v;
     }
-    {
-        for (int u = 0; u < per_thread; ++u) {
-            const int e = e0 + u;
-            if (e >= E) break;
-            start[e] += base;
-        }
+    const int32_t total = __shfl_sync(0xffffffffu, winc, 31);
+    const int32_t base = __shfl_sync(0xffffffffu, winc - ws, warp) + incl - sum;
+    for (int u = 0; u < per_thread; ++u) {
+        const int e = e0 + u;
+        if (e >= E) break;
+        start[e] += base;
+        // rank 0 has no earlier CTA: its first places are the experts' offsets
+        if (rank == 0) offsets[e] = start[e];
     }
     if (rank == 0 && threadIdx.x == 0) offsets[E] = total;
     __syncthreads();
-    // rank 0 has no earlier CTA: its first places are the experts' offsets
-    if (rank == 0)
-        for (int e = threadIdx.x; e < E; e += blockDim.x) offsets[e] = start[e];
     // the strips' places in order
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t i = s * 32 + lane;
-        int e = (i < n) ? idx[i] : -1;
-        if (e < 0 || e >= E) e = E;
-        const uint32_t peers = __match_any_sync(0xffffffffu, e);
-        const uint32_t below = peers & ((1u << lane) - 1);
-        int32_t p = -1;
-        if (e < E) p = start[e] + mine[e] + __popc(below);
-        __syncwarp();
-        if (e < E && below == 0) mine[e] += __popc(peers);
-        if (i < n) {
-            slot_pos[i] = p;
-            if (p >= 0) sorted_slot[p] = static_cast<int32_t>(i);
+    if (per > kSortBatch) load(s0);
+    for (int64_t s = s0; s < s1; s += kSortBatch) {
+        if (s != s0) load(s);
+        uint32_t peers[kSortBatch];
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) {
+            if (ex[u] < 0 || ex[u] >= E) ex[u] = E;
+            peers[u] = __match_any_sync(0xffffffffu, ex[u]);
         }
-        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) {
+            const int64_t i = (s + u) * 32 + lane;
+            if (s + u >= s1) break;
+            const uint32_t below = peers[u] & ((1u << lane) - 1);
+            int32_t p = -1;
+            if (ex[u] < E) p = start[ex[u]] + mine[ex[u]] + __popc(below);
+            __syncwarp();
+            if (ex[u] < E && below == 0) mine[ex[u]] += __popc(peers[u]);
+            __syncwarp();
+            if (i < n) {
+                slot_pos[i] = p;
+                if (p >= 0) sorted_slot[p] = static_cast<int32_t>(i);
+            }
+        }
     }
     for (int64_t p = total + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; p < n;
          p += static_cast<int64_t>(C) * blockDim.x)
@@ -184,16 +217,20 @@ __global__ void permute_kernel(const uint8_t* __restrict__ x, int64_t x_stride, 
 // a time, their FMAs run in slot order.
 constexpr int kUnpermBatch = 8;
 
-template <int V>
-__global__ void __launch_bounds__(128) unpermute_kernel(const void* __restrict__ rows, int64_t ld_rows, int dt,
-                                                        int64_t n_rows, const int32_t* __restrict__ slot_pos,
+template <int V, int DT>
+__global__ void __launch_bounds__(128) unpermute_kernel(const void* __restrict__ rows, int64_t ld_rows, int64_t n_rows,
+                                                        const int32_t* __restrict__ slot_pos,
                                                         const float* __restrict__ w, int64_t T, int k, int D,
-                                                        void* __restrict__ y, int64_t ld_y, int dty, int64_t chunks) {
-    const int64_t gw = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+                                                        void* __restrict__ y, int64_t ld_y, int dty, uint32_t chunks) {
     const int lane = threadIdx.x & 31;
-    if (gw >= T * chunks) return;
-    const int64_t t = gw / chunks;
-    const int64_t col = (gw - t * chunks) * (32 * V) + lane * V;
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t per_block = blockDim.x >> 5;
+    // grid: (chunks of columns in blocks of warps, tokens)
+    const uint32_t ch = blockIdx.x * per_block + warp;
+    if (ch >= chunks) return;
+    const int64_t t = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
+    if (t >= T) return;
+    const int col = static_cast<int>(ch) * (32 * V) + lane * V;
     int32_t p_lane = (lane < k) ? slot_pos[t * k + lane] : -1;
     if (p_lane >= n_rows) p_lane = -1;
     const float w_lane = (lane < k) ? (w ? w[t * k + lane] : 1.0f) : 0.0f;
@@ -205,7 +242,7 @@ __global__ void __launch_bounds__(128) unpermute_kernel(const void* __restrict__
 #pragma unroll
         for (int u = 0; u < kUnpermBatch; ++u) {
             const int64_t p = __shfl_sync(0xffffffffu, p_lane, (j0 + u) & 31);
-            if (j0 + u < k && p >= 0 && col < D) r[u] = load_raw<V>(rows, p * ld_rows + col, dt);
+            if (j0 + u < k && p >= 0 && col < D) r[u] = load_stream<V, DT>(rows, p * ld_rows + col);
         }
 #pragma unroll
         for (int u = 0; u < kUnpermBatch; ++u) {
@@ -213,7 +250,7 @@ __global__ void __launch_bounds__(128) unpermute_kernel(const void* __restrict__
             const float wj = __shfl_sync(0xffffffffu, w_lane, (j0 + u) & 31);
             if (j0 + u < k && p >= 0 && col < D) {
                 float f[V];
-                raw_to_f32(r[u], dt, f);
+                raw_to_f32(r[u], DT, f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
             }
@@ -227,15 +264,15 @@ __global__ void __launch_bounds__(128) unpermute_kernel(const void* __restrict__
 // dot product is summed over the lanes in a fixed order.
 constexpr int kBackBatch = 4;
 
-template <int V>
+template <int V, int DT>
 __global__ void __launch_bounds__(256) unpermute_backward_kernel(
-    const void* __restrict__ dy, int64_t ld_dy, int dty, const void* __restrict__ rows, int64_t ld_rows, int dt,
-    int64_t n_rows, const int32_t* __restrict__ slot_pos, const float* __restrict__ w, int64_t T, int k, int D,
+    const void* __restrict__ dy, int64_t ld_dy, int dty, const void* __restrict__ rows, int64_t ld_rows,
+    int64_t n_rows, const int32_t* __restrict__ slot_pos, const float* __restrict__ w, int64_t slots, int k, int D,
     void* __restrict__ d_rows, int64_t ld_d, float* __restrict__ d_w) {
     const int64_t s = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
-    if (s >= T * k) return;
-    const int64_t t = s / k;
+    if (s >= slots) return;
+    const int64_t t = static_cast<uint32_t>(s) / static_cast<uint32_t>(k);      // slots < 2^31
     const int64_t p = slot_pos[s];
     if (p < 0 || p >= n_rows) {
         if (d_w && lane == 0) d_w[s] = 0.0f;
@@ -243,32 +280,32 @@ __global__ void __launch_bounds__(256) unpermute_backward_kernel(
     }
     const float wj = w ? w[s] : 1.0f;
     float dot = 0.0f;
-    for (int64_t c0 = lane * V; c0 < D; c0 += 32 * V * kBackBatch) {
+    for (int c0 = lane * V; c0 < D; c0 += 32 * V * kBackBatch) {
         RawVec<V> g[kBackBatch], r[kBackBatch];
 #pragma unroll
         for (int u = 0; u < kBackBatch; ++u) {
-            const int64_t c = c0 + 32 * V * u;
+            const int c = c0 + 32 * V * u;
             if (c < D) {
                 g[u] = load_raw<V>(dy, t * ld_dy + c, dty);
-                if (d_w) r[u] = load_raw<V>(rows, p * ld_rows + c, dt);
+                if (d_w) r[u] = load_stream<V, DT>(rows, p * ld_rows + c);
             }
         }
 #pragma unroll
         for (int u = 0; u < kBackBatch; ++u) {
-            const int64_t c = c0 + 32 * V * u;
+            const int c = c0 + 32 * V * u;
             if (c < D) {
                 float f[V];
                 raw_to_f32(g[u], dty, f);
                 if (d_w) {
                     float q[V];
-                    raw_to_f32(r[u], dt, q);
+                    raw_to_f32(r[u], DT, q);
 #pragma unroll
                     for (int i = 0; i < V; ++i) dot = fmaf(f[i], q[i], dot);
                 }
                 if (d_rows) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) f[i] *= wj;
-                    store_vec(d_rows, p * ld_d + c, dt, f);
+                    store_stream<V, DT>(d_rows, p * ld_d + c, f);
                 }
             }
         }
@@ -309,11 +346,11 @@ cudaError_t launch_sort(const int32_t* idx, int64_t n, int E, int32_t* offsets, 
     if (n < 0 || E < 1 || E > kSortMaxE) return cudaErrorInvalidValue;
     // one CTA up to 8,192 slots, then up to 8 (the portable cluster size)
     int C = 1;
-    while (C < 8 && n > static_cast<int64_t>(C) * 8192) C *= 2;
+    while (C < kSortMaxCluster && n > static_cast<int64_t>(C) * 8192) C *= 2;
     const int64_t steps = (n + 31) / 32;
     int W = 4;
     while (W < kSortMaxWarps && static_cast<int64_t>(W) * C < steps) W *= 2;
-    const size_t smem = sizeof(int32_t) * (static_cast<size_t>(W) + 2) * E;
+    const size_t smem = sizeof(int32_t) * (static_cast<size_t>(W) + 2) * ((E + 3) & ~3);
     static_assert(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE <= kSmemLimit, "sort tables");
     if (smem > 48 * 1024) {
         const cudaError_t err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -342,19 +379,42 @@ bool rows_by_8(const void* p, int64_t ld, int dt, int D) {
     return D % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
 }
 
+namespace {
+
+template <int V, int DT>
+cudaError_t unpermute_as(const void* rows, int64_t ld_rows, int64_t n_rows, const int32_t* slot_pos, const float* w,
+                         int64_t T, int k, int D, void* y, int64_t ld_y, int dty, cudaStream_t s) {
+    const uint32_t chunks = static_cast<uint32_t>((D + 32 * V - 1) / (32 * V));
+    const uint32_t warps = chunks < 4 ? chunks : 4;
+    const uint32_t gy = T < 65535 ? static_cast<uint32_t>(T) : 65535u;
+    const dim3 grid((chunks + warps - 1) / warps, gy, static_cast<unsigned>((T + gy - 1) / gy));
+    unpermute_kernel<V, DT><<<grid, warps * 32, 0, s>>>(rows, ld_rows, n_rows, slot_pos, w, T, k, D, y, ld_y, dty, chunks);
+    return cudaGetLastError();
+}
+
+template <int V, int DT>
+cudaError_t unpermute_backward_as(const void* dy, int64_t ld_dy, int dty, const void* rows, int64_t ld_rows,
+                                  int64_t n_rows, const int32_t* slot_pos, const float* w, int64_t T, int k, int D,
+                                  void* d_rows, int64_t ld_d, float* d_w, cudaStream_t s) {
+    unpermute_backward_kernel<V, DT><<<blocks_of(T * k, 256), 256, 0, s>>>(
+        dy, ld_dy, dty, rows, ld_rows, n_rows, slot_pos, w, T * k, k, D, d_rows, ld_d, d_w);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_unpermute(const void* rows, int64_t ld_rows, int dt, int64_t n_rows, const int32_t* slot_pos,
                              const float* w, int64_t T, int k, int D, void* y, int64_t ld_y, int dty, cudaStream_t s) {
     const bool v8 = rows_by_8(rows, ld_rows, dt, D) && rows_by_8(y, ld_y, dty, D);
-    const int64_t chunks = (D + (v8 ? 255 : 31)) / (v8 ? 256 : 32);
-    const int64_t warps = T * chunks;
-    if (!grid_ok(warps, 128)) return cudaErrorInvalidValue;
-    if (v8)
-        unpermute_kernel<8><<<blocks_of(warps, 128), 128, 0, s>>>(rows, ld_rows, dt, n_rows, slot_pos, w, T, k, D, y,
-                                                                  ld_y, dty, chunks);
-    else
-        unpermute_kernel<1><<<blocks_of(warps, 128), 128, 0, s>>>(rows, ld_rows, dt, n_rows, slot_pos, w, T, k, D, y,
-                                                                  ld_y, dty, chunks);
-    return cudaGetLastError();
+    auto run = [&](auto f) { return f(rows, ld_rows, n_rows, slot_pos, w, T, k, D, y, ld_y, dty, s); };
+    if (v8) {
+        if (dt == ELEM_F32) return run(unpermute_as<8, ELEM_F32>);
+        if (dt == ELEM_BF16) return run(unpermute_as<8, ELEM_BF16>);
+        return run(unpermute_as<8, ELEM_F16>);
+    }
+    if (dt == ELEM_F32) return run(unpermute_as<1, ELEM_F32>);
+    if (dt == ELEM_BF16) return run(unpermute_as<1, ELEM_BF16>);
+    return run(unpermute_as<1, ELEM_F16>);
 }
 
 cudaError_t launch_unpermute_backward(const void* dy, int64_t ld_dy, int dty, const void* rows, int64_t ld_rows, int dt,
@@ -362,15 +422,18 @@ cudaError_t launch_unpermute_backward(const void* dy, int64_t ld_dy, int dty, co
                                       void* d_rows, int64_t ld_d, float* d_w, cudaStream_t s) {
     const bool v8 = rows_by_8(dy, ld_dy, dty, D) && (!d_w || rows_by_8(rows, ld_rows, dt, D)) &&
                     (!d_rows || rows_by_8(d_rows, ld_d, dt, D));
-    const int64_t warps = T * k;
-    if (!grid_ok(warps, 256)) return cudaErrorInvalidValue;
-    if (v8)
-        unpermute_backward_kernel<8><<<blocks_of(warps, 256), 256, 0, s>>>(
-            dy, ld_dy, dty, rows, ld_rows, dt, n_rows, slot_pos, w, T, k, D, d_rows, ld_d, d_w);
-    else
-        unpermute_backward_kernel<1><<<blocks_of(warps, 256), 256, 0, s>>>(
-            dy, ld_dy, dty, rows, ld_rows, dt, n_rows, slot_pos, w, T, k, D, d_rows, ld_d, d_w);
-    return cudaGetLastError();
+    if (!grid_ok(T * k, 256)) return cudaErrorInvalidValue;
+    auto run = [&](auto f) {
+        return f(dy, ld_dy, dty, rows, ld_rows, n_rows, slot_pos, w, T, k, D, d_rows, ld_d, d_w, s);
+    };
+    if (v8) {
+        if (dt == ELEM_F32) return run(unpermute_backward_as<8, ELEM_F32>);
+        if (dt == ELEM_BF16) return run(unpermute_backward_as<8, ELEM_BF16>);
+        return run(unpermute_backward_as<8, ELEM_F16>);
+    }
+    if (dt == ELEM_F32) return run(unpermute_backward_as<1, ELEM_F32>);
+    if (dt == ELEM_BF16) return run(unpermute_backward_as<1, ELEM_BF16>);
+    return run(unpermute_backward_as<1, ELEM_F16>);
 }
 
 }  // namespace moe

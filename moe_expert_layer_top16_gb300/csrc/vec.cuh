@@ -58,6 +58,20 @@ __device__ __forceinline__ RawVec<1> load_raw<1>(const void* base, int64_t off, 
     return r;
 }
 
+// Data that goes by once: loads and stores that leave L2 first.
+template <int V, int DT>
+__device__ __forceinline__ RawVec<V> load_stream(const void* base, int64_t off) {
+    RawVec<V> r;
+    if constexpr (V == 8) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + off * (DT == ELEM_F32 ? 4 : 2));
+        r.a = __ldcs(p);
+        if constexpr (DT == ELEM_F32) r.b = __ldcs(p + 1);
+    } else {
+        r = load_raw<1>(base, off, DT);
+    }
+    return r;
+}
+
 __device__ __forceinline__ void words_to_f32(const uint4& w, int dt, float* v) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -121,6 +135,20 @@ __device__ __forceinline__ void store_vec(void* base, int64_t off, int dt, const
         static_cast<__nv_bfloat16*>(base)[off] = __float2bfloat16_rn(v[0]);
     else
         static_cast<__half*>(base)[off] = __float2half_rn(v[0]);
+}
+
+template <int V, int DT>
+__device__ __forceinline__ void store_stream(void* base, int64_t off, const float (&v)[V]) {
+    if constexpr (V == 8 && DT == ELEM_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off);
+        __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+    } else if constexpr (V == 8) {
+        __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off),
+               make_uint4(pack2(v[0], v[1], DT), pack2(v[2], v[3], DT), pack2(v[4], v[5], DT), pack2(v[6], v[7], DT)));
+    } else {
+        store_vec(base, off, DT, v);
+    }
 }
 
 // The value that a store in type dt keeps.
