@@ -39,7 +39,8 @@ constexpr int kNormMaxStages = 8;
 // of threads takes every (8 m)-th row, so that its rows all start at the same
 // place in their first window and thread i owns the same columns in each.
 //
-// A row is owned by TPR threads; a block holds blockDim / TPR such groups.
+// A row is owned by a group of tpr threads; a block holds blockDim / tpr
+// groups, which share its weights.
 struct Rows {
     int tpr, lane_in_group, group, groups;
     int64_t first, step;        // rows first, first + step, ...
@@ -52,9 +53,9 @@ __device__ __forceinline__ Rows rows_of(int tpr, int64_t ld) {
     r.groups = blockDim.x / tpr;
     r.group = threadIdx.x / tpr;
     r.lane_in_group = threadIdx.x - r.group * tpr;
-    r.first = static_cast<int64_t>(blockIdx.x) * r.groups + r.group;
+    r.first = blockIdx.x + static_cast<int64_t>(gridDim.x) * r.group;
     r.step = static_cast<int64_t>(gridDim.x) * r.groups;
-    r.shift = static_cast<int>((r.first * ld) & (kNormVec - 1));
+    r.shift = static_cast<int>((blockIdx.x * ld) & (kNormVec - 1));
     return r;
 }
 
@@ -75,70 +76,182 @@ __device__ __forceinline__ void cp_async_wait(int n) {
     }
 }
 
+// Two fp32 values in a register pair: the packed multiply and add take two
+// elements an instruction.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 split(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float sum2(Pair p) {
+    const float2 f = split(p);
+    return f.x + f.y;
+}
+// A 16-bit pair as fp32.
+__device__ __forceinline__ Pair widen(uint32_t w, int dt) {
+    if (dt == ELEM_BF16) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    __half2 h;
+    memcpy(&h, &w, 4);
+    const float2 f = __half22float2(h);
+    return pair(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t narrow(Pair p, int dt) {
+    const float2 f = split(p);
+    return pack2(f.x, f.y, dt);
+}
+
+// Where a window lies in its row: EDGE instances have first and last windows
+// that are only partly inside.
+template <bool EDGE>
+__device__ __forceinline__ bool whole(int c, int D) {
+    return !EDGE || (c >= 0 && c + kNormVec <= D);
+}
+
 // One window of a row into this thread's own slots (a 16-byte slot, two for
 // fp32, `pitch` bytes apart): what a thread copies it alone reads, so that the
 // ring needs no barriers.  off: the window's first element in the matrix; c:
-// its column, negative in a first window that starts in the row before.
-__device__ __forceinline__ void fetch(uint8_t* slot, int pitch, const void* base, int64_t off, int c, int D, int dt) {
+// its column, negative in a first window that starts in the row before; left:
+// the matrix's elements from the window's first on.  A partial window is
+// copied whole while it lies inside the matrix (the values outside the row
+// are masked later); a window that reaches behind the matrix's last element
+// goes element by element.
+template <bool EDGE>
+__device__ __forceinline__ void fetch(uint8_t* slot, int pitch, const void* base, int64_t off, int c, int D, int dt,
+                                      int64_t left) {
     const uint8_t* src = static_cast<const uint8_t*>(base) + off * elem_bytes(dt);
-    if (c >= 0 && c + kNormVec <= D) {
-        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
-        cp_async16(dst, src);
-        if (dt == ELEM_F32) cp_async16(dst + pitch, src + 16);
-        return;
-    }
+    if constexpr (EDGE) {
+        if (left < kNormVec) {
 #pragma unroll 1
-    for (int j = 0; j < kNormVec; ++j) {
-        if (c + j < 0 || c + j >= D) continue;       // left as they are: never used
-        if (dt == ELEM_F32)
-            reinterpret_cast<uint32_t*>(slot + (j >> 2) * pitch)[j & 3] = reinterpret_cast<const uint32_t*>(src)[j];
-        else
-            reinterpret_cast<uint16_t*>(slot)[j] = reinterpret_cast<const uint16_t*>(src)[j];
+            for (int j = 0; j < kNormVec; ++j) {
+                if (c + j < 0 || c + j >= D) continue;
+                if (dt == ELEM_F32)
+                    reinterpret_cast<uint32_t*>(slot + (j >> 2) * pitch)[j & 3] = reinterpret_cast<const uint32_t*>(src)[j];
+                else
+                    reinterpret_cast<uint16_t*>(slot)[j] = reinterpret_cast<const uint16_t*>(src)[j];
+            }
+            return;
+        }
     }
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
+    cp_async16(dst, src);
+    if (dt == ELEM_F32) cp_async16(dst + pitch, src + 16);
 }
 
 // The window's values, zero outside the row.
-__device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, int c, int D, float (&v)[8]) {
-    RawVec<8> r;
-    r.a = *reinterpret_cast<const uint4*>(slot);
-    r.b = dt == ELEM_F32 ? *reinterpret_cast<const uint4*>(slot + pitch) : make_uint4(0, 0, 0, 0);
-    raw_to_f32(r, dt, v);
-    if (c < 0 || c + kNormVec > D) {
+template <bool EDGE>
+__device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, int c, int D, Pair (&v)[4]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(slot);
+    if (dt == ELEM_F32) {
+        const uint4 b = *reinterpret_cast<const uint4*>(slot + pitch);
+        v[0] = pair(__uint_as_float(a.x), __uint_as_float(a.y));
+        v[1] = pair(__uint_as_float(a.z), __uint_as_float(a.w));
+        v[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y));
+        v[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
+    } else {
+        v[0] = widen(a.x, dt);
+        v[1] = widen(a.y, dt);
+        v[2] = widen(a.z, dt);
+        v[3] = widen(a.w, dt);
+    }
+    if (!whole<EDGE>(c, D)) {
 #pragma unroll
-        for (int j = 0; j < kNormVec; ++j) v[j] = (c + j >= 0 && c + j < D) ? v[j] : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = split(v[j]);
+            const int e = c + 2 * j;
+            v[j] = pair(e >= 0 && e < D ? f.x : 0.0f, e + 1 >= 0 && e + 1 < D ? f.y : 0.0f);
+        }
     }
 }
 
-__device__ __forceinline__ void put(void* base, int64_t off, int c, int D, int dt, const float (&v)[8]) {
-    if (c >= 0 && c + kNormVec <= D) {
-        store_vec(base, off, dt, v);
+// Store a window, and leave in v the values as stored.
+template <bool EDGE, bool BACK>
+__device__ __forceinline__ void put(void* base, int64_t off, int c, int D, int dt, Pair (&v)[4]) {
+    uint8_t* dst = static_cast<uint8_t*>(base) + off * elem_bytes(dt);
+    if (dt == ELEM_F32) {
+        if (whole<EDGE>(c, D)) {
+            const float2 p = split(v[0]), q = split(v[1]), r = split(v[2]), s = split(v[3]);
+            reinterpret_cast<float4*>(dst)[0] = make_float4(p.x, p.y, q.x, q.y);
+            reinterpret_cast<float4*>(dst)[1] = make_float4(r.x, r.y, s.x, s.y);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = split(v[j]);
+                const int e = c + 2 * j;
+                if (e >= 0 && e < D) reinterpret_cast<float*>(dst)[2 * j] = f.x;
+                if (e + 1 >= 0 && e + 1 < D) reinterpret_cast<float*>(dst)[2 * j + 1] = f.y;
+            }
+        }
         return;
     }
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < kNormVec; ++j) {
-        const float o[1] = {v[j]};
-        if (c + j >= 0 && c + j < D) store_vec(base, off + j, dt, o);
+    for (int j = 0; j < 4; ++j) {
+        w[j] = narrow(v[j], dt);
+        if (BACK) v[j] = widen(w[j], dt);
+    }
+    if (whole<EDGE>(c, D)) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = c + 2 * j;
+            if (e >= 0 && e < D) reinterpret_cast<uint16_t*>(dst)[2 * j] = static_cast<uint16_t>(w[j] & 0xFFFFu);
+            if (e + 1 >= 0 && e + 1 < D) reinterpret_cast<uint16_t*>(dst)[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
+        }
     }
 }
 
-// A thread's weights wait in its own slots of shared memory, as fp32.
+// A column block's weights in shared memory, as fp32: two 16-byte slots
+// `pitch` bytes apart.
 __device__ __forceinline__ void keep(uint8_t* slot, int pitch, const float (&v)[8]) {
     *reinterpret_cast<float4*>(slot) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(slot + pitch) = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void kept(const uint8_t* slot, int pitch, float (&v)[8]) {
+__device__ __forceinline__ void kept(const uint8_t* slot, int pitch, Pair (&v)[4]) {
     const float4 a = *reinterpret_cast<const float4*>(slot), b = *reinterpret_cast<const float4*>(slot + pitch);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    v[0] = pair(a.x, a.y);
+    v[1] = pair(a.z, a.w);
+    v[2] = pair(b.x, b.y);
+    v[3] = pair(b.z, b.w);
 }
 
-// v *= the vector's columns c .. c + 7 (those inside the row).
-__device__ __forceinline__ void times_columns(float (&v)[8], const void* w, int c, int D, int dt) {
+// Columns c .. c + 7 of a weight vector (1 outside the row, or without one).
+// The eight loads are in flight together: one at a time they cost a launch of
+// few rows more than its rows.
+__device__ __forceinline__ void load_columns(float (&v)[8], const void* w, int c, int D, int dt) {
+    if (!w) {
 #pragma unroll
-    for (int j = 0; j < kNormVec; ++j) {
-        float f[1] = {1.0f};
-        if (c + j >= 0 && c + j < D) raw_to_f32(load_raw<1>(w, c + j, dt), dt, f);
-        v[j] *= f[0];
+        for (int j = 0; j < kNormVec; ++j) v[j] = 1.0f;
+    } else if (dt == ELEM_F32) {
+        const float* p = static_cast<const float*>(w);
+#pragma unroll
+        for (int j = 0; j < kNormVec; ++j) v[j] = (c + j >= 0 && c + j < D) ? __ldg(p + c + j) : 1.0f;
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(w);
+        uint16_t u[kNormVec];
+#pragma unroll
+        for (int j = 0; j < kNormVec; ++j)
+            u[j] = (c + j >= 0 && c + j < D) ? __ldg(p + c + j)
+                                             : static_cast<uint16_t>(dt == ELEM_BF16 ? 0x3F80 : 0x3C00);
+#pragma unroll
+        for (int j = 0; j < kNormVec; ++j)
+            v[j] = dt == ELEM_BF16 ? __uint_as_float(static_cast<uint32_t>(u[j]) << 16) : __half2float(__ushort_as_half(u[j]));
     }
 }
 
@@ -175,135 +288,120 @@ __device__ __forceinline__ float token_gate(const void* gate, int64_t t, int dt)
 // Slots a thread has for one window of type dt (none: no such matrix).
 __host__ __device__ __forceinline__ int window_slots(bool there, int dt) { return there ? (dt == ELEM_F32 ? 2 : 1) : 0; }
 
-// Forward.  A thread keeps `stages` batches of RB rows in flight by cp.async;
-// the rows of a batch share the barriers of the sums.  X, Y, U: element types
-// fixed at compile time (-1: as the arguments say).
-template <int NV, int RB, int MAXT, int X, int Y, int U>
-__global__ void __launch_bounds__(MAXT) block_norm_kernel(const NormArgs a, int tpr, int stages) {
+// Forward.  A group keeps `stages` rows in flight by cp.async.  X, Y, U:
+// element types fixed at compile time (-1: as the arguments say).
+template <int NV, bool EDGE, int X, int Y, int U>
+__global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int tpr, int stages) {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float red[2][RB][kNormMaxWarps];
+    __shared__ float red[2][1][kNormMaxWarps];
     int buf = 0;
     const int dx = X >= 0 ? X : a.dt_x, dy = Y >= 0 ? Y : a.dt_y, du = U >= 0 ? U : a.dt_u;
     const Rows g = rows_of(tpr, a.ld_x);
     const bool post = a.y != nullptr, pre = a.u != nullptr;
-    const int D = a.D;
-    const int T = static_cast<int>(a.T), row_step = static_cast<int>(g.step);
-    const int pitch = blockDim.x * 16;
+    const int D = a.D, T = static_cast<int>(a.T);
+    const int pitch = blockDim.x * 16, wpitch = tpr * 16;
     const int xw = window_slots(true, dx), yw = window_slots(post, dy), slots = xw + yw;
-    uint8_t* weights = ring + threadIdx.x * 16;                   // [NV][post 2, pre 2] slots
-    uint8_t* mine = weights + NV * 4 * pitch;                     // [stages][RB][NV][slots]
+    uint8_t* weights = ring + g.lane_in_group * 16;               // [NV][post 2, pre 2] slots, shared by the groups
+    uint8_t* mine = ring + NV * 4 * wpitch + threadIdx.x * 16;    // [stages][NV][slots]
     const int c0 = g.lane_in_group * kNormVec - g.shift, step = tpr * kNormVec;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-        if (post && a.w_post) times_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
-        if (post && a.gate_kind == NORM_GATE_CHANNEL) times_columns(w, a.gate, c0 + i * step, D, a.dt_w);
-        keep(weights + i * 4 * pitch, pitch, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-        if (pre && a.w_pre) times_columns(w, a.w_pre, c0 + i * step, D, a.dt_w);
-        keep(weights + (i * 4 + 2) * pitch, pitch, w);
-    }
     auto issue = [&](int64_t t, int stage) {
-        uint8_t* s = mine + stage * (RB * NV * slots * pitch);
-#pragma unroll
-        for (int b = 0; b < RB; ++b, t += row_step) {
-            if (t >= T) break;
+        if (t < T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
                 if (c >= D) break;
-                uint8_t* p = s + (b * NV + i) * slots * pitch;
-                if (post) fetch(p, pitch, a.y, t * a.ld_y + c, c, D, dy);
-                fetch(p + yw * pitch, pitch, a.x, t * a.ld_x + c, c, D, dx);
+                uint8_t* p = mine + (stage * NV + i) * slots * pitch;
+                if (post) fetch<EDGE>(p, pitch, a.y, t * a.ld_y + c, c, D, dy, (T - 1 - t) * a.ld_y + D - c);
+                fetch<EDGE>(p + yw * pitch, pitch, a.x, t * a.ld_x + c, c, D, dx, (T - 1 - t) * a.ld_x + D - c);
             }
         }
         cp_async_commit();
     };
-    for (int k = 0; k + 1 < stages; ++k) issue(g.first + static_cast<int64_t>(k) * RB * row_step, k);
+    for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step, k);
+    if (g.group == 0) {
+        const void* gate = a.gate_kind == NORM_GATE_CHANNEL ? a.gate : nullptr;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[8], f[8], n[8];
+            load_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
+            load_columns(f, gate, c0 + i * step, D, a.dt_w);
+            load_columns(n, a.w_pre, c0 + i * step, D, a.dt_w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] *= f[j];
+            keep(weights + i * 4 * wpitch, wpitch, w);
+            keep(weights + (i * 4 + 2) * wpitch, wpitch, n);
+        }
+    }
+    __syncthreads();
     int stage = 0, ahead = stages - 1;
     const float inv_d = 1.0f / static_cast<float>(D);
-    for (int64_t t = g.first; t < T; t += static_cast<int64_t>(RB) * row_step) {
-        issue(t + static_cast<int64_t>(stages - 1) * RB * row_step, ahead);
+    const Pair res = pair(a.res_scale, a.res_scale);
+    for (int64_t t = g.first; t < T; t += g.step) {
+        issue(t + (stages - 1) * g.step, ahead);
         if (++ahead == stages) ahead = 0;
         cp_async_wait(stages - 1);
-        const uint8_t* s = mine + stage * (RB * NV * slots * pitch);
+        const uint8_t* s = mine + stage * (NV * slots * pitch);
         if (++stage == stages) stage = 0;
-        float v[RB][NV][8];
-        float ss[RB];
+        Pair v[NV][4];
+        float q = 0.0f;
         if (post) {
-#pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                ss[b] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = c0 + i * step;
-                    if (c >= D || t + b * row_step >= T) break;
-                    unpack(s + (b * NV + i) * slots * pitch, pitch, dy, c, D, v[b][i]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ss[b] = fmaf(v[b][i][j], v[b][i][j], ss[b]);
-                }
-            }
-            group_sums<RB>(ss, g, red, buf);
-        }
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            const int64_t tb = t + b * row_step;
-            float q = 0.0f;
-            if (post) {
-                q = rsqrtf(ss[b] * inv_d + a.eps);
-                if (a.gate_kind == NORM_GATE_TOKEN && tb < T) q *= token_gate(a.gate, tb, a.dt_w);
-            }
-            ss[b] = 0.0f;
+            Pair acc = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
-                if (c >= D || tb >= T) break;
-                const uint8_t* p = s + ((b * NV + i) * slots + yw) * pitch;
-                if (post) {
-                    float x[8], w[8];
-                    unpack(p, pitch, dx, c, D, x);
-                    kept(weights + i * 4 * pitch, pitch, w);
+                if (c >= D) break;
+                unpack<EDGE>(s + i * slots * pitch, pitch, dy, c, D, v[i]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[b][i][j] = fmaf(a.res_scale, x[j], q * w[j] * v[b][i][j]);
-                    put(a.h, tb * a.ld_h + c, c, D, dx, v[b][i]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[b][i][j] = round_to(v[b][i][j], dx);
-                } else {
-                    unpack(p, pitch, dx, c, D, v[b][i]);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss[b] = fmaf(v[b][i][j], v[b][i][j], ss[b]);
+                for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
             }
+            float ss[1] = {sum2(acc)};
+            group_sums<1>(ss, g, red, buf);
+            q = rsqrtf(ss[0] * inv_d + a.eps);
+            if (a.gate_kind == NORM_GATE_TOKEN) q *= token_gate(a.gate, t, a.dt_w);
+        }
+        const Pair qq = pair(q, q);
+        Pair acc = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + i * step;
+            if (c >= D) break;
+            const uint8_t* p = s + (i * slots + yw) * pitch;
+            if (post) {
+                Pair x[4], w[4];
+                unpack<EDGE>(p, pitch, dx, c, D, x);
+                kept(weights + i * 4 * wpitch, wpitch, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = fma2(res, x[j], mul2(mul2(qq, w[j]), v[i][j]));
+                put<EDGE, true>(a.h, t * a.ld_h + c, c, D, dx, v[i]);
+            } else {
+                unpack<EDGE>(p, pitch, dx, c, D, v[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
         }
         if (pre) {
-            group_sums<RB>(ss, g, red, buf);
+            float ss[1] = {sum2(acc)};
+            group_sums<1>(ss, g, red, buf);
+            const float r = rsqrtf(ss[0] * inv_d + a.eps);
+            const Pair rr = pair(r, r);
 #pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                const int64_t tb = t + b * row_step;
-                const float r = rsqrtf(ss[b] * inv_d + a.eps);
+            for (int i = 0; i < NV; ++i) {
+                const int c = c0 + i * step;
+                if (c >= D) break;
+                Pair w[4];
+                kept(weights + (i * 4 + 2) * wpitch, wpitch, w);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = c0 + i * step;
-                    if (c >= D || tb >= T) break;
-                    float w[8];
-                    kept(weights + (i * 4 + 2) * pitch, pitch, w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[b][i][j] = v[b][i][j] * r * w[j];
-                    put(a.u, tb * a.ld_u + c, c, D, du, v[b][i]);
-                }
+                for (int j = 0; j < 4; ++j) v[i][j] = mul2(mul2(v[i][j], rr), w[j]);
+                put<EDGE, false>(a.u, t * a.ld_u + c, c, D, du, v[i]);
             }
         }
     }
 }
 
-// Gradients, with the same ring, a row at a time.  The column sums of a
-// thread's rows stay in registers (sum du h^ and sum total y^, times the
-// token's gate), are added over the block's groups through shared memory and
-// go to part[block][2][D].
-template <int NV, int MAXT, int X, int Y, int U>
+// Gradients, with the same ring.  The column sums of a thread's rows stay in
+// registers (sum du h^ and sum total y^, times the token's gate), are added
+// over the block's groups through shared memory and go to part[block][2][D].
+template <int NV, int MAXT, bool EDGE, int X, int Y, int U>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][3][kNormMaxWarps];
@@ -312,31 +410,12 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
     const int tx = X >= 0 ? X : a.dt_x, ty = Y >= 0 ? Y : a.dt_y, tu = U >= 0 ? U : a.dt_u;
     const bool post = a.y != nullptr, pre = a.du != nullptr, has_dh = a.dh != nullptr;
     const Rows g = rows_of(tpr, pre ? a.ld_h : a.ld_dh);
-    const int D = a.D;
-    const int T = static_cast<int>(a.T), row_step = static_cast<int>(g.step);
+    const int D = a.D, T = static_cast<int>(a.T);
     const int pitch = blockDim.x * 16;
     const int off_u = window_slots(pre, tx), off_d = off_u + window_slots(pre, tu), off_y = off_d + window_slots(has_dh, tx);
     const int slots = off_y + window_slots(post, ty);             // a window's
-    uint8_t* weights = ring + threadIdx.x * 16;                   // [NV][post 2, pre 2] slots
-    uint8_t* mine = weights + NV * 4 * pitch;                     // [stages][NV][slots]
+    uint8_t* mine = ring + threadIdx.x * 16;                      // [stages][NV][slots]
     const int c0 = g.lane_in_group * kNormVec - g.shift, step = tpr * kNormVec;
-    float s_pre[NV][8], s_post[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s_pre[i][j] = s_post[i][j] = 0.0f;
-            w[j] = 1.0f;
-        }
-        if (post && a.w_post) times_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
-        if (post && a.gate_kind == NORM_GATE_CHANNEL) times_columns(w, a.gate, c0 + i * step, D, a.dt_w);
-        keep(weights + i * 4 * pitch, pitch, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-        if (pre && a.w_pre) times_columns(w, a.w_pre, c0 + i * step, D, a.dt_w);
-        keep(weights + (i * 4 + 2) * pitch, pitch, w);
-    }
     auto issue = [&](int64_t t, int stage) {
         if (t < T) {
 #pragma unroll
@@ -345,146 +424,158 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
                 if (c >= D) break;
                 uint8_t* s = mine + (stage * NV + i) * slots * pitch;
                 if (pre) {
-                    fetch(s, pitch, a.h, t * a.ld_h + c, c, D, tx);
-                    fetch(s + off_u * pitch, pitch, a.du, t * a.ld_du + c, c, D, tu);
+                    fetch<EDGE>(s, pitch, a.h, t * a.ld_h + c, c, D, tx, (T - 1 - t) * a.ld_h + D - c);
+                    fetch<EDGE>(s + off_u * pitch, pitch, a.du, t * a.ld_du + c, c, D, tu, (T - 1 - t) * a.ld_du + D - c);
                 }
-                if (has_dh) fetch(s + off_d * pitch, pitch, a.dh, t * a.ld_dh + c, c, D, tx);
-                if (post) fetch(s + off_y * pitch, pitch, a.y, t * a.ld_y + c, c, D, ty);
+                if (has_dh) fetch<EDGE>(s + off_d * pitch, pitch, a.dh, t * a.ld_dh + c, c, D, tx, (T - 1 - t) * a.ld_dh + D - c);
+                if (post) fetch<EDGE>(s + off_y * pitch, pitch, a.y, t * a.ld_y + c, c, D, ty, (T - 1 - t) * a.ld_y + D - c);
             }
         }
         cp_async_commit();
     };
-    for (int k = 0; k + 1 < stages; ++k) issue(g.first + static_cast<int64_t>(k) * row_step, k);
+    for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step, k);
+    // this thread's weights: w_post (times a channel gate) and w_pre
+    Pair s_pre[NV][4], s_post[NV][4], wp[NV][4], wn[NV][4];
+    const void* gate_c = a.gate_kind == NORM_GATE_CHANNEL ? a.gate : nullptr;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float w[8], f[8], n[8];
+        load_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
+        load_columns(f, gate_c, c0 + i * step, D, a.dt_w);
+        load_columns(n, a.w_pre, c0 + i * step, D, a.dt_w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s_pre[i][j] = s_post[i][j] = 0;
+            wp[i][j] = pair(w[2 * j] * f[2 * j], w[2 * j + 1] * f[2 * j + 1]);
+            wn[i][j] = pair(n[2 * j], n[2 * j + 1]);
+        }
+    }
     int stage = 0, ahead = stages - 1;
     const float inv_d = 1.0f / static_cast<float>(D);
-    for (int64_t t = g.first; t < T; t += row_step) {
-        issue(t + static_cast<int64_t>(stages - 1) * row_step, ahead);
+    const Pair res = post ? pair(a.res_scale, a.res_scale) : pair(1.0f, 1.0f);
+    for (int64_t t = g.first; t < T; t += g.step) {
+        issue(t + (stages - 1) * g.step, ahead);
         if (++ahead == stages) ahead = 0;
         cp_async_wait(stages - 1);
         const uint8_t* s = mine + stage * (NV * slots * pitch);
         if (++stage == stages) stage = 0;
-        float sums[3] = {0.0f, 0.0f, 0.0f};     // h^2, a h, y^2
+        Pair hh = 0, uh = 0, yy = 0;            // h^2, a h, y^2
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
             if (c >= D) break;
             const uint8_t* p = s + i * slots * pitch;
             if (pre) {
-                float h[8], u[8], w[8];
-                unpack(p, pitch, tx, c, D, h);
-                unpack(p + off_u * pitch, pitch, tu, c, D, u);
-                kept(weights + (i * 4 + 2) * pitch, pitch, w);
+                Pair h[4], u[4];
+                unpack<EDGE>(p, pitch, tx, c, D, h);
+                unpack<EDGE>(p + off_u * pitch, pitch, tu, c, D, u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sums[0] = fmaf(h[j], h[j], sums[0]);
-                    sums[1] = fmaf(u[j] * w[j], h[j], sums[1]);
+                for (int j = 0; j < 4; ++j) {
+                    hh = fma2(h[j], h[j], hh);
+                    uh = fma2(mul2(u[j], wn[i][j]), h[j], uh);
                 }
             }
             if (post) {
-                float y[8];
-                unpack(p + off_y * pitch, pitch, ty, c, D, y);
+                Pair y[4];
+                unpack<EDGE>(p + off_y * pitch, pitch, ty, c, D, y);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sums[2] = fmaf(y[j], y[j], sums[2]);
+                for (int j = 0; j < 4; ++j) yy = fma2(y[j], y[j], yy);
             }
         }
+        float sums[3] = {sum2(hh), sum2(uh), sum2(yy)};
         group_sums<3>(sums, g, red, buf);
         const float r = rsqrtf(sums[0] * inv_d + a.eps);
         const float m = r * r * sums[1] * inv_d;       // mean(a h^) / rms(h)
         const float q = rsqrtf(sums[2] * inv_d + a.eps);
         const float gt = (post && a.gate_kind == NORM_GATE_TOKEN) ? token_gate(a.gate, t, a.dt_w) : 1.0f;
-        float total[NV][8];
-        float d[1] = {0.0f};                           // sum total w_post (channel gate) y
+        const Pair rr = pair(r, r), rm = pair(-r * m, -r * m), qg = pair(q * gt, q * gt);
+        Pair total[NV][4];
+        Pair py = 0;                                   // sum total w_post (channel gate) y
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
             if (c >= D) break;
             const uint8_t* p = s + i * slots * pitch;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) total[i][j] = 0.0f;
-            if (has_dh) unpack(p + off_d * pitch, pitch, tx, c, D, total[i]);
+            for (int j = 0; j < 4; ++j) total[i][j] = 0;
+            if (has_dh) unpack<EDGE>(p + off_d * pitch, pitch, tx, c, D, total[i]);
             if (pre) {
-                float h[8], u[8], w[8];
-                unpack(p, pitch, tx, c, D, h);
-                unpack(p + off_u * pitch, pitch, tu, c, D, u);
-                kept(weights + (i * 4 + 2) * pitch, pitch, w);
+                Pair h[4], u[4];
+                unpack<EDGE>(p, pitch, tx, c, D, h);
+                unpack<EDGE>(p + off_u * pitch, pitch, tu, c, D, u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s_pre[i][j] = fmaf(u[j], h[j] * r, s_pre[i][j]);
-                    total[i][j] += r * (u[j] * w[j] - h[j] * m);
+                for (int j = 0; j < 4; ++j) {
+                    const Pair ur = mul2(u[j], rr);
+                    s_pre[i][j] = fma2(ur, h[j], s_pre[i][j]);
+                    total[i][j] = fma2(h[j], rm, fma2(ur, wn[i][j], total[i][j]));
                 }
             }
             if (a.dx) {
-                float o[8];
+                Pair o[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = post ? a.res_scale * total[i][j] : total[i][j];
-                put(a.dx, t * a.ld_dx + c, c, D, tx, o);
+                for (int j = 0; j < 4; ++j) o[j] = mul2(res, total[i][j]);
+                put<EDGE, false>(a.dx, t * a.ld_dx + c, c, D, tx, o);
             }
             if (post) {
-                float y[8], w[8];
-                unpack(p + off_y * pitch, pitch, ty, c, D, y);
-                kept(weights + i * 4 * pitch, pitch, w);
+                Pair y[4];
+                unpack<EDGE>(p + off_y * pitch, pitch, ty, c, D, y);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s_post[i][j] = fmaf(total[i][j] * gt, y[j] * q, s_post[i][j]);
-                    total[i][j] *= w[j];
-                    d[0] = fmaf(total[i][j], y[j], d[0]);
+                for (int j = 0; j < 4; ++j) {
+                    s_post[i][j] = fma2(total[i][j], mul2(y[j], qg), s_post[i][j]);
+                    total[i][j] = mul2(total[i][j], wp[i][j]);
+                    py = fma2(total[i][j], y[j], py);
                 }
             }
         }
         if (post) {
+            float d[1] = {sum2(py)};
             group_sums<1>(d, g, red1, buf1);
             if (a.d_gate_token && g.lane_in_group == 0) a.d_gate_token[t] = d[0] * q;
             if (a.dy) {
-                const float n = q * q * d[0] * inv_d;      // mean(p y^) / (g rms(y))
-                const float f = q * gt;
+                const float n = -q * q * d[0] * inv_d;     // -mean(p y^) / (g rms(y))
+                const Pair nn = pair(n, n);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = c0 + i * step;
                     if (c >= D) break;
-                    float y[8], o[8];
-                    unpack(s + (i * slots + off_y) * pitch, pitch, ty, c, D, y);
+                    Pair y[4];
+                    unpack<EDGE>(s + (i * slots + off_y) * pitch, pitch, ty, c, D, y);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = f * (total[i][j] - y[j] * n);
-                    put(a.dy, t * a.ld_dy + c, c, D, ty, o);
+                    for (int j = 0; j < 4; ++j) y[j] = mul2(qg, fma2(y[j], nn, total[i][j]));
+                    put<EDGE, false>(a.dy, t * a.ld_dy + c, c, D, ty, y);
                 }
             }
         }
     }
     if (!a.part) return;
     float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * D;
-    if (g.groups == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = c0 + i * step + j;
-                if (c >= 0 && c < D) {
-                    out[c] = s_pre[i][j];
-                    out[D + c] = s_post[i][j];
-                }
-            }
-        return;
-    }
-    // groups in turn add their columns (their windows may start at different
-    // columns) to the block's, in the ring's memory
+    // the groups in turn add their columns to the block's, in the ring's
+    // memory (one group: straight to the part)
+    float* acc = g.groups == 1 ? out : reinterpret_cast<float*>(ring);
     cp_async_wait(0);
-    float* acc = reinterpret_cast<float*>(ring);
     __syncthreads();
     for (int k = 0; k < g.groups; ++k) {
-        if (g.group == k)
+        if (g.group == k) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = c0 + i * step + j;
+                for (int j = 0; j < 4; ++j) {
+                    const int c = c0 + i * step + 2 * j;
+                    const float2 f = split(s_pre[i][j]), e = split(s_post[i][j]);
                     if (c >= 0 && c < D) {
-                        acc[c] = (k ? acc[c] : 0.0f) + s_pre[i][j];
-                        acc[D + c] = (k ? acc[D + c] : 0.0f) + s_post[i][j];
+                        acc[c] = (k ? acc[c] : 0.0f) + f.x;
+                        acc[D + c] = (k ? acc[D + c] : 0.0f) + e.x;
+                    }
+                    if (c + 1 >= 0 && c + 1 < D) {
+                        acc[c + 1] = (k ? acc[c + 1] : 0.0f) + f.y;
+                        acc[D + c + 1] = (k ? acc[D + c + 1] : 0.0f) + e.y;
                     }
                 }
+        }
         __syncthreads();
     }
-    for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) out[c] = acc[c];
+    if (g.groups > 1)
+        for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) out[c] = acc[c];
 }
 
 // ------------------------------------------------------------------ rows element by element
@@ -691,55 +782,54 @@ struct Alike {
     }
 };
 
-// How a launch covers T rows of D elements.  Threads own one window each up to
-// max_threads windows a row, two beyond; rows of few windows share a block of
-// about 256 threads.  The ring takes what an SM's shared memory gives to the
-// blocks that its registers hold, up to eight batches of rows.
+// How a launch covers T rows of D elements: a group of tpr threads owns a row,
+// nv windows a thread; the ring takes the shared memory that is left, up to
+// eight rows a group.
 struct Shape {
     int nv, tpr, threads, stages, grid;
+    bool edge;                  // some windows lie only partly in their row
     size_t smem;
 };
 constexpr int kNormSmem = kSmemLimit - 2048;     // without the sums' static part
 
-bool shape_of(int64_t T, int D, const Alike& al, int slots, int batch, int max_threads, int max_nv, int regs, int sms,
-              int most, Shape* s) {
+// two_from: rows of more windows than this have two a thread; group_threads:
+// threads of a block's groups together at most; weight_slots: shared 16-byte
+// slots a window; regs: of a thread.
+bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int group_threads, int weight_slots, int regs,
+              int sms, int most, Shape* s) {
     if (!al.ok) return false;
     const int windows = (D + (al.odd ? kNormVec - 1 : 0) + kNormVec - 1) / kNormVec;
-    if (windows > max_nv * max_threads) return false;
-    s->nv = 1;
-    while (s->nv * max_threads < windows) s->nv *= 2;
-    if (s->nv > 1) batch = 1;
+    if (windows > 2 * 1024) return false;
+    s->edge = al.odd || D % kNormVec;
+    s->nv = windows > two_from ? 2 : 1;
     s->tpr = ((windows + s->nv - 1) / s->nv + 31) / 32 * 32;
-    int groups = s->tpr >= 256 ? 1 : 256 / s->tpr;
-    while (groups > 1 && static_cast<int64_t>(groups) * sms > T) groups /= 2;      // few rows: over the SMs first
+    const int stage = s->nv * slots * 16, fixed = s->nv * weight_slots * s->tpr * 16;      // bytes a thread; a block
+    int groups = std::max(1, std::min(group_threads / s->tpr, 8));
+    while (groups > 1 && (static_cast<int64_t>(groups) * sms > T || 2 * groups * s->tpr * stage + fixed > kNormSmem)) --groups;
     s->threads = s->tpr * groups;
-    int per_sm = 65536 / (regs * s->threads);
-    per_sm = std::max(1, std::min(per_sm, 2048 / s->threads));
-    const int stage = s->nv * batch * slots * s->threads * 16, fixed = s->nv * 4 * s->threads * 16;
-    // at least two batches in flight a block
-    while (per_sm > 1 && per_sm * (2 * stage + fixed + 1024) > kNormSmem) --per_sm;
+    int per_sm = std::max(1, std::min(65536 / (regs * s->threads), 2048 / s->threads));
+    // at least two rows in flight a group
+    while (per_sm > 1 && per_sm * (2 * stage * s->threads + fixed + 1024) > kNormSmem) --per_sm;
     int64_t grid = std::min<int64_t>((T + groups - 1) / groups, static_cast<int64_t>(sms) * per_sm);
     if (grid > most) grid = most;
-    if (al.odd && grid * groups < T) {
-        // a row's place in its windows has to be the same in all rows of a
-        // group: blocks x groups is a multiple of 8
-        const int64_t unit = groups >= 8 ? 1 : 8 / groups;
-        if (grid < unit) return false;
-        grid = grid / unit * unit;
+    // a row's place in its windows has to be the same in all rows of a block
+    if (al.odd && (groups > 1 || grid < T)) {
+        if (grid < 8) return false;
+        grid = grid / 8 * 8;
     }
     s->grid = static_cast<int>(grid);
     const int per_block = std::min<int>(per_sm, static_cast<int>((grid + sms - 1) / sms));
-    const int64_t batches = (T + grid * groups * batch - 1) / (grid * groups * batch);  // of a group at most
-    int st = (kNormSmem / per_block - 1024 - fixed) / stage;
+    const int64_t rows = (T + grid * groups - 1) / (grid * groups);                        // of a group at most
+    int st = (kNormSmem / per_block - 1024 - fixed) / (stage * s->threads);
     st = std::max(1, std::min<int>(st, kNormMaxStages));
-    s->stages = static_cast<int>(std::min<int64_t>(st, batches));
-    s->smem = static_cast<size_t>(s->stages) * stage + fixed;
+    s->stages = static_cast<int>(std::min<int64_t>(st, rows));
+    s->smem = static_cast<size_t>(s->stages) * stage * s->threads + fixed;
     return s->smem <= static_cast<size_t>(kNormSmem);
 }
 
 template <typename Args>
 cudaError_t run_rows(void (*kern)(Args, int, int), const Args& a, const Shape& sh, size_t smem, cudaStream_t s) {
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {         // with the static part, up to 48 KB need no attribute
         const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
         if (err != cudaSuccess) return err;
     }
@@ -747,19 +837,18 @@ cudaError_t run_rows(void (*kern)(Args, int, int), const Args& a, const Shape& s
     return cudaGetLastError();
 }
 
-// Threads at most, by windows a thread: the forward kernel holds a batch of
-// two rows at one window; the backward kernel's column sums take more
-// registers, 896 threads leave it 72.
-template <int X, int Y, int U>
+template <bool EDGE, int X, int Y, int U>
 cudaError_t forward_as(const NormArgs& a, const Shape& sh, cudaStream_t s) {
-    if (sh.nv == 2) return run_rows(block_norm_kernel<2, 1, 1024, X, Y, U>, a, sh, sh.smem, s);
-    return run_rows(block_norm_kernel<1, 2, 1024, X, Y, U>, a, sh, sh.smem, s);
+    if (sh.nv == 2) return run_rows(block_norm_kernel<2, EDGE, X, Y, U>, a, sh, sh.smem, s);
+    return run_rows(block_norm_kernel<1, EDGE, X, Y, U>, a, sh, sh.smem, s);
 }
-template <int X, int Y, int U>
+// Two windows a thread take about 120 registers (column sums, weights and the
+// row's gradient): 512 threads; wider rows take 1,024 threads and spill.
+template <bool EDGE, int X, int Y, int U>
 cudaError_t backward_as(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
-    if (sh.nv == 2) return run_rows(block_norm_backward_kernel<2, 1024, X, Y, U>, a, sh, smem, s);
-    if (sh.threads > 896) return run_rows(block_norm_backward_kernel<1, 1024, X, Y, U>, a, sh, smem, s);
-    return run_rows(block_norm_backward_kernel<1, 896, X, Y, U>, a, sh, smem, s);
+    if (sh.nv == 1) return run_rows(block_norm_backward_kernel<1, 512, EDGE, X, Y, U>, a, sh, smem, s);
+    if (sh.threads <= 512) return run_rows(block_norm_backward_kernel<2, 512, EDGE, X, Y, U>, a, sh, smem, s);
+    return run_rows(block_norm_backward_kernel<2, 1024, true, -1, -1, -1>, a, sh, smem, s);
 }
 
 int plain_threads(int D) { return std::min(1024, std::max(32, (D + kPlainColumns / 4 - 1) / (kPlainColumns / 4) + 31) / 32 * 32); }
@@ -785,11 +874,19 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     al.add(a.u, a.ld_u);
     Shape sh;
     const int slots = window_slots(true, a.dt_x) + window_slots(a.y, a.dt_y);
-    if (shape_of(a.T, a.D, al, slots, 2, 1024, 2, 64, sms, 1 << 30, &sh)) {
+    // 896 threads in two groups of 448 for 7,168 elements: the one group's
+    // sums overlap the other's loads and stores
+    if (shape_of(a.T, a.D, al, slots, 256, 1024, 4, 64, sms, 1 << 30, &sh)) {
         const bool b = a.dt_x == ELEM_BF16 && (!a.u || a.dt_u == ELEM_BF16);
-        if (b && (!a.y || a.dt_y == ELEM_BF16)) return forward_as<ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, s);
-        if (b && a.dt_y == ELEM_F32) return forward_as<ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, s);
-        return forward_as<-1, -1, -1>(a, sh, s);
+        const bool f = a.dt_x == ELEM_F32 && (!a.u || a.dt_u == ELEM_F32) && (!a.y || a.dt_y == ELEM_F32);
+        if (b && (!a.y || a.dt_y == ELEM_BF16))
+            return sh.edge ? forward_as<true, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, s)
+                           : forward_as<false, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, s);
+        if (f)
+            return sh.edge ? forward_as<true, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, s)
+                           : forward_as<false, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, s);
+        if (b && a.dt_y == ELEM_F32 && !sh.edge) return forward_as<false, ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, s);
+        return forward_as<true, -1, -1, -1>(a, sh, s);
     }
     const int threads = plain_threads(a.D);
     block_norm_plain_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.T, static_cast<int64_t>(sms) * (2048 / threads))),
@@ -819,15 +916,24 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     const int most = norm_parts(a.T, a.D);
     Shape sh;
     int parts;
-    if (shape_of(a.T, a.D, al, slots, 1, 1024, 2, 72, sms, most, &sh)) {
+    if (shape_of(a.T, a.D, al, slots, 512, 512, 0, 128, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
         if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.D));
         parts = sh.grid;
-        const bool b = (!(a.h || a.dh || a.dx) || a.dt_x == ELEM_BF16) && (!a.du || a.dt_u == ELEM_BF16);
-        if (b && (!a.y || a.dt_y == ELEM_BF16)) err = backward_as<ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, smem, s);
-        else if (b && a.dt_y == ELEM_F32) err = backward_as<ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, smem, s);
-        else err = backward_as<-1, -1, -1>(a, sh, smem, s);
+        const bool rows = a.h || a.dh || a.dx;
+        const bool b = (!rows || a.dt_x == ELEM_BF16) && (!a.du || a.dt_u == ELEM_BF16);
+        const bool f = (!rows || a.dt_x == ELEM_F32) && (!a.du || a.dt_u == ELEM_F32) && (!a.y || a.dt_y == ELEM_F32);
+        if (b && (!a.y || a.dt_y == ELEM_BF16))
+            err = sh.edge ? backward_as<true, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, smem, s)
+                          : backward_as<false, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, smem, s);
+        else if (f)
+            err = sh.edge ? backward_as<true, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, smem, s)
+                          : backward_as<false, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, smem, s);
+        else if (b && a.dt_y == ELEM_F32 && !sh.edge)
+            err = backward_as<false, ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, smem, s);
+        else
+            err = backward_as<true, -1, -1, -1>(a, sh, smem, s);
     } else {
         parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.T, most), 2 * sms));
         const int threads = std::min(1024, (a.D + 31) / 32 * 32);

@@ -352,7 +352,7 @@ cudaError_t launch_sort(const int32_t* idx, int64_t n, int E, int32_t* offsets, 
     while (W < kSortMaxWarps && static_cast<int64_t>(W) * C < steps) W *= 2;
     const size_t smem = sizeof(int32_t) * (static_cast<size_t>(W) + 2) * ((E + 3) & ~3);
     static_assert(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE <= kSmemLimit, "sort tables");
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {         // with the static part, up to 48 KB need no attribute
         const cudaError_t err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      static_cast<int>(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE));
         if (err != cudaSuccess) return err;

@@ -202,3 +202,29 @@ def test_same_call_same_bits():
                                            w_pre=s["w_pre"], gate=s["gate"])
     a, b = call(), call()
     assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.parametrize("D", [1, 2, 3, 5, 7, 9, 13, 255, 1003])
+@pytest.mark.parametrize("T", [1, 2, 9, 1300])
+def test_narrow_and_odd_rows(T, D):
+    """Rows that share 16-byte words: neighbours and what lies behind the last row stay as they were."""
+    for t in (F32, BF16):
+        s = make(T, D, t, t, F32, None, seed=T + D)
+        w, r = s["w_post"], s["w_pre"]
+        flat = torch.full((T * D + 64,), 3.0, device=DEV).to(t)
+        h_out, u_out = flat[:T * D].view(T, D), flat.clone()[:T * D].view(T, D)
+        h, u = moe.block_norm(s["x"], s["y"], w_post=w, w_pre=r, res_scale=0.75, eps=EPS, out_h=h_out, out_u=u_out)
+        assert (flat[T * D:] == 3).all()
+        c = (D / 64 + 16) * 2.0 ** -24
+        add = w.double() * s["y"].double() / rms(s["y"].double())
+        ref = 0.75 * s["x"].double() + add
+        tol = add.abs() * c + ref.abs() * 2.0 ** -23
+        assert ((h.double() - ref).abs() <= tol + (ref.abs() + tol) * HALF[t] + TINY[t]).all()
+        f = h.double()
+        ref = r.double() * f / rms(f)
+        assert ((u.double() - ref).abs() <= ref.abs() * (c + HALF[t] * (1 + c)) + TINY[t]).all()
+        got = moe.block_norm_backward(s["dh"], None, h, s["y"], w_post=w, res_scale=0.75, eps=EPS)
+        yh = s["y"].double() / rms(s["y"].double())
+        terms = s["dh"].double() * yh
+        tol = terms.abs().sum(0) * (2 * c + (T + 24) * 2.0 ** -24)
+        assert ((got["dw_post"].double() - terms.sum(0)).abs() <= tol).all()
