@@ -406,7 +406,7 @@ MOE_API moe_status moe_unpermute_backward(const void *dy, int64_t ld_dy, int32_t
  * the gate are not used).  u = NULL: only h.  w_post / w_pre = NULL: ones.
  * The gate is a value a channel ([D]), a value a token ([T]), or absent.
  * Weights and gate share one type.  h has x's type and may be x itself (same
- * address and stride).  T >= 0, 1 <= D <= 16384, eps >= 0. */
+ * address and stride).  0 <= T <= 2^30, 1 <= D <= 16384, eps >= 0. */
 typedef enum {
     MOE_GATE_NONE = 0,
     MOE_GATE_CHANNEL = 1,

@@ -1539,7 +1539,7 @@ moe_status moe_unpermute_backward(const void* dy, int64_t ld_dy, int32_t dy_dtyp
 }
 
 moe_status moe_block_norm(const moe_block_norm_args* p, void* stream) {
-    if (!p || p->T < 0 || p->D < 1 || p->D > kNormMaxWidth || !known_dtype(p->x_dtype) || !(p->eps >= 0.0f))
+    if (!p || p->T < 0 || p->T > kNormMaxRows || p->D < 1 || p->D > kNormMaxWidth || !known_dtype(p->x_dtype) || !(p->eps >= 0.0f))
         return MOE_ERR_INVALID_ARG;
     if ((!p->y && !p->u) || (p->y && !p->h)) return MOE_ERR_INVALID_ARG;
     if (p->gate_kind != MOE_GATE_NONE && p->gate_kind != MOE_GATE_CHANNEL && p->gate_kind != MOE_GATE_TOKEN)
@@ -1589,7 +1589,7 @@ size_t moe_block_norm_workspace_bytes(int32_t T, int32_t D) {
 }
 
 moe_status moe_block_norm_backward(const moe_block_norm_backward_args* p, void* stream) {
-    if (!p || p->T < 0 || p->D < 1 || p->D > kNormMaxWidth || !known_dtype(p->x_dtype) || !(p->eps >= 0.0f))
+    if (!p || p->T < 0 || p->T > kNormMaxRows || p->D < 1 || p->D > kNormMaxWidth || !known_dtype(p->x_dtype) || !(p->eps >= 0.0f))
         return MOE_ERR_INVALID_ARG;
     if (p->gate_kind != MOE_GATE_NONE && p->gate_kind != MOE_GATE_CHANNEL && p->gate_kind != MOE_GATE_TOKEN)
         return MOE_ERR_INVALID_ARG;

@@ -322,6 +322,7 @@ cudaError_t launch_unpermute_backward(const void* dy, int64_t ld_dy, int dty, co
 // ------------------------------------------------------------------ norms round a block (norm.cu)
 enum NormGate : int { NORM_GATE_NONE = 0, NORM_GATE_CHANNEL = 1, NORM_GATE_TOKEN = 2 };
 constexpr int kNormMaxWidth = 16384;
+constexpr int kNormMaxRows = 1 << 30;    // row numbers some steps ahead stay inside 32 bits
 constexpr int kNormParts = 304;
 int norm_parts(int64_t T, int D);        // blocks of a backward pass (rows of partial column sums) at most
 struct NormArgs {

@@ -279,6 +279,36 @@ __device__ __forceinline__ void group_sums(float (&v)[N], const Rows& g, float (
     buf ^= 1;
 }
 
+// Three sums at once: the lanes halve what they carry with each exchange (two
+// values after the first, one after the second), so that six exchanges do what
+// fifteen would; lane 8 k then holds value k of the warp.
+__device__ __forceinline__ void group_sums3(float (&v)[3], const Rows& g, float (*red)[4][kNormMaxWarps], int& buf) {
+    const int lane = threadIdx.x & 31;
+    const bool up = lane & 16, odd = lane & 8;
+    // lanes 0-15 keep values 0 and 1, lanes 16-31 value 2
+    float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
+    float b = __shfl_xor_sync(0xffffffffu, v[1], 16);
+    a += up ? v[2] : v[0];
+    b = up ? 0.0f : b + v[1];
+    const float c = __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+    float s = (odd ? b : a) + c;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (g.tpr > 32) {
+        const int warp = threadIdx.x >> 5, warps = g.tpr >> 5, warp0 = g.group * warps;
+        if ((lane & 7) == 0) red[buf][lane >> 3][warp] = s;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
+        s = 0.0f;
+        for (int w = lane & 7; w < warps; w += 8) s += red[buf][lane >> 3][warp0 + w];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        buf ^= 1;
+    }
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+    v[1] = __shfl_sync(0xffffffffu, s, 8);
+    v[2] = __shfl_sync(0xffffffffu, s, 16);
+}
+
 __device__ __forceinline__ float token_gate(const void* gate, int64_t t, int dt) {
     float g[1];
     raw_to_f32(load_raw<1>(gate, t, dt), dt, g);
@@ -401,60 +431,67 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 // Gradients, with the same ring.  The column sums of a thread's rows stay in
 // registers (sum du h^ and sum total y^, times the token's gate), are added
 // over the block's groups through shared memory and go to part[block][2][D].
+// The weights wait in shared memory, which leaves registers for 28 warps.
 template <int NV, int MAXT, bool EDGE, int X, int Y, int U>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages) {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float red[2][3][kNormMaxWarps];
+    __shared__ float red[2][4][kNormMaxWarps];
     __shared__ float red1[2][1][kNormMaxWarps];
     int buf = 0, buf1 = 0;
     const int tx = X >= 0 ? X : a.dt_x, ty = Y >= 0 ? Y : a.dt_y, tu = U >= 0 ? U : a.dt_u;
     const bool post = a.y != nullptr, pre = a.du != nullptr, has_dh = a.dh != nullptr;
     const Rows g = rows_of(tpr, pre ? a.ld_h : a.ld_dh);
-    const int D = a.D, T = static_cast<int>(a.T);
-    const int pitch = blockDim.x * 16;
+    const int D = a.D, T = static_cast<int>(a.T), row_step = static_cast<int>(g.step);
+    const int pitch = blockDim.x * 16, wpitch = tpr * 16;
     const int off_u = window_slots(pre, tx), off_d = off_u + window_slots(pre, tu), off_y = off_d + window_slots(has_dh, tx);
     const int slots = off_y + window_slots(post, ty);             // a window's
-    uint8_t* mine = ring + threadIdx.x * 16;                      // [stages][NV][slots]
+    uint8_t* weights = ring + g.lane_in_group * 16;               // [NV][post 2, pre 2] slots, shared by the groups
+    uint8_t* mine = ring + NV * 4 * wpitch + threadIdx.x * 16;    // [stages][NV][slots]
     const int c0 = g.lane_in_group * kNormVec - g.shift, step = tpr * kNormVec;
-    auto issue = [&](int64_t t, int stage) {
+    auto issue = [&](int t, int stage) {
         if (t < T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
                 if (c >= D) break;
                 uint8_t* s = mine + (stage * NV + i) * slots * pitch;
+                // only the last rows have windows that reach behind the matrix
+                const int64_t rows_left = (EDGE && t + kNormVec >= T) ? T - 1 - t : kNormVec;
                 if (pre) {
-                    fetch<EDGE>(s, pitch, a.h, t * a.ld_h + c, c, D, tx, (T - 1 - t) * a.ld_h + D - c);
-                    fetch<EDGE>(s + off_u * pitch, pitch, a.du, t * a.ld_du + c, c, D, tu, (T - 1 - t) * a.ld_du + D - c);
+                    fetch<EDGE>(s, pitch, a.h, t * a.ld_h + c, c, D, tx, rows_left * a.ld_h + D - c);
+                    fetch<EDGE>(s + off_u * pitch, pitch, a.du, t * a.ld_du + c, c, D, tu, rows_left * a.ld_du + D - c);
                 }
-                if (has_dh) fetch<EDGE>(s + off_d * pitch, pitch, a.dh, t * a.ld_dh + c, c, D, tx, (T - 1 - t) * a.ld_dh + D - c);
-                if (post) fetch<EDGE>(s + off_y * pitch, pitch, a.y, t * a.ld_y + c, c, D, ty, (T - 1 - t) * a.ld_y + D - c);
+                if (has_dh) fetch<EDGE>(s + off_d * pitch, pitch, a.dh, t * a.ld_dh + c, c, D, tx, rows_left * a.ld_dh + D - c);
+                if (post) fetch<EDGE>(s + off_y * pitch, pitch, a.y, t * a.ld_y + c, c, D, ty, rows_left * a.ld_y + D - c);
             }
         }
         cp_async_commit();
     };
-    for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step, k);
-    // this thread's weights: w_post (times a channel gate) and w_pre
-    Pair s_pre[NV][4], s_post[NV][4], wp[NV][4], wn[NV][4];
-    const void* gate_c = a.gate_kind == NORM_GATE_CHANNEL ? a.gate : nullptr;
+    for (int k = 0; k + 1 < stages; ++k) issue(static_cast<int>(g.first) + k * row_step, k);
+    if (g.group == 0) {
+        const void* gate = a.gate_kind == NORM_GATE_CHANNEL ? a.gate : nullptr;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float w[8], f[8], n[8];
-        load_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
-        load_columns(f, gate_c, c0 + i * step, D, a.dt_w);
-        load_columns(n, a.w_pre, c0 + i * step, D, a.dt_w);
+        for (int i = 0; i < NV; ++i) {
+            float w[8], f[8], n[8];
+            load_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
+            load_columns(f, gate, c0 + i * step, D, a.dt_w);
+            load_columns(n, a.w_pre, c0 + i * step, D, a.dt_w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            s_pre[i][j] = s_post[i][j] = 0;
-            wp[i][j] = pair(w[2 * j] * f[2 * j], w[2 * j + 1] * f[2 * j + 1]);
-            wn[i][j] = pair(n[2 * j], n[2 * j + 1]);
+            for (int j = 0; j < 8; ++j) w[j] *= f[j];
+            keep(weights + i * 4 * wpitch, wpitch, w);
+            keep(weights + (i * 4 + 2) * wpitch, wpitch, n);
         }
     }
+    Pair s_pre[NV][4], s_post[NV][4];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s_pre[i][j] = s_post[i][j] = 0;
+    __syncthreads();
     int stage = 0, ahead = stages - 1;
     const float inv_d = 1.0f / static_cast<float>(D);
-    const Pair res = post ? pair(a.res_scale, a.res_scale) : pair(1.0f, 1.0f);
-    for (int64_t t = g.first; t < T; t += g.step) {
-        issue(t + (stages - 1) * g.step, ahead);
+    for (int t = static_cast<int>(g.first); t < T; t += row_step) {
+        issue(t + (stages - 1) * row_step, ahead);
         if (++ahead == stages) ahead = 0;
         cp_async_wait(stages - 1);
         const uint8_t* s = mine + stage * (NV * slots * pitch);
@@ -466,13 +503,14 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             if (c >= D) break;
             const uint8_t* p = s + i * slots * pitch;
             if (pre) {
-                Pair h[4], u[4];
+                Pair h[4], u[4], w[4];
                 unpack<EDGE>(p, pitch, tx, c, D, h);
                 unpack<EDGE>(p + off_u * pitch, pitch, tu, c, D, u);
+                kept(weights + (i * 4 + 2) * wpitch, wpitch, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     hh = fma2(h[j], h[j], hh);
-                    uh = fma2(mul2(u[j], wn[i][j]), h[j], uh);
+                    uh = fma2(mul2(u[j], w[j]), h[j], uh);
                 }
             }
             if (post) {
@@ -483,7 +521,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             }
         }
         float sums[3] = {sum2(hh), sum2(uh), sum2(yy)};
-        group_sums<3>(sums, g, red, buf);
+        group_sums3(sums, g, red, buf);
         const float r = rsqrtf(sums[0] * inv_d + a.eps);
         const float m = r * r * sums[1] * inv_d;       // mean(a h^) / rms(h)
         const float q = rsqrtf(sums[2] * inv_d + a.eps);
@@ -500,29 +538,33 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             for (int j = 0; j < 4; ++j) total[i][j] = 0;
             if (has_dh) unpack<EDGE>(p + off_d * pitch, pitch, tx, c, D, total[i]);
             if (pre) {
-                Pair h[4], u[4];
+                Pair h[4], u[4], w[4];
                 unpack<EDGE>(p, pitch, tx, c, D, h);
                 unpack<EDGE>(p + off_u * pitch, pitch, tu, c, D, u);
+                kept(weights + (i * 4 + 2) * wpitch, wpitch, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const Pair ur = mul2(u[j], rr);
                     s_pre[i][j] = fma2(ur, h[j], s_pre[i][j]);
-                    total[i][j] = fma2(h[j], rm, fma2(ur, wn[i][j], total[i][j]));
+                    total[i][j] = fma2(h[j], rm, fma2(ur, w[j], total[i][j]));
                 }
             }
             if (a.dx) {
+                const float rs = post ? a.res_scale : 1.0f;
+                const Pair res = pair(rs, rs);
                 Pair o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[j] = mul2(res, total[i][j]);
                 put<EDGE, false>(a.dx, t * a.ld_dx + c, c, D, tx, o);
             }
             if (post) {
-                Pair y[4];
+                Pair y[4], w[4];
                 unpack<EDGE>(p + off_y * pitch, pitch, ty, c, D, y);
+                kept(weights + i * 4 * wpitch, wpitch, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     s_post[i][j] = fma2(total[i][j], mul2(y[j], qg), s_post[i][j]);
-                    total[i][j] = mul2(total[i][j], wp[i][j]);
+                    total[i][j] = mul2(total[i][j], w[j]);
                     py = fma2(total[i][j], y[j], py);
                 }
             }
@@ -842,13 +884,13 @@ cudaError_t forward_as(const NormArgs& a, const Shape& sh, cudaStream_t s) {
     if (sh.nv == 2) return run_rows(block_norm_kernel<2, EDGE, X, Y, U>, a, sh, sh.smem, s);
     return run_rows(block_norm_kernel<1, EDGE, X, Y, U>, a, sh, sh.smem, s);
 }
-// Two windows a thread take about 120 registers (column sums, weights and the
-// row's gradient): 512 threads; wider rows take 1,024 threads and spill.
+// The column sums and a row's gradient take 72 registers: 896 threads; up to
+// 1,024 windows a row spill a few, wider rows more.
 template <bool EDGE, int X, int Y, int U>
 cudaError_t backward_as(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
-    if (sh.nv == 1) return run_rows(block_norm_backward_kernel<1, 512, EDGE, X, Y, U>, a, sh, smem, s);
-    if (sh.threads <= 512) return run_rows(block_norm_backward_kernel<2, 512, EDGE, X, Y, U>, a, sh, smem, s);
-    return run_rows(block_norm_backward_kernel<2, 1024, true, -1, -1, -1>, a, sh, smem, s);
+    if (sh.nv == 2) return run_rows(block_norm_backward_kernel<2, 1024, true, -1, -1, -1>, a, sh, smem, s);
+    if (sh.threads <= 896) return run_rows(block_norm_backward_kernel<1, 896, EDGE, X, Y, U>, a, sh, smem, s);
+    return run_rows(block_norm_backward_kernel<1, 1024, EDGE, X, Y, U>, a, sh, smem, s);
 }
 
 int plain_threads(int D) { return std::min(1024, std::max(32, (D + kPlainColumns / 4 - 1) / (kPlainColumns / 4) + 31) / 32 * 32); }
@@ -916,7 +958,7 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     const int most = norm_parts(a.T, a.D);
     Shape sh;
     int parts;
-    if (shape_of(a.T, a.D, al, slots, 512, 512, 0, 128, sms, most, &sh)) {
+    if (shape_of(a.T, a.D, al, slots, 1024, 896, 4, 72, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
         if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.D));
