@@ -366,9 +366,13 @@ typedef enum {
  *   sorted_slot int32 [T * k]   flat slot t k + j at each sorted place, equal
  *                               experts in slot order; -1 behind offsets[E]
  *   slot_pos    int32 [T][k]    place of each slot, -1 for a dropped one
- * T >= 0, 1 <= k <= 32, T k < 2^31, 1 <= E <= 1024. */
+ * T >= 0, 1 <= k <= 32, T k < 2^31, 1 <= E <= 1024.  `workspace` (4-byte
+ * aligned) holds moe_sort_workspace_bytes(T, k, E) bytes, none for small
+ * batches; calls that overlap need one each. */
+MOE_API size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t E);
 MOE_API moe_status moe_sort(const int32_t *idx, int32_t T, int32_t k, int32_t E, int32_t *offsets,
-                            int32_t *sorted_slot, int32_t *slot_pos, void *stream);
+                            int32_t *sorted_slot, int32_t *slot_pos, void *workspace, size_t workspace_bytes,
+                            void *stream);
 
 /* rows[slot_pos[t][j]] = x[t] for every slot: rows of row_bytes bytes of any
  * type (activations, MXFP4 or MXFP8 codes, scales).  Strides in bytes, at

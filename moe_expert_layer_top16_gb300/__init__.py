@@ -34,7 +34,8 @@ PRECISION_MX, PRECISION_MIXED = 0, 1
 ENTRY_POINTS = ("moe_plan", "moe_forward", "moe_forward_host", "moe_get_device_status", "moe_workspace_bytes",
                 "moe_free", "moe_status_str", "moe_mxfp4_encode", "moe_mx_gemm", "moe_mma_probe",
                 "moe_ep_row_bytes", "moe_ep_dispatch", "moe_ep_combine", "moe_quantile_balance", "moe_set_bias",
-                "moe_mx_gemm_noalloc", "moe_sort", "moe_permute", "moe_unpermute", "moe_unpermute_backward",
+                "moe_mx_gemm_noalloc", "moe_sort", "moe_sort_workspace_bytes", "moe_permute", "moe_unpermute",
+                "moe_unpermute_backward",
                 "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward", "moe_mxfp4_quantize",
                 "moe_mxfp4_decode", "moe_mx4_gemm", "moe_forward_block")
 

@@ -52,7 +52,7 @@ def declare(L):
     """Argument types of the entry points below (called once, when libmoe is loaded)."""
     P, i32, i64 = C.c_void_p, C.c_int32, C.c_int64
     for name, args in (
-            ("moe_sort", [P, i32, i32, i32, P, P, P, P]),
+            ("moe_sort", [P, i32, i32, i32, P, P, P, P, C.c_size_t, P]),
             ("moe_permute", [P, i64, i64, i32, i32, P, i64, P, i64, P]),
             ("moe_unpermute", [P, i64, i32, i64, P, P, i32, i32, i32, P, i64, i32, P]),
             ("moe_unpermute_backward", [P, i64, i32, P, i64, i32, i64, P, P, i32, i32, i32, P, i64, P, P]),
@@ -65,6 +65,8 @@ def declare(L):
         f = getattr(L, name)
         f.restype = C.c_int
         f.argtypes = args
+    L.moe_sort_workspace_bytes.restype = C.c_size_t
+    L.moe_sort_workspace_bytes.argtypes = [i32, i32, i32]
     L.moe_block_norm_workspace_bytes.restype = C.c_size_t
     L.moe_block_norm_workspace_bytes.argtypes = [i32, i32]
 
@@ -178,8 +180,11 @@ def sort_by_expert(idx: torch.Tensor, n_experts: int, stream=None):
     slot_pos = torch.empty((T, k), dtype=torch.int32, device=where)
     sorted_slot = torch.empty(T * k, dtype=torch.int32, device=where)
     offsets = torch.empty(E + 1, dtype=torch.int32, device=where)
-    _call(lib().moe_sort, "moe_sort", dev, stream, idx.data_ptr(), T, k, E, offsets.data_ptr(), sorted_slot.data_ptr(),
-          slot_pos.data_ptr())
+    L = lib()
+    size = L.moe_sort_workspace_bytes(T, k, E)
+    work = torch.empty(size, dtype=torch.uint8, device=where) if size else None
+    _call(L.moe_sort, "moe_sort", dev, stream, idx.data_ptr(), T, k, E, offsets.data_ptr(), sorted_slot.data_ptr(),
+          slot_pos.data_ptr(), _p(work), size)
     return offsets, sorted_slot, slot_pos
 
 

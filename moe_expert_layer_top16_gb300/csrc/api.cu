@@ -1491,14 +1491,21 @@ bool map_fp4(CUtensorMap* m, const void* codes, int64_t rows, int64_t K, int box
 
 extern "C" {
 
+size_t moe_sort_workspace_bytes(int32_t T, int32_t k, int32_t E) {
+    return slots_ok(T, k) && E >= 1 && E <= 1024 ? sort_workspace_bytes(static_cast<int64_t>(T) * k, E) : 0;
+}
+
 moe_status moe_sort(const int32_t* idx, int32_t T, int32_t k, int32_t E, int32_t* offsets, int32_t* sorted_slot,
-                    int32_t* slot_pos, void* stream) {
+                    int32_t* slot_pos, void* workspace, size_t workspace_bytes, void* stream) {
     if (!slots_ok(T, k) || E < 1 || E > 1024 || !offsets) return MOE_ERR_INVALID_ARG;
     if (T > 0 && (!idx || !sorted_slot || !slot_pos)) return MOE_ERR_INVALID_ARG;
-    if (!aligned(idx, 4) || !aligned(offsets, 4) || !aligned(sorted_slot, 4) || !aligned(slot_pos, 4))
+    if (!aligned(idx, 4) || !aligned(offsets, 4) || !aligned(sorted_slot, 4) || !aligned(slot_pos, 4) ||
+        !aligned(workspace, 4))
         return MOE_ERR_INVALID_ARG;
+    const size_t need = moe_sort_workspace_bytes(T, k, E);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
     return cuda_status(launch_sort(idx, static_cast<int64_t>(T) * k, E, offsets, sorted_slot, slot_pos,
-                                   static_cast<cudaStream_t>(stream)));
+                                   static_cast<int32_t*>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_permute(const void* x, int64_t x_stride, int64_t row_bytes, int32_t T, int32_t k,

@@ -308,8 +308,9 @@ cudaError_t launch_quantile_balance(const float* logits, const float* bias, int 
 // ------------------------------------------------------------------ tokens by expert and back (route.cu)
 // Strides in elements of their matrix (permute: in bytes); element types are
 // ElemType values (vec.cuh).
+size_t sort_workspace_bytes(int64_t n, int E);
 cudaError_t launch_sort(const int32_t* idx, int64_t n, int E, int32_t* offsets, int32_t* sorted_slot,
-                        int32_t* slot_pos, cudaStream_t s);
+                        int32_t* slot_pos, int32_t* work, cudaStream_t s);
 cudaError_t launch_permute(const uint8_t* x, int64_t x_stride, int64_t row_bytes, int64_t T, int k,
                            const int32_t* slot_pos, int64_t n_rows, uint8_t* rows, int64_t rows_stride,
                            cudaStream_t s);

@@ -14,50 +14,86 @@
 //
 // Every place is written by exactly one thread and every sum runs in a fixed
 // order: results do not depend on scheduling.
-#include <cooperative_groups.h>
-
 #include "internal.h"
 #include "vec.cuh"
 
 namespace moe {
 
-namespace cg = cooperative_groups;
-
 namespace {
 
 // ------------------------------------------------------------------ sort
-// A counting sort in one launch of one cluster.  Warp w of the cluster owns a
-// contiguous strip of slots and counts its experts in a row of its own
-// (cnt[w][E], shared memory; integer atomics, whose order does not matter).  A
-// scan over the CTA's warps, then over the cluster's CTAs (distributed shared
-// memory), then over experts turns the counts into each strip's first place of
+// A counting sort.  Warp w of a CTA owns a contiguous strip of slots and counts
+// its experts in a row of its own (cnt[w][E], shared memory; integer atomics,
+// whose order does not matter).  A scan over the CTA's warps, then over the
+// CTAs, then over experts turns the counts into each strip's first place of
 // every expert.  A second pass over the strip hands the places out, 32 slots a
 // step: match.any finds a slot's equals, the lanes below it are its rank, and
 // the lowest lane of each set moves the strip's next place on.  The loads of
 // kSortBatch steps are in flight together: a strip's steps are short, and one
 // at a time each would pay a round trip to memory.
+//
+// Up to kSortOne slots one CTA does it all in one launch.  Beyond, a first
+// launch counts each CTA's experts into the workspace, and every CTA of the
+// second sums the counts of the CTAs before it: a cluster of eight CTAs with
+// distributed shared memory took 33 us for 131,072 slots, bound by the
+// shared-memory pipes of eight SMs, 64 CTAs in two launches take 14.5.
 constexpr int kSortMaxE = 1024;
 constexpr int kSortMaxWarps = 32;
-constexpr int kSortBatch = 8;
-constexpr int kSortMaxCluster = 8;
+constexpr int kSortBatch = 4;
+constexpr int64_t kSortOne = 4096;         // slots of a single-CTA sort
+constexpr int kSortMaxCtas = 152;
+
+// CTAs of a sort of n slots: 2,048 slots each, until every SM has one.
+int sort_ctas(int64_t n) {
+    if (n <= kSortOne) return 1;
+    const int64_t c = (n + 2047) / 2048;
+    return static_cast<int>(c < kSortMaxCtas ? c : kSortMaxCtas);
+}
+
+// Slots of CTA c of C: [first, last), whole 32-slot steps.
+__device__ __forceinline__ void sort_range(int64_t n, int C, int c, int64_t& first, int64_t& last) {
+    const int64_t steps = (n + 31) / 32;
+    const int64_t per = (steps + C - 1) / C;
+    first = min(c * per, steps);
+    last = min(first + per, steps);
+}
+
+__global__ void __launch_bounds__(512) sort_count_kernel(const int32_t* __restrict__ idx, int64_t n, int E,
+                                                         int32_t* __restrict__ counts) {
+    extern __shared__ __align__(16) int32_t sm[];
+    pdl_trigger();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) sm[e] = 0;
+    __syncthreads();
+    int64_t s0, s1;
+    sort_range(n, gridDim.x, blockIdx.x, s0, s1);
+    const int64_t i1 = min(s1 * 32, n);
+    for (int64_t i = s0 * 32 + threadIdx.x; i < i1; i += 4 * blockDim.x) {
+        int32_t e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e[u] = i + u * blockDim.x < i1 ? idx[i + u * blockDim.x] : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (e[u] >= 0 && e[u] < E) atomicAdd(&sm[e[u]], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) counts[static_cast<int64_t>(blockIdx.x) * E + e] = sm[e];
+}
 
 __global__ void __launch_bounds__(kSortMaxWarps * 32)
-    sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, int32_t* __restrict__ offsets,
-                int32_t* __restrict__ sorted_slot, int32_t* __restrict__ slot_pos, int C) {
+    sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, const int32_t* __restrict__ counts,
+                int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_slot, int32_t* __restrict__ slot_pos) {
     extern __shared__ __align__(16) int32_t sm[];
     __shared__ int32_t warp_sum[32];
-    const int W = blockDim.x >> 5;
+    const int W = blockDim.x >> 5, C = gridDim.x, rank = blockIdx.x;
     const int Ep = (E + 3) & ~3;       // rows of whole 16-byte words
     int32_t* cnt = sm;                 // [W][Ep]
-    int32_t* tot = sm + W * Ep;        // [Ep] this CTA's counts
-    int32_t* start = tot + Ep;         // [Ep] this CTA's first place of each expert
+    int32_t* start = sm + W * Ep;      // [Ep] this CTA's first place of each expert
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(blockIdx.x);
+    int64_t first, last;
+    sort_range(n, C, rank, first, last);
     // strips of whole 32-slot steps
-    const int64_t steps = (n + 31) / 32;
-    const int64_t per = (steps + static_cast<int64_t>(C) * W - 1) / (static_cast<int64_t>(C) * W);
-    const int64_t s0 = (static_cast<int64_t>(rank) * W + warp) * per;
-    const int64_t s1 = s0 + per < steps ? s0 + per : steps;
+    const int64_t per = (last - first + W - 1) / W;
+    const int64_t s0 = min(first + warp * per, last), s1 = min(s0 + per, last);
     int32_t ex[kSortBatch];
     auto load = [&](int64_t s) {
 #pragma unroll
@@ -77,42 +113,39 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
             if (ex[u] >= 0 && ex[u] < E) atomicAdd(&mine[ex[u]], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int32_t run = 0;
-        for (int w0 = 0; w0 < W; w0 += 8) {
-            int32_t c[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) c[u] = w0 + u < W ? cnt[(w0 + u) * Ep + e] : 0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (w0 + u < W) cnt[(w0 + u) * Ep + e] = run;
-                run += c[u];
-            }
-        }
-        tot[e] = run;
-    }
-    // each thread's run of consecutive experts: earlier CTAs' counts and the
-    // cluster's total
-    if (C > 1) cg::this_cluster().sync();
-    else __syncthreads();
+    // each thread's run of consecutive experts: the strips before each strip,
+    // the CTAs before this one, and all of them
+    if (C > 1) pdl_wait();             // the counts of the launch before
     const int per_thread = (E + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
     const int e0 = threadIdx.x * per_thread;
     int32_t sum = 0;
     for (int u = 0; u < per_thread; ++u) {
         const int e = e0 + u;
         if (e >= E) break;
-        int32_t before = 0, all = 0;
-        if (C > 1) {
-            int32_t v[kSortMaxCluster];
+        int32_t run = 0;
+        for (int w0 = 0; w0 < W; w0 += 8) {
+            int32_t c[8];
 #pragma unroll
-            for (int c = 0; c < kSortMaxCluster; ++c) v[c] = c < C ? cg::this_cluster().map_shared_rank(tot, c)[e] : 0;
+            for (int v = 0; v < 8; ++v) c[v] = w0 + v < W ? cnt[(w0 + v) * Ep + e] : 0;
 #pragma unroll
-            for (int c = 0; c < kSortMaxCluster; ++c) {
-                before += (c < rank) ? v[c] : 0;
-                all += v[c];
+            for (int v = 0; v < 8; ++v) {
+                if (w0 + v < W) cnt[(w0 + v) * Ep + e] = run;
+                run += c[v];
             }
-        } else {
-            all = tot[e];
+        }
+        int32_t before = 0, all = run;
+        if (C > 1) {
+            all = 0;
+            for (int c0 = 0; c0 < C; c0 += 16) {
+                int32_t v[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = c0 + c < C ? counts[static_cast<int64_t>(c0 + c) * E + e] : 0;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    before += c0 + c < rank ? v[c] : 0;
+                    all += v[c];
+                }
+            }
         }
         start[e] = sum + before;       // within this thread's run so far
         sum += all;
@@ -139,7 +172,7 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
         const int e = e0 + u;
         if (e >= E) break;
         start[e] += base;
-        // rank 0 has no earlier CTA: its first places are the experts' offsets
+        // no CTA before rank 0: its first places are the experts' offsets
         if (rank == 0) offsets[e] = start[e];
     }
     if (rank == 0 && threadIdx.x == 0) offsets[E] = total;
@@ -173,8 +206,6 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
     for (int64_t p = total + static_cast<int64_t>(rank) * blockDim.x + threadIdx.x; p < n;
          p += static_cast<int64_t>(C) * blockDim.x)
         sorted_slot[p] = -1;
-    // no CTA leaves while another may still read its counts
-    if (C > 1) cg::this_cluster().sync();
 }
 
 // ------------------------------------------------------------------ permute
@@ -213,11 +244,13 @@ __global__ void permute_kernel(const uint8_t* __restrict__ x, int64_t x_stride, 
 }
 
 // ------------------------------------------------------------------ unpermute
-// One warp per (token, 32 V columns): the slots' loads are issued a batch at
-// a time, their FMAs run in slot order.
+// One warp per (token, 32 V columns), or, element by element, per 4 times 32
+// columns, so that a warp that reads 64 bytes at a time has enough of them in
+// flight: the slots' loads are issued a batch at a time, their FMAs run in
+// slot order.
 constexpr int kUnpermBatch = 8;
 
-template <int V, int DT>
+template <int V, int U, int DT>
 __global__ void __launch_bounds__(128) unpermute_kernel(const void* __restrict__ rows, int64_t ld_rows, int64_t n_rows,
                                                         const int32_t* __restrict__ slot_pos,
                                                         const float* __restrict__ w, int64_t T, int k, int D,
@@ -230,33 +263,43 @@ __global__ void __launch_bounds__(128) unpermute_kernel(const void* __restrict__
     if (ch >= chunks) return;
     const int64_t t = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
     if (t >= T) return;
-    const int col = static_cast<int>(ch) * (32 * V) + lane * V;
+    const int col = static_cast<int>(ch) * (32 * V * U) + lane * V;
     int32_t p_lane = (lane < k) ? slot_pos[t * k + lane] : -1;
     if (p_lane >= n_rows) p_lane = -1;
     const float w_lane = (lane < k) ? (w ? w[t * k + lane] : 1.0f) : 0.0f;
-    float acc[V];
+    float acc[U][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    for (int g = 0; g < U; ++g)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[g][i] = 0.0f;
     for (int j0 = 0; j0 < k; j0 += kUnpermBatch) {
-        RawVec<V> r[kUnpermBatch];
+        RawVec<V> r[kUnpermBatch][U];
 #pragma unroll
         for (int u = 0; u < kUnpermBatch; ++u) {
             const int64_t p = __shfl_sync(0xffffffffu, p_lane, (j0 + u) & 31);
-            if (j0 + u < k && p >= 0 && col < D) r[u] = load_stream<V, DT>(rows, p * ld_rows + col);
+            if (j0 + u < k && p >= 0)
+#pragma unroll
+                for (int g = 0; g < U; ++g)
+                    if (col + 32 * V * g < D) r[u][g] = load_stream<V, DT>(rows, p * ld_rows + col + 32 * V * g);
         }
 #pragma unroll
         for (int u = 0; u < kUnpermBatch; ++u) {
             const int32_t p = __shfl_sync(0xffffffffu, p_lane, (j0 + u) & 31);
             const float wj = __shfl_sync(0xffffffffu, w_lane, (j0 + u) & 31);
-            if (j0 + u < k && p >= 0 && col < D) {
-                float f[V];
-                raw_to_f32(r[u], DT, f);
+            if (j0 + u < k && p >= 0)
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
-            }
+                for (int g = 0; g < U; ++g)
+                    if (col + 32 * V * g < D) {
+                        float f[V];
+                        raw_to_f32(r[u][g], DT, f);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) acc[g][i] = fmaf(wj, f[i], acc[g][i]);
+                    }
         }
     }
-    if (col < D) store_vec(y, t * ld_y + col, dty, acc);
+#pragma unroll
+    for (int g = 0; g < U; ++g)
+        if (col + 32 * V * g < D) store_vec(y, t * ld_y + col + 32 * V * g, dty, acc[g]);
 }
 
 // ------------------------------------------------------------------ unpermute, backward
@@ -341,24 +384,33 @@ cudaError_t permute_as(const uint8_t* x, int64_t x_stride, int64_t row_bytes, in
 
 }  // namespace
 
+size_t sort_workspace_bytes(int64_t n, int E) {
+    const int C = sort_ctas(n);
+    return C > 1 ? sizeof(int32_t) * static_cast<size_t>(C) * E : 0;
+}
+
 cudaError_t launch_sort(const int32_t* idx, int64_t n, int E, int32_t* offsets, int32_t* sorted_slot,
-                        int32_t* slot_pos, cudaStream_t s) {
+                        int32_t* slot_pos, int32_t* work, cudaStream_t s) {
     if (n < 0 || E < 1 || E > kSortMaxE) return cudaErrorInvalidValue;
-    // one CTA up to 8,192 slots, then up to 8 (the portable cluster size)
-    int C = 1;
-    while (C < kSortMaxCluster && n > static_cast<int64_t>(C) * 8192) C *= 2;
-    const int64_t steps = (n + 31) / 32;
+    const int C = sort_ctas(n);
+    if (C > 1 && !work) return cudaErrorInvalidValue;
+    const int64_t steps = ((n + 31) / 32 + C - 1) / C;
     int W = 4;
-    while (W < kSortMaxWarps && static_cast<int64_t>(W) * C < steps) W *= 2;
-    const size_t smem = sizeof(int32_t) * (static_cast<size_t>(W) + 2) * ((E + 3) & ~3);
-    static_assert(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE <= kSmemLimit, "sort tables");
+    while (W < (C > 1 ? 16 : kSortMaxWarps) && W < steps) W *= 2;
+    const size_t row = sizeof(int32_t) * static_cast<size_t>((E + 3) & ~3), smem = row * (W + 1);
+    static_assert(sizeof(int32_t) * (kSortMaxWarps + 1) * kSortMaxE <= kSmemLimit - 1024, "sort tables");
     if (smem > 40 * 1024) {         // with the static part, up to 48 KB need no attribute
         const cudaError_t err = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(sizeof(int32_t) * (kSortMaxWarps + 2) * kSortMaxE));
+                                                     static_cast<int>(sizeof(int32_t) * (kSortMaxWarps + 1) * kSortMaxE));
         if (err != cudaSuccess) return err;
     }
-    return launch_ex_cluster(sort_kernel, dim3(C), dim3(W * 32), smem, s, false, C, idx, n, E, offsets, sorted_slot,
-                             slot_pos, C);
+    if (C > 1) {
+        sort_count_kernel<<<C, 512, row, s>>>(idx, n, E, work);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+    }
+    return launch_ex(sort_kernel, dim3(C), dim3(W * 32), smem, s, C > 1, idx, n, E,
+                     static_cast<const int32_t*>(work), offsets, sorted_slot, slot_pos);
 }
 
 cudaError_t launch_permute(const uint8_t* x, int64_t x_stride, int64_t row_bytes, int64_t T, int k,
@@ -384,11 +436,12 @@ namespace {
 template <int V, int DT>
 cudaError_t unpermute_as(const void* rows, int64_t ld_rows, int64_t n_rows, const int32_t* slot_pos, const float* w,
                          int64_t T, int k, int D, void* y, int64_t ld_y, int dty, cudaStream_t s) {
-    const uint32_t chunks = static_cast<uint32_t>((D + 32 * V - 1) / (32 * V));
+    constexpr int U = V == 1 ? 4 : 1;
+    const uint32_t chunks = static_cast<uint32_t>((D + 32 * V * U - 1) / (32 * V * U));
     const uint32_t warps = chunks < 4 ? chunks : 4;
     const uint32_t gy = T < 65535 ? static_cast<uint32_t>(T) : 65535u;
     const dim3 grid((chunks + warps - 1) / warps, gy, static_cast<unsigned>((T + gy - 1) / gy));
-    unpermute_kernel<V, DT><<<grid, warps * 32, 0, s>>>(rows, ld_rows, n_rows, slot_pos, w, T, k, D, y, ld_y, dty, chunks);
+    unpermute_kernel<V, U, DT><<<grid, warps * 32, 0, s>>>(rows, ld_rows, n_rows, slot_pos, w, T, k, D, y, ld_y, dty, chunks);
     return cudaGetLastError();
 }
 

@@ -27,9 +27,12 @@ def refuse(f, good, changes):
 
 
 def test_sort(L):
-    refuse(L.moe_sort, [P, 4, 2, 8, P, P, P, None],
+    refuse(L.moe_sort, [P, 4, 2, 8, P, P, P, None, 0, None],
            [(0, None), (1, -1), (2, 0), (2, 33), (3, 0), (3, 1025), (4, None), (5, None), (6, None), (0, ODD), (4, ODD),
-            (1, 2 ** 30)])
+            (1, 2 ** 30), (7, ODD)])
+    need = L.moe_sort_workspace_bytes(9000, 16, 896)
+    assert need > 0 and L.moe_sort_workspace_bytes(64, 16, 896) == 0 and L.moe_sort_workspace_bytes(-1, 16, 896) == 0
+    refuse(L.moe_sort, [P, 9000, 16, 896, P, P, P, P, need, None], [(7, None), (8, need - 1)])
 
 
 def test_permute(L):
