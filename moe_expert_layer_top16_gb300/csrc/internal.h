@@ -366,7 +366,7 @@ struct Mx4Params {
     int stages, stage_bytes;
 };
 // Token rows of a work item and of a TMA box of B, for `N` rows in G groups.
-void mx4_tiles(int M, int N, int G, int* nt, int* b_box);
+void mx4_tiles(int N, int G, int* nt, int* b_box);
 cudaError_t launch_mx4_gemm(const Mx4Params& p, cudaStream_t s);
 
 // ------------------------------------------------------------------ tensor-core rate probe (peak.cu)

@@ -214,21 +214,32 @@ __global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __rest
 // pads B's rows to 16 only.  A stage is 256 elements of K: 128 bytes a row of
 // A and of B, in the 128-byte swizzle.  Roles:
 //   warp 0      TMA producer of both operands
-//   warp 1      MMA issuer: scale copies shared memory -> TMEM, four MMAs of
-//               K = 64, commit
-//   warps 2-5   scales: warp q takes every fourth stage; it reads the row-major
-//               scales of the stage's rows and arranges them as the copy wants
-//               them (row r of 128 in 16-byte slot r % 32, word r / 32)
-//   warps 6-9   epilogue
-// The scale warps read ahead of the free stage, so that the caller's row-major
-// scales need no launch that rearranges them.
+//   warp 1      MMA issuer: four MMAs of K = 64 a stage, and a commit
+//   warps 4-7   scales: the four warps read the row-major scales of the item's
+//               rows four stages at a time (32 bytes of a row), one batch
+//               ahead in registers, share them through shared memory and
+//               write each its quarter of TMEM, which holds up to four stages'
+//               scales: row r of 128 in lane r % 32, column r / 32.  The
+//               caller's scales need no launch that rearranges them, and the
+//               MMA thread issues no copies: with six shared-memory-to-TMEM
+//               copies a stage its issue rate set the pace.
+//   warps 8-11  epilogue
+// Warps 2 and 3 only meet the others at the barriers: a warp writes and reads
+// the TMEM lanes of its number modulo 4.
 constexpr int kMx4BlockM = 128;
 constexpr int kMx4BlockK = 256;
-constexpr int kMx4NtMax = 224;                    // two accumulators and two sets of scale columns in 512
+constexpr int kMx4NtMax = 208;                    // two accumulators and four sets of scale columns in 512
+constexpr int kMx4NtGroup = 192;                  // of grouped products: boxes of 32 rows
 constexpr int kMx4ABytes = kMx4BlockM * 128;
-constexpr int kMx4ScaleWarps = 4;
-constexpr int kMx4Threads = (2 + kMx4ScaleWarps + 4) * 32;
+constexpr int kMx4Threads = 12 * 32;
 constexpr int kMx4MaxStages = 16;
+constexpr int kMx4MinStages = 4;
+constexpr int kMx4MaxSets = 4;
+constexpr int kMx4SetCols = 24;                   // 2 x 4 columns of A's scales, 2 x 8 of B's
+constexpr int kMx4Batch = 4;                      // stages whose scales are loaded together: 32 bytes of a row
+constexpr int kMx4ScaleRows = kMx4BlockM + (kMx4NtMax + 31) / 32 * 32;
+constexpr int kMx4ScaleBytes = kMx4ScaleRows * 32;
+constexpr int kMx4RowLoads = (2 * (kMx4BlockM + kMx4NtMax) + 127) / 128;      // 16-byte pieces of a batch a thread
 constexpr int kMx4TmemCols = 512;
 constexpr int kMx4MaxGroups = 1024;
 constexpr int kMx4BarBytes = (3 * kMx4MaxStages + 5) * 8 + 24;
@@ -262,16 +273,22 @@ __device__ __forceinline__ Mx4Item mx4_item(const Mx4Geometry& g, int64_t it) {
     return w;
 }
 
-// Eight scale codes of a row, as two words.  Rows are K / 32 bytes apart: a
-// multiple of 8 bytes when `wide`, else of 4 (and the last stage may hold one
-// word only).
-__device__ __forceinline__ uint2 load_scales(const uint8_t* p, bool wide, bool second) {
-    if (wide) return __ldg(reinterpret_cast<const uint2*>(p));
-    uint2 r;
-    r.x = __ldg(reinterpret_cast<const uint32_t*>(p));
-    r.y = second ? __ldg(reinterpret_cast<const uint32_t*>(p + 4)) : 0u;
+// Sixteen scale codes (two stages) of a row, of which `left` codes (a multiple
+// of 4) belong to the row, as words; codes behind the row read as 0.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* at, int left, bool wide) {
+    if (wide) return __ldg(reinterpret_cast<const uint4*>(at));
+    uint4 r = make_uint4(0, 0, 0, 0);
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(at);
+    r.x = __ldg(p);
+    if (left > 4) r.y = __ldg(p + 1);
+    if (left > 8) r.z = __ldg(p + 2);
+    if (left > 12) r.w = __ldg(p + 3);
     return r;
 }
+
+// Place of 16-byte half `h` of row r in the shared rows of 32 bytes: halves
+// swap every four rows, so that eight rows' halves lie in different banks.
+__device__ __forceinline__ int scale_place(int r, int h) { return r * 32 + ((h ^ ((r >> 2) & 1)) << 4); }
 
 __device__ __forceinline__ bool mx4_drain(uint64_t* bar, uint32_t parity, int* status) {
     const uint64_t t0 = globaltimer_ns();
@@ -297,18 +314,19 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int S = pin(p.stages), stage_bytes = pin(p.stage_bytes);
     const int M = pin(p.M), K = pin(p.K), nt = pin(p.nt), G = pin(p.G), b_box = pin(p.b_box);
-    const int atoms_max = (nt + 127) / 128;
-    const int off_b = kMx4ABytes, off_sfa = off_b + nt * 128, off_sfb = off_sfa + 1024;
+    const int off_b = kMx4ABytes;
+    const int sets = min(kMx4MaxSets, (kMx4TmemCols - 2 * nt) / kMx4SetCols);
     uint8_t* tail = base + S * stage_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(tail);      // operands of a stage have landed
-    uint64_t* sfull = full + kMx4MaxStages;                  // its scales are arranged
+    uint8_t* scales = tail;                                  // [128 of A, then nt of B][32]
+    uint64_t* full = reinterpret_cast<uint64_t*>(tail + kMx4ScaleBytes);      // operands of a stage have landed
+    uint64_t* sfull = full + kMx4MaxStages;                  // its scales are in TMEM
     uint64_t* empty = sfull + kMx4MaxStages;
     uint64_t* tfull = empty + kMx4MaxStages;                 // [2]
     uint64_t* tempty = tfull + 2;                            // [2]
     uint64_t* tdown = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdown + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* tile_off = reinterpret_cast<int*>(tail + kMx4BarBytes);
+    int* tile_off = reinterpret_cast<int*>(tail + kMx4ScaleBytes + kMx4BarBytes);
     int* first = tile_off + G + 1;
     int* count = first + G + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -317,7 +335,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&sfull[s], 1);
+            mbar_init(&sfull[s], 4);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -411,46 +429,47 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, used = 0;
+        uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, set = 0;
         bool any = false;
+        // descriptors of stage 0; a stage further on adds its offset (the
+        // start-address field counts 16-byte units)
+        const uint64_t ad0 = sdesc_sw128(smem_u32(base)), bd0 = sdesc_sw128(smem_u32(base + off_b));
+        const uint32_t sf0 = tmem + 2u * static_cast<uint32_t>(nt);
         for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
             const Mx4Item w = mx4_item(geo, it);
             const int nm = (w.n + 15) & ~15;
-            const int atoms = (nm + 127) / 128;
             bool ok = mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, status, DEV_TIMEOUT_MMA);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * static_cast<uint32_t>(nt);
             const uint32_t idesc0 = idesc_mxf4(kMx4BlockM, nm);
             for (int kt = 0; kt < KT; ++kt) {
-                ok = mbar_wait(&full[stage], phase, abort_flag, status, DEV_TIMEOUT_MMA) &&
-                     mbar_wait(&sfull[stage], phase, abort_flag, status, DEV_TIMEOUT_MMA);
-                if (!__all_sync(0xffffffffu, ok)) goto mma_done;
-                tc_fence_after();
-                // consecutive stages use different scale columns
-                const uint32_t sfa = tmem + 2u * static_cast<uint32_t>(nt) + (used++ & 1u) * 24u;
-                const uint32_t sfb = sfa + 8u;
+                // a stage that is already there is seen so by every lane at
+                // once: the warp-wide vote only on the waiting path
+                if (!mbar_try_wait(&full[stage], phase) || !mbar_try_wait(&sfull[stage], phase)) {
+                    ok = mbar_wait(&full[stage], phase, abort_flag, status, DEV_TIMEOUT_MMA) &&
+                         mbar_wait(&sfull[stage], phase, abort_flag, status, DEV_TIMEOUT_MMA);
+                    if (!__all_sync(0xffffffffu, ok)) goto mma_done;
+                }
+                tc_fence_after();                      // the scales were written by other threads
+                const uint64_t off = static_cast<uint64_t>(stage) * (static_cast<uint32_t>(stage_bytes) >> 4);
+                const uint64_t ad = ad0 + off, bd = bd0 + off;
+                const uint32_t sfa = sf0 + set * kMx4SetCols, sfb = sfa + 8u;
+                const bool both = K - kt * kMx4BlockK > 128;
                 if (elect_one()) {
-                    uint8_t* sb = base + stage * stage_bytes;
-                    const uint64_t ad = sdesc_sw128(smem_u32(sb)), bd = sdesc_sw128(smem_u32(sb + off_b));
-                    const int halves = (K - kt * kMx4BlockK > 128) ? 2 : 1;
-                    for (int h = 0; h < halves; ++h) {
-                        tc_cp_32x128b_x4(sfa + 4u * h, sdesc_rows16(smem_u32(sb + off_sfa + h * 512)));
-                        for (int a = 0; a < atoms; ++a)
-                            tc_cp_32x128b_x4(sfb + 8u * h + 4u * a,
-                                             sdesc_rows16(smem_u32(sb + off_sfb + (h * atoms_max + a) * 512)));
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            // scale ids 0 and 2: the low and high half of each scale word
-                            const uint32_t idesc = idesc0 | (2u * i) << 4 | (2u * i) << 29;
-                            mma_mxf4(d, ad + 4 * h + 2 * i, bd + 4 * h + 2 * i, idesc, sfa + 4u * h, sfb + 8u * h,
-                                     (kt | h | i) != 0 ? 1u : 0u);
-                        }
+                    // scale ids 0 and 2: the low and high half of each scale word
+                    constexpr uint32_t high = 2u << 4 | 2u << 29;
+                    mma_mxf4(d, ad, bd, idesc0, sfa, sfb, kt != 0 ? 1u : 0u);
+                    mma_mxf4(d, ad + 2, bd + 2, idesc0 | high, sfa, sfb, 1u);
+                    if (both) {
+                        mma_mxf4(d, ad + 4, bd + 4, idesc0, sfa + 4u, sfb + 8u, 1u);
+                        mma_mxf4(d, ad + 6, bd + 6, idesc0 | high, sfa + 4u, sfb + 8u, 1u);
                     }
                     tc_commit(&empty[stage]);
                 }
                 any = true;
                 __syncwarp();
+                if (++set == static_cast<uint32_t>(sets)) set = 0;
                 if (++stage == static_cast<uint32_t>(S)) {
                     stage = 0;
                     phase ^= 1;
@@ -470,58 +489,131 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
             }
             __syncwarp();
         }
-    } else if (warp < 2 + kMx4ScaleWarps) {
+    } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ scales
-        const int q = warp - 2;
-        const int64_t pitch = K / 32;
-        const bool wide_a = (K % 256 == 0) && (reinterpret_cast<uintptr_t>(p.sfa) & 7) == 0;
-        const bool wide_b = (K % 256 == 0) && (reinterpret_cast<uintptr_t>(p.sfb) & 7) == 0;
-        int64_t c0 = 0;                       // stages of earlier items
-        bool ok = true;
-        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, c0 += KT) {
-            const Mx4Item w = mx4_item(geo, it);
-            const int atoms = (w.n + 127) / 128;
-            for (int kt = static_cast<int>((q - c0) & (kMx4ScaleWarps - 1)); kt < KT; kt += kMx4ScaleWarps) {
-                const bool second = K - kt * kMx4BlockK > 128;
-                uint2 va[4], vb[8];
+        const int q = warp & 3, tid = threadIdx.x & 127;
+        const uint32_t t_lane = static_cast<uint32_t>(32 * q) << 16;
+        const int pitch = K / 32;
+        const bool wide_a = K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.sfa) & 15) == 0;
+        const bool wide_b = K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.sfb) & 15) == 0;
+        const int batches = (KT + kMx4Batch - 1) / kMx4Batch;
+        // piece i of this thread: half (tid & 1) of row 64 i + tid / 2, rows of
+        // A first; a batch is read while the one before it is in use
+        uint4 piece[kMx4RowLoads];
+        const uint8_t* at[kMx4RowLoads];               // this thread's rows of the item, null: none
+        auto aim = [&](const Mx4Item& w) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 32 * i + lane;
-                    va[i] = make_uint2(0, 0);
-                    if (w.m0 + r < M) va[i] = load_scales(p.sfa + (w.a_row + r) * pitch + kt * 8, wide_a, second);
+            for (int i = 0; i < kMx4RowLoads; ++i) {
+                const int r = 64 * i + (tid >> 1), b = r - kMx4BlockM;
+                at[i] = nullptr;
+                if (i < 2 && w.m0 + r < M) at[i] = p.sfa + static_cast<int64_t>(w.a_row + r) * pitch + (tid & 1) * 16;
+                if (i >= 2 && b < w.n) at[i] = p.sfb + static_cast<int64_t>(w.b_row + b) * pitch + (tid & 1) * 16;
+            }
+        };
+        auto read = [&](int batch) {
+            const int c = batch * (8 * kMx4Batch), left = pitch - c - (tid & 1) * 16;
+#pragma unroll
+            for (int i = 0; i < kMx4RowLoads; ++i) {
+                piece[i] = make_uint4(0, 0, 0, 0);
+                if (at[i] && left > 0) piece[i] = load_scales(at[i] + c, left, i < 2 ? wide_a : wide_b);
+            }
+        };
+        int64_t it = blockIdx.x;
+        int batch = 0, n = 0, n_next = 0;
+        if (it < items) {
+            const Mx4Item w = mx4_item(geo, it);
+            n_next = w.n;
+            aim(w);
+            read(0);
+        }
+        uint32_t stage = 0, set = 0, turn = 0;
+        uint32_t old_stage = 0, old_phase = 0;         // of the turn that last used the set
+        bool ok = true;
+        while (it < items) {
+            // the four warps have read the batch before, and leave together if
+            // a wait of one of them ran out
+            uint32_t all;
+            __syncwarp();
+            asm volatile(
+                "{\n\t.reg .pred p, r;\n\t"
+                "setp.ne.u32 p, %1, 0;\n\t"
+                "bar.red.and.pred r, 1, 128, p;\n\t"
+                "selp.u32 %0, 1, 0, r;\n\t}"
+                : "=r"(all)
+                : "r"(ok ? 1u : 0u)
+                : "memory");
+            if (!all) break;
+            n = n_next;
+#pragma unroll
+            for (int i = 0; i < kMx4RowLoads; ++i) {
+                const int r = 64 * i + (tid >> 1);
+                if (i < 2 || r - kMx4BlockM < n) *reinterpret_cast<uint4*>(scales + scale_place(r, tid & 1)) = piece[i];
+            }
+            named_bar_sync(2, 128);
+            const int stages_here = min(kMx4Batch, KT - batch * kMx4Batch);
+            if (++batch == batches) {
+                batch = 0;
+                it += gridDim.x;
+                if (it < items) {
+                    const Mx4Item w = mx4_item(geo, it);
+                    n_next = w.n;
+                    aim(w);
                 }
+            }
+            if (it < items) read(batch);
+            // two stages from each 16-byte half
+#pragma unroll
+            for (int h = 0; h < kMx4Batch / 2; ++h) {
+                if (2 * h >= stages_here) break;
+                uint4 a[4], b[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a[i] = *reinterpret_cast<const uint4*>(scales + scale_place(32 * i + lane, h));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int r = 32 * i + lane;
-                    vb[i] = make_uint2(0, 0);
-                    if (r < w.n) vb[i] = load_scales(p.sfb + static_cast<int64_t>(w.b_row + r) * pitch + kt * 8, wide_b, second);
+                    // rows behind the item's last: their columns are never stored
+                    b[i] = make_uint4(0, 0, 0, 0);
+                    if (32 * i < kMx4NtMax && 32 * i < n)
+                        b[i] = *reinterpret_cast<const uint4*>(scales + scale_place(kMx4BlockM + 32 * i + lane, h));
                 }
-                const int64_t c = c0 + kt;
-                const uint32_t stage = static_cast<uint32_t>(c % S), phase = static_cast<uint32_t>((c / S) & 1);
-                ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag, status, DEV_TIMEOUT_PRODUCER);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* sb = base + stage * stage_bytes;
-                uint4* sa = reinterpret_cast<uint4*>(sb + off_sfa);
-                sa[lane] = make_uint4(va[0].x, va[1].x, va[2].x, va[3].x);
-                sa[32 + lane] = make_uint4(va[0].y, va[1].y, va[2].y, va[3].y);
-                uint4* sfb = reinterpret_cast<uint4*>(sb + off_sfb);
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    if (a < atoms) {
-                        sfb[a * 32 + lane] = make_uint4(vb[4 * a].x, vb[4 * a + 1].x, vb[4 * a + 2].x, vb[4 * a + 3].x);
-                        sfb[(atoms_max + a) * 32 + lane] =
-                            make_uint4(vb[4 * a].y, vb[4 * a + 1].y, vb[4 * a + 2].y, vb[4 * a + 3].y);
+                for (int k = 0; k < 2; ++k) {
+                    if (2 * h + k >= stages_here || !ok) break;
+                    // the MMAs that read this set's last scales are done
+                    if (turn >= static_cast<uint32_t>(sets)) {
+                        if (!mbar_try_wait(&empty[old_stage], old_phase)) {
+                            ok = mbar_wait(&empty[old_stage], old_phase, abort_flag, status, DEV_TIMEOUT_PRODUCER);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                        }
+                        if (++old_stage == static_cast<uint32_t>(S)) {
+                            old_stage = 0;
+                            old_phase ^= 1;
+                        }
                     }
+                    tc_fence_after();
+                    const uint32_t cols = tmem + t_lane + 2u * static_cast<uint32_t>(nt) + set * kMx4SetCols;
+                    uint32_t lo[8], hi[8], av[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        lo[i] = k ? b[i].z : b[i].x;
+                        hi[i] = k ? b[i].w : b[i].y;
+                        av[i] = i < 4 ? (k ? a[i & 3].z : a[i & 3].x) : (k ? a[i & 3].w : a[i & 3].y);
+                    }
+                    tmem_st8(cols, av);
+                    tmem_st8(cols + 8, lo);
+                    tmem_st8(cols + 16, hi);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sfull[stage]);
+                    ++turn;
+                    if (++set == static_cast<uint32_t>(sets)) set = 0;
+                    if (++stage == static_cast<uint32_t>(S)) stage = 0;
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfull[stage]);
             }
         }
-    } else {
+    } else if (warp >= 8) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3;         // TMEM lanes this warp may read
         const uint32_t t_lane = static_cast<uint32_t>(32 * quarter) << 16;
@@ -570,39 +662,36 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     }
 }
 
-int mx4_stage_bytes(int nt) {
-    const int bytes = kMx4ABytes + nt * 128 + 1024 + ((nt + 127) / 128) * 1024;
-    return (bytes + 1023) & ~1023;
-}
+int mx4_stage_bytes(int nt) { return (kMx4ABytes + nt * 128 + 1023) & ~1023; }
 
 int mx4_table_bytes(int G) { return (3 * (G + 1) * 4 + 15) & ~15; }
 
 }  // namespace
 
-void mx4_tiles(int M, int N, int G, int* nt, int* b_box) {
-    // one group: equal tiles; several: room for about twice the mean
-    int n;
+void mx4_tiles(int N, int G, int* nt, int* b_box) {
     if (G == 1) {
+        // equal tiles, a box each
         const int tiles = (N + kMx4NtMax - 1) / kMx4NtMax;
-        n = (N + tiles - 1) / tiles;
-    } else {
-        n = static_cast<int>((2 * static_cast<int64_t>(N) + G - 1) / G);
+        *nt = ((N + tiles - 1) / tiles + 15) & ~15;
+        *b_box = *nt;
+        return;
     }
-    n = n > kMx4NtMax ? kMx4NtMax : (n < 16 ? 16 : n);
+    // room for about twice the mean; boxes that follow a short group's rows
+    int64_t n = (2 * static_cast<int64_t>(N) + G - 1) / G;
+    n = n > kMx4NtGroup ? kMx4NtGroup : (n < 16 ? 16 : n);
     *b_box = n > 64 ? 32 : 16;
-    *nt = (n + *b_box - 1) / *b_box * *b_box;
-    (void)M;
+    *nt = static_cast<int>((n + *b_box - 1) / *b_box * *b_box);
 }
 
 cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
     Mx4Params p = in;
     if (p.M < 1 || p.N < 1 || p.K < 128 || p.K % 128 || p.G < 1 || p.G > kMx4MaxGroups) return cudaErrorInvalidValue;
-    if (p.nt < 16 || p.nt > kMx4NtMax || p.nt % p.b_box) return cudaErrorInvalidValue;
+    if (p.nt < 16 || p.nt > kMx4NtMax || p.nt % 16 || p.b_box < 16 || p.nt % p.b_box) return cudaErrorInvalidValue;
     p.stage_bytes = mx4_stage_bytes(p.nt);
-    const int fixed = 1024 + kMx4BarBytes + mx4_table_bytes(p.G);
+    const int fixed = 1024 + kMx4ScaleBytes + kMx4BarBytes + mx4_table_bytes(p.G);
     p.stages = (kSmemLimit - fixed) / p.stage_bytes;
     if (p.stages > kMx4MaxStages) p.stages = kMx4MaxStages;
-    if (p.stages < 2) return cudaErrorInvalidValue;
+    if (p.stages < kMx4MinStages) return cudaErrorInvalidValue;
     const size_t smem = fixed + static_cast<size_t>(p.stages) * p.stage_bytes;
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);

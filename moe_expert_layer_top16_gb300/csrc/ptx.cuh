@@ -221,6 +221,15 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// Each thread of the warp writes 8 consecutive 32-bit columns of its lane; the
+// columns hold the values once tmem_wait_st has returned.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Shared-memory matrix descriptor (tcgen05 form): K-major operand tile whose
 // rows are 128 bytes, stored in 8-row / 1024-byte atoms with the 128-byte
 // swizzle (the layout TMA writes with CU_TENSOR_MAP_SWIZZLE_128B).  The tile
