@@ -1487,6 +1487,19 @@ bool map_fp4(CUtensorMap* m, const void* codes, int64_t rows, int64_t K, int box
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Their scales [rows][K / 32], boxes of 32 bytes (1,024 elements) x box_rows.
+bool map_fp4_scales(CUtensorMap* m, const void* scales, int64_t rows, int64_t K, int box_rows) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 32), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 32)};
+    cuuint32_t box[2] = {32, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t es[2] = {1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(scales), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1698,6 +1711,11 @@ moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t
     Mx4Params p;
     mx4_tiles(N, G, &p.nt, &p.b_box);
     if (!map_fp4(&p.tmA, a_codes, static_cast<int64_t>(G) * M, K, 128) || !map_fp4(&p.tmB, b_codes, N, K, p.b_box))
+        return MOE_ERR_INVALID_ARG;
+    // TMA wants rows and addresses of whole 16 bytes
+    p.sf_tma = K % 512 == 0 && aligned(a_scales, 16) && aligned(b_scales, 16);
+    if (p.sf_tma && (!map_fp4_scales(&p.tmSA, a_scales, static_cast<int64_t>(G) * M, K, 128) ||
+                     !map_fp4_scales(&p.tmSB, b_scales, N, K, p.nt)))
         return MOE_ERR_INVALID_ARG;
     p.sfa = a_scales;
     p.sfb = b_scales;

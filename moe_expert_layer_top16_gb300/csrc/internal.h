@@ -353,6 +353,8 @@ cudaError_t launch_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int
 struct Mx4Params {
     CUtensorMap tmA;            // [G * M][K / 2] bytes, boxes of 128 bytes x 128 rows, 128-byte swizzle
     CUtensorMap tmB;            // [N][K / 2] bytes, boxes of 128 bytes x b_box rows
+    CUtensorMap tmSA, tmSB;     // sf_tma: the scales, boxes of 32 bytes x 128 and nt rows, 32-byte swizzle
+    int sf_tma;
     const uint8_t* sfa;         // [G * M][K / 32]
     const uint8_t* sfb;         // [N][K / 32]
     const int32_t* offsets;     // [G + 1], or null (G == 1): all N rows

@@ -215,21 +215,23 @@ __global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __rest
 // A and of B, in the 128-byte swizzle.  Roles:
 //   warp 0      TMA producer of both operands
 //   warp 1      MMA issuer: four MMAs of K = 64 a stage, and a commit
-//   warps 4-7   scales: the four warps read the row-major scales of the item's
-//               rows four stages at a time (32 bytes of a row), one batch
-//               ahead in registers, share them through shared memory and
-//               write each its quarter of TMEM, which holds up to four stages'
-//               scales: row r of 128 in lane r % 32, column r / 32.  The
-//               caller's scales need no launch that rearranges them, and the
-//               MMA thread issues no copies: with six shared-memory-to-TMEM
-//               copies a stage its issue rate set the pace.
+//   warps 4-7   scales: the row-major scales of the item's rows come to shared
+//               memory four stages at a time (32 bytes of a row), and the four
+//               warps write each its quarter of TMEM, which holds up to four
+//               stages' scales: row r of 128 in lane r % 32, column r / 32.
+//               The caller's scales need no launch that rearranges them, and
+//               the MMA thread issues no copies: with six shared-memory-to-
+//               TMEM copies a stage its issue rate set the pace.
+//   warp 3      TMA producer of the scales, where their rows are multiples of
+//               16 bytes (K a multiple of 512); else warps 4-7 load them
+//               themselves, a batch ahead in registers.  Their gathers of 16
+//               bytes a row then cost the scale warps 215 to 290 cycles a stage.
 //   warps 8-11  epilogue
-// Warps 2 and 3 only meet the others at the barriers: a warp writes and reads
-// the TMEM lanes of its number modulo 4.
+// A warp writes and reads the TMEM lanes of its number modulo 4.
 constexpr int kMx4BlockM = 128;
 constexpr int kMx4BlockK = 256;
-constexpr int kMx4NtMax = 208;                    // two accumulators and four sets of scale columns in 512
-constexpr int kMx4NtGroup = 192;                  // of grouped products: boxes of 32 rows
+constexpr int kMx4NtMax = 192;                    // two accumulators and four sets of scale columns in 512;
+                                                  // five stages (208: four)
 constexpr int kMx4ABytes = kMx4BlockM * 128;
 constexpr int kMx4Threads = 12 * 32;
 constexpr int kMx4MaxStages = 16;
@@ -238,11 +240,12 @@ constexpr int kMx4MaxSets = 4;
 constexpr int kMx4SetCols = 24;                   // 2 x 4 columns of A's scales, 2 x 8 of B's
 constexpr int kMx4Batch = 4;                      // stages whose scales are loaded together: 32 bytes of a row
 constexpr int kMx4ScaleRows = kMx4BlockM + (kMx4NtMax + 31) / 32 * 32;
-constexpr int kMx4ScaleBytes = kMx4ScaleRows * 32;
+constexpr int kMx4ScaleBuf = kMx4ScaleRows * 32;  // a batch: 128 rows of A, then B's
+constexpr int kMx4ScaleBytes = 2 * kMx4ScaleBuf;
 constexpr int kMx4RowLoads = (2 * (kMx4BlockM + kMx4NtMax) + 127) / 128;      // 16-byte pieces of a batch a thread
 constexpr int kMx4TmemCols = 512;
 constexpr int kMx4MaxGroups = 1024;
-constexpr int kMx4BarBytes = (3 * kMx4MaxStages + 5) * 8 + 24;
+constexpr int kMx4BarBytes = (3 * kMx4MaxStages + 9) * 8 + 24;
 
 struct Mx4Item {
     int a_row, m0, b_row, n;
@@ -275,8 +278,7 @@ __device__ __forceinline__ Mx4Item mx4_item(const Mx4Geometry& g, int64_t it) {
 
 // Sixteen scale codes (two stages) of a row, of which `left` codes (a multiple
 // of 4) belong to the row, as words; codes behind the row read as 0.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* at, int left, bool wide) {
-    if (wide) return __ldg(reinterpret_cast<const uint4*>(at));
+__device__ __forceinline__ uint4 load_scales(const uint8_t* at, int left) {
     uint4 r = make_uint4(0, 0, 0, 0);
     const uint32_t* p = reinterpret_cast<const uint32_t*>(at);
     r.x = __ldg(p);
@@ -308,7 +310,7 @@ __device__ __forceinline__ void store_out(void* out, int64_t off, float v) {
     else static_cast<__half*>(out)[off] = __float2half_rn(v);
 }
 
-template <int DT>
+template <int DT, bool SFT>
 __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -317,13 +319,15 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     const int off_b = kMx4ABytes;
     const int sets = min(kMx4MaxSets, (kMx4TmemCols - 2 * nt) / kMx4SetCols);
     uint8_t* tail = base + S * stage_bytes;
-    uint8_t* scales = tail;                                  // [128 of A, then nt of B][32]
+    uint8_t* scales = tail;                                  // [2][128 of A, then nt of B][32]
     uint64_t* full = reinterpret_cast<uint64_t*>(tail + kMx4ScaleBytes);      // operands of a stage have landed
     uint64_t* sfull = full + kMx4MaxStages;                  // its scales are in TMEM
     uint64_t* empty = sfull + kMx4MaxStages;
     uint64_t* tfull = empty + kMx4MaxStages;                 // [2]
     uint64_t* tempty = tfull + 2;                            // [2]
-    uint64_t* tdown = tempty + 2;
+    uint64_t* cfull = tempty + 2;                            // [2] a batch of scales has landed
+    uint64_t* cempty = cfull + 2;                            // [2]
+    uint64_t* tdown = cempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tdown + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* tile_off = reinterpret_cast<int*>(tail + kMx4ScaleBytes + kMx4BarBytes);
@@ -341,12 +345,18 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 4);
+            mbar_init(&cfull[b], 1);
+            mbar_init(&cempty[b], 4);
         }
         mbar_init(tdown, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&p.tmA);
         prefetch_tmap(&p.tmB);
+        if (SFT) {
+            prefetch_tmap(&p.tmSA);
+            prefetch_tmap(&p.tmSB);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kMx4TmemCols);
@@ -489,33 +499,68 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
             }
             __syncwarp();
         }
+    } else if (SFT && warp == 3) {
+        // ------------------------------------------------------------ producer of the scales
+        const int batches = (KT + kMx4Batch - 1) / kMx4Batch;
+        uint32_t buf = 0, phase = 0, issued = 0, issued_parity = 0;
+        bool ok = true;
+        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+            const Mx4Item w = mx4_item(geo, it);
+            for (int b = 0; b < batches; ++b) {
+                ok = mbar_wait(&cempty[buf], phase ^ 1, abort_flag, status, DEV_TIMEOUT_PRODUCER);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    uint8_t* d = scales + buf * kMx4ScaleBuf;
+                    mbar_arrive_expect_tx(&cfull[buf], static_cast<uint32_t>((kMx4BlockM + nt) * 32));
+                    tma_load_2d(d, &p.tmSA, &cfull[buf], b * 32, w.a_row);
+                    tma_load_2d(d + kMx4BlockM * 32, &p.tmSB, &cfull[buf], b * 32, w.b_row);
+                }
+                __syncwarp();
+                issued |= 1u << buf;
+                issued_parity = (issued_parity & ~(1u << buf)) | (phase << buf);
+                buf ^= 1;
+                if (buf == 0) phase ^= 1;
+            }
+        }
+        if (*abort_flag && lane == 0) {
+            for (int b = 0; b < 2; ++b)
+                if (issued & (1u << b)) mx4_drain(&cfull[b], (issued_parity >> b) & 1u, status);
+        }
+        __syncwarp();
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ scales
         const int q = warp & 3, tid = threadIdx.x & 127;
         const uint32_t t_lane = static_cast<uint32_t>(32 * q) << 16;
         const int pitch = K / 32;
-        const bool wide_a = K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.sfa) & 15) == 0;
-        const bool wide_b = K % 512 == 0 && (reinterpret_cast<uintptr_t>(p.sfb) & 15) == 0;
         const int batches = (KT + kMx4Batch - 1) / kMx4Batch;
-        // piece i of this thread: half (tid & 1) of row 64 i + tid / 2, rows of
-        // A first; a batch is read while the one before it is in use
-        uint4 piece[kMx4RowLoads];
-        const uint8_t* at[kMx4RowLoads];               // this thread's rows of the item, null: none
+        // without TMA: piece i of this thread is half (tid & 1) of row 64 i +
+        // tid / 2, rows of A first; a batch is read while the one before it is
+        // in use
+        constexpr int kPieces = SFT ? 1 : kMx4RowLoads;
+        uint4 piece[kPieces];
+        const uint8_t* at[kPieces];                    // this thread's rows of the item, null: none
         auto aim = [&](const Mx4Item& w) {
+            if constexpr (!SFT) {
 #pragma unroll
-            for (int i = 0; i < kMx4RowLoads; ++i) {
-                const int r = 64 * i + (tid >> 1), b = r - kMx4BlockM;
-                at[i] = nullptr;
-                if (i < 2 && w.m0 + r < M) at[i] = p.sfa + static_cast<int64_t>(w.a_row + r) * pitch + (tid & 1) * 16;
-                if (i >= 2 && b < w.n) at[i] = p.sfb + static_cast<int64_t>(w.b_row + b) * pitch + (tid & 1) * 16;
+                for (int i = 0; i < kPieces; ++i) {
+                    const int r = 64 * i + (tid >> 1), b = r - kMx4BlockM;
+                    at[i] = nullptr;
+                    if (i < 2 && w.m0 + r < M) at[i] = p.sfa + static_cast<int64_t>(w.a_row + r) * pitch + (tid & 1) * 16;
+                    if (i >= 2 && b < w.n) at[i] = p.sfb + static_cast<int64_t>(w.b_row + b) * pitch + (tid & 1) * 16;
+                }
             }
         };
         auto read = [&](int batch) {
-            const int c = batch * (8 * kMx4Batch), left = pitch - c - (tid & 1) * 16;
+            if constexpr (!SFT) {
+                const int c = batch * (8 * kMx4Batch), left = pitch - c - (tid & 1) * 16;
 #pragma unroll
-            for (int i = 0; i < kMx4RowLoads; ++i) {
-                piece[i] = make_uint4(0, 0, 0, 0);
-                if (at[i] && left > 0) piece[i] = load_scales(at[i] + c, left, i < 2 ? wide_a : wide_b);
+                for (int i = 0; i < kPieces; ++i) {
+                    piece[i] = make_uint4(0, 0, 0, 0);
+                    if (at[i] && left > 0) piece[i] = load_scales(at[i] + c, left);
+                }
             }
         };
         int64_t it = blockIdx.x;
@@ -528,28 +573,37 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         }
         uint32_t stage = 0, set = 0, turn = 0;
         uint32_t old_stage = 0, old_phase = 0;         // of the turn that last used the set
+        uint32_t buf = 0, buf_phase = 0;
         bool ok = true;
         while (it < items) {
-            // the four warps have read the batch before, and leave together if
-            // a wait of one of them ran out
-            uint32_t all;
-            __syncwarp();
-            asm volatile(
-                "{\n\t.reg .pred p, r;\n\t"
-                "setp.ne.u32 p, %1, 0;\n\t"
-                "bar.red.and.pred r, 1, 128, p;\n\t"
-                "selp.u32 %0, 1, 0, r;\n\t}"
-                : "=r"(all)
-                : "r"(ok ? 1u : 0u)
-                : "memory");
-            if (!all) break;
             n = n_next;
+            if (SFT) {
+                if (!mbar_try_wait(&cfull[buf], buf_phase)) {
+                    ok = mbar_wait(&cfull[buf], buf_phase, abort_flag, status, DEV_TIMEOUT_PRODUCER);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+                if (!ok) break;
+            } else {
+                // the four warps have read the batch before, and leave together
+                // if a wait of one of them ran out
+                uint32_t all;
+                __syncwarp();
+                asm volatile(
+                    "{\n\t.reg .pred p, r;\n\t"
+                    "setp.ne.u32 p, %1, 0;\n\t"
+                    "bar.red.and.pred r, 1, 128, p;\n\t"
+                    "selp.u32 %0, 1, 0, r;\n\t}"
+                    : "=r"(all)
+                    : "r"(ok ? 1u : 0u)
+                    : "memory");
+                if (!all) break;
 #pragma unroll
-            for (int i = 0; i < kMx4RowLoads; ++i) {
-                const int r = 64 * i + (tid >> 1);
-                if (i < 2 || r - kMx4BlockM < n) *reinterpret_cast<uint4*>(scales + scale_place(r, tid & 1)) = piece[i];
+                for (int i = 0; i < kPieces; ++i) {
+                    const int r = 64 * i + (tid >> 1);
+                    if (i < 2 || r - kMx4BlockM < n) *reinterpret_cast<uint4*>(scales + scale_place(r, tid & 1)) = piece[i];
+                }
+                named_bar_sync(2, 128);
             }
-            named_bar_sync(2, 128);
             const int stages_here = min(kMx4Batch, KT - batch * kMx4Batch);
             if (++batch == batches) {
                 batch = 0;
@@ -561,20 +615,25 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
                 }
             }
             if (it < items) read(batch);
+            const uint8_t* rows = scales + buf * kMx4ScaleBuf;
             // two stages from each 16-byte half
 #pragma unroll
             for (int h = 0; h < kMx4Batch / 2; ++h) {
-                if (2 * h >= stages_here) break;
                 uint4 a[4], b[8];
+                if (2 * h < stages_here) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    a[i] = *reinterpret_cast<const uint4*>(scales + scale_place(32 * i + lane, h));
+                    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const uint4*>(rows + scale_place(32 * i + lane, h));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // rows behind the item's last: their columns are never stored
-                    b[i] = make_uint4(0, 0, 0, 0);
-                    if (32 * i < kMx4NtMax && 32 * i < n)
-                        b[i] = *reinterpret_cast<const uint4*>(scales + scale_place(kMx4BlockM + 32 * i + lane, h));
+                    for (int i = 0; i < 8; ++i) {
+                        // rows behind the item's last: their columns are never stored
+                        b[i] = make_uint4(0, 0, 0, 0);
+                        if (32 * i < kMx4NtMax && 32 * i < n)
+                            b[i] = *reinterpret_cast<const uint4*>(rows + scale_place(kMx4BlockM + 32 * i + lane, h));
+                    }
+                }
+                if (SFT && h == kMx4Batch / 2 - 1) {   // the buffer has been read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&cempty[buf]);
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -611,6 +670,10 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
                     if (++set == static_cast<uint32_t>(sets)) set = 0;
                     if (++stage == static_cast<uint32_t>(S)) stage = 0;
                 }
+            }
+            if (SFT) {
+                buf ^= 1;
+                if (buf == 0) buf_phase ^= 1;
             }
         }
     } else if (warp >= 8) {
@@ -678,7 +741,7 @@ void mx4_tiles(int N, int G, int* nt, int* b_box) {
     }
     // room for about twice the mean; boxes that follow a short group's rows
     int64_t n = (2 * static_cast<int64_t>(N) + G - 1) / G;
-    n = n > kMx4NtGroup ? kMx4NtGroup : (n < 16 ? 16 : n);
+    n = n > kMx4NtMax ? kMx4NtMax : (n < 16 ? 16 : n);
     *b_box = n > 64 ? 32 : 16;
     *nt = static_cast<int>((n + *b_box - 1) / *b_box * *b_box);
 }
@@ -706,9 +769,14 @@ cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
         kern<<<grid, kMx4Threads, smem, s>>>(p);
         return cudaGetLastError();
     };
-    if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32>);
-    if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16>);
-    return run(mx4_gemm_kernel<ELEM_F16>);
+    if (p.sf_tma) {
+        if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32, true>);
+        if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16, true>);
+        return run(mx4_gemm_kernel<ELEM_F16, true>);
+    }
+    if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32, false>);
+    if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16, false>);
+    return run(mx4_gemm_kernel<ELEM_F16, false>);
 }
 
 namespace {
