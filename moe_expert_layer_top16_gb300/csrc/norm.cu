@@ -27,37 +27,50 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxWarps = 32;
-constexpr int kNormVec = 8;                  // elements of a window
 constexpr int kNormMaxStages = 8;
 
-// ------------------------------------------------------------------ rows by windows of 8 elements
-// A row is cut at the 8-element windows of its matrix (16 bytes of a 16-bit
-// type, 32 of fp32), not at its own start: for rows of any length the windows
-// inside a row are whole 16-byte words, and only its first and last window
-// may be partial.  All matrices of a launch have 16-byte aligned bases and row
-// strides that are equal modulo 8, so a row lies alike in all of them; a group
-// of threads takes every (8 m)-th row, so that its rows all start at the same
-// place in their first window and thread i owns the same columns in each.
+// ------------------------------------------------------------------ rows by windows
+// A row is cut at the windows of its matrix (8 elements: 16 bytes of a 16-bit
+// type; 4 where every matrix is fp32), not at its own start: for rows of any
+// length the windows inside a row are whole 16-byte words, and only its first
+// and last window may be partial.  All matrices of a launch have 16-byte
+// aligned bases and row strides that are equal modulo a window, so a row lies
+// alike in all of them; a block takes every (8 m)-th row, so that its rows all
+// start at the same place in their first window and thread i owns the same
+// columns in each.
 //
 // A row is owned by a group of tpr threads; a block holds blockDim / tpr
 // groups, which share its weights.
 struct Rows {
     int tpr, lane_in_group, group, groups;
-    int64_t first, step;        // rows first, first + step, ...
+    int first, step;            // rows first, first + step, ...
     int shift;                  // elements of the first window that belong to the row before
 };
 
-__device__ __forceinline__ Rows rows_of(int tpr, int64_t ld) {
+__device__ __forceinline__ Rows rows_of(int tpr, int64_t ld, int window) {
     Rows r;
     r.tpr = tpr;
     r.groups = blockDim.x / tpr;
     r.group = threadIdx.x / tpr;
     r.lane_in_group = threadIdx.x - r.group * tpr;
-    r.first = blockIdx.x + static_cast<int64_t>(gridDim.x) * r.group;
-    r.step = static_cast<int64_t>(gridDim.x) * r.groups;
-    r.shift = static_cast<int>((blockIdx.x * ld) & (kNormVec - 1));
+    r.first = blockIdx.x + gridDim.x * r.group;
+    r.step = gridDim.x * r.groups;
+    r.shift = static_cast<int>((blockIdx.x * ld) & (window - 1));
     return r;
 }
+
+// Element types that an instance of the kernels is made for (RUN: as the
+// arguments say): of x, dx, h and dh, and of y.  u has x's type, except in the
+// forward F32 instance, whose u has any.  The backward instances other than
+// RUN have both norms and every matrix of them.
+enum NormKind : int { NORM_RUN = 0, NORM_BF16 = 1, NORM_BF16_Y32 = 2, NORM_F32 = 3 };
+template <int KIND>
+struct Kind {
+    static constexpr int window = KIND == NORM_F32 ? 4 : 8;
+    static constexpr bool full = KIND != NORM_RUN;
+    static constexpr int x = KIND == NORM_RUN ? -1 : (KIND == NORM_F32 ? ELEM_F32 : ELEM_BF16);
+    static constexpr int y = KIND == NORM_RUN ? -1 : (KIND == NORM_BF16 ? ELEM_BF16 : ELEM_F32);
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -116,29 +129,27 @@ __device__ __forceinline__ uint32_t narrow(Pair p, int dt) {
     return pack2(f.x, f.y, dt);
 }
 
-// Where a window lies in its row: EDGE instances have first and last windows
-// that are only partly inside.
-template <bool EDGE>
+// Whether a window lies in its row as a whole: EDGE instances have first and
+// last windows that do not.
+template <bool EDGE, int W>
 __device__ __forceinline__ bool whole(int c, int D) {
-    return !EDGE || (c >= 0 && c + kNormVec <= D);
+    return !EDGE || (c >= 0 && c + W <= D);
 }
 
-// One window of a row into this thread's own slots (a 16-byte slot, two for
-// fp32, `pitch` bytes apart): what a thread copies it alone reads, so that the
-// ring needs no barriers.  off: the window's first element in the matrix; c:
-// its column, negative in a first window that starts in the row before; left:
-// the matrix's elements from the window's first on.  A partial window is
-// copied whole while it lies inside the matrix (the values outside the row
-// are masked later); a window that reaches behind the matrix's last element
-// goes element by element.
-template <bool EDGE>
-__device__ __forceinline__ void fetch(uint8_t* slot, int pitch, const void* base, int64_t off, int c, int D, int dt,
-                                      int64_t left) {
-    const uint8_t* src = static_cast<const uint8_t*>(base) + off * elem_bytes(dt);
+// One window of a row into this thread's own slots (a 16-byte slot; two,
+// `pitch` bytes apart, for eight fp32): what a thread copies it alone reads, so
+// that the ring needs no barriers.  src: the window's first element; c: its
+// column, negative in a first window that starts in the row before; left: the
+// matrix's elements from the window's first on.  A partial window is copied
+// whole while it lies inside the matrix (the values outside the row are masked
+// later); a window that reaches behind the matrix's last element goes element
+// by element.
+template <bool EDGE, int W>
+__device__ __forceinline__ void fetch(uint8_t* slot, int pitch, const uint8_t* src, int c, int D, int dt, int64_t left) {
     if constexpr (EDGE) {
-        if (left < kNormVec) {
+        if (left < W) {
 #pragma unroll 1
-            for (int j = 0; j < kNormVec; ++j) {
+            for (int j = 0; j < W; ++j) {
                 if (c + j < 0 || c + j >= D) continue;
                 if (dt == ELEM_F32)
                     reinterpret_cast<uint32_t*>(slot + (j >> 2) * pitch)[j & 3] = reinterpret_cast<const uint32_t*>(src)[j];
@@ -150,28 +161,30 @@ __device__ __forceinline__ void fetch(uint8_t* slot, int pitch, const void* base
     }
     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
     cp_async16(dst, src);
-    if (dt == ELEM_F32) cp_async16(dst + pitch, src + 16);
+    if (W == 8 && dt == ELEM_F32) cp_async16(dst + pitch, src + 16);
 }
 
 // The window's values, zero outside the row.
-template <bool EDGE>
-__device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, int c, int D, Pair (&v)[4]) {
+template <bool EDGE, int W>
+__device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, int c, int D, Pair (&v)[W / 2]) {
     const uint4 a = *reinterpret_cast<const uint4*>(slot);
-    if (dt == ELEM_F32) {
-        const uint4 b = *reinterpret_cast<const uint4*>(slot + pitch);
+    if (W == 4 || dt == ELEM_F32) {
         v[0] = pair(__uint_as_float(a.x), __uint_as_float(a.y));
         v[1] = pair(__uint_as_float(a.z), __uint_as_float(a.w));
-        v[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y));
-        v[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
-    } else {
+        if constexpr (W == 8) {
+            const uint4 b = *reinterpret_cast<const uint4*>(slot + pitch);
+            v[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y));
+            v[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
+        }
+    } else if constexpr (W == 8) {
         v[0] = widen(a.x, dt);
         v[1] = widen(a.y, dt);
         v[2] = widen(a.z, dt);
         v[3] = widen(a.w, dt);
     }
-    if (!whole<EDGE>(c, D)) {
+    if (!whole<EDGE, W>(c, D)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < W / 2; ++j) {
             const float2 f = split(v[j]);
             const int e = c + 2 * j;
             v[j] = pair(e >= 0 && e < D ? f.x : 0.0f, e + 1 >= 0 && e + 1 < D ? f.y : 0.0f);
@@ -179,18 +192,22 @@ __device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, i
     }
 }
 
-// Store a window, and leave in v the values as stored.
-template <bool EDGE, bool BACK>
-__device__ __forceinline__ void put(void* base, int64_t off, int c, int D, int dt, Pair (&v)[4]) {
-    uint8_t* dst = static_cast<uint8_t*>(base) + off * elem_bytes(dt);
+// Store a window, and (BACK) leave in v the values as stored.
+template <bool EDGE, int W, bool BACK>
+__device__ __forceinline__ void put(uint8_t* dst, int c, int D, int dt, Pair (&v)[W / 2]) {
+    const bool all = whole<EDGE, W>(c, D);
     if (dt == ELEM_F32) {
-        if (whole<EDGE>(c, D)) {
-            const float2 p = split(v[0]), q = split(v[1]), r = split(v[2]), s = split(v[3]);
-            reinterpret_cast<float4*>(dst)[0] = make_float4(p.x, p.y, q.x, q.y);
-            reinterpret_cast<float4*>(dst)[1] = make_float4(r.x, r.y, s.x, s.y);
-        } else {
+        if (all) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < W / 4; ++j) {
+                const float2 p = split(v[2 * j]), q = split(v[2 * j + 1]);
+                reinterpret_cast<float4*>(dst)[j] = make_float4(p.x, p.y, q.x, q.y);
+            }
+        }
+        if constexpr (EDGE) {
+            if (all) return;
+#pragma unroll
+            for (int j = 0; j < W / 2; ++j) {
                 const float2 f = split(v[j]);
                 const int e = c + 2 * j;
                 if (e >= 0 && e < D) reinterpret_cast<float*>(dst)[2 * j] = f.x;
@@ -199,17 +216,20 @@ __device__ __forceinline__ void put(void* base, int64_t off, int c, int D, int d
         }
         return;
     }
-    uint32_t w[4];
+    uint32_t w[W / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < W / 2; ++j) {
         w[j] = narrow(v[j], dt);
         if (BACK) v[j] = widen(w[j], dt);
     }
-    if (whole<EDGE>(c, D)) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
+    if (all) {
+        if constexpr (W == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    }
+    if constexpr (EDGE) {
+        if (all) return;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < W / 2; ++j) {
             const int e = c + 2 * j;
             if (e >= 0 && e < D) reinterpret_cast<uint16_t*>(dst)[2 * j] = static_cast<uint16_t>(w[j] & 0xFFFFu);
             if (e + 1 >= 0 && e + 1 < D) reinterpret_cast<uint16_t*>(dst)[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
@@ -217,41 +237,64 @@ __device__ __forceinline__ void put(void* base, int64_t off, int c, int D, int d
     }
 }
 
-// A column block's weights in shared memory, as fp32: two 16-byte slots
+// A column block's weights in shared memory, as fp32: W / 4 16-byte slots
 // `pitch` bytes apart.
-__device__ __forceinline__ void keep(uint8_t* slot, int pitch, const float (&v)[8]) {
-    *reinterpret_cast<float4*>(slot) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(slot + pitch) = make_float4(v[4], v[5], v[6], v[7]);
+template <int W>
+__device__ __forceinline__ void keep(uint8_t* slot, int pitch, const float (&v)[W]) {
+#pragma unroll
+    for (int j = 0; j < W / 4; ++j)
+        *reinterpret_cast<float4*>(slot + j * pitch) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
-__device__ __forceinline__ void kept(const uint8_t* slot, int pitch, Pair (&v)[4]) {
-    const float4 a = *reinterpret_cast<const float4*>(slot), b = *reinterpret_cast<const float4*>(slot + pitch);
-    v[0] = pair(a.x, a.y);
-    v[1] = pair(a.z, a.w);
-    v[2] = pair(b.x, b.y);
-    v[3] = pair(b.z, b.w);
+template <int W>
+__device__ __forceinline__ void kept(const uint8_t* slot, int pitch, Pair (&v)[W / 2]) {
+#pragma unroll
+    for (int j = 0; j < W / 4; ++j) {
+        const float4 a = *reinterpret_cast<const float4*>(slot + j * pitch);
+        v[2 * j] = pair(a.x, a.y);
+        v[2 * j + 1] = pair(a.z, a.w);
+    }
 }
 
-// Columns c .. c + 7 of a weight vector (1 outside the row, or without one).
-// The eight loads are in flight together: one at a time they cost a launch of
+// Columns c .. c + W - 1 of a weight vector (1 outside the row, or without one).
+// The loads are in flight together: one at a time they cost a launch of
 // few rows more than its rows.
-__device__ __forceinline__ void load_columns(float (&v)[8], const void* w, int c, int D, int dt) {
+template <int W>
+__device__ __forceinline__ void load_columns(float (&v)[W], const void* w, int c, int D, int dt) {
     if (!w) {
 #pragma unroll
-        for (int j = 0; j < kNormVec; ++j) v[j] = 1.0f;
+        for (int j = 0; j < W; ++j) v[j] = 1.0f;
     } else if (dt == ELEM_F32) {
         const float* p = static_cast<const float*>(w);
 #pragma unroll
-        for (int j = 0; j < kNormVec; ++j) v[j] = (c + j >= 0 && c + j < D) ? __ldg(p + c + j) : 1.0f;
+        for (int j = 0; j < W; ++j) v[j] = (c + j >= 0 && c + j < D) ? __ldg(p + c + j) : 1.0f;
     } else {
         const uint16_t* p = static_cast<const uint16_t*>(w);
-        uint16_t u[kNormVec];
+        uint16_t u[W];
 #pragma unroll
-        for (int j = 0; j < kNormVec; ++j)
+        for (int j = 0; j < W; ++j)
             u[j] = (c + j >= 0 && c + j < D) ? __ldg(p + c + j)
                                              : static_cast<uint16_t>(dt == ELEM_BF16 ? 0x3F80 : 0x3C00);
 #pragma unroll
-        for (int j = 0; j < kNormVec; ++j)
+        for (int j = 0; j < W; ++j)
             v[j] = dt == ELEM_BF16 ? __uint_as_float(static_cast<uint32_t>(u[j]) << 16) : __half2float(__ushort_as_half(u[j]));
+    }
+}
+
+// The block's weights: NV windows of w_post times a channel gate, then of
+// w_pre, 2 W / 4 slots each.
+template <int NV, int W, typename Args>
+__device__ __forceinline__ void keep_weights(uint8_t* slots, int pitch, const Args& a, int c0, int step) {
+    const void* gate = a.gate_kind == NORM_GATE_CHANNEL ? a.gate : nullptr;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float w[W], f[W], n[W];
+        load_columns<W>(w, a.w_post, c0 + i * step, a.D, a.dt_w);
+        load_columns<W>(f, gate, c0 + i * step, a.D, a.dt_w);
+        load_columns<W>(n, a.w_pre, c0 + i * step, a.D, a.dt_w);
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j] *= f[j];
+        keep<W>(slots + i * (W / 2) * pitch, pitch, w);
+        keep<W>(slots + (i * (W / 2) + W / 4) * pitch, pitch, n);
     }
 }
 
@@ -316,63 +359,73 @@ __device__ __forceinline__ float token_gate(const void* gate, int64_t t, int dt)
 }
 
 // Slots a thread has for one window of type dt (none: no such matrix).
-__host__ __device__ __forceinline__ int window_slots(bool there, int dt) { return there ? (dt == ELEM_F32 ? 2 : 1) : 0; }
+__host__ __device__ __forceinline__ int window_slots(bool there, int dt, int window) {
+    return there ? (dt == ELEM_F32 ? window / 4 : 1) : 0;
+}
 
-// Forward.  A group keeps `stages` rows in flight by cp.async.  X, Y, U:
-// element types fixed at compile time (-1: as the arguments say).
-template <int NV, bool EDGE, int X, int Y, int U>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int tpr, int stages) {
+// This thread's first window of the next row of a matrix that goes by.
+__device__ __forceinline__ uint8_t* run(const void* base, int64_t ld, int dt, const Rows& g, int c0) {
+    return static_cast<uint8_t*>(const_cast<void*>(base)) + (g.first * ld + c0) * elem_bytes(dt);
+}
+// Bytes from a group's row to its next one, in each matrix (kernel arguments,
+// so that they take no registers).
+struct Steps {
+    int64_t x, y, h, u, dh, du, dx, dy;
+};
+
+// Forward.  A group keeps `stages` rows in flight by cp.async.
+template <int NV, bool EDGE, int KIND>
+__global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int tpr, int stages, const Steps st) {
+    using K = Kind<KIND>;
+    constexpr int W = K::window;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][1][kNormMaxWarps];
     int buf = 0;
-    const int dx = X >= 0 ? X : a.dt_x, dy = Y >= 0 ? Y : a.dt_y, du = U >= 0 ? U : a.dt_u;
-    const Rows g = rows_of(tpr, a.ld_x);
+    const int dx = K::x >= 0 ? K::x : a.dt_x, dy = K::y >= 0 ? K::y : a.dt_y;
+    const int du = KIND == NORM_BF16 || KIND == NORM_BF16_Y32 ? K::x : a.dt_u;
     const bool post = a.y != nullptr, pre = a.u != nullptr;
+    const Rows g = rows_of(tpr, a.ld_x, W);
     const int D = a.D, T = static_cast<int>(a.T);
     const int pitch = blockDim.x * 16, wpitch = tpr * 16;
-    const int xw = window_slots(true, dx), yw = window_slots(post, dy), slots = xw + yw;
-    uint8_t* weights = ring + g.lane_in_group * 16;               // [NV][post 2, pre 2] slots, shared by the groups
-    uint8_t* mine = ring + NV * 4 * wpitch + threadIdx.x * 16;    // [stages][NV][slots]
-    const int c0 = g.lane_in_group * kNormVec - g.shift, step = tpr * kNormVec;
-    auto issue = [&](int64_t t, int stage) {
+    const int yw = window_slots(post, dy, W), slots = yw + window_slots(true, dx, W);
+    uint8_t* weights = ring + g.lane_in_group * 16;
+    uint8_t* mine = ring + NV * (W / 2) * wpitch + threadIdx.x * 16;        // [stages][NV][slots]
+    const int c0 = g.lane_in_group * W - g.shift, step = tpr * W;
+    const int stage_pitch = NV * slots * pitch;
+    uint8_t *rx = run(a.x, a.ld_x, dx, g, c0), *ry = run(a.y, a.ld_y, dy, g, c0);
+    uint8_t *rh = run(a.h, a.ld_h, dx, g, c0), *ru = run(a.u, a.ld_u, du, g, c0);
+    int ahead = 0;                        // stage that the next row goes to
+    auto issue = [&](int t) {
         if (t < T) {
+            uint8_t* s = mine + ahead * stage_pitch;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
                 if (c >= D) break;
-                uint8_t* p = mine + (stage * NV + i) * slots * pitch;
-                if (post) fetch<EDGE>(p, pitch, a.y, t * a.ld_y + c, c, D, dy, (T - 1 - t) * a.ld_y + D - c);
-                fetch<EDGE>(p + yw * pitch, pitch, a.x, t * a.ld_x + c, c, D, dx, (T - 1 - t) * a.ld_x + D - c);
+                uint8_t* p = s + i * slots * pitch;
+                // only the last rows have windows that reach behind the matrix
+                const int64_t rows_left = (EDGE && t + W >= T) ? T - 1 - t : W;
+                if (post) fetch<EDGE, W>(p, pitch, ry + i * step * elem_bytes(dy), c, D, dy, rows_left * a.ld_y + D - c);
+                fetch<EDGE, W>(p + yw * pitch, pitch, rx + i * step * elem_bytes(dx), c, D, dx, rows_left * a.ld_x + D - c);
             }
+            ry += st.y;
+            rx += st.x;
         }
         cp_async_commit();
+        if (++ahead == stages) ahead = 0;
     };
-    for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step, k);
-    if (g.group == 0) {
-        const void* gate = a.gate_kind == NORM_GATE_CHANNEL ? a.gate : nullptr;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float w[8], f[8], n[8];
-            load_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
-            load_columns(f, gate, c0 + i * step, D, a.dt_w);
-            load_columns(n, a.w_pre, c0 + i * step, D, a.dt_w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] *= f[j];
-            keep(weights + i * 4 * wpitch, wpitch, w);
-            keep(weights + (i * 4 + 2) * wpitch, wpitch, n);
-        }
-    }
+    for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step);
+    if (g.group == 0) keep_weights<NV, W>(weights, wpitch, a, c0, step);
     __syncthreads();
-    int stage = 0, ahead = stages - 1;
+    int stage = 0;
     const float inv_d = 1.0f / static_cast<float>(D);
     const Pair res = pair(a.res_scale, a.res_scale);
-    for (int64_t t = g.first; t < T; t += g.step) {
-        issue(t + (stages - 1) * g.step, ahead);
-        if (++ahead == stages) ahead = 0;
+    for (int t = g.first; t < T; t += g.step) {
+        issue(t + (stages - 1) * g.step);
         cp_async_wait(stages - 1);
-        const uint8_t* s = mine + stage * (NV * slots * pitch);
+        const uint8_t* s = mine + stage * stage_pitch;
         if (++stage == stages) stage = 0;
-        Pair v[NV][4];
+        Pair v[NV][W / 2];
         float q = 0.0f;
         if (post) {
             Pair acc = 0;
@@ -380,9 +433,9 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
                 if (c >= D) break;
-                unpack<EDGE>(s + i * slots * pitch, pitch, dy, c, D, v[i]);
+                unpack<EDGE, W>(s + i * slots * pitch, pitch, dy, c, D, v[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
+                for (int j = 0; j < W / 2; ++j) acc = fma2(v[i][j], v[i][j], acc);
             }
             float ss[1] = {sum2(acc)};
             group_sums<1>(ss, g, red, buf);
@@ -397,18 +450,19 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
             if (c >= D) break;
             const uint8_t* p = s + (i * slots + yw) * pitch;
             if (post) {
-                Pair x[4], w[4];
-                unpack<EDGE>(p, pitch, dx, c, D, x);
-                kept(weights + i * 4 * wpitch, wpitch, w);
+                Pair x[W / 2], w[W / 2];
+                unpack<EDGE, W>(p, pitch, dx, c, D, x);
+                kept<W>(weights + i * (W / 2) * wpitch, wpitch, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] = fma2(res, x[j], mul2(mul2(qq, w[j]), v[i][j]));
-                put<EDGE, true>(a.h, t * a.ld_h + c, c, D, dx, v[i]);
+                for (int j = 0; j < W / 2; ++j) v[i][j] = fma2(res, x[j], mul2(mul2(qq, w[j]), v[i][j]));
+                put<EDGE, W, true>(rh + i * step * elem_bytes(dx), c, D, dx, v[i]);
             } else {
-                unpack<EDGE>(p, pitch, dx, c, D, v[i]);
+                unpack<EDGE, W>(p, pitch, dx, c, D, v[i]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc = fma2(v[i][j], v[i][j], acc);
+            for (int j = 0; j < W / 2; ++j) acc = fma2(v[i][j], v[i][j], acc);
         }
+        rh += st.h;
         if (pre) {
             float ss[1] = {sum2(acc)};
             group_sums<1>(ss, g, red, buf);
@@ -418,12 +472,13 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
                 if (c >= D) break;
-                Pair w[4];
-                kept(weights + (i * 4 + 2) * wpitch, wpitch, w);
+                Pair w[W / 2];
+                kept<W>(weights + (i * (W / 2) + W / 4) * wpitch, wpitch, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i][j] = mul2(mul2(v[i][j], rr), w[j]);
-                put<EDGE, false>(a.u, t * a.ld_u + c, c, D, du, v[i]);
+                for (int j = 0; j < W / 2; ++j) v[i][j] = mul2(mul2(v[i][j], rr), w[j]);
+                put<EDGE, W, false>(ru + i * step * elem_bytes(du), c, D, du, v[i]);
             }
+            ru += st.u;
         }
     }
 }
@@ -432,69 +487,71 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 // registers (sum du h^ and sum total y^, times the token's gate), are added
 // over the block's groups through shared memory and go to part[block][2][D].
 // The weights wait in shared memory, which leaves registers for 28 warps.
-template <int NV, int MAXT, bool EDGE, int X, int Y, int U>
-__global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages) {
+template <int NV, int MAXT, bool EDGE, int KIND>
+__global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages,
+                                                                   const Steps st) {
+    using K = Kind<KIND>;
+    constexpr int W = K::window;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][4][kNormMaxWarps];
     __shared__ float red1[2][1][kNormMaxWarps];
     int buf = 0, buf1 = 0;
-    const int tx = X >= 0 ? X : a.dt_x, ty = Y >= 0 ? Y : a.dt_y, tu = U >= 0 ? U : a.dt_u;
-    const bool post = a.y != nullptr, pre = a.du != nullptr, has_dh = a.dh != nullptr;
-    const Rows g = rows_of(tpr, pre ? a.ld_h : a.ld_dh);
-    const int D = a.D, T = static_cast<int>(a.T), row_step = static_cast<int>(g.step);
+    const int tx = K::x >= 0 ? K::x : a.dt_x, ty = K::y >= 0 ? K::y : a.dt_y, tu = K::x >= 0 ? K::x : a.dt_u;
+    const bool post = K::full || a.y != nullptr, pre = K::full || a.du != nullptr, has_dh = K::full || a.dh != nullptr;
+    const bool want_dx = K::full || a.dx != nullptr, want_dy = K::full || a.dy != nullptr;
+    const Rows g = rows_of(tpr, pre ? a.ld_h : a.ld_dh, W);
+    const int D = a.D, T = static_cast<int>(a.T);
     const int pitch = blockDim.x * 16, wpitch = tpr * 16;
-    const int off_u = window_slots(pre, tx), off_d = off_u + window_slots(pre, tu), off_y = off_d + window_slots(has_dh, tx);
-    const int slots = off_y + window_slots(post, ty);             // a window's
-    uint8_t* weights = ring + g.lane_in_group * 16;               // [NV][post 2, pre 2] slots, shared by the groups
-    uint8_t* mine = ring + NV * 4 * wpitch + threadIdx.x * 16;    // [stages][NV][slots]
-    const int c0 = g.lane_in_group * kNormVec - g.shift, step = tpr * kNormVec;
-    auto issue = [&](int t, int stage) {
+    const int off_u = window_slots(pre, tx, W), off_d = off_u + window_slots(pre, tu, W),
+              off_y = off_d + window_slots(has_dh, tx, W), slots = off_y + window_slots(post, ty, W);     // a window's
+    uint8_t* weights = ring + g.lane_in_group * 16;
+    uint8_t* mine = ring + NV * (W / 2) * wpitch + threadIdx.x * 16;        // [stages][NV][slots]
+    const int c0 = g.lane_in_group * W - g.shift, step = tpr * W;
+    const int stage_pitch = NV * slots * pitch;
+    uint8_t *rh = run(a.h, a.ld_h, tx, g, c0), *ru = run(a.du, a.ld_du, tu, g, c0);
+    uint8_t *rd = run(a.dh, a.ld_dh, tx, g, c0), *ry = run(a.y, a.ld_y, ty, g, c0);
+    uint8_t *ox = run(a.dx, a.ld_dx, tx, g, c0), *oy = run(a.dy, a.ld_dy, ty, g, c0);
+    int ahead = 0;                        // stage that the next row goes to
+    auto issue = [&](int t) {
         if (t < T) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
                 if (c >= D) break;
-                uint8_t* s = mine + (stage * NV + i) * slots * pitch;
+                uint8_t* s = mine + ahead * stage_pitch + i * slots * pitch;
                 // only the last rows have windows that reach behind the matrix
-                const int64_t rows_left = (EDGE && t + kNormVec >= T) ? T - 1 - t : kNormVec;
+                const int64_t rows_left = (EDGE && t + W >= T) ? T - 1 - t : W;
                 if (pre) {
-                    fetch<EDGE>(s, pitch, a.h, t * a.ld_h + c, c, D, tx, rows_left * a.ld_h + D - c);
-                    fetch<EDGE>(s + off_u * pitch, pitch, a.du, t * a.ld_du + c, c, D, tu, rows_left * a.ld_du + D - c);
+                    fetch<EDGE, W>(s, pitch, rh + i * step * elem_bytes(tx), c, D, tx, rows_left * a.ld_h + D - c);
+                    fetch<EDGE, W>(s + off_u * pitch, pitch, ru + i * step * elem_bytes(tu), c, D, tu, rows_left * a.ld_du + D - c);
                 }
-                if (has_dh) fetch<EDGE>(s + off_d * pitch, pitch, a.dh, t * a.ld_dh + c, c, D, tx, rows_left * a.ld_dh + D - c);
-                if (post) fetch<EDGE>(s + off_y * pitch, pitch, a.y, t * a.ld_y + c, c, D, ty, rows_left * a.ld_y + D - c);
+                if (has_dh)
+                    fetch<EDGE, W>(s + off_d * pitch, pitch, rd + i * step * elem_bytes(tx), c, D, tx, rows_left * a.ld_dh + D - c);
+                if (post)
+                    fetch<EDGE, W>(s + off_y * pitch, pitch, ry + i * step * elem_bytes(ty), c, D, ty, rows_left * a.ld_y + D - c);
             }
+            rh += st.h;
+            ru += st.du;
+            rd += st.dh;
+            ry += st.y;
         }
         cp_async_commit();
+        if (++ahead == stages) ahead = 0;
     };
-    for (int k = 0; k + 1 < stages; ++k) issue(static_cast<int>(g.first) + k * row_step, k);
-    if (g.group == 0) {
-        const void* gate = a.gate_kind == NORM_GATE_CHANNEL ? a.gate : nullptr;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float w[8], f[8], n[8];
-            load_columns(w, a.w_post, c0 + i * step, D, a.dt_w);
-            load_columns(f, gate, c0 + i * step, D, a.dt_w);
-            load_columns(n, a.w_pre, c0 + i * step, D, a.dt_w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] *= f[j];
-            keep(weights + i * 4 * wpitch, wpitch, w);
-            keep(weights + (i * 4 + 2) * wpitch, wpitch, n);
-        }
-    }
-    Pair s_pre[NV][4], s_post[NV][4];
+    for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step);
+    if (g.group == 0) keep_weights<NV, W>(weights, wpitch, a, c0, step);
+    Pair s_pre[NV][W / 2], s_post[NV][W / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s_pre[i][j] = s_post[i][j] = 0;
+        for (int j = 0; j < W / 2; ++j) s_pre[i][j] = s_post[i][j] = 0;
     __syncthreads();
-    int stage = 0, ahead = stages - 1;
+    int stage = 0;
     const float inv_d = 1.0f / static_cast<float>(D);
-    for (int t = static_cast<int>(g.first); t < T; t += row_step) {
-        issue(t + (stages - 1) * row_step, ahead);
-        if (++ahead == stages) ahead = 0;
+    for (int t = g.first; t < T; t += g.step) {
+        issue(t + (stages - 1) * g.step);
         cp_async_wait(stages - 1);
-        const uint8_t* s = mine + stage * (NV * slots * pitch);
+        const uint8_t* s = mine + stage * stage_pitch;
         if (++stage == stages) stage = 0;
         Pair hh = 0, uh = 0, yy = 0;            // h^2, a h, y^2
 #pragma unroll
@@ -503,21 +560,21 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             if (c >= D) break;
             const uint8_t* p = s + i * slots * pitch;
             if (pre) {
-                Pair h[4], u[4], w[4];
-                unpack<EDGE>(p, pitch, tx, c, D, h);
-                unpack<EDGE>(p + off_u * pitch, pitch, tu, c, D, u);
-                kept(weights + (i * 4 + 2) * wpitch, wpitch, w);
+                Pair h[W / 2], u[W / 2], w[W / 2];
+                unpack<EDGE, W>(p, pitch, tx, c, D, h);
+                unpack<EDGE, W>(p + off_u * pitch, pitch, tu, c, D, u);
+                kept<W>(weights + (i * (W / 2) + W / 4) * wpitch, wpitch, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < W / 2; ++j) {
                     hh = fma2(h[j], h[j], hh);
                     uh = fma2(mul2(u[j], w[j]), h[j], uh);
                 }
             }
             if (post) {
-                Pair y[4];
-                unpack<EDGE>(p + off_y * pitch, pitch, ty, c, D, y);
+                Pair y[W / 2];
+                unpack<EDGE, W>(p + off_y * pitch, pitch, ty, c, D, y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) yy = fma2(y[j], y[j], yy);
+                for (int j = 0; j < W / 2; ++j) yy = fma2(y[j], y[j], yy);
             }
         }
         float sums[3] = {sum2(hh), sum2(uh), sum2(yy)};
@@ -527,7 +584,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         const float q = rsqrtf(sums[2] * inv_d + a.eps);
         const float gt = (post && a.gate_kind == NORM_GATE_TOKEN) ? token_gate(a.gate, t, a.dt_w) : 1.0f;
         const Pair rr = pair(r, r), rm = pair(-r * m, -r * m), qg = pair(q * gt, q * gt);
-        Pair total[NV][4];
+        Pair total[NV][W / 2];
         Pair py = 0;                                   // sum total w_post (channel gate) y
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -535,59 +592,61 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             if (c >= D) break;
             const uint8_t* p = s + i * slots * pitch;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) total[i][j] = 0;
-            if (has_dh) unpack<EDGE>(p + off_d * pitch, pitch, tx, c, D, total[i]);
+            for (int j = 0; j < W / 2; ++j) total[i][j] = 0;
+            if (has_dh) unpack<EDGE, W>(p + off_d * pitch, pitch, tx, c, D, total[i]);
             if (pre) {
-                Pair h[4], u[4], w[4];
-                unpack<EDGE>(p, pitch, tx, c, D, h);
-                unpack<EDGE>(p + off_u * pitch, pitch, tu, c, D, u);
-                kept(weights + (i * 4 + 2) * wpitch, wpitch, w);
+                Pair h[W / 2], u[W / 2], w[W / 2];
+                unpack<EDGE, W>(p, pitch, tx, c, D, h);
+                unpack<EDGE, W>(p + off_u * pitch, pitch, tu, c, D, u);
+                kept<W>(weights + (i * (W / 2) + W / 4) * wpitch, wpitch, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < W / 2; ++j) {
                     const Pair ur = mul2(u[j], rr);
                     s_pre[i][j] = fma2(ur, h[j], s_pre[i][j]);
                     total[i][j] = fma2(h[j], rm, fma2(ur, w[j], total[i][j]));
                 }
             }
-            if (a.dx) {
+            if (want_dx) {
                 const float rs = post ? a.res_scale : 1.0f;
                 const Pair res = pair(rs, rs);
-                Pair o[4];
+                Pair o[W / 2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = mul2(res, total[i][j]);
-                put<EDGE, false>(a.dx, t * a.ld_dx + c, c, D, tx, o);
+                for (int j = 0; j < W / 2; ++j) o[j] = mul2(res, total[i][j]);
+                put<EDGE, W, false>(ox + i * step * elem_bytes(tx), c, D, tx, o);
             }
             if (post) {
-                Pair y[4], w[4];
-                unpack<EDGE>(p + off_y * pitch, pitch, ty, c, D, y);
-                kept(weights + i * 4 * wpitch, wpitch, w);
+                Pair y[W / 2], w[W / 2];
+                unpack<EDGE, W>(p + off_y * pitch, pitch, ty, c, D, y);
+                kept<W>(weights + i * (W / 2) * wpitch, wpitch, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < W / 2; ++j) {
                     s_post[i][j] = fma2(total[i][j], mul2(y[j], qg), s_post[i][j]);
                     total[i][j] = mul2(total[i][j], w[j]);
                     py = fma2(total[i][j], y[j], py);
                 }
             }
         }
+        ox += st.dx;
         if (post) {
             float d[1] = {sum2(py)};
             group_sums<1>(d, g, red1, buf1);
             if (a.d_gate_token && g.lane_in_group == 0) a.d_gate_token[t] = d[0] * q;
-            if (a.dy) {
+            if (want_dy) {
                 const float n = -q * q * d[0] * inv_d;     // -mean(p y^) / (g rms(y))
                 const Pair nn = pair(n, n);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = c0 + i * step;
                     if (c >= D) break;
-                    Pair y[4];
-                    unpack<EDGE>(s + (i * slots + off_y) * pitch, pitch, ty, c, D, y);
+                    Pair y[W / 2];
+                    unpack<EDGE, W>(s + (i * slots + off_y) * pitch, pitch, ty, c, D, y);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = mul2(qg, fma2(y[j], nn, total[i][j]));
-                    put<EDGE, false>(a.dy, t * a.ld_dy + c, c, D, ty, y);
+                    for (int j = 0; j < W / 2; ++j) y[j] = mul2(qg, fma2(y[j], nn, total[i][j]));
+                    put<EDGE, W, false>(oy + i * step * elem_bytes(ty), c, D, ty, y);
                 }
             }
         }
+        oy += st.dy;
     }
     if (!a.part) return;
     float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * D;
@@ -601,7 +660,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < W / 2; ++j) {
                     const int c = c0 + i * step + 2 * j;
                     const float2 f = split(s_pre[i][j]), e = split(s_post[i][j]);
                     if (c >= 0 && c < D) {
@@ -812,15 +871,17 @@ cudaError_t sm_count(int* sms) {
 
 // Collects whether a launch's matrices lie alike in their windows.
 struct Alike {
+    int window;
     bool ok = true;
     int64_t ld = -1;
     bool odd = false;           // rows start at different places in their windows
+    explicit Alike(int w) : window(w) {}
     void add(const void* p, int64_t l) {
         if (!p) return;
         if (reinterpret_cast<uintptr_t>(p) % 16) ok = false;
-        if (ld >= 0 && ((ld ^ l) & (kNormVec - 1))) ok = false;
+        if (ld >= 0 && ((ld ^ l) & (window - 1))) ok = false;
         ld = l;
-        odd = odd || (l & (kNormVec - 1));
+        odd = odd || (l & (window - 1));
     }
 };
 
@@ -834,18 +895,19 @@ struct Shape {
 };
 constexpr int kNormSmem = kSmemLimit - 2048;     // without the sums' static part
 
-// two_from: rows of more windows than this have two a thread; group_threads:
-// threads of a block's groups together at most; weight_slots: shared 16-byte
-// slots a window; regs: of a thread.
-bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int group_threads, int weight_slots, int regs,
-              int sms, int most, Shape* s) {
+// slots: of a window in the ring; two_from: rows of more windows than this
+// have two a thread; group_threads: threads of a block's groups together at
+// most; regs: of a thread; most: blocks.
+bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int group_threads, int regs, int sms, int most,
+              Shape* s) {
     if (!al.ok) return false;
-    const int windows = (D + (al.odd ? kNormVec - 1 : 0) + kNormVec - 1) / kNormVec;
+    const int W = al.window;
+    const int windows = (D + (al.odd ? W - 1 : 0) + W - 1) / W;
     if (windows > 2 * 1024) return false;
-    s->edge = al.odd || D % kNormVec;
+    s->edge = al.odd || D % W;
     s->nv = windows > two_from ? 2 : 1;
     s->tpr = ((windows + s->nv - 1) / s->nv + 31) / 32 * 32;
-    const int stage = s->nv * slots * 16, fixed = s->nv * weight_slots * s->tpr * 16;      // bytes a thread; a block
+    const int stage = s->nv * slots * 16, fixed = s->nv * (W / 2) * s->tpr * 16;      // bytes a thread; a block
     int groups = std::max(1, std::min(group_threads / s->tpr, 8));
     while (groups > 1 && (static_cast<int64_t>(groups) * sms > T || 2 * groups * s->tpr * stage + fixed > kNormSmem)) --groups;
     s->threads = s->tpr * groups;
@@ -869,29 +931,63 @@ bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int gr
     return s->smem <= static_cast<size_t>(kNormSmem);
 }
 
+Steps steps_of(const NormArgs& a, int64_t rows) {
+    Steps s = {};
+    s.x = rows * a.ld_x * elem_bytes(a.dt_x);
+    s.y = rows * a.ld_y * elem_bytes(a.dt_y);
+    s.h = rows * a.ld_h * elem_bytes(a.dt_x);
+    s.u = rows * a.ld_u * elem_bytes(a.dt_u);
+    return s;
+}
+Steps steps_of(const NormBackArgs& a, int64_t rows) {
+    Steps s = {};
+    s.h = rows * a.ld_h * elem_bytes(a.dt_x);
+    s.du = rows * a.ld_du * elem_bytes(a.dt_u);
+    s.dh = rows * a.ld_dh * elem_bytes(a.dt_x);
+    s.y = rows * a.ld_y * elem_bytes(a.dt_y);
+    s.dx = rows * a.ld_dx * elem_bytes(a.dt_x);
+    s.dy = rows * a.ld_dy * elem_bytes(a.dt_y);
+    return s;
+}
+
 template <typename Args>
-cudaError_t run_rows(void (*kern)(Args, int, int), const Args& a, const Shape& sh, size_t smem, cudaStream_t s) {
+cudaError_t run_rows(void (*kern)(Args, int, int, Steps), const Args& a, const Shape& sh, size_t smem, cudaStream_t s) {
     if (smem > 40 * 1024) {         // with the static part, up to 48 KB need no attribute
         const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
         if (err != cudaSuccess) return err;
     }
-    kern<<<sh.grid, sh.threads, smem, s>>>(a, sh.tpr, sh.stages);
+    const int64_t rows = static_cast<int64_t>(sh.grid) * (sh.threads / sh.tpr);
+    kern<<<sh.grid, sh.threads, smem, s>>>(a, sh.tpr, sh.stages, steps_of(a, rows));
     return cudaGetLastError();
 }
 
-template <bool EDGE, int X, int Y, int U>
+template <bool EDGE, int KIND>
 cudaError_t forward_as(const NormArgs& a, const Shape& sh, cudaStream_t s) {
-    if (sh.nv == 2) return run_rows(block_norm_kernel<2, EDGE, X, Y, U>, a, sh, sh.smem, s);
-    return run_rows(block_norm_kernel<1, EDGE, X, Y, U>, a, sh, sh.smem, s);
+    if (sh.nv == 2) return run_rows(block_norm_kernel<2, EDGE, KIND>, a, sh, sh.smem, s);
+    return run_rows(block_norm_kernel<1, EDGE, KIND>, a, sh, sh.smem, s);
 }
-// The column sums and a row's gradient take 72 registers: 896 threads; up to
-// 1,024 windows a row spill a few, wider rows more.
-template <bool EDGE, int X, int Y, int U>
+// The column sums and a row's gradient of one window of eight (or two of four)
+// take 72 registers: 896 threads.  A block of 449 to 512 has an SM to itself
+// either way and takes 128; up to 1,024 threads a row spill a few, wider rows
+// more.
+template <int NV, bool EDGE, int KIND>
+cudaError_t backward_nv(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
+    if (sh.threads > 896) return run_rows(block_norm_backward_kernel<NV, 1024, EDGE, KIND>, a, sh, smem, s);
+    if (sh.threads > 448 && sh.threads <= 512)
+        return run_rows(block_norm_backward_kernel<NV, 512, EDGE, KIND>, a, sh, smem, s);
+    return run_rows(block_norm_backward_kernel<NV, 896, EDGE, KIND>, a, sh, smem, s);
+}
+template <bool EDGE, int KIND>
 cudaError_t backward_as(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
-    if (sh.nv == 2) return run_rows(block_norm_backward_kernel<2, 1024, true, -1, -1, -1>, a, sh, smem, s);
-    if (sh.threads <= 896) return run_rows(block_norm_backward_kernel<1, 896, EDGE, X, Y, U>, a, sh, smem, s);
-    return run_rows(block_norm_backward_kernel<1, 1024, EDGE, X, Y, U>, a, sh, smem, s);
+    if (sh.nv == 1) return backward_nv<1, EDGE, KIND>(a, sh, smem, s);
+    if constexpr (KIND == NORM_F32) return backward_nv<2, EDGE, KIND>(a, sh, smem, s);
+    return run_rows(block_norm_backward_kernel<2, 1024, true, NORM_RUN>, a, sh, smem, s);
 }
+
+// Windows of four for rows of fp32, as long as two a thread cover the row.  The
+// forward rule does not ask for u's type: a fused call and its two parts then
+// add in the same order, and give the same bits.
+bool fours(int D, int x, int y) { return D <= 8000 && x == ELEM_F32 && y == ELEM_F32; }
 
 int plain_threads(int D) { return std::min(1024, std::max(32, (D + kPlainColumns / 4 - 1) / (kPlainColumns / 4) + 31) / 32 * 32); }
 
@@ -909,26 +1005,27 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
-    Alike al;
+    const int ty = a.y ? a.dt_y : a.dt_x, tu = a.u ? a.dt_u : a.dt_x;
+    int kind = NORM_RUN;
+    if (a.dt_x == ELEM_BF16 && tu == ELEM_BF16)
+        kind = ty == ELEM_BF16 ? NORM_BF16 : (ty == ELEM_F32 ? NORM_BF16_Y32 : NORM_RUN);
+    else if (fours(a.D, a.dt_x, ty))
+        kind = NORM_F32;
+    const int W = kind == NORM_F32 ? 4 : 8;
+    Alike al(W);
     al.add(a.x, a.ld_x);
     al.add(a.y, a.ld_y);
     al.add(a.h, a.ld_h);
     al.add(a.u, a.ld_u);
     Shape sh;
-    const int slots = window_slots(true, a.dt_x) + window_slots(a.y, a.dt_y);
+    const int slots = window_slots(true, a.dt_x, W) + window_slots(a.y, a.dt_y, W);
     // 896 threads in two groups of 448 for 7,168 elements: the one group's
     // sums overlap the other's loads and stores
-    if (shape_of(a.T, a.D, al, slots, 256, 1024, 4, 64, sms, 1 << 30, &sh)) {
-        const bool b = a.dt_x == ELEM_BF16 && (!a.u || a.dt_u == ELEM_BF16);
-        const bool f = a.dt_x == ELEM_F32 && (!a.u || a.dt_u == ELEM_F32) && (!a.y || a.dt_y == ELEM_F32);
-        if (b && (!a.y || a.dt_y == ELEM_BF16))
-            return sh.edge ? forward_as<true, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, s)
-                           : forward_as<false, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, s);
-        if (f)
-            return sh.edge ? forward_as<true, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, s)
-                           : forward_as<false, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, s);
-        if (b && a.dt_y == ELEM_F32 && !sh.edge) return forward_as<false, ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, s);
-        return forward_as<true, -1, -1, -1>(a, sh, s);
+    if (shape_of(a.T, a.D, al, slots, 256, 1024, 64, sms, 1 << 30, &sh)) {
+        if (kind == NORM_BF16) return sh.edge ? forward_as<true, NORM_BF16>(a, sh, s) : forward_as<false, NORM_BF16>(a, sh, s);
+        if (kind == NORM_F32) return sh.edge ? forward_as<true, NORM_F32>(a, sh, s) : forward_as<false, NORM_F32>(a, sh, s);
+        if (kind == NORM_BF16_Y32 && !sh.edge) return forward_as<false, NORM_BF16_Y32>(a, sh, s);
+        return forward_as<true, NORM_RUN>(a, sh, s);
     }
     const int threads = plain_threads(a.D);
     block_norm_plain_kernel<<<static_cast<unsigned>(std::min<int64_t>(a.T, static_cast<int64_t>(sms) * (2048 / threads))),
@@ -946,36 +1043,37 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
-    Alike al;
+    int kind = NORM_RUN;
+    if (a.y && a.du && a.dh && a.dx && a.dy && a.dt_u == a.dt_x) {
+        if (a.dt_x == ELEM_BF16) kind = a.dt_y == ELEM_BF16 ? NORM_BF16 : (a.dt_y == ELEM_F32 ? NORM_BF16_Y32 : NORM_RUN);
+        else if (fours(a.D, a.dt_x, a.dt_y)) kind = NORM_F32;
+    }
+    const int W = kind == NORM_F32 ? 4 : 8;
+    Alike al(W);
     al.add(a.h, a.ld_h);
     al.add(a.du, a.ld_du);
     al.add(a.dh, a.ld_dh);
     al.add(a.y, a.ld_y);
     al.add(a.dx, a.ld_dx);
     al.add(a.dy, a.ld_dy);
-    const int slots = window_slots(a.du, a.dt_x) + window_slots(a.du, a.dt_u) + window_slots(a.dh, a.dt_x) +
-                      window_slots(a.y, a.dt_y);
+    const int slots = window_slots(a.du, a.dt_x, W) + window_slots(a.du, a.dt_u, W) + window_slots(a.dh, a.dt_x, W) +
+                      window_slots(a.y, a.dt_y, W);
     const int most = norm_parts(a.T, a.D);
     Shape sh;
     int parts;
-    if (shape_of(a.T, a.D, al, slots, 1024, 896, 4, 72, sms, most, &sh)) {
+    if (shape_of(a.T, a.D, al, slots, W == 4 ? 256 : 1024, 896, 72, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
         if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.D));
         parts = sh.grid;
-        const bool rows = a.h || a.dh || a.dx;
-        const bool b = (!rows || a.dt_x == ELEM_BF16) && (!a.du || a.dt_u == ELEM_BF16);
-        const bool f = (!rows || a.dt_x == ELEM_F32) && (!a.du || a.dt_u == ELEM_F32) && (!a.y || a.dt_y == ELEM_F32);
-        if (b && (!a.y || a.dt_y == ELEM_BF16))
-            err = sh.edge ? backward_as<true, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, smem, s)
-                          : backward_as<false, ELEM_BF16, ELEM_BF16, ELEM_BF16>(a, sh, smem, s);
-        else if (f)
-            err = sh.edge ? backward_as<true, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, smem, s)
-                          : backward_as<false, ELEM_F32, ELEM_F32, ELEM_F32>(a, sh, smem, s);
-        else if (b && a.dt_y == ELEM_F32 && !sh.edge)
-            err = backward_as<false, ELEM_BF16, ELEM_F32, ELEM_BF16>(a, sh, smem, s);
+        if (kind == NORM_BF16)
+            err = sh.edge ? backward_as<true, NORM_BF16>(a, sh, smem, s) : backward_as<false, NORM_BF16>(a, sh, smem, s);
+        else if (kind == NORM_F32)
+            err = sh.edge ? backward_as<true, NORM_F32>(a, sh, smem, s) : backward_as<false, NORM_F32>(a, sh, smem, s);
+        else if (kind == NORM_BF16_Y32 && !sh.edge)
+            err = backward_as<false, NORM_BF16_Y32>(a, sh, smem, s);
         else
-            err = backward_as<true, -1, -1, -1>(a, sh, smem, s);
+            err = backward_as<true, NORM_RUN>(a, sh, smem, s);
     } else {
         parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.T, most), 2 * sms));
         const int threads = std::min(1024, (a.D + 31) / 32 * 32);
