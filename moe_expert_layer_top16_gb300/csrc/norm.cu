@@ -322,19 +322,16 @@ __device__ __forceinline__ void group_sums(float (&v)[N], const Rows& g, float (
     buf ^= 1;
 }
 
-// Three sums at once: the lanes halve what they carry with each exchange (two
+// Four sums at once: the lanes halve what they carry with each exchange (two
 // values after the first, one after the second), so that six exchanges do what
-// fifteen would; lane 8 k then holds value k of the warp.
-__device__ __forceinline__ void group_sums3(float (&v)[3], const Rows& g, float (*red)[4][kNormMaxWarps], int& buf) {
+// twenty would; lane 8 k then holds value k of the warp.
+__device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float (*red)[4][kNormMaxWarps], int& buf) {
     const int lane = threadIdx.x & 31;
     const bool up = lane & 16, odd = lane & 8;
-    // lanes 0-15 keep values 0 and 1, lanes 16-31 value 2
-    float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
-    float b = __shfl_xor_sync(0xffffffffu, v[1], 16);
-    a += up ? v[2] : v[0];
-    b = up ? 0.0f : b + v[1];
-    const float c = __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
-    float s = (odd ? b : a) + c;
+    // lanes 0-15 keep values 0 and 1, lanes 16-31 values 2 and 3
+    const float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16) + (up ? v[2] : v[0]);
+    const float b = __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16) + (up ? v[3] : v[1]);
+    float s = __shfl_xor_sync(0xffffffffu, odd ? a : b, 8) + (odd ? b : a);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (g.tpr > 32) {
@@ -342,14 +339,15 @@ __device__ __forceinline__ void group_sums3(float (&v)[3], const Rows& g, float 
         if ((lane & 7) == 0) red[buf][lane >> 3][warp] = s;
         asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
         s = 0.0f;
-        for (int w = lane & 7; w < warps; w += 8) s += red[buf][lane >> 3][warp0 + w];
+#pragma unroll
+        for (int w = 0; w < kNormMaxWarps; w += 8)
+            if (w + (lane & 7) < warps) s += red[buf][lane >> 3][warp0 + w + (lane & 7)];
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         buf ^= 1;
     }
-    v[0] = __shfl_sync(0xffffffffu, s, 0);
-    v[1] = __shfl_sync(0xffffffffu, s, 8);
-    v[2] = __shfl_sync(0xffffffffu, s, 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, s, 8 * i);
 }
 
 __device__ __forceinline__ float token_gate(const void* gate, int64_t t, int dt) {
@@ -486,7 +484,9 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 // Gradients, with the same ring.  The column sums of a thread's rows stay in
 // registers (sum du h^ and sum total y^, times the token's gate), are added
 // over the block's groups through shared memory and go to part[block][2][D].
-// The weights wait in shared memory, which leaves registers for 28 warps.
+// The weights wait in shared memory, which leaves registers for 28 warps.  The
+// sums over row t + 1 that its norms need are taken together with the one over
+// row t that its dy needs: one barrier a row, and the work of both before it.
 template <int NV, int MAXT, bool EDGE, int KIND>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages,
                                                                    const Steps st) {
@@ -494,8 +494,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
     constexpr int W = K::window;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][4][kNormMaxWarps];
-    __shared__ float red1[2][1][kNormMaxWarps];
-    int buf = 0, buf1 = 0;
+    int buf = 0;
     const int tx = K::x >= 0 ? K::x : a.dt_x, ty = K::y >= 0 ? K::y : a.dt_y, tu = K::x >= 0 ? K::x : a.dt_u;
     const bool post = K::full || a.y != nullptr, pre = K::full || a.du != nullptr, has_dh = K::full || a.dh != nullptr;
     const bool want_dx = K::full || a.dx != nullptr, want_dy = K::full || a.dy != nullptr;
@@ -538,7 +537,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         cp_async_commit();
         if (++ahead == stages) ahead = 0;
     };
-    for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step);
+    // one stage: the group has one row
+    for (int k = 0; k < max(stages - 1, 1); ++k) issue(g.first + k * g.step);
     if (g.group == 0) keep_weights<NV, W>(weights, wpitch, a, c0, step);
     Pair s_pre[NV][W / 2], s_post[NV][W / 2];
 #pragma unroll
@@ -548,12 +548,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
     __syncthreads();
     int stage = 0;
     const float inv_d = 1.0f / static_cast<float>(D);
-    for (int t = g.first; t < T; t += g.step) {
-        issue(t + (stages - 1) * g.step);
-        cp_async_wait(stages - 1);
-        const uint8_t* s = mine + stage * stage_pitch;
-        if (++stage == stages) stage = 0;
-        Pair hh = 0, uh = 0, yy = 0;            // h^2, a h, y^2
+    // h^2, a h and y^2 of this thread's part of the row in stage `s`
+    auto squares = [&](const uint8_t* s, float (&v)[4]) {
+        Pair hh = 0, uh = 0, yy = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
@@ -577,11 +574,27 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
                 for (int j = 0; j < W / 2; ++j) yy = fma2(y[j], y[j], yy);
             }
         }
-        float sums[3] = {sum2(hh), sum2(uh), sum2(yy)};
-        group_sums3(sums, g, red, buf);
-        const float r = rsqrtf(sums[0] * inv_d + a.eps);
-        const float m = r * r * sums[1] * inv_d;       // mean(a h^) / rms(h)
-        const float q = rsqrtf(sums[2] * inv_d + a.eps);
+        v[0] = sum2(hh);
+        v[1] = sum2(uh);
+        v[2] = sum2(yy);
+    };
+    float r = 0.0f, m = 0.0f, q = 0.0f;                // 1 / rms(h), mean(a h^) / rms(h), 1 / rms(y)
+    auto norms = [&](const float (&v)[4]) {
+        r = rsqrtf(v[0] * inv_d + a.eps);
+        m = r * r * v[1] * inv_d;
+        q = rsqrtf(v[2] * inv_d + a.eps);
+    };
+    if (g.first < T) {
+        cp_async_wait(stages > 1 ? stages - 2 : 0);
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        squares(mine, v);
+        group_sums4(v, g, red, buf);
+        norms(v);
+    }
+    for (int t = g.first; t < T; t += g.step) {
+        if (stages > 1) issue(t + (stages - 1) * g.step);
+        const uint8_t* s = mine + stage * stage_pitch;
+        if (++stage == stages) stage = 0;
         const float gt = (post && a.gate_kind == NORM_GATE_TOKEN) ? token_gate(a.gate, t, a.dt_w) : 1.0f;
         const Pair rr = pair(r, r), rm = pair(-r * m, -r * m), qg = pair(q * gt, q * gt);
         Pair total[NV][W / 2];
@@ -627,12 +640,18 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             }
         }
         ox += st.dx;
+        float v[4] = {0.0f, 0.0f, 0.0f, sum2(py)};
+        const bool more = t + g.step < T;
+        if (more) {
+            // the next row has landed: later ones may be in flight
+            cp_async_wait(stages > 1 ? stages - 2 : 0);
+            squares(mine + stage * stage_pitch, v);
+        }
+        group_sums4(v, g, red, buf);
         if (post) {
-            float d[1] = {sum2(py)};
-            group_sums<1>(d, g, red1, buf1);
-            if (a.d_gate_token && g.lane_in_group == 0) a.d_gate_token[t] = d[0] * q;
+            if (a.d_gate_token && g.lane_in_group == 0) a.d_gate_token[t] = v[3] * q;
             if (want_dy) {
-                const float n = -q * q * d[0] * inv_d;     // -mean(p y^) / (g rms(y))
+                const float n = -q * q * v[3] * inv_d;     // -mean(p y^) / (g rms(y))
                 const Pair nn = pair(n, n);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -647,6 +666,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             }
         }
         oy += st.dy;
+        norms(v);
     }
     if (!a.part) return;
     float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * D;
@@ -897,9 +917,10 @@ constexpr int kNormSmem = kSmemLimit - 2048;     // without the sums' static par
 
 // slots: of a window in the ring; two_from: rows of more windows than this
 // have two a thread; group_threads: threads of a block's groups together at
-// most; regs: of a thread; most: blocks.
-bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int group_threads, int regs, int sms, int most,
-              Shape* s) {
+// most; regs: of a thread; deep: rows of a group in the ring, where there is
+// room; most: blocks.
+bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int group_threads, int regs, int deep, int sms,
+              int most, Shape* s) {
     if (!al.ok) return false;
     const int W = al.window;
     const int windows = (D + (al.odd ? W - 1 : 0) + W - 1) / W;
@@ -909,11 +930,11 @@ bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int gr
     s->tpr = ((windows + s->nv - 1) / s->nv + 31) / 32 * 32;
     const int stage = s->nv * slots * 16, fixed = s->nv * (W / 2) * s->tpr * 16;      // bytes a thread; a block
     int groups = std::max(1, std::min(group_threads / s->tpr, 8));
-    while (groups > 1 && (static_cast<int64_t>(groups) * sms > T || 2 * groups * s->tpr * stage + fixed > kNormSmem)) --groups;
+    while (groups > 1 && (static_cast<int64_t>(groups) * sms > T || deep * groups * s->tpr * stage + fixed > kNormSmem)) --groups;
     s->threads = s->tpr * groups;
     int per_sm = std::max(1, std::min(65536 / (regs * s->threads), 2048 / s->threads));
-    // at least two rows in flight a group
-    while (per_sm > 1 && per_sm * (2 * stage * s->threads + fixed + 1024) > kNormSmem) --per_sm;
+    // at least `deep` rows in the ring of a group
+    while (per_sm > 1 && per_sm * (deep * stage * s->threads + fixed + 1024) > kNormSmem) --per_sm;
     int64_t grid = std::min<int64_t>((T + groups - 1) / groups, static_cast<int64_t>(sms) * per_sm);
     if (grid > most) grid = most;
     // a row's place in its windows has to be the same in all rows of a block
@@ -927,6 +948,7 @@ bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int gr
     int st = (kNormSmem / per_block - 1024 - fixed) / (stage * s->threads);
     st = std::max(1, std::min<int>(st, kNormMaxStages));
     s->stages = static_cast<int>(std::min<int64_t>(st, rows));
+    if (deep > 2 && s->stages < 2 && rows > 1) return false;         // two rows are in use at once
     s->smem = static_cast<size_t>(s->stages) * stage * s->threads + fixed;
     return s->smem <= static_cast<size_t>(kNormSmem);
 }
@@ -1021,7 +1043,7 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     const int slots = window_slots(true, a.dt_x, W) + window_slots(a.y, a.dt_y, W);
     // 896 threads in two groups of 448 for 7,168 elements: the one group's
     // sums overlap the other's loads and stores
-    if (shape_of(a.T, a.D, al, slots, 256, 1024, 64, sms, 1 << 30, &sh)) {
+    if (shape_of(a.T, a.D, al, slots, 256, 1024, 64, 2, sms, 1 << 30, &sh)) {
         if (kind == NORM_BF16) return sh.edge ? forward_as<true, NORM_BF16>(a, sh, s) : forward_as<false, NORM_BF16>(a, sh, s);
         if (kind == NORM_F32) return sh.edge ? forward_as<true, NORM_F32>(a, sh, s) : forward_as<false, NORM_F32>(a, sh, s);
         if (kind == NORM_BF16_Y32 && !sh.edge) return forward_as<false, NORM_BF16_Y32>(a, sh, s);
@@ -1061,7 +1083,7 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     const int most = norm_parts(a.T, a.D);
     Shape sh;
     int parts;
-    if (shape_of(a.T, a.D, al, slots, W == 4 ? 256 : 1024, 896, 72, sms, most, &sh)) {
+    if (shape_of(a.T, a.D, al, slots, W == 4 ? 256 : 1024, 896, 72, 3, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
         if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.D));
