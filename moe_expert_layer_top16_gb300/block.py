@@ -80,10 +80,12 @@ def _require(ok, what):
         _bad(what)
 
 
-# The current stream's handle without building a Stream object (2.8 us a call
-# on the host of a GB300), where this PyTorch has that shortcut.
+# The current stream's handle without a Stream object (2.8 us a call on the
+# host of a GB300) and the current device without a check of the context, where
+# this PyTorch has those shortcuts.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_current_device = torch.cuda.current_device
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_empty = torch.empty
 
 
 def _device(t, what):
@@ -96,15 +98,10 @@ def _device(t, what):
     return dev
 
 
-def _call(entry, name, dev, stream, *args):
-    """The entry point with `args` and the stream, on device `dev`."""
-    if dev == _current_device():
-        code = entry(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            code = entry(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if code != 0:
-        _check(code, name)
+def _on(dev, f, *args, **kwargs):
+    """f with device `dev` current."""
+    with torch.cuda.device(dev):
+        return f(*args, **kwargs)
 
 
 def _rows(t, what):
@@ -174,17 +171,22 @@ def sort_by_expert(idx: torch.Tensor, n_experts: int, stream=None):
     E = int(n_experts)
     if not 1 <= E <= 1024:
         _bad("sort_by_expert: 1 <= n_experts <= 1024")
+    if dev != _current():
+        return _on(dev, sort_by_expert, idx, E, stream)
     idx = idx.contiguous()
     T, k = idx.shape
     where = idx.device
-    slot_pos = torch.empty((T, k), dtype=torch.int32, device=where)
-    sorted_slot = torch.empty(T * k, dtype=torch.int32, device=where)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=where)
+    slot_pos = _empty((T, k), dtype=torch.int32, device=where)
+    sorted_slot = _empty(T * k, dtype=torch.int32, device=where)
+    offsets = _empty(E + 1, dtype=torch.int32, device=where)
     L = lib()
     size = L.moe_sort_workspace_bytes(T, k, E)
-    work = torch.empty(size, dtype=torch.uint8, device=where) if size else None
-    _call(L.moe_sort, "moe_sort", dev, stream, idx.data_ptr(), T, k, E, offsets.data_ptr(), sorted_slot.data_ptr(),
-          slot_pos.data_ptr(), _p(work), size)
+    work = _empty(size, dtype=torch.uint8, device=where) if size else None
+    code = L.moe_sort(idx.data_ptr(), T, k, E, offsets.data_ptr(), sorted_slot.data_ptr(), slot_pos.data_ptr(),
+                      work.data_ptr() if size else None, size,
+                      _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_sort")
     return offsets, sorted_slot, slot_pos
 
 
@@ -193,6 +195,8 @@ def permute(x: torch.Tensor, slot_pos: torch.Tensor, out: Optional[torch.Tensor]
     (codes and scales too); out [n][D], by default T * k new rows, whose places
     that no slot names are not initialised."""
     dev = _device(x, "permute")
+    if dev != _current():
+        return _on(dev, permute, x, slot_pos, out, stream)
     T, k = _slots(slot_pos, dev, "permute")
     if x.dim() != 2 or x.shape[0] != T or x.shape[1] < 1:
         _bad("permute: x is [T][D]")
@@ -200,12 +204,14 @@ def permute(x: torch.Tensor, slot_pos: torch.Tensor, out: Optional[torch.Tensor]
     D, size = x.shape[1], x.element_size()
     if out is None:
         n, ld_rows = T * k, D
-        out = torch.empty((n, D), dtype=x.dtype, device=x.device)
+        out = _empty((n, D), dtype=x.dtype, device=x.device)
     else:
         n = out.shape[0] if out.dim() == 2 else -1
         ld_rows = _out_rows(out, n, D, x.dtype, dev, "permute")
-    _call(lib().moe_permute, "moe_permute", dev, stream, x.data_ptr(), ld * size, D * size, T, k, slot_pos.data_ptr(), n,
-          out.data_ptr(), ld_rows * size)
+    code = lib().moe_permute(x.data_ptr(), ld * size, D * size, T, k, slot_pos.data_ptr(), n, out.data_ptr(), ld_rows * size,
+                             _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_permute")
     return out
 
 
@@ -213,6 +219,8 @@ def unpermute(rows: torch.Tensor, slot_pos: torch.Tensor, weights: Optional[torc
               out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] rows[slot_pos[t, j]] (see moe_unpermute); y [T][D] of out_dtype (default: rows')."""
     dev = _device(rows, "unpermute")
+    if dev != _current():
+        return _on(dev, unpermute, rows, slot_pos, weights, out_dtype, out, stream)
     T, k = _slots(slot_pos, dev, "unpermute")
     if rows.dim() != 2 or rows.shape[1] < 1:
         _bad("unpermute: rows is [n][D]")
@@ -223,11 +231,14 @@ def unpermute(rows: torch.Tensor, slot_pos: torch.Tensor, weights: Optional[torc
     if dtype not in DTYPES:
         _bad("unpermute: output type")
     if out is None:
-        out, ld_y = torch.empty((T, D), dtype=dtype, device=rows.device), D
+        out, ld_y = _empty((T, D), dtype=dtype, device=rows.device), D
     else:
         ld_y = _out_rows(out, T, D, dtype, dev, "unpermute")
-    _call(lib().moe_unpermute, "moe_unpermute", dev, stream, rows.data_ptr(), ld, DTYPES[rows.dtype], n,
-          slot_pos.data_ptr(), _p(w), T, k, D, out.data_ptr(), ld_y, DTYPES[dtype])
+    code = lib().moe_unpermute(rows.data_ptr(), ld, DTYPES[rows.dtype], n, slot_pos.data_ptr(),
+                               None if w is None else w.data_ptr(), T, k, D, out.data_ptr(), ld_y, DTYPES[dtype],
+                               _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_unpermute")
     return out
 
 
@@ -244,6 +255,8 @@ def unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, slot_pos: torch.Ten
     or None; d_weights float32 [T][k], or None).  out: where d_rows goes; a new
     one's places that no slot names are not initialised."""
     dev = _device(dy, "unpermute_backward")
+    if dev != _current():
+        return _on(dev, unpermute_backward, dy, rows, slot_pos, weights, out, need_rows, need_weights, stream)
     T, k = _slots(slot_pos, dev, "unpermute_backward")
     if dy.dim() != 2 or dy.shape[0] != T or dy.shape[1] < 1 or rows.dim() != 2 or rows.shape[1] != dy.shape[1] \
             or rows.get_device() != dev:
@@ -256,12 +269,15 @@ def unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, slot_pos: torch.Ten
     if not need_rows:
         out = None
     elif out is None:
-        out = torch.empty((n, D), dtype=rows.dtype, device=rows.device)
+        out = _empty((n, D), dtype=rows.dtype, device=rows.device)
     else:
         ld_d = _out_rows(out, n, D, rows.dtype, dev, "unpermute_backward")
-    d_w = torch.empty((T, k), dtype=torch.float32, device=rows.device) if need_weights else None
-    _call(lib().moe_unpermute_backward, "moe_unpermute_backward", dev, stream, dy.data_ptr(), ld_dy, DTYPES[dy.dtype],
-          rows.data_ptr(), ld, DTYPES[rows.dtype], n, slot_pos.data_ptr(), _p(w), T, k, D, _p(out), ld_d, _p(d_w))
+    d_w = _empty((T, k), dtype=torch.float32, device=rows.device) if need_weights else None
+    code = lib().moe_unpermute_backward(dy.data_ptr(), ld_dy, DTYPES[dy.dtype], rows.data_ptr(), ld, DTYPES[rows.dtype], n,
+                                        slot_pos.data_ptr(), _p(w), T, k, D, _p(out), ld_d, _p(d_w),
+                                        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_unpermute_backward")
     return out, d_w
 
 
@@ -329,6 +345,9 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Opt
     contiguous rows."""
     what = "block_norm"
     dev = _device(x, what)
+    if dev != _current():
+        return _on(dev, block_norm, x, y, w_post=w_post, w_pre=w_pre, gate=gate, gate_per=gate_per, res_scale=res_scale,
+                   eps=eps, u_dtype=u_dtype, need_u=need_u, out_h=out_h, out_u=out_u, stream=stream)
     shape = x.shape
     if not shape or shape[-1] < 1:
         _bad("block_norm: x is [..., D]")
@@ -345,7 +364,7 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Opt
         yr, ld_y = _rows(y, what)
         y_p, y_type = yr.data_ptr(), DTYPES[yr.dtype]
         if out_h is None:
-            h = torch.empty(shape, dtype=x.dtype, device=x.device)
+            h = _empty(shape, dtype=x.dtype, device=x.device)
         else:
             h, ld_h = out_h, _out_like(out_h, shape, T, x.dtype, dev, what)
         h_p = h.data_ptr()
@@ -358,7 +377,7 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Opt
         if dt not in DTYPES:
             _bad("block_norm: u_dtype")
         if out_u is None:
-            u = torch.empty(shape, dtype=dt, device=x.device)
+            u = _empty(shape, dtype=dt, device=x.device)
         else:
             u, ld_u = out_u, _out_like(out_u, shape, T, dt, dev, what)
         u_p, u_type = u.data_ptr(), DTYPES[dt]
@@ -368,7 +387,9 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Opt
     if T:
         a = _BlockNormArgs(xr.data_ptr(), ld_x, y_p, ld_y, _p(w_post), _p(w_pre), gate_p, h_p, ld_h, u_p, ld_u, T, D,
                            DTYPES[xr.dtype], y_type, u_type, w_type, kind, res_scale, eps)
-        _call(lib().moe_block_norm, "moe_block_norm", dev, stream, a)
+        code = lib().moe_block_norm(a, _raw_stream(dev) if stream is None else stream.cuda_stream)
+        if code:
+            _check(code, "moe_block_norm")
     return h, u
 
 
@@ -384,6 +405,9 @@ def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], 
     the weights' and the gate's out."""
     what = "block_norm_backward"
     dev = _device(h, what)
+    if dev != _current():
+        return _on(dev, block_norm_backward, dh, du, h, y, w_post=w_post, w_pre=w_pre, gate=gate, gate_per=gate_per,
+                   res_scale=res_scale, eps=eps, need_weights=need_weights, stream=stream)
     shape, where = h.shape, h.device
     if not shape or shape[-1] < 1 or (dh is None and du is None):
         _bad("block_norm_backward: dh or du, and h [..., D]")
@@ -406,12 +430,12 @@ def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], 
         du_p, u_type = dur.data_ptr(), DTYPES[dur.dtype]
     else:
         w_pre = None
-    dx = torch.empty(shape, dtype=h.dtype, device=where)
+    dx = _empty(shape, dtype=h.dtype, device=where)
     dy = None
     if y is not None:
         yr, ld_y = _rows(y, what)
         y_p, y_type = yr.data_ptr(), DTYPES[yr.dtype]
-        dy = torch.empty(shape, dtype=y.dtype, device=where)
+        dy = _empty(shape, dtype=y.dtype, device=where)
         dy_p = dy.data_ptr()
         gate, kind = _gate(gate, gate_per, T, D, dev, what)
         gate_p = _p(gate)
@@ -422,21 +446,23 @@ def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], 
     if need_weights:
         columns = 0
         if w_post is not None:
-            dw_post, columns = torch.empty(D, dtype=torch.float32, device=where), 1
+            dw_post, columns = _empty(D, dtype=torch.float32, device=where), 1
         if w_pre is not None:
-            dw_pre, columns = torch.empty(D, dtype=torch.float32, device=where), 1
+            dw_pre, columns = _empty(D, dtype=torch.float32, device=where), 1
         if kind == GATE_CHANNEL:
-            d_gate, columns = torch.empty(D, dtype=torch.float32, device=where), 1
+            d_gate, columns = _empty(D, dtype=torch.float32, device=where), 1
         elif kind == GATE_TOKEN:
-            d_gate = torch.empty(T, dtype=torch.float32, device=where)
+            d_gate = _empty(T, dtype=torch.float32, device=where)
         if columns and T:
             size = lib().moe_block_norm_workspace_bytes(T, D)
-            work = torch.empty(size, dtype=torch.uint8, device=where)
+            work = _empty(size, dtype=torch.uint8, device=where)
             work_p = work.data_ptr()
     a = _BlockNormBackwardArgs(dh_p, ld_dh, du_p, ld_du, hr.data_ptr(), ld_h, y_p, ld_y, _p(w_post), _p(w_pre), gate_p,
                                dx.data_ptr(), D, dy_p, D, _p(dw_post), _p(dw_pre), _p(d_gate), work_p, size, T, D,
                                DTYPES[hr.dtype], y_type, u_type, w_type, kind, res_scale, eps)
-    _call(lib().moe_block_norm_backward, "moe_block_norm_backward", dev, stream, a)
+    code = lib().moe_block_norm_backward(a, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_block_norm_backward")
     return dict(dx=dx, dy=dy, dw_post=dw_post, dw_pre=dw_pre, d_gate=d_gate)
 
 
@@ -445,22 +471,27 @@ def mxfp4_quantize(x: torch.Tensor, stream=None):
     """MXFP4 of x [..., K] (float32, bfloat16 or float16; K a multiple of 32):
     (codes uint8 [..., K/2], scales uint8 [..., K/32]); see moe_mxfp4_quantize."""
     dev = _device(x, "mxfp4_quantize")
+    if dev != _current():
+        return _on(dev, mxfp4_quantize, x, stream)
     shape = x.shape
     if not shape or shape[-1] < 32 or shape[-1] % 32:
         _bad("mxfp4_quantize: K is a multiple of 32")
     K = shape[-1]
     xr, ld = _rows(x, "mxfp4_quantize")
-    codes = torch.empty(shape[:-1] + (K // 2,), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(shape[:-1] + (K // 32,), dtype=torch.uint8, device=x.device)
-    _call(lib().moe_mxfp4_quantize, "moe_mxfp4_quantize", dev, stream, xr.data_ptr(), ld, DTYPES[xr.dtype], xr.shape[0], K,
-          codes.data_ptr(), scales.data_ptr())
+    lead = tuple(shape[:-1])
+    codes = _empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
+    scales = _empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
+    code = lib().moe_mxfp4_quantize(xr.data_ptr(), ld, DTYPES[xr.dtype], xr.shape[0], K, codes.data_ptr(), scales.data_ptr(),
+                                    _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_mxfp4_quantize")
     return codes, scales
 
 
 def _mx4(codes, scales, what):
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.shape or not scales.shape \
-            or codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != 16 * scales.shape[-1] \
-            or codes.shape[-1] < 16 or codes.get_device() != scales.get_device():
+    c, s = tuple(codes.shape), tuple(scales.shape)
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not c or not s or c[:-1] != s[:-1] \
+            or c[-1] != 16 * s[-1] or c[-1] < 16 or codes.get_device() != scales.get_device():
         _bad(what + ": codes uint8 [..., K/2] and scales uint8 [..., K/32] of one device")
     return codes.contiguous(), scales.contiguous()
 
@@ -468,13 +499,17 @@ def _mx4(codes, scales, what):
 def mxfp4_decode(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """The values [..., K] that MXFP4 codes and scales stand for, rounded to `dtype`."""
     dev = _device(codes, "mxfp4_decode")
+    if dev != _current():
+        return _on(dev, mxfp4_decode, codes, scales, dtype, stream)
     codes, scales = _mx4(codes, scales, "mxfp4_decode")
     if dtype not in DTYPES:
         _bad("mxfp4_decode: output type")
     K = codes.shape[-1] * 2
-    x = torch.empty(codes.shape[:-1] + (K,), dtype=dtype, device=codes.device)
-    _call(lib().moe_mxfp4_decode, "moe_mxfp4_decode", dev, stream, codes.data_ptr(), scales.data_ptr(), x.numel() // K, K,
-          x.data_ptr(), K, DTYPES[dtype])
+    x = _empty(tuple(codes.shape[:-1]) + (K,), dtype=dtype, device=codes.device)
+    code = lib().moe_mxfp4_decode(codes.data_ptr(), scales.data_ptr(), x.numel() // K, K, x.data_ptr(), K, DTYPES[dtype],
+                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_mxfp4_decode")
     return x
 
 
@@ -487,6 +522,8 @@ def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tenso
     A[g].  Rows that belong to no group are left as they were."""
     what = "mx4_gemm"
     dev = _device(a_codes, what)
+    if dev != _current():
+        return _on(dev, mx4_gemm, a_codes, a_scales, b_codes, b_scales, offsets, out, out_dtype, status, stream)
     a_codes, a_scales = _mx4(a_codes, a_scales, what)
     b_codes, b_scales = _mx4(b_codes, b_scales, what)
     if b_codes.dim() != 2 or b_codes.shape[1] != a_codes.shape[-1] or b_codes.get_device() != dev:
@@ -507,9 +544,12 @@ def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tenso
     if dtype not in DTYPES:
         _bad("mx4_gemm: output type")
     if out is None:
-        out, ld = torch.empty((N, M), dtype=dtype, device=a_codes.device), M
+        out, ld = _empty((N, M), dtype=dtype, device=a_codes.device), M
     else:
         ld = _out_rows(out, N, M, dtype, dev, what)
-    _call(lib().moe_mx4_gemm, "moe_mx4_gemm", dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), G, M,
-          b_codes.data_ptr(), b_scales.data_ptr(), N, K, _p(offsets), out.data_ptr(), ld, DTYPES[dtype], _p(status))
+    code = lib().moe_mx4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), G, M, b_codes.data_ptr(), b_scales.data_ptr(), N, K,
+                              _p(offsets), out.data_ptr(), ld, DTYPES[dtype], _p(status),
+                              _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if code:
+        _check(code, "moe_mx4_gemm")
     return out
