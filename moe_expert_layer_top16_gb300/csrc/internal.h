@@ -364,11 +364,13 @@ struct Mx4Params {
     int G, M, N, K;
     int dt_out;
     int nt;                     // tokens of a work item at most
-    int b_box;
+    int b_box;                  // rows of a box of B (pairs: half of nt)
+    int pair;                   // on CTA pairs
     int stages, stage_bytes;
 };
-// Token rows of a work item and of a TMA box of B, for `N` rows in G groups.
-void mx4_tiles(int N, int G, int* nt, int* b_box);
+// Token rows of a work item and of a TMA box of B, for `N` rows in G groups,
+// and whether CTA pairs are used.
+void mx4_tiles(int M, int N, int G, int* nt, int* b_box, int* pair);
 cudaError_t launch_mx4_gemm(const Mx4Params& p, cudaStream_t s);
 
 // ------------------------------------------------------------------ tensor-core rate probe (peak.cu)

@@ -8,6 +8,9 @@
 //   product    out[n][m] = sum_k dq(B[n][k]) dq(A[g(n)][m][k]), A and B both
 //              MXFP4, on tcgen05 kind::mxf4 (K = 64 an instruction, twice the
 //              rate of the MXFP8 kind), fp32 accumulation
+#include <algorithm>
+#include <type_traits>
+
 #include "internal.h"
 #include "mx.cuh"
 #include "ptx.cuh"
@@ -228,6 +231,20 @@ __global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __rest
 //               bytes a row then cost the scale warps 215 to 290 cycles a stage.
 //   warps 8-11  epilogue
 // A warp writes and reads the TMEM lanes of its number modulo 4.
+//
+// Wide items run on CTA pairs (clusters of two, cta_group::2): M = 256, each
+// CTA holds its 128 rows of A, half of the item's rows of B and, in its TMEM,
+// the scales of its rows of A and of all of B's.  The even CTA issues the MMAs
+// of both; copies and scale writes of both count on its barriers, its commits
+// arrive on both CTAs'.  Unpaired, 41 KB of operands a stage came into an SM at
+// 64 bytes a cycle, which bounded the product; a pair's CTA takes 28 KB.
+#ifndef MOE_MX4_PAIR
+#define MOE_MX4_PAIR 1
+#endif
+#ifndef MOE_MX4_PAIR_FROM
+#define MOE_MX4_PAIR_FROM 96
+#endif
+constexpr int kMx4PairFrom = MOE_MX4_PAIR_FROM;   // tokens of a work item from which on pairs are used
 constexpr int kMx4BlockM = 128;
 constexpr int kMx4BlockK = 256;
 constexpr int kMx4NtMax = 192;                    // two accumulators and four sets of scale columns in 512;
@@ -252,7 +269,7 @@ struct Mx4Item {
 };
 
 struct Mx4Geometry {
-    int M, m_tiles, nt, G;
+    int M, m_rows, m_first, m_tiles, nt, G;      // m_rows: rows of A of an item, m_first: this CTA's first of them
     const int* tile_off;     // [G + 1] first token tile of each group
     const int* first;        // [G + 1] first row; first[G]: unused
     const int* count;        // [G]
@@ -269,7 +286,7 @@ __device__ __forceinline__ Mx4Item mx4_item(const Mx4Geometry& g, int64_t it) {
     }
     const int j = tile - g.tile_off[lo];
     Mx4Item w;
-    w.m0 = mt * kMx4BlockM;
+    w.m0 = mt * g.m_rows + g.m_first;
     w.a_row = lo * g.M + w.m0;
     w.b_row = g.first[lo] + j * g.nt;
     w.n = min(g.nt, g.count[lo] - j * g.nt);
@@ -310,7 +327,7 @@ __device__ __forceinline__ void store_out(void* out, int64_t off, float v) {
     else static_cast<__half*>(out)[off] = __float2half_rn(v);
 }
 
-template <int DT, bool SFT>
+template <int DT, bool SFT, bool PAIR>
 __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -335,16 +352,19 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     int* count = first + G + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* status = pin(p.status);
+    const int cta = PAIR ? static_cast<int>(cluster_ctarank()) : 0;      // the even CTA (0) issues the MMAs
+    const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+    const int units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&sfull[s], 4);
+            mbar_init(&sfull[s], PAIR && cta == 0 ? 8 : 4);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 4);
+            mbar_init(&tempty[b], PAIR && cta == 0 ? 8 : 4);
             mbar_init(&cfull[b], 1);
             mbar_init(&cempty[b], 4);
         }
@@ -359,8 +379,13 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         }
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, kMx4TmemCols);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(tmem_slot, kMx4TmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, kMx4TmemCols);
+            tmem_relinquish();
+        }
     }
     if (warp == 2) {
         // token tiles of each group, from the offsets (kept inside [0, N])
@@ -393,10 +418,13 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     }
     tc_fence_before();
     __syncthreads();
+    // a pair's barriers are initialised before either CTA signals the other's
+    if constexpr (PAIR) cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int m_tiles = (M + kMx4BlockM - 1) / kMx4BlockM;
-    const Mx4Geometry geo{M, m_tiles, nt, G, tile_off, first, count};
+    constexpr int kRows = PAIR ? 2 * kMx4BlockM : kMx4BlockM;
+    const int m_tiles = (M + kRows - 1) / kRows;
+    const Mx4Geometry geo{M, kRows, cta * kMx4BlockM, m_tiles, nt, G, tile_off, first, count};
     const int64_t items = static_cast<int64_t>(tile_off[G]) * m_tiles;
     const int KT = (K + kMx4BlockK - 1) / kMx4BlockK;
 
@@ -404,18 +432,29 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         // ------------------------------------------------------------ producer
         uint32_t stage = 0, phase = 0, issued = 0, issued_parity = 0;
         bool ok = true;
-        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        for (int64_t it = unit; ok && it < items; it += units) {
             const Mx4Item w = mx4_item(geo, it);
             const int nm = (w.n + 15) & ~15;
             const int nbox = (nm + b_box - 1) / b_box;
-            const uint32_t tx = static_cast<uint32_t>(kMx4ABytes + nbox * b_box * 128);
+            // (a pair: one box of half of the item's rows in each CTA, both
+            // counted on the even one's barrier)
+            const uint32_t tx = PAIR ? 2u * static_cast<uint32_t>(kMx4ABytes + b_box * 128)
+                                     : static_cast<uint32_t>(kMx4ABytes + nbox * b_box * 128);
             for (int kt = 0; kt < KT; ++kt) {
                 ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag, status, DEV_TIMEOUT_PRODUCER);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                if (elect_one()) {
+                if constexpr (PAIR) {
+                    if (elect_one()) {
+                        uint8_t* sb = base + stage * stage_bytes;
+                        const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+                        if (cta == 0) mbar_arrive_expect_tx(&full[stage], tx);
+                        tma_load_2d_pair(sb, &p.tmA, fb, kt * 128, w.a_row);
+                        tma_load_2d_pair(sb + off_b, &p.tmB, fb, kt * 128, w.b_row + cta * (nm >> 1));
+                    }
+                } else if (elect_one()) {
                     uint8_t* sb = base + stage * stage_bytes;
                     mbar_arrive_expect_tx(&full[stage], tx);
                     tma_load_2d(sb, &p.tmA, &full[stage], kt * 128, w.a_row);
@@ -431,13 +470,26 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
                 }
             }
         }
-        if (*abort_flag && lane == 0) {
-            // every copy in flight lands before the CTA leaves
+        if constexpr (PAIR) {
+            // the even CTA's MMAs read this CTA's stages and its commits arrive
+            // here: every stage is released before this CTA leaves
+            for (int i = 0; ok && i < S; ++i) {
+                ok = mbar_wait(&empty[stage], phase ^ 1, abort_flag, status, DEV_TIMEOUT_PRODUCER);
+                ok = __all_sync(0xffffffffu, ok);
+                if (++stage == static_cast<uint32_t>(S)) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (*abort_flag && lane == 0 && cta == 0) {
+            // every copy in flight lands before the CTA leaves (a pair's all
+            // count on the even CTA's barriers)
             for (int s = 0; s < S; ++s)
                 if (issued & (1u << s)) mx4_drain(&full[s], (issued_parity >> s) & 1u, status);
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && cta == 0) {
         // ------------------------------------------------------------ MMA issuer
         uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, set = 0;
         bool any = false;
@@ -445,14 +497,14 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         // start-address field counts 16-byte units)
         const uint64_t ad0 = sdesc_sw128(smem_u32(base)), bd0 = sdesc_sw128(smem_u32(base + off_b));
         const uint32_t sf0 = tmem + 2u * static_cast<uint32_t>(nt);
-        for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        for (int64_t it = unit; it < items; it += units) {
             const Mx4Item w = mx4_item(geo, it);
             const int nm = (w.n + 15) & ~15;
             bool ok = mbar_wait(&tempty[acc], acc_phase ^ 1, abort_flag, status, DEV_TIMEOUT_MMA);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * static_cast<uint32_t>(nt);
-            const uint32_t idesc0 = idesc_mxf4(kMx4BlockM, nm);
+            const uint32_t idesc0 = idesc_mxf4(kRows, nm);
             for (int kt = 0; kt < KT; ++kt) {
                 // a stage that is already there is seen so by every lane at
                 // once: the warp-wide vote only on the waiting path
@@ -469,13 +521,18 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
                 if (elect_one()) {
                     // scale ids 0 and 2: the low and high half of each scale word
                     constexpr uint32_t high = 2u << 4 | 2u << 29;
-                    mma_mxf4(d, ad, bd, idesc0, sfa, sfb, kt != 0 ? 1u : 0u);
-                    mma_mxf4(d, ad + 2, bd + 2, idesc0 | high, sfa, sfb, 1u);
+                    auto mma = [&](int j, uint32_t id, uint32_t fa, uint32_t fb, uint32_t add) {
+                        if constexpr (PAIR) mma_mxf4_pair(d, ad + 2 * j, bd + 2 * j, id, fa, fb, add);
+                        else mma_mxf4(d, ad + 2 * j, bd + 2 * j, id, fa, fb, add);
+                    };
+                    mma(0, idesc0, sfa, sfb, kt != 0 ? 1u : 0u);
+                    mma(1, idesc0 | high, sfa, sfb, 1u);
                     if (both) {
-                        mma_mxf4(d, ad + 4, bd + 4, idesc0, sfa + 4u, sfb + 8u, 1u);
-                        mma_mxf4(d, ad + 6, bd + 6, idesc0 | high, sfa + 4u, sfb + 8u, 1u);
+                        mma(2, idesc0, sfa + 4u, sfb + 8u, 1u);
+                        mma(3, idesc0 | high, sfa + 4u, sfb + 8u, 1u);
                     }
-                    tc_commit(&empty[stage]);
+                    if constexpr (PAIR) tc_commit_pair(&empty[stage], 3);
+                    else tc_commit(&empty[stage]);
                 }
                 any = true;
                 __syncwarp();
@@ -485,7 +542,10 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
                     phase ^= 1;
                 }
             }
-            if (elect_one()) tc_commit(&tfull[acc]);
+            if (elect_one()) {
+                if constexpr (PAIR) tc_commit_pair(&tfull[acc], 3);
+                else tc_commit(&tfull[acc]);
+            }
             __syncwarp();
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
@@ -494,7 +554,8 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         // every tcgen05 operation finishes before TMEM is freed
         if (any) {
             if (elect_one()) {
-                tc_commit(tdown);
+                if constexpr (PAIR) tc_commit_pair(tdown, 1);
+                else tc_commit(tdown);
                 mx4_drain(tdown, 0, status);
             }
             __syncwarp();
@@ -504,7 +565,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         const int batches = (KT + kMx4Batch - 1) / kMx4Batch;
         uint32_t buf = 0, phase = 0, issued = 0, issued_parity = 0;
         bool ok = true;
-        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        for (int64_t it = unit; ok && it < items; it += units) {
             const Mx4Item w = mx4_item(geo, it);
             for (int b = 0; b < batches; ++b) {
                 ok = mbar_wait(&cempty[buf], phase ^ 1, abort_flag, status, DEV_TIMEOUT_PRODUCER);
@@ -563,7 +624,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
                 }
             }
         };
-        int64_t it = blockIdx.x;
+        int64_t it = unit;
         int batch = 0, n = 0, n_next = 0;
         if (it < items) {
             const Mx4Item w = mx4_item(geo, it);
@@ -607,7 +668,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
             const int stages_here = min(kMx4Batch, KT - batch * kMx4Batch);
             if (++batch == batches) {
                 batch = 0;
-                it += gridDim.x;
+                it += units;
                 if (it < items) {
                     const Mx4Item w = mx4_item(geo, it);
                     n_next = w.n;
@@ -665,7 +726,12 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sfull[stage]);
+                    if (lane == 0) {
+                        // (the columns are written: tcgen05.wait::st; nothing in memory
+                        // to order, and a release at cluster scope costs a microsecond)
+                        if (PAIR && cta == 1) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&sfull[stage]), 0));
+                        else mbar_arrive(&sfull[stage]);
+                    }
                     ++turn;
                     if (++set == static_cast<uint32_t>(sets)) set = 0;
                     if (++stage == static_cast<uint32_t>(S)) stage = 0;
@@ -681,7 +747,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
         const int quarter = warp & 3;         // TMEM lanes this warp may read
         const uint32_t t_lane = static_cast<uint32_t>(32 * quarter) << 16;
         uint32_t acc = 0, acc_phase = 0;
-        for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        for (int64_t it = unit; it < items; it += units) {
             const Mx4Item w = mx4_item(geo, it);
             const bool ok = mbar_wait(&tfull[acc], acc_phase, abort_flag, status, DEV_TIMEOUT_EPILOGUE);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -712,45 +778,57 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[acc]);
+            if (lane == 0) {
+                // (this warp's TMEM loads are complete: nothing else to order)
+                if (PAIR && cta == 1) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[acc]), 0));
+                else mbar_arrive(&tempty[acc]);
+            }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
         }
     }
     tc_fence_before();
     __syncthreads();
+    // neither CTA of a pair frees TMEM or leaves while the other may still
+    // signal its barriers
+    if constexpr (PAIR) cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, kMx4TmemCols);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, kMx4TmemCols);
+        else tmem_dealloc(tmem, kMx4TmemCols);
     }
 }
 
-int mx4_stage_bytes(int nt) { return (kMx4ABytes + nt * 128 + 1023) & ~1023; }
+int mx4_stage_bytes(int nt, bool pair) { return (kMx4ABytes + (pair ? nt / 2 : nt) * 128 + 1023) & ~1023; }
 
 int mx4_table_bytes(int G) { return (3 * (G + 1) * 4 + 15) & ~15; }
 
 }  // namespace
 
-void mx4_tiles(int N, int G, int* nt, int* b_box) {
+void mx4_tiles(int M, int N, int G, int* nt, int* b_box, int* pair) {
     if (G == 1) {
         // equal tiles, a box each
         const int tiles = (N + kMx4NtMax - 1) / kMx4NtMax;
         *nt = ((N + tiles - 1) / tiles + 15) & ~15;
         *b_box = *nt;
-        return;
+    } else {
+        // room for about twice the mean; boxes that follow a short group's rows
+        int64_t n = (2 * static_cast<int64_t>(N) + G - 1) / G;
+        n = n > kMx4NtMax ? kMx4NtMax : (n < 16 ? 16 : n);
+        *b_box = n > 64 ? 32 : 16;
+        *nt = static_cast<int>((n + *b_box - 1) / *b_box * *b_box);
     }
-    // room for about twice the mean; boxes that follow a short group's rows
-    int64_t n = (2 * static_cast<int64_t>(N) + G - 1) / G;
-    n = n > kMx4NtMax ? kMx4NtMax : (n < 16 ? 16 : n);
-    *b_box = n > 64 ? 32 : 16;
-    *nt = static_cast<int>((n + *b_box - 1) / *b_box * *b_box);
+    *pair = MOE_MX4_PAIR && *nt >= kMx4PairFrom && M > kMx4BlockM;
+    if (*pair) *b_box = *nt / 2;
 }
 
 cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
     Mx4Params p = in;
     if (p.M < 1 || p.N < 1 || p.K < 128 || p.K % 128 || p.G < 1 || p.G > kMx4MaxGroups) return cudaErrorInvalidValue;
-    if (p.nt < 16 || p.nt > kMx4NtMax || p.nt % 16 || p.b_box < 16 || p.nt % p.b_box) return cudaErrorInvalidValue;
-    p.stage_bytes = mx4_stage_bytes(p.nt);
+    const bool pair = p.pair != 0;
+    if (p.nt < 16 || p.nt > kMx4NtMax || p.nt % 16 || (pair ? 2 * p.b_box != p.nt : (p.b_box < 16 || p.nt % p.b_box)))
+        return cudaErrorInvalidValue;
+    p.stage_bytes = mx4_stage_bytes(p.nt, pair);
     const int fixed = 1024 + kMx4ScaleBytes + kMx4BarBytes + mx4_table_bytes(p.G);
     p.stages = (kSmemLimit - fixed) / p.stage_bytes;
     if (p.stages > kMx4MaxStages) p.stages = kMx4MaxStages;
@@ -760,23 +838,25 @@ cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    const int64_t m_tiles = (p.M + kMx4BlockM - 1) / kMx4BlockM;
+    const int64_t m_tiles = (p.M + (pair ? 2 : 1) * kMx4BlockM - 1) / ((pair ? 2 : 1) * kMx4BlockM);
     const int64_t most = m_tiles * ((p.N + p.nt - 1) / p.nt + p.G - 1);
-    const int grid = static_cast<int>(most < sms ? most : sms);
+    const int64_t units = std::min<int64_t>(most, pair ? std::max(1, gemm_pair_clusters()) : sms);
     auto run = [&](void (*kern)(Mx4Params)) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
-        kern<<<grid, kMx4Threads, smem, s>>>(p);
+        if (pair)
+            return launch_ex_cluster(kern, dim3(static_cast<unsigned>(2 * units)), dim3(kMx4Threads), smem, s, false, 2, p);
+        kern<<<static_cast<unsigned>(units), kMx4Threads, smem, s>>>(p);
         return cudaGetLastError();
     };
-    if (p.sf_tma) {
-        if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32, true>);
-        if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16, true>);
-        return run(mx4_gemm_kernel<ELEM_F16, true>);
-    }
-    if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32, false>);
-    if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16, false>);
-    return run(mx4_gemm_kernel<ELEM_F16, false>);
+    auto with = [&](auto sft, auto paired) {
+        constexpr bool SFT = decltype(sft)::value, PAIR = decltype(paired)::value;
+        if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32, SFT, PAIR>);
+        if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16, SFT, PAIR>);
+        return run(mx4_gemm_kernel<ELEM_F16, SFT, PAIR>);
+    };
+    if (pair) return p.sf_tma ? with(std::true_type{}, std::true_type{}) : with(std::false_type{}, std::true_type{});
+    return p.sf_tma ? with(std::true_type{}, std::false_type{}) : with(std::false_type{}, std::false_type{});
 }
 
 namespace {
