@@ -237,14 +237,12 @@ __global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __rest
 // the scales of its rows of A and of all of B's.  The even CTA issues the MMAs
 // of both; copies and scale writes of both count on its barriers, its commits
 // arrive on both CTAs'.  Unpaired, 41 KB of operands a stage came into an SM at
-// 64 bytes a cycle, which bounded the product; a pair's CTA takes 28 KB.
-#ifndef MOE_MX4_PAIR
-#define MOE_MX4_PAIR 1
-#endif
-#ifndef MOE_MX4_PAIR_FROM
-#define MOE_MX4_PAIR_FROM 96
-#endif
-constexpr int kMx4PairFrom = MOE_MX4_PAIR_FROM;   // tokens of a work item from which on pairs are used
+// 64 bytes a cycle, which bounded the product; a pair's CTA takes 28 KB.  Groups
+// of few rows are bound by A's way from HBM, which pairs do not shorten.  Pairs
+// against single CTAs, M = 8192, K = 7168: 4,096 rows 82.3 and 90.5 us, 1,024
+// rows 31.3 and 33.4, 512 rows 24.4 and 24.9; 64 groups of 146 rows (M = 1024,
+// K = 3584) 37.9 and 35.9, 16 of 125 rows 13.5 and 12.4.
+constexpr int kMx4PairRows = 512;                 // rows of B a group, on average, from which on pairs are used
 constexpr int kMx4BlockM = 128;
 constexpr int kMx4BlockK = 256;
 constexpr int kMx4NtMax = 192;                    // two accumulators and four sets of scale columns in 512;
@@ -818,7 +816,7 @@ void mx4_tiles(int M, int N, int G, int* nt, int* b_box, int* pair) {
         *b_box = n > 64 ? 32 : 16;
         *nt = static_cast<int>((n + *b_box - 1) / *b_box * *b_box);
     }
-    *pair = MOE_MX4_PAIR && *nt >= kMx4PairFrom && M > kMx4BlockM;
+    *pair = N >= static_cast<int64_t>(kMx4PairRows) * G && M > kMx4BlockM;
     if (*pair) *b_box = *nt / 2;
 }
 
