@@ -377,7 +377,8 @@ MOE_API moe_status moe_sort(const int32_t *idx, int32_t T, int32_t k, int32_t E,
 /* rows[slot_pos[t][j]] = x[t] for every slot: rows of row_bytes bytes of any
  * type (activations, MXFP4 or MXFP8 codes, scales).  Strides in bytes, at
  * least row_bytes.  Places that no slot names are left as they were; a place
- * outside [0, n_rows) counts as dropped. */
+ * outside [0, n_rows) counts as dropped.  No two slots may name one place
+ * (moe_sort's do not). */
 MOE_API moe_status moe_permute(const void *x, int64_t x_stride, int64_t row_bytes, int32_t T, int32_t k,
                                const int32_t *slot_pos, int64_t n_rows, void *rows, int64_t rows_stride,
                                void *stream);
@@ -386,7 +387,7 @@ MOE_API moe_status moe_permute(const void *x, int64_t x_stride, int64_t row_byte
  * the layer's combine.  w fp32 [T][k]; with w = NULL every weight is one,
  * which is the gradient of moe_permute.  Dropped slots (a place outside
  * [0, n_rows)) add nothing and their rows are not read; a token without kept
- * slots gets zeros.  D >= 1. */
+ * slots gets zeros.  1 <= D <= 2^30. */
 MOE_API moe_status moe_unpermute(const void *rows, int64_t ld_rows, int32_t dtype, int64_t n_rows,
                                  const int32_t *slot_pos, const float *w, int32_t T, int32_t k, int32_t D, void *y,
                                  int64_t ld_y, int32_t y_dtype, void *stream);
@@ -395,7 +396,8 @@ MOE_API moe_status moe_unpermute(const void *rows, int64_t ld_rows, int32_t dtyp
  *   d_rows[slot_pos[t][j]] = w[t][j] dy[t]   (type of rows; places that no
  *                                             slot names are left as they were)
  *   d_w[t][j] = <dy[t], rows[slot_pos[t][j]]>   fp32, 0 for a dropped slot
- * Either output may be NULL (rows is read only for d_w). */
+ * Either output may be NULL (rows is read only for d_w).  For d_rows no two
+ * slots may name one place. */
 MOE_API moe_status moe_unpermute_backward(const void *dy, int64_t ld_dy, int32_t dy_dtype, const void *rows,
                                           int64_t ld_rows, int32_t dtype, int64_t n_rows, const int32_t *slot_pos,
                                           const float *w, int32_t T, int32_t k, int32_t D, void *d_rows,
@@ -483,7 +485,7 @@ MOE_API moe_status moe_block_norm_backward(const moe_block_norm_backward_args *a
 /* MXFP4 of activations: x [rows][K] of any moe_dtype into codes [rows][K/2]
  * (4-byte aligned) and scales [rows][K/32], by moe_mxfp4_encode's rule.  A
  * block that holds an infinity or a NaN gets scale code 255 (not a number)
- * and codes 0.  K a multiple of 32, rows >= 0. */
+ * and codes 0.  K a multiple of 32, rows >= 0, rows K <= 2^48. */
 MOE_API moe_status moe_mxfp4_quantize(const void *x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t K,
                                       uint8_t *codes, uint8_t *scales, void *stream);
 
@@ -501,7 +503,7 @@ MOE_API moe_status moe_mxfp4_decode(const uint8_t *codes, const uint8_t *scales,
  * [G + 1], ascending, as moe_sort writes them (values are kept inside [0, N]);
  * NULL with G = 1: all rows.  Rows outside [offsets[0], offsets[G]) are left
  * as they were.  M >= 1, N >= 0, K a multiple of 128, 1 <= G <= 1024,
- * G M < 2^31.  dev_status (device int32, optional) receives a non-zero code if
+ * G M <= 2^31 - 256.  dev_status (device int32, optional) receives a non-zero code if
  * a bounded wait inside the kernel ran out, as with moe_mx_gemm.  A device of
  * compute capability 10.3 is needed. */
 MOE_API moe_status moe_mx4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, int32_t G, int32_t M,

@@ -288,6 +288,10 @@ class Plan:
         next_u = next_w_pre h / rms(h) is the next block's input, to be given to
         its call as `u`, which then computes no norm of its own."""
         what = "forward_block"
+        if stream is not None:
+            return block._on(self.device.index, stream, self.forward_block, x, w_pre=w_pre, w_post=w_post, gate=gate,
+                             gate_per=gate_per, res_scale=res_scale, eps=eps, u=u, next_w_pre=next_w_pre,
+                             need_next_u=need_next_u)
         block._require(x.is_cuda and x.device == self.device and x.dim() == 2 and x.shape[1] == self.cfg.d_model
                        and x.dtype in block.DTYPES, "forward_block: x is [T][D] on the plan's device")
         x = x.contiguous()
@@ -316,7 +320,7 @@ class Plan:
                          ("gate", gate), ("next_w_pre", next_w_pre)):
                 setattr(a, n, None if t is None else t.data_ptr())
             a.x_dtype, a.res_scale, a.eps = block.DTYPES[x.dtype], res_scale, eps
-            _check(lib().moe_forward_block(self._h, C.byref(a), T, _stream_ptr(stream)), "moe_forward_block")
+            _check(lib().moe_forward_block(self._h, C.byref(a), T, _stream_ptr()), "moe_forward_block")
         return h, next_u
 
     def forward_host(self, x_host: torch.Tensor, y_host: torch.Tensor, stream=None):

@@ -3,11 +3,13 @@ behind and before a block, and four-bit activations with their product.
 
 Argument marshalling for the stand-alone entry points of ``include/moe.h``;
 nothing is computed here.  Every function takes CUDA tensors of one device,
-runs on that device's current stream (or `stream`), does not synchronise, and
-can be captured in a CUDA graph.  Rows may be strided (a copy is made only
-where a row's elements are not contiguous).  Bad arguments raise
-:class:`MoeError` with MOE_ERR_INVALID_ARG before anything is enqueued.
-Gradients are calls of their own; nothing is recorded for autograd.
+runs on that device's current stream, does not synchronise, and can be captured
+in a CUDA graph.  With `stream` (a torch.cuda.Stream of that device) it runs as
+inside ``with torch.cuda.stream(stream)``: what it allocates, outputs among it,
+belongs to that stream, and the inputs have to be ready there.  Rows may be
+strided (a copy is made only where a row's elements are not contiguous).  Bad
+arguments raise :class:`MoeError` with MOE_ERR_INVALID_ARG before anything is
+enqueued.  Gradients are calls of their own; nothing is recorded for autograd.
 """
 from __future__ import annotations
 
@@ -98,10 +100,22 @@ def _device(t, what):
     return dev
 
 
-def _on(dev, f, *args, **kwargs):
-    """f with device `dev` current."""
-    with torch.cuda.device(dev):
+def _on(dev, stream, f, *args, **kwargs):
+    """f with device `dev`, or its stream `stream`, current.  Copies and workspaces then belong to the stream that
+    reads them: memory of another stream may be handed out again before the kernels are through with it."""
+    if stream is None:
+        with torch.cuda.device(dev):
+            return f(*args, **kwargs)
+    if not isinstance(stream, torch.cuda.Stream) or stream.device_index != dev:
+        _bad(f.__name__ + ": stream is a torch.cuda.Stream of the tensors' device")
+    with torch.cuda.stream(stream):
         return f(*args, **kwargs)
+
+
+def _int32(n, what):
+    """Sizes go to the entry points as 32-bit integers, which the call would cut off."""
+    if n > 0x7fffffff:
+        _bad(what + ": sizes below 2^31")
 
 
 def _rows(t, what):
@@ -145,6 +159,7 @@ def _out_rows(out, T, D, dtype, dev, what):
 def _slots(slot_pos, dev, what):
     if slot_pos.dtype != torch.int32 or slot_pos.dim() != 2 or not slot_pos.is_contiguous() or slot_pos.get_device() != dev:
         _bad(what + ": slot_pos is a contiguous int32 [T][k] on the same device")
+    _int32(slot_pos.numel(), what)
     return slot_pos.shape
 
 
@@ -171,8 +186,9 @@ def sort_by_expert(idx: torch.Tensor, n_experts: int, stream=None):
     E = int(n_experts)
     if not 1 <= E <= 1024:
         _bad("sort_by_expert: 1 <= n_experts <= 1024")
-    if dev != _current():
-        return _on(dev, sort_by_expert, idx, E, stream)
+    _int32(idx.numel(), "sort_by_expert")
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, sort_by_expert, idx, E)
     idx = idx.contiguous()
     T, k = idx.shape
     where = idx.device
@@ -183,8 +199,7 @@ def sort_by_expert(idx: torch.Tensor, n_experts: int, stream=None):
     size = L.moe_sort_workspace_bytes(T, k, E)
     work = _empty(size, dtype=torch.uint8, device=where) if size else None
     code = L.moe_sort(idx.data_ptr(), T, k, E, offsets.data_ptr(), sorted_slot.data_ptr(), slot_pos.data_ptr(),
-                      work.data_ptr() if size else None, size,
-                      _raw_stream(dev) if stream is None else stream.cuda_stream)
+                      work.data_ptr() if size else None, size, _raw_stream(dev))
     if code:
         _check(code, "moe_sort")
     return offsets, sorted_slot, slot_pos
@@ -195,8 +210,8 @@ def permute(x: torch.Tensor, slot_pos: torch.Tensor, out: Optional[torch.Tensor]
     (codes and scales too); out [n][D], by default T * k new rows, whose places
     that no slot names are not initialised."""
     dev = _device(x, "permute")
-    if dev != _current():
-        return _on(dev, permute, x, slot_pos, out, stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, permute, x, slot_pos, out)
     T, k = _slots(slot_pos, dev, "permute")
     if x.dim() != 2 or x.shape[0] != T or x.shape[1] < 1:
         _bad("permute: x is [T][D]")
@@ -208,8 +223,7 @@ def permute(x: torch.Tensor, slot_pos: torch.Tensor, out: Optional[torch.Tensor]
     else:
         n = out.shape[0] if out.dim() == 2 else -1
         ld_rows = _out_rows(out, n, D, x.dtype, dev, "permute")
-    code = lib().moe_permute(x.data_ptr(), ld * size, D * size, T, k, slot_pos.data_ptr(), n, out.data_ptr(), ld_rows * size,
-                             _raw_stream(dev) if stream is None else stream.cuda_stream)
+    code = lib().moe_permute(x.data_ptr(), ld * size, D * size, T, k, slot_pos.data_ptr(), n, out.data_ptr(), ld_rows * size, _raw_stream(dev))
     if code:
         _check(code, "moe_permute")
     return out
@@ -219,13 +233,14 @@ def unpermute(rows: torch.Tensor, slot_pos: torch.Tensor, weights: Optional[torc
               out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] rows[slot_pos[t, j]] (see moe_unpermute); y [T][D] of out_dtype (default: rows')."""
     dev = _device(rows, "unpermute")
-    if dev != _current():
-        return _on(dev, unpermute, rows, slot_pos, weights, out_dtype, out, stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, unpermute, rows, slot_pos, weights, out_dtype, out)
     T, k = _slots(slot_pos, dev, "unpermute")
     if rows.dim() != 2 or rows.shape[1] < 1:
         _bad("unpermute: rows is [n][D]")
     rows, ld = _rows(rows, "unpermute")
     n, D = rows.shape
+    _int32(D, "unpermute")
     w = _weights_of(weights, slot_pos, "unpermute")
     dtype = out_dtype or (rows.dtype if out is None else out.dtype)
     if dtype not in DTYPES:
@@ -235,8 +250,7 @@ def unpermute(rows: torch.Tensor, slot_pos: torch.Tensor, weights: Optional[torc
     else:
         ld_y = _out_rows(out, T, D, dtype, dev, "unpermute")
     code = lib().moe_unpermute(rows.data_ptr(), ld, DTYPES[rows.dtype], n, slot_pos.data_ptr(),
-                               None if w is None else w.data_ptr(), T, k, D, out.data_ptr(), ld_y, DTYPES[dtype],
-                               _raw_stream(dev) if stream is None else stream.cuda_stream)
+                               None if w is None else w.data_ptr(), T, k, D, out.data_ptr(), ld_y, DTYPES[dtype], _raw_stream(dev))
     if code:
         _check(code, "moe_unpermute")
     return out
@@ -255,8 +269,8 @@ def unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, slot_pos: torch.Ten
     or None; d_weights float32 [T][k], or None).  out: where d_rows goes; a new
     one's places that no slot names are not initialised."""
     dev = _device(dy, "unpermute_backward")
-    if dev != _current():
-        return _on(dev, unpermute_backward, dy, rows, slot_pos, weights, out, need_rows, need_weights, stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, unpermute_backward, dy, rows, slot_pos, weights, out, need_rows, need_weights)
     T, k = _slots(slot_pos, dev, "unpermute_backward")
     if dy.dim() != 2 or dy.shape[0] != T or dy.shape[1] < 1 or rows.dim() != 2 or rows.shape[1] != dy.shape[1] \
             or rows.get_device() != dev:
@@ -264,6 +278,7 @@ def unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, slot_pos: torch.Ten
     dy, ld_dy = _rows(dy, "unpermute_backward")
     rows, ld = _rows(rows, "unpermute_backward")
     n, D = rows.shape
+    _int32(D, "unpermute_backward")
     w = _weights_of(weights, slot_pos, "unpermute_backward")
     ld_d = D
     if not need_rows:
@@ -274,8 +289,7 @@ def unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, slot_pos: torch.Ten
         ld_d = _out_rows(out, n, D, rows.dtype, dev, "unpermute_backward")
     d_w = _empty((T, k), dtype=torch.float32, device=rows.device) if need_weights else None
     code = lib().moe_unpermute_backward(dy.data_ptr(), ld_dy, DTYPES[dy.dtype], rows.data_ptr(), ld, DTYPES[rows.dtype], n,
-                                        slot_pos.data_ptr(), _p(w), T, k, D, _p(out), ld_d, _p(d_w),
-                                        _raw_stream(dev) if stream is None else stream.cuda_stream)
+                                        slot_pos.data_ptr(), _p(w), T, k, D, _p(out), ld_d, _p(d_w), _raw_stream(dev))
     if code:
         _check(code, "moe_unpermute_backward")
     return out, d_w
@@ -345,15 +359,16 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Opt
     contiguous rows."""
     what = "block_norm"
     dev = _device(x, what)
-    if dev != _current():
-        return _on(dev, block_norm, x, y, w_post=w_post, w_pre=w_pre, gate=gate, gate_per=gate_per, res_scale=res_scale,
-                   eps=eps, u_dtype=u_dtype, need_u=need_u, out_h=out_h, out_u=out_u, stream=stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, block_norm, x, y, w_post=w_post, w_pre=w_pre, gate=gate, gate_per=gate_per, res_scale=res_scale,
+                   eps=eps, u_dtype=u_dtype, need_u=need_u, out_h=out_h, out_u=out_u)
     shape = x.shape
     if not shape or shape[-1] < 1:
         _bad("block_norm: x is [..., D]")
     D = shape[-1]
     xr, ld_x = _rows(x, what)
     T = xr.shape[0]
+    _int32(max(T, D), what)
     h, u = x, None
     y_p = h_p = u_p = gate_p = None
     ld_y = ld_h = ld_u = D
@@ -387,7 +402,7 @@ def block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, *, w_post: Opt
     if T:
         a = _BlockNormArgs(xr.data_ptr(), ld_x, y_p, ld_y, _p(w_post), _p(w_pre), gate_p, h_p, ld_h, u_p, ld_u, T, D,
                            DTYPES[xr.dtype], y_type, u_type, w_type, kind, res_scale, eps)
-        code = lib().moe_block_norm(a, _raw_stream(dev) if stream is None else stream.cuda_stream)
+        code = lib().moe_block_norm(a, _raw_stream(dev))
         if code:
             _check(code, "moe_block_norm")
     return h, u
@@ -405,9 +420,9 @@ def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], 
     the weights' and the gate's out."""
     what = "block_norm_backward"
     dev = _device(h, what)
-    if dev != _current():
-        return _on(dev, block_norm_backward, dh, du, h, y, w_post=w_post, w_pre=w_pre, gate=gate, gate_per=gate_per,
-                   res_scale=res_scale, eps=eps, need_weights=need_weights, stream=stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, block_norm_backward, dh, du, h, y, w_post=w_post, w_pre=w_pre, gate=gate, gate_per=gate_per,
+                   res_scale=res_scale, eps=eps, need_weights=need_weights)
     shape, where = h.shape, h.device
     if not shape or shape[-1] < 1 or (dh is None and du is None):
         _bad("block_norm_backward: dh or du, and h [..., D]")
@@ -419,6 +434,7 @@ def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], 
         _bad("block_norm_backward: dh has h's type")
     hr, ld_h = _rows(h, what)
     T = hr.shape[0]
+    _int32(max(T, D), what)
     dh_p = du_p = y_p = dy_p = gate_p = work_p = None
     ld_dh = ld_du = ld_y = D
     u_type = y_type = kind = size = 0
@@ -460,7 +476,7 @@ def block_norm_backward(dh: Optional[torch.Tensor], du: Optional[torch.Tensor], 
     a = _BlockNormBackwardArgs(dh_p, ld_dh, du_p, ld_du, hr.data_ptr(), ld_h, y_p, ld_y, _p(w_post), _p(w_pre), gate_p,
                                dx.data_ptr(), D, dy_p, D, _p(dw_post), _p(dw_pre), _p(d_gate), work_p, size, T, D,
                                DTYPES[hr.dtype], y_type, u_type, w_type, kind, res_scale, eps)
-    code = lib().moe_block_norm_backward(a, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    code = lib().moe_block_norm_backward(a, _raw_stream(dev))
     if code:
         _check(code, "moe_block_norm_backward")
     return dict(dx=dx, dy=dy, dw_post=dw_post, dw_pre=dw_pre, d_gate=d_gate)
@@ -471,8 +487,8 @@ def mxfp4_quantize(x: torch.Tensor, stream=None):
     """MXFP4 of x [..., K] (float32, bfloat16 or float16; K a multiple of 32):
     (codes uint8 [..., K/2], scales uint8 [..., K/32]); see moe_mxfp4_quantize."""
     dev = _device(x, "mxfp4_quantize")
-    if dev != _current():
-        return _on(dev, mxfp4_quantize, x, stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, mxfp4_quantize, x)
     shape = x.shape
     if not shape or shape[-1] < 32 or shape[-1] % 32:
         _bad("mxfp4_quantize: K is a multiple of 32")
@@ -481,8 +497,7 @@ def mxfp4_quantize(x: torch.Tensor, stream=None):
     lead = tuple(shape[:-1])
     codes = _empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
     scales = _empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
-    code = lib().moe_mxfp4_quantize(xr.data_ptr(), ld, DTYPES[xr.dtype], xr.shape[0], K, codes.data_ptr(), scales.data_ptr(),
-                                    _raw_stream(dev) if stream is None else stream.cuda_stream)
+    code = lib().moe_mxfp4_quantize(xr.data_ptr(), ld, DTYPES[xr.dtype], xr.shape[0], K, codes.data_ptr(), scales.data_ptr(), _raw_stream(dev))
     if code:
         _check(code, "moe_mxfp4_quantize")
     return codes, scales
@@ -499,15 +514,14 @@ def _mx4(codes, scales, what):
 def mxfp4_decode(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """The values [..., K] that MXFP4 codes and scales stand for, rounded to `dtype`."""
     dev = _device(codes, "mxfp4_decode")
-    if dev != _current():
-        return _on(dev, mxfp4_decode, codes, scales, dtype, stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, mxfp4_decode, codes, scales, dtype)
     codes, scales = _mx4(codes, scales, "mxfp4_decode")
     if dtype not in DTYPES:
         _bad("mxfp4_decode: output type")
     K = codes.shape[-1] * 2
     x = _empty(tuple(codes.shape[:-1]) + (K,), dtype=dtype, device=codes.device)
-    code = lib().moe_mxfp4_decode(codes.data_ptr(), scales.data_ptr(), x.numel() // K, K, x.data_ptr(), K, DTYPES[dtype],
-                                  _raw_stream(dev) if stream is None else stream.cuda_stream)
+    code = lib().moe_mxfp4_decode(codes.data_ptr(), scales.data_ptr(), x.numel() // K, K, x.data_ptr(), K, DTYPES[dtype], _raw_stream(dev))
     if code:
         _check(code, "moe_mxfp4_decode")
     return x
@@ -522,8 +536,8 @@ def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tenso
     A[g].  Rows that belong to no group are left as they were."""
     what = "mx4_gemm"
     dev = _device(a_codes, what)
-    if dev != _current():
-        return _on(dev, mx4_gemm, a_codes, a_scales, b_codes, b_scales, offsets, out, out_dtype, status, stream)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, mx4_gemm, a_codes, a_scales, b_codes, b_scales, offsets, out, out_dtype, status)
     a_codes, a_scales = _mx4(a_codes, a_scales, what)
     b_codes, b_scales = _mx4(b_codes, b_scales, what)
     if b_codes.dim() != 2 or b_codes.shape[1] != a_codes.shape[-1] or b_codes.get_device() != dev:
@@ -540,6 +554,7 @@ def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tenso
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev):
         _bad("mx4_gemm: status is int32 on A's device")
     N, K = b_codes.shape[0], 2 * b_codes.shape[1]
+    _int32(max(G, M, N, K), what)
     dtype = out_dtype or (torch.float32 if out is None else out.dtype)
     if dtype not in DTYPES:
         _bad("mx4_gemm: output type")
@@ -548,8 +563,7 @@ def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tenso
     else:
         ld = _out_rows(out, N, M, dtype, dev, what)
     code = lib().moe_mx4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), G, M, b_codes.data_ptr(), b_scales.data_ptr(), N, K,
-                              _p(offsets), out.data_ptr(), ld, DTYPES[dtype], _p(status),
-                              _raw_stream(dev) if stream is None else stream.cuda_stream)
+                              _p(offsets), out.data_ptr(), ld, DTYPES[dtype], _p(status), _raw_stream(dev))
     if code:
         _check(code, "moe_mx4_gemm")
     return out

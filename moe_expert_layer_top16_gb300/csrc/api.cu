@@ -1474,6 +1474,13 @@ bool slots_ok(int32_t T, int32_t k) {
     return T >= 0 && k >= 1 && k <= 32 && static_cast<int64_t>(T) * k <= 0x7fffffff;
 }
 
+constexpr int kMaxColumns = 1 << 30;             // column numbers a chunk ahead stay inside 32 bits
+
+// Elements of a quantised matrix: their number fits 63 bits with room.
+bool blocks_ok(int64_t rows, int64_t K) {
+    return rows >= 0 && K > 0 && K % 32 == 0 && rows <= (int64_t(1) << 48) / K;
+}
+
 // MXFP4 codes [rows][K / 2] as bytes, boxes of 128 bytes (256 elements) x box_rows.
 bool map_fp4(CUtensorMap* m, const void* codes, int64_t rows, int64_t K, int box_rows) {
     EncodeTiledFn f = encode_fn();
@@ -1534,7 +1541,7 @@ moe_status moe_permute(const void* x, int64_t x_stride, int64_t row_bytes, int32
 moe_status moe_unpermute(const void* rows, int64_t ld_rows, int32_t dtype, int64_t n_rows, const int32_t* slot_pos,
                          const float* w, int32_t T, int32_t k, int32_t D, void* y, int64_t ld_y, int32_t y_dtype,
                          void* stream) {
-    if (!slots_ok(T, k) || n_rows < 0 || D < 1 || !known_dtype(dtype) || !known_dtype(y_dtype))
+    if (!slots_ok(T, k) || n_rows < 0 || D < 1 || D > kMaxColumns || !known_dtype(dtype) || !known_dtype(y_dtype))
         return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
     if ((n_rows > 0 && !matrix_ok(rows, ld_rows, dtype, D)) || !matrix_ok(y, ld_y, y_dtype, D) || !slot_pos ||
@@ -1547,7 +1554,7 @@ moe_status moe_unpermute(const void* rows, int64_t ld_rows, int32_t dtype, int64
 moe_status moe_unpermute_backward(const void* dy, int64_t ld_dy, int32_t dy_dtype, const void* rows, int64_t ld_rows,
                                   int32_t dtype, int64_t n_rows, const int32_t* slot_pos, const float* w, int32_t T,
                                   int32_t k, int32_t D, void* d_rows, int64_t ld_d_rows, float* d_w, void* stream) {
-    if (!slots_ok(T, k) || n_rows < 0 || D < 1 || !known_dtype(dtype) || !known_dtype(dy_dtype))
+    if (!slots_ok(T, k) || n_rows < 0 || D < 1 || D > kMaxColumns || !known_dtype(dtype) || !known_dtype(dy_dtype))
         return MOE_ERR_INVALID_ARG;
     if (T == 0 || (!d_rows && !d_w)) return MOE_OK;
     if (!matrix_ok(dy, ld_dy, dy_dtype, D) || !slot_pos || !aligned(slot_pos, 4) || !aligned(w, 4) || !aligned(d_w, 4))
@@ -1676,7 +1683,7 @@ moe_status moe_block_norm_backward(const moe_block_norm_backward_args* p, void* 
 
 moe_status moe_mxfp4_quantize(const void* x, int64_t ld_x, int32_t dtype, int64_t rows, int64_t K, uint8_t* codes,
                               uint8_t* scales, void* stream) {
-    if (rows < 0 || K <= 0 || K % 32 || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    if (!blocks_ok(rows, K) || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!x || !aligned_elem(x, dtype) || ld_x < K || !codes || !scales || !aligned(codes, 4)) return MOE_ERR_INVALID_ARG;
     return cuda_status(launch_mxfp4_quantize(x, ld_x, dtype, rows, K, codes, scales, static_cast<cudaStream_t>(stream)));
@@ -1684,7 +1691,7 @@ moe_status moe_mxfp4_quantize(const void* x, int64_t ld_x, int32_t dtype, int64_
 
 moe_status moe_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* x, int64_t ld_x,
                             int32_t dtype, void* stream) {
-    if (rows < 0 || K <= 0 || K % 32 || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    if (!blocks_ok(rows, K) || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
     if (!x || !aligned_elem(x, dtype) || ld_x < K || !codes || !scales || !aligned(codes, 4)) return MOE_ERR_INVALID_ARG;
     return cuda_status(launch_mxfp4_decode(codes, scales, rows, K, x, ld_x, dtype, static_cast<cudaStream_t>(stream)));
@@ -1693,7 +1700,7 @@ moe_status moe_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int64_t
 moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t G, int32_t M, const uint8_t* b_codes,
                         const uint8_t* b_scales, int32_t N, int32_t K, const int32_t* offsets, void* out,
                         int64_t ld_out, int32_t out_dtype, int32_t* dev_status, void* stream) {
-    if (G < 1 || G > 1024 || M < 1 || N < 0 || K < 128 || K % 128 || static_cast<int64_t>(G) * M > 0x7fffffff ||
+    if (G < 1 || G > 1024 || M < 1 || N < 0 || K < 128 || K % 128 || static_cast<int64_t>(G) * M > 0x7fffff00 ||
         !known_dtype(out_dtype) || (!offsets && G != 1))
         return MOE_ERR_INVALID_ARG;
     if (N == 0) return MOE_OK;

@@ -260,3 +260,78 @@ def test_wide_batch_of_rows():
     h, u = moe.block_norm(x, x)
     keep = [0, 65535, 65536, T - 1]
     assert torch.equal(h[keep], moe.block_norm(x[keep], x[keep])[0])
+
+
+def test_memory_of_the_streams_argument():
+    """Copies and workspaces of a call belong to the stream it runs on: the current stream may hand out and overwrite
+    whatever was allocated and freed there while the other stream has not begun."""
+    T, k, E, D = 3000, 4, 40, 256
+    g = torch.Generator(device=DEV).manual_seed(3)
+    idx = torch.randint(0, E, (k, T), generator=g, device=DEV, dtype=torch.int32).t()            # strided: copied first
+    x = torch.randn(D, T, generator=g, device=DEV).t()
+    du, y = torch.randn(T, D, generator=g, device=DEV), torch.randn(D, T, generator=g, device=DEV).t()
+    w = torch.randn(D, generator=g, device=DEV)
+
+    def calls(**kw):
+        offsets, order, pos = moe.sort_by_expert(idx, E, **kw)
+        b = moe.block_norm_backward(None, du, x, y, w_post=w, w_pre=w, **kw)
+        return dict(offsets=offsets, order=order, pos=pos, rows=moe.permute(x, pos, **kw), q=moe.mxfp4_quantize(x, **kw)[0],
+                    u=moe.block_norm(x, y, w_pre=w, **kw)[1], **{n: t for n, t in b.items() if t is not None})
+    ref = calls()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                      # about ten milliseconds
+        got = calls(stream=side)
+        junk = [torch.full((n,), -1, dtype=torch.int32, device=DEV) for n in (T * k, T * k, T * D, T * D, T * D, 2 * D * T, 64 * E) * 4]
+        torch.cuda.synchronize()
+        assert same(ref, got)
+        del junk
+
+
+def test_stream_of_another_device_kind_is_refused():
+    x = torch.zeros(4, 64, device=DEV)
+    for stream in (torch.cuda.current_stream().cuda_stream, torch.cuda.Event()):
+        with pytest.raises(moe.MoeError) as e:
+            moe.block_norm(x, stream=stream)
+        assert e.value.code == moe.MOE_ERR_INVALID_ARG
+
+
+def test_more_slots_than_32_bits_are_refused():
+    idx = torch.zeros(1, 1, dtype=torch.int32, device=DEV).expand(2 ** 31, 1)
+    with pytest.raises(moe.MoeError) as e:
+        moe.sort_by_expert(idx, 4)
+    assert e.value.code == moe.MOE_ERR_INVALID_ARG
+
+
+def test_rows_behind_four_gigabytes():
+    """Row offsets past 32 bits, in elements: a few tokens in the last rows of a tall matrix."""
+    D, n = 8192, 2 ** 31 // 8192 + 40
+    rows = torch.zeros(n, D, dtype=BF16, device=DEV)
+    x = torch.randn(5, D, device=DEV).to(BF16)
+    pos = torch.tensor([[n - 1, 0], [n - 2, -1], [n - 30, 3], [n - 31, n], [2, n - 9]], dtype=torch.int32, device=DEV)
+    moe.permute(x, pos, out=rows)
+    keep = pos.clamp(-1, n)
+    for t in range(5):
+        for p in keep[t].tolist():
+            if 0 <= p < n:
+                assert torch.equal(rows[p], x[t])
+    w = torch.rand(5, 2, device=DEV)
+    y = moe.unpermute(rows, pos, w, out_dtype=F32)
+    ok = ((pos >= 0) & (pos < n)).float()
+    want = x.double() * (w * ok).double().sum(1, keepdim=True)
+    assert ((y.double() - want).abs() <= 3 * 2.0 ** -24 * x.double().abs() * (w * ok).double().sum(1, keepdim=True)).all()
+    d_rows, d_w = moe.unpermute_backward(x, rows, pos, w, out=torch.zeros_like(rows))
+    for t in range(5):
+        for j, p in enumerate(pos[t].tolist()):
+            if 0 <= p < n:
+                assert torch.equal(d_rows[p], (x[t].float() * w[t, j]).to(BF16))
+    del d_rows
+    ref = (x.double() ** 2).sum(1, keepdim=True) * ok.double()
+    assert ((d_w.double() - ref).abs() <= ref * (D / 32 + 8) * 2.0 ** -24).all()
+    # the norms' first and last rows
+    tall = rows.view(n, D)
+    tall[-1], tall[0] = x[0], x[1]
+    h, u = moe.block_norm(tall)
+    assert torch.equal(u[[0, -1]], moe.block_norm(tall[[0, -1]])[1])

@@ -153,3 +153,26 @@ def test_binding_refuses_what_it_can_see():
         block._mx4(c, s[:, :1], "x")
     with pytest.raises(moe.MoeError):
         block._out_rows(torch.zeros(1, 8).expand(4, 8), 4, 8, torch.float32, d, "x")
+
+
+def test_sizes_behind_the_last(L):
+    """Sizes whose index arithmetic would leave its integers."""
+    P16 = C.c_void_p(4096)
+    assert L.moe_unpermute(P, 2 ** 31, 0, 8, P, P, 4, 2, 2 ** 30 + 1, P, 2 ** 31, 0, None) == BAD
+    assert L.moe_unpermute_backward(P, 2 ** 31, 0, P, 2 ** 31, 0, 8, P, P, 4, 2, 2 ** 30 + 1, P, 2 ** 31, P, None) == BAD
+    for rows, K in ((2 ** 44, 32), (2 ** 62, 64), (2 ** 20, 2 ** 60)):
+        assert L.moe_mxfp4_quantize(P, K, 0, rows, K, P, P, None) == BAD
+        assert L.moe_mxfp4_decode(P, P, rows, K, P, K, 0, None) == BAD
+    assert L.moe_mx4_gemm(P16, P16, 1, 2 ** 31 - 255, P16, P16, 16, 128, None, P16, 2 ** 31, 0, None, None) == BAD
+
+
+def test_stream_of_another_kind():
+    x = torch.zeros(4, 64)
+    for stream in (0, "s", None.__class__):
+        with pytest.raises(moe.MoeError) as e:
+            block._on(0, stream, moe.block_norm, x)
+        assert e.value.code == BAD
+    for n in (2 ** 31, 2 ** 40):
+        with pytest.raises(moe.MoeError):
+            block._int32(n, "x")
+    block._int32(2 ** 31 - 1, "x")
