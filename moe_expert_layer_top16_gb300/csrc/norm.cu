@@ -164,15 +164,27 @@ __device__ __forceinline__ void fetch(uint8_t* slot, int pitch, const uint8_t* s
     if (W == 8 && dt == ELEM_F32) cp_async16(dst + pitch, src + 16);
 }
 
+// A window's words as they were copied (b: of eight fp32 only).
+struct Words {
+    uint4 a, b;
+};
+template <int W>
+__device__ __forceinline__ Words words(const uint8_t* slot, int pitch, int dt) {
+    Words w;
+    w.a = *reinterpret_cast<const uint4*>(slot);
+    if (W == 8 && dt == ELEM_F32) w.b = *reinterpret_cast<const uint4*>(slot + pitch);
+    return w;
+}
+
 // The window's values, zero outside the row.
 template <bool EDGE, int W>
-__device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, int c, int D, Pair (&v)[W / 2]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(slot);
+__device__ __forceinline__ void unpack(const Words& w, int dt, int c, int D, Pair (&v)[W / 2]) {
+    const uint4& a = w.a;
     if (W == 4 || dt == ELEM_F32) {
         v[0] = pair(__uint_as_float(a.x), __uint_as_float(a.y));
         v[1] = pair(__uint_as_float(a.z), __uint_as_float(a.w));
         if constexpr (W == 8) {
-            const uint4 b = *reinterpret_cast<const uint4*>(slot + pitch);
+            const uint4& b = w.b;
             v[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y));
             v[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
         }
@@ -190,6 +202,11 @@ __device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, i
             v[j] = pair(e >= 0 && e < D ? f.x : 0.0f, e + 1 >= 0 && e + 1 < D ? f.y : 0.0f);
         }
     }
+}
+
+template <bool EDGE, int W>
+__device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, int c, int D, Pair (&v)[W / 2]) {
+    unpack<EDGE, W>(words<W>(slot, pitch, dt), dt, c, D, v);
 }
 
 // Store a window, and (BACK) leave in v the values as stored.
@@ -325,7 +342,10 @@ __device__ __forceinline__ void group_sums(float (&v)[N], const Rows& g, float (
 // Four sums at once: the lanes halve what they carry with each exchange (two
 // values after the first, one after the second), so that six exchanges do what
 // twenty would; lane 8 k then holds value k of the warp.
-__device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float (*red)[4][kNormMaxWarps], int& buf) {
+// `between` is done before the barrier: what the threads that arrive first do
+// while they would wait.
+template <typename F>
+__device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float (*red)[4][kNormMaxWarps], int& buf, F between) {
     const int lane = threadIdx.x & 31;
     const bool up = lane & 16, odd = lane & 8;
     // lanes 0-15 keep values 0 and 1, lanes 16-31 values 2 and 3
@@ -337,6 +357,7 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
     if (g.tpr > 32) {
         const int warp = threadIdx.x >> 5, warps = g.tpr >> 5, warp0 = g.group * warps;
         if ((lane & 7) == 0) red[buf][lane >> 3][warp] = s;
+        between();
         asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
         s = 0.0f;
 #pragma unroll
@@ -345,6 +366,8 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         buf ^= 1;
+    } else {
+        between();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, s, 8 * i);
@@ -537,8 +560,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         cp_async_commit();
         if (++ahead == stages) ahead = 0;
     };
-    // one stage: the group has one row
-    for (int k = 0; k < max(stages - 1, 1); ++k) issue(g.first + k * g.step);
+    for (int k = 0; k < stages; ++k) issue(g.first + k * g.step);
     if (g.group == 0) keep_weights<NV, W>(weights, wpitch, a, c0, step);
     Pair s_pre[NV][W / 2], s_post[NV][W / 2];
 #pragma unroll
@@ -585,19 +607,19 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         q = rsqrtf(v[2] * inv_d + a.eps);
     };
     if (g.first < T) {
-        cp_async_wait(stages > 1 ? stages - 2 : 0);
+        cp_async_wait(stages - 1);
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         squares(mine, v);
-        group_sums4(v, g, red, buf);
+        group_sums4(v, g, red, buf, [] {});
         norms(v);
     }
     for (int t = g.first; t < T; t += g.step) {
-        if (stages > 1) issue(t + (stages - 1) * g.step);
         const uint8_t* s = mine + stage * stage_pitch;
         if (++stage == stages) stage = 0;
         const float gt = (post && a.gate_kind == NORM_GATE_TOKEN) ? token_gate(a.gate, t, a.dt_w) : 1.0f;
         const Pair rr = pair(r, r), rm = pair(-r * m, -r * m), qg = pair(q * gt, q * gt);
         Pair total[NV][W / 2];
+        Words kept_y[NV];
         Pair py = 0;                                   // sum total w_post (channel gate) y
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -629,7 +651,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             }
             if (post) {
                 Pair y[W / 2], w[W / 2];
-                unpack<EDGE, W>(p + off_y * pitch, pitch, ty, c, D, y);
+                kept_y[i] = words<W>(p + off_y * pitch, pitch, ty);
+                unpack<EDGE, W>(kept_y[i], ty, c, D, y);
                 kept<W>(weights + i * (W / 2) * wpitch, wpitch, w);
 #pragma unroll
                 for (int j = 0; j < W / 2; ++j) {
@@ -644,10 +667,11 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         const bool more = t + g.step < T;
         if (more) {
             // the next row has landed: later ones may be in flight
-            cp_async_wait(stages > 1 ? stages - 2 : 0);
+            cp_async_wait(stages - 2);
             squares(mine + stage * stage_pitch, v);
         }
-        group_sums4(v, g, red, buf);
+        // this thread is through with row t's slots
+        group_sums4(v, g, red, buf, [&] { issue(t + stages * g.step); });
         if (post) {
             if (a.d_gate_token && g.lane_in_group == 0) a.d_gate_token[t] = v[3] * q;
             if (want_dy) {
@@ -658,7 +682,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
                     const int c = c0 + i * step;
                     if (c >= D) break;
                     Pair y[W / 2];
-                    unpack<EDGE, W>(s + (i * slots + off_y) * pitch, pitch, ty, c, D, y);
+                    unpack<EDGE, W>(kept_y[i], ty, c, D, y);
 #pragma unroll
                     for (int j = 0; j < W / 2; ++j) y[j] = mul2(qg, fma2(y[j], nn, total[i][j]));
                     put<EDGE, W, false>(oy + i * step * elem_bytes(ty), c, D, ty, y);
