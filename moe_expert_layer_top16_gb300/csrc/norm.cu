@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "ptx.cuh"
 #include "vec.cuh"
 
 namespace moe {
@@ -40,22 +41,31 @@ constexpr int kNormMaxStages = 8;
 // columns in each.
 //
 // A row is owned by a group of tpr threads; a block holds blockDim / tpr
-// groups, which share its weights.
+// groups, which share its weights.  A row too wide for one block is split over
+// the blocks of a cluster (each one group), a part of the columns each.
+constexpr int kNormMaxSplit = 4;
 struct Rows {
     int tpr, lane_in_group, group, groups;
+    int unit, units;            // this block among the blocks (its cluster among the clusters)
+    int part, parts;            // this block in its cluster
     int first, step;            // rows first, first + step, ...
     int shift;                  // elements of the first window that belong to the row before
 };
 
+template <bool SPLIT>
 __device__ __forceinline__ Rows rows_of(int tpr, int64_t ld, int window) {
     Rows r;
     r.tpr = tpr;
+    r.part = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+    r.parts = SPLIT ? static_cast<int>(cluster_ctas()) : 1;
+    r.unit = SPLIT ? static_cast<int>(blockIdx.x) / r.parts : static_cast<int>(blockIdx.x);
+    r.units = SPLIT ? static_cast<int>(gridDim.x) / r.parts : static_cast<int>(gridDim.x);
     r.groups = blockDim.x / tpr;
     r.group = threadIdx.x / tpr;
     r.lane_in_group = threadIdx.x - r.group * tpr;
-    r.first = blockIdx.x + gridDim.x * r.group;
-    r.step = gridDim.x * r.groups;
-    r.shift = static_cast<int>((blockIdx.x * ld) & (window - 1));
+    r.first = r.unit + r.units * r.group;
+    r.step = r.units * r.groups;
+    r.shift = static_cast<int>((r.unit * ld) & (window - 1));
     return r;
 }
 
@@ -76,11 +86,15 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Wait until at most n of this thread's copy groups are in flight.
+// Wait until at most n of this thread's copy groups are in flight (one: the
+// widest rows, tested first).
 __device__ __forceinline__ void cp_async_wait(int n) {
+    if (n == 1) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        return;
+    }
     switch (n) {
         case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
         case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
         case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
         case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
@@ -212,7 +226,7 @@ __device__ __forceinline__ void unpack(const uint8_t* slot, int pitch, int dt, i
 // Store a window, and (BACK) leave in v the values as stored.
 template <bool EDGE, int W, bool BACK>
 __device__ __forceinline__ void put(uint8_t* dst, int c, int D, int dt, Pair (&v)[W / 2]) {
-    const bool all = whole<EDGE, W>(c, D);
+    const bool all = EDGE ? whole<EDGE, W>(c, D) : c < D;
     if (dt == ELEM_F32) {
         if (all) {
 #pragma unroll
@@ -251,6 +265,21 @@ __device__ __forceinline__ void put(uint8_t* dst, int c, int D, int dt, Pair (&v
             if (e >= 0 && e < D) reinterpret_cast<uint16_t*>(dst)[2 * j] = static_cast<uint16_t>(w[j] & 0xFFFFu);
             if (e + 1 >= 0 && e + 1 < D) reinterpret_cast<uint16_t*>(dst)[2 * j + 1] = static_cast<uint16_t>(w[j] >> 16);
         }
+    }
+}
+
+// A thread behind the row's last window computes like the others, on zeros,
+// and stores nothing (a test and two branches less in every step of a row):
+// EDGE instances mask what it reads, the others clear its slots once.
+template <int NV, bool EDGE>
+__device__ __forceinline__ void clear_behind(uint8_t* mine, int pitch, int stages, int slots, int c0, int step, int D) {
+    if constexpr (!EDGE) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (c0 + i * step >= D)
+                for (int k = 0; k < stages; ++k)
+                    for (int j = 0; j < slots; ++j)
+                        *reinterpret_cast<uint4*>(mine + ((k * NV + i) * slots + j) * pitch) = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -343,9 +372,11 @@ __device__ __forceinline__ void group_sums(float (&v)[N], const Rows& g, float (
 // values after the first, one after the second), so that six exchanges do what
 // twenty would; lane 8 k then holds value k of the warp.
 // `between` is done before the barrier: what the threads that arrive first do
-// while they would wait.
-template <typename F>
-__device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float (*red)[4][kNormMaxWarps], int& buf, F between) {
+// while they would wait.  Split rows: each warp's sums go to every block of the
+// cluster, whose barrier takes the place of the group's (a block writes a
+// buffer again one barrier after the others have read it).
+template <bool SPLIT, int WARPS, typename F>
+__device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float (*red)[4][WARPS], int& buf, F between) {
     const int lane = threadIdx.x & 31;
     const bool up = lane & 16, odd = lane & 8;
     // lanes 0-15 keep values 0 and 1, lanes 16-31 values 2 and 3
@@ -354,14 +385,25 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
     float s = __shfl_xor_sync(0xffffffffu, odd ? a : b, 8) + (odd ? b : a);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (g.tpr > 32) {
-        const int warp = threadIdx.x >> 5, warps = g.tpr >> 5, warp0 = g.group * warps;
-        if ((lane & 7) == 0) red[buf][lane >> 3][warp] = s;
-        between();
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
+    if (SPLIT || g.tpr > 32) {
+        const int warp = threadIdx.x >> 5, warps = (g.tpr >> 5) * g.parts, warp0 = g.group * warps;
+        if constexpr (SPLIT) {
+            if ((lane & 7) == 0) {
+                const uint32_t at = smem_u32(&red[buf][lane >> 3][g.part * (g.tpr >> 5) + warp]);
+                for (int r = 0; r < g.parts; ++r)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(at, r)), "f"(s) : "memory");
+            }
+            between();
+            __syncwarp();
+            cluster_sync_all();
+        } else {
+            if ((lane & 7) == 0) red[buf][lane >> 3][warp] = s;
+            between();
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
+        }
         s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kNormMaxWarps; w += 8)
+        for (int w = 0; w < WARPS; w += 8)
             if (w + (lane & 7) < warps) s += red[buf][lane >> 3][warp0 + w + (lane & 7)];
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -405,7 +447,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
     const int dx = K::x >= 0 ? K::x : a.dt_x, dy = K::y >= 0 ? K::y : a.dt_y;
     const int du = KIND == NORM_BF16 || KIND == NORM_BF16_Y32 ? K::x : a.dt_u;
     const bool post = a.y != nullptr, pre = a.u != nullptr;
-    const Rows g = rows_of(tpr, a.ld_x, W);
+    const Rows g = rows_of<false>(tpr, a.ld_x, W);
     const int D = a.D, T = static_cast<int>(a.T);
     const int pitch = blockDim.x * 16, wpitch = tpr * 16;
     const int yw = window_slots(post, dy, W), slots = yw + window_slots(true, dx, W);
@@ -435,6 +477,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
         cp_async_commit();
         if (++ahead == stages) ahead = 0;
     };
+    clear_behind<NV, EDGE>(mine, pitch, stages, slots, c0, step, D);
     for (int k = 0; k + 1 < stages; ++k) issue(g.first + k * g.step);
     if (g.group == 0) keep_weights<NV, W>(weights, wpitch, a, c0, step);
     __syncthreads();
@@ -453,7 +496,6 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
-                if (c >= D) break;
                 unpack<EDGE, W>(s + i * slots * pitch, pitch, dy, c, D, v[i]);
 #pragma unroll
                 for (int j = 0; j < W / 2; ++j) acc = fma2(v[i][j], v[i][j], acc);
@@ -468,7 +510,6 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
-            if (c >= D) break;
             const uint8_t* p = s + (i * slots + yw) * pitch;
             if (post) {
                 Pair x[W / 2], w[W / 2];
@@ -492,7 +533,6 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = c0 + i * step;
-                if (c >= D) break;
                 Pair w[W / 2];
                 kept<W>(weights + (i * (W / 2) + W / 4) * wpitch, wpitch, w);
 #pragma unroll
@@ -510,25 +550,27 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 // The weights wait in shared memory, which leaves registers for 28 warps.  The
 // sums over row t + 1 that its norms need are taken together with the one over
 // row t that its dy needs: one barrier a row, and the work of both before it.
-template <int NV, int MAXT, bool EDGE, int KIND>
+template <int NV, int MAXT, bool EDGE, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages,
                                                                    const Steps st) {
     using K = Kind<KIND>;
     constexpr int W = K::window;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float red[2][4][kNormMaxWarps];
+    constexpr int kWarps = MAXT / 32 * (SPLIT ? kNormMaxSplit : 1);
+    __shared__ float red[2][4][(kWarps + 7) / 8 * 8];
     int buf = 0;
     const int tx = K::x >= 0 ? K::x : a.dt_x, ty = K::y >= 0 ? K::y : a.dt_y, tu = K::x >= 0 ? K::x : a.dt_u;
     const bool post = K::full || a.y != nullptr, pre = K::full || a.du != nullptr, has_dh = K::full || a.dh != nullptr;
     const bool want_dx = K::full || a.dx != nullptr, want_dy = K::full || a.dy != nullptr;
-    const Rows g = rows_of(tpr, pre ? a.ld_h : a.ld_dh, W);
+    const Rows g = rows_of<SPLIT>(tpr, pre ? a.ld_h : a.ld_dh, W);
+    if constexpr (SPLIT) cluster_sync_all();           // the others' shared memory is there
     const int D = a.D, T = static_cast<int>(a.T);
     const int pitch = blockDim.x * 16, wpitch = tpr * 16;
     const int off_u = window_slots(pre, tx, W), off_d = off_u + window_slots(pre, tu, W),
               off_y = off_d + window_slots(has_dh, tx, W), slots = off_y + window_slots(post, ty, W);     // a window's
     uint8_t* weights = ring + g.lane_in_group * 16;
     uint8_t* mine = ring + NV * (W / 2) * wpitch + threadIdx.x * 16;        // [stages][NV][slots]
-    const int c0 = g.lane_in_group * W - g.shift, step = tpr * W;
+    const int step = tpr * W, c0 = g.lane_in_group * W - g.shift + g.part * NV * step;
     const int stage_pitch = NV * slots * pitch;
     uint8_t *rh = run(a.h, a.ld_h, tx, g, c0), *ru = run(a.du, a.ld_du, tu, g, c0);
     uint8_t *rd = run(a.dh, a.ld_dh, tx, g, c0), *ry = run(a.y, a.ld_y, ty, g, c0);
@@ -610,7 +652,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         cp_async_wait(stages - 1);
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         squares(mine, v);
-        group_sums4(v, g, red, buf, [] {});
+        group_sums4<SPLIT>(v, g, red, buf, [] {});
         norms(v);
     }
     for (int t = g.first; t < T; t += g.step) {
@@ -671,9 +713,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             squares(mine + stage * stage_pitch, v);
         }
         // this thread is through with row t's slots
-        group_sums4(v, g, red, buf, [&] { issue(t + stages * g.step); });
+        group_sums4<SPLIT>(v, g, red, buf, [&] { issue(t + stages * g.step); });
         if (post) {
-            if (a.d_gate_token && g.lane_in_group == 0) a.d_gate_token[t] = v[3] * q;
+            if (a.d_gate_token && g.lane_in_group == 0 && g.part == 0) a.d_gate_token[t] = v[3] * q;
             if (want_dy) {
                 const float n = -q * q * v[3] * inv_d;     // -mean(p y^) / (g rms(y))
                 const Pair nn = pair(n, n);
@@ -693,7 +735,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         norms(v);
     }
     if (!a.part) return;
-    float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * D;
+    float* out = a.part + static_cast<int64_t>(g.unit) * 2 * D;
     // the groups in turn add their columns to the block's, in the ring's
     // memory (one group: straight to the part)
     float* acc = g.groups == 1 ? out : reinterpret_cast<float*>(ring);
@@ -933,33 +975,37 @@ struct Alike {
 // nv windows a thread; the ring takes the shared memory that is left, up to
 // eight rows a group.
 struct Shape {
-    int nv, tpr, threads, stages, grid;
+    int nv, tpr, threads, stages, grid, split;
     bool edge;                  // some windows lie only partly in their row
     size_t smem;
 };
 constexpr int kNormSmem = kSmemLimit - 2048;     // without the sums' static part
 
-// slots: of a window in the ring; two_from: rows of more windows than this
-// have two a thread; group_threads: threads of a block's groups together at
-// most; regs: of a thread; deep: rows of a group in the ring, where there is
-// room; most: blocks.
-bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int group_threads, int regs, int deep, int sms,
-              int most, Shape* s) {
-    if (!al.ok) return false;
+// What a kernel allows: rows of more than two_from windows have two a thread;
+// group_threads: threads of a block's groups together at most, row_threads of
+// one; regs: of a thread; deep: rows of a group in the ring, where there is
+// room; split: blocks that share a row at most.
+struct Rule {
+    int two_from, group_threads, row_threads, regs, deep, split;
+};
+
+// slots: of a window in the ring; most: blocks (clusters).
+bool shape_of(int64_t T, int D, const Alike& al, int slots, const Rule& rule, int sms, int64_t most, int split, Shape* s) {
     const int W = al.window;
-    const int windows = (D + (al.odd ? W - 1 : 0) + W - 1) / W;
-    if (windows > 2 * 1024) return false;
+    const int row = (D + (al.odd ? W - 1 : 0) + W - 1) / W, windows = (row + split - 1) / split;
+    if (windows > 2 * rule.row_threads) return false;
+    s->split = split;
     s->edge = al.odd || D % W;
-    s->nv = windows > two_from ? 2 : 1;
+    s->nv = split > 1 || windows > rule.two_from ? 2 : 1;
     s->tpr = ((windows + s->nv - 1) / s->nv + 31) / 32 * 32;
     const int stage = s->nv * slots * 16, fixed = s->nv * (W / 2) * s->tpr * 16;      // bytes a thread; a block
-    int groups = std::max(1, std::min(group_threads / s->tpr, 8));
-    while (groups > 1 && (static_cast<int64_t>(groups) * sms > T || deep * groups * s->tpr * stage + fixed > kNormSmem)) --groups;
+    int groups = split > 1 ? 1 : std::max(1, std::min(rule.group_threads / s->tpr, 8));
+    while (groups > 1 && (static_cast<int64_t>(groups) * sms > T || rule.deep * groups * s->tpr * stage + fixed > kNormSmem)) --groups;
     s->threads = s->tpr * groups;
-    int per_sm = std::max(1, std::min(65536 / (regs * s->threads), 2048 / s->threads));
+    int per_sm = std::max(1, std::min(65536 / (rule.regs * s->threads), 2048 / s->threads));
     // at least `deep` rows in the ring of a group
-    while (per_sm > 1 && per_sm * (deep * stage * s->threads + fixed + 1024) > kNormSmem) --per_sm;
-    int64_t grid = std::min<int64_t>((T + groups - 1) / groups, static_cast<int64_t>(sms) * per_sm);
+    while (per_sm > 1 && per_sm * (rule.deep * stage * s->threads + fixed + 1024) > kNormSmem) --per_sm;
+    int64_t grid = std::min<int64_t>((T + groups - 1) / groups, std::max(1, sms * per_sm / split));
     if (grid > most) grid = most;
     // a row's place in its windows has to be the same in all rows of a block
     if (al.odd && (groups > 1 || grid < T)) {
@@ -967,14 +1013,22 @@ bool shape_of(int64_t T, int D, const Alike& al, int slots, int two_from, int gr
         grid = grid / 8 * 8;
     }
     s->grid = static_cast<int>(grid);
-    const int per_block = std::min<int>(per_sm, static_cast<int>((grid + sms - 1) / sms));
+    const int per_block = std::min<int>(per_sm, static_cast<int>((grid * split + sms - 1) / sms));
     const int64_t rows = (T + grid * groups - 1) / (grid * groups);                        // of a group at most
     int st = (kNormSmem / per_block - 1024 - fixed) / (stage * s->threads);
     st = std::max(1, std::min<int>(st, kNormMaxStages));
     s->stages = static_cast<int>(std::min<int64_t>(st, rows));
-    if (deep > 2 && s->stages < 2 && rows > 1) return false;         // two rows are in use at once
+    if (rule.deep > 2 && s->stages < 2 && rows > 1) return false;         // two rows are in use at once
     s->smem = static_cast<size_t>(s->stages) * stage * s->threads + fixed;
     return s->smem <= static_cast<size_t>(kNormSmem);
+}
+
+// The fewest blocks a row that its windows and the ring's rows fit in.
+bool shape_of(int64_t T, int D, const Alike& al, int slots, const Rule& rule, int sms, int64_t most, Shape* s) {
+    if (!al.ok) return false;
+    for (int split = 1; split <= rule.split; split *= 2)
+        if (shape_of(T, D, al, slots, rule, sms, most, split, s)) return true;
+    return false;
 }
 
 Steps steps_of(const NormArgs& a, int64_t rows) {
@@ -1003,6 +1057,9 @@ cudaError_t run_rows(void (*kern)(Args, int, int, Steps), const Args& a, const S
         if (err != cudaSuccess) return err;
     }
     const int64_t rows = static_cast<int64_t>(sh.grid) * (sh.threads / sh.tpr);
+    if (sh.split > 1)
+        return launch_ex_cluster(kern, dim3(sh.grid * sh.split), dim3(sh.threads), smem, s, false, sh.split, a, sh.tpr,
+                                 sh.stages, steps_of(a, rows));
     kern<<<sh.grid, sh.threads, smem, s>>>(a, sh.tpr, sh.stages, steps_of(a, rows));
     return cudaGetLastError();
 }
@@ -1012,22 +1069,19 @@ cudaError_t forward_as(const NormArgs& a, const Shape& sh, cudaStream_t s) {
     if (sh.nv == 2) return run_rows(block_norm_kernel<2, EDGE, KIND>, a, sh, sh.smem, s);
     return run_rows(block_norm_kernel<1, EDGE, KIND>, a, sh, sh.smem, s);
 }
-// The column sums and a row's gradient of one window of eight (or two of four)
-// take 72 registers: 896 threads.  A block of 449 to 512 has an SM to itself
-// either way and takes 128; up to 1,024 threads a row spill a few, wider rows
-// more.
-template <int NV, bool EDGE, int KIND>
-cudaError_t backward_nv(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
-    if (sh.threads > 896) return run_rows(block_norm_backward_kernel<NV, 1024, EDGE, KIND>, a, sh, smem, s);
-    if (sh.threads > 448 && sh.threads <= 512)
-        return run_rows(block_norm_backward_kernel<NV, 512, EDGE, KIND>, a, sh, smem, s);
-    return run_rows(block_norm_backward_kernel<NV, 896, EDGE, KIND>, a, sh, smem, s);
-}
+// Two windows a thread in one block of up to 512 threads a SM, 128 registers
+// each: the sums' exchange, the copies' and the loop's instructions are paid
+// for 16 elements at a time.  4,096 x 7,168 bf16 70 us, one window a thread in
+// 896 threads of 72 registers 84; 4,096 x 3,584 fp32 53 and 86.  Narrow rows
+// have one window a thread; where that takes 72 registers, 896 threads.
+template <bool EDGE, int KIND>
+constexpr bool lean = !EDGE && (KIND == NORM_BF16 || KIND == NORM_F32);
 template <bool EDGE, int KIND>
 cudaError_t backward_as(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
-    if (sh.nv == 1) return backward_nv<1, EDGE, KIND>(a, sh, smem, s);
-    if constexpr (KIND == NORM_F32) return backward_nv<2, EDGE, KIND>(a, sh, smem, s);
-    return run_rows(block_norm_backward_kernel<2, 1024, true, NORM_RUN>, a, sh, smem, s);
+    constexpr int kNarrow = lean<EDGE, KIND> ? 896 : 512;
+    if (sh.split > 1) return run_rows(block_norm_backward_kernel<2, 512, EDGE, KIND, true>, a, sh, smem, s);
+    if (sh.nv == 2) return run_rows(block_norm_backward_kernel<2, 512, EDGE, KIND, false>, a, sh, smem, s);
+    return run_rows(block_norm_backward_kernel<1, kNarrow, EDGE, KIND, false>, a, sh, smem, s);
 }
 
 // Windows of four for rows of fp32, as long as two a thread cover the row.  The
@@ -1067,7 +1121,7 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     const int slots = window_slots(true, a.dt_x, W) + window_slots(a.y, a.dt_y, W);
     // 896 threads in two groups of 448 for 7,168 elements: the one group's
     // sums overlap the other's loads and stores
-    if (shape_of(a.T, a.D, al, slots, 256, 1024, 64, 2, sms, 1 << 30, &sh)) {
+    if (shape_of(a.T, a.D, al, slots, Rule{256, 1024, 1024, 64, 2, 1}, sms, 1 << 30, &sh)) {
         if (kind == NORM_BF16) return sh.edge ? forward_as<true, NORM_BF16>(a, sh, s) : forward_as<false, NORM_BF16>(a, sh, s);
         if (kind == NORM_F32) return sh.edge ? forward_as<true, NORM_F32>(a, sh, s) : forward_as<false, NORM_F32>(a, sh, s);
         if (kind == NORM_BF16_Y32 && !sh.edge) return forward_as<false, NORM_BF16_Y32>(a, sh, s);
@@ -1107,7 +1161,13 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     const int most = norm_parts(a.T, a.D);
     Shape sh;
     int parts;
-    if (shape_of(a.T, a.D, al, slots, W == 4 ? 256 : 1024, 896, 72, 3, sms, most, &sh)) {
+    // the widest row with one window a thread: 1,024 elements of bf16 (28 us for
+    // 8,192 rows, two windows 30; 2,048 elements 46 and 38), of fp32 too (32 and
+    // 32), 2,048 with y in fp32 (53 and 56)
+    const int two_from = kind == NORM_BF16 ? 128 : 256;
+    const bool lean_row = !al.odd && a.D % W == 0 && (kind == NORM_BF16 || kind == NORM_F32) && a.D <= two_from * W;
+    const Rule rule = {two_from, lean_row ? 896 : 512, 512, lean_row ? 72 : 128, 3, kNormMaxSplit};
+    if (shape_of(a.T, a.D, al, slots, rule, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
         if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.D));

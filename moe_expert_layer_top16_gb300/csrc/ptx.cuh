@@ -334,6 +334,11 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
 // scales and all of B's scales, at the same shared-memory and TMEM offsets.
 // The even CTA of the pair (rank 0) issues the MMAs for both.  Every tcgen05
 // instruction of a kernel that pairs CTAs names cta_group::2.
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

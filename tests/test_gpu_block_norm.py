@@ -228,3 +228,40 @@ def test_narrow_and_odd_rows(T, D):
         terms = s["dh"].double() * yh
         tol = terms.abs().sum(0) * (2 * c + (T + 24) * 2.0 ** -24)
         assert ((got["dw_post"].double() - terms.sum(0)).abs() <= tol).all()
+
+
+# rows that several blocks share, many rows a block, first and last windows that are partial
+WIDE = [(300, 7168, F32, F32, F32, "channel"), (41, 8200, F32, F32, F32, "token"), (600, 4101, F32, F32, F32, "channel"),
+        (333, 8193, BF16, BF16, F32, "channel"), (190, 12288, BF16, BF16, BF16, "token"), (170, 7167, BF16, F32, F32, "channel"),
+        (100, 16383, F32, F32, F32, "channel"), (640, 16384, F32, F32, F32, None), (90, 16384, F16, F32, F32, "token"),
+        (1300, 2048, BF16, F32, F32, "channel"), (1300, 2056, BF16, BF16, F32, "token"), (1300, 1028, F32, F32, F32, "channel")]
+
+
+@pytest.mark.parametrize("T,D,tx,ty,tw,gate", WIDE)
+@pytest.mark.parametrize("given", ["both", "dh", "du", "pre"])
+def test_backward_wide(T, D, tx, ty, tw, gate, given):
+    test_backward(T, D, tx, ty, tw, gate, given)
+
+
+@pytest.mark.parametrize("T,D,tx,ty,tw,gate", [WIDE[0], WIDE[2], WIDE[6]])
+def test_backward_wide_again_and_in_a_graph(T, D, tx, ty, tw, gate):
+    """Split rows: the same bits in every run, eager and captured, two replays at once on two streams."""
+    s = make(T, D, tx, ty, tw, gate, seed=3)
+    call = lambda: moe.block_norm_backward(s["dh"], s["du"].to(tx), s["x"], s["y"], w_post=s["w_post"], w_pre=s["w_pre"],  # noqa: E731
+                                           gate=s["gate"], gate_per=gate, res_scale=0.75, eps=EPS)
+    ref = call()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call()
+        graphs.append((g, out))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for st, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, out in graphs:
+        for n, t in ref.items():
+            assert torch.equal(t, out[n]), n
