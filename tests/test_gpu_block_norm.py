@@ -234,13 +234,22 @@ def test_narrow_and_odd_rows(T, D):
 WIDE = [(300, 7168, F32, F32, F32, "channel"), (41, 8200, F32, F32, F32, "token"), (600, 4101, F32, F32, F32, "channel"),
         (333, 8193, BF16, BF16, F32, "channel"), (190, 12288, BF16, BF16, BF16, "token"), (170, 7167, BF16, F32, F32, "channel"),
         (100, 16383, F32, F32, F32, "channel"), (640, 16384, F32, F32, F32, None), (90, 16384, F16, F32, F32, "token"),
-        (1300, 2048, BF16, F32, F32, "channel"), (1300, 2056, BF16, BF16, F32, "token"), (1300, 1028, F32, F32, F32, "channel")]
+        (1300, 2048, BF16, F32, F32, "channel"), (1300, 2056, BF16, BF16, F32, "token"), (1300, 1028, F32, F32, F32, "channel"),
+        (900, 1031, F16, F16, F32, "channel"), (700, 3583, BF16, F32, F32, "token"), (200, 7168, F16, F16, F16, "channel"),
+        (500, 1000, F16, F32, F16, "token"), (2500, 512, F16, F16, F32, None), (200, 8192, F32, F32, F32, "channel"),
+        (2500, 512, F32, F32, F32, "channel"), (2500, 1024, F32, F32, F32, "token"), (900, 5120, F32, F32, F32, "channel"),
+        (2500, 511, BF16, BF16, F32, "channel"), (2500, 96, F16, F32, F32, None)]
 
 
 @pytest.mark.parametrize("T,D,tx,ty,tw,gate", WIDE)
 @pytest.mark.parametrize("given", ["both", "dh", "du", "pre"])
 def test_backward_wide(T, D, tx, ty, tw, gate, given):
     test_backward(T, D, tx, ty, tw, gate, given)
+
+
+@pytest.mark.parametrize("T,D,tx,ty,tw,gate", WIDE)
+def test_forward_wide(T, D, tx, ty, tw, gate):
+    test_forward(T, D, tx, ty, tw, gate, None)
 
 
 @pytest.mark.parametrize("T,D,tx,ty,tw,gate", [WIDE[0], WIDE[2], WIDE[6]])
