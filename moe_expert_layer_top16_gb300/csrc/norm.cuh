@@ -325,9 +325,26 @@ __device__ __forceinline__ void kept(const uint8_t* slot, int pitch, Pair (&v)[W
 // few rows more than its rows.
 template <int W>
 __device__ __forceinline__ void load_columns(float (&v)[W], const void* w, int c, int D, int dt) {
+    const uint8_t* at = static_cast<const uint8_t*>(w) + static_cast<int64_t>(c) * elem_bytes(dt);
+    const bool words = c >= 0 && c + W <= D && reinterpret_cast<uintptr_t>(at) % (W * elem_bytes(dt) < 16 ? 8 : 16) == 0;
     if (!w) {
 #pragma unroll
         for (int j = 0; j < W; ++j) v[j] = 1.0f;
+    } else if (words && dt == ELEM_F32) {
+        float4 q[W / 4];
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) q[j] = __ldg(reinterpret_cast<const float4*>(at) + j);
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) v[4 * j] = q[j].x, v[4 * j + 1] = q[j].y, v[4 * j + 2] = q[j].z, v[4 * j + 3] = q[j].w;
+    } else if (words) {
+        uint2 q[W / 4];
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) q[j] = __ldg(reinterpret_cast<const uint2*>(at) + j);
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) {
+            const float2 lo = split(widen(q[j].x, dt)), hi = split(widen(q[j].y, dt));
+            v[4 * j] = lo.x, v[4 * j + 1] = lo.y, v[4 * j + 2] = hi.x, v[4 * j + 3] = hi.y;
+        }
     } else if (dt == ELEM_F32) {
         const float* p = static_cast<const float*>(w);
 #pragma unroll
