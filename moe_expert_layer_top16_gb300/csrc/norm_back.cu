@@ -246,20 +246,30 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
     for (int k = 0; k < g.groups; ++k) {
         if (g.group == k) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                const int c = c0 + i * step;
+                auto add = [&](const Pair (&sum)[W / 2], float* to) {
+                    if (c >= 0 && c + W <= D && reinterpret_cast<uintptr_t>(to + c) % 16 == 0) {
 #pragma unroll
-                for (int j = 0; j < W / 2; ++j) {
-                    const int c = c0 + i * step + 2 * j;
-                    const float2 f = split(s_pre[i][j]), e = split(s_post[i][j]);
-                    if (c >= 0 && c < D) {
-                        acc[c] = (k ? acc[c] : 0.0f) + f.x;
-                        acc[D + c] = (k ? acc[D + c] : 0.0f) + e.x;
+                        for (int j = 0; j < W / 4; ++j) {
+                            const float2 f = split(sum[2 * j]), e = split(sum[2 * j + 1]);
+                            float4* at = reinterpret_cast<float4*>(to + c) + j;
+                            const float4 o = k ? *at : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            *at = make_float4(o.x + f.x, o.y + f.y, o.z + e.x, o.w + e.y);
+                        }
+                        return;
                     }
-                    if (c + 1 >= 0 && c + 1 < D) {
-                        acc[c + 1] = (k ? acc[c + 1] : 0.0f) + f.y;
-                        acc[D + c + 1] = (k ? acc[D + c + 1] : 0.0f) + e.y;
+#pragma unroll
+                    for (int j = 0; j < W / 2; ++j) {
+                        const float2 f = split(sum[j]);
+                        const int e = c + 2 * j;
+                        if (e >= 0 && e < D) to[e] = (k ? to[e] : 0.0f) + f.x;
+                        if (e + 1 >= 0 && e + 1 < D) to[e + 1] = (k ? to[e + 1] : 0.0f) + f.y;
                     }
-                }
+                };
+                add(s_pre[i], acc);
+                add(s_post[i], acc + D);
+            }
         }
         __syncthreads();
     }
