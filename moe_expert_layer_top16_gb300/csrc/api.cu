@@ -1611,8 +1611,8 @@ moe_status moe_block_norm(const moe_block_norm_args* p, void* stream) {
 }
 
 size_t moe_block_norm_workspace_bytes(int32_t T, int32_t D) {
-    if (T < 0 || D < 1) return 0;
-    return sizeof(float) * 2 * static_cast<size_t>(D) * static_cast<size_t>(norm_parts(T, D));
+    if (T < 0 || D < 1 || D > kNormMaxWidth) return 0;
+    return sizeof(float) * 2 * static_cast<size_t>(norm_pitch(D)) * static_cast<size_t>(norm_parts(T, D));
 }
 
 moe_status moe_block_norm_backward(const moe_block_norm_backward_args* p, void* stream) {

@@ -326,6 +326,9 @@ constexpr int kNormMaxWidth = 16384;
 constexpr int kNormMaxRows = 1 << 30;    // row numbers some steps ahead stay inside 32 bits
 constexpr int kNormParts = 304;
 int norm_parts(int64_t T, int D);        // blocks of a backward pass (rows of partial column sums) at most
+// Columns of a part: rows that do not start at a window keep their places in
+// the windows there, so that the sums are stored by 16 bytes.
+inline int norm_pitch(int D) { return D % 8 ? (D + 14) / 8 * 8 : D; }
 struct NormArgs {
     const void *x, *y, *w_post, *w_pre, *gate;
     void *h, *u;
@@ -337,7 +340,9 @@ struct NormBackArgs {
     const void *dh, *du, *h, *y, *w_post, *w_pre, *gate;
     void *dx, *dy;
     float *dw_post, *dw_pre, *d_gate_channel, *d_gate_token;
-    float* part;                         // [grid][2][D], or null: no column sums wanted
+    float* part;                         // [grid][2][pitch], or null: no column sums wanted
+    int pitch, mask;                     // set by the launch: norm_pitch(D); column c of block b's part lies at
+                                         // c + (b ld & mask)
     int64_t ld_dh, ld_du, ld_h, ld_y, ld_dx, ld_dy, T;
     int D, dt_x, dt_y, dt_u, dt_w, gate_kind;
     float res_scale, eps;

@@ -48,7 +48,7 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
 
 // Gradients, with the same ring.  The column sums of a thread's rows stay in
 // registers (sum du h^ and sum total y^, times the token's gate), are added
-// over the block's groups through shared memory and go to part[block][2][D].
+// over the block's groups through shared memory and go to the block's part.
 // The weights wait in shared memory, which leaves registers for 28 warps.  The
 // sums over row t + 1 that its norms need are taken together with the one over
 // row t that its dy needs: one barrier a row, and the work of both before it.
@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         norms(v);
     }
     if (!a.part) return;
-    float* out = a.part + static_cast<int64_t>(g.unit) * 2 * D;
+    const int pitch_c = a.pitch, shift_c = g.shift & a.mask;
+    float* out = a.part + static_cast<int64_t>(g.unit) * 2 * pitch_c;
     // the groups in turn add their columns to the block's, in the ring's
     // memory (one group: straight to the part)
     float* acc = g.groups == 1 ? out : reinterpret_cast<float*>(ring);
@@ -247,9 +248,11 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         if (g.group == k) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = c0 + i * step;
+                // the window's place in the part (outside the row its sums are zero)
+                const int c = c0 + i * step + shift_c;
+                if (c - shift_c >= D) break;
                 auto add = [&](const Pair (&sum)[W / 2], float* to) {
-                    if (c >= 0 && c + W <= D && reinterpret_cast<uintptr_t>(to + c) % 16 == 0) {
+                    if (c >= 0 && c + W <= pitch_c && reinterpret_cast<uintptr_t>(to + c) % 16 == 0) {
 #pragma unroll
                         for (int j = 0; j < W / 4; ++j) {
                             const float2 f = split(sum[2 * j]), e = split(sum[2 * j + 1]);
@@ -263,18 +266,18 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
                     for (int j = 0; j < W / 2; ++j) {
                         const float2 f = split(sum[j]);
                         const int e = c + 2 * j;
-                        if (e >= 0 && e < D) to[e] = (k ? to[e] : 0.0f) + f.x;
-                        if (e + 1 >= 0 && e + 1 < D) to[e + 1] = (k ? to[e + 1] : 0.0f) + f.y;
+                        if (e >= 0 && e < pitch_c) to[e] = (k ? to[e] : 0.0f) + f.x;
+                        if (e + 1 >= 0 && e + 1 < pitch_c) to[e + 1] = (k ? to[e + 1] : 0.0f) + f.y;
                     }
                 };
                 add(s_pre[i], acc);
-                add(s_post[i], acc + D);
+                add(s_post[i], acc + pitch_c);
             }
         }
         __syncthreads();
     }
     if (g.groups > 1)
-        for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) out[c] = acc[c];
+        for (int c = threadIdx.x; c < 2 * pitch_c; c += blockDim.x) out[c] = acc[c];
 }
 
 constexpr int kPlainColumns = 16;       // columns a thread: widths up to 16 * 1024
@@ -355,13 +358,13 @@ __global__ void __launch_bounds__(1024) block_norm_backward_plain_kernel(const N
         }
     }
     if (a.part) {
-        float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
+        float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.pitch;
 #pragma unroll
         for (int i = 0; i < kPlainColumns; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= a.D) break;
             out[c] = s_pre[i];
-            out[a.D + c] = s_post[i];
+            out[a.pitch + c] = s_post[i];
         }
     }
 }
@@ -369,14 +372,14 @@ __global__ void __launch_bounds__(1024) block_norm_backward_plain_kernel(const N
 // Column sums of the CTAs' parts, in a fixed order, and the weights' and the
 // channel gate's gradients from them.
 constexpr int kColGroups = 16;
-__global__ void __launch_bounds__(32 * kColGroups) norm_columns_kernel(const NormBackArgs a, int parts) {
+__global__ void __launch_bounds__(32 * kColGroups) norm_columns_kernel(const NormBackArgs a, int parts, int ld) {
     __shared__ float red[kColGroups][33];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     const int which = blockIdx.y;                 // 0: sum du h^, 1: sum total g y^
     float s = 0.0f;
     if (c < a.D)
-        for (int p = g; p < parts; p += kColGroups) s += a.part[(static_cast<int64_t>(p) * 2 + which) * a.D + c];
+        for (int p = g; p < parts; p += kColGroups) s += a.part[(static_cast<int64_t>(p) * 2 + which) * a.pitch + c + (p * ld & a.mask)];
     red[g][lane] = s;
     __syncthreads();
     if (g != 0 || c >= a.D) return;
@@ -429,7 +432,8 @@ int norm_parts(int64_t T, int D) {
     return static_cast<int>(std::max<int64_t>(1, std::min(T, most)));
 }
 
-cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
+cudaError_t launch_block_norm_backward(const NormBackArgs& in, cudaStream_t s) {
+    NormBackArgs a = in;
     if (a.D < 1 || a.D > kNormMaxWidth || a.T < 0) return cudaErrorInvalidValue;
     if (a.T == 0) {
         if (!a.dw_pre && !a.dw_post && !a.d_gate_channel) return cudaSuccess;
@@ -456,6 +460,8 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     const int slots = window_slots(a.du, a.dt_x, W) + window_slots(a.du, a.dt_u, W) + window_slots(a.dh, a.dt_x, W) +
                       window_slots(a.y, a.dt_y, W);
     const int most = norm_parts(a.T, a.D);
+    a.pitch = norm_pitch(a.D);
+    a.mask = a.D % 8 ? W - 1 : 0;
     Shape sh;
     int parts;
     // the widest row with one window a thread: 1,024 elements of bf16 (28 us for
@@ -467,7 +473,7 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     if (shape_of(a.T, a.D, al, slots, rule, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
-        if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.D));
+        if (a.part && sh.threads > sh.tpr) smem = std::max(smem, sizeof(float) * 2 * static_cast<size_t>(a.pitch));
         parts = sh.grid;
         err = with_kind(kind, sh.edge, [&](auto edge, auto k) {
             return backward_as<decltype(edge)::value, decltype(k)::value>(a, sh, smem, s);
@@ -475,11 +481,12 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& a, cudaStream_t s) {
     } else {
         parts = static_cast<int>(std::min<int64_t>(std::min<int64_t>(a.T, most), 2 * sms));
         const int threads = std::min(1024, (a.D + 31) / 32 * 32);
+        a.mask = 0;
         block_norm_backward_plain_kernel<<<parts, threads, 0, s>>>(a);
         err = cudaGetLastError();
     }
     if (err != cudaSuccess || !a.part) return err;
-    norm_columns_kernel<<<dim3((a.D + 31) / 32, 2), 32 * kColGroups, 0, s>>>(a, parts);
+    norm_columns_kernel<<<dim3((a.D + 31) / 32, 2), 32 * kColGroups, 0, s>>>(a, parts, static_cast<int>((a.du ? a.ld_h : a.ld_dh) & 7));
     return cudaGetLastError();
 }
 
