@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         norms(v);
     }
     if (!a.part) return;
+    pdl_trigger();                     // the columns' kernel may come up while the parts are written
     const int pitch_c = a.pitch, shift_c = g.shift & a.mask;
     float* out = a.part + static_cast<int64_t>(g.unit) * 2 * pitch_c;
     // the groups in turn add their columns to the block's, in the ring's
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(1024) block_norm_backward_plain_kernel(const N
         }
     }
     if (a.part) {
+        pdl_trigger();
         float* out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.pitch;
 #pragma unroll
         for (int i = 0; i < kPlainColumns; ++i) {
@@ -377,6 +379,7 @@ __global__ void __launch_bounds__(32 * kColGroups) norm_columns_kernel(const Nor
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     const int which = blockIdx.y;                 // 0: sum du h^, 1: sum total g y^
+    pdl_wait();
     float s = 0.0f;
     if (c < a.D)
         for (int p = g; p < parts; p += kColGroups) s += a.part[(static_cast<int64_t>(p) * 2 + which) * a.pitch + c + (p * ld & a.mask)];
@@ -486,8 +489,8 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& in, cudaStream_t s) {
         err = cudaGetLastError();
     }
     if (err != cudaSuccess || !a.part) return err;
-    norm_columns_kernel<<<dim3((a.D + 31) / 32, 2), 32 * kColGroups, 0, s>>>(a, parts, static_cast<int>((a.du ? a.ld_h : a.ld_dh) & 7));
-    return cudaGetLastError();
+    return launch_ex(norm_columns_kernel, dim3((a.D + 31) / 32, 2), dim3(32 * kColGroups), 0, s, true, a, parts,
+                     static_cast<int>((a.du ? a.ld_h : a.ld_dh) & 7));
 }
 
 }  // namespace moe
