@@ -1,5 +1,5 @@
 // The norms behind and before a block, with the block's gate and the residual
-// scale, in one pass over the rows; and its gradients.
+// scale, in one pass over the rows (its gradients: norm_back.cu).
 //
 //   rms(v)  = sqrt(mean(v^2) + eps)
 //   h       = r x + g w_post y / rms(y)       r: residual scale, g: gate of the
@@ -16,7 +16,9 @@
 // Bound by HBM: every row of every matrix goes by once.  A row's windows wait
 // in shared memory (a ring that cp.async fills some rows ahead), so that the
 // sums over the row (of y^2, then of h^2) need no second read.  All sums are
-// fp32.
+// fp32.  Measured: 8,192 x 7,168 bf16 84 us (470 MB, 5.6 TB/s; 69 us at the
+// rate of a plain copy), 4,096 x 7,168 fp32 83 (69); 64 rows of bf16 with y in
+// fp32 5 us, which is the launch, two trips to memory and two sums in turn.
 #include "norm.cuh"
 
 namespace moe {

@@ -15,7 +15,7 @@ constexpr int kNormMaxStages = 8;
 
 // ------------------------------------------------------------------ rows by windows
 // A row is cut at the windows of its matrix (8 elements: 16 bytes of a 16-bit
-// type; 4 where every matrix is fp32), not at its own start: for rows of any
+// type; 4 for an fp32 x), not at its own start: for rows of any
 // length the windows inside a row are whole 16-byte words, and only its first
 // and last window may be partial.  All matrices of a launch have 16-byte
 // aligned bases and row strides that are equal modulo a window, so a row lies

@@ -49,9 +49,14 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
 // Gradients, with the same ring.  The column sums of a thread's rows stay in
 // registers (sum du h^ and sum total y^, times the token's gate), are added
 // over the block's groups through shared memory and go to the block's part.
-// The weights wait in shared memory, which leaves registers for 28 warps.  The
+// The weights wait in shared memory, which leaves registers for the sums.  The
 // sums over row t + 1 that its norms need are taken together with the one over
 // row t that its dy needs: one barrier a row, and the work of both before it.
+// What bounds it: HBM for whole rows of up to 8,192 elements of 16 bits or
+// 5,632 of fp32 (4,096 x 7,168 bf16 62 us, 352 MB, 5.7 TB/s; 52 us at the rate
+// of a plain copy; 4,096 x 5,120 fp32 74 and 74); the cluster's barrier, of a
+// microsecond, for split ones (4,096 x 7,168 fp32 150 and 104); the few warps
+// that mask partial windows for rows of odd lengths (4,096 x 7,167 bf16 97).
 template <int NV, int MAXT, bool EDGE, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages,
                                                                    const Steps st) {
@@ -410,9 +415,10 @@ __global__ void norm_zero_kernel(const NormBackArgs a) {
 
 // Two windows a thread in one block of up to 512 threads a SM, 128 registers
 // each: the sums' exchange, the copies' and the loop's instructions are paid
-// for 16 elements at a time.  4,096 x 7,168 bf16 70 us, one window a thread in
-// 896 threads of 72 registers 84; 4,096 x 3,584 fp32 53 and 86.  Narrow rows
-// have one window a thread; where that takes 72 registers, 896 threads.
+// for 16 elements at a time.  With all else alike, 4,096 x 7,168 bf16 70 us, one
+// window a thread in 896 threads of 72 registers 84; 4,096 x 3,584 fp32 53 and
+// 86.  Narrow rows have one window a thread; where that takes 72 registers, 896
+// threads.
 // Whole fp32 rows of up to 5,632 elements, whose ring has room for two rows,
 // are not split: 704 threads of 88 registers.  4,096 x 5,120 76 us, split 128.
 constexpr int kWideRow = 704;
@@ -467,9 +473,9 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& in, cudaStream_t s) {
     a.mask = a.D % 8 ? W - 1 : 0;
     Shape sh;
     int parts;
-    // the widest row with one window a thread: 1,024 elements of bf16 (28 us for
-    // 8,192 rows, two windows 30; 2,048 elements 46 and 38), of fp32 too (32 and
-    // 32), 2,048 with y in fp32 (53 and 56)
+    // the widest row with one window a thread: 1,024 elements of 16 bits (8,192
+    // rows: 28 us, two windows 30; 2,048 elements 46 and 38) and of fp32 (32 and
+    // 32), 2,048 with y in fp32 (53 and 56), all else alike
     const int two_from = kind == NORM_BF16 || kind == NORM_F16 ? 128 : 256;
     const bool whole_row = !al.odd && a.D % W == 0, lean_row = whole_row && lean_kind(kind) && a.D <= two_from * W;
     const Rule rule = {two_from, lean_row ? 896 : 512, whole_row && kind == NORM_F32 ? kWideRow : 512, 512, lean_row ? 72 : 128, 3, kNormMaxSplit, 0};

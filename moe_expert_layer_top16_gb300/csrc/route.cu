@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(kSortMaxWarps * 32)
 // One warp per (token, chunk of the row, group of slots): the chunk's loads
 // are issued once, then stored to each slot's place.  V: the widest word that
 // both matrices' addresses, strides and the row's length are multiples of.
+// Bound by HBM writes: 8,192 tokens of 3,584 bf16 to 16 places each 150 us (1.0
+// GB, 6.6 TB/s; 147 at the rate of a plain copy).
 constexpr int kPermWords = 4;     // words a lane holds
 
 template <typename V>
@@ -247,7 +249,7 @@ __global__ void permute_kernel(const uint8_t* __restrict__ x, int64_t x_stride, 
 // One warp per (token, 32 V columns), or, element by element, per 4 times 32
 // columns, so that a warp that reads 64 bytes at a time has enough of them in
 // flight: the slots' loads are issued a batch at a time, their FMAs run in
-// slot order.
+// slot order.  4,096 x 16 rows of 3,584 bf16: 68 us, 7.2 TB/s (mostly reads).
 constexpr int kUnpermBatch = 8;
 
 template <int V, int U, int DT>
