@@ -16,8 +16,8 @@
 // Bound by HBM: every row of every matrix goes by once.  A row's windows wait
 // in shared memory (a ring that cp.async fills some rows ahead), so that the
 // sums over the row (of y^2, then of h^2) need no second read.  All sums are
-// fp32.  Measured: 8,192 x 7,168 bf16 84 us (470 MB, 5.6 TB/s; 69 us at the
-// rate of a plain copy), 4,096 x 7,168 fp32 83 (69); 64 rows of bf16 with y in
+// fp32.  Measured: 8,192 x 7,168 bf16 81 us (470 MB, 5.8 TB/s; 69 us at the
+// rate of a plain copy), fp32 163 (139); 64 rows of bf16 with y in
 // fp32 5 us, which is the launch, two trips to memory and two sums in turn.
 #include "norm.cuh"
 
@@ -217,9 +217,14 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     al.add(a.u, a.ld_u);
     Shape sh;
     const int slots = window_slots(true, a.dt_x, W) + window_slots(a.y, a.dt_y, W);
-    // 896 threads in two groups of 448 for 7,168 elements: the one group's
-    // sums overlap the other's loads and stores
-    if (shape_of(a.T, a.D, al, slots, Rule{256, 1024, 1024, 1024, 64, 2, kNormMaxSplit, W == 4 ? 2 : 3}, sms, 1 << 30, &sh)) {
+    // Two windows a thread from 65 on (8,192 x 2,048 bf16 22 us, one 26; 1,024
+    // fp32 21 and 24).  Two groups a block overlap the one's sums with the
+    // other's loads and stores; many whole rows of 448 windows or more are
+    // better off with one group and a ring of four rows (8,192 x 7,168 bf16 81.5
+    // and 84 us, 4,096 fp32 82.5 and 95; of 1,024 rows 15.3 and 13).
+    const bool mixed = a.dt_x != ELEM_F32 && ty == ELEM_F32, whole_row = !al.odd && a.D % W == 0;
+    const int deep = mixed ? 2 : (whole_row && a.D >= 448 * W && a.T >= 32 * static_cast<int64_t>(sms) ? 4 : 3);
+    if (shape_of(a.T, a.D, al, slots, Rule{64, 1024, 1024, 1024, 64, deep, 1, kNormMaxSplit, W == 4 ? 2 : 3}, sms, 1 << 30, &sh)) {
         if (kind == NORM_F32_Y16) return forward_as<true, NORM_F32_Y16>(a, sh, s);
         return with_kind(kind, sh.edge, [&](auto edge, auto k) {
             return forward_as<decltype(edge)::value, decltype(k)::value>(a, sh, s);

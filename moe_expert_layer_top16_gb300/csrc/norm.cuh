@@ -497,10 +497,10 @@ constexpr int kNormSmem = kSmemLimit - 2048;     // without the sums' static par
 // What a kernel allows: rows of more than two_from windows have two a thread;
 // group_threads: threads of a block's groups together at most, row_threads of
 // one, part_threads of a block of a split row; regs: of a thread; deep: rows of a group in the ring, where there is
-// room; split: blocks that share a row at most; slots_for: slots of a window
+// room, rows_used: in use at once; split: blocks that share a row at most; slots_for: slots of a window
 // that have to fit, if there are as many or not (0: as there are).
 struct Rule {
-    int two_from, group_threads, row_threads, part_threads, regs, deep, split, slots_for;
+    int two_from, group_threads, row_threads, part_threads, regs, deep, rows_used, split, slots_for;
 };
 
 // slots: of a window in the ring; most: blocks (clusters).
@@ -537,7 +537,7 @@ inline bool shape_of(int64_t T, int D, const Alike& al, int slots, const Rule& r
     int st = (kNormSmem / per_block - 1024 - fixed) / (stage * s->threads);
     st = std::max(1, std::min<int>(st, kNormMaxStages));
     s->stages = static_cast<int>(std::min<int64_t>(st, rows));
-    if (rule.deep > 2 && s->stages < 2 && rows > 1) return false;         // two rows are in use at once
+    if (s->stages < std::min<int64_t>(rule.rows_used, rows)) return false;
     s->smem = static_cast<size_t>(s->stages) * stage * s->threads + fixed;
     return s->smem <= static_cast<size_t>(kNormSmem);
 }

@@ -478,7 +478,7 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& in, cudaStream_t s) {
     // 32), 2,048 with y in fp32 (53 and 56), all else alike
     const int two_from = kind == NORM_BF16 || kind == NORM_F16 ? 128 : 256;
     const bool whole_row = !al.odd && a.D % W == 0, lean_row = whole_row && lean_kind(kind) && a.D <= two_from * W;
-    const Rule rule = {two_from, lean_row ? 896 : 512, whole_row && kind == NORM_F32 ? kWideRow : 512, 512, lean_row ? 72 : 128, 3, kNormMaxSplit, 0};
+    const Rule rule = {two_from, lean_row ? 896 : 512, whole_row && kind == NORM_F32 ? kWideRow : 512, 512, lean_row ? 72 : 128, 3, 2, kNormMaxSplit, 0};
     if (shape_of(a.T, a.D, al, slots, rule, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
