@@ -417,20 +417,17 @@ __global__ void norm_zero_kernel(const NormBackArgs a) {
 // each: the sums' exchange, the copies' and the loop's instructions are paid
 // for 16 elements at a time.  With all else alike, 4,096 x 7,168 bf16 70 us, one
 // window a thread in 896 threads of 72 registers 84; 4,096 x 3,584 fp32 53 and
-// 86.  Narrow rows have one window a thread; where that takes 72 registers, 896
-// threads.
+// 86.  Narrow rows have one window a thread.
 // Whole fp32 rows of up to 5,632 elements, whose ring has room for two rows,
 // are not split: 704 threads of 88 registers.  4,096 x 5,120 76 us, split 128.
 constexpr int kWideRow = 704;
-constexpr bool lean_kind(int kind) { return kind == NORM_BF16 || kind == NORM_F16 || kind == NORM_F32; }
 template <bool EDGE, int KIND>
 cudaError_t backward_as(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
-    constexpr int kNarrow = !EDGE && lean_kind(KIND) ? 896 : 512;
     if (sh.split > 1) return run_rows(block_norm_backward_kernel<2, 512, EDGE, KIND, true>, a, sh, smem, s);
     if constexpr (!EDGE && KIND == NORM_F32)
         if (sh.nv == 2 && sh.threads > 512) return run_rows(block_norm_backward_kernel<2, kWideRow, EDGE, KIND, false>, a, sh, smem, s);
     if (sh.nv == 2) return run_rows(block_norm_backward_kernel<2, 512, EDGE, KIND, false>, a, sh, smem, s);
-    return run_rows(block_norm_backward_kernel<1, kNarrow, EDGE, KIND, false>, a, sh, smem, s);
+    return run_rows(block_norm_backward_kernel<1, 512, EDGE, KIND, false>, a, sh, smem, s);
 }
 
 }  // namespace
@@ -473,12 +470,11 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& in, cudaStream_t s) {
     a.mask = a.D % 8 ? W - 1 : 0;
     Shape sh;
     int parts;
-    // the widest row with one window a thread: 1,024 elements of 16 bits (8,192
-    // rows: 28 us, two windows 30; 2,048 elements 46 and 38) and of fp32 (32 and
-    // 32), 2,048 with y in fp32 (53 and 56), all else alike
-    const int two_from = kind == NORM_BF16 || kind == NORM_F16 ? 128 : 256;
-    const bool whole_row = !al.odd && a.D % W == 0, lean_row = whole_row && lean_kind(kind) && a.D <= two_from * W;
-    const Rule rule = {two_from, lean_row ? 896 : 512, whole_row && kind == NORM_F32 ? kWideRow : 512, 512, lean_row ? 72 : 128, 3, 2, kNormMaxSplit, 0};
+    // one window a thread up to 64 (8,192 rows of 1,024 bf16 25.7 us, two 23.7);
+    // with y in fp32 up to 256 (29.5 and 31.7), and two groups a block rather
+    // than a third row in the ring (3,584 columns 79 and 96)
+    const bool mixed = a.dt_x != ELEM_F32 && a.y && a.dt_y == ELEM_F32, whole_row = !al.odd && a.D % W == 0;
+    const Rule rule = {mixed ? 256 : 64, 512, whole_row && kind == NORM_F32 ? kWideRow : 512, 512, 128, mixed ? 2 : 3, 2, kNormMaxSplit, 0};
     if (shape_of(a.T, a.D, al, slots, rule, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
