@@ -37,9 +37,10 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
     const int du = K::small ? K::x : a.dt_u;
     const bool post = a.y != nullptr, pre = a.u != nullptr;
     const Rows g = rows_of<SPLIT>(tpr, a.ld_x, W);
-    if constexpr (SPLIT) cluster_sync_all();           // the others' shared memory is there
+    __shared__ Exchange exchange;
+    if constexpr (SPLIT) exchange_start(&exchange);
     auto row_sum = [&](float v) {
-        if constexpr (SPLIT) return cluster_sum(v, g, red, buf);
+        if constexpr (SPLIT) return cluster_sum(v, g, red, &exchange, buf);
         else {
             float ss[1] = {v};
             group_sums<1>(ss, g, reinterpret_cast<float (*)[1][kNormMaxWarps]>(red), buf);

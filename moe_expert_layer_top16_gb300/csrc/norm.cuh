@@ -404,27 +404,50 @@ __device__ __forceinline__ void group_sums(float (&v)[N], const Rows& g, float (
     buf ^= 1;
 }
 
-// Split rows: a warp's value goes to every block of the cluster, whose barrier
-// takes the place of the group's (a block writes a buffer again one barrier
-// after the others have read it).
-__device__ __forceinline__ void send_all(const float* here, const Rows& g, float v) {
-    const uint32_t at = smem_u32(here);
-    for (int r = 0; r < g.parts; ++r)
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(at, r)), "f"(v) : "memory");
+// Split rows: a warp's value goes to every block of the cluster by a store that
+// counts on the receiver's mbarrier.  (A cluster barrier's release also waits
+// for the thread's stores to memory, a microsecond a row.)  A buffer and its
+// mbarrier are used in every other turn: a block sends for turn n + 2 once it
+// has every warp's values of turn n + 1, which they send after they have read
+// those of turn n.  Nothing a user can do makes a wait run out; if one does,
+// the sums become NaN.
+struct Exchange {
+    uint64_t bar[2];
+    int lost;
+};
+__device__ __forceinline__ void exchange_start(Exchange* x) {
+    if (threadIdx.x == 0) {
+        mbar_init(&x->bar[0], 1);
+        mbar_init(&x->bar[1], 1);
+        x->lost = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    cluster_sync_all();
 }
-__device__ __forceinline__ float cluster_sum(float v, const Rows& g, float (*red)[kNormMaxSplit * kNormMaxWarps], int& buf) {
+__device__ __forceinline__ void send_all(const float* here, Exchange* x, int turn, const Rows& g, float v) {
+    const uint32_t at = smem_u32(here), bar = smem_u32(&x->bar[turn & 1]);
+    for (int r = 0; r < g.parts; ++r) st_async_f32(mapa_shared(at, r), v, mapa_shared(bar, r));
+}
+// Values of this turn that a block gets: one of each of `count` a warp.
+__device__ __forceinline__ bool receive_all(Exchange* x, int turn, const Rows& g, int count) {
+    if (threadIdx.x == 0)
+        mbar_arrive_expect_tx(&x->bar[turn & 1], static_cast<uint32_t>(g.parts * (g.tpr >> 5) * count * 4));
+    return mbar_wait(&x->bar[turn & 1], (turn >> 1) & 1, &x->lost, nullptr, 0);
+}
+__device__ __forceinline__ float cluster_sum(float v, const Rows& g, float (*red)[kNormMaxSplit * kNormMaxWarps], Exchange* x,
+                                             int& turn) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     const int lane = threadIdx.x & 31, warps = g.tpr >> 5;
-    if (lane == 0) send_all(&red[buf][g.part * warps + (threadIdx.x >> 5)], g, v);
+    if (lane == 0) send_all(&red[turn & 1][g.part * warps + (threadIdx.x >> 5)], x, turn, g, v);
     __syncwarp();
-    cluster_sync_all();
-    v = 0.0f;
-    for (int w = lane; w < g.parts * warps; w += 32) v += red[buf][w];
+    v = receive_all(x, turn, g, 1) ? 0.0f : __uint_as_float(0x7FC00000u);
+    for (int w = lane; w < g.parts * warps; w += 32) v += red[turn & 1][w];
     __syncwarp();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    buf ^= 1;
+    ++turn;
     return v;
 }
 
@@ -492,7 +515,14 @@ struct Shape {
     bool edge;                  // some windows lie only partly in their row
     size_t smem;
 };
-constexpr int kNormSmem = kSmemLimit - 2048;     // without the sums' static part
+constexpr int kNormStatic = 2304;                // the sums' static part at most
+constexpr int kNormSmem = kSmemLimit - kNormStatic;
+
+// Dynamic shared memory of each of `blocks` blocks on one SM (1 KB a block is
+// the system's).
+constexpr int room_of(int blocks) {
+    return blocks == 1 ? kNormSmem : (kSmemLimit + 1024) / blocks - 1024 - kNormStatic;
+}
 
 // What a kernel allows: rows of more than two_from windows have two a thread;
 // group_threads: threads of a block's groups together at most, row_threads of
@@ -520,7 +550,7 @@ inline bool shape_of(int64_t T, int D, const Alike& al, int slots, const Rule& r
     s->threads = s->tpr * groups;
     int per_sm = std::max(1, std::min(65536 / (rule.regs * s->threads), 2048 / s->threads));
     // at least `deep` rows in the ring of a group
-    while (per_sm > 1 && per_sm * (rule.deep * stage * s->threads + fixed + 1024) > kNormSmem) --per_sm;
+    while (per_sm > 1 && rule.deep * stage * s->threads + fixed > room_of(per_sm)) --per_sm;
     // clusters of four: the SMs of a GPC are not all multiples of four (with 38
     // clusters for 152 SMs two waited for the others: twice the time)
     const int units = sms * per_sm / split - (split > 2 ? 2 : 0);
@@ -534,7 +564,7 @@ inline bool shape_of(int64_t T, int D, const Alike& al, int slots, const Rule& r
     s->grid = static_cast<int>(grid);
     const int per_block = std::min<int>(per_sm, static_cast<int>((grid * split + sms - 1) / sms));
     const int64_t rows = (T + grid * groups - 1) / (grid * groups);                        // of a group at most
-    int st = (kNormSmem / per_block - 1024 - fixed) / (stage * s->threads);
+    int st = (room_of(per_block) - fixed) / (stage * s->threads);
     st = std::max(1, std::min<int>(st, kNormMaxStages));
     s->stages = static_cast<int>(std::min<int64_t>(st, rows));
     if (s->stages < std::min<int64_t>(rule.rows_used, rows)) return false;

@@ -11,7 +11,8 @@ namespace {
 // `between` is done before the barrier: what the threads that arrive first do
 // while they would wait.
 template <bool SPLIT, int WARPS, typename F>
-__device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float (*red)[4][WARPS], int& buf, F between) {
+__device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float (*red)[4][WARPS], Exchange* exchange, int& buf,
+                                            F between) {
     const int lane = threadIdx.x & 31;
     const bool up = lane & 16, odd = lane & 8;
     // lanes 0-15 keep values 0 and 1, lanes 16-31 values 2 and 3
@@ -23,22 +24,22 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
     if (SPLIT || g.tpr > 32) {
         const int warp = threadIdx.x >> 5, warps = (g.tpr >> 5) * g.parts, warp0 = g.group * warps;
         if constexpr (SPLIT) {
-            if ((lane & 7) == 0) send_all(&red[buf][lane >> 3][g.part * (g.tpr >> 5) + warp], g, s);
+            if ((lane & 7) == 0) send_all(&red[buf & 1][lane >> 3][g.part * (g.tpr >> 5) + warp], exchange, buf, g, s);
             between();
             __syncwarp();
-            cluster_sync_all();
+            s = receive_all(exchange, buf, g, 4) ? 0.0f : __uint_as_float(0x7FC00000u);
         } else {
             if ((lane & 7) == 0) red[buf][lane >> 3][warp] = s;
             between();
             asm volatile("bar.sync %0, %1;" ::"r"(1 + g.group), "r"(g.tpr) : "memory");
+            s = 0.0f;
         }
-        s = 0.0f;
 #pragma unroll
         for (int w = 0; w < WARPS; w += 8)
-            if (w + (lane & 7) < warps) s += red[buf][lane >> 3][warp0 + w + (lane & 7)];
+            if (w + (lane & 7) < warps) s += red[SPLIT ? buf & 1 : buf][lane >> 3][warp0 + w + (lane & 7)];
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        buf ^= 1;
+        buf = SPLIT ? buf + 1 : buf ^ 1;
     } else {
         between();
     }
@@ -70,7 +71,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
     const bool post = K::full || a.y != nullptr, pre = K::full || a.du != nullptr, has_dh = K::full || a.dh != nullptr;
     const bool want_dx = K::full || a.dx != nullptr, want_dy = K::full || a.dy != nullptr;
     const Rows g = rows_of<SPLIT>(tpr, pre ? a.ld_h : a.ld_dh, W);
-    if constexpr (SPLIT) cluster_sync_all();           // the others' shared memory is there
+    __shared__ Exchange exchange;
+    if constexpr (SPLIT) exchange_start(&exchange);
     const int D = a.D, T = static_cast<int>(a.T);
     const int pitch = blockDim.x * 16, wpitch = tpr * 16;
     const int off_u = window_slots(pre, tx, W), off_d = off_u + window_slots(pre, tu, W),
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
         cp_async_wait(stages - 1);
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         squares(mine, v);
-        group_sums4<SPLIT>(v, g, red, buf, [] {});
+        group_sums4<SPLIT>(v, g, red, &exchange, buf, [] {});
         norms(v);
     }
     for (int t = g.first; t < T; t += g.step) {
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBac
             squares(mine + stage * stage_pitch, v);
         }
         // this thread is through with row t's slots
-        group_sums4<SPLIT>(v, g, red, buf, [&] { issue(t + stages * g.step); });
+        group_sums4<SPLIT>(v, g, red, &exchange, buf, [&] { issue(t + stages * g.step); });
         if (post) {
             if (a.d_gate_token && g.lane_in_group == 0 && g.part == 0) a.d_gate_token[t] = v[3] * q;
             if (want_dy) {

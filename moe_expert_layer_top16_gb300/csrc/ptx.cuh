@@ -356,6 +356,14 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Store a word in the shared memory of a CTA of the cluster and count its four
+// bytes on that CTA's mbarrier (shared::cluster addresses), without ordering
+// anything else that the thread has written.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
+}
 // Arrive on an mbarrier of another CTA of the cluster, without ordering the
 // thread's earlier memory accesses (a release at cluster scope waits until
 // the thread's global stores are visible, about a microsecond after an
