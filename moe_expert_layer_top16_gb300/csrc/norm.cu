@@ -222,9 +222,10 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     // fp32 21 and 24).  Two groups a block overlap the one's sums with the
     // other's loads and stores; many whole rows of 448 windows or more are
     // better off with one group and a ring of four rows (8,192 x 7,168 bf16 81.5
-    // and 84 us, 4,096 fp32 82.5 and 95; of 1,024 rows 15.3 and 13).
+    // and 84 us, 4,096 fp32 82.5 and 95; of 1,024 rows 15.3 and 13).  Odd rows
+    // are better off with two groups than with a third row (7,167 48 and 63).
     const bool mixed = a.dt_x != ELEM_F32 && ty == ELEM_F32, whole_row = !al.odd && a.D % W == 0;
-    const int deep = mixed ? 2 : (whole_row && a.D >= 448 * W && a.T >= 32 * static_cast<int64_t>(sms) ? 4 : 3);
+    const int deep = mixed || !whole_row ? 2 : (a.D >= 448 * W && a.T >= 32 * static_cast<int64_t>(sms) ? 4 : 3);
     if (shape_of(a.T, a.D, al, slots, Rule{64, 1024, 1024, 1024, 64, deep, 1, kNormMaxSplit, W == 4 ? 2 : 3}, sms, 1 << 30, &sh)) {
         if (kind == NORM_F32_Y16) return forward_as<true, NORM_F32_Y16>(a, sh, s);
         return with_kind(kind, sh.edge, [&](auto edge, auto k) {

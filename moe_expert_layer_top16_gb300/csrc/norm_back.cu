@@ -53,11 +53,10 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
 // The weights wait in shared memory, which leaves registers for the sums.  The
 // sums over row t + 1 that its norms need are taken together with the one over
 // row t that its dy needs: one barrier a row, and the work of both before it.
-// What bounds it: HBM for whole rows of up to 8,192 elements of 16 bits or
-// 5,632 of fp32 (4,096 x 7,168 bf16 62 us, 352 MB, 5.7 TB/s; 52 us at the rate
-// of a plain copy; 4,096 x 5,120 fp32 89 and 74); the cluster's barrier, of a
-// microsecond, for split ones (4,096 x 7,168 fp32 168 and 104); the few warps
-// that mask partial windows for rows of odd lengths (4,096 x 7,167 bf16 99).
+// What bounds it: HBM for whole rows (4,096 x 7,168 bf16 62 us, 352 MB, 5.7
+// TB/s; 52 us at the rate of a plain copy; fp32, split over two blocks, 111 and
+// 104); for rows of odd lengths the few warps that mask partial windows (4,096
+// x 7,167 bf16 99).
 template <int NV, int MAXT, bool EDGE, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages,
                                                                    const Steps st) {
@@ -420,15 +419,11 @@ __global__ void norm_zero_kernel(const NormBackArgs a) {
 // for 16 elements at a time.  With all else alike, 4,096 x 7,168 bf16 70 us, one
 // window a thread in 896 threads of 72 registers 87; 4,096 x 3,584 fp32 (h, du
 // and dh one tensor) 53 and 86.  Narrow rows have one window a thread.
-// Whole fp32 rows of up to 5,632 elements, whose ring has room for two rows,
-// are not split: 704 threads of 88 registers.  4,096 x 5,120 (one tensor again)
-// 76 us, split 128.
-constexpr int kWideRow = 704;
+// Wider rows than 1,024 windows are split, where one block of 704 threads would
+// do too (4,096 x 5,120 fp32 83.5 us, one block 88.6).
 template <bool EDGE, int KIND>
 cudaError_t backward_as(const NormBackArgs& a, const Shape& sh, size_t smem, cudaStream_t s) {
     if (sh.split > 1) return run_rows(block_norm_backward_kernel<2, 512, EDGE, KIND, true>, a, sh, smem, s);
-    if constexpr (!EDGE && KIND == NORM_F32)
-        if (sh.nv == 2 && sh.threads > 512) return run_rows(block_norm_backward_kernel<2, kWideRow, EDGE, KIND, false>, a, sh, smem, s);
     if (sh.nv == 2) return run_rows(block_norm_backward_kernel<2, 512, EDGE, KIND, false>, a, sh, smem, s);
     return run_rows(block_norm_backward_kernel<1, 512, EDGE, KIND, false>, a, sh, smem, s);
 }
@@ -476,8 +471,8 @@ cudaError_t launch_block_norm_backward(const NormBackArgs& in, cudaStream_t s) {
     // one window a thread up to 64 (one tensor for h, du and dh: 8,192 rows of 1,024 bf16 25.7 us, two 23.7);
     // with y in fp32 up to 256 (29.5 and 31.7), and two groups a block rather
     // than a third row in the ring (3,584 columns 79 and 96)
-    const bool mixed = a.dt_x != ELEM_F32 && a.y && a.dt_y == ELEM_F32, whole_row = !al.odd && a.D % W == 0;
-    const Rule rule = {mixed ? 256 : 64, 512, whole_row && kind == NORM_F32 ? kWideRow : 512, 512, 128, mixed ? 2 : 3, 2, kNormMaxSplit, 0};
+    const bool mixed = a.dt_x != ELEM_F32 && a.y && a.dt_y == ELEM_F32;
+    const Rule rule = {mixed ? 256 : 64, 512, 512, 512, 128, mixed ? 2 : 3, 2, kNormMaxSplit, 0};
     if (shape_of(a.T, a.D, al, slots, rule, sms, most, &sh)) {
         // the end of the kernel adds the groups' columns in the ring's memory
         size_t smem = sh.smem;
