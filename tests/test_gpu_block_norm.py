@@ -274,3 +274,33 @@ def test_backward_wide_again_and_in_a_graph(T, D, tx, ty, tw, gate):
     for _, out in graphs:
         for n, t in ref.items():
             assert torch.equal(t, out[n]), n
+
+
+@pytest.mark.parametrize("T,D,t", [(64, 256, BF16), (1300, 1001, BF16), (300, 7168, F32), (200, 7168, F16), (41, 5001, F32)])
+def test_backward_in_place(T, D, t):
+    """dx over dh or du, dy over y: the same bits as with outputs of their own (and a misaligned base, element by element)."""
+    import ctypes as C
+    from moe_expert_layer_top16_gb300 import block
+    code = block.DTYPES[t]
+    s = make(T, D, t, t, F32, "channel", seed=7)
+    du = s["du"].to(t)
+    work = torch.empty(moe.lib().moe_block_norm_workspace_bytes(T, D) + 64, dtype=torch.uint8, device=DEV)
+
+    def call(dh, du, y, dx, dy):
+        grads = [torch.empty(D, device=DEV) for _ in range(3)]
+        a = block._BlockNormBackwardArgs(
+            dh.data_ptr(), D, du.data_ptr(), D, s["x"].data_ptr(), D, y.data_ptr(), D, s["w_post"].data_ptr(), s["w_pre"].data_ptr(),
+            s["gate"].data_ptr(), dx.data_ptr(), D, dy.data_ptr(), D, *(g.data_ptr() for g in grads), work.data_ptr(), work.numel(),
+            T, D, code, code, code, 0, moe.block.GATE_CHANNEL, 0.75, EPS)
+        assert moe.lib().moe_block_norm_backward(C.byref(a), torch.cuda.current_stream().cuda_stream) == moe.MOE_OK
+        return [dx.clone(), dy.clone()] + grads
+
+    for off in (0, 1):                                      # off: bases of one element more than a multiple of 16 bytes
+        own = lambda v: torch.cat([v.reshape(-1)[:off], v.reshape(-1)])[off:].view(T, D)  # noqa: E731
+        ref = call(own(s["dh"]), own(du), own(s["y"]), own(s["dh"]), own(s["y"]))
+        dh, y = own(s["dh"]), own(s["y"])
+        for got in (call(dh, own(du), y, dh, y),):
+            assert all(torch.equal(a, b) for a, b in zip(ref, got))
+        u, y = own(du), own(s["y"])
+        got = call(own(s["dh"]), u, y, u, y)
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
