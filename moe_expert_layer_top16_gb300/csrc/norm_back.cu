@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(1024) block_norm_backward_plain_kernel(const N
 
 // Column sums of the CTAs' parts, in a fixed order, and the weights' and the
 // channel gate's gradients from them.
-constexpr int kColGroups = 16;
+constexpr int kColGroups = 16, kColBatch = 10;     // loads in flight: 152 parts in one go
 __global__ void __launch_bounds__(32 * kColGroups) norm_columns_kernel(const NormBackArgs a, int parts, int ld) {
     __shared__ float red[kColGroups][33];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
@@ -387,8 +387,20 @@ __global__ void __launch_bounds__(32 * kColGroups) norm_columns_kernel(const Nor
     const int which = blockIdx.y;                 // 0: sum du h^, 1: sum total g y^
     pdl_wait();
     float s = 0.0f;
-    if (c < a.D)
-        for (int p = g; p < parts; p += kColGroups) s += a.part[(static_cast<int64_t>(p) * 2 + which) * a.pitch + c + (p * ld & a.mask)];
+    if (c < a.D) {
+        const float* from = a.part + static_cast<int64_t>(which) * a.pitch + c;
+        const int64_t part = 2 * static_cast<int64_t>(a.pitch);
+        for (int p = g; p < parts; p += kColBatch * kColGroups) {
+            float v[kColBatch];
+#pragma unroll
+            for (int u = 0; u < kColBatch; ++u) {
+                const int q = p + u * kColGroups;
+                v[u] = q < parts ? from[q * part + (q * ld & a.mask)] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kColBatch; ++u) s += v[u];
+        }
+    }
     red[g][lane] = s;
     __syncthreads();
     if (g != 0 || c >= a.D) return;
