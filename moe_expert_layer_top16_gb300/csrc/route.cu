@@ -14,6 +14,8 @@
 //
 // Every place is written by exactly one thread and every sum runs in a fixed
 // order: results do not depend on scheduling.
+#include <algorithm>
+
 #include "internal.h"
 #include "vec.cuh"
 
@@ -36,18 +38,28 @@ namespace {
 // launch counts each CTA's experts into the workspace, and every CTA of the
 // second sums the counts of the CTAs before it: a cluster of eight CTAs with
 // distributed shared memory took 33 us for 131,072 slots, bound by the
-// shared-memory pipes of eight SMs, 64 CTAs in two launches take 14.5.
+// shared-memory pipes of eight SMs, 64 CTAs in two launches take 14.5.  (One
+// launch up to 4,096 slots, 11.7 us at most on the device, where two would take
+// 7.3: the second launch and its workspace cost the host four.)
 constexpr int kSortMaxE = 1024;
 constexpr int kSortMaxWarps = 32;
 constexpr int kSortBatch = 4;
 constexpr int64_t kSortOne = 4096;         // slots of a single-CTA sort
+constexpr int kSortSlots = 2048;
 constexpr int kSortMaxCtas = 152;
+constexpr int kSortCounts = 1 << 16;
 
-// CTAs of a sort of n slots: 2,048 slots each, until every SM has one.
-int sort_ctas(int64_t n) {
+// CTAs of a sort of n slots.  Each reads all CTAs' counts, so that many of them
+// pay for short strips only with few experts: half of kSortSlots a CTA up to 32
+// (16,384 slots 8.0 us, 9.2 with half as many CTAs; 65,536 on 32 CTAs 11.1, on
+// 64 13.0), then kSortSlots until every SM has one or there are kSortCounts
+// counts (262,144 slots of 896 experts on 128 CTAs 33.6 us, on 73 17.5).
+int sort_ctas(int64_t n, int E) {
     if (n <= kSortOne) return 1;
-    const int64_t c = (n + 2047) / 2048;
-    return static_cast<int>(c < kSortMaxCtas ? c : kSortMaxCtas);
+    const int64_t half = (2 * n + kSortSlots - 1) / kSortSlots, whole = (n + kSortSlots - 1) / kSortSlots;
+    const int64_t c = std::max(whole, std::min<int64_t>(half, 32));
+    const int most = std::min(kSortMaxCtas, std::max(32, kSortCounts / E));
+    return static_cast<int>(c < most ? c : most);
 }
 
 // Slots of CTA c of C: [first, last), whole 32-slot steps.
@@ -410,18 +422,19 @@ cudaError_t permute_as(const uint8_t* x, int64_t x_stride, int64_t row_bytes, in
 }  // namespace
 
 size_t sort_workspace_bytes(int64_t n, int E) {
-    const int C = sort_ctas(n);
+    const int C = sort_ctas(n, E);
     return C > 1 ? sizeof(int32_t) * static_cast<size_t>(C) * E : 0;
 }
 
 cudaError_t launch_sort(const int32_t* idx, int64_t n, int E, int32_t* offsets, int32_t* sorted_slot,
                         int32_t* slot_pos, int32_t* work, cudaStream_t s) {
     if (n < 0 || E < 1 || E > kSortMaxE) return cudaErrorInvalidValue;
-    const int C = sort_ctas(n);
+    const int C = sort_ctas(n, E);
     if (C > 1 && !work) return cudaErrorInvalidValue;
     const int64_t steps = ((n + 31) / 32 + C - 1) / C;
     int W = 4;
-    while (W < (C > 1 ? 16 : kSortMaxWarps) && W < steps) W *= 2;
+    // (more warps than a short strip each needs make the scan over them longer)
+    while (W < (C > 1 && steps <= kSortSlots / 32 ? 16 : kSortMaxWarps) && W < steps) W *= 2;
     const size_t row = sizeof(int32_t) * static_cast<size_t>((E + 3) & ~3), smem = row * (W + 1);
     static_assert(sizeof(int32_t) * (kSortMaxWarps + 1) * kSortMaxE <= kSmemLimit - 1024, "sort tables");
     if (smem > 40 * 1024) {         // with the static part, up to 48 KB need no attribute

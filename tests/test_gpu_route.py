@@ -192,3 +192,20 @@ def test_empty_batch():
     assert moe.unpermute(x, pos).shape == (0, 16)
     d_rows, d_w = moe.unpermute_backward(x, x, pos)
     assert d_rows.shape == (0, 16) and d_w.shape == (0, 4)
+
+
+@pytest.mark.parametrize("T,k,E", [(257, 16, 896), (1024, 16, 5), (2049, 16, 1024), (16384, 16, 896), (40001, 15, 64), (70000, 16, 1)])
+def test_sort_at_its_launches_borders(T, k, E):
+    """Few and many CTAs, short and long strips, against a stable sort."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    idx = torch.randint(-1 if T % 2 else 0, E, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    offsets, sorted_slot, slot_pos = moe.sort_by_expert(idx, E)
+    flat = idx.reshape(-1).long()
+    key = torch.where(flat < 0, torch.full_like(flat, E), flat)
+    order = torch.sort(key, stable=True).indices
+    n = int((flat >= 0).sum())
+    assert torch.equal(offsets.long(), torch.searchsorted(key.sort().values, torch.arange(E + 1, device=DEV)))
+    assert torch.equal(sorted_slot[:n].long(), order[:n]) and (sorted_slot[n:] == -1).all()
+    place = torch.full_like(flat, -1)
+    place[order[:n]] = torch.arange(n, device=DEV)
+    assert torch.equal(slot_pos.reshape(-1).long(), place)
