@@ -189,3 +189,27 @@ def test_empty_product():
     ops = operands(8, 1, 128, 4, 256)
     out = moe.mx4_gemm(ops[0][0], ops[1][0], ops[2][:0], ops[3][:0])
     assert out.shape == (0, 128)
+
+
+@pytest.mark.parametrize("N,M,K", [(73, 256, 1024), (600, 512, 512), (9, 384, 128)])
+def test_operands_written_just_before(N, M, K):
+    """The product's launch overlaps the kernel before it: both operands written by that kernel, in memory that earlier
+    calls have used, and its output read by the next, without a wait between them."""
+    g = torch.Generator(device=DEV).manual_seed(N)
+    xs = [torch.randn(N, K, generator=g, device=DEV) for _ in range(12)]
+    ws = [torch.randn(M, K, generator=g, device=DEV) for _ in range(12)]
+    out = [moe.mx4_gemm(*moe.mxfp4_quantize(w), *moe.mxfp4_quantize(x)) for x, w in zip(xs, ws)]
+    back = [moe.mx4_gemm(*moe.mxfp4_quantize(x), *moe.mxfp4_quantize(w)) for x, w in zip(xs, ws)]
+    again = [moe.mxfp4_quantize(o) for o in out] if M % 32 == 0 else []
+    torch.cuda.synchronize()
+    for i, (x, w) in enumerate(zip(xs, ws)):
+        a, b = moe.mxfp4_quantize(w), moe.mxfp4_quantize(x)
+        torch.cuda.synchronize()
+        ref = moe.mx4_gemm(*a, *b)
+        torch.cuda.synchronize()
+        assert torch.equal(out[i], ref)
+        # the other way round: the same products added in another grouping of rows, the same order of K
+        assert torch.equal(back[i], ref.t())
+        if again:
+            q = moe.mxfp4_quantize(ref)
+            assert torch.equal(again[i][0], q[0]) and torch.equal(again[i][1], q[1])
