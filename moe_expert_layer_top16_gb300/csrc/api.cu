@@ -1716,7 +1716,9 @@ moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t
     if (err != cudaSuccess) return cuda_status(err);
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
     Mx4Params p;
-    mx4_tiles(M, N, G, &p.nt, &p.b_box, &p.pair);
+    err = mx4_pair_clusters(M, N, G, &p.pair_clusters);
+    if (err != cudaSuccess) return cuda_status(err);
+    mx4_tiles(N, G, p.pair_clusters > 0, &p.nt, &p.b_box);
     if (!map_fp4(&p.tmA, a_codes, static_cast<int64_t>(G) * M, K, 128) || !map_fp4(&p.tmB, b_codes, N, K, p.b_box))
         return MOE_ERR_INVALID_ARG;
     // TMA wants rows and addresses of whole 16 bytes

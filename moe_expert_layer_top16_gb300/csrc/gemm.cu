@@ -1075,30 +1075,15 @@ cudaError_t gemm_setup() {
 }
 
 int gemm_pair_clusters() {
-    static int device = -1, clusters = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev == device) return clusters;
-    // the pair kernels run one CTA per SM (their shared memory): how many
-    // two-CTA clusters of the largest configuration are resident at once
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3((2 + 4 * kEpiGroups + 1) * 32);
-    cfg.dynamicSmemBytes = kSmemLimit;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    // one CTA per SM (their shared memory), of the largest configuration
+    static PerDevice counts;
     int n = 0;
-    if (raise_smem<KIND_MX, SET_F32, true>() != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, mx_gemm_kernel<KIND_MX, SET_F32, true>, &cfg) != cudaSuccess)
-        n = 0;
-    device = dev;
-    clusters = n;
-    return clusters;
+    const cudaError_t err = once_a_device(
+        counts, [](int* c) { return resident_pairs(mx_gemm_kernel<KIND_MX, SET_F32, true>, (2 + 4 * kEpiGroups + 1) * 32, kSmemLimit, c); },
+        &n);
+    if (err == cudaSuccess) return n;
+    cudaGetLastError();            // no pairs: not an error of the launches that follow
+    return 0;
 }
 
 cudaError_t launch_gemm(const GemmParams& p, int grid, cudaStream_t s, bool pdl) {

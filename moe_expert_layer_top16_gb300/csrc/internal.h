@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace moe {
@@ -54,6 +55,49 @@ inline cudaError_t launch_ex_cluster(void (*kern)(KArgs...), dim3 grid, dim3 blo
     cfg.attrs = at;
     cfg.numAttrs = pdl ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// A count of each device, asked for once.  Host threads that share nothing
+// else come here, each with a device of its own current: an entry holds the
+// count plus one (0: not known yet) and is published whole.  A query that
+// fails is not kept.
+struct PerDevice {
+    static constexpr int kDevices = 64;
+    std::atomic<int> known[kDevices];
+};
+template <typename Query>
+cudaError_t once_a_device(PerDevice& counts, Query query, int* n) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    std::atomic<int>* at = dev >= 0 && dev < PerDevice::kDevices ? &counts.known[dev] : nullptr;
+    if (const int known = at ? at->load(std::memory_order_relaxed) : 0) {
+        *n = known - 1;
+        return cudaSuccess;
+    }
+    err = query(n);
+    if (err == cudaSuccess && at) at->store(*n + 1, std::memory_order_relaxed);
+    return err;
+}
+
+// Clusters of two CTAs of `kern` that are resident on the device at once, with
+// the largest shared memory that a CTA may have.
+template <typename... KArgs>
+cudaError_t resident_pairs(void (*kern)(KArgs...), int threads, int smem, int* n) {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
 }
 
 // Device status codes (sticky; read by moe_get_device_status).
@@ -370,12 +414,13 @@ struct Mx4Params {
     int dt_out;
     int nt;                     // tokens of a work item at most
     int b_box;                  // rows of a box of B (pairs: half of nt)
-    int pair;                   // on CTA pairs
+    int pair_clusters;          // CTA pairs at most; 0: single CTAs
     int stages, stage_bytes;
 };
-// Token rows of a work item and of a TMA box of B, for `N` rows in G groups,
-// and whether CTA pairs are used.
-void mx4_tiles(int M, int N, int G, int* nt, int* b_box, int* pair);
+// CTA pairs that a product of these sizes may use (0: single CTAs do it).
+cudaError_t mx4_pair_clusters(int M, int N, int G, int* clusters);
+// Token rows of a work item and of a TMA box of B, for `N` rows in G groups.
+void mx4_tiles(int N, int G, bool pair, int* nt, int* b_box);
 cudaError_t launch_mx4_gemm(const Mx4Params& p, cudaStream_t s);
 
 // ------------------------------------------------------------------ tensor-core rate probe (peak.cu)

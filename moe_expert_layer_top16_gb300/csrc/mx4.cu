@@ -822,7 +822,16 @@ int mx4_table_bytes(int G) { return (3 * (G + 1) * 4 + 15) & ~15; }
 
 }  // namespace
 
-void mx4_tiles(int M, int N, int G, int* nt, int* b_box, int* pair) {
+cudaError_t mx4_pair_clusters(int M, int N, int G, int* clusters) {
+    *clusters = 0;
+    if (N < static_cast<int64_t>(kMx4PairRows) * G || M <= kMx4BlockM) return cudaSuccess;
+    // (its instances differ in neither threads nor shared memory, which decide)
+    static PerDevice counts;
+    return once_a_device(
+        counts, [](int* c) { return resident_pairs(mx4_gemm_kernel<ELEM_F32, true, true>, kMx4Threads, kSmemLimit, c); }, clusters);
+}
+
+void mx4_tiles(int N, int G, bool pair, int* nt, int* b_box) {
     if (G == 1) {
         // equal tiles, a box each
         const int tiles = (N + kMx4NtMax - 1) / kMx4NtMax;
@@ -835,14 +844,13 @@ void mx4_tiles(int M, int N, int G, int* nt, int* b_box, int* pair) {
         *b_box = n > 64 ? 32 : 16;
         *nt = static_cast<int>((n + *b_box - 1) / *b_box * *b_box);
     }
-    *pair = N >= static_cast<int64_t>(kMx4PairRows) * G && M > kMx4BlockM;
-    if (*pair) *b_box = *nt / 2;
+    if (pair) *b_box = *nt / 2;
 }
 
 cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
     Mx4Params p = in;
     if (p.M < 1 || p.N < 1 || p.K < 128 || p.K % 128 || p.G < 1 || p.G > kMx4MaxGroups) return cudaErrorInvalidValue;
-    const bool pair = p.pair != 0;
+    const bool pair = p.pair_clusters > 0;
     if (p.nt < 16 || p.nt > kMx4NtMax || p.nt % 16 || (pair ? 2 * p.b_box != p.nt : (p.b_box < 16 || p.nt % p.b_box)))
         return cudaErrorInvalidValue;
     p.stage_bytes = mx4_stage_bytes(p.nt, pair);
@@ -857,7 +865,7 @@ cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     const int64_t m_tiles = (p.M + (pair ? 2 : 1) * kMx4BlockM - 1) / ((pair ? 2 : 1) * kMx4BlockM);
     const int64_t most = m_tiles * ((p.N + p.nt - 1) / p.nt + p.G - 1);
-    const int64_t units = std::min<int64_t>(most, pair ? std::max(1, gemm_pair_clusters()) : sms);
+    const int64_t units = std::min<int64_t>(most, pair ? p.pair_clusters : sms);
     auto run = [&](void (*kern)(Mx4Params)) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;

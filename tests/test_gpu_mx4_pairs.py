@@ -5,6 +5,10 @@ groups whose rows of A end inside a pair's 256.  The bound is test_gpu_mx4's:
 fp16 ends at 65,504: an exact value of 65,520 (half a step further) and more
 rounds to an infinity of its sign, which the random scales reach here and
 there among the millions of values of a case."""
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -73,3 +77,40 @@ def test_not_a_number_stays_in_its_row(K):
     bad[700] = True
     bad[709:, 5] = True
     assert out[bad].isnan().all() and torch.equal(out[~bad], ref[~bad])
+
+
+def threads_first_products():
+    """Several host threads' first products, at once: all paired, each on a stream of its own."""
+    n, M, N, K = 8, 512, 1024, 512
+    ops = [base.operands(i, 1, M, N, K) for i in range(n)]
+    out = [torch.empty(N, M, device=DEV) for _ in range(n)]
+    torch.cuda.synchronize()
+    go, bad = threading.Barrier(n), []
+
+    def one(i):
+        try:
+            side = torch.cuda.Stream()
+            go.wait()
+            for _ in range(3):
+                moe.mx4_gemm(ops[i][0][0], ops[i][1][0], ops[i][2], ops[i][3], out=out[i], stream=side)
+            side.synchronize()
+        except Exception as e:      # noqa: BLE001
+            bad.append(e)
+            go.abort()
+
+    threads = [threading.Thread(target=one, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+    for o, got in zip(ops, out):
+        assert torch.equal(got, moe.mx4_gemm(o[0][0], o[1][0], o[2], o[3]))
+        check(o, [0, N], got, F32, K)
+
+
+def test_first_products_of_several_threads():
+    """In a process of their own: nothing that they share has been asked for yet."""
+    r = subprocess.run([sys.executable, "-c", "import sys; sys.path[:0] = %r; import test_gpu_mx4_pairs as t; t.threads_first_products()"
+                        % (sys.path,)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
