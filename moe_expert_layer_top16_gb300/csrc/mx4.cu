@@ -306,14 +306,15 @@ __device__ __forceinline__ Mx4Item mx4_item(const Mx4Geometry& g, int64_t it) {
 }
 
 // Sixteen scale codes (two stages) of a row, of which `left` codes (a multiple
-// of 4) belong to the row, as words; codes behind the row read as 0.
+// of 4) belong to the row, as words; codes behind the row read as 0.  Plain
+// loads: the kernel before this one, which it overlaps, may have written them.
 __device__ __forceinline__ uint4 load_scales(const uint8_t* at, int left) {
     uint4 r = make_uint4(0, 0, 0, 0);
     const uint32_t* p = reinterpret_cast<const uint32_t*>(at);
-    r.x = __ldg(p);
-    if (left > 4) r.y = __ldg(p + 1);
-    if (left > 8) r.z = __ldg(p + 2);
-    if (left > 12) r.w = __ldg(p + 3);
+    r.x = p[0];
+    if (left > 4) r.y = p[1];
+    if (left > 8) r.z = p[2];
+    if (left > 12) r.w = p[3];
     return r;
 }
 

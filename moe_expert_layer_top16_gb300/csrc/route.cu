@@ -91,8 +91,10 @@ __global__ void __launch_bounds__(512) sort_count_kernel(const int32_t* __restri
     for (int e = threadIdx.x; e < E; e += blockDim.x) counts[static_cast<int64_t>(blockIdx.x) * E + e] = sm[e];
 }
 
+// counts is written by the launch that this one overlaps: plain loads, as the
+// non-coherent path is for memory that nobody writes while the kernel lives.
 __global__ void __launch_bounds__(kSortMaxWarps * 32)
-    sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, const int32_t* __restrict__ counts,
+    sort_kernel(const int32_t* __restrict__ idx, int64_t n, int E, const int32_t* counts,
                 int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_slot, int32_t* __restrict__ slot_pos) {
     extern __shared__ __align__(16) int32_t sm[];
     __shared__ int32_t warp_sum[32];
