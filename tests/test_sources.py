@@ -15,7 +15,7 @@ def code(name):
         return re.sub(r"//[^\n]*", "", f.read())
 
 
-@pytest.mark.parametrize("name", ["gemm.cu", "mx4.cu"])
+@pytest.mark.parametrize("name", UNITS)
 def test_statics_are_safe_to_share(name):
     """A mutable static inside a function is written by whichever host thread comes first, while others read it."""
     plain = [m.group(0).strip() for m in re.finditer(r"^[ \t]+static (?!const |constexpr |__device__)[^;(]*;", code(name), re.M)
