@@ -1722,13 +1722,15 @@ moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t
     if (err != cudaSuccess) return cuda_status(err);
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
     Mx4Params p;
+    p.dt_out = out_dtype;
+    // TMA wants rows and addresses of whole 16 bytes
+    p.sf_tma = K % 512 == 0 && aligned(a_scales, 16) && aligned(b_scales, 16);
     err = mx4_pair_clusters(M, N, G, &p.pair_clusters);
+    if (err == cudaSuccess) err = mx4_setup(p);
     if (err != cudaSuccess) return cuda_status(err);
     mx4_tiles(N, G, p.pair_clusters > 0, &p.nt, &p.b_box);
     if (!map_fp4(&p.tmA, a_codes, static_cast<int64_t>(G) * M, K, 128) || !map_fp4(&p.tmB, b_codes, N, K, p.b_box))
         return MOE_ERR_INVALID_ARG;
-    // TMA wants rows and addresses of whole 16 bytes
-    p.sf_tma = K % 512 == 0 && aligned(a_scales, 16) && aligned(b_scales, 16);
     if (p.sf_tma && (!map_fp4_scales(&p.tmSA, a_scales, static_cast<int64_t>(G) * M, K, 128) ||
                      !map_fp4_scales(&p.tmSB, b_scales, N, K, p.nt)))
         return MOE_ERR_INVALID_ARG;
@@ -1742,7 +1744,6 @@ moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t
     p.M = M;
     p.N = N;
     p.K = K;
-    p.dt_out = out_dtype;
     return cuda_status(launch_mx4_gemm(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -421,6 +421,10 @@ struct Mx4Params {
 cudaError_t mx4_pair_clusters(int M, int N, int G, int* clusters);
 // Token rows of a work item and of a TMA box of B, for `N` rows in G groups.
 void mx4_tiles(int N, int G, bool pair, int* nt, int* b_box);
+// The kernel's shared memory limit, before its descriptors are encoded: a host
+// thread whose first CUDA call this is has no context until the runtime gives it
+// one here, and the encoder, a driver call, wants one.
+cudaError_t mx4_setup(const Mx4Params& p);
 cudaError_t launch_mx4_gemm(const Mx4Params& p, cudaStream_t s);
 
 // ------------------------------------------------------------------ tensor-core rate probe (peak.cu)

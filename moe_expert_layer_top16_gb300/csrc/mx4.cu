@@ -11,7 +11,6 @@
 //              MXFP4, on tcgen05 kind::mxf4 (K = 64 an instruction, twice the
 //              rate of the MXFP8 kind), fp32 accumulation
 #include <algorithm>
-#include <type_traits>
 
 #include "internal.h"
 #include "mx.cuh"
@@ -817,6 +816,16 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_gemm_kernel(const __grid_c
     }
 }
 
+template <bool SFT, bool PAIR>
+auto mx4_kernel_as(int dt_out) {
+    return dt_out == ELEM_F32 ? mx4_gemm_kernel<ELEM_F32, SFT, PAIR>
+                              : (dt_out == ELEM_BF16 ? mx4_gemm_kernel<ELEM_BF16, SFT, PAIR> : mx4_gemm_kernel<ELEM_F16, SFT, PAIR>);
+}
+auto mx4_kernel(int dt_out, bool sf_tma, bool pair) {
+    if (pair) return sf_tma ? mx4_kernel_as<true, true>(dt_out) : mx4_kernel_as<false, true>(dt_out);
+    return sf_tma ? mx4_kernel_as<true, false>(dt_out) : mx4_kernel_as<false, false>(dt_out);
+}
+
 int mx4_stage_bytes(int nt, bool pair) { return (kMx4ABytes + (pair ? nt / 2 : nt) * 128 + 1023) & ~1023; }
 
 int mx4_table_bytes(int G) { return (3 * (G + 1) * 4 + 15) & ~15; }
@@ -830,6 +839,11 @@ cudaError_t mx4_pair_clusters(int M, int N, int G, int* clusters) {
     static PerDevice counts;
     return once_a_device(
         counts, [](int* c) { return resident_pairs(mx4_gemm_kernel<ELEM_F32, true, true>, kMx4Threads, kSmemLimit, c); }, clusters);
+}
+
+cudaError_t mx4_setup(const Mx4Params& p) {
+    return cudaFuncSetAttribute(mx4_kernel(p.dt_out, p.sf_tma, p.pair_clusters > 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmemLimit);
 }
 
 void mx4_tiles(int N, int G, bool pair, int* nt, int* b_box) {
@@ -867,21 +881,10 @@ cudaError_t launch_mx4_gemm(const Mx4Params& in, cudaStream_t s) {
     const int64_t m_tiles = (p.M + (pair ? 2 : 1) * kMx4BlockM - 1) / ((pair ? 2 : 1) * kMx4BlockM);
     const int64_t most = m_tiles * ((p.N + p.nt - 1) / p.nt + p.G - 1);
     const int64_t units = std::min<int64_t>(most, pair ? p.pair_clusters : sms);
-    auto run = [&](void (*kern)(Mx4Params)) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-        if (e != cudaSuccess) return e;
-        if (pair)
-            return launch_ex_cluster(kern, dim3(static_cast<unsigned>(2 * units)), dim3(kMx4Threads), smem, s, true, 2, p);
-        return launch_ex(kern, dim3(static_cast<unsigned>(units)), dim3(kMx4Threads), smem, s, true, p);
-    };
-    auto with = [&](auto sft, auto paired) {
-        constexpr bool SFT = decltype(sft)::value, PAIR = decltype(paired)::value;
-        if (p.dt_out == ELEM_F32) return run(mx4_gemm_kernel<ELEM_F32, SFT, PAIR>);
-        if (p.dt_out == ELEM_BF16) return run(mx4_gemm_kernel<ELEM_BF16, SFT, PAIR>);
-        return run(mx4_gemm_kernel<ELEM_F16, SFT, PAIR>);
-    };
-    if (pair) return p.sf_tma ? with(std::true_type{}, std::true_type{}) : with(std::false_type{}, std::true_type{});
-    return p.sf_tma ? with(std::true_type{}, std::false_type{}) : with(std::false_type{}, std::false_type{});
+    void (*kern)(Mx4Params) = mx4_kernel(p.dt_out, p.sf_tma, pair);
+    if (pair)
+        return launch_ex_cluster(kern, dim3(static_cast<unsigned>(2 * units)), dim3(kMx4Threads), smem, s, true, 2, p);
+    return launch_ex(kern, dim3(static_cast<unsigned>(units)), dim3(kMx4Threads), smem, s, true, p);
 }
 
 namespace {
