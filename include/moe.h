@@ -502,8 +502,8 @@ MOE_API moe_status moe_mxfp4_decode(const uint8_t *codes, const uint8_t *scales,
  * out [N][M] of out_dtype with row stride ld_out.  offsets: device int32
  * [G + 1], ascending, as moe_sort writes them (values are kept inside [0, N]);
  * NULL with G = 1: all rows.  Rows outside [offsets[0], offsets[G]) are left
- * as they were.  M >= 1, N >= 0, K a multiple of 128, 1 <= G <= 1024,
- * G M <= 2^31 - 256.  dev_status (device int32, optional) receives a non-zero code if
+ * as they were.  M >= 1, 0 <= N <= 2^31 - 256, K a multiple of 128 up to
+ * 2^24, 1 <= G <= 1024, G M <= 2^31 - 256.  dev_status (device int32, optional) receives a non-zero code if
  * a bounded wait inside the kernel ran out, as with moe_mx_gemm.  A device of
  * compute capability 10.3 is needed. */
 MOE_API moe_status moe_mx4_gemm(const uint8_t *a_codes, const uint8_t *a_scales, int32_t G, int32_t M,

@@ -1482,6 +1482,10 @@ bool slots_ok(int32_t T, int32_t k) {
 
 constexpr int kMaxColumns = 1 << 30;             // column numbers a chunk ahead stay inside 32 bits
 
+// K of a four-bit product: its loop over K, which one of the kernel's bounded
+// waits covers, takes some 20 ms at most.
+constexpr int kMx4MaxK = 1 << 24;
+
 // Elements of a quantised matrix: their number fits 63 bits with room.
 bool blocks_ok(int64_t rows, int64_t K) {
     return rows >= 0 && K > 0 && K % 32 == 0 && rows <= (int64_t(1) << 48) / K;
@@ -1706,7 +1710,8 @@ moe_status moe_mxfp4_decode(const uint8_t* codes, const uint8_t* scales, int64_t
 moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t G, int32_t M, const uint8_t* b_codes,
                         const uint8_t* b_scales, int32_t N, int32_t K, const int32_t* offsets, void* out,
                         int64_t ld_out, int32_t out_dtype, int32_t* dev_status, void* stream) {
-    if (G < 1 || G > 1024 || M < 1 || N < 0 || K < 128 || K % 128 || static_cast<int64_t>(G) * M > 0x7fffff00 ||
+    if (G < 1 || G > 1024 || M < 1 || N < 0 || N > 0x7fffff00 || K < 128 || K > kMx4MaxK || K % 128 ||
+        static_cast<int64_t>(G) * M > 0x7fffff00 ||
         !known_dtype(out_dtype) || (!offsets && G != 1))
         return MOE_ERR_INVALID_ARG;
     if (N == 0) return MOE_OK;

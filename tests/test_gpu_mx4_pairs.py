@@ -114,3 +114,16 @@ def test_first_products_of_several_threads():
     r = subprocess.run([sys.executable, "-c", "import sys; sys.path[:0] = %r; import test_gpu_mx4_pairs as t; t.threads_first_products()"
                         % (sys.path,)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_longest_k():
+    """K = 2^24, the largest: sums of ones, which fp32 adds exactly, and of the last element alone."""
+    K, M, N = 2 ** 24, 3, 2
+    one = torch.full((M, K // 2), 0x22, dtype=torch.uint8, device=DEV)
+    b = torch.full((N, K // 2), 0x22, dtype=torch.uint8, device=DEV)
+    b[1] = 0
+    b[1, -1] = 0x70                                        # 6 in the last place
+    scales = torch.full((M, K // 32), 127, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = moe.mx4_gemm(one, scales, b, scales[:N], status=status)
+    assert status.item() == 0 and out.tolist() == [[2.0 ** 24] * M, [6.0] * M]

@@ -176,3 +176,13 @@ def test_stream_of_another_kind():
         with pytest.raises(moe.MoeError):
             block._int32(n, "x")
     block._int32(2 ** 31 - 1, "x")
+
+
+def test_four_bit_product_behind_its_last_sizes(L):
+    """K and N whose tile counts would leave 32 bits: 2^31 - 128 gave a negative number of stages, and with it an
+    output that no product had been written to."""
+    good = [P, P, 1, 1, P, P, 1, 128, None, P, 1, 0, None, None]
+    for i, v in ((7, 2 ** 31 - 128), (7, 2 ** 24 + 128), (6, 2 ** 31 - 1), (6, 2 ** 31 - 255)):
+        args = list(good)
+        args[i] = v
+        assert L.moe_mx4_gemm(*args) == BAD, (i, v)
