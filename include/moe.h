@@ -348,10 +348,23 @@ MOE_API moe_status moe_mx_gemm_noalloc(const uint8_t *a_codes, const uint8_t *a_
  * elements (moe_permute: in bytes); a row's elements are contiguous.  Element
  * types are moe_dtype values; every sum, norm and gradient is accumulated in
  * fp32 and rounded once (to nearest even) when it is stored.  Sums run in a
- * fixed order, so that results do not change from call to call.  Rows whose
- * address and stride are multiples of 16 bytes and whose length is a multiple
- * of 8 elements go by in 16-byte words, others element by element.  Outputs
- * must not overlap inputs except where a call says so. */
+ * fixed order, so that results do not change from call to call.  Where a call
+ * does not ask for more, any address that is a multiple of the element's size
+ * and any stride of at least a row will do; they decide how the rows go by:
+ *   moe_permute     in the widest word, of 16 bytes at most, that addresses,
+ *                   strides and the row's length are multiples of
+ *   moe_unpermute   and its gradients: by 16 bytes where addresses and strides
+ *                   are multiples of 16 bytes and D is one of 8, else element
+ *                   by element
+ *   the norms       by 16 bytes, rows of any length among them, where every
+ *                   matrix's address is a multiple of 16 bytes and their
+ *                   strides are equal modulo 8 elements (4 if x is fp32; in
+ *                   the gradients, if every matrix is there and fp32), else
+ *                   element by element, which takes two to eleven times as long
+ *   quantise,       by 16 bytes where x's address and stride are multiples of
+ *   decode          16 bytes, else element by element
+ * Outputs must not overlap inputs except where a call says so.  Host threads
+ * may call at once, each on a stream of its own. */
 typedef enum {
     MOE_DTYPE_F32 = 0,
     MOE_DTYPE_BF16 = 1,
@@ -412,7 +425,9 @@ MOE_API moe_status moe_unpermute_backward(const void *dy, int64_t ld_dy, int32_t
  * the gate are not used).  u = NULL: only h.  w_post / w_pre = NULL: ones.
  * The gate is a value a channel ([D]), a value a token ([T]), or absent.
  * Weights and gate share one type.  h has x's type and may be x itself (same
- * address and stride).  0 <= T <= 2^30, 1 <= D <= 16384, eps >= 0. */
+ * address and stride).  Squares are taken in fp32: values of magnitude above
+ * 10^17 overflow, and with eps = 0 those below 10^-18 lose digits.
+ * 0 <= T <= 2^30, 1 <= D <= 16384, eps >= 0. */
 typedef enum {
     MOE_GATE_NONE = 0,
     MOE_GATE_CHANNEL = 1,

@@ -13,7 +13,6 @@
 #include <algorithm>
 
 #include "internal.h"
-#include "mx.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
 
@@ -240,14 +239,19 @@ __global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __rest
 // of both; copies and scale writes of both count on its barriers, its commits
 // arrive on both CTAs'.
 //
-// What bounds it: shared memory's 128 bytes a cycle.  A paired stage (256 x 192
-// x 256) moves 28 KB in by TMA, out again to the MMAs, and 11 KB of scales, 540
-// cycles of the 590 that it takes; the MMAs alone would take 417 (9.5 PFLOP/s,
-// measured with operands that stay).  8,192 x 8,192 x 7,168: 153 us, 6.3
-// PFLOP/s.  Items of 208 rows, the scales' columns written by two groups of
-// warps or two stages at a time changed that by less than 2%, or for the worse.
+// 8,192 x 8,192 x 7,168 takes 153 us, 6.3 PFLOP/s, with the tensor pipe active
+// 66% of the launch (the MMAs' 102 us); K = 14,336 295, so that 28 stages more an
+// item cost 141.  What bounds a stage is not settled.  Paired (256 x 192 x 256)
+// it moves 28 KB in by TMA, out again to the MMAs, and 11 KB of scales: some 540
+// cycles at 128 bytes a cycle, more than the MMAs need.  But items of 208 rows,
+// two rounds of items fewer, gained less than 2%, as did the scales' columns
+// written by two groups of warps or two stages at a time, or lost.  1,376 items
+// on 76 pairs are 18.1 rounds: the last holds eight items, 4% of the time.  Few stages an item are bound by the epilogue: an
+// output of 8,192 x 8,192 takes 118 us at K = 512 and 137 at 3,584, in bf16 and in
+// fp32.  Gathered scales: K = 7,040 235 us, 3,456 147; 64 groups of 146 rows (M
+// = 1,024) 38 us at K = 3,456, 36 at 3,584.
 // Decode (73 rows for 64 groups of 1,024 x 3,584) is bound by the weights' way
-// from HBM: 21 us for 85 MB.
+// from HBM: 20 us for 85 MB; at K = 3,456 28.
 //
 // Unpaired, 41 KB of operands a stage came into an SM at
 // 64 bytes a cycle, which bounded the product; a pair's CTA takes 28 KB.  Groups

@@ -17,8 +17,10 @@
 // in shared memory (a ring that cp.async fills some rows ahead), so that the
 // sums over the row (of y^2, then of h^2) need no second read.  All sums are
 // fp32.  Measured: 8,192 x 7,168 bf16 81 us (470 MB, 5.8 TB/s; 69 us at the
-// rate of a plain copy), fp32 163 (139); 64 rows of bf16 with y in
-// fp32 5 us, which is the launch, two trips to memory and two sums in turn.
+// rate of a plain copy), fp32 163 (139), bf16 with y in fp32 118 (87); 2,048 x
+// 16,384 fp32, split over two blocks, 90 (79); 64 rows of bf16 with y in fp32 5
+// us, which is the launch, two trips to memory and two sums in turn.  Element by
+// element (bases off 16 bytes) 8,192 x 7,168 bf16 361, fp32 382.
 #include "norm.cuh"
 
 namespace moe {
@@ -204,8 +206,9 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
-    // the window, and so the order of a row's sums, goes by x's type alone: a
-    // fused call and its two parts give the same bits
+    // the window goes by x's type alone: where the matrices lie alike, at equal
+    // strides, a fused call and its two parts sum a row in the same order and
+    // give the same bits
     const int ty = a.y ? a.dt_y : a.dt_x, tu = a.u ? a.dt_u : a.dt_x;
     int kind = NORM_RUN;
     if (a.dt_x == ELEM_F32) kind = ty == ELEM_F32 ? NORM_F32 : NORM_F32_Y16;
@@ -222,8 +225,12 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
     // fp32 21 and 24).  Two groups a block overlap the one's sums with the
     // other's loads and stores; many whole rows of 448 windows or more are
     // better off with one group and a ring of four rows (8,192 x 7,168 bf16 81.5
-    // and 84 us, 4,096 fp32 82.5 and 95; of 1,024 rows 15.3 and 13).  Odd rows
-    // are better off with two groups than with a third row (7,167 48 and 63).
+    // and 84.6 us, 4,096 fp32 80.5 and 94.5; of 1,024 rows 15.3 and 12.9).  Near
+    // the rule's borders the two are within 5%, or 10% for the widest: four rows
+    // and three, 8,192 x 3,456 bf16 38.5 and 40.3, 3,584 40.7 and 40.8; 4,560 x
+    // 7,168 bf16 48.4 and 46.8, 4,864 51.1 and 49.4; 4,560 x 4,096 fp32 48.0 and
+    // 52.1, 4,864 50.6 and 56.6.  Odd rows are better off with two groups than
+    // with a third row (7,167 48 and 63).
     const bool mixed = a.dt_x != ELEM_F32 && ty == ELEM_F32, whole_row = !al.odd && a.D % W == 0;
     const int deep = mixed || !whole_row ? 2 : (a.D >= 448 * W && a.T >= 32 * static_cast<int64_t>(sms) ? 4 : 3);
     if (shape_of(a.T, a.D, al, slots, Rule{64, 1024, 1024, 1024, 64, deep, 1, kNormMaxSplit, W == 4 ? 2 : 3}, sms, 1 << 30, &sh)) {

@@ -54,9 +54,13 @@ __device__ __forceinline__ void group_sums4(float (&v)[4], const Rows& g, float 
 // sums over row t + 1 that its norms need are taken together with the one over
 // row t that its dy needs: one barrier a row, and the work of both before it.
 // What bounds it: HBM for whole rows (4,096 x 7,168 bf16 62 us, 352 MB, 5.7
-// TB/s; 52 us at the rate of a plain copy; fp32, split over two blocks, 111 and
+// TB/s; 52 us at the rate of a plain copy; fp32, split over two blocks, 113 and
 // 104); for rows of odd lengths the few warps that mask partial windows (4,096
-// x 7,167 bf16 99).
+// x 7,167 bf16 99).  Calls without dh, du or y, or with du of another type than
+// h, take the instance whose types are looked up at run time and whose registers
+// spill: 4,096 x 7,168 bf16 without y 118 us (35), without du 121 (35), without dh
+// 152 (43); fp32 with du in bf16 430 (95).  Element by element, bases off 16
+// bytes: bf16 688, fp32 539.
 template <int NV, int MAXT, bool EDGE, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(const NormBackArgs a, int tpr, int stages,
                                                                    const Steps st) {

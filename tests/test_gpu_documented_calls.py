@@ -197,3 +197,41 @@ def test_numpy_is_not_a_tensor():
         with pytest.raises(moe.MoeError) as e:
             f()
         assert e.value.code == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("T,D", [(5, 264), (3, 16384), (9, 1001)])
+@pytest.mark.parametrize("size,eps", [(1e17, 1e-6), (1e17, 0.0), (1e-17, 0.0)])
+@pytest.mark.parametrize("t", [F32, BF16])
+def test_norms_of_large_and_small_values(T, D, size, eps, t):
+    """The magnitudes that moe.h names, 10^-18 to 10^17: within the usual bounds of the formulas in 64 bits."""
+    g = torch.Generator(device=DEV).manual_seed(D)
+    v = lambda *s: ((0.1 + 0.89 * torch.rand(*s, generator=g, device=DEV)) *      # noqa: E731
+                    torch.where(torch.rand(*s, generator=g, device=DEV) < 0.5, -1.0, 1.0))
+    x, y, du, dh = (v(T, D) * size).to(t), (v(T, D) * size).to(t), v(T, D).to(t), v(T, D).to(t)
+    w = v(D)
+    assert float(torch.maximum(x.abs().max(), y.abs().max())) <= 1e17 and float(torch.minimum(x.abs().min(), y.abs().min())) >= 9e-19
+    rms = lambda a: (a.square().mean(-1, keepdim=True) + eps).sqrt()      # noqa: E731
+    c = (D / 64 + 24) * 2.0 ** -24
+    xd, yd, wd = x.double(), y.double(), w.double()
+    h, u = moe.block_norm(x, y, w_post=w, w_pre=w, res_scale=0.75, eps=eps)
+    add = wd * yd / rms(yd)
+    ref = 0.75 * xd + add
+    tol = add.abs() * c + ref.abs() * 2.0 ** -23
+    assert ((h.double() - ref).abs() <= tol + (ref.abs() + tol) * base.HALF[t]).all()
+    # the norm alone, of values of that size
+    _, u = moe.block_norm(x, w_pre=w, eps=eps)
+    ref = wd * xd / rms(xd)
+    assert ((u.double() - ref).abs() <= ref.abs() * (c + base.HALF[t] * (1 + c))).all()
+    got = moe.block_norm_backward(dh, du, x, y, w_post=w, w_pre=w, res_scale=0.75, eps=eps)
+    a, hh = du.double() * wd, xd / rms(xd)
+    total = dh.double() + (a - hh * (a * hh).mean(-1, keepdim=True)) / rms(xd)
+    mag = dh.double().abs() + (a.abs() + hh.abs() * (a * hh).abs().mean(-1, keepdim=True)) / rms(xd)
+    ref = 0.75 * total
+    assert ((got["dx"].double() - ref).abs() <= mag * c + (ref.abs() + mag * c) * base.HALF[t]).all()
+    yh, p, pm = yd / rms(yd), total * wd, mag * wd.abs()
+    ref = (p - yh * (p * yh).mean(-1, keepdim=True)) / rms(yd)
+    m = (pm + yh.abs() * (pm * yh.abs()).mean(-1, keepdim=True)) / rms(yd)
+    keep = ref.abs() < 1e38                               # what the gradient's type holds
+    assert ((got["dy"].double() - ref).abs() <= m * 2 * c + (ref.abs() + m * 2 * c) * base.HALF[t] + norms.TINY[t])[keep].all()
+    terms, tm = (total * yh).sum(0), (mag * yh.abs()).sum(0)
+    assert ((got["dw_post"].double() - terms).abs() <= tm * (2 * c + (T + 24) * 2.0 ** -24)).all()
