@@ -59,3 +59,61 @@ def test_products_of_reused_operands(N, M, K):
         q = moe.mxfp4_quantize(x)
         torch.cuda.synchronize()
         assert torch.equal(o, moe.mx4_gemm(*w, *q))
+
+
+CASES = ["alone", "kernel before the wait", "copy after the wait", "memset after the wait", "kernel after the wait"]
+
+
+def prepared(kind):
+    """An operator's call, its inputs and what it gives for them."""
+    g = torch.Generator(device=DEV).manual_seed(len(kind))
+    x, w = torch.randn(600, 1024, generator=g, device=DEV), torch.randn(512, 1024, generator=g, device=DEV)
+    a, idx = moe.mxfp4_quantize(w), torch.randint(0, 61, (3000, 7), generator=g, device=DEV, dtype=torch.int32)
+    call = {"product": lambda c, s, i, v: [moe.mx4_gemm(*a, c, s)], "sort": lambda c, s, i, v: moe.sort_by_expert(i, 61),
+            "quantise": lambda c, s, i, v: moe.mxfp4_quantize(v),
+            "gradients": lambda c, s, i, v: [moe.block_norm_backward(v, v, v, v, w_post=v[0], w_pre=v[1])["dw_post"]]}[kind]
+    inputs = (*moe.mxfp4_quantize(x), idx, x)
+    return call, inputs, [t.clone() for t in call(*inputs)]
+
+
+def behind(call, inputs, late, other, case, cycles):
+    """The call on `late`, which another stream fills from `inputs` after so many cycles, behind a wait for that stream."""
+    main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    side.wait_stream(main)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(cycles)
+        for t, v in zip(late, inputs):
+            t.copy_(v)
+    if case == "kernel before the wait":
+        moe.mxfp4_quantize(other)                 # which lets its successor start early
+    main.wait_stream(side)
+    if case == "copy after the wait":
+        other.copy_(other * 2)
+    if case == "memset after the wait":
+        other.zero_()
+    if case == "kernel after the wait":
+        moe.mxfp4_quantize(other)
+    return call(*late)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("kind", ["product", "sort", "quantise", "gradients"])
+@pytest.mark.parametrize("case", CASES)
+def test_behind_another_streams_work(kind, case, captured):
+    """Eager, and as nodes of a graph whose launch depends on two others."""
+    call, inputs, want = prepared(kind)
+    late, other = [torch.full_like(t, 3) for t in inputs], torch.randn(64, 1024, device=DEV)
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = behind(call, inputs, late, other, case, 2_000_000)
+    for _ in range(2):
+        for t in late:
+            t.fill_(3)
+        if captured:
+            graph.replay()
+        else:
+            got = behind(call, inputs, late, other, case, 20_000_000)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
