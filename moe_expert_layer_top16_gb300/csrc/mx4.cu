@@ -246,10 +246,11 @@ __global__ void __launch_bounds__(256) mxfp4_decode_kernel(const uint8_t* __rest
 // cycles at 128 bytes a cycle, more than the MMAs need.  But items of 208 rows,
 // two rounds of items fewer, gained less than 2%, as did the scales' columns
 // written by two groups of warps or two stages at a time, or lost.  1,376 items
-// on 76 pairs are 18.1 rounds: the last holds eight items, 4% of the time.  Few stages an item are bound by the epilogue: an
-// output of 8,192 x 8,192 takes 118 us at K = 512 and 137 at 3,584, in bf16 and in
-// fp32.  Gathered scales: K = 7,040 235 us, 3,456 147; 64 groups of 146 rows (M
-// = 1,024) 38 us at K = 3,456, 36 at 3,584.
+// on 76 pairs are 18.1 rounds: the last holds eight items, 4% of the time.
+// Items of few stages are bound by the epilogue: an output of 8,192 x 8,192 takes
+// 118 us at K = 512 and 137 at 3,584, in bf16 and in fp32.  Gathered scales: K =
+// 7,040 235 us, 3,456 147; 64 groups of 146 rows (M = 1,024) 38 us at K = 3,456,
+// 36 at 3,584.
 // Decode (73 rows for 64 groups of 1,024 x 3,584) is bound by the weights' way
 // from HBM: 20 us for 85 MB; at K = 3,456 28.
 //
