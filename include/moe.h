@@ -526,6 +526,93 @@ MOE_API moe_status moe_mx4_gemm(const uint8_t *a_codes, const uint8_t *a_scales,
                                 const int32_t *offsets, void *out, int64_t ld_out, int32_t out_dtype,
                                 int32_t *dev_status, void *stream);
 
+/* The router as operators of their own.  logits [T][E] of any moe_dtype, row
+ * stride ld_logits in elements; they go by 16 bytes where the address and the
+ * stride are multiples of 16 bytes and E is one of 8, else element by element.
+ * 1 <= k <= 32, k <= E <= 1024, T >= 0.  score_fn is a moe_score_fn.  A logit
+ * of minus infinity or NaN closes the expert for the token (no score, no
+ * gradient); plus infinity counts as the largest finite number.
+ *
+ * Selection: the k experts with the largest keys in descending order, equal
+ * keys by the lower expert.  The key is the logit; with a bias (sigmoid only)
+ * it is sigmoid(l_e) + bias[e] in 64 bits, and a bias of minus infinity or NaN
+ * closes the expert for every token (plus infinity counts as the largest
+ * number).  Gates, in slot order:
+ *   normalize != 0   scale s_j / sum of the winners' s, with s = sigmoid(l)
+ *                    (MOE_SCORE_SIGMOID_BIAS) or e^l (MOE_SCORE_SOFTMAX);
+ *                    nothing underflows, whatever the logits
+ *   normalize == 0   scale sigmoid(l_j), or scale e^l_j / sum over all E of e^l
+ * A token with fewer than k open experts has idx -1 and gate 0 in the slots
+ * behind them; a token whose mask is 0 has them in all.  moe_sort takes such
+ * slots as dropped. */
+typedef struct {
+    const void *logits;
+    int64_t ld_logits;
+    const float *bias;        /* [E], or NULL */
+    const uint8_t *mask;      /* [T], or NULL: every token is routed */
+    int32_t *idx;             /* [T][k] */
+    float *gates;             /* [T][k] */
+    int32_t T, E, k;
+    int32_t dtype;            /* of the logits */
+    int32_t score_fn, normalize;
+    float scale;
+} moe_select_args;
+MOE_API moe_status moe_select(const moe_select_args *args, void *stream);
+
+/* Balance loss and per-expert counts.  sequences: device int32 [S + 1],
+ * ascending, sequence s is rows [sequences[s], sequences[s + 1]) (values are
+ * kept inside [0, T]); NULL with S = 1: all rows.  idx [T][k] as moe_select
+ * writes it; entries outside [0, E) are dropped slots, and a token whose slots
+ * are all dropped is not counted.  With p_te the share of expert e in the
+ * scores of token t (s_te / sum_e s_te, s as above) and n_s the counted tokens:
+ *   counts[s][e] = slots of the sequence that name e      tokens[s] = n_s
+ *   loss[s] = E / (k n_s) sum_e counts[s][e] mean_t p_te   (0 without tokens)
+ * which is 1 if counts or shares are even.  A mean over sequences, or a weight,
+ * is the caller's.  `workspace` (16-byte aligned) holds
+ * moe_balance_loss_workspace_bytes(T, E, S) bytes; calls that overlap need one
+ * each.  1 <= S <= 2^20. */
+typedef struct {
+    const void *logits;
+    int64_t ld_logits;
+    const int32_t *idx;       /* [T][k] */
+    const int32_t *sequences; /* [S + 1], or NULL */
+    float *loss;              /* [S] */
+    int32_t *counts;          /* [S][E] */
+    int32_t *tokens;          /* [S] */
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t T, E, k, S;
+    int32_t dtype, score_fn;
+} moe_balance_loss_args;
+MOE_API size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E, int32_t S);
+MOE_API moe_status moe_balance_loss(const moe_balance_loss_args *args, void *stream);
+
+/* Gradient with respect to the logits of the gates (d_gates [T][k], NULL:
+ * none), of the losses (d_loss [S], NULL: none; counts, tokens and sequences
+ * as moe_balance_loss had and wrote them), or of both, in one pass:
+ *   r_e = 1 - sigmoid(l_e) for sigmoid scores, 1 for softmax;  g = scale d_gates
+ *   gates   normalize != 0   w_j r_j (g_j - sum_i g_i w_i)   w: gates / scale
+ *           normalize == 0   g_j s_j r_j; softmax p_e (g_e - sum_i g_i p_i)
+ *   losses  p_e r_e (a_e - sum_i p_i a_i)   a_e = d_loss E counts[e] / (k n^2)
+ * The selection itself has no gradient, nor has the bias.  d_logits [T][E] of
+ * the logits' type, all of it written (0 for tokens that nothing counts); it
+ * may be logits itself (same address and stride).  An expert that two slots of
+ * a token name gets both. */
+typedef struct {
+    const void *logits;
+    int64_t ld_logits;
+    const int32_t *idx;
+    const float *d_gates;
+    const float *d_loss;
+    const int32_t *counts, *tokens, *sequences;
+    void *d_logits;
+    int64_t ld_d_logits;
+    int32_t T, E, k, S;
+    int32_t dtype, score_fn, normalize;
+    float scale;
+} moe_router_backward_args;
+MOE_API moe_status moe_router_backward(const moe_router_backward_args *args, void *stream);
+
 /* One block of a model round the layer: the norm before it, the layer, and
  * the norm behind it with gate and residual scale (and, with next_w_pre or
  * next_u, the norm before the next block):

@@ -37,7 +37,8 @@ ENTRY_POINTS = ("moe_plan", "moe_forward", "moe_forward_host", "moe_get_device_s
                 "moe_mx_gemm_noalloc", "moe_sort", "moe_sort_workspace_bytes", "moe_permute", "moe_unpermute",
                 "moe_unpermute_backward",
                 "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward", "moe_mxfp4_quantize",
-                "moe_mxfp4_decode", "moe_mx4_gemm", "moe_forward_block")
+                "moe_mxfp4_decode", "moe_mx4_gemm", "moe_forward_block", "moe_select", "moe_balance_loss",
+                "moe_balance_loss_workspace_bytes", "moe_router_backward")
 
 
 class MoeError(RuntimeError):
@@ -125,8 +126,9 @@ def lib(build_if_missing: bool = False):
             L.moe_mma_probe.argtypes = [i32, i32, i32, P, C.POINTER(C.c_double), P]
             L.moe_mx_gemm_noalloc.restype = C.c_int
             L.moe_mx_gemm_noalloc.argtypes = [P, P, i32, P, P, i32, i32, P, P, P]
-            from . import block
+            from . import block, router
             block.declare(L)
+            router.declare(L)
             _lib = L
     return _lib
 
@@ -401,3 +403,4 @@ def debug_buffers(cfg, T: int, device, fields=DEBUG_FIELDS) -> dict:
 from . import block  # noqa: E402
 from .block import (block_norm, block_norm_backward, mx4_gemm, mxfp4_decode, mxfp4_quantize, permute,  # noqa: E402,F401
                     permute_backward, sort_by_expert, unpermute, unpermute_backward)
+from .router import balance_loss, router_backward, select_experts  # noqa: E402,F401

@@ -1491,6 +1491,13 @@ bool blocks_ok(int64_t rows, int64_t K) {
     return rows >= 0 && K > 0 && K % 32 == 0 && rows <= (int64_t(1) << 48) / K;
 }
 
+// Sizes and kinds of the router's operators.
+constexpr int kMaxSequences = 1 << 20;
+bool router_ok(int32_t T, int32_t E, int32_t k, int32_t dtype, int32_t score_fn) {
+    return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= 32 && k <= E && known_dtype(dtype) &&
+           (score_fn == MOE_SCORE_SIGMOID_BIAS || score_fn == MOE_SCORE_SOFTMAX);
+}
+
 // MXFP4 codes [rows][K / 2] as bytes, boxes of 128 bytes (256 elements) x box_rows.
 bool map_fp4(CUtensorMap* m, const void* codes, int64_t rows, int64_t K, int box_rows) {
     EncodeTiledFn f = encode_fn();
@@ -1750,6 +1757,94 @@ moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t
     p.N = N;
     p.K = K;
     return cuda_status(launch_mx4_gemm(p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_select(const moe_select_args* p, void* stream) {
+    if (!p || !router_ok(p->T, p->E, p->k, p->dtype, p->score_fn)) return MOE_ERR_INVALID_ARG;
+    if (p->bias && p->score_fn != MOE_SCORE_SIGMOID_BIAS) return MOE_ERR_INVALID_ARG;
+    if (p->T == 0) return MOE_OK;
+    if (!matrix_ok(p->logits, p->ld_logits, p->dtype, p->E) || !aligned(p->bias, 4) || !p->idx || !aligned(p->idx, 4) ||
+        !p->gates || !aligned(p->gates, 4))
+        return MOE_ERR_INVALID_ARG;
+    SelectArgs a = {};
+    a.logits = p->logits;
+    a.ld = p->ld_logits;
+    a.T = p->T;
+    a.bias = p->bias;
+    a.mask = p->mask;
+    a.idx = p->idx;
+    a.gates = p->gates;
+    a.E = p->E;
+    a.k = p->k;
+    a.dt = p->dtype;
+    a.sigmoid = p->score_fn == MOE_SCORE_SIGMOID_BIAS;
+    a.normalize = p->normalize;
+    a.scale = p->scale;
+    return cuda_status(launch_select(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t E, int32_t S) {
+    if (T < 0 || E < 1 || E > 1024 || S < 1 || S > kMaxSequences) return 0;
+    return balance_workspace_bytes(T, E, S);
+}
+
+moe_status moe_balance_loss(const moe_balance_loss_args* p, void* stream) {
+    if (!p || !router_ok(p->T, p->E, p->k, p->dtype, p->score_fn)) return MOE_ERR_INVALID_ARG;
+    if (p->S < 1 || p->S > kMaxSequences || (!p->sequences && p->S != 1) || !aligned(p->sequences, 4)) return MOE_ERR_INVALID_ARG;
+    if (!p->loss || !aligned(p->loss, 4) || !p->counts || !aligned(p->counts, 4) || !p->tokens || !aligned(p->tokens, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (p->T > 0 && (!matrix_ok(p->logits, p->ld_logits, p->dtype, p->E) || !p->idx || !aligned(p->idx, 4) || !p->workspace ||
+                     !aligned(p->workspace, 16) || p->workspace_bytes < balance_workspace_bytes(p->T, p->E, p->S)))
+        return MOE_ERR_INVALID_ARG;
+    BalanceArgs a = {};
+    a.logits = p->logits;
+    a.ld = p->ld_logits;
+    a.T = p->T;
+    a.idx = p->idx;
+    a.seq = p->sequences;
+    a.loss = p->loss;
+    a.counts = p->counts;
+    a.tokens = p->tokens;
+    a.part = static_cast<float*>(p->workspace);
+    a.E = p->E;
+    a.k = p->k;
+    a.S = p->S;
+    a.dt = p->dtype;
+    a.sigmoid = p->score_fn == MOE_SCORE_SIGMOID_BIAS;
+    return cuda_status(launch_balance(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_router_backward(const moe_router_backward_args* p, void* stream) {
+    if (!p || !router_ok(p->T, p->E, p->k, p->dtype, p->score_fn) || (!p->d_gates && !p->d_loss)) return MOE_ERR_INVALID_ARG;
+    if (p->d_loss && (p->S < 1 || p->S > kMaxSequences || (!p->sequences && p->S != 1) || !p->counts || !p->tokens))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(p->d_gates, 4) || !aligned(p->d_loss, 4) || !aligned(p->counts, 4) || !aligned(p->tokens, 4) ||
+        !aligned(p->sequences, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (p->T == 0) return MOE_OK;
+    if (!matrix_ok(p->logits, p->ld_logits, p->dtype, p->E) || !p->idx || !aligned(p->idx, 4) ||
+        !matrix_ok(p->d_logits, p->ld_d_logits, p->dtype, p->E))
+        return MOE_ERR_INVALID_ARG;
+    RouterBackArgs a = {};
+    a.logits = p->logits;
+    a.ld = p->ld_logits;
+    a.T = p->T;
+    a.idx = p->idx;
+    a.d_gates = p->d_gates;
+    a.d_loss = p->d_loss;
+    a.counts = p->counts;
+    a.tokens = p->tokens;
+    a.seq = p->sequences;
+    a.d_logits = p->d_logits;
+    a.ld_d = p->ld_d_logits;
+    a.E = p->E;
+    a.k = p->k;
+    a.S = p->S;
+    a.dt = p->dtype;
+    a.sigmoid = p->score_fn == MOE_SCORE_SIGMOID_BIAS;
+    a.normalize = p->normalize;
+    a.scale = p->scale;
+    return cuda_status(launch_router_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_forward_block(void* plan, const moe_block_args* b, int32_t T, void* stream) {

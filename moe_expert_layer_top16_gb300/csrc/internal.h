@@ -427,6 +427,51 @@ void mx4_tiles(int N, int G, bool pair, int* nt, int* b_box);
 cudaError_t mx4_setup(const Mx4Params& p);
 cudaError_t launch_mx4_gemm(const Mx4Params& p, cudaStream_t s);
 
+// ------------------------------------------------------------------ the router's operators (select.cu)
+// Logits [T][E] of type dt with row stride ld in elements; 1 <= k <= 32, k <= E <= 1024.
+struct SelectArgs {
+    const void* logits;
+    int64_t ld, T;
+    const float* bias;          // [E], or null: ranked by the logits
+    const uint8_t* mask;        // [T], or null; 0: a token that is routed nowhere
+    int32_t* idx;               // [T][k]
+    float* gates;               // [T][k]
+    int E, k, dt, sigmoid, normalize;
+    float scale;
+};
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t s);
+struct BalanceArgs {
+    const void* logits;
+    int64_t ld, T;
+    const int32_t* idx;         // [T][k]
+    const int32_t* seq;         // [S + 1], or null (S == 1): all rows
+    float* loss;                // [S]
+    int32_t* counts;            // [S][E]
+    int32_t* tokens;            // [S]
+    float* part;                // workspace
+    int E, k, S, dt, sigmoid;
+    int pitch;                  // set by the launch, like per: E in whole 16-byte words
+    int64_t per;                // tokens of a block
+};
+size_t balance_workspace_bytes(int64_t T, int E, int S);
+cudaError_t launch_balance(BalanceArgs a, cudaStream_t s);
+struct RouterBackArgs {
+    const void* logits;
+    int64_t ld, T;
+    const int32_t* idx;
+    const float* d_gates;       // [T][k], or null
+    const float* d_loss;        // [S], or null; with it counts, tokens and seq of the balance loss
+    const int32_t* counts;
+    const int32_t* tokens;
+    const int32_t* seq;
+    void* d_logits;             // [T][E] of type dt
+    int64_t ld_d;
+    int E, k, S, dt, sigmoid, normalize;
+    int pitch;                  // set by the launch
+    float scale;
+};
+cudaError_t launch_router_backward(RouterBackArgs a, cudaStream_t s);
+
 // ------------------------------------------------------------------ tensor-core rate probe (peak.cu)
 enum ProbeKind : int { PROBE_MX_E2M1_E4M3 = 0, PROBE_MX_E4M3_E4M3 = 1, PROBE_BF16 = 2 };
 // grid CTAs each issue iters x 4 MMAs of M = 128 x n; *flops = their FLOPs

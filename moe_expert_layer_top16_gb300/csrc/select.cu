@@ -1,0 +1,721 @@
+// The router as operators of their own.
+//
+//   select     the k experts of each token with the largest keys, and their
+//              gates.  Key: the logit l, or with a bias sigmoid(l) + b; equal
+//              keys by the lower expert.  Gates: the winners' scores over
+//              their sum, or as they are
+//   balance    for each sequence of tokens the counts c_e of its slots, the
+//              mean share P_e of each expert in its tokens' scores, and
+//              L = E / (k n) sum_e c_e P_e   (1 when both are even)
+//   backward   the gradient of gates and losses with respect to the logits,
+//              both in one pass over them
+//
+// A token's logits are one warp's: a lane holds them in registers, eight
+// neighbours at a time where rows allow it.  Every sum runs in a fixed order.
+#include <algorithm>
+#include <cfloat>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+// A logit as the operators read it: what is not a number closes an expert like
+// minus infinity, plus infinity counts as the largest number.
+__device__ __forceinline__ float open_logit(float l) { return l == l ? fminf(l, FLT_MAX) : -INFINITY; }
+
+// A lane's part of a row: value i V + j is that of expert (32 i + lane) V + j;
+// minus infinity behind the last expert.
+template <int V, int NI>
+__device__ __forceinline__ void load_row(const void* base, int64_t off, int E, int dt, int lane, float (&v)[NI * V]) {
+    RawVec<V> raw[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = (32 * i + lane) * V;
+        if (e < E) raw[i] = load_raw<V>(base, off + e, dt);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = (32 * i + lane) * V;
+        float f[V];
+        if (e < E) raw_to_f32(raw[i], dt, f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i * V + j] = e < E ? open_logit(f[j]) : -INFINITY;
+    }
+}
+
+// ------------------------------------------------------------------ reductions over a warp
+// Floats as unsigned integers of the same order (0: below every number).
+__device__ __forceinline__ uint32_t order_bits(float k) {
+    const uint32_t u = (k == 0.0f) ? 0u : __float_as_uint(k);     // -0 ties with +0, as the floats compare
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float bits_order(uint32_t b) {
+    return __uint_as_float((b & 0x80000000u) ? (b & 0x7fffffffu) : ~b);
+}
+__device__ __forceinline__ float warp_max(float v) { return bits_order(__reduce_max_sync(kAll, order_bits(v))); }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+// ------------------------------------------------------------------ scores
+// Scores of values v[N] as multiples of a common factor that keeps them from
+// underflow, and their sum over the warp.  Softmax: e^(v - max).  Sigmoid:
+// sigmoid(v) = e^min(v, 0) / (1 + e^-|v|), its numerator over the largest one,
+// which is 1 unless every value is negative.  Closed values give 0.
+template <int N>
+__device__ __forceinline__ float scores(const float (&v)[N], bool sigmoid, float (&x)[N]) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, v[i]);
+    top = warp_max(top);
+    float sum = 0.0f;
+    if (top == -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = 0.0f;
+        return 0.0f;
+    }
+    if (!sigmoid) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            x[i] = expf(v[i] - top);
+            sum += x[i];
+        }
+    } else if (top >= 0.0f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float u = expf(-fabsf(v[i]));
+            x[i] = (v[i] >= 0.0f ? 1.0f : u) / (1.0f + u);
+            sum += x[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            x[i] = expf(v[i] - top) / (1.0f + expf(v[i]));
+            sum += x[i];
+        }
+    }
+    return warp_sum(sum);
+}
+
+__device__ __forceinline__ float sigmoid_of(float v) {
+    const float u = expf(-fabsf(v));
+    return (v >= 0.0f ? 1.0f : u) / (1.0f + u);
+}
+// 1 - sigmoid(v) without the cancellation.
+__device__ __forceinline__ float sigmoid_rest(float v) {
+    const float u = expf(-fabsf(v));
+    return (v >= 0.0f ? u : 1.0f) / (1.0f + u);
+}
+
+// ------------------------------------------------------------------ select
+// The k-th largest of the lanes' largest keys is at most the k-th largest key:
+// what reaches it, some 1.4 k of the keys, are the candidates, which go to
+// shared memory and are ranked by counting the better ones.  (k rounds of a
+// warp-wide maximum over all keys, the first form of this kernel, are kept for
+// rows with more than kCand candidates: many equal keys.)
+//
+// Keys with a bias are defined in 64 bits, whose exponentials would take some
+// ten times as long as the logits' way from memory.  They are estimated in 32:
+// |estimate - key| <= 1e-6 + 2^-22 |estimate| (__expf is off by 2 + 1.17 |l|
+// units in the last place, which sigmoid(l) (1 - sigmoid(l)) turns into less
+// than 2^-22 at most, the sum and the quotient add 2^-23 and the rounding of
+// the sum with b), candidates are what reaches the bound less twice that, and
+// only where two candidates are nearer than that and not equal in logit and bias are
+// the candidates ranked by keys of 64 bits.
+constexpr int kCand = 64;
+constexpr int kSelectWarps = 4;
+constexpr float kNear = 4e-6f, kNearRel = 0x1p-20f;
+
+struct Candidate {
+    float key, l, b;
+    int e;
+};
+
+__device__ __forceinline__ float key32(float l, float b) {
+    return l == -INFINITY ? -INFINITY : __frcp_rn(1.0f + __expf(-l)) + b;
+}
+__device__ __forceinline__ double key64(float l, float b) {
+    return 1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(b);
+}
+// A bias of minus infinity or not a number closes an expert as well.
+__device__ __forceinline__ float open_bias(float b) { return open_logit(b); }
+
+// Descending over the lanes.
+__device__ __forceinline__ uint32_t bitonic_step(uint32_t x, int lane, int stride, bool down) {
+    const uint32_t y = __shfl_xor_sync(kAll, x, stride);
+    return (((lane & stride) == 0) == down) ? max(x, y) : min(x, y);
+}
+__device__ __forceinline__ uint32_t sort_lanes(uint32_t x, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int stride = size / 2; stride > 0; stride /= 2) x = bitonic_step(x, lane, stride, (lane & size) == 0);
+    return x;
+}
+
+// Rows with too many candidates: k rounds, each the largest key of 64 bits
+// below the pick before, in the order (key descending, expert ascending).
+__device__ __noinline__ void select_rounds(const SelectArgs& a, int64_t t, int lane, int* win, float* win_l) {
+    double last = INFINITY;
+    int last_e = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double best = -INFINITY;
+        int best_e = 0x7fffffff;
+        float best_l = 0.0f;
+        for (int e = lane; e < a.E; e += 32) {
+            float f[1];
+            raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, a.dt), a.dt, f);
+            const float l = open_logit(f[0]), b = a.bias ? open_bias(a.bias[e]) : 0.0f;
+            if (l == -INFINITY || b == -INFINITY) continue;
+            const double key = a.bias ? key64(l, b) : static_cast<double>(l);
+            if ((key < last || (key == last && e > last_e)) && key > best) {
+                best = key;
+                best_e = e;
+                best_l = l;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const double k2 = __shfl_xor_sync(kAll, best, o);
+            const int e2 = __shfl_xor_sync(kAll, best_e, o);
+            const float l2 = __shfl_xor_sync(kAll, best_l, o);
+            if (k2 > best || (k2 == best && e2 < best_e)) {
+                best = k2;
+                best_e = e2;
+                best_l = l2;
+            }
+        }
+        if (lane == 0 && best_e < a.E) {
+            win[j] = best_e;
+            win_l[j] = best_l;
+        }
+        last = best;
+        last_e = best_e;
+        if (best_e >= a.E) break;
+    }
+}
+
+template <int V, int NI>
+__global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectArgs a) {
+    __shared__ __align__(16) Candidate s_cand[kSelectWarps][kCand];
+    __shared__ double s_key[kSelectWarps][kCand];
+    __shared__ int s_win[kSelectWarps][32];
+    __shared__ float s_win_l[kSelectWarps][32];
+    constexpr int N = NI * V;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kSelectWarps + warp;
+    if (t >= a.T) return;
+    const int E = a.E, k = a.k;
+    if (a.mask && !a.mask[t]) {
+        if (lane < k) {
+            a.idx[t * k + lane] = -1;
+            a.gates[t * k + lane] = 0.0f;
+        }
+        return;
+    }
+    Candidate* cand = s_cand[warp];
+    float v[N];
+    load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+    uint32_t key[N];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e0 = (32 * i + lane) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = i * V + j;
+            float est = v[c];
+            if (a.bias && e0 < E) est = key32(est, open_bias(a.bias[e0 + j]));
+            key[c] = est == -INFINITY ? 0u : order_bits(est);
+        }
+    }
+    // the bound: the k-th largest of 32 or 64 disjoint sets' largest keys
+    uint32_t h0 = 0, h1 = 0;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        if (c < N / 2)
+            h0 = max(h0, key[c]);
+        else
+            h1 = max(h1, key[c]);
+    }
+    uint32_t least;
+    if (k <= 16) {
+        least = sort_lanes(max(h0, h1), lane);
+    } else {
+        h0 = sort_lanes(h0, lane);
+        h1 = __shfl_sync(kAll, sort_lanes(h1, lane), 31 - lane);
+        least = max(h0, h1);             // the 32 largest of both, as a bitonic sequence
+#pragma unroll
+        for (int stride = 16; stride > 0; stride /= 2) least = bitonic_step(least, lane, stride, true);
+    }
+    least = __shfl_sync(kAll, least, k - 1);
+    if (a.bias && least) {
+        const float f = bits_order(least);
+        least = order_bits(f - (kNear + kNearRel * fabsf(f)));
+    }
+    least = max(least, 1u);
+    uint32_t mask = 0;
+#pragma unroll
+    for (int c = 0; c < N; ++c) mask |= key[c] >= least ? 1u << c : 0u;
+    const int mine = __popc(mask);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += n;
+    }
+    const int n = __shfl_sync(kAll, incl, 31);
+    s_win[warp][lane] = -1;
+    s_win_l[warp][lane] = -INFINITY;
+    if (n > kCand) {
+        __syncwarp();
+        select_rounds(a, t, lane, s_win[warp], s_win_l[warp]);
+    } else {
+        int pos = incl - mine;
+        while (mask) {
+            const int c = __ffs(mask) - 1;
+            mask &= mask - 1;
+            cand[pos++].e = (32 * (c / V) + lane) * V + c % V;
+        }
+        __syncwarp();
+        Candidate own[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int p = lane + 32 * u;
+            if (p < n) {
+                own[u].e = cand[p].e;
+                float f[1];
+                raw_to_f32(load_raw<1>(a.logits, t * a.ld + own[u].e, a.dt), a.dt, f);
+                own[u].l = open_logit(f[0]);
+                own[u].b = a.bias ? open_bias(a.bias[own[u].e]) : 0.0f;
+                own[u].key = a.bias ? key32(own[u].l, own[u].b) : own[u].l;
+                cand[p] = own[u];
+            }
+        }
+        __syncwarp();
+        int rank[2] = {0, 0};
+        bool near = false;
+        for (int p = 0; p < n; ++p) {
+            const Candidate q = cand[p];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (lane + 32 * u >= n) continue;
+                rank[u] += (q.key > own[u].key || (q.key == own[u].key && q.e < own[u].e)) ? 1 : 0;
+                if (a.bias)
+                    near |= fabsf(q.key - own[u].key) <= kNear + kNearRel * fabsf(own[u].key) &&
+                            !(q.l == own[u].l && q.b == own[u].b);
+            }
+        }
+        if (a.bias && __any_sync(kAll, near)) {
+            double exact[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                rank[u] = 0;
+                if (lane + 32 * u < n) s_key[warp][lane + 32 * u] = exact[u] = key64(own[u].l, own[u].b);
+            }
+            __syncwarp();
+            for (int p = 0; p < n; ++p) {
+                const double q = s_key[warp][p];
+                const int e = cand[p].e;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (lane + 32 * u < n) rank[u] += (q > exact[u] || (q == exact[u] && e < own[u].e)) ? 1 : 0;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (lane + 32 * u < n && rank[u] < k) {
+                s_win[warp][rank[u]] = own[u].e;
+                s_win_l[warp][rank[u]] = own[u].l;
+            }
+    }
+    __syncwarp();
+    const int e = s_win[warp][lane];             // -1 behind the last slot and where no expert was left
+    const float l[1] = {s_win_l[warp][lane]};
+    float w[1];
+    if (a.normalize) {
+        const float sum = scores(l, a.sigmoid != 0, w);
+        w[0] = sum > 0.0f ? w[0] / sum : 0.0f;
+    } else if (a.sigmoid) {
+        w[0] = e >= 0 ? sigmoid_of(l[0]) : 0.0f;
+    } else {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < N; ++c) top = fmaxf(top, v[c]);
+        top = warp_max(top);
+        if (top > -INFINITY)
+#pragma unroll
+            for (int c = 0; c < N; ++c) sum += expf(v[c] - top);
+        sum = warp_sum(sum);
+        w[0] = e >= 0 ? expf(l[0] - top) / sum : 0.0f;
+    }
+    if (lane < k) {
+        a.idx[t * k + lane] = e;
+        a.gates[t * k + lane] = a.scale * w[0];
+    }
+}
+
+// ------------------------------------------------------------------ sequences
+// Borders of the sequences, kept inside the rows.
+__device__ __forceinline__ int64_t border(const int32_t* seq, int s, int S, int64_t T) {
+    if (!seq) return s == 0 ? 0 : T;
+    return min(max(static_cast<int64_t>(seq[s]), static_cast<int64_t>(0)), T);
+}
+
+// The sequence that row t is in, -1: in none.  32 borders at a time.
+__device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int64_t T, int64_t t, int lane) {
+    if (!seq) return 0;
+    // number of sequences that end at or before t
+    int lo = 0, hi = S;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = min(lo + (lane + 1) * step, hi) - 1;            // last sequence of the lane's part
+        const uint32_t over = __ballot_sync(kAll, border(seq, at + 1, S, T) > t);
+        if (over == 0) {
+            lo = hi;
+        } else {
+            const int part = __ffs(over) - 1;
+            const int first = lo + part * step, last = min(first + step, hi) - 1;
+            lo = first;
+            hi = last;                   // the last one ends behind t: the answer is at most its number
+        }
+    }
+    return lo < S && border(seq, lo, S, T) <= t ? lo : -1;
+}
+
+// ------------------------------------------------------------------ balance
+// Block b takes the tokens [b per, (b + 1) per).  Its warps add up their
+// tokens' shares in registers; at the end of each sequence inside the block the
+// warps' sums are added in shared memory, and the block's part of the sequence
+// goes to row b + s of the workspace: both numbers only grow along the tokens,
+// so that no two parts share a row.  A cluster of eight CTAs for each sequence
+// then adds its parts, each CTA an eighth of the experts.
+constexpr int kBalWarps = 16;
+constexpr int kBalCtas = 8;
+
+template <int V, int NI>
+__global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const BalanceArgs a) {
+    extern __shared__ __align__(16) float s_sum[];       // [kBalWarps][pitch], then int32 [pitch] counts
+    __shared__ int s_tokens;
+    constexpr int N = NI * V;
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = a.E, k = a.k, P = a.pitch;
+    int32_t* hist = reinterpret_cast<int32_t*>(s_sum + kBalWarps * P);
+    const int64_t t0 = blockIdx.x * a.per, t1 = min(t0 + a.per, a.T);
+    // the first sequence that ends behind t0 (every warp finds the same)
+    int s = 0;
+    if (a.seq) {
+        int lo = 0, hi = a.S;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (border(a.seq, mid + 1, a.S, a.T) > t0)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        s = lo;
+    }
+    for (; s < a.S; ++s) {
+        const int64_t first = border(a.seq, s, a.S, a.T);
+        if (first >= t1) break;
+        const int64_t f = max(first, t0), l = min(border(a.seq, s + 1, a.S, a.T), t1);
+        if (l <= f) continue;
+        for (int e = threadIdx.x; e < P; e += blockDim.x) hist[e] = 0;
+        if (threadIdx.x == 0) s_tokens = 0;
+        __syncthreads();
+        float acc[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] = 0.0f;
+        int used = 0;
+        for (int64_t t = f + warp; t < l; t += kBalWarps) {
+            const int e = lane < k ? a.idx[t * k + lane] : -1;
+            const bool kept = e >= 0 && e < E;
+            if (!__any_sync(kAll, kept)) continue;
+            if (kept) atomicAdd(&hist[e], 1);
+            ++used;
+            float v[N], x[N];
+            load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+            const float sum = scores(v, a.sigmoid != 0, x);
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int c = 0; c < N; ++c) acc[c] = fmaf(x[c], inv, acc[c]);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e0 = (32 * i + lane) * V;
+            if (e0 < E)
+#pragma unroll
+                for (int j = 0; j < V; ++j) s_sum[warp * P + e0 + j] = acc[i * V + j];
+        }
+        if (lane == 0) atomicAdd(&s_tokens, used);
+        __syncthreads();
+        float* part = a.part + (blockIdx.x + static_cast<int64_t>(s)) * (2 * P + 4);
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kBalWarps; ++w) sum += s_sum[w * P + e];
+            part[e] = sum;
+            reinterpret_cast<int32_t*>(part)[P + e] = hist[e];
+        }
+        if (threadIdx.x == 0) reinterpret_cast<int32_t*>(part)[2 * P] = s_tokens;
+        __syncthreads();
+    }
+}
+
+// The parts are written by the launch that this one overlaps: plain loads.
+__global__ void __launch_bounds__(512) balance_sum_kernel(const BalanceArgs a) {
+    __shared__ float s_sum[4][128];
+    __shared__ int s_cnt[4][128];
+    __shared__ int s_tok[16];
+    __shared__ float s_loss[kBalCtas];
+    const int rank = blockIdx.x % kBalCtas, s = blockIdx.x / kBalCtas;
+    const int col = threadIdx.x & 127, row = threadIdx.x >> 7;
+    const int per = (a.E + kBalCtas - 1) / kBalCtas;
+    const int e = rank * per + col;
+    const bool mine = col < per && e < a.E;
+    const int64_t stride = 2 * a.pitch + 4;
+    const int64_t first = border(a.seq, s, a.S, a.T), last = border(a.seq, s + 1, a.S, a.T);
+    const int64_t b0 = last > first ? first / a.per : 0, b1 = last > first ? (last - 1) / a.per + 1 : 0;
+    cluster_sync_all();                // every CTA runs before its shared memory is written to
+    pdl_wait();
+    float sum = 0.0f;
+    int cnt = 0, tok = 0;
+    if (mine) {
+#pragma unroll 4
+        for (int64_t b = b0 + row; b < b1; b += 4) {
+            const float* part = a.part + (b + s) * stride;
+            sum += part[e];
+            cnt += reinterpret_cast<const int32_t*>(part)[a.pitch + e];
+        }
+    }
+    for (int64_t b = b0 + threadIdx.x; b < b1; b += blockDim.x)
+        tok += reinterpret_cast<const int32_t*>(a.part + (b + s) * stride)[2 * a.pitch];
+    tok = __reduce_add_sync(kAll, tok);
+    if ((threadIdx.x & 31) == 0) s_tok[threadIdx.x >> 5] = tok;
+    s_sum[row][col] = sum;
+    s_cnt[row][col] = cnt;
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        sum = (s_sum[0][col] + s_sum[1][col]) + (s_sum[2][col] + s_sum[3][col]);
+        cnt = (s_cnt[0][col] + s_cnt[1][col]) + (s_cnt[2][col] + s_cnt[3][col]);
+        if (mine) a.counts[static_cast<int64_t>(s) * a.E + e] = cnt;
+        s_sum[0][col] = mine ? static_cast<float>(cnt) * sum : 0.0f;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const float x = warp_sum((s_sum[0][threadIdx.x] + s_sum[0][threadIdx.x + 32]) +
+                                 (s_sum[0][threadIdx.x + 64] + s_sum[0][threadIdx.x + 96]));
+        if (threadIdx.x == 0) {
+            const uint32_t at = mapa_shared(smem_u32(&s_loss[rank]), 0);
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+        }
+    }
+    cluster_sync_all();
+    if (rank == 0 && threadIdx.x == 0) {
+        int n = 0;
+        for (int w = 0; w < 16; ++w) n += s_tok[w];
+        float x = 0.0f;
+        for (int r = 0; r < kBalCtas; ++r) x += s_loss[r];
+        const float m = static_cast<float>(max(n, 1));
+        a.loss[s] = (static_cast<float>(a.E) / static_cast<float>(a.k)) * (x / m) / m;
+        a.tokens[s] = n;
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// With shares p, a_e = dL E c_e / (k n^2) and r_e = 1 - sigmoid(l_e) (1 for
+// softmax), the loss gives p_e r_e (a_e - sum p a).  With g = scale d_gates and
+// the gates w over the winners, the gates give w_j r_j (g_j - sum g w); not
+// normalised, g_j s_j r_j, or for the softmax over all p_e ([e won] g_e - sum g p).
+// A lane holds slot j = lane; the slots' values meet their experts' lanes in a row
+// of shared memory.
+constexpr int kBackWarps = 4;
+
+template <int V, int NI>
+__global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const RouterBackArgs a) {
+    extern __shared__ __align__(16) float s_rows[];      // [kBackWarps][pitch]
+    constexpr int N = NI * V;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kBackWarps + warp;
+    if (t >= a.T) return;
+    const int E = a.E, k = a.k;
+    const bool sigmoid = a.sigmoid != 0;
+    float* srow = s_rows + warp * a.pitch;
+    float v[N], d[N];
+    load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+    int e = lane < k ? a.idx[t * k + lane] : -1;
+    if (e < 0 || e >= E) e = -1;
+    const bool any = __any_sync(kAll, e >= 0);
+    const int s = a.d_loss && any ? sequence_of(a.seq, a.S, a.T, t, lane) : -1;
+    const bool all = !a.normalize && !sigmoid && a.d_gates;       // gates by the softmax over all
+    float inv = 0.0f;
+    if (any && (s >= 0 || all)) {
+        const float sum = scores(v, sigmoid, d);
+        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    }
+    float shift = 0.0f;                                  // what is taken from every share
+    if (a.d_gates && any) {
+        float l = -INFINITY, g = 0.0f;
+        if (e >= 0) {
+            float f[1];
+            raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, a.dt), a.dt, f);
+            l = open_logit(f[0]);
+            g = a.scale * a.d_gates[t * k + lane];
+        }
+        float val;
+        if (a.normalize) {
+            const float lv[1] = {l};
+            float w[1];
+            const float sum = scores(lv, sigmoid, w);
+            w[0] = sum > 0.0f ? w[0] / sum : 0.0f;
+            val = w[0] * (g - warp_sum(w[0] * g));
+            if (sigmoid) val *= sigmoid_rest(l);
+        } else if (sigmoid) {
+            val = g * sigmoid_of(l) * sigmoid_rest(l);
+        } else {
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < N; ++c) top = fmaxf(top, v[c]);
+            top = warp_max(top);
+            val = l > -INFINITY ? g * expf(l - top) * inv : 0.0f;
+            shift = warp_sum(val);
+        }
+        if (l == -INFINITY) val = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e0 = (32 * i + lane) * V;
+            if (e0 < E)
+#pragma unroll
+                for (int j = 0; j < V; ++j) srow[e0 + j] = 0.0f;
+        }
+        __syncwarp();
+        const uint32_t same = __match_any_sync(kAll, e);
+        if (__any_sync(kAll, e >= 0 && (same & (same - 1)))) {
+            for (int j = 0; j < k; ++j) {                // an expert named twice: slots in turn
+                if (lane == j && e >= 0) srow[e] += val;
+                __syncwarp();
+            }
+        } else if (e >= 0) {
+            srow[e] = val;
+        }
+        __syncwarp();
+    }
+    float inner = 0.0f;
+    const int32_t* cnt = nullptr;
+    float f = 0.0f;
+    if (s >= 0) {
+        const float n = static_cast<float>(max(a.tokens[s], 1));
+        f = a.d_loss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n;
+        cnt = a.counts + static_cast<int64_t>(s) * E;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e0 = (32 * i + lane) * V;
+            if (e0 < E)
+#pragma unroll
+                for (int j = 0; j < V; ++j) inner = fmaf(d[i * V + j] * inv, f * static_cast<float>(cnt[e0 + j]), inner);
+        }
+        inner = warp_sum(inner);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e0 = (32 * i + lane) * V;
+        if (e0 >= E) continue;
+        float o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = i * V + j;
+            float r = 0.0f;
+            if (s >= 0) {
+                r = d[c] * inv * (f * static_cast<float>(cnt[e0 + j]) - inner);
+                if (sigmoid) r *= sigmoid_rest(v[c]);
+            }
+            if (a.d_gates && any) {
+                r += srow[e0 + j];
+                if (all) r -= d[c] * inv * shift;
+            }
+            o[j] = r;
+        }
+        store_vec(a.d_logits, t * a.ld_d + e0, a.dt, o);
+    }
+}
+
+// Whether rows go by eight values at a time.
+bool rows_wide(const void* p, int64_t ld, int dt, int E) {
+    return E % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
+}
+
+// f<V, NI> with the fewest registers that hold E values a warp.
+#define MOE_ROW_FORMS(RUN, wide, E)              \
+    if (wide) {                                  \
+        if ((E) <= 256) return RUN(8, 1);        \
+        if ((E) <= 512) return RUN(8, 2);        \
+        return RUN(8, 4);                        \
+    }                                            \
+    if ((E) <= 256) return RUN(1, 8);            \
+    return RUN(1, 32)
+
+int64_t balance_per(int64_t T) {
+    const int64_t per = (T + 151) / 152;
+    return std::max<int64_t>(per, 1);
+}
+
+template <int V, int NI>
+cudaError_t balance_as(const BalanceArgs& a, cudaStream_t s) {
+    if (a.T > 0) {
+        const unsigned blocks = static_cast<unsigned>((a.T + a.per - 1) / a.per);
+        const size_t smem = sizeof(float) * static_cast<size_t>(kBalWarps + 1) * a.pitch;
+        if (smem > 48 * 1024 - 256) {
+            const cudaError_t err = cudaFuncSetAttribute(balance_parts_kernel<V, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                         static_cast<int>(sizeof(float) * (kBalWarps + 1) * 1024));
+            if (err != cudaSuccess) return err;
+        }
+        balance_parts_kernel<V, NI><<<blocks, kBalWarps * 32, smem, s>>>(a);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+    }
+    return launch_ex_cluster(balance_sum_kernel, dim3(static_cast<unsigned>(a.S) * kBalCtas), dim3(512), 0, s, a.T > 0, kBalCtas, a);
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(int64_t T, int E, int S) {
+    if (T == 0) return 0;
+    const int64_t per = balance_per(T), blocks = (T + per - 1) / per;
+    return sizeof(float) * static_cast<size_t>(blocks + S) * static_cast<size_t>(2 * ((E + 3) & ~3) + 4);
+}
+
+cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
+    if (a.T == 0) return cudaSuccess;
+    const unsigned blocks = static_cast<unsigned>((a.T + kSelectWarps - 1) / kSelectWarps);
+#define MOE_RUN(V, NI) (select_kernel<V, NI><<<blocks, kSelectWarps * 32, 0, s>>>(a), cudaGetLastError())
+    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E), a.E);
+#undef MOE_RUN
+}
+
+cudaError_t launch_balance(BalanceArgs a, cudaStream_t s) {
+    a.per = balance_per(a.T);
+    a.pitch = (a.E + 3) & ~3;
+#define MOE_RUN(V, NI) balance_as<V, NI>(a, s)
+    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E), a.E);
+#undef MOE_RUN
+}
+
+cudaError_t launch_router_backward(RouterBackArgs a, cudaStream_t s) {
+    if (a.T == 0) return cudaSuccess;
+    a.pitch = (a.E + 3) & ~3;
+    const unsigned blocks = static_cast<unsigned>((a.T + kBackWarps - 1) / kBackWarps);
+    const size_t smem = a.d_gates ? sizeof(float) * kBackWarps * static_cast<size_t>(a.pitch) : 0;
+#define MOE_RUN(V, NI) (router_backward_kernel<V, NI><<<blocks, kBackWarps * 32, smem, s>>>(a), cudaGetLastError())
+    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E) && rows_wide(a.d_logits, a.ld_d, a.dt, a.E), a.E);
+#undef MOE_RUN
+}
+
+}  // namespace moe
