@@ -526,6 +526,58 @@ MOE_API moe_status moe_mx4_gemm(const uint8_t *a_codes, const uint8_t *a_scales,
                                 const int32_t *offsets, void *out, int64_t ld_out, int32_t out_dtype,
                                 int32_t *dev_status, void *stream);
 
+/* Products of a few rows, which are not quantised, with four-bit weights: for
+ * decoded tokens, whose time is the weights' way from memory.
+ *   y[n][m] = sum_k w[m][k] x[n][k]
+ * Codes [G][M][K/2] (16-byte aligned), two a byte like moe_mxfp4_encode's, and
+ * scales [G][M][K/group], one for each `group` weights along K:
+ *   MOE_W4_MXFP4  E2M1 codes, E8M0 scales, group 32: what moe_mxfp4_encode and
+ *                 moe_mxfp4_quantize write and moe_mx4_gemm reads
+ *   MOE_W4_INT4   codes c that stand for c - 8; scales of scale_dtype (any
+ *                 moe_dtype), group 32, 64 or 128
+ * Without idx: one matrix (G = 1), x [T][K], out [T][M].  With idx int32 [T][k]
+ * (moe_select's, or any): slot (t, j) has matrix idx[t][j] and the row x[t], or
+ * with x_per_slot x[t k + j], and
+ *   weights NULL   out[t k + j][m] = that slot's product; 0 for a slot whose
+ *                  entry is outside [0, G)
+ *   weights fp32   out[t][m] = sum_j weights[t][j] product, over the slots that
+ *   [T][k]         are inside [0, G), in fp32
+ * With up_codes and up_scales (a second set of matrices of the same sizes, not
+ * with weights) a product is SiLU(y) times the second matrix' y, each in fp32.
+ * A matrix that many slots name is read for each of them: beyond a few tokens
+ * sort the slots and use moe_mx4_gemm.
+ *
+ * The values of x are split into 32s along K and held to 2^-39 of the largest in
+ * their 32 (fp32: 2^-63), so that bf16 and fp16 values are exact down to 2^-28 of
+ * it; products and sums are fp32.  x's rows go by 16 bytes where address and
+ * stride are multiples of 16 bytes, else element by element.  T >= 0, T k <
+ * 2^31, 1 <= k <= 32, M >= 1, G M <= 2^31 - 256, K a multiple of the group up
+ * to 2^24. */
+typedef enum {
+    MOE_W4_MXFP4 = 0,
+    MOE_W4_INT4 = 1
+} moe_w4_format;
+
+typedef struct {
+    const uint8_t *codes;
+    const void *scales;
+    const uint8_t *up_codes;  /* or NULL, as up_scales */
+    const void *up_scales;
+    const void *x;
+    int64_t ld_x;
+    const int32_t *idx;       /* [T][k], or NULL */
+    const float *weights;     /* [T][k], or NULL */
+    void *out;
+    int64_t ld_out;
+    int32_t T, k;             /* k is not read without idx */
+    int32_t G, M, K, group;
+    int32_t x_per_slot;
+    int32_t format;           /* moe_w4_format */
+    int32_t scale_dtype;      /* MOE_W4_INT4 */
+    int32_t x_dtype, out_dtype;
+} moe_w4_matvec_args;
+MOE_API moe_status moe_w4_matvec(const moe_w4_matvec_args *args, void *stream);
+
 /* The router as operators of their own.  logits [T][E] of any moe_dtype, row
  * stride ld_logits in elements; they go by 16 bytes where the address and the
  * stride are multiples of 16 bytes and E is one of 8, else element by element.

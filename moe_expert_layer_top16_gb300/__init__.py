@@ -38,7 +38,7 @@ ENTRY_POINTS = ("moe_plan", "moe_forward", "moe_forward_host", "moe_get_device_s
                 "moe_unpermute_backward",
                 "moe_block_norm", "moe_block_norm_workspace_bytes", "moe_block_norm_backward", "moe_mxfp4_quantize",
                 "moe_mxfp4_decode", "moe_mx4_gemm", "moe_forward_block", "moe_select", "moe_balance_loss",
-                "moe_balance_loss_workspace_bytes", "moe_router_backward")
+                "moe_balance_loss_workspace_bytes", "moe_router_backward", "moe_w4_matvec")
 
 
 class MoeError(RuntimeError):
@@ -402,5 +402,5 @@ def debug_buffers(cfg, T: int, device, fields=DEBUG_FIELDS) -> dict:
 
 from . import block  # noqa: E402
 from .block import (block_norm, block_norm_backward, mx4_gemm, mxfp4_decode, mxfp4_quantize, permute,  # noqa: E402,F401
-                    permute_backward, sort_by_expert, unpermute, unpermute_backward)
+                    permute_backward, sort_by_expert, unpermute, unpermute_backward, w4_matvec)
 from .router import balance_loss, router_backward, select_experts  # noqa: E402,F401

@@ -1,5 +1,6 @@
 """Operators round the layer: tokens sorted by expert and back, the norms
-behind and before a block, and four-bit activations with their product.
+behind and before a block, four-bit activations with their product, and products
+of a few rows with four-bit weights.
 
 Argument marshalling for the stand-alone entry points of ``include/moe.h``;
 nothing is computed here.  Every function takes CUDA tensors of one device,
@@ -50,6 +51,13 @@ class _BlockArgs(C.Structure):
                [("res_scale", C.c_float), ("eps", C.c_float)]
 
 
+class _W4MatvecArgs(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("codes", "scales", "up_codes", "up_scales", "x")] + [("ld_x", C.c_int64)] + \
+               [(n, C.c_void_p) for n in ("idx", "weights", "out")] + [("ld_out", C.c_int64)] + \
+               [(n, C.c_int32) for n in ("T", "k", "G", "M", "K", "group", "x_per_slot", "format", "scale_dtype", "x_dtype",
+                                         "out_dtype")]
+
+
 def declare(L):
     """Argument types of the entry points below (called once, when libmoe is loaded)."""
     P, i32, i64 = C.c_void_p, C.c_int32, C.c_int64
@@ -63,6 +71,7 @@ def declare(L):
             ("moe_mxfp4_quantize", [P, i64, i32, i64, i64, P, P, P]),
             ("moe_mxfp4_decode", [P, P, i64, i64, P, i64, i32, P]),
             ("moe_mx4_gemm", [P, P, i32, i32, P, P, i32, i32, P, P, i64, i32, P, P]),
+            ("moe_w4_matvec", [C.POINTER(_W4MatvecArgs), P]),
             ("moe_forward_block", [P, C.POINTER(_BlockArgs), i32, P])):
         f = getattr(L, name)
         f.restype = C.c_int
@@ -566,4 +575,87 @@ def mx4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Tenso
                               _p(offsets), out.data_ptr(), ld, DTYPES[dtype], _p(status), _raw_stream(dev))
     if code:
         _check(code, "moe_mx4_gemm")
+    return out
+
+
+W4_MXFP4, W4_INT4 = 0, 1
+
+
+def _w4(codes, scales, dims, dev, what):
+    """Contiguous (codes, scales), and the group that a scale is for: codes uint8 [..., K/2], scales [..., K/group]."""
+    if not isinstance(codes, torch.Tensor) or not isinstance(scales, torch.Tensor) or codes.dtype != torch.uint8 \
+            or (scales.dtype != torch.uint8 and scales.dtype not in DTYPES) or codes.dim() != dims \
+            or scales.shape[:-1] != codes.shape[:-1] or scales.dim() != dims or codes.numel() == 0 or scales.shape[-1] < 1 \
+            or codes.get_device() != dev or scales.get_device() != dev:
+        _bad(what + ": codes uint8 [..., M, K/2] and scales [..., M, K/group] on x's device")
+    K, n = 2 * codes.shape[-1], scales.shape[-1]
+    if K % n or K // n not in ((32,) if scales.dtype == torch.uint8 else (32, 64, 128)):
+        _bad(what + ": a scale for 32 weights (E8M0), or for 32, 64 or 128 (floating scales)")
+    return codes.contiguous(), scales.contiguous(), K // n
+
+
+def w4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, up=None, idx: Optional[torch.Tensor] = None,
+              weights: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Products of a few rows with four-bit weights (see moe_w4_matvec), x not
+    quantised.  scales uint8: MXFP4 as mxfp4_quantize writes it; scales float32,
+    bfloat16 or float16: codes 0 to 15 that stand for -8 to 7.  One matrix codes
+    [M][K/2]: x [N][K] or [K] gives [N][M] or [M].  With idx int32 [T][k] and
+    codes [G][M][K/2]: x [T][K], or [T][k][K] with a row for each slot, gives
+    [T][k][M], zeros for slots outside [0, G); with weights float32 [T][k] the
+    weighted sum over a token's slots, [T][M].  up: a second (codes, scales), for
+    SiLU(product) times its product.  The result has out_dtype (default: x's)."""
+    what = "w4_matvec"
+    dev = _device(x, what)
+    if dev != _current() or stream is not None:
+        return _on(dev, stream, w4_matvec, x, codes, scales, up=up, idx=idx, weights=weights, out_dtype=out_dtype, out=out)
+    codes, scales, group = _w4(codes, scales, 2 if idx is None else 3, dev, what)
+    M, K = codes.shape[-2], 2 * codes.shape[-1]
+    if up is not None:
+        if not isinstance(up, (tuple, list)) or len(up) != 2:
+            _bad(what + ": up is (codes, scales)")
+        up_codes, up_scales, _ = _w4(up[0], up[1], codes.dim(), dev, what)
+        if up_codes.shape != codes.shape or up_scales.shape != scales.shape or up_scales.dtype != scales.dtype:
+            _bad(what + ": up has the sizes and types of the first matrix")
+    if not x.dim() or x.shape[-1] != K:
+        _bad(what + ": x [..., K]")
+    G, k, per_slot = 1, 1, 0
+    if idx is None:
+        if x.dim() > 2 or weights is not None:
+            _bad(what + ": without idx, x is [N][K] or [K] and there are no weights")
+        lead = tuple(x.shape[:-1])
+        T = lead[0] if lead else 1
+    else:
+        if idx.dtype != torch.int32 or idx.dim() != 2 or idx.get_device() != dev:
+            _bad(what + ": idx is int32 [T][k] on the same device")
+        G, (T, k) = codes.shape[0], idx.shape
+        _int32(idx.numel(), what)
+        per_slot = int(x.dim() == 3)
+        if tuple(x.shape[:-1]) not in ((T,), (T, k)):
+            _bad(what + ": x is [T][K] or [T][k][K]")
+        idx = idx.contiguous()
+        weights = _weights_of(weights, idx, what)
+        lead = (T,) if weights is not None else (T, k)
+        if weights is not None and up is not None:
+            _bad(what + ": up and weights do not go together")
+    xr, ld = _rows(x, what)
+    _int32(max(T, K, G * M), what)
+    dtype = out_dtype or (x.dtype if out is None else out.dtype)
+    if dtype not in DTYPES:
+        _bad(what + ": output type")
+    shape = lead + (M,)
+    n = T if len(lead) < 2 else T * k
+    if out is None:
+        out, ld_out = _empty(shape, dtype=dtype, device=x.device), M
+    else:
+        ld_out = _out_like(out, shape, n, dtype, dev, what)
+    if n:
+        ints = scales.dtype != torch.uint8
+        a = _W4MatvecArgs(codes.data_ptr(), scales.data_ptr(), None if up is None else up_codes.data_ptr(),
+                          None if up is None else up_scales.data_ptr(), xr.data_ptr(), ld, _p(idx), _p(weights), out.data_ptr(),
+                          ld_out, T, k, G, M, K, group, per_slot, W4_INT4 if ints else W4_MXFP4,
+                          DTYPES[scales.dtype] if ints else 0, DTYPES[xr.dtype], DTYPES[dtype])
+        code = lib().moe_w4_matvec(a, _raw_stream(dev))
+        if code:
+            _check(code, "moe_w4_matvec")
     return out

@@ -1759,6 +1759,50 @@ moe_status moe_mx4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int32_t
     return cuda_status(launch_mx4_gemm(p, static_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_w4_matvec(const moe_w4_matvec_args* p, void* stream) {
+    if (!p || p->T < 0 || p->M < 1 || p->G < 1 || p->K < 32 || p->K > kMx4MaxK ||
+        static_cast<int64_t>(p->G) * p->M > 0x7fffff00 || !known_dtype(p->x_dtype) || !known_dtype(p->out_dtype))
+        return MOE_ERR_INVALID_ARG;
+    const bool ints = p->format == MOE_W4_INT4;
+    if (!ints && p->format != MOE_W4_MXFP4) return MOE_ERR_INVALID_ARG;
+    if (ints ? (p->group != 32 && p->group != 64 && p->group != 128) || !known_dtype(p->scale_dtype) : p->group != 32)
+        return MOE_ERR_INVALID_ARG;
+    if (p->K % p->group) return MOE_ERR_INVALID_ARG;
+    if (p->idx ? !slots_ok(p->T, p->k) : p->G != 1 || p->weights) return MOE_ERR_INVALID_ARG;
+    if (!p->up_codes != !p->up_scales || (p->up_codes && p->weights)) return MOE_ERR_INVALID_ARG;
+    if (p->T == 0) return MOE_OK;
+    if (!p->codes || !aligned(p->codes, 16) || !aligned(p->up_codes, 16) || !p->scales || !aligned(p->idx, 4) ||
+        !aligned(p->weights, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (ints && (!aligned_elem(p->scales, p->scale_dtype) || !aligned_elem(p->up_scales, p->scale_dtype)))
+        return MOE_ERR_INVALID_ARG;
+    if (!matrix_ok(p->x, p->ld_x, p->x_dtype, p->K) || !matrix_ok(p->out, p->ld_out, p->out_dtype, p->M))
+        return MOE_ERR_INVALID_ARG;
+    MatvecArgs a = {};
+    a.codes = p->codes;
+    a.scales = static_cast<const uint8_t*>(p->scales);
+    a.up_codes = p->up_codes;
+    a.up_scales = static_cast<const uint8_t*>(p->up_scales);
+    a.x = p->x;
+    a.ld_x = p->ld_x;
+    a.N = p->T;
+    a.idx = p->idx;
+    a.weights = p->weights;
+    a.out = p->out;
+    a.ld_out = p->ld_out;
+    a.G = p->G;
+    a.M = p->M;
+    a.K = p->K;
+    a.k = p->idx ? p->k : 1;
+    a.x_per_slot = p->x_per_slot;
+    a.format = p->format;
+    a.shift = p->group == 32 ? 0 : p->group == 64 ? 1 : 2;
+    a.dt_scale = ints ? p->scale_dtype : MOE_DTYPE_F32;
+    a.dt_x = p->x_dtype;
+    a.dt_out = p->out_dtype;
+    return cuda_status(launch_matvec(a, static_cast<cudaStream_t>(stream)));
+}
+
 moe_status moe_select(const moe_select_args* p, void* stream) {
     if (!p || !router_ok(p->T, p->E, p->k, p->dtype, p->score_fn)) return MOE_ERR_INVALID_ARG;
     if (p->bias && p->score_fn != MOE_SCORE_SIGMOID_BIAS) return MOE_ERR_INVALID_ARG;

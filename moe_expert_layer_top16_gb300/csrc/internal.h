@@ -472,6 +472,30 @@ struct RouterBackArgs {
 };
 cudaError_t launch_router_backward(RouterBackArgs a, cudaStream_t s);
 
+// ------------------------------------------------------------------ products of a few rows (matvec.cu)
+struct MatvecArgs {
+    const uint8_t* codes;       // [G][M][K / 2]
+    const uint8_t* scales;      // [G][M][K / group]
+    const uint8_t* up_codes;    // a second matrix of the same sizes, or null
+    const uint8_t* up_scales;
+    const void* x;              // rows of K: [N], or with x_per_slot [N k]
+    int64_t ld_x, N;
+    const int32_t* idx;         // [N][k], or null (one matrix)
+    const float* weights;       // [N][k], or null
+    void* out;                  // rows of M: [N], or with idx and without weights [N k]
+    int64_t ld_out;
+    int G, M, K, k, x_per_slot;
+    int format;                 // 0: E2M1 with E8M0; 1: integers with scales of dt_scale
+    int shift;                  // log2(group / 32)
+    int dt_scale, dt_x, dt_out;
+    // set by the launch
+    int nv, parts;              // rows of a set, fp16 parts of a value
+    int64_t sets;
+    int kw, cap, blocks;        // warps of a team, units of K in shared memory, blocks of a set
+    int x_wide, scale_pairs;
+};
+cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s);
+
 // ------------------------------------------------------------------ tensor-core rate probe (peak.cu)
 enum ProbeKind : int { PROBE_MX_E2M1_E4M3 = 0, PROBE_MX_E4M3_E4M3 = 1, PROBE_BF16 = 2 };
 // grid CTAs each issue iters x 4 MMAs of M = 128 x n; *flops = their FLOPs
