@@ -492,7 +492,7 @@ struct MatvecArgs {
     int nv, parts;              // rows of a set, fp16 parts of a value
     int64_t sets;
     int kw, cap, blocks;        // warps of a team, units of K in shared memory, blocks of a set
-    int x_wide, scale_load;
+    int x_wide, scale_piece;
 };
 cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s);
 

@@ -47,6 +47,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 16;                // rows of a team's tile
 constexpr int kMvMaxThreads = 512;
 constexpr int kMaxSegs = 32;             // slots of a token
+constexpr int kMvSmem = 224 * 1024;      // dynamic shared memory of a block at most
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -87,106 +88,143 @@ __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&h)[4]) {
 // Kinds of scale: E8M0 (with E2M1 codes), two bytes or four (with integers).
 enum ScaleKind : int { SCALE_E8M0 = 0, SCALE_16 = 1, SCALE_32 = 2 };
 
-// How a row's scales are loaded: a pair of groups of 32 as one word (rows start on
-// whole words), one scale for both (groups of 64 and 128), or one by one.
-enum ScaleLoad : int { LOAD_PAIR = 0, LOAD_ONE = 1, LOAD_TWO = 2 };
-
-// What a lane loads for a unit of K of one matrix: its codes of rows g and g + 8
-// and the scales of its two accumulator columns in both rows, as they lie in memory
-// (a pair of 8 or 16 bits in s[0], s[2]).
-template <int LV>
-struct Codes {
-    uint32_t lo[LV / 4], hi[LV / 4];
-    uint32_t s[4];                       // row g: column 0, 1; row g + 8: column 0, 1
-};
-
-// The scales of groups kb and kb + 1 (of 32; the second may lie behind the last) of
-// the row at `row`.
-template <int SK>
-__device__ __forceinline__ void load_scales(const uint8_t* row, int kb, int KB, int shift, int how, uint32_t& s0, uint32_t& s1) {
-    using T = typename std::conditional<SK == SCALE_E8M0, uint8_t, typename std::conditional<SK == SCALE_16, uint16_t, uint32_t>::type>::type;
-    const T* r = reinterpret_cast<const T*>(row);
-    if (how == LOAD_PAIR) {
-        if constexpr (SK == SCALE_E8M0)
-            s0 = __ldg(reinterpret_cast<const uint16_t*>(r + kb));
-        else if constexpr (SK == SCALE_16)
-            s0 = __ldg(reinterpret_cast<const uint32_t*>(r + kb));
-        else {
-            const uint2 both = __ldg(reinterpret_cast<const uint2*>(r + kb));
-            s0 = both.x;
-            s1 = both.y;
-        }
-    } else if (how == LOAD_ONE) {
-        s0 = __ldg(r + (kb >> shift));
-    } else {
-        s0 = __ldg(r + kb);
-        s1 = kb + 1 < KB ? __ldg(r + kb + 1) : 0;
-    }
+__device__ __forceinline__ void ld_shared(uint32_t (&b)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(addr));
 }
+__device__ __forceinline__ void ld_shared(uint32_t (&b)[2], uint32_t addr) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(addr));
+}
+__device__ __forceinline__ void ld_shared(uint32_t (&b)[1], uint32_t addr) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+
+// Asynchronous copies to shared memory; zeros instead where `on` is not set.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Two scales as they lie in a word.
 template <int SK>
-__device__ __forceinline__ float2 scale_values(uint32_t s0, uint32_t s1, int how, bool bf16) {
+__device__ __forceinline__ float2 two_scales(uint32_t v, bool bf16) {
     if constexpr (SK == SCALE_E8M0) {
-        const uint16_t two = static_cast<uint16_t>(how == LOAD_PAIR ? s0 : s0 | (s1 << 8));
-        uint32_t v;                      // 2^-127 for code 0, NaN for 255
-        asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(v) : "h"(two));
-        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-    } else if constexpr (SK == SCALE_32) {
-        return make_float2(__uint_as_float(s0), __uint_as_float(how == LOAD_ONE ? s0 : s1));
+        uint32_t r;                      // 2^-127 for code 0, NaN for 255
+        asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+        return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
     } else {
-        const uint32_t v = how == LOAD_PAIR ? s0 : s0 | ((how == LOAD_ONE ? s0 : s1) << 16);
         if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
         __half2 h;
         memcpy(&h, &v, 4);
         return __half22float2(h);
     }
 }
-
-// Weights go by once: past L1.
-template <int LV>
-__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t (&w)[LV / 4]) {
-    if constexpr (LV == 16) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(p));
+// The scales of N (2 or 4) groups of 32 from group gi of a unit on; the row's scales of the unit lie at `row`.
+template <int SK, int N>
+__device__ __forceinline__ void read_scales(uint32_t row, int gi, int shift, bool bf16, float (&s)[N]) {
+    if constexpr (SK == SCALE_E8M0) {
+        if constexpr (N == 2) {
+            const float2 v = two_scales<SK>(ld_shared_u16(row + gi), false);
+            s[0] = v.x;
+            s[1] = v.y;
+        } else {
+            uint32_t w[1];
+            ld_shared(w, row + gi);
+            const float2 v = two_scales<SK>(w[0] & 0xFFFFu, false), u = two_scales<SK>(w[0] >> 16, false);
+            s[0] = v.x;
+            s[1] = v.y;
+            s[2] = u.x;
+            s[3] = u.y;
+        }
+    } else if constexpr (SK == SCALE_16) {
+        if (shift == 0) {
+            uint32_t w[N / 2];
+            ld_shared(w, row + 2 * gi);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float2 v = two_scales<SK>(w[i], bf16);
+                s[2 * i] = v.x;
+                s[2 * i + 1] = v.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) s[2 * i] = s[2 * i + 1] = two_scales<SK>(ld_shared_u16(row + 2 * ((gi + 2 * i) >> shift)), bf16).x;
+        }
     } else {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        uint32_t w[N];
+        if (shift == 0) {
+            ld_shared(w, row + 4 * gi);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                uint32_t v[1];
+                ld_shared(v, row + 4 * ((gi + 2 * i) >> shift));
+                s[2 * i] = s[2 * i + 1] = __uint_as_float(v[0]);
+            }
+        }
     }
 }
 
-__device__ __forceinline__ void ld_shared(uint32_t (&b)[4], uint32_t addr) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(addr));
+// The warps of a team: at most eight teams have more than one.
+__device__ __forceinline__ void team_sync(int team, int warps) {
+    if (warps == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(warps * 32) : "memory");
 }
 
-// Shared memory: x as fp16 [unit][word of 8][vector][lane of the row], 16 bytes each;
-// as many zero bytes as a unit has; factors [unit][vector][group] in fp32; the warps'
-// sums [2][team][matrix][warp][row][vector].
-template <int LV, int NT, bool DUAL>
+// A unit is 256 k of a team's 16 rows: 128 bytes of a row.  Its codes go by cp.async to a ring of D slots that each
+// warp has for itself, [half of 64 bytes][row][16 bytes], the four pieces of a row's half in an order that keeps the
+// reads free of bank conflicts.
+constexpr int kUK = 256;
+constexpr int kUnitGroups = kUK / 32;
+constexpr int kCodeBytes = kRows * kUK / 2;
+__device__ __forceinline__ int piece(int row, int i) { return i ^ (((row >> 2) & 1) | (row & 2)); }
+
+// GP groups of 32 share an MMA's columns (1, 2 or 4), 8 / GP vectors a tile of columns, NT tiles.  Shared memory: x as
+// fp16 [unit][half][part of GP groups][word of 8][vector][lane of the row], 16 bytes each; as many zero bytes as a
+// unit has (read by the lanes off the diagonal); factors of the groups in fp32; the warps' sums
+// [team][matrix][warp][vector][row]; the rings.
+template <int SK, int GP, int NT, bool DUAL, int D>
 struct Layout {
-    static constexpr int UK = 8 * LV;            // k of a unit: four lanes' codes
-    static constexpr int GP = UK / 32;           // groups of 32 in it
-    static constexpr int VT = 8 / GP;            // vectors of an MMA's columns
+    static constexpr int VT = 8 / GP;            // vectors of a tile
     static constexpr int VS = NT * VT;           // vectors there is room for
     static constexpr int NM = DUAL ? 2 : 1;
-    static constexpr int PF = 64 / LV / NM;      // units whose loads are in flight
-    static constexpr int kUnitX = UK * VS * 2, kUnitF = VS * GP * 4;
-    static constexpr int sums(int warps) { return 2 * NM * warps * kRows * VS * 4; }
+    static constexpr int kUnitX = kUK * VS * 2, kUnitF = VS * kUnitGroups * 4;
+    static constexpr int kZero = GP == 1 ? 0 : kUnitX;
+    static constexpr int kScaleRow = kUnitGroups * (SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4);
+    static constexpr int kSlot = NM * (kCodeBytes + kRows * kScaleRow);
+    static constexpr int kWarp = NM * kRows * VS * 4 + D * kSlot;     // of a warp: sums and ring
 };
 
-template <int SK, int LV, int NT, bool DUAL>
+template <int SK, int GP, int NT, bool DUAL, int D>
 __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs a) {
-    using L = Layout<LV, NT, DUAL>;
-    constexpr int UK = L::UK, GP = L::GP, VT = L::VT, VS = L::VS, NM = L::NM, PF = L::PF;
+    using L = Layout<SK, GP, NT, DUAL, D>;
+    constexpr int VT = L::VT, VS = L::VS, NM = L::NM, PARTS = 4 / GP;
+    constexpr int AC = GP == 1 ? 4 : 2;  // sums of a lane and tile: two rows, and two vectors where a column is one
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ int s_expert[kMaxSegs];
     __shared__ int64_t s_row[kMaxSegs];
     __shared__ float s_gate[kMaxSegs];
     __shared__ int s_segs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int KW = a.kw, team = warp / KW, kwarp = warp % KW, teams = (blockDim.x >> 5) / KW;
+    const int KW = a.kw, team = warp / KW, kwarp = warp % KW, warps = blockDim.x >> 5, teams = warps / KW;
     const int64_t set = static_cast<int64_t>(blockIdx.x) % a.sets;
     const int part = static_cast<int>(blockIdx.x / a.sets);
-    const int K = a.K, KB = K / 32, M = a.M, how = a.scale_load;
-    const int cps = (K + UK - 1) / UK;   // units of a segment
+    const int K = a.K, KB = K / 32, M = a.M;
+    const int cps = (K + kUK - 1) / kUK;   // units of a segment
     // the vectors: rows of x (one matrix), a slot's row, or a token's slots one behind the other
     const int nv = a.idx ? 1 : static_cast<int>(min(static_cast<int64_t>(a.nv), a.N - set * a.nv));
     if (warp == 0) {
@@ -213,24 +251,25 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
         }
         if (lane == 0) s_segs = n;
     }
-    const int cap = a.cap;               // units that fit
+    const int cap = a.cap;               // units of x that fit
     uint8_t* xv = sm;
     uint8_t* zero = xv + static_cast<size_t>(cap) * L::kUnitX;
-    float* xf = reinterpret_cast<float*>(zero + L::kUnitX);
-    float* red = xf + static_cast<size_t>(cap) * (VS * GP);
-    for (int i = threadIdx.x * 16; i < L::kUnitX; i += blockDim.x * 16) *reinterpret_cast<uint4*>(zero + i) = make_uint4(0, 0, 0, 0);
+    float* xf = reinterpret_cast<float*>(zero + L::kZero);
+    float* red = xf + static_cast<size_t>(cap) * (VS * kUnitGroups);
+    const uint32_t ring = smem_u32(red) + warps * (NM * kRows * VS * 4) + warp * (D * L::kSlot);
+    for (int i = threadIdx.x * 16; i < L::kZero; i += blockDim.x * 16) *reinterpret_cast<uint4*>(zero + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const int segs = s_segs, units = segs * cps;
 
     // x of the units [u0, u1) to shared memory: a thread takes eight values, four threads a group
     auto stage = [&](int u0, int u1) {
-        constexpr int per_unit = UK / 8;
+        constexpr int per_unit = kUK / 8;
         const int vvt = nv * a.parts, total = (u1 - u0) * per_unit * nv;
         for (int i0 = 0; i0 < total; i0 += blockDim.x) {
             const int i = i0 + threadIdx.x;
             const bool in = i < total;
             const int c = i % per_unit, rest = in ? i / per_unit : 0, u = nv == 1 ? rest : rest / nv, n = rest - u * nv;
-            const int seg = segs == 1 ? 0 : (u0 + u) / cps, k = ((u0 + u) - seg * cps) * UK + c * 8;
+            const int seg = segs == 1 ? 0 : (u0 + u) / cps, k = ((u0 + u) - seg * cps) * kUK + c * 8;
             float f[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = 0.0f;
@@ -259,13 +298,15 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
             int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
             ex = max(ex, a.parts == 1 ? -126 : -100);
             if (top == 0.0f) ex = 0;
-            const float to = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);     // 2^-126 at least: ex <= 113
+            const float to = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
             const float back = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= to;
-            const int word = LV == 16 ? c % 4 : c % 2, t = LV == 16 ? c / 4 : c / 2;
-            uint4* xo = reinterpret_cast<uint4*>(xv) + ((u * (LV / 4) + word) * VS) * 4 + t;
-            float* fo = xf + u * (VS * GP) + c / 4;
+            // lane t of a row holds the codes of 8 GP values of each part of 32 GP
+            const int of_part = c % (4 * GP), t = of_part / GP, word = of_part % GP, gi = c / 4;
+            uint4* xo = reinterpret_cast<uint4*>(xv) + ((u * (kUK / 32) + c / (4 * GP) * GP + word) * VS) * 4 + t;
+            float* fo = xf + u * (VS * kUnitGroups) + (GP == 1 ? gi * VS : gi);
+            constexpr int fs = GP == 1 ? 1 : kUnitGroups;
             for (int p = 0; p < a.parts; ++p) {
                 __half h[8];
 #pragma unroll
@@ -285,42 +326,37 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
                 const int vv = n * a.parts + p;
                 if (in) {
                     xo[vv * 4] = v;
-                    if ((c & 3) == 0) fo[vv * GP] = s_gate[seg] * back * __uint_as_float(static_cast<uint32_t>(127 - 12 * p) << 23);
+                    if ((c & 3) == 0) fo[vv * fs] = s_gate[seg] * back * __uint_as_float(static_cast<uint32_t>(127 - 12 * p) << 23);
                 }
             }
             if (in && n == 0)                                    // vectors that are not there
                 for (int vv = vvt; vv < VS; ++vv) {
                     xo[vv * 4] = make_uint4(0, 0, 0, 0);
-                    if ((c & 3) == 0) fo[vv * GP] = 0.0f;
+                    if ((c & 3) == 0) fo[vv * fs] = 0.0f;
                 }
         }
     };
 
     // this lane's places
-    const int64_t row_bytes = K / 2, srow_bytes = static_cast<int64_t>(KB >> a.shift) * (SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4);
-    const int kb_lane = LV == 16 ? 2 * (t4 & 1) : 0;                      // first group of its two columns
+    constexpr int kScaleSize = SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4;
+    const int64_t row_bytes = K / 2, srow_bytes = static_cast<int64_t>(KB >> a.shift) * kScaleSize;
     const bool bf16 = a.dt_scale == ELEM_BF16;
-    // B fragments: the lane's column is that of vector vb in group gb; values in the rows of that group's lanes,
-    // zeros elsewhere
-    const int vb = g / GP, gb = g % GP;
-    const bool diagonal = gb == (LV == 16 ? t4 : t4 / 2);
+    // B fragments: the lane's column is that of vector vb in group gb of a part; values in the rows of that group's
+    // lanes, zeros elsewhere
+    const int vb = g / GP;
+    const bool diagonal = g % GP == t4 * GP / 4;
     const uint32_t x_base = smem_u32(diagonal ? xv + (vb * 4 + t4) * 16 : zero);
     const uint32_t x_step = diagonal ? L::kUnitX : 0;
-    const int vc = LV == 16 ? t4 / 2 : t4;                               // vector of its accumulator columns
-    const float* f_lane = xf + vc * GP + kb_lane;
+    // its two accumulator columns: groups g2 and g2 + 1 of vector vc, or vectors vc and vc + 1
+    const int vc = GP == 4 ? t4 / 2 : GP == 2 ? t4 : 2 * t4, g2 = GP == 4 ? 2 * (t4 & 1) : 0;
+    const float* f_lane = xf + (GP == 1 ? vc : vc * kUnitGroups + g2);
+    // in a slot: where it puts its pieces of codes, and where it finds the codes of its MMA rows
+    const uint32_t put = g * 64 + piece(g, t4) * 16;
 
     const int tiles = (M + kRows - 1) / kRows;
     const int tile_step = a.blocks * teams;
-    struct Place {                       // the rows of a tile
-        int64_t lo, hi;
-    };
-    auto place = [&](int tile) {
-        return Place{min(static_cast<int64_t>(tile) * kRows + g, static_cast<int64_t>(M) - 1),
-                     min(static_cast<int64_t>(tile) * kRows + g + 8, static_cast<int64_t>(M) - 1)};
-    };
-    Codes<LV> q[PF][NM];
-    // unit u of the rows at p
-    auto fetch = [&](Codes<LV> (&w)[NM], const Place& p, int u) {
+    // unit u of the rows from r on to a slot
+    auto fetch = [&](uint32_t slot, int64_t r, int u) {
         int64_t e = s_expert[0];
         int c = u;
         if (segs > 1) {
@@ -328,134 +364,212 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
             c = u - seg * cps;
             e = s_expert[seg];
         }
-        const int64_t lo = e * M + p.lo, hi = e * M + p.hi;
-        const int k = c * UK + t4 * (2 * LV), kb = c * GP + kb_lane;
+        const int64_t last = M - 1;
+        const int64_t lo = e * M + min(r + g, last), hi = e * M + min(r + g + 8, last);
+        const int k = c * kUK + t4 * 32;
+        const bool on0 = k < K, on1 = k + 128 < K;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            const uint8_t* codes = (m ? a.up_codes : a.codes) + k / 2;
+            const uint8_t* codes = (m ? a.up_codes : a.codes) + (on0 ? k / 2 : 0);
+            const uint32_t to = slot + m * kCodeBytes + put;
+            const uint8_t *pl = codes + lo * row_bytes, *ph = codes + hi * row_bytes;
+            copy16(to, pl, on0);
+            copy16(to + 512, ph, on0);
+            copy16(to + 1024, on1 ? pl + 64 : pl, on1);
+            copy16(to + 1536, on1 ? ph + 64 : ph, on1);
+        }
+        // scales: pieces of 16, 8 or 4 bytes where all rows start on whole pieces, else one by one
+        const int bytes = (kUnitGroups >> a.shift) * kScaleSize;
+        const int size = a.scale_piece > 0 ? a.scale_piece : kScaleSize, lg = 31 - __clz(bytes / size);   // 2^lg pieces
+        const int64_t r0 = e * M + r;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), M - r)) - 1;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
             const uint8_t* scales = m ? a.up_scales : a.scales;
-            if (k < K) {
-                load_codes<LV>(codes + lo * row_bytes, w[m].lo);
-                load_codes<LV>(codes + hi * row_bytes, w[m].hi);
-            } else {
-#pragma unroll
-                for (int i = 0; i < LV / 4; ++i) w[m].lo[i] = w[m].hi[i] = 0;
-            }
-            w[m].s[0] = w[m].s[1] = w[m].s[2] = w[m].s[3] = 0;
-            if (kb < KB) {
-                load_scales<SK>(scales + lo * srow_bytes, kb, KB, a.shift, how, w[m].s[0], w[m].s[1]);
-                load_scales<SK>(scales + hi * srow_bytes, kb, KB, a.shift, how, w[m].s[2], w[m].s[3]);
+            const uint32_t to = slot + NM * kCodeBytes + m * (kRows * L::kScaleRow);
+            for (int i = lane; i < kRows << lg; i += 32) {
+                const int row = i >> lg, off = (i & ((1 << lg) - 1)) * size;
+                const int64_t at = static_cast<int64_t>(c) * bytes + off;
+                const bool on = at < srow_bytes;
+                const uint8_t* src = scales + (r0 + min(row, rows)) * srow_bytes + (on ? at : 0);
+                const uint32_t dst = to + row * L::kScaleRow + off;
+                if (a.scale_piece == 16)
+                    copy16(dst, src, on);
+                else if (a.scale_piece == 8)
+                    copy_small<8>(dst, src, on);
+                else if (a.scale_piece == 4)
+                    copy_small<4>(dst, src, on);
+                else if (kScaleSize == 1)
+                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst), "r"(static_cast<uint32_t>(on ? *src : 0)) : "memory");
+                else
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(on ? *reinterpret_cast<const uint16_t*>(src) : static_cast<uint16_t>(0)) : "memory");
             }
         }
     };
 
-    float acc[NM][NT][2];
-    // adds the products of a unit whose x is number ul in shared memory
-    auto work = [&](const Codes<LV> (&w)[NM], int ul) {
+    float acc[NM][NT][AC];
+    // adds the products of the unit in a slot, whose x is number ul in shared memory
+    auto work = [&](uint32_t slot, int ul) {
         const uint32_t x_at = x_base + ul * x_step;
-        float c[NM][NT][4];
+        const float* f_at = f_lane + ul * (VS * kUnitGroups);
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+        for (int half = 0; half < 2; ++half) {
+            float s4[NM][2][4];
+            if constexpr (GP == 1) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) c[m][n][0] = c[m][n][1] = c[m][n][2] = c[m][n][3] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < LV / 4; ++i) {
-            uint32_t b[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) ld_shared(b[n], x_at + (i * VS + n * VT) * 64);
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                uint32_t lo[4], hi[4];
-                if constexpr (SK == SCALE_E8M0) {
-                    e2m1_pairs(w[m].lo[i], lo);
-                    e2m1_pairs(w[m].hi[i], hi);
-                } else {
-                    int4_pairs(w[m].lo[i], lo);
-                    int4_pairs(w[m].hi[i], hi);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_16816(c[m][n], lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                    mma_16816(c[m][n], lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+                for (int m = 0; m < NM; ++m) {
+                    const uint32_t row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
+                    read_scales<SK, 4>(row, half * 4, a.shift, bf16, s4[m][0]);
+                    read_scales<SK, 4>(row + 8 * L::kScaleRow, half * 4, a.shift, bf16, s4[m][1]);
                 }
             }
-        }
-        // behind the last group codes, values and scales are zero
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const float2 s = scale_values<SK>(w[m].s[0], w[m].s[1], how, bf16), r = scale_values<SK>(w[m].s[2], w[m].s[3], how, bf16);
+            for (int part = 0; part < PARTS; ++part) {
+                uint32_t lo[NM][GP], hi[NM][GP];
+                // the lane's 4 GP bytes of the part's 16 GP in a row
+                const uint32_t at = slot + half * 1024 + g * 64 +
+                                    (GP == 4 ? piece(g, t4) * 16 : GP == 2 ? piece(g, 2 * part + t4 / 2) * 16 + (t4 & 1) * 8 : piece(g, part) * 16 + t4 * 4);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 f = *reinterpret_cast<const float2*>(f_lane + (ul * VS + n * VT) * GP);
-                acc[m][n][0] = fmaf(c[m][n][1] * s.y, f.y, fmaf(c[m][n][0] * s.x, f.x, acc[m][n][0]));
-                acc[m][n][1] = fmaf(c[m][n][3] * r.y, f.y, fmaf(c[m][n][2] * r.x, f.x, acc[m][n][1]));
+                for (int m = 0; m < NM; ++m) {
+                    ld_shared(lo[m], at + m * kCodeBytes);
+                    ld_shared(hi[m], at + m * kCodeBytes + 512);
+                }
+                float c[NM][NT][4];
+#pragma unroll
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) c[m][n][0] = c[m][n][1] = c[m][n][2] = c[m][n][3] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < GP; ++w) {
+                    uint32_t b[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) ld_shared(b[n], x_at + (((half * PARTS + part) * GP + w) * VS + n * VT) * 64);
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) {
+                        uint32_t p[4], q[4];
+                        if constexpr (SK == SCALE_E8M0) {
+                            e2m1_pairs(lo[m][w], p);
+                            e2m1_pairs(hi[m][w], q);
+                        } else {
+                            int4_pairs(lo[m][w], p);
+                            int4_pairs(hi[m][w], q);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_16816(c[m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
+                            mma_16816(c[m][n], p[2], q[2], p[3], q[3], b[n][2], b[n][3]);
+                        }
+                    }
+                }
+                // behind the last group codes, values and scales are zero
+                const int gi = half * 4 + part * GP;
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    if constexpr (GP == 1) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float2 f = *reinterpret_cast<const float2*>(f_at + gi * VS + n * VT);
+                            acc[m][n][0] = fmaf(c[m][n][0] * s4[m][0][part], f.x, acc[m][n][0]);
+                            acc[m][n][1] = fmaf(c[m][n][1] * s4[m][0][part], f.y, acc[m][n][1]);
+                            acc[m][n][2] = fmaf(c[m][n][2] * s4[m][1][part], f.x, acc[m][n][2]);
+                            acc[m][n][3] = fmaf(c[m][n][3] * s4[m][1][part], f.y, acc[m][n][3]);
+                        }
+                    } else {
+                        const uint32_t row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
+                        float s[2], r[2];
+                        read_scales<SK, 2>(row, gi + g2, a.shift, bf16, s);
+                        read_scales<SK, 2>(row + 8 * L::kScaleRow, gi + g2, a.shift, bf16, r);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float2 f = *reinterpret_cast<const float2*>(f_at + n * VT * kUnitGroups + gi);
+                            acc[m][n][0] = fmaf(c[m][n][1] * s[1], f.y, fmaf(c[m][n][0] * s[0], f.x, acc[m][n][0]));
+                            acc[m][n][1] = fmaf(c[m][n][3] * r[1], f.y, fmaf(c[m][n][2] * r[0], f.x, acc[m][n][1]));
+                        }
+                    }
+                }
             }
         }
     };
 
-    // A warp's units of a tile are a run of them, PF of them in flight; the loads of the next tile's first ones are
-    // issued while the last of this one's are worked on.
+    // A warp's units of a tile are a run of them; the copies of D units are in flight, those of the next tile's first
+    // ones while the last of this one's are worked on.  Each unit is a group of copies (or an empty one).
     const bool whole = units <= cap;     // all of x fits: staged once
-    bool ahead = false;                  // q holds the first units already
-    int flip = 0;
+    bool ahead = false;                  // the ring holds the first units already
+    int at = 0;                          // slot of the next unit
+    float* mine = red + team * (NM * KW * kRows * VS);
     for (int tile0 = part * teams; tile0 < tiles; tile0 += tile_step) {
         const int tile = tile0 + team;
         const bool live = tile < tiles;
-        const Place here = place(tile), next = place(tile + tile_step);
-        const bool more = whole && tile + tile_step < tiles;
+        const int64_t here = static_cast<int64_t>(tile) * kRows;
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = 0.0f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < AC; ++i) acc[m][n][i] = 0.0f;
         for (int u0 = 0; u0 < units; u0 += cap) {
             const int u1 = min(u0 + cap, units), per = (u1 - u0 + KW - 1) / KW;
-            const int first = min(u0 + kwarp * per, u1), last = min(first + per, u1);
-            if (live && !ahead)
-#pragma unroll
-                for (int i = 0; i < PF; ++i)
-                    if (first + i < last) fetch(q[i], here, first + i);
+            const int first = min(u0 + kwarp * per, u1), last = min(first + per, u1), run = last - first;
+            // the i-th unit from this run's first on: behind the run's last, the next tiles' (if x stays)
+            auto issue = [&](int i, uint32_t slot) {
+                int tl = tile;
+                while (i >= run && tl < tiles && run > 0) {
+                    i -= run;
+                    tl = whole ? tl + tile_step : tiles;
+                }
+                if (tl < tiles && i < run) fetch(slot, static_cast<int64_t>(tl) * kRows, first + i);
+                copy_commit();
+            };
+            if (live && !ahead) {
+                at = 0;
+                for (int i = 0; i < D; ++i) issue(i, ring + i * L::kSlot);
+            }
             if (!whole || tile0 == part * teams) {
                 __syncthreads();
                 stage(u0, u1);
                 __syncthreads();
             }
             if (!live) continue;
-            for (int ub = first; ub < last; ub += PF) {
-                const bool end = ub + PF >= last;
-#pragma unroll
-                for (int i = 0; i < PF; ++i) {
-                    if (ub + i < last) work(q[i], ub + i - u0);
-                    if (!end) {
-                        if (ub + PF + i < last) fetch(q[i], here, ub + PF + i);
-                    } else if (more && first + i < last) {
-                        fetch(q[i], next, first + i);
-                    }
-                }
+            for (int i = 0; i < run; ++i) {
+                copy_wait<D - 1>();
+                __syncwarp();
+                const uint32_t slot = ring + at * L::kSlot;
+                work(slot, first + i - u0);
+                __syncwarp();
+                issue(i + D, slot);
+                at = at + 1 == D ? 0 : at + 1;
             }
-            ahead = more;
+            ahead = whole;
         }
         // the warps' sums, then the rows' outputs
-        float* mine = red + (flip * teams + team) * (NM * KW * kRows * VS);
-        flip ^= 1;
         if (live) {
+            team_sync(team, KW);         // the last tile's are read
 #pragma unroll
             for (int m = 0; m < NM; ++m)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float lo = acc[m][n][0], hi = acc[m][n][1];
-                    if (LV == 16) {
-                        lo += __shfl_xor_sync(kAll, lo, 1);
-                        hi += __shfl_xor_sync(kAll, hi, 1);
-                    }
-                    if (LV == 8 || (t4 & 1) == 0) {
-                        mine[((m * KW + kwarp) * VS + n * VT + vc) * kRows + g] = lo;
-                        mine[((m * KW + kwarp) * VS + n * VT + vc) * kRows + g + 8] = hi;
+                    float* to = mine + ((m * KW + kwarp) * VS + n * VT + vc) * kRows + g;
+                    if constexpr (GP == 1) {
+                        to[0] = acc[m][n][0];
+                        to[kRows] = acc[m][n][1];
+                        to[8] = acc[m][n][2];
+                        to[kRows + 8] = acc[m][n][3];
+                    } else {
+                        float lo = acc[m][n][0], hi = acc[m][n][1];
+                        if (GP == 4) {
+                            lo += __shfl_xor_sync(kAll, lo, 1);
+                            hi += __shfl_xor_sync(kAll, hi, 1);
+                        }
+                        if (GP == 2 || (t4 & 1) == 0) {
+                            to[0] = lo;
+                            to[8] = hi;
+                        }
                     }
                 }
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(KW * 32) : "memory");
+            team_sync(team, KW);
             for (int o = threadIdx.x - team * KW * 32; o < kRows * nv; o += KW * 32) {
                 const int r = o % kRows, n = o / kRows;
-                const int64_t m = static_cast<int64_t>(tile) * kRows + r;
+                const int64_t m = here + r;
                 if (m >= M) continue;
                 float y[NM];
 #pragma unroll
@@ -475,18 +589,18 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
 // Warps of a block, of a team and blocks of a set.  Two blocks of 8 warps an SM where x fits, else one of 16.  A block
 // takes a set's tiles in rounds, a round as long as a warp's run of units and some three more for its start and end:
 // the split of K among a team's warps that makes that shortest.
-template <int SK, int LV, int NT, bool DUAL>
+template <int SK, int GP, int NT, bool DUAL, int D>
 cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
-    using L = Layout<LV, NT, DUAL>;
+    using L = Layout<SK, GP, NT, DUAL, D>;
     const int tiles = (a.M + kRows - 1) / kRows;
-    const int64_t units = static_cast<int64_t>(a.weights ? a.k : 1) * ((a.K + L::UK - 1) / L::UK);
+    const int64_t units = static_cast<int64_t>(a.weights ? a.k : 1) * ((a.K + kUK - 1) / kUK);
     const size_t unit_bytes = L::kUnitX + L::kUnitF;
-    const bool two = units * unit_bytes + L::kUnitX + L::sums(8) <= 108 * 1024;
+    const bool two = units * unit_bytes + L::kZero + 8 * L::kWarp <= 110 * 1024;
     const int warps = two ? 8 : 16, resident = two ? 304 : 152;
-    a.cap = static_cast<int>(std::min<int64_t>(units, (220 * 1024 - L::kUnitX - L::sums(16)) / unit_bytes));
-    const size_t smem = a.cap * unit_bytes + L::kUnitX + L::sums(warps);
+    a.cap = static_cast<int>(std::min<int64_t>(units, (kMvSmem - L::kZero - warps * L::kWarp) / unit_bytes));
+    const size_t smem = a.cap * unit_bytes + L::kZero + warps * L::kWarp;
     if (smem > 40 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(matvec_kernel<SK, LV, NT, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+        const cudaError_t err = cudaFuncSetAttribute(matvec_kernel<SK, GP, NT, DUAL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMvSmem);
         if (err != cudaSuccess) return err;
     }
     // a set of its own for each slot: some four rounds of blocks, as many of them may have nothing to do
@@ -496,24 +610,26 @@ cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
         const int teams = warps / kw;
         const int64_t blocks = std::min<int64_t>((tiles + teams - 1) / teams, most);
         const int64_t rounds = (tiles + blocks * teams - 1) / (blocks * teams), waves = (a.sets * blocks + resident - 1) / resident;
-        const int64_t cost = waves * rounds * ((units + kw - 1) / kw + 3);
+        const int64_t cost = waves * rounds * (2 * ((units + kw - 1) / kw) + 3);
         if (cost < best) {
             best = cost;
             a.kw = kw;
             a.blocks = static_cast<int>(blocks);
         }
     }
-    matvec_kernel<SK, LV, NT, DUAL><<<static_cast<unsigned>(a.sets * a.blocks), warps * 32, smem, s>>>(a);
+    matvec_kernel<SK, GP, NT, DUAL, D><<<static_cast<unsigned>(a.sets * a.blocks), warps * 32, smem, s>>>(a);
     return cudaGetLastError();
 }
 
+// Vectors (three for an fp32 row) against the columns of one MMA: four groups of a row's lanes and two vectors, two and
+// four, one and eight, or two MMAs of eight.
 template <int SK, bool DUAL>
 cudaError_t matvec_of(const MatvecArgs& a, cudaStream_t s) {
     const int vv = a.nv * a.parts;
-    if (vv <= 2) return matvec_as<SK, 16, 1, DUAL>(a, s);
-    if (vv <= 4) return matvec_as<SK, 8, 1, DUAL>(a, s);
-    if (vv <= 8) return matvec_as<SK, 8, 2, DUAL>(a, s);
-    return matvec_as<SK, 8, 3, DUAL>(a, s);
+    if (vv <= 2) return matvec_as<SK, 4, 1, DUAL, DUAL ? 2 : 3>(a, s);
+    if (vv <= 4) return matvec_as<SK, 2, 1, DUAL, DUAL ? 2 : 3>(a, s);
+    if (vv <= 8) return matvec_as<SK, 1, 1, DUAL, 2>(a, s);
+    return matvec_as<SK, 1, 2, DUAL, 2>(a, s);
 }
 
 }  // namespace
@@ -531,9 +647,10 @@ cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s) {
     if (a.sets == 0) return cudaSuccess;
     a.x_wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld_x * elem_bytes(a.dt_x)) % 16 == 0;
     const int size = a.format == 0 ? 1 : elem_bytes(a.dt_scale);
-    const bool pairs = (a.K / 32) % 2 == 0 && reinterpret_cast<uintptr_t>(a.scales) % (2 * size) == 0 &&
-                       reinterpret_cast<uintptr_t>(a.up_scales) % (2 * size) == 0;
-    a.scale_load = a.shift > 0 ? LOAD_ONE : pairs ? LOAD_PAIR : LOAD_TWO;
+    // pieces of a row's scales of a unit, as large as addresses and rows allow
+    const uint64_t lie = reinterpret_cast<uintptr_t>(a.scales) | reinterpret_cast<uintptr_t>(a.up_scales) |
+                         static_cast<uint64_t>((a.K / 32) >> a.shift) * size | static_cast<uint64_t>((kUnitGroups >> a.shift) * size);
+    a.scale_piece = lie % 16 == 0 ? 16 : lie % 8 == 0 ? 8 : lie % 4 == 0 ? 4 : 0;
     if (a.format == 0) return a.up_codes ? matvec_of<SCALE_E8M0, true>(a, s) : matvec_of<SCALE_E8M0, false>(a, s);
     if (a.dt_scale == ELEM_F32) return a.up_codes ? matvec_of<SCALE_32, true>(a, s) : matvec_of<SCALE_32, false>(a, s);
     return a.up_codes ? matvec_of<SCALE_16, true>(a, s) : matvec_of<SCALE_16, false>(a, s);
