@@ -47,14 +47,21 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 16;                // rows of a team's tile
 constexpr int kMvMaxThreads = 512;
 constexpr int kMaxSegs = 32;             // slots of a token
+constexpr int kStage = 4;                // loads of x that a thread has in flight
 constexpr int kMvSmem = 224 * 1024;      // dynamic shared memory of a block at most
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Eight codes as four pairs of fp16: E2M1 in order, (0, 1) (2, 3) (4, 5) (6, 7).
@@ -70,11 +77,16 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&h)[4]) {
 }
 // Integers c - 8, in the order (0, 4) (1, 5) (2, 6) (3, 7): a code in the low
 // bits of an fp16 1024 is 1024 + c, four bits higher 1024 + 16 c.
-__device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&h)[4]) {
+__device__ __forceinline__ uint32_t merged(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t r;                          // (w & mask) | bits
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+    return r;
+}
+__device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&h)[4], uint32_t mask, uint32_t bits) {
     const __half2 low = __float2half2_rn(-1032.0f), sixteenth = __float2half2_rn(0.0625f), high = __float2half2_rn(-72.0f);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const uint32_t a = ((w >> (8 * u)) & 0x000F000Fu) | 0x64006400u, b = ((w >> (8 * u)) & 0x00F000F0u) | 0x64006400u;
+        const uint32_t v = u ? w >> 8 : w, a = merged(v, mask, bits), b = merged(v, mask << 4, bits);
         __half2 p, q;
         memcpy(&p, &a, 4);
         memcpy(&q, &b, 4);
@@ -88,19 +100,21 @@ __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&h)[4]) {
 // Kinds of scale: E8M0 (with E2M1 codes), two bytes or four (with integers).
 enum ScaleKind : int { SCALE_E8M0 = 0, SCALE_16 = 1, SCALE_32 = 2 };
 
-__device__ __forceinline__ void ld_shared(uint32_t (&b)[4], uint32_t addr) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(addr));
-}
-__device__ __forceinline__ void ld_shared(uint32_t (&b)[2], uint32_t addr) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(addr));
-}
-__device__ __forceinline__ void ld_shared(uint32_t (&b)[1], uint32_t addr) {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b[0]) : "r"(addr));
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
+template <int N>
+__device__ __forceinline__ void ld_words(uint32_t (&b)[N], const uint8_t* p) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        b[0] = v.x;
+        b[1] = v.y;
+        b[2] = v.z;
+        b[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        b[0] = v.x;
+        b[1] = v.y;
+    } else {
+        b[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
 }
 
 // Asynchronous copies to shared memory; zeros instead where `on` is not set.
@@ -131,15 +145,15 @@ __device__ __forceinline__ float2 two_scales(uint32_t v, bool bf16) {
 }
 // The scales of N (2 or 4) groups of 32 from group gi of a unit on; the row's scales of the unit lie at `row`.
 template <int SK, int N>
-__device__ __forceinline__ void read_scales(uint32_t row, int gi, int shift, bool bf16, float (&s)[N]) {
+__device__ __forceinline__ void read_scales(const uint8_t* row, int gi, int shift, bool bf16, float (&s)[N]) {
     if constexpr (SK == SCALE_E8M0) {
         if constexpr (N == 2) {
-            const float2 v = two_scales<SK>(ld_shared_u16(row + gi), false);
+            const float2 v = two_scales<SK>(*reinterpret_cast<const uint16_t*>(row + gi), false);
             s[0] = v.x;
             s[1] = v.y;
         } else {
             uint32_t w[1];
-            ld_shared(w, row + gi);
+            ld_words(w, row + gi);
             const float2 v = two_scales<SK>(w[0] & 0xFFFFu, false), u = two_scales<SK>(w[0] >> 16, false);
             s[0] = v.x;
             s[1] = v.y;
@@ -149,7 +163,7 @@ __device__ __forceinline__ void read_scales(uint32_t row, int gi, int shift, boo
     } else if constexpr (SK == SCALE_16) {
         if (shift == 0) {
             uint32_t w[N / 2];
-            ld_shared(w, row + 2 * gi);
+            ld_words(w, row + 2 * gi);
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
                 const float2 v = two_scales<SK>(w[i], bf16);
@@ -158,19 +172,19 @@ __device__ __forceinline__ void read_scales(uint32_t row, int gi, int shift, boo
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) s[2 * i] = s[2 * i + 1] = two_scales<SK>(ld_shared_u16(row + 2 * ((gi + 2 * i) >> shift)), bf16).x;
+            for (int i = 0; i < N / 2; ++i) s[2 * i] = s[2 * i + 1] = two_scales<SK>(*reinterpret_cast<const uint16_t*>(row + 2 * ((gi + 2 * i) >> shift)), bf16).x;
         }
     } else {
         uint32_t w[N];
         if (shift == 0) {
-            ld_shared(w, row + 4 * gi);
+            ld_words(w, row + 4 * gi);
 #pragma unroll
             for (int i = 0; i < N; ++i) s[i] = __uint_as_float(w[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
                 uint32_t v[1];
-                ld_shared(v, row + 4 * ((gi + 2 * i) >> shift));
+                ld_words(v, row + 4 * ((gi + 2 * i) >> shift));
                 s[2 * i] = s[2 * i + 1] = __uint_as_float(v[0]);
             }
         }
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
     const int KW = a.kw, team = warp / KW, kwarp = warp % KW, warps = blockDim.x >> 5, teams = warps / KW;
     const int64_t set = static_cast<int64_t>(blockIdx.x) % a.sets;
     const int part = static_cast<int>(blockIdx.x / a.sets);
-    const int K = a.K, KB = K / 32, M = a.M;
+    const int K = a.K, M = a.M;
     const int cps = (K + kUK - 1) / kUK;   // units of a segment
     // the vectors: rows of x (one matrix), a slot's row, or a token's slots one behind the other
     const int nv = a.idx ? 1 : static_cast<int>(min(static_cast<int64_t>(a.nv), a.N - set * a.nv));
@@ -256,7 +270,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
     uint8_t* zero = xv + static_cast<size_t>(cap) * L::kUnitX;
     float* xf = reinterpret_cast<float*>(zero + L::kZero);
     float* red = xf + static_cast<size_t>(cap) * (VS * kUnitGroups);
-    const uint32_t ring = smem_u32(red) + warps * (NM * kRows * VS * 4) + warp * (D * L::kSlot);
+    uint8_t* ring = reinterpret_cast<uint8_t*>(red) + warps * (NM * kRows * VS * 4) + warp * (D * L::kSlot);
     for (int i = threadIdx.x * 16; i < L::kZero; i += blockDim.x * 16) *reinterpret_cast<uint4*>(zero + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const int segs = s_segs, units = segs * cps;
@@ -265,25 +279,31 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
     auto stage = [&](int u0, int u1) {
         constexpr int per_unit = kUK / 8;
         const int vvt = nv * a.parts, total = (u1 - u0) * per_unit * nv;
-        for (int i0 = 0; i0 < total; i0 += blockDim.x) {
-            const int i = i0 + threadIdx.x;
+        for (int i0 = 0; i0 < total; i0 += kStage * blockDim.x) {
+            RawVec<8> raw[kStage];
+#pragma unroll
+            for (int j = 0; j < kStage; ++j) {
+                const int i = i0 + j * blockDim.x + threadIdx.x;
+                const int c = i % per_unit, rest = i / per_unit, u = nv == 1 ? rest : rest / nv, n = rest - u * nv;
+                const int seg = segs == 1 ? 0 : (u0 + u) / cps, k = ((u0 + u) - seg * cps) * kUK + c * 8;
+                raw[j].a = raw[j].b = make_uint4(0, 0, 0, 0);
+                if (a.x_wide && i < total && k < K) raw[j] = load_raw<8>(a.x, (s_row[seg] + n) * a.ld_x + k, a.dt_x);
+            }
+#pragma unroll
+          for (int j = 0; j < kStage; ++j) {
+            if (i0 + j * blockDim.x >= total) break;
+            const int i = i0 + j * blockDim.x + threadIdx.x;
             const bool in = i < total;
             const int c = i % per_unit, rest = in ? i / per_unit : 0, u = nv == 1 ? rest : rest / nv, n = rest - u * nv;
             const int seg = segs == 1 ? 0 : (u0 + u) / cps, k = ((u0 + u) - seg * cps) * kUK + c * 8;
             float f[8];
+            raw_to_f32(raw[j], a.dt_x, f);
+            if (!a.x_wide && in && k < K) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-            if (in && k < K) {
-                const int64_t off = (s_row[seg] + n) * a.ld_x + k;
-                if (a.x_wide) {
-                    raw_to_f32(load_raw<8>(a.x, off, a.dt_x), a.dt_x, f);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float e[1];
-                        raw_to_f32(load_raw<1>(a.x, off + j, a.dt_x), a.dt_x, e);
-                        f[j] = e[0];
-                    }
+                for (int x = 0; x < 8; ++x) {
+                    float e[1];
+                    raw_to_f32(load_raw<1>(a.x, (s_row[seg] + n) * a.ld_x + k + x, a.dt_x), a.dt_x, e);
+                    f[x] = e[0];
                 }
             }
             float top = 0.0f;
@@ -334,83 +354,119 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
                     xo[vv * 4] = make_uint4(0, 0, 0, 0);
                     if ((c & 3) == 0) fo[vv * fs] = 0.0f;
                 }
+          }
         }
     };
 
     // this lane's places
     constexpr int kScaleSize = SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4;
-    const int64_t row_bytes = K / 2, srow_bytes = static_cast<int64_t>(KB >> a.shift) * kScaleSize;
+    const int64_t row_bytes = K / 2, srow_bytes = static_cast<int64_t>(K / 32 >> a.shift) * kScaleSize;
     const bool bf16 = a.dt_scale == ELEM_BF16;
     // B fragments: the lane's column is that of vector vb in group gb of a part; values in the rows of that group's
     // lanes, zeros elsewhere
     const int vb = g / GP;
     const bool diagonal = g % GP == t4 * GP / 4;
-    const uint32_t x_base = smem_u32(diagonal ? xv + (vb * 4 + t4) * 16 : zero);
+    const uint8_t* x_base = diagonal ? xv + (vb * 4 + t4) * 16 : zero;
     const uint32_t x_step = diagonal ? L::kUnitX : 0;
     // its two accumulator columns: groups g2 and g2 + 1 of vector vc, or vectors vc and vc + 1
     const int vc = GP == 4 ? t4 / 2 : GP == 2 ? t4 : 2 * t4, g2 = GP == 4 ? 2 * (t4 & 1) : 0;
     const float* f_lane = xf + (GP == 1 ? vc : vc * kUnitGroups + g2);
-    // in a slot: where it puts its pieces of codes, and where it finds the codes of its MMA rows
-    const uint32_t put = g * 64 + piece(g, t4) * 16;
 
     const int tiles = (M + kRows - 1) / kRows;
     const int tile_step = a.blocks * teams;
-    // unit u of the rows from r on to a slot
-    auto fetch = [&](uint32_t slot, int64_t r, int u) {
-        int64_t e = s_expert[0];
-        int c = u;
-        if (segs > 1) {
-            const int seg = u / cps;
-            c = u - seg * cps;
-            e = s_expert[seg];
-        }
-        const int64_t last = M - 1;
-        const int64_t lo = e * M + min(r + g, last), hi = e * M + min(r + g + 8, last);
-        const int k = c * kUK + t4 * 32;
-        const bool on0 = k < K, on1 = k + 128 < K;
+    // The next unit to copy: pointers of this lane's pieces of codes (row g, row g + 8) and of scales, which move along a
+    // segment.  Scales go by pieces of 16, 8 or 4 bytes where all rows start on whole pieces, else one by one.
+    const int unit_scales = (kUnitGroups >> a.shift) * kScaleSize;                    // bytes of a row
+    const int size = a.scale_piece > 0 ? a.scale_piece : kScaleSize, lg = 31 - __clz(unit_scales / size);
+    const int srow = lane >> lg, soff = (lane & ((1 << lg) - 1)) * size, sstep = 32 >> lg;
+    const uint32_t put = g * 64 + piece(g, t4) * 16;
+    struct {
+        int tile, u, c;                  // tile, unit, unit in its segment
+        const uint8_t *lo[NM], *hi[NM], *s[NM];
+        int64_t back;                    // from the scales' pointer to the first row's
+        int rows;                        // from the tile's first to the matrix' last
+    } cur;
+    auto aim = [&](int tile, int u) {
+        cur.tile = tile;
+        cur.u = u;
+        const int seg = segs > 1 ? u / cps : 0;
+        cur.c = u - seg * cps;
+        const int r = tile * kRows;
+        cur.rows = M - r;
+        const int64_t row = static_cast<int64_t>(s_expert[seg]) * M + r;
+        const int64_t lo = (row + (g < cur.rows ? g : 0)) * row_bytes + cur.c * (kUK / 2) + t4 * 16, up = g + 8 < cur.rows ? 8 * row_bytes : 0;
+        const int64_t of_row = min(srow, kRows) * srow_bytes + soff, sc = row * srow_bytes + static_cast<int64_t>(cur.c) * unit_scales + of_row;
+        cur.back = -of_row;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            const uint8_t* codes = (m ? a.up_codes : a.codes) + (on0 ? k / 2 : 0);
-            const uint32_t to = slot + m * kCodeBytes + put;
-            const uint8_t *pl = codes + lo * row_bytes, *ph = codes + hi * row_bytes;
-            copy16(to, pl, on0);
-            copy16(to + 512, ph, on0);
-            copy16(to + 1024, on1 ? pl + 64 : pl, on1);
-            copy16(to + 1536, on1 ? ph + 64 : ph, on1);
+            cur.lo[m] = (m ? a.up_codes : a.codes) + lo;
+            cur.hi[m] = cur.lo[m] + up;
+            cur.s[m] = (m ? a.up_scales : a.scales) + sc;
         }
-        // scales: pieces of 16, 8 or 4 bytes where all rows start on whole pieces, else one by one
-        const int bytes = (kUnitGroups >> a.shift) * kScaleSize;
-        const int size = a.scale_piece > 0 ? a.scale_piece : kScaleSize, lg = 31 - __clz(bytes / size);   // 2^lg pieces
-        const int64_t r0 = e * M + r;
-        const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), M - r)) - 1;
+    };
+    auto copy_scales = [&](uint32_t dst, const uint8_t* src, bool on) {
+        if (a.scale_piece == 8)
+            copy_small<8>(dst, src, on);
+        else if (a.scale_piece == 16)
+            copy16(dst, src, on);
+        else if (a.scale_piece == 4)
+            copy_small<4>(dst, src, on);
+        else if (kScaleSize == 1)
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst), "r"(static_cast<uint32_t>(on ? *src : 0)) : "memory");
+        else
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(on ? *reinterpret_cast<const uint16_t*>(src) : static_cast<uint16_t>(0)) : "memory");
+    };
+    auto fetch = [&](uint8_t* slot) {
+        const int left = K - cur.c * kUK;
+        const uint32_t to = smem_u32(slot) + put, sto = smem_u32(slot) + NM * kCodeBytes + srow * L::kScaleRow + soff;
+        if (left >= kUK && cur.rows >= kRows) {
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const uint8_t* scales = m ? a.up_scales : a.scales;
-            const uint32_t to = slot + NM * kCodeBytes + m * (kRows * L::kScaleRow);
-            for (int i = lane; i < kRows << lg; i += 32) {
-                const int row = i >> lg, off = (i & ((1 << lg) - 1)) * size;
-                const int64_t at = static_cast<int64_t>(c) * bytes + off;
-                const bool on = at < srow_bytes;
-                const uint8_t* src = scales + (r0 + min(row, rows)) * srow_bytes + (on ? at : 0);
-                const uint32_t dst = to + row * L::kScaleRow + off;
-                if (a.scale_piece == 16)
-                    copy16(dst, src, on);
-                else if (a.scale_piece == 8)
-                    copy_small<8>(dst, src, on);
-                else if (a.scale_piece == 4)
-                    copy_small<4>(dst, src, on);
-                else if (kScaleSize == 1)
-                    asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst), "r"(static_cast<uint32_t>(on ? *src : 0)) : "memory");
-                else
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(on ? *reinterpret_cast<const uint16_t*>(src) : static_cast<uint16_t>(0)) : "memory");
+            for (int m = 0; m < NM; ++m) {
+                copy16(to + m * kCodeBytes, cur.lo[m], true);
+                copy16(to + m * kCodeBytes + 512, cur.hi[m], true);
+                copy16(to + m * kCodeBytes + 1024, cur.lo[m] + 64, true);
+                copy16(to + m * kCodeBytes + 1536, cur.hi[m] + 64, true);
+                if (srow < kRows) copy_scales(sto + m * (kRows * L::kScaleRow), cur.s[m], true);
+                for (int row = sstep; srow + row < kRows; row += sstep)
+                    copy_scales(sto + m * (kRows * L::kScaleRow) + row * L::kScaleRow, cur.s[m] + row * srow_bytes, true);
+            }
+        } else {
+            // behind the row's end the first address of its unit, which is not read
+            const bool on0 = t4 * 32 < left, on1 = t4 * 32 + 128 < left;
+            const int sleft = static_cast<int>(srow_bytes) - cur.c * unit_scales;        // K / 8 at most
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const uint8_t *lo = cur.lo[m] - (on0 ? 0 : t4 * 16), *hi = cur.hi[m] - (on0 ? 0 : t4 * 16);
+                copy16(to + m * kCodeBytes, lo, on0 && g < cur.rows);
+                copy16(to + m * kCodeBytes + 512, hi, on0 && g + 8 < cur.rows);
+                copy16(to + m * kCodeBytes + 1024, lo + (on1 ? 64 : 0), on1 && g < cur.rows);
+                copy16(to + m * kCodeBytes + 1536, hi + (on1 ? 64 : 0), on1 && g + 8 < cur.rows);
+                for (int row = 0; srow + row < kRows; row += sstep) {
+                    const bool on = soff < sleft && srow + row < cur.rows;
+                    copy_scales(sto + m * (kRows * L::kScaleRow) + row * L::kScaleRow, cur.s[m] + (on ? row * srow_bytes : cur.back), on);
+                }
+            }
+        }
+        ++cur.u;
+        if (++cur.c == cps && cur.u < units) {
+            aim(cur.tile, cur.u);
+        } else {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                cur.lo[m] += kUK / 2;
+                cur.hi[m] += kUK / 2;
+                cur.s[m] += unit_scales;
             }
         }
     };
 
+    // in registers: an instruction takes one constant
+    uint32_t mask4 = 0x000F000Fu, bits4 = 0x64006400u;
+    asm volatile("" : "+r"(mask4), "+r"(bits4));
     float acc[NM][NT][AC];
     // adds the products of the unit in a slot, whose x is number ul in shared memory
-    auto work = [&](uint32_t slot, int ul) {
-        const uint32_t x_at = x_base + ul * x_step;
+    auto work = [&](const uint8_t* slot, int ul) {
+        const uint8_t* x_at = x_base + ul * x_step;
         const float* f_at = f_lane + ul * (VS * kUnitGroups);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -418,7 +474,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
             if constexpr (GP == 1) {
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
-                    const uint32_t row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
+                    const uint8_t* row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
                     read_scales<SK, 4>(row, half * 4, a.shift, bf16, s4[m][0]);
                     read_scales<SK, 4>(row + 8 * L::kScaleRow, half * 4, a.shift, bf16, s4[m][1]);
                 }
@@ -427,23 +483,19 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
             for (int part = 0; part < PARTS; ++part) {
                 uint32_t lo[NM][GP], hi[NM][GP];
                 // the lane's 4 GP bytes of the part's 16 GP in a row
-                const uint32_t at = slot + half * 1024 + g * 64 +
+                const uint8_t* at = slot + half * 1024 + g * 64 +
                                     (GP == 4 ? piece(g, t4) * 16 : GP == 2 ? piece(g, 2 * part + t4 / 2) * 16 + (t4 & 1) * 8 : piece(g, part) * 16 + t4 * 4);
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
-                    ld_shared(lo[m], at + m * kCodeBytes);
-                    ld_shared(hi[m], at + m * kCodeBytes + 512);
+                    ld_words(lo[m], at + m * kCodeBytes);
+                    ld_words(hi[m], at + m * kCodeBytes + 512);
                 }
                 float c[NM][NT][4];
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) c[m][n][0] = c[m][n][1] = c[m][n][2] = c[m][n][3] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < GP; ++w) {
                     uint32_t b[NT][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) ld_shared(b[n], x_at + (((half * PARTS + part) * GP + w) * VS + n * VT) * 64);
+                    for (int n = 0; n < NT; ++n) ld_words(b[n], x_at + (((half * PARTS + part) * GP + w) * VS + n * VT) * 64);
 #pragma unroll
                     for (int m = 0; m < NM; ++m) {
                         uint32_t p[4], q[4];
@@ -451,12 +503,15 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
                             e2m1_pairs(lo[m][w], p);
                             e2m1_pairs(hi[m][w], q);
                         } else {
-                            int4_pairs(lo[m][w], p);
-                            int4_pairs(hi[m][w], q);
+                            int4_pairs(lo[m][w], p, mask4, bits4);
+                            int4_pairs(hi[m][w], q, mask4, bits4);
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            mma_16816(c[m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
+                            if (w == 0)
+                                mma_16816_first(c[m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
+                            else
+                                mma_16816(c[m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
                             mma_16816(c[m][n], p[2], q[2], p[3], q[3], b[n][2], b[n][3]);
                         }
                     }
@@ -475,7 +530,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
                             acc[m][n][3] = fmaf(c[m][n][3] * s4[m][1][part], f.y, acc[m][n][3]);
                         }
                     } else {
-                        const uint32_t row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
+                        const uint8_t* row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
                         float s[2], r[2];
                         read_scales<SK, 2>(row, gi + g2, a.shift, bf16, s);
                         read_scales<SK, 2>(row + 8 * L::kScaleRow, gi + g2, a.shift, bf16, r);
@@ -500,7 +555,6 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
     for (int tile0 = part * teams; tile0 < tiles; tile0 += tile_step) {
         const int tile = tile0 + team;
         const bool live = tile < tiles;
-        const int64_t here = static_cast<int64_t>(tile) * kRows;
 #pragma unroll
         for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -510,19 +564,16 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
         for (int u0 = 0; u0 < units; u0 += cap) {
             const int u1 = min(u0 + cap, units), per = (u1 - u0 + KW - 1) / KW;
             const int first = min(u0 + kwarp * per, u1), last = min(first + per, u1), run = last - first;
-            // the i-th unit from this run's first on: behind the run's last, the next tiles' (if x stays)
-            auto issue = [&](int i, uint32_t slot) {
-                int tl = tile;
-                while (i >= run && tl < tiles && run > 0) {
-                    i -= run;
-                    tl = whole ? tl + tile_step : tiles;
-                }
-                if (tl < tiles && i < run) fetch(slot, static_cast<int64_t>(tl) * kRows, first + i);
+            // the next unit of this run, or (if x stays) the first of the next tile's
+            auto issue = [&](uint8_t* slot) {
+                if (cur.u >= last && whole && run > 0 && cur.tile + tile_step < tiles) aim(cur.tile + tile_step, first);
+                if (cur.u < last) fetch(slot);
                 copy_commit();
             };
             if (live && !ahead) {
                 at = 0;
-                for (int i = 0; i < D; ++i) issue(i, ring + i * L::kSlot);
+                aim(tile, first);
+                for (int i = 0; i < D; ++i) issue(ring + i * L::kSlot);
             }
             if (!whole || tile0 == part * teams) {
                 __syncthreads();
@@ -533,10 +584,10 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
             for (int i = 0; i < run; ++i) {
                 copy_wait<D - 1>();
                 __syncwarp();
-                const uint32_t slot = ring + at * L::kSlot;
+                uint8_t* slot = ring + at * L::kSlot;
                 work(slot, first + i - u0);
                 __syncwarp();
-                issue(i + D, slot);
+                issue(slot);
                 at = at + 1 == D ? 0 : at + 1;
             }
             ahead = whole;
@@ -569,7 +620,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
             team_sync(team, KW);
             for (int o = threadIdx.x - team * KW * 32; o < kRows * nv; o += KW * 32) {
                 const int r = o % kRows, n = o / kRows;
-                const int64_t m = here + r;
+                const int64_t m = static_cast<int64_t>(tile) * kRows + r;
                 if (m >= M) continue;
                 float y[NM];
 #pragma unroll
@@ -610,7 +661,7 @@ cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
         const int teams = warps / kw;
         const int64_t blocks = std::min<int64_t>((tiles + teams - 1) / teams, most);
         const int64_t rounds = (tiles + blocks * teams - 1) / (blocks * teams), waves = (a.sets * blocks + resident - 1) / resident;
-        const int64_t cost = waves * rounds * (2 * ((units + kw - 1) / kw) + 3);
+        const int64_t cost = waves * rounds * (2 * ((units + kw - 1) / kw) + 1);
         if (cost < best) {
             best = cost;
             a.kw = kw;
