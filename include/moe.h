@@ -552,7 +552,8 @@ MOE_API moe_status moe_mx4_gemm(const uint8_t *a_codes, const uint8_t *a_scales,
  * it; products and sums are fp32.  x's rows go by 16 bytes where address and
  * stride are multiples of 16 bytes, else element by element.  T >= 0, T k <
  * 2^31, 1 <= k <= 32, M >= 1, G M <= 2^31 - 256, K a multiple of the group up
- * to 2^24. */
+ * to 2^24.  dev_status receives a non-zero code if a bounded wait inside the
+ * kernel ran out, as with moe_mx_gemm. */
 typedef enum {
     MOE_W4_MXFP4 = 0,
     MOE_W4_INT4 = 1
@@ -575,6 +576,7 @@ typedef struct {
     int32_t format;           /* moe_w4_format */
     int32_t scale_dtype;      /* MOE_W4_INT4 */
     int32_t x_dtype, out_dtype;
+    int32_t *dev_status;      /* device int32, or NULL */
 } moe_w4_matvec_args;
 MOE_API moe_status moe_w4_matvec(const moe_w4_matvec_args *args, void *stream);
 

@@ -55,7 +55,7 @@ class _W4MatvecArgs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("codes", "scales", "up_codes", "up_scales", "x")] + [("ld_x", C.c_int64)] + \
                [(n, C.c_void_p) for n in ("idx", "weights", "out")] + [("ld_out", C.c_int64)] + \
                [(n, C.c_int32) for n in ("T", "k", "G", "M", "K", "group", "x_per_slot", "format", "scale_dtype", "x_dtype",
-                                         "out_dtype")]
+                                         "out_dtype")] + [("dev_status", C.c_void_p)]
 
 
 def declare(L):
@@ -596,7 +596,7 @@ def _w4(codes, scales, dims, dev, what):
 
 def w4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, up=None, idx: Optional[torch.Tensor] = None,
               weights: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
-              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+              out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Products of a few rows with four-bit weights (see moe_w4_matvec), x not
     quantised.  scales uint8: MXFP4 as mxfp4_quantize writes it; scales float32,
     bfloat16 or float16: codes 0 to 15 that stand for -8 to 7.  One matrix codes
@@ -608,7 +608,8 @@ def w4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, up=
     what = "w4_matvec"
     dev = _device(x, what)
     if dev != _current() or stream is not None:
-        return _on(dev, stream, w4_matvec, x, codes, scales, up=up, idx=idx, weights=weights, out_dtype=out_dtype, out=out)
+        return _on(dev, stream, w4_matvec, x, codes, scales, up=up, idx=idx, weights=weights, out_dtype=out_dtype, out=out,
+                   status=status)
     codes, scales, group = _w4(codes, scales, 2 if idx is None else 3, dev, what)
     M, K = codes.shape[-2], 2 * codes.shape[-1]
     if up is not None:
@@ -643,6 +644,8 @@ def w4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, up=
     dtype = out_dtype or (x.dtype if out is None else out.dtype)
     if dtype not in DTYPES:
         _bad(what + ": output type")
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev):
+        _bad(what + ": status is int32 on x's device")
     shape = lead + (M,)
     n = T if len(lead) < 2 else T * k
     if out is None:
@@ -654,7 +657,7 @@ def w4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, up=
         a = _W4MatvecArgs(codes.data_ptr(), scales.data_ptr(), None if up is None else up_codes.data_ptr(),
                           None if up is None else up_scales.data_ptr(), xr.data_ptr(), ld, _p(idx), _p(weights), out.data_ptr(),
                           ld_out, T, k, G, M, K, group, per_slot, W4_INT4 if ints else W4_MXFP4,
-                          DTYPES[scales.dtype] if ints else 0, DTYPES[xr.dtype], DTYPES[dtype])
+                          DTYPES[scales.dtype] if ints else 0, DTYPES[xr.dtype], DTYPES[dtype], _p(status))
         code = lib().moe_w4_matvec(a, _raw_stream(dev))
         if code:
             _check(code, "moe_w4_matvec")

@@ -1511,6 +1511,12 @@ bool map_fp4(CUtensorMap* m, const void* codes, int64_t rows, int64_t K, int box
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The codes of a product of a few rows, a box a unit of its kernel.
+bool matvec_maps(MatvecArgs& a) {
+    const int64_t rows = static_cast<int64_t>(a.G) * a.M;
+    return map_fp4(&a.map, a.codes, rows, a.K, 16) && (!a.up_codes || map_fp4(&a.up_map, a.up_codes, rows, a.K, 16));
+}
+
 // Their scales [rows][K / 32], boxes of 32 bytes (1,024 elements) x box_rows.
 bool map_fp4_scales(CUtensorMap* m, const void* scales, int64_t rows, int64_t K, int box_rows) {
     EncodeTiledFn f = encode_fn();
@@ -1776,8 +1782,10 @@ moe_status moe_w4_matvec(const moe_w4_matvec_args* p, void* stream) {
         return MOE_ERR_INVALID_ARG;
     if (ints && (!aligned_elem(p->scales, p->scale_dtype) || !aligned_elem(p->up_scales, p->scale_dtype)))
         return MOE_ERR_INVALID_ARG;
-    if (!matrix_ok(p->x, p->ld_x, p->x_dtype, p->K) || !matrix_ok(p->out, p->ld_out, p->out_dtype, p->M))
+    if (!matrix_ok(p->x, p->ld_x, p->x_dtype, p->K) || !matrix_ok(p->out, p->ld_out, p->out_dtype, p->M) ||
+        !aligned(p->dev_status, 4))
         return MOE_ERR_INVALID_ARG;
+    if (!encode_fn()) return MOE_ERR_UNSUPPORTED;
     MatvecArgs a = {};
     a.codes = p->codes;
     a.scales = static_cast<const uint8_t*>(p->scales);
@@ -1800,6 +1808,8 @@ moe_status moe_w4_matvec(const moe_w4_matvec_args* p, void* stream) {
     a.dt_scale = ints ? p->scale_dtype : MOE_DTYPE_F32;
     a.dt_x = p->x_dtype;
     a.dt_out = p->out_dtype;
+    a.status = p->dev_status;
+    a.make_maps = matvec_maps;
     return cuda_status(launch_matvec(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -474,6 +474,7 @@ cudaError_t launch_router_backward(RouterBackArgs a, cudaStream_t s);
 
 // ------------------------------------------------------------------ products of a few rows (matvec.cu)
 struct MatvecArgs {
+    CUtensorMap map, up_map;    // the codes as [G M][K / 2] bytes, boxes of 128 bytes x 16 rows, 128-byte swizzle
     const uint8_t* codes;       // [G][M][K / 2]
     const uint8_t* scales;      // [G][M][K / group]
     const uint8_t* up_codes;    // a second matrix of the same sizes, or null
@@ -488,11 +489,16 @@ struct MatvecArgs {
     int format;                 // 0: E2M1 with E8M0; 1: integers with scales of dt_scale
     int shift;                  // log2(group / 32)
     int dt_scale, dt_x, dt_out;
+    int* status;                // or null: receives a code if a wait inside the kernel ran out
+    bool (*make_maps)(MatvecArgs& a);
     // set by the launch
     int nv, parts;              // rows of a set, fp16 parts of a value
     int64_t sets;
-    int kw, cap, blocks;        // warps of a team, units of K in shared memory, blocks of a set
-    int x_wide, scale_piece;
+    int kw_log, cap, blocks;    // log2 of a team's warps, units of x in shared memory, blocks of a set
+    int cps, tiles;             // units of a segment, tiles of rows
+    int x_wide, scale_piece;    // x's rows by 16 bytes; bytes of a copy of scales, 0: one by one
+    int scale_size, scale_log;  // bytes of a piece, log2 of a row's pieces in a unit
+    int unit_scales, srow;      // bytes of a row's scales in a unit, and of all
 };
 cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s);
 

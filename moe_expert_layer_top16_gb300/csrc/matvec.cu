@@ -47,8 +47,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 16;                // rows of a team's tile
 constexpr int kMvMaxThreads = 512;
 constexpr int kMaxSegs = 32;             // slots of a token
-constexpr int kStage = 4;                // loads of x that a thread has in flight
-constexpr int kMvSmem = 224 * 1024;      // dynamic shared memory of a block at most
+constexpr int kMvSmem = 222 * 1024;      // dynamic shared memory of a block at most, but for the first 1,024-byte boundary
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
@@ -119,7 +118,7 @@ __device__ __forceinline__ void ld_words(uint32_t (&b)[N], const uint8_t* p) {
 
 // Asynchronous copies to shared memory; zeros instead where `on` is not set.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool on) {
@@ -143,51 +142,24 @@ __device__ __forceinline__ float2 two_scales(uint32_t v, bool bf16) {
         return __half22float2(h);
     }
 }
-// The scales of N (2 or 4) groups of 32 from group gi of a unit on; the row's scales of the unit lie at `row`.
-template <int SK, int N>
-__device__ __forceinline__ void read_scales(const uint8_t* row, int gi, int shift, bool bf16, float (&s)[N]) {
-    if constexpr (SK == SCALE_E8M0) {
-        if constexpr (N == 2) {
-            const float2 v = two_scales<SK>(*reinterpret_cast<const uint16_t*>(row + gi), false);
-            s[0] = v.x;
-            s[1] = v.y;
-        } else {
-            uint32_t w[1];
-            ld_words(w, row + gi);
-            const float2 v = two_scales<SK>(w[0] & 0xFFFFu, false), u = two_scales<SK>(w[0] >> 16, false);
-            s[0] = v.x;
-            s[1] = v.y;
-            s[2] = u.x;
-            s[3] = u.y;
-        }
-    } else if constexpr (SK == SCALE_16) {
+// The scales of groups gi (even) and gi + 1 of a unit; the row's scales of the unit lie at `row`.
+template <int SK>
+__device__ __forceinline__ void read_scales(const uint8_t* row, int gi, int shift, bool bf16, float (&s)[2]) {
+    if constexpr (SK == SCALE_32) {
         if (shift == 0) {
-            uint32_t w[N / 2];
-            ld_words(w, row + 2 * gi);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                const float2 v = two_scales<SK>(w[i], bf16);
-                s[2 * i] = v.x;
-                s[2 * i + 1] = v.y;
-            }
+            const float2 v = *reinterpret_cast<const float2*>(row + 4 * gi);
+            s[0] = v.x;
+            s[1] = v.y;
         } else {
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) s[2 * i] = s[2 * i + 1] = two_scales<SK>(*reinterpret_cast<const uint16_t*>(row + 2 * ((gi + 2 * i) >> shift)), bf16).x;
+            s[0] = s[1] = *reinterpret_cast<const float*>(row + 4 * (gi >> shift));
         }
     } else {
-        uint32_t w[N];
-        if (shift == 0) {
-            ld_words(w, row + 4 * gi);
-#pragma unroll
-            for (int i = 0; i < N; ++i) s[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                uint32_t v[1];
-                ld_words(v, row + 4 * ((gi + 2 * i) >> shift));
-                s[2 * i] = s[2 * i + 1] = __uint_as_float(v[0]);
-            }
-        }
+        const float2 v = two_scales<SK>(SK == SCALE_E8M0 ? *reinterpret_cast<const uint16_t*>(row + gi)
+                                        : shift == 0     ? *reinterpret_cast<const uint32_t*>(row + 2 * gi)
+                                                         : *reinterpret_cast<const uint16_t*>(row + 2 * (gi >> shift)),
+                                        bf16);
+        s[0] = v.x;
+        s[1] = SK == SCALE_E8M0 || shift == 0 ? v.y : v.x;
     }
 }
 
@@ -199,18 +171,20 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
         asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(warps * 32) : "memory");
 }
 
-// A unit is 256 k of a team's 16 rows: 128 bytes of a row.  Its codes go by cp.async to a ring of D slots that each
-// warp has for itself, [half of 64 bytes][row][16 bytes], the four pieces of a row's half in an order that keeps the
-// reads free of bank conflicts.
+// A unit is 256 k of a team's 16 rows: 128 bytes of a row.  Each warp has a ring of D units for itself: the codes come
+// by TMA, a box of 16 rows of 128 bytes in the 128-byte swizzle (piece i of 16 bytes of row r lies at piece i ^ (r % 8)),
+// the scales by cp.async.  The MMA's row g is row `row_of(g)` of the tile and g + 8 eight behind it: with the three
+// bits of g in reverse order, the lanes that shared memory serves at once, a quarter, half or whole warp of them, find
+// their pieces in different banks.
 constexpr int kUK = 256;
 constexpr int kUnitGroups = kUK / 32;
 constexpr int kCodeBytes = kRows * kUK / 2;
-__device__ __forceinline__ int piece(int row, int i) { return i ^ (((row >> 2) & 1) | (row & 2)); }
+__device__ __forceinline__ int row_of(int g) { return (g >> 2) | (g & 2) | ((g & 1) << 2); }
 
-// GP groups of 32 share an MMA's columns (1, 2 or 4), 8 / GP vectors a tile of columns, NT tiles.  Shared memory: x as
-// fp16 [unit][half][part of GP groups][word of 8][vector][lane of the row], 16 bytes each; as many zero bytes as a
-// unit has (read by the lanes off the diagonal); factors of the groups in fp32; the warps' sums
-// [team][matrix][warp][vector][row]; the rings.
+// GP groups of 32 share an MMA's columns (1, 2 or 4), 8 / GP vectors a tile of columns, NT tiles.  Shared memory: the
+// rings' codes, [warp][slot][matrix]; x as fp16 [unit][half][part of GP groups][word of 8][vector][lane of the row], 16
+// bytes each; as many zero bytes as a unit has (read by the lanes off the diagonal); factors of the groups in fp32; the
+// warps' sums [team][matrix][warp][vector][row]; the rings' scales.
 template <int SK, int GP, int NT, bool DUAL, int D>
 struct Layout {
     static constexpr int VT = 8 / GP;            // vectors of a tile
@@ -219,148 +193,182 @@ struct Layout {
     static constexpr int kUnitX = kUK * VS * 2, kUnitF = VS * kUnitGroups * 4;
     static constexpr int kZero = GP == 1 ? 0 : kUnitX;
     static constexpr int kScaleRow = kUnitGroups * (SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4);
-    static constexpr int kSlot = NM * (kCodeBytes + kRows * kScaleRow);
-    static constexpr int kWarp = NM * kRows * VS * 4 + D * kSlot;     // of a warp: sums and ring
+    static constexpr int kScales = NM * kRows * kScaleRow;
+    static constexpr int kWarp = NM * kRows * VS * 4 + D * (NM * kCodeBytes + kScales);     // of a warp: sums and ring
 };
 
+// Waits, with a limit, for a copy that nobody will use.
+__device__ __noinline__ void matvec_drain(uint64_t* bar, uint32_t parity, int* status) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (status) atomicCAS(status, 0, DEV_TIMEOUT_TEARDOWN);
+            return;
+        }
+}
+
 template <int SK, int GP, int NT, bool DUAL, int D>
-__global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs a) {
+__global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_constant__ MatvecArgs a) {
     using L = Layout<SK, GP, NT, DUAL, D>;
     constexpr int VT = L::VT, VS = L::VS, NM = L::NM, PARTS = 4 / GP;
     constexpr int AC = GP == 1 ? 4 : 2;  // sums of a lane and tile: two rows, and two vectors where a column is one
-    extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int s_expert[kMaxSegs];
-    __shared__ int64_t s_row[kMaxSegs];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ int s_expert[kMaxSegs], s_row[kMaxSegs], s_segs, s_abort;
+    __shared__ __align__(8) uint64_t s_full[kMvMaxThreads / 32][D];
     __shared__ float s_gate[kMaxSegs];
-    __shared__ int s_segs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    const int KW = a.kw, team = warp / KW, kwarp = warp % KW, warps = blockDim.x >> 5, teams = warps / KW;
-    const int64_t set = static_cast<int64_t>(blockIdx.x) % a.sets;
-    const int part = static_cast<int>(blockIdx.x / a.sets);
-    const int K = a.K, M = a.M;
-    const int cps = (K + kUK - 1) / kUK;   // units of a segment
-    // the vectors: rows of x (one matrix), a slot's row, or a token's slots one behind the other
-    const int nv = a.idx ? 1 : static_cast<int>(min(static_cast<int64_t>(a.nv), a.N - set * a.nv));
-    if (warp == 0) {
-        int n = 1;
-        if (!a.idx) {
-            if (lane == 0) {
-                s_expert[0] = 0;
-                s_row[0] = set * a.nv;
-                s_gate[0] = 1.0f;
-            }
-        } else {
-            const int per = a.weights ? a.k : 1;
-            const int64_t slot = set * per + lane;
-            const int e = lane < per ? a.idx[slot] : -1;
+    const int KW = 1 << a.kw_log, team = warp >> a.kw_log, kwarp = warp & (KW - 1), warps = blockDim.x >> 5, teams = warps >> a.kw_log;
+    const uint32_t sets = static_cast<uint32_t>(a.sets), part = sets == 1 ? blockIdx.x : blockIdx.x / sets, set = blockIdx.x - part * sets;
+    const int K = a.K, M = a.M, cps = a.cps;
+    uint64_t* const full = s_full[warp];
+    volatile int* const abort_flag = &s_abort;
+    if (threadIdx.x == 0) s_abort = 0;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    // the vectors: rows of x (one matrix), a slot's row, or a token's slots one behind the other, whose numbers below 2^31
+    // go to shared memory
+    const int nv = a.idx ? 1 : static_cast<int>(min(static_cast<int64_t>(a.nv), a.N - static_cast<int64_t>(set) * a.nv));
+    int segs = 1, expert = 0;
+    int64_t xrow = static_cast<int64_t>(set) * a.nv;
+    if (a.weights) {
+        if (warp == 0) {
+            const int slot = static_cast<int>(set) * a.k + lane;
+            const int e = lane < a.k ? a.idx[slot] : -1;
             const bool kept = e >= 0 && e < a.G;
             const uint32_t all = __ballot_sync(kAll, kept);
-            n = __popc(all);
             if (kept) {
                 const int at = __popc(all & ((1u << lane) - 1));
                 s_expert[at] = e;
-                s_row[at] = a.x_per_slot ? slot : slot / a.k;
-                s_gate[at] = a.weights ? a.weights[slot] : 1.0f;
+                s_row[at] = a.x_per_slot ? slot : static_cast<int>(set);
+                s_gate[at] = a.weights[slot];
             }
+            if (lane == 0) s_segs = __popc(all);
         }
-        if (lane == 0) s_segs = n;
+        __syncthreads();
+        segs = s_segs;
+    } else if (a.idx) {
+        expert = a.idx[set];
+        segs = expert >= 0 && expert < a.G ? 1 : 0;
+        xrow = a.x_per_slot ? set : set / static_cast<uint32_t>(a.k);
     }
+    const int units = segs * cps;
     const int cap = a.cap;               // units of x that fit
-    uint8_t* xv = sm;
+    uint8_t* const codes = sm + warp * (D * NM * kCodeBytes);
+    uint8_t* xv = sm + warps * (D * NM * kCodeBytes);
     uint8_t* zero = xv + static_cast<size_t>(cap) * L::kUnitX;
     float* xf = reinterpret_cast<float*>(zero + L::kZero);
     float* red = xf + static_cast<size_t>(cap) * (VS * kUnitGroups);
-    uint8_t* ring = reinterpret_cast<uint8_t*>(red) + warps * (NM * kRows * VS * 4) + warp * (D * L::kSlot);
+    uint8_t* const scales = reinterpret_cast<uint8_t*>(red) + warps * (NM * kRows * VS * 4) + warp * (D * L::kScales);
     for (int i = threadIdx.x * 16; i < L::kZero; i += blockDim.x * 16) *reinterpret_cast<uint4*>(zero + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    const int segs = s_segs, units = segs * cps;
 
-    // x of the units [u0, u1) to shared memory: a thread takes eight values, four threads a group
-    auto stage = [&](int u0, int u1) {
-        constexpr int per_unit = kUK / 8;
-        const int vvt = nv * a.parts, total = (u1 - u0) * per_unit * nv;
-        for (int i0 = 0; i0 < total; i0 += kStage * blockDim.x) {
-            RawVec<8> raw[kStage];
-#pragma unroll
-            for (int j = 0; j < kStage; ++j) {
-                const int i = i0 + j * blockDim.x + threadIdx.x;
-                const int c = i % per_unit, rest = i / per_unit, u = nv == 1 ? rest : rest / nv, n = rest - u * nv;
-                const int seg = segs == 1 ? 0 : (u0 + u) / cps, k = ((u0 + u) - seg * cps) * kUK + c * 8;
-                raw[j].a = raw[j].b = make_uint4(0, 0, 0, 0);
-                if (a.x_wide && i < total && k < K) raw[j] = load_raw<8>(a.x, (s_row[seg] + n) * a.ld_x + k, a.dt_x);
+    // x of the units [u0, u1) to shared memory.  A warp takes a unit of a vector, a lane eight values, four lanes a
+    // group.  The values come by cp.async to where their fp16 parts go, and are made these parts in place by the lane
+    // that copied them.
+    constexpr int fs = GP == 1 ? 1 : kUnitGroups;                // from a vector's factor to the next one's
+    const int x_word = lane / (4 * GP) * GP + lane % (4 * GP) % GP;      // lane t of a row holds the codes of 8 GP values of each part of 32 GP
+    uint8_t* const x_lane = xv + (x_word * (VS * 4) + lane % (4 * GP) / GP) * 16;
+    const int64_t x0 = xrow * a.ld_x + lane * 8;
+    auto copy_x = [&](int u0, int u1) {
+        const int items = (u1 - u0) * nv;
+#pragma unroll 1
+        for (int j = warp; j < items; j += warps) {
+            int u = j, n = 0, k = (u0 + j) * kUK;
+            int64_t off = x0;
+            if (nv > 1) {                // one segment
+                u = j / nv;
+                n = j - u * nv;
+                off += n * a.ld_x;
+                k = (u0 + u) * kUK;
+            } else if (a.weights) {
+                const int seg = (u0 + j) / cps;
+                off = s_row[seg] * a.ld_x + lane * 8;
+                k = (u0 + j - seg * cps) * kUK;
             }
-#pragma unroll
-          for (int j = 0; j < kStage; ++j) {
-            if (i0 + j * blockDim.x >= total) break;
-            const int i = i0 + j * blockDim.x + threadIdx.x;
-            const bool in = i < total;
-            const int c = i % per_unit, rest = in ? i / per_unit : 0, u = nv == 1 ? rest : rest / nv, n = rest - u * nv;
-            const int seg = segs == 1 ? 0 : (u0 + u) / cps, k = ((u0 + u) - seg * cps) * kUK + c * 8;
+            const bool on = k + lane * 8 < K;
+            const uint8_t* src = static_cast<const uint8_t*>(a.x) + (off + (on ? k : -lane * 8)) * (a.parts > 1 ? 4 : 2);
+            const uint32_t dst = smem_u32(x_lane + u * L::kUnitX + n * a.parts * 64);
+            copy16(dst, src, on);
+            if (a.parts > 1) copy16(dst + 64, src + 16, on);
+        }
+    };
+    auto stage = [&](int u0, int u1) {
+        const int vvt = nv * a.parts, items = (u1 - u0) * nv;
+        float* const f_to = xf + (GP == 1 ? lane / 4 * VS : lane / 4);
+#pragma unroll 1
+        for (int j = warp; j < items; j += warps) {
+            const int u = nv == 1 ? j : j / nv, n = j - u * nv, seg = a.weights ? (u0 + u) / cps : 0;
+            uint8_t* xo = x_lane + u * L::kUnitX + n * a.parts * 64;
+            const float gate = a.weights ? s_gate[seg] : 1.0f;
             float f[8];
-            raw_to_f32(raw[j], a.dt_x, f);
-            if (!a.x_wide && in && k < K) {
+            if (a.x_wide) {
+                RawVec<8> raw;
+                raw.a = *reinterpret_cast<const uint4*>(xo);
+                if (a.parts > 1) raw.b = *reinterpret_cast<const uint4*>(xo + 64);
+                raw_to_f32(raw, a.dt_x, f);
+            } else {
+                const int64_t off = a.weights ? s_row[seg] * a.ld_x + lane * 8 : x0 + n * a.ld_x;
+                const int k = (u0 + u - seg * cps) * kUK;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    float e[1];
-                    raw_to_f32(load_raw<1>(a.x, (s_row[seg] + n) * a.ld_x + k + x, a.dt_x), a.dt_x, e);
+                    float e[1] = {0.0f};
+                    if (k + lane * 8 < K) raw_to_f32(load_raw<1>(a.x, off + k + x, a.dt_x), a.dt_x, e);
                     f[x] = e[0];
                 }
             }
-            float top = 0.0f;
+            float top = 0.0f;                                    // (fmaxf goes past NaN)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float m = fabsf(f[j]);
-                if (m < INFINITY) top = fmaxf(top, m);          // infinities and NaN stay what they are
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+            if (top == INFINITY) {                               // infinities stay what they are
+                top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fabsf(f[i]) < INFINITY ? fmaxf(top, fabsf(f[i])) : top;
             }
             top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
             top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
             // 2^-ex brings it into [2^14, 2^15); the factors, with those of the parts, stay normal numbers
             int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14;
-            ex = max(ex, a.parts == 1 ? -126 : -100);
-            if (top == 0.0f) ex = 0;
+            ex = top == 0.0f ? 0 : max(ex, a.parts == 1 ? -126 : -100);
             const float to = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-            const float back = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+            const float back = gate * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] *= to;
-            // lane t of a row holds the codes of 8 GP values of each part of 32 GP
-            const int of_part = c % (4 * GP), t = of_part / GP, word = of_part % GP, gi = c / 4;
-            uint4* xo = reinterpret_cast<uint4*>(xv) + ((u * (kUK / 32) + c / (4 * GP) * GP + word) * VS) * 4 + t;
-            float* fo = xf + u * (VS * kUnitGroups) + (GP == 1 ? gi * VS : gi);
-            constexpr int fs = GP == 1 ? 1 : kUnitGroups;
+            for (int i = 0; i < 8; ++i) f[i] *= to;
+            float* fo = f_to + u * (VS * kUnitGroups) + n * a.parts * fs;
             for (int p = 0; p < a.parts; ++p) {
-                __half h[8];
+                __half2 h[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(f[j]);
+                for (int i = 0; i < 4; ++i)                      // integers come in the order (0, 4) (1, 5) (2, 6) (3, 7)
+                    h[i] = SK == SCALE_E8M0 ? __floats2half2_rn(f[2 * i], f[2 * i + 1]) : __floats2half2_rn(f[i], f[i + 4]);
                 if (a.parts > 1)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float r = (f[j] - __half2float(h[j])) * 4096.0f;
-                        f[j] = r == r ? r : 0.0f;                // nothing is left of an infinity
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v = __half22float2(h[i]);
+                        float& lo = f[SK == SCALE_E8M0 ? 2 * i : i];
+                        float& hi = f[SK == SCALE_E8M0 ? 2 * i + 1 : i + 4];
+                        const float r = (lo - v.x) * 4096.0f, s = (hi - v.y) * 4096.0f;
+                        lo = r == r ? r : 0.0f;                  // nothing is left of an infinity
+                        hi = s == s ? s : 0.0f;
                     }
-                __half o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)                      // integers come in the order (0, 4) (1, 5) (2, 6) (3, 7)
-                    o[j] = SK == SCALE_E8M0 ? h[j] : h[(j & 1) * 4 + j / 2];
                 uint4 v;
-                memcpy(&v, o, 16);
-                const int vv = n * a.parts + p;
-                if (in) {
-                    xo[vv * 4] = v;
-                    if ((c & 3) == 0) fo[vv * fs] = s_gate[seg] * back * __uint_as_float(static_cast<uint32_t>(127 - 12 * p) << 23);
-                }
+                memcpy(&v, h, 16);
+                *reinterpret_cast<uint4*>(xo + p * 64) = v;
+                if ((lane & 3) == 0) fo[p * fs] = back * __uint_as_float(static_cast<uint32_t>(127 - 12 * p) << 23);
             }
-            if (in && n == 0)                                    // vectors that are not there
-                for (int vv = vvt; vv < VS; ++vv) {
-                    xo[vv * 4] = make_uint4(0, 0, 0, 0);
-                    if ((c & 3) == 0) fo[vv * fs] = 0.0f;
+            if (n == 0)                                          // vectors that are not there
+                for (int p = vvt; p < VS; ++p) {
+                    *reinterpret_cast<uint4*>(xo + p * 64) = make_uint4(0, 0, 0, 0);
+                    if ((lane & 3) == 0) fo[p * fs] = 0.0f;
                 }
-          }
         }
     };
 
     // this lane's places
     constexpr int kScaleSize = SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4;
-    const int64_t row_bytes = K / 2, srow_bytes = static_cast<int64_t>(K / 32 >> a.shift) * kScaleSize;
+    const int64_t srow_bytes = a.srow;
     const bool bf16 = a.dt_scale == ELEM_BF16;
     // B fragments: the lane's column is that of vector vb in group gb of a part; values in the rows of that group's
     // lanes, zeros elsewhere
@@ -372,37 +380,27 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
     const int vc = GP == 4 ? t4 / 2 : GP == 2 ? t4 : 2 * t4, g2 = GP == 4 ? 2 * (t4 & 1) : 0;
     const float* f_lane = xf + (GP == 1 ? vc : vc * kUnitGroups + g2);
 
-    const int tiles = (M + kRows - 1) / kRows;
-    const int tile_step = a.blocks * teams;
-    // The next unit to copy: pointers of this lane's pieces of codes (row g, row g + 8) and of scales, which move along a
+    const int tiles = a.tiles, tile_step = a.blocks * teams;
+    // The next unit to copy: its codes' first row, and the pointer of this lane's piece of its scales, which moves along a
     // segment.  Scales go by pieces of 16, 8 or 4 bytes where all rows start on whole pieces, else one by one.
-    const int unit_scales = (kUnitGroups >> a.shift) * kScaleSize;                    // bytes of a row
-    const int size = a.scale_piece > 0 ? a.scale_piece : kScaleSize, lg = 31 - __clz(unit_scales / size);
+    const int unit_scales = a.unit_scales, size = a.scale_size, lg = a.scale_log;     // bytes of a row, 2^lg pieces
     const int srow = lane >> lg, soff = (lane & ((1 << lg) - 1)) * size, sstep = 32 >> lg;
-    const uint32_t put = g * 64 + piece(g, t4) * 16;
     struct {
         int tile, u, c;                  // tile, unit, unit in its segment
-        const uint8_t *lo[NM], *hi[NM], *s[NM];
+        int row;                         // of all matrices
+        const uint8_t* s[NM];
         int64_t back;                    // from the scales' pointer to the first row's
         int rows;                        // from the tile's first to the matrix' last
-    } cur;
-    auto aim = [&](int tile, int u) {
-        cur.tile = tile;
-        cur.u = u;
-        const int seg = segs > 1 ? u / cps : 0;
-        cur.c = u - seg * cps;
-        const int r = tile * kRows;
-        cur.rows = M - r;
-        const int64_t row = static_cast<int64_t>(s_expert[seg]) * M + r;
-        const int64_t lo = (row + (g < cur.rows ? g : 0)) * row_bytes + cur.c * (kUK / 2) + t4 * 16, up = g + 8 < cur.rows ? 8 * row_bytes : 0;
-        const int64_t of_row = min(srow, kRows) * srow_bytes + soff, sc = row * srow_bytes + static_cast<int64_t>(cur.c) * unit_scales + of_row;
+    } cur = {};
+    auto aim = [&] {
+        const int seg = segs > 1 ? cur.u / cps : 0;
+        cur.c = cur.u - seg * cps;
+        cur.rows = M - cur.tile * kRows;
+        cur.row = (a.weights ? s_expert[seg] : expert) * M + cur.tile * kRows;       // G M < 2^31
+        const int64_t of_row = min(srow, kRows) * srow_bytes + soff, sc = cur.row * srow_bytes + static_cast<int64_t>(cur.c) * unit_scales + of_row;
         cur.back = -of_row;
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            cur.lo[m] = (m ? a.up_codes : a.codes) + lo;
-            cur.hi[m] = cur.lo[m] + up;
-            cur.s[m] = (m ? a.up_scales : a.scales) + sc;
-        }
+        for (int m = 0; m < NM; ++m) cur.s[m] = (m ? a.up_scales : a.scales) + sc;
     };
     auto copy_scales = [&](uint32_t dst, const uint8_t* src, bool on) {
         if (a.scale_piece == 8)
@@ -416,48 +414,28 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
         else
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(on ? *reinterpret_cast<const uint16_t*>(src) : static_cast<uint16_t>(0)) : "memory");
     };
-    auto fetch = [&](uint8_t* slot) {
-        const int left = K - cur.c * kUK;
-        const uint32_t to = smem_u32(slot) + put, sto = smem_u32(slot) + NM * kCodeBytes + srow * L::kScaleRow + soff;
-        if (left >= kUK && cur.rows >= kRows) {
+    auto fetch = [&](int at) {
+        // rows behind the last of all matrices and codes behind a row's end come as zeros; rows of the next matrix are
+        // not stored
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&full[at], NM * kCodeBytes);
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                copy16(to + m * kCodeBytes, cur.lo[m], true);
-                copy16(to + m * kCodeBytes + 512, cur.hi[m], true);
-                copy16(to + m * kCodeBytes + 1024, cur.lo[m] + 64, true);
-                copy16(to + m * kCodeBytes + 1536, cur.hi[m] + 64, true);
-                if (srow < kRows) copy_scales(sto + m * (kRows * L::kScaleRow), cur.s[m], true);
-                for (int row = sstep; srow + row < kRows; row += sstep)
-                    copy_scales(sto + m * (kRows * L::kScaleRow) + row * L::kScaleRow, cur.s[m] + row * srow_bytes, true);
-            }
-        } else {
-            // behind the row's end the first address of its unit, which is not read
-            const bool on0 = t4 * 32 < left, on1 = t4 * 32 + 128 < left;
-            const int sleft = static_cast<int>(srow_bytes) - cur.c * unit_scales;        // K / 8 at most
-#pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                const uint8_t *lo = cur.lo[m] - (on0 ? 0 : t4 * 16), *hi = cur.hi[m] - (on0 ? 0 : t4 * 16);
-                copy16(to + m * kCodeBytes, lo, on0 && g < cur.rows);
-                copy16(to + m * kCodeBytes + 512, hi, on0 && g + 8 < cur.rows);
-                copy16(to + m * kCodeBytes + 1024, lo + (on1 ? 64 : 0), on1 && g < cur.rows);
-                copy16(to + m * kCodeBytes + 1536, hi + (on1 ? 64 : 0), on1 && g + 8 < cur.rows);
-                for (int row = 0; srow + row < kRows; row += sstep) {
-                    const bool on = soff < sleft && srow + row < cur.rows;
-                    copy_scales(sto + m * (kRows * L::kScaleRow) + row * L::kScaleRow, cur.s[m] + (on ? row * srow_bytes : cur.back), on);
-                }
-            }
+            for (int m = 0; m < NM; ++m)
+                tma_load_2d(codes + (at * NM + m) * kCodeBytes, m ? &a.up_map : &a.map, &full[at], cur.c * (kUK / 2), cur.row);
         }
+        const uint32_t sto = smem_u32(scales) + at * L::kScales + srow * L::kScaleRow + soff;
+        const bool in_row = soff < static_cast<int>(srow_bytes) - cur.c * unit_scales;   // K / 8 at most
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll 1
+            for (int row = 0; srow + row < kRows; row += sstep) {
+                const bool on = in_row && srow + row < cur.rows;
+                copy_scales(sto + m * (kRows * L::kScaleRow) + row * L::kScaleRow, cur.s[m] + (on ? row * srow_bytes : cur.back), on);
+            }
         ++cur.u;
-        if (++cur.c == cps && cur.u < units) {
-            aim(cur.tile, cur.u);
-        } else {
+        ++cur.c;
 #pragma unroll
-            for (int m = 0; m < NM; ++m) {
-                cur.lo[m] += kUK / 2;
-                cur.hi[m] += kUK / 2;
-                cur.s[m] += unit_scales;
-            }
-        }
+        for (int m = 0; m < NM; ++m) cur.s[m] += unit_scales;
     };
 
     // in registers: an instruction takes one constant
@@ -465,80 +443,89 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
     asm volatile("" : "+r"(mask4), "+r"(bits4));
     float acc[NM][NT][AC];
     // adds the products of the unit in a slot, whose x is number ul in shared memory
-    auto work = [&](const uint8_t* slot, int ul) {
+    const int row0 = row_of(g);
+    const uint8_t* const c_lane = codes + row0 * 128;
+    const uint8_t* const s_lane = scales + row0 * L::kScaleRow;
+    auto work = [&](int at_slot, int ul) {
+        const uint8_t* slot = c_lane + at_slot * (NM * kCodeBytes);
         const uint8_t* x_at = x_base + ul * x_step;
         const float* f_at = f_lane + ul * (VS * kUnitGroups);
+        // The MMAs of a part follow one another in one accumulator, some 22 cycles each: two parts at a time.
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float s4[NM][2][4];
-            if constexpr (GP == 1) {
+        for (int pair = 0; pair < PARTS; ++pair) {
+            // parts 2 pair and 2 pair + 1 of the unit's 2 PARTS
+            uint32_t lo[2][NM][GP], hi[2][NM][GP];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int q = 2 * pair + h, half = q / PARTS, part = q % PARTS;
+                // the lane's 4 GP bytes of the part's 16 GP in a row
+                const int piece = half * 4 + (GP == 4 ? t4 : GP == 2 ? 2 * part + t4 / 2 : part);
+                const uint8_t* at = slot + (piece ^ row0) * 16 + (GP == 4 ? 0 : GP == 2 ? (t4 & 1) * 8 : t4 * 4);
 #pragma unroll
                 for (int m = 0; m < NM; ++m) {
-                    const uint8_t* row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
-                    read_scales<SK, 4>(row, half * 4, a.shift, bf16, s4[m][0]);
-                    read_scales<SK, 4>(row + 8 * L::kScaleRow, half * 4, a.shift, bf16, s4[m][1]);
+                    ld_words(lo[h][m], at + m * kCodeBytes);
+                    ld_words(hi[h][m], at + m * kCodeBytes + 1024);
                 }
             }
+            float c[2][NM][NT][4];
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-                uint32_t lo[NM][GP], hi[NM][GP];
-                // the lane's 4 GP bytes of the part's 16 GP in a row
-                const uint8_t* at = slot + half * 1024 + g * 64 +
-                                    (GP == 4 ? piece(g, t4) * 16 : GP == 2 ? piece(g, 2 * part + t4 / 2) * 16 + (t4 & 1) * 8 : piece(g, part) * 16 + t4 * 4);
+            for (int w = 0; w < GP; ++w) {
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    ld_words(lo[m], at + m * kCodeBytes);
-                    ld_words(hi[m], at + m * kCodeBytes + 512);
-                }
-                float c[NM][NT][4];
-#pragma unroll
-                for (int w = 0; w < GP; ++w) {
+                for (int h = 0; h < 2; ++h) {
                     uint32_t b[NT][4];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) ld_words(b[n], x_at + (((half * PARTS + part) * GP + w) * VS + n * VT) * 64);
+                    for (int n = 0; n < NT; ++n) ld_words(b[n], x_at + (((2 * pair + h) * GP + w) * VS + n * VT) * 64);
 #pragma unroll
                     for (int m = 0; m < NM; ++m) {
                         uint32_t p[4], q[4];
                         if constexpr (SK == SCALE_E8M0) {
-                            e2m1_pairs(lo[m][w], p);
-                            e2m1_pairs(hi[m][w], q);
+                            e2m1_pairs(lo[h][m][w], p);
+                            e2m1_pairs(hi[h][m][w], q);
                         } else {
-                            int4_pairs(lo[m][w], p, mask4, bits4);
-                            int4_pairs(hi[m][w], q, mask4, bits4);
+                            int4_pairs(lo[h][m][w], p, mask4, bits4);
+                            int4_pairs(hi[h][m][w], q, mask4, bits4);
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             if (w == 0)
-                                mma_16816_first(c[m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
+                                mma_16816_first(c[h][m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
                             else
-                                mma_16816(c[m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
-                            mma_16816(c[m][n], p[2], q[2], p[3], q[3], b[n][2], b[n][3]);
+                                mma_16816(c[h][m][n], p[0], q[0], p[1], q[1], b[n][0], b[n][1]);
+                            mma_16816(c[h][m][n], p[2], q[2], p[3], q[3], b[n][2], b[n][3]);
                         }
                     }
                 }
-                // behind the last group codes, values and scales are zero
-                const int gi = half * 4 + part * GP;
+            }
+            // behind the last group codes, values and scales are zero
+            const int gi = 2 * pair * GP;
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    if constexpr (GP == 1) {
+            for (int m = 0; m < NM; ++m) {
+                const uint8_t* row = s_lane + at_slot * L::kScales + m * (kRows * L::kScaleRow);
+                if constexpr (GP == 1) {
+                    float s[2], r[2];
+                    read_scales<SK>(row, gi, a.shift, bf16, s);
+                    read_scales<SK>(row + 8 * L::kScaleRow, gi, a.shift, bf16, r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const float2 f = *reinterpret_cast<const float2*>(f_at + gi * VS + n * VT);
-                            acc[m][n][0] = fmaf(c[m][n][0] * s4[m][0][part], f.x, acc[m][n][0]);
-                            acc[m][n][1] = fmaf(c[m][n][1] * s4[m][0][part], f.y, acc[m][n][1]);
-                            acc[m][n][2] = fmaf(c[m][n][2] * s4[m][1][part], f.x, acc[m][n][2]);
-                            acc[m][n][3] = fmaf(c[m][n][3] * s4[m][1][part], f.y, acc[m][n][3]);
+                            const float2 f = *reinterpret_cast<const float2*>(f_at + (gi + h) * VS + n * VT);
+                            acc[m][n][0] = fmaf(c[h][m][n][0] * s[h], f.x, acc[m][n][0]);
+                            acc[m][n][1] = fmaf(c[h][m][n][1] * s[h], f.y, acc[m][n][1]);
+                            acc[m][n][2] = fmaf(c[h][m][n][2] * r[h], f.x, acc[m][n][2]);
+                            acc[m][n][3] = fmaf(c[h][m][n][3] * r[h], f.y, acc[m][n][3]);
                         }
-                    } else {
-                        const uint8_t* row = slot + NM * kCodeBytes + (m * kRows + g) * L::kScaleRow;
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
                         float s[2], r[2];
-                        read_scales<SK, 2>(row, gi + g2, a.shift, bf16, s);
-                        read_scales<SK, 2>(row + 8 * L::kScaleRow, gi + g2, a.shift, bf16, r);
+                        read_scales<SK>(row, gi + h * GP + g2, a.shift, bf16, s);
+                        read_scales<SK>(row + 8 * L::kScaleRow, gi + h * GP + g2, a.shift, bf16, r);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const float2 f = *reinterpret_cast<const float2*>(f_at + n * VT * kUnitGroups + gi);
-                            acc[m][n][0] = fmaf(c[m][n][1] * s[1], f.y, fmaf(c[m][n][0] * s[0], f.x, acc[m][n][0]));
-                            acc[m][n][1] = fmaf(c[m][n][3] * r[1], f.y, fmaf(c[m][n][2] * r[0], f.x, acc[m][n][1]));
+                            const float2 f = *reinterpret_cast<const float2*>(f_at + n * VT * kUnitGroups + gi + h * GP);
+                            acc[m][n][0] = fmaf(c[h][m][n][1] * s[1], f.y, fmaf(c[h][m][n][0] * s[0], f.x, acc[m][n][0]));
+                            acc[m][n][1] = fmaf(c[h][m][n][3] * r[1], f.y, fmaf(c[h][m][n][2] * r[0], f.x, acc[m][n][1]));
                         }
                     }
                 }
@@ -551,6 +538,9 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
     const bool whole = units <= cap;     // all of x fits: staged once
     bool ahead = false;                  // the ring holds the first units already
     int at = 0;                          // slot of the next unit
+    uint32_t phase = 0;                  // of the slots' barriers, a bit each
+    uint32_t armed = 0;                  // slots that a copy was issued for and not waited for
+    bool ok = true;                      // no wait has run out
     float* mine = red + team * (NM * KW * kRows * VS);
     for (int tile0 = part * teams; tile0 < tiles; tile0 += tile_step) {
         const int tile = tile0 + team;
@@ -564,30 +554,54 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
         for (int u0 = 0; u0 < units; u0 += cap) {
             const int u1 = min(u0 + cap, units), per = (u1 - u0 + KW - 1) / KW;
             const int first = min(u0 + kwarp * per, u1), last = min(first + per, u1), run = last - first;
-            // the next unit of this run, or (if x stays) the first of the next tile's
-            auto issue = [&](uint8_t* slot) {
-                if (cur.u >= last && whole && run > 0 && cur.tile + tile_step < tiles) aim(cur.tile + tile_step, first);
-                if (cur.u < last) fetch(slot);
+            const bool need = !whole || tile0 == static_cast<int>(part) * teams;      // x of these units
+            if (need && a.x_wide) {
+                if (tile0 != static_cast<int>(part) * teams || u0 > 0) __syncthreads();   // the last ones are read
+                copy_x(u0, u1);
                 copy_commit();
-            };
+            }
             if (live && !ahead) {
-                at = 0;
-                aim(tile, first);
-                for (int i = 0; i < D; ++i) issue(ring + i * L::kSlot);
+                cur.tile = tile;
+                cur.u = first;
+                cur.c = cps;
             }
-            if (!whole || tile0 == part * teams) {
-                __syncthreads();
-                stage(u0, u1);
-                __syncthreads();
-            }
-            if (!live) continue;
-            for (int i = 0; i < run; ++i) {
-                copy_wait<D - 1>();
-                __syncwarp();
-                uint8_t* slot = ring + at * L::kSlot;
-                work(slot, first + i - u0);
-                __syncwarp();
-                issue(slot);
+            // D copies ahead, the wait for x, the units in turn
+            for (int i = live && !ahead ? -D : 0; i < run || (need && i <= 0); ++i) {
+                if (i == 0 && need) {
+                    if (live)            // x is older than the D units
+                        copy_wait<D>();
+                    else
+                        copy_wait<0>();
+                    if (!a.x_wide) __syncthreads();
+                    stage(u0, u1);
+                    __syncthreads();
+                }
+                if (i >= 0) {
+                    if (i >= run || !live) break;
+                    copy_wait<D - 1>();
+                    ok = ok && mbar_wait(&full[at], (phase >> at) & 1, abort_flag, a.status, DEV_TIMEOUT_PRODUCER);
+                    ok = __all_sync(kAll, ok);
+                    if (ok) {
+                        phase ^= 1u << at;
+                        armed &= ~(1u << at);
+                    }
+                    if (ok) work(at, first + i - u0);
+                    __syncwarp();
+                }
+                // the next unit of this run, or (if x stays) the first of the next tile's
+                if (cur.u >= last && whole && run > 0 && cur.tile + tile_step < tiles) {
+                    cur.tile += tile_step;
+                    cur.u = first;
+                    cur.c = cps;
+                }
+                if (cur.u < last) {
+                    if (cur.c == cps) aim();
+                    if (ok) {
+                        fetch(at);
+                        armed |= 1u << at;
+                    }
+                }
+                copy_commit();
                 at = at + 1 == D ? 0 : at + 1;
             }
             ahead = whole;
@@ -599,7 +613,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
             for (int m = 0; m < NM; ++m)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float* to = mine + ((m * KW + kwarp) * VS + n * VT + vc) * kRows + g;
+                    float* to = mine + ((m * KW + kwarp) * VS + n * VT + vc) * kRows + row0;
                     if constexpr (GP == 1) {
                         to[0] = acc[m][n][0];
                         to[kRows] = acc[m][n][1];
@@ -631,43 +645,52 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const MatvecArgs 
                 }
                 float v[1] = {y[0]};
                 if constexpr (DUAL) v[0] = y[0] / (1.0f + expf(-y[0])) * y[1];
-                store_vec(a.out, (set * a.nv + n) * a.ld_out + m, a.dt_out, v);
+                store_vec(a.out, (static_cast<int64_t>(set) * a.nv + n) * a.ld_out + m, a.dt_out, v);
             }
         }
     }
+    // a wait ran out: this warp's copies land before its shared memory goes to another block
+    if (!ok)
+        for (int i = 0; i < D; ++i)
+            if (armed & (1u << i)) matvec_drain(&full[i], (phase >> i) & 1, a.status);
 }
 
-// Warps of a block, of a team and blocks of a set.  Two blocks of 8 warps an SM where x fits, else one of 16.  A block
-// takes a set's tiles in rounds, a round as long as a warp's run of units and some three more for its start and end:
-// the split of K among a team's warps that makes that shortest.
+int ilog2(int n) { return n > 1 ? 1 + ilog2(n / 2) : 0; }
+
+// Warps of a block and of a team, and blocks of a set.  16 warps an SM, in one block or, where both fit, in two.  A
+// block's time, in halves of a unit: its share of x, and rounds of tiles, each as long as a warp's run and its start and
+// end; the split that makes the waves of blocks shortest.
 template <int SK, int GP, int NT, bool DUAL, int D>
 cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
     using L = Layout<SK, GP, NT, DUAL, D>;
-    const int tiles = (a.M + kRows - 1) / kRows;
-    const int64_t units = static_cast<int64_t>(a.weights ? a.k : 1) * ((a.K + kUK - 1) / kUK);
+    const int tiles = a.tiles;
+    const int64_t units = static_cast<int64_t>(a.weights ? a.k : 1) * a.cps;
     const size_t unit_bytes = L::kUnitX + L::kUnitF;
     const bool two = units * unit_bytes + L::kZero + 8 * L::kWarp <= 110 * 1024;
-    const int warps = two ? 8 : 16, resident = two ? 304 : 152;
-    a.cap = static_cast<int>(std::min<int64_t>(units, (kMvSmem - L::kZero - warps * L::kWarp) / unit_bytes));
-    const size_t smem = a.cap * unit_bytes + L::kZero + warps * L::kWarp;
-    if (smem > 40 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(matvec_kernel<SK, GP, NT, DUAL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMvSmem);
-        if (err != cudaSuccess) return err;
-    }
-    // a set of its own for each slot: some four rounds of blocks, as many of them may have nothing to do
-    const int64_t most = a.idx ? std::max<int64_t>(1, (4 * resident + a.sets - 1) / a.sets) : std::max<int64_t>(1, resident / a.sets);
     int64_t best = INT64_MAX;
-    for (int kw = 1; kw <= warps; kw *= 2) {
-        const int teams = warps / kw;
-        const int64_t blocks = std::min<int64_t>((tiles + teams - 1) / teams, most);
-        const int64_t rounds = (tiles + blocks * teams - 1) / (blocks * teams), waves = (a.sets * blocks + resident - 1) / resident;
-        const int64_t cost = waves * rounds * (2 * ((units + kw - 1) / kw) + 1);
-        if (cost < best) {
-            best = cost;
-            a.kw = kw;
-            a.blocks = static_cast<int>(blocks);
+    int warps = 16;
+    for (int w = two ? 8 : 16; w <= 16; w *= 2) {
+        // a set of its own for each slot: some four waves of blocks, as many of them may have nothing to do
+        const int64_t resident = 152 * 16 / w, most = std::max<int64_t>(1, a.idx ? (4 * resident + a.sets - 1) / a.sets : resident / a.sets);
+        for (int kw = 1; kw <= w; kw *= 2) {
+            const int teams = w / kw;
+            const int64_t blocks = std::min<int64_t>((tiles + teams - 1) / teams, most);
+            const int64_t rounds = (tiles + blocks * teams - 1) / (blocks * teams), waves = (a.sets * blocks + resident - 1) / resident;
+            const int64_t cost = waves * (units * a.nv / w + rounds * (2 * ((units + kw - 1) / kw) + 1));
+            if (cost < best) {
+                best = cost;
+                warps = w;
+                a.kw_log = ilog2(kw);
+                a.blocks = static_cast<int>(blocks);
+            }
         }
     }
+    a.cap = static_cast<int>(std::min<int64_t>(units, (kMvSmem - L::kZero - warps * L::kWarp) / unit_bytes));
+    const size_t smem = 1024 + a.cap * unit_bytes + L::kZero + warps * L::kWarp;
+    // (also gives a host thread its context, which the tensor maps' encoder, a driver call, wants)
+    const cudaError_t err = cudaFuncSetAttribute(matvec_kernel<SK, GP, NT, DUAL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMvSmem + 1024);
+    if (err != cudaSuccess) return err;
+    if (!a.make_maps(a)) return cudaErrorInvalidValue;
     matvec_kernel<SK, GP, NT, DUAL, D><<<static_cast<unsigned>(a.sets * a.blocks), warps * 32, smem, s>>>(a);
     return cudaGetLastError();
 }
@@ -677,8 +700,8 @@ cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
 template <int SK, bool DUAL>
 cudaError_t matvec_of(const MatvecArgs& a, cudaStream_t s) {
     const int vv = a.nv * a.parts;
-    if (vv <= 2) return matvec_as<SK, 4, 1, DUAL, DUAL ? 2 : 3>(a, s);
-    if (vv <= 4) return matvec_as<SK, 2, 1, DUAL, DUAL ? 2 : 3>(a, s);
+    if (vv <= 2) return matvec_as<SK, 4, 1, DUAL, DUAL ? 2 : 4>(a, s);
+    if (vv <= 4) return matvec_as<SK, 2, 1, DUAL, DUAL ? 2 : 4>(a, s);
     if (vv <= 8) return matvec_as<SK, 1, 1, DUAL, 2>(a, s);
     return matvec_as<SK, 1, 2, DUAL, 2>(a, s);
 }
@@ -702,6 +725,12 @@ cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s) {
     const uint64_t lie = reinterpret_cast<uintptr_t>(a.scales) | reinterpret_cast<uintptr_t>(a.up_scales) |
                          static_cast<uint64_t>((a.K / 32) >> a.shift) * size | static_cast<uint64_t>((kUnitGroups >> a.shift) * size);
     a.scale_piece = lie % 16 == 0 ? 16 : lie % 8 == 0 ? 8 : lie % 4 == 0 ? 4 : 0;
+    a.scale_size = a.scale_piece > 0 ? a.scale_piece : size;
+    a.unit_scales = (kUnitGroups >> a.shift) * size;
+    a.scale_log = ilog2(a.unit_scales / a.scale_size);
+    a.srow = (a.K / 32 >> a.shift) * size;
+    a.cps = (a.K + kUK - 1) / kUK;
+    a.tiles = static_cast<int>((static_cast<int64_t>(a.M) + kRows - 1) / kRows);
     if (a.format == 0) return a.up_codes ? matvec_of<SCALE_E8M0, true>(a, s) : matvec_of<SCALE_E8M0, false>(a, s);
     if (a.dt_scale == ELEM_F32) return a.up_codes ? matvec_of<SCALE_32, true>(a, s) : matvec_of<SCALE_32, false>(a, s);
     return a.up_codes ? matvec_of<SCALE_16, true>(a, s) : matvec_of<SCALE_16, false>(a, s);

@@ -30,7 +30,7 @@ def call(L, **kw):
 
 
 @pytest.mark.parametrize("bad", [dict(codes=None), dict(codes=P + 8), dict(scales=None), dict(x=None), dict(x=P + 1), dict(ld_x=255), dict(out=None), dict(out=P + 1),
-                                 dict(ld_out=63), dict(idx=P + 1), dict(weights=P + 2), dict(T=-1), dict(k=0), dict(k=33), dict(T=2 ** 30), dict(G=0), dict(M=0),
+                                 dict(ld_out=63), dict(idx=P + 1), dict(weights=P + 2), dict(dev_status=P + 2), dict(T=-1), dict(k=0), dict(k=33), dict(T=2 ** 30), dict(G=0), dict(M=0),
                                  dict(G=2 ** 16, M=2 ** 15), dict(K=0), dict(K=48, ld_x=48), dict(K=2 ** 24 + 32, ld_x=2 ** 25), dict(group=64), dict(group=16), dict(format=2),
                                  dict(format=-1), dict(x_dtype=3), dict(out_dtype=-1), dict(idx=None), dict(idx=None, G=1), dict(up_codes=P, up_scales=P),
                                  dict(weights=None, up_codes=P), dict(weights=None, up_scales=P), dict(weights=None, up_codes=P + 8, up_scales=P),
