@@ -496,8 +496,7 @@ struct MatvecArgs {
     int64_t sets;
     int kw_log, cap, blocks;    // log2 of a team's warps, units of x in shared memory, blocks of a set
     int cps, tiles;             // units of a segment, tiles of rows
-    int x_wide, scale_piece;    // x's rows by 16 bytes; bytes of a copy of scales, 0: one by one
-    int scale_size, scale_log;  // bytes of a piece, log2 of a row's pieces in a unit
+    int x_wide, scale_piece;    // x's rows by 16 bytes; bytes of a load of scales, 0: one by one
     int unit_scales, srow;      // bytes of a row's scales in a unit, and of all
 };
 cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s);

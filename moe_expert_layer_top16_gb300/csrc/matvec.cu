@@ -45,6 +45,8 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 16;                // rows of a team's tile
+constexpr int kUK = 256;                 // k of a unit
+constexpr int kUnitGroups = kUK / 32;
 constexpr int kMvMaxThreads = 512;
 constexpr int kMaxSegs = 32;             // slots of a token
 constexpr int kMvSmem = 222 * 1024;      // dynamic shared memory of a block at most, but for the first 1,024-byte boundary
@@ -120,13 +122,7 @@ __device__ __forceinline__ void ld_words(uint32_t (&b)[N], const uint8_t* p) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(on ? N : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Two scales as they lie in a word.
 template <int SK>
@@ -142,24 +138,66 @@ __device__ __forceinline__ float2 two_scales(uint32_t v, bool bf16) {
         return __half22float2(h);
     }
 }
-// The scales of groups gi (even) and gi + 1 of a unit; the row's scales of the unit lie at `row`.
-template <int SK>
-__device__ __forceinline__ void read_scales(const uint8_t* row, int gi, int shift, bool bf16, float (&s)[2]) {
-    if constexpr (SK == SCALE_32) {
+// A row's scales of a unit, W words as they lie in memory: `bytes` of them, in pieces of 16, 8 or 4 bytes.
+__device__ __forceinline__ void ld_global(uint32_t& a, const uint8_t* p) { asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(a) : "l"(p)); }
+__device__ __forceinline__ void ld_global(uint32_t& a, uint32_t& b, const uint8_t* p) {
+    asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "l"(p));
+}
+__device__ __forceinline__ void ld_global(uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d, const uint8_t* p) {
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "l"(p));
+}
+template <int W>
+__device__ __forceinline__ void load_row_scales(uint32_t (&w)[W], const uint8_t* p, int bytes, int piece) {
+    if (W >= 4 && piece == 16) {
+#pragma unroll
+        for (int i = 0; i + 3 < W; i += 4)
+            if (4 * i < bytes) ld_global(w[i], w[i + 1], w[i + 2], w[i + 3], p + 4 * i);
+    } else if (piece == 8) {
+#pragma unroll
+        for (int i = 0; i + 1 < W; i += 2)
+            if (4 * i < bytes) ld_global(w[i], w[i + 1], p + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (4 * i < bytes) ld_global(w[i], p + 4 * i);
+    }
+}
+// The same one by one, `left` bytes of them; behind them zeros.
+template <int SK, int W>
+__device__ __forceinline__ void load_row_scales_one(uint32_t (&w)[W], const uint8_t* p, int n, int left) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0;
+    constexpr int size = SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4;
+#pragma unroll
+    for (int i = 0; i < kUnitGroups; ++i) {
+        if (i >= n || i * size >= left) break;
+        if constexpr (SK == SCALE_E8M0) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
+        if constexpr (SK == SCALE_16) w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
+        if constexpr (SK == SCALE_32) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    }
+}
+// The scales of groups 2 q and 2 q + 1, or with `odd` (q even then) of the two behind them.
+template <int SK, int W>
+__device__ __forceinline__ void pair_of_scales(const uint32_t (&w)[W], int q, int odd, int shift, bool bf16, float (&s)[2]) {
+    if constexpr (SK == SCALE_E8M0) {
+        const float2 v = two_scales<SK>(w[q / 2] >> (16 * (q % 2) + 16 * odd), false);
+        s[0] = v.x;
+        s[1] = v.y;
+    } else if constexpr (SK == SCALE_16) {
         if (shift == 0) {
-            const float2 v = *reinterpret_cast<const float2*>(row + 4 * gi);
+            const float2 v = two_scales<SK>(odd ? w[(q + 1) % W] : w[q], bf16);
             s[0] = v.x;
             s[1] = v.y;
         } else {
-            s[0] = s[1] = *reinterpret_cast<const float*>(row + 4 * (gi >> shift));
+            s[0] = s[1] = two_scales<SK>(shift == 1 ? w[q / 2] >> (16 * (q % 2) + 16 * odd) : w[0] >> (16 * (q / 2)), bf16).x;
         }
     } else {
-        const float2 v = two_scales<SK>(SK == SCALE_E8M0 ? *reinterpret_cast<const uint16_t*>(row + gi)
-                                        : shift == 0     ? *reinterpret_cast<const uint32_t*>(row + 2 * gi)
-                                                         : *reinterpret_cast<const uint16_t*>(row + 2 * (gi >> shift)),
-                                        bf16);
-        s[0] = v.x;
-        s[1] = SK == SCALE_E8M0 || shift == 0 ? v.y : v.x;
+        if (shift == 0) {
+            s[0] = __uint_as_float(odd ? w[(2 * q + 2) % W] : w[2 * q]);
+            s[1] = __uint_as_float(odd ? w[(2 * q + 3) % W] : w[2 * q + 1]);
+        } else {
+            s[0] = s[1] = __uint_as_float(shift == 1 ? (odd ? w[(q + 1) % W] : w[q]) : w[q / 2]);
+        }
     }
 }
 
@@ -173,18 +211,18 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
 
 // A unit is 256 k of a team's 16 rows: 128 bytes of a row.  Each warp has a ring of D units for itself: the codes come
 // by TMA, a box of 16 rows of 128 bytes in the 128-byte swizzle (piece i of 16 bytes of row r lies at piece i ^ (r % 8)),
-// the scales by cp.async.  The MMA's row g is row `row_of(g)` of the tile and g + 8 eight behind it: with the three
+// The scales go to registers, a unit ahead: four lanes read the same 8 bytes of an MXFP4 row.  (By cp.async or by TMA to
+// shared memory and from there they cost more instructions than all else but the conversion of the codes: 155,648 rows
+// of 7,168 120 us, without scales 100.)  The MMA's row g is row `row_of(g)` of the tile and g + 8 eight behind it: with the three
 // bits of g in reverse order, the lanes that shared memory serves at once, a quarter, half or whole warp of them, find
 // their pieces in different banks.
-constexpr int kUK = 256;
-constexpr int kUnitGroups = kUK / 32;
 constexpr int kCodeBytes = kRows * kUK / 2;
 __device__ __forceinline__ int row_of(int g) { return (g >> 2) | (g & 2) | ((g & 1) << 2); }
 
 // GP groups of 32 share an MMA's columns (1, 2 or 4), 8 / GP vectors a tile of columns, NT tiles.  Shared memory: the
 // rings' codes, [warp][slot][matrix]; x as fp16 [unit][half][part of GP groups][word of 8][vector][lane of the row], 16
 // bytes each; as many zero bytes as a unit has (read by the lanes off the diagonal); factors of the groups in fp32; the
-// warps' sums [team][matrix][warp][vector][row]; the rings' scales.
+// warps' sums [team][matrix][warp][vector][row].
 template <int SK, int GP, int NT, bool DUAL, int D>
 struct Layout {
     static constexpr int VT = 8 / GP;            // vectors of a tile
@@ -192,9 +230,8 @@ struct Layout {
     static constexpr int NM = DUAL ? 2 : 1;
     static constexpr int kUnitX = kUK * VS * 2, kUnitF = VS * kUnitGroups * 4;
     static constexpr int kZero = GP == 1 ? 0 : kUnitX;
-    static constexpr int kScaleRow = kUnitGroups * (SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4);
-    static constexpr int kScales = NM * kRows * kScaleRow;
-    static constexpr int kWarp = NM * kRows * VS * 4 + D * (NM * kCodeBytes + kScales);     // of a warp: sums and ring
+    static constexpr int W = SK == SCALE_E8M0 ? 2 : SK == SCALE_16 ? 4 : 8;             // words of a row's scales in a unit
+    static constexpr int kWarp = NM * kRows * VS * 4 + D * NM * kCodeBytes;             // of a warp: sums and ring
 };
 
 // Waits, with a limit, for a copy that nobody will use.
@@ -263,7 +300,6 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
     uint8_t* zero = xv + static_cast<size_t>(cap) * L::kUnitX;
     float* xf = reinterpret_cast<float*>(zero + L::kZero);
     float* red = xf + static_cast<size_t>(cap) * (VS * kUnitGroups);
-    uint8_t* const scales = reinterpret_cast<uint8_t*>(red) + warps * (NM * kRows * VS * 4) + warp * (D * L::kScales);
     for (int i = threadIdx.x * 16; i < L::kZero; i += blockDim.x * 16) *reinterpret_cast<uint4*>(zero + i) = make_uint4(0, 0, 0, 0);
 
     // x of the units [u0, u1) to shared memory.  A warp takes a unit of a vector, a lane eight values, four lanes a
@@ -367,8 +403,6 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
     };
 
     // this lane's places
-    constexpr int kScaleSize = SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4;
-    const int64_t srow_bytes = a.srow;
     const bool bf16 = a.dt_scale == ELEM_BF16;
     // B fragments: the lane's column is that of vector vb in group gb of a part; values in the rows of that group's
     // lanes, zeros elsewhere
@@ -381,61 +415,53 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
     const float* f_lane = xf + (GP == 1 ? vc : vc * kUnitGroups + g2);
 
     const int tiles = a.tiles, tile_step = a.blocks * teams;
-    // The next unit to copy: its codes' first row, and the pointer of this lane's piece of its scales, which moves along a
-    // segment.  Scales go by pieces of 16, 8 or 4 bytes where all rows start on whole pieces, else one by one.
-    const int unit_scales = a.unit_scales, size = a.scale_size, lg = a.scale_log;     // bytes of a row, 2^lg pieces
-    const int srow = lane >> lg, soff = (lane & ((1 << lg) - 1)) * size, sstep = 32 >> lg;
-    struct {
-        int tile, u, c;                  // tile, unit, unit in its segment
-        int row;                         // of all matrices
-        const uint8_t* s[NM];
-        int64_t back;                    // from the scales' pointer to the first row's
-        int rows;                        // from the tile's first to the matrix' last
-    } cur = {};
-    auto aim = [&] {
-        const int seg = segs > 1 ? cur.u / cps : 0;
-        cur.c = cur.u - seg * cps;
-        cur.rows = M - cur.tile * kRows;
-        cur.row = (a.weights ? s_expert[seg] : expert) * M + cur.tile * kRows;       // G M < 2^31
-        const int64_t of_row = min(srow, kRows) * srow_bytes + soff, sc = cur.row * srow_bytes + static_cast<int64_t>(cur.c) * unit_scales + of_row;
-        cur.back = -of_row;
-#pragma unroll
-        for (int m = 0; m < NM; ++m) cur.s[m] = (m ? a.up_scales : a.scales) + sc;
-    };
-    auto copy_scales = [&](uint32_t dst, const uint8_t* src, bool on) {
-        if (a.scale_piece == 8)
-            copy_small<8>(dst, src, on);
-        else if (a.scale_piece == 16)
-            copy16(dst, src, on);
-        else if (a.scale_piece == 4)
-            copy_small<4>(dst, src, on);
-        else if (kScaleSize == 1)
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst), "r"(static_cast<uint32_t>(on ? *src : 0)) : "memory");
-        else
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(on ? *reinterpret_cast<const uint16_t*>(src) : static_cast<uint16_t>(0)) : "memory");
-    };
-    auto fetch = [&](int at) {
-        // rows behind the last of all matrices and codes behind a row's end come as zeros; rows of the next matrix are
-        // not stored
+    // The next unit to copy: its tile, its number, those left of the run, its number in its segment, its row of all
+    // matrices.  Rows behind the last of all matrices and codes behind a row's end come as zeros; rows of the next matrix
+    // are not stored.
+    int c_tile = 0, c_u = 0, c_left = 0, c_c = 0, c_row = 0;
+    auto copy_next = [&](int at) {
+        if (c_c == cps) {
+            const int seg = segs > 1 ? c_u / cps : 0;
+            c_c = c_u - seg * cps;
+            c_row = (a.weights ? s_expert[seg] : expert) * M + c_tile * kRows;           // G M < 2^31
+        }
         if (elect_one()) {
             mbar_arrive_expect_tx(&full[at], NM * kCodeBytes);
 #pragma unroll
             for (int m = 0; m < NM; ++m)
-                tma_load_2d(codes + (at * NM + m) * kCodeBytes, m ? &a.up_map : &a.map, &full[at], cur.c * (kUK / 2), cur.row);
+                tma_load_2d(codes + (at * NM + m) * kCodeBytes, m ? &a.up_map : &a.map, &full[at], c_c * (kUK / 2), c_row);
         }
-        const uint32_t sto = smem_u32(scales) + at * L::kScales + srow * L::kScaleRow + soff;
-        const bool in_row = soff < static_cast<int>(srow_bytes) - cur.c * unit_scales;   // K / 8 at most
+        ++c_u;
+        ++c_c;
+        --c_left;
+    };
+    // The next unit's scales: where its row lies, the bytes from there to the row's end, and to row g + 8.
+    const int row0 = row_of(g), unit_scales = a.unit_scales;
+    uint32_t next[NM][2][L::W], now[NM][2][L::W];
+    const uint8_t* s_at = nullptr;
+    int s_left = 0, s_below = 0;
+    auto aim_scales = [&](int tile, int u) {
+        const int seg = segs > 1 ? u / cps : 0, lo = min(tile * kRows + row0, M - 1), hi = min(tile * kRows + row0 + 8, M - 1);
+        const int64_t row = static_cast<int64_t>(a.weights ? s_expert[seg] : expert) * M + lo;
+        const int off = (u - seg * cps) * unit_scales;
+        s_at = a.scales + row * a.srow + off;
+        s_left = a.srow - off;
+        s_below = (hi - lo) * a.srow;
+    };
+    auto load_scales = [&] {
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll 1
-            for (int row = 0; srow + row < kRows; row += sstep) {
-                const bool on = in_row && srow + row < cur.rows;
-                copy_scales(sto + m * (kRows * L::kScaleRow) + row * L::kScaleRow, cur.s[m] + (on ? row * srow_bytes : cur.back), on);
+        for (int m = 0; m < NM; ++m) {
+            const uint8_t* p = m ? s_at + (a.up_scales - a.scales) : s_at;
+            if (a.scale_piece > 0 && s_left >= unit_scales) {
+                load_row_scales(next[m][0], p, unit_scales, a.scale_piece);
+                load_row_scales(next[m][1], p + s_below, unit_scales, a.scale_piece);
+            } else {
+                load_row_scales_one<SK>(next[m][0], p, kUnitGroups >> a.shift, s_left);
+                load_row_scales_one<SK>(next[m][1], p + s_below, kUnitGroups >> a.shift, s_left);
             }
-        ++cur.u;
-        ++cur.c;
-#pragma unroll
-        for (int m = 0; m < NM; ++m) cur.s[m] += unit_scales;
+        }
+        s_at += unit_scales;
+        s_left -= unit_scales;
     };
 
     // in registers: an instruction takes one constant
@@ -443,9 +469,8 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
     asm volatile("" : "+r"(mask4), "+r"(bits4));
     float acc[NM][NT][AC];
     // adds the products of the unit in a slot, whose x is number ul in shared memory
-    const int row0 = row_of(g);
     const uint8_t* const c_lane = codes + row0 * 128;
-    const uint8_t* const s_lane = scales + row0 * L::kScaleRow;
+    const int odd = GP == 4 ? t4 & 1 : 0;
     auto work = [&](int at_slot, int ul) {
         const uint8_t* slot = c_lane + at_slot * (NM * kCodeBytes);
         const uint8_t* x_at = x_base + ul * x_step;
@@ -500,11 +525,10 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
             const int gi = 2 * pair * GP;
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
-                const uint8_t* row = s_lane + at_slot * L::kScales + m * (kRows * L::kScaleRow);
                 if constexpr (GP == 1) {
                     float s[2], r[2];
-                    read_scales<SK>(row, gi, a.shift, bf16, s);
-                    read_scales<SK>(row + 8 * L::kScaleRow, gi, a.shift, bf16, r);
+                    pair_of_scales<SK>(now[m][0], pair, 0, a.shift, bf16, s);
+                    pair_of_scales<SK>(now[m][1], pair, 0, a.shift, bf16, r);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -519,8 +543,8 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float s[2], r[2];
-                        read_scales<SK>(row, gi + h * GP + g2, a.shift, bf16, s);
-                        read_scales<SK>(row + 8 * L::kScaleRow, gi + h * GP + g2, a.shift, bf16, r);
+                        pair_of_scales<SK>(now[m][0], (2 * pair + h) * GP / 2, odd, a.shift, bf16, s);
+                        pair_of_scales<SK>(now[m][1], (2 * pair + h) * GP / 2, odd, a.shift, bf16, r);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const float2 f = *reinterpret_cast<const float2*>(f_at + n * VT * kUnitGroups + gi + h * GP);
@@ -534,12 +558,11 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
     };
 
     // A warp's units of a tile are a run of them; the copies of D units are in flight, those of the next tile's first
-    // ones while the last of this one's are worked on.  Each unit is a group of copies (or an empty one).
+    // ones while the last of this one's are worked on.
     const bool whole = units <= cap;     // all of x fits: staged once
     bool ahead = false;                  // the ring holds the first units already
-    int at = 0;                          // slot of the next unit
-    uint32_t phase = 0;                  // of the slots' barriers, a bit each
-    uint32_t armed = 0;                  // slots that a copy was issued for and not waited for
+    int at = 0, flying = 0;              // slot of the next unit, slots with a copy that was not waited for
+    uint32_t phase = 0;                  // of the next slot's barrier
     bool ok = true;                      // no wait has run out
     float* mine = red + team * (NM * KW * kRows * VS);
     for (int tile0 = part * teams; tile0 < tiles; tile0 += tile_step) {
@@ -552,57 +575,67 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < AC; ++i) acc[m][n][i] = 0.0f;
         for (int u0 = 0; u0 < units; u0 += cap) {
-            const int u1 = min(u0 + cap, units), per = (u1 - u0 + KW - 1) / KW;
-            const int first = min(u0 + kwarp * per, u1), last = min(first + per, u1), run = last - first;
+            const int u1 = min(u0 + cap, units), per = (u1 - u0 + KW - 1) >> a.kw_log;
+            const int first = min(u0 + kwarp * per, u1), run = min(first + per, u1) - first;
             const bool need = !whole || tile0 == static_cast<int>(part) * teams;      // x of these units
             if (need && a.x_wide) {
                 if (tile0 != static_cast<int>(part) * teams || u0 > 0) __syncthreads();   // the last ones are read
                 copy_x(u0, u1);
-                copy_commit();
             }
-            if (live && !ahead) {
-                cur.tile = tile;
-                cur.u = first;
-                cur.c = cps;
+            const bool fill = live && !ahead && ok && run > 0;
+            if (fill) {
+                c_tile = tile;
+                c_u = first;
+                c_c = cps;
+                c_left = run;
+                aim_scales(tile, first);
+                load_scales();
             }
             // D copies ahead, the wait for x, the units in turn
-            for (int i = live && !ahead ? -D : 0; i < run || (need && i <= 0); ++i) {
+            for (int i = fill ? -D : 0; i < run || (need && i <= 0); ++i) {
                 if (i == 0 && need) {
-                    if (live)            // x is older than the D units
-                        copy_wait<D>();
-                    else
-                        copy_wait<0>();
+                    copy_wait();
                     if (!a.x_wide) __syncthreads();
                     stage(u0, u1);
                     __syncthreads();
                 }
                 if (i >= 0) {
-                    if (i >= run || !live) break;
-                    copy_wait<D - 1>();
-                    ok = ok && mbar_wait(&full[at], (phase >> at) & 1, abort_flag, a.status, DEV_TIMEOUT_PRODUCER);
-                    ok = __all_sync(kAll, ok);
-                    if (ok) {
-                        phase ^= 1u << at;
-                        armed &= ~(1u << at);
+                    if (i >= run || !live || !ok) break;
+#pragma unroll
+                    for (int m = 0; m < NM; ++m)
+#pragma unroll
+                        for (int w = 0; w < L::W; ++w) {
+                            now[m][0][w] = next[m][0][w];
+                            now[m][1][w] = next[m][1][w];
+                        }
+                    if (i + 1 < run) {
+                        if (segs > 1 && s_left <= 0) aim_scales(tile, first + i + 1);
+                        load_scales();
+                    } else if (whole && tile + tile_step < tiles) {
+                        aim_scales(tile + tile_step, first);
+                        load_scales();
                     }
-                    if (ok) work(at, first + i - u0);
+                    ok = __all_sync(kAll, mbar_wait(&full[at], phase, abort_flag, a.status, DEV_TIMEOUT_PRODUCER));
+                    if (!ok) break;
+                    --flying;
+                    work(at, first + i - u0);
                     __syncwarp();
                 }
                 // the next unit of this run, or (if x stays) the first of the next tile's
-                if (cur.u >= last && whole && run > 0 && cur.tile + tile_step < tiles) {
-                    cur.tile += tile_step;
-                    cur.u = first;
-                    cur.c = cps;
+                if (c_left == 0 && whole && c_tile + tile_step < tiles) {
+                    c_tile += tile_step;
+                    c_u = first;
+                    c_c = cps;
+                    c_left = run;
                 }
-                if (cur.u < last) {
-                    if (cur.c == cps) aim();
-                    if (ok) {
-                        fetch(at);
-                        armed |= 1u << at;
-                    }
+                if (c_left > 0) {
+                    copy_next(at);
+                    ++flying;
                 }
-                copy_commit();
-                at = at + 1 == D ? 0 : at + 1;
+                if (++at == D) {
+                    at = 0;
+                    if (i >= 0) phase ^= 1;
+                }
             }
             ahead = whole;
         }
@@ -650,9 +683,13 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
         }
     }
     // a wait ran out: this warp's copies land before its shared memory goes to another block
-    if (!ok)
-        for (int i = 0; i < D; ++i)
-            if (armed & (1u << i)) matvec_drain(&full[i], (phase >> i) & 1, a.status);
+    for (; !ok && flying > 0; --flying) {
+        matvec_drain(&full[at], phase, a.status);
+        if (++at == D) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
 }
 
 int ilog2(int n) { return n > 1 ? 1 + ilog2(n / 2) : 0; }
@@ -722,13 +759,11 @@ cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s) {
     a.x_wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld_x * elem_bytes(a.dt_x)) % 16 == 0;
     const int size = a.format == 0 ? 1 : elem_bytes(a.dt_scale);
     // pieces of a row's scales of a unit, as large as addresses and rows allow
-    const uint64_t lie = reinterpret_cast<uintptr_t>(a.scales) | reinterpret_cast<uintptr_t>(a.up_scales) |
-                         static_cast<uint64_t>((a.K / 32) >> a.shift) * size | static_cast<uint64_t>((kUnitGroups >> a.shift) * size);
-    a.scale_piece = lie % 16 == 0 ? 16 : lie % 8 == 0 ? 8 : lie % 4 == 0 ? 4 : 0;
-    a.scale_size = a.scale_piece > 0 ? a.scale_piece : size;
-    a.unit_scales = (kUnitGroups >> a.shift) * size;
-    a.scale_log = ilog2(a.unit_scales / a.scale_size);
     a.srow = (a.K / 32 >> a.shift) * size;
+    a.unit_scales = (kUnitGroups >> a.shift) * size;
+    const uint64_t lie = reinterpret_cast<uintptr_t>(a.scales) | reinterpret_cast<uintptr_t>(a.up_scales) |
+                         static_cast<uint64_t>(a.srow) | static_cast<uint64_t>(a.unit_scales);
+    a.scale_piece = lie % 16 == 0 ? 16 : lie % 8 == 0 ? 8 : lie % 4 == 0 ? 4 : 0;
     a.cps = (a.K + kUK - 1) / kUK;
     a.tiles = static_cast<int>((static_cast<int64_t>(a.M) + kRows - 1) / kRows);
     if (a.format == 0) return a.up_codes ? matvec_of<SCALE_E8M0, true>(a, s) : matvec_of<SCALE_E8M0, false>(a, s);
