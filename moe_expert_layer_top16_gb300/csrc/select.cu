@@ -27,7 +27,8 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 // A logit as the operators read it: what is not a number closes an expert like
 // minus infinity, plus infinity counts as the largest number.
-__device__ __forceinline__ float open_logit(float l) { return l == l ? fminf(l, FLT_MAX) : -INFINITY; }
+// (fmaxf and fminf go past NaN.)
+__device__ __forceinline__ float open_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
 // A lane's part of a row: value i V + j is that of expert (32 i + lane) V + j;
 // minus infinity behind the last expert.
@@ -50,15 +51,11 @@ __device__ __forceinline__ void load_row(const void* base, int64_t off, int E, i
 }
 
 // ------------------------------------------------------------------ reductions over a warp
-// Floats as unsigned integers of the same order (0: below every number).
-__device__ __forceinline__ uint32_t order_bits(float k) {
-    const uint32_t u = (k == 0.0f) ? 0u : __float_as_uint(k);     // -0 ties with +0, as the floats compare
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
 }
-__device__ __forceinline__ float bits_order(uint32_t b) {
-    return __uint_as_float((b & 0x80000000u) ? (b & 0x7fffffffu) : ~b);
-}
-__device__ __forceinline__ float warp_max(float v) { return bits_order(__reduce_max_sync(kAll, order_bits(v))); }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
@@ -71,7 +68,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // sigmoid(v) = e^min(v, 0) / (1 + e^-|v|), its numerator over the largest one,
 // which is 1 unless every value is negative.  Closed values give 0.
 template <int N>
-__device__ __forceinline__ float scores(const float (&v)[N], bool sigmoid, float (&x)[N]) {
+__device__ __forceinline__ float scores(float (&v)[N], bool sigmoid) {
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, v[i]);
@@ -79,27 +76,27 @@ __device__ __forceinline__ float scores(const float (&v)[N], bool sigmoid, float
     float sum = 0.0f;
     if (top == -INFINITY) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = 0.0f;
+        for (int i = 0; i < N; ++i) v[i] = 0.0f;
         return 0.0f;
     }
     if (!sigmoid) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x[i] = expf(v[i] - top);
-            sum += x[i];
+            v[i] = expf(v[i] - top);
+            sum += v[i];
         }
     } else if (top >= 0.0f) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float u = expf(-fabsf(v[i]));
-            x[i] = (v[i] >= 0.0f ? 1.0f : u) / (1.0f + u);
-            sum += x[i];
+            v[i] = __fdividef(v[i] >= 0.0f ? 1.0f : u, 1.0f + u);
+            sum += v[i];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x[i] = expf(v[i] - top) / (1.0f + expf(v[i]));
-            sum += x[i];
+            v[i] = __fdividef(expf(v[i] - top), 1.0f + expf(v[i]));
+            sum += v[i];
         }
     }
     return warp_sum(sum);
@@ -117,19 +114,19 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 
 // ------------------------------------------------------------------ select
 // The k-th largest of the lanes' largest keys is at most the k-th largest key:
-// what reaches it, some 1.4 k of the keys, are the candidates, which go to
-// shared memory and are ranked by counting the better ones.  (k rounds of a
-// warp-wide maximum over all keys, the first form of this kernel, are kept for
-// rows with more than kCand candidates: many equal keys.)
+// what reaches it, some 1.4 k of the keys, are the candidates, whose numbers go
+// to shared memory.  Up to 32 of them are sorted over the lanes, up to kCand
+// ranked by counting the better ones; rows with more (many equal keys) take k
+// rounds of a maximum over the row.
 //
 // Keys with a bias are defined in 64 bits, whose exponentials would take some
 // ten times as long as the logits' way from memory.  They are estimated in 32:
 // |estimate - key| <= 1e-6 + 2^-22 |estimate| (__expf is off by 2 + 1.17 |l|
 // units in the last place, which sigmoid(l) (1 - sigmoid(l)) turns into less
-// than 2^-22 at most, the sum and the quotient add 2^-23 and the rounding of
-// the sum with b), candidates are what reaches the bound less twice that, and
-// only where two candidates are nearer than that and not equal in logit and bias are
-// the candidates ranked by keys of 64 bits.
+// than 2^-22 at most, sum and quotient add 2^-22, the sum with b its own
+// rounding), candidates are what reaches the bound less twice that, and only
+// where two neighbours in the order are nearer than that and not equal in logit
+// and bias are the candidates ranked by keys of 64 bits.
 constexpr int kCand = 64;
 constexpr int kSelectWarps = 4;
 constexpr float kNear = 4e-6f, kNearRel = 0x1p-20f;
@@ -140,7 +137,8 @@ struct Candidate {
 };
 
 __device__ __forceinline__ float key32(float l, float b) {
-    return l == -INFINITY ? -INFINITY : __frcp_rn(1.0f + __expf(-l)) + b;
+    const float s = __fdividef(1.0f, 1.0f + __expf(-l)) + b;
+    return l == -INFINITY ? -INFINITY : s;
 }
 __device__ __forceinline__ double key64(float l, float b) {
     return 1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(b);
@@ -149,16 +147,30 @@ __device__ __forceinline__ double key64(float l, float b) {
 __device__ __forceinline__ float open_bias(float b) { return open_logit(b); }
 
 // Descending over the lanes.
-__device__ __forceinline__ uint32_t bitonic_step(uint32_t x, int lane, int stride, bool down) {
-    const uint32_t y = __shfl_xor_sync(kAll, x, stride);
-    return (((lane & stride) == 0) == down) ? max(x, y) : min(x, y);
+__device__ __forceinline__ float bitonic_step(float x, int lane, int stride, bool down) {
+    const float y = __shfl_xor_sync(kAll, x, stride);
+    return (((lane & stride) == 0) == down) ? fmaxf(x, y) : fminf(x, y);
 }
-__device__ __forceinline__ uint32_t sort_lanes(uint32_t x, int lane) {
+__device__ __forceinline__ float sort_lanes(float x, int lane) {
 #pragma unroll
     for (int size = 2; size <= 32; size *= 2)
 #pragma unroll
         for (int stride = size / 2; stride > 0; stride /= 2) x = bitonic_step(x, lane, stride, (lane & size) == 0);
     return x;
+}
+// Keys with their experts, by (key descending, expert ascending).
+__device__ __forceinline__ void sort_keys(float& key, int& e, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int stride = size / 2; stride > 0; stride /= 2) {
+            const float k2 = __shfl_xor_sync(kAll, key, stride);
+            const int e2 = __shfl_xor_sync(kAll, e, stride);
+            const bool other = k2 > key || (k2 == key && e2 < e);            // the partner's is the better one
+            const bool take = other == (((lane & stride) == 0) == ((lane & size) == 0));
+            key = take ? k2 : key;
+            e = take ? e2 : e;
+        }
 }
 
 // Rows with too many candidates: k rounds, each the largest key of 64 bits
@@ -222,48 +234,47 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
         return;
     }
     Candidate* cand = s_cand[warp];
+    auto logit = [&](int e) {
+        float f[1];
+        raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, a.dt), a.dt, f);
+        return open_logit(f[0]);
+    };
+    // keys; without a bias these are the logits
     float v[N];
-    load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
-    uint32_t key[N];
+    if (a.bias) {
+        float b[N];
+        load_row<V, NI>(a.bias, 0, E, ELEM_F32, lane, b);
+        load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e0 = (32 * i + lane) * V;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = i * V + j;
-            float est = v[c];
-            if (a.bias && e0 < E) est = key32(est, open_bias(a.bias[e0 + j]));
-            key[c] = est == -INFINITY ? 0u : order_bits(est);
-        }
+        for (int c = 0; c < N; ++c) v[c] = key32(v[c], b[c]);
+    } else {
+        load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
     }
     // the bound: the k-th largest of 32 or 64 disjoint sets' largest keys
-    uint32_t h0 = 0, h1 = 0;
+    float h0 = -INFINITY, h1 = -INFINITY;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
         if (c < N / 2)
-            h0 = max(h0, key[c]);
+            h0 = fmaxf(h0, v[c]);
         else
-            h1 = max(h1, key[c]);
+            h1 = fmaxf(h1, v[c]);
     }
-    uint32_t least;
+    float least;
     if (k <= 16) {
-        least = sort_lanes(max(h0, h1), lane);
+        least = sort_lanes(fmaxf(h0, h1), lane);
     } else {
         h0 = sort_lanes(h0, lane);
         h1 = __shfl_sync(kAll, sort_lanes(h1, lane), 31 - lane);
-        least = max(h0, h1);             // the 32 largest of both, as a bitonic sequence
+        least = fmaxf(h0, h1);           // the 32 largest of both, as a bitonic sequence
 #pragma unroll
         for (int stride = 16; stride > 0; stride /= 2) least = bitonic_step(least, lane, stride, true);
     }
     least = __shfl_sync(kAll, least, k - 1);
-    if (a.bias && least) {
-        const float f = bits_order(least);
-        least = order_bits(f - (kNear + kNearRel * fabsf(f)));
-    }
-    least = max(least, 1u);
+    if (a.bias) least -= kNear + kNearRel * fabsf(least);
+    least = fmaxf(least, -FLT_MAX);      // (fewer than k sets have an open expert: all that are open)
     uint32_t mask = 0;
 #pragma unroll
-    for (int c = 0; c < N; ++c) mask |= key[c] >= least ? 1u << c : 0u;
+    for (int c = 0; c < N; ++c) mask |= v[c] >= least ? 1u << c : 0u;
     const int mine = __popc(mask);
     int incl = mine;
 #pragma unroll
@@ -272,12 +283,9 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
         if (lane >= o) incl += n;
     }
     const int n = __shfl_sync(kAll, incl, 31);
-    s_win[warp][lane] = -1;
-    s_win_l[warp][lane] = -INFINITY;
-    if (n > kCand) {
-        __syncwarp();
-        select_rounds(a, t, lane, s_win[warp], s_win_l[warp]);
-    } else {
+    int e = -1;                          // of slot `lane`; -1 behind the last slot and where no expert was left
+    float l[1] = {-INFINITY};
+    if (n <= kCand) {
         int pos = incl - mine;
         while (mask) {
             const int c = __ffs(mask) - 1;
@@ -285,68 +293,113 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
             cand[pos++].e = (32 * (c / V) + lane) * V + c % V;
         }
         __syncwarp();
-        Candidate own[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int p = lane + 32 * u;
-            if (p < n) {
-                own[u].e = cand[p].e;
-                float f[1];
-                raw_to_f32(load_raw<1>(a.logits, t * a.ld + own[u].e, a.dt), a.dt, f);
-                own[u].l = open_logit(f[0]);
-                own[u].b = a.bias ? open_bias(a.bias[own[u].e]) : 0.0f;
-                own[u].key = a.bias ? key32(own[u].l, own[u].b) : own[u].l;
-                cand[p] = own[u];
+    }
+    if (n <= 32) {
+        e = lane < n ? cand[lane].e : 0x7fffffff;
+        float key = -INFINITY;
+        if (lane < n) key = a.bias ? key32(logit(e), open_bias(a.bias[e])) : logit(e);
+        sort_keys(key, e, lane);
+        float bias = 0.0f;
+        if (lane < n) {
+            l[0] = logit(e);
+            if (a.bias) bias = open_bias(a.bias[e]);
+        }
+        if (a.bias) {
+            const float key2 = __shfl_down_sync(kAll, key, 1), l2 = __shfl_down_sync(kAll, l[0], 1), b2 = __shfl_down_sync(kAll, bias, 1);
+            const bool near = lane < k && lane + 1 < n && key - key2 <= kNear + kNearRel * fabsf(key) && !(l2 == l[0] && b2 == bias);
+            if (__any_sync(kAll, near)) {
+                const double exact = lane < n ? key64(l[0], bias) : -INFINITY;
+                int rank = 0;
+                for (int p = 0; p < n; ++p) {
+                    const double q = __shfl_sync(kAll, exact, p);
+                    const int f = __shfl_sync(kAll, e, p);
+                    rank += (q > exact || (q == exact && f < e)) ? 1 : 0;
+                }
+                if (lane < n) {
+                    s_win[warp][rank] = e;
+                    s_win_l[warp][rank] = l[0];
+                }
+                __syncwarp();
+                if (lane < n) {
+                    e = s_win[warp][lane];
+                    l[0] = s_win_l[warp][lane];
+                }
             }
         }
+        if (lane >= min(n, k)) {
+            e = -1;
+            l[0] = -INFINITY;
+        }
+    } else {
+        s_win[warp][lane] = -1;
+        s_win_l[warp][lane] = -INFINITY;
         __syncwarp();
-        int rank[2] = {0, 0};
-        bool near = false;
-        for (int p = 0; p < n; ++p) {
-            const Candidate q = cand[p];
+        if (n > kCand) {
+            select_rounds(a, t, lane, s_win[warp], s_win_l[warp]);
+        } else {
+            // two candidates a lane
+            Candidate own[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                if (lane + 32 * u >= n) continue;
-                rank[u] += (q.key > own[u].key || (q.key == own[u].key && q.e < own[u].e)) ? 1 : 0;
-                if (a.bias)
-                    near |= fabsf(q.key - own[u].key) <= kNear + kNearRel * fabsf(own[u].key) &&
-                            !(q.l == own[u].l && q.b == own[u].b);
-            }
-        }
-        if (a.bias && __any_sync(kAll, near)) {
-            double exact[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                rank[u] = 0;
-                if (lane + 32 * u < n) s_key[warp][lane + 32 * u] = exact[u] = key64(own[u].l, own[u].b);
+                const int p = lane + 32 * u;
+                if (p < n) {
+                    own[u].e = cand[p].e;
+                    own[u].l = logit(own[u].e);
+                    own[u].b = a.bias ? open_bias(a.bias[own[u].e]) : 0.0f;
+                    own[u].key = a.bias ? key32(own[u].l, own[u].b) : own[u].l;
+                    cand[p] = own[u];
+                }
             }
             __syncwarp();
+            int rank[2] = {0, 0};
+            bool near = false;
             for (int p = 0; p < n; ++p) {
-                const double q = s_key[warp][p];
-                const int e = cand[p].e;
+                const Candidate q = cand[p];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (lane + 32 * u < n) rank[u] += (q > exact[u] || (q == exact[u] && e < own[u].e)) ? 1 : 0;
+                for (int u = 0; u < 2; ++u) {
+                    if (lane + 32 * u >= n) continue;
+                    rank[u] += (q.key > own[u].key || (q.key == own[u].key && q.e < own[u].e)) ? 1 : 0;
+                    if (a.bias)
+                        near |= fabsf(q.key - own[u].key) <= kNear + kNearRel * fabsf(own[u].key) &&
+                                !(q.l == own[u].l && q.b == own[u].b);
+                }
             }
+            if (a.bias && __any_sync(kAll, near)) {
+                double exact[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    rank[u] = 0;
+                    if (lane + 32 * u < n) s_key[warp][lane + 32 * u] = exact[u] = key64(own[u].l, own[u].b);
+                }
+                __syncwarp();
+                for (int p = 0; p < n; ++p) {
+                    const double q = s_key[warp][p];
+                    const int f = cand[p].e;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (lane + 32 * u < n) rank[u] += (q > exact[u] || (q == exact[u] && f < own[u].e)) ? 1 : 0;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (lane + 32 * u < n && rank[u] < k) {
+                    s_win[warp][rank[u]] = own[u].e;
+                    s_win_l[warp][rank[u]] = own[u].l;
+                }
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (lane + 32 * u < n && rank[u] < k) {
-                s_win[warp][rank[u]] = own[u].e;
-                s_win_l[warp][rank[u]] = own[u].l;
-            }
+        __syncwarp();
+        e = s_win[warp][lane];
+        l[0] = s_win_l[warp][lane];
     }
-    __syncwarp();
-    const int e = s_win[warp][lane];             // -1 behind the last slot and where no expert was left
-    const float l[1] = {s_win_l[warp][lane]};
-    float w[1];
+    float w;
     if (a.normalize) {
-        const float sum = scores(l, a.sigmoid != 0, w);
-        w[0] = sum > 0.0f ? w[0] / sum : 0.0f;
+        float x[1] = {l[0]};
+        const float sum = scores(x, a.sigmoid != 0);
+        w = sum > 0.0f ? x[0] / sum : 0.0f;
     } else if (a.sigmoid) {
-        w[0] = e >= 0 ? sigmoid_of(l[0]) : 0.0f;
+        w = e >= 0 ? sigmoid_of(l[0]) : 0.0f;
     } else {
-        float top = -INFINITY, sum = 0.0f;
+        float top = -INFINITY, sum = 0.0f;           // (no bias goes with softmax: v are the logits)
 #pragma unroll
         for (int c = 0; c < N; ++c) top = fmaxf(top, v[c]);
         top = warp_max(top);
@@ -354,11 +407,11 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
 #pragma unroll
             for (int c = 0; c < N; ++c) sum += expf(v[c] - top);
         sum = warp_sum(sum);
-        w[0] = e >= 0 ? expf(l[0] - top) / sum : 0.0f;
+        w = e >= 0 ? expf(l[0] - top) / sum : 0.0f;
     }
     if (lane < k) {
         a.idx[t * k + lane] = e;
-        a.gates[t * k + lane] = a.scale * w[0];
+        a.gates[t * k + lane] = a.scale * w;
     }
 }
 
@@ -397,7 +450,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int64_t T,
 // goes to row b + s of the workspace: both numbers only grow along the tokens,
 // so that no two parts share a row.  A cluster of eight CTAs for each sequence
 // then adds its parts, each CTA an eighth of the experts.
-constexpr int kBalWarps = 16;
+constexpr int kBalWarps = 12;
 constexpr int kBalCtas = 8;
 
 template <int V, int NI>
@@ -441,12 +494,12 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const 
             if (!__any_sync(kAll, kept)) continue;
             if (kept) atomicAdd(&hist[e], 1);
             ++used;
-            float v[N], x[N];
+            float v[N];
             load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
-            const float sum = scores(v, a.sigmoid != 0, x);
+            const float sum = scores(v, a.sigmoid != 0);
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-            for (int c = 0; c < N; ++c) acc[c] = fmaf(x[c], inv, acc[c]);
+            for (int c = 0; c < N; ++c) acc[c] = fmaf(v[c], inv, acc[c]);
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -471,10 +524,11 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const 
 }
 
 // The parts are written by the launch that this one overlaps: plain loads.
-__global__ void __launch_bounds__(512) balance_sum_kernel(const BalanceArgs a) {
-    __shared__ float s_sum[4][128];
-    __shared__ int s_cnt[4][128];
-    __shared__ int s_tok[16];
+constexpr int kSumRows = 8;              // threads that share an expert's parts
+__global__ void __launch_bounds__(128 * kSumRows) balance_sum_kernel(const BalanceArgs a) {
+    __shared__ float s_sum[kSumRows][128];
+    __shared__ int s_cnt[kSumRows][128];
+    __shared__ int s_tok[4 * kSumRows];
     __shared__ float s_loss[kBalCtas];
     const int rank = blockIdx.x % kBalCtas, s = blockIdx.x / kBalCtas;
     const int col = threadIdx.x & 127, row = threadIdx.x >> 7;
@@ -489,8 +543,8 @@ __global__ void __launch_bounds__(512) balance_sum_kernel(const BalanceArgs a) {
     float sum = 0.0f;
     int cnt = 0, tok = 0;
     if (mine) {
-#pragma unroll 4
-        for (int64_t b = b0 + row; b < b1; b += 4) {
+#pragma unroll 8
+        for (int64_t b = b0 + row; b < b1; b += kSumRows) {
             const float* part = a.part + (b + s) * stride;
             sum += part[e];
             cnt += reinterpret_cast<const int32_t*>(part)[a.pitch + e];
@@ -504,8 +558,11 @@ __global__ void __launch_bounds__(512) balance_sum_kernel(const BalanceArgs a) {
     s_cnt[row][col] = cnt;
     __syncthreads();
     if (threadIdx.x < 128) {
-        sum = (s_sum[0][col] + s_sum[1][col]) + (s_sum[2][col] + s_sum[3][col]);
-        cnt = (s_cnt[0][col] + s_cnt[1][col]) + (s_cnt[2][col] + s_cnt[3][col]);
+#pragma unroll
+        for (int r = 1; r < kSumRows; ++r) {
+            sum += s_sum[r][col];
+            cnt += s_cnt[r][col];
+        }
         if (mine) a.counts[static_cast<int64_t>(s) * a.E + e] = cnt;
         s_sum[0][col] = mine ? static_cast<float>(cnt) * sum : 0.0f;
     }
@@ -521,7 +578,7 @@ __global__ void __launch_bounds__(512) balance_sum_kernel(const BalanceArgs a) {
     cluster_sync_all();
     if (rank == 0 && threadIdx.x == 0) {
         int n = 0;
-        for (int w = 0; w < 16; ++w) n += s_tok[w];
+        for (int w = 0; w < 4 * kSumRows; ++w) n += s_tok[w];
         float x = 0.0f;
         for (int r = 0; r < kBalCtas; ++r) x += s_loss[r];
         const float m = static_cast<float>(max(n, 1));
@@ -536,8 +593,30 @@ __global__ void __launch_bounds__(512) balance_sum_kernel(const BalanceArgs a) {
 // the gates w over the winners, the gates give w_j r_j (g_j - sum g w); not
 // normalised, g_j s_j r_j, or for the softmax over all p_e ([e won] g_e - sum g p).
 // A lane holds slot j = lane; the slots' values meet their experts' lanes in a row
-// of shared memory.
+// of shared memory.  One exponential a logit: sigmoid(l) and 1 - sigmoid(l) are
+// {1, u} / (1 + u) with u = e^-|l|, and u is kept, with l's sign, for the second pass.
 constexpr int kBackWarps = 4;
+
+// Eight (or one) counts as floats.
+template <int V>
+__device__ __forceinline__ void load_counts(const int32_t* p, bool wide, float (&c)[V]) {
+    if constexpr (V == 8) {
+        if (wide) {
+            const int4 a = __ldg(reinterpret_cast<const int4*>(p)), b = __ldg(reinterpret_cast<const int4*>(p) + 1);
+            c[0] = static_cast<float>(a.x);
+            c[1] = static_cast<float>(a.y);
+            c[2] = static_cast<float>(a.z);
+            c[3] = static_cast<float>(a.w);
+            c[4] = static_cast<float>(b.x);
+            c[5] = static_cast<float>(b.y);
+            c[6] = static_cast<float>(b.z);
+            c[7] = static_cast<float>(b.w);
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) c[j] = static_cast<float>(__ldg(p + j));
+}
 
 template <int V, int NI>
 __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const RouterBackArgs a) {
@@ -549,53 +628,86 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
     const int E = a.E, k = a.k;
     const bool sigmoid = a.sigmoid != 0;
     float* srow = s_rows + warp * a.pitch;
-    float v[N], d[N];
-    load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
     int e = lane < k ? a.idx[t * k + lane] : -1;
     if (e < 0 || e >= E) e = -1;
     const bool any = __any_sync(kAll, e >= 0);
     const int s = a.d_loss && any ? sequence_of(a.seq, a.S, a.T, t, lane) : -1;
     const bool all = !a.normalize && !sigmoid && a.d_gates;       // gates by the softmax over all
-    float inv = 0.0f;
-    if (any && (s >= 0 || all)) {
-        const float sum = scores(v, sigmoid, d);
+    // x: scores as multiples of p; with sigmoid scores u, negative where the logit is
+    float x[N];
+    float inv = 0.0f, top = -INFINITY, inner = 0.0f, f = 0.0f;
+    bool low = false;                                    // sigmoid scores of negative logits only: x are the scores
+    const int32_t* cnt = nullptr;
+    const bool wide = E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.counts) & 15) == 0;
+    const bool shared = any && (s >= 0 || all);
+    if (shared) {
+        load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, x);
+#pragma unroll
+        for (int c = 0; c < N; ++c) top = fmaxf(top, x[c]);
+        top = warp_max(top);
+        if (s >= 0) {
+            const float n = static_cast<float>(max(a.tokens[s], 1));
+            f = a.d_loss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n;
+            cnt = a.counts + static_cast<int64_t>(s) * E;
+        }
+        low = sigmoid && top < 0.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e0 = (32 * i + lane) * V;
+            float ct[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) ct[j] = 0.0f;
+            if (cnt && e0 < E) load_counts<V>(cnt + e0, wide, ct);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = i * V + j;
+                float y;
+                if (top == -INFINITY) {
+                    y = x[c] = 0.0f;
+                } else if (!sigmoid) {
+                    y = x[c] = expf(x[c] - top);
+                } else if (!low) {
+                    const float u = expf(-fabsf(x[c]));
+                    y = __fdividef(x[c] >= 0.0f ? 1.0f : u, 1.0f + u);
+                    x[c] = copysignf(u, x[c]);
+                } else {
+                    y = __fdividef(expf(x[c] - top), 1.0f + expf(x[c]));
+                    x[c] = y;
+                }
+                sum += y;
+                inner = fmaf(y, f * ct[j], inner);
+            }
+        }
+        sum = warp_sum(sum);
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        inner = warp_sum(inner) * inv;
     }
     float shift = 0.0f;                                  // what is taken from every share
-    if (a.d_gates && any) {
+    const bool gates = a.d_gates && any;
+    if (gates) {
         float l = -INFINITY, g = 0.0f;
         if (e >= 0) {
-            float f[1];
-            raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, a.dt), a.dt, f);
-            l = open_logit(f[0]);
+            float q[1];
+            raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, a.dt), a.dt, q);
+            l = open_logit(q[0]);
             g = a.scale * a.d_gates[t * k + lane];
         }
         float val;
         if (a.normalize) {
-            const float lv[1] = {l};
-            float w[1];
-            const float sum = scores(lv, sigmoid, w);
+            float w[1] = {l};
+            const float sum = scores(w, sigmoid);
             w[0] = sum > 0.0f ? w[0] / sum : 0.0f;
             val = w[0] * (g - warp_sum(w[0] * g));
             if (sigmoid) val *= sigmoid_rest(l);
         } else if (sigmoid) {
             val = g * sigmoid_of(l) * sigmoid_rest(l);
         } else {
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < N; ++c) top = fmaxf(top, v[c]);
-            top = warp_max(top);
             val = l > -INFINITY ? g * expf(l - top) * inv : 0.0f;
             shift = warp_sum(val);
         }
         if (l == -INFINITY) val = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e0 = (32 * i + lane) * V;
-            if (e0 < E)
-#pragma unroll
-                for (int j = 0; j < V; ++j) srow[e0 + j] = 0.0f;
-        }
+        for (int c = lane * 4; c < a.pitch; c += 128) *reinterpret_cast<float4*>(srow + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         __syncwarp();
         const uint32_t same = __match_any_sync(kAll, e);
         if (__any_sync(kAll, e >= 0 && (same & (same - 1)))) {
@@ -608,40 +720,51 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
         }
         __syncwarp();
     }
-    float inner = 0.0f;
-    const int32_t* cnt = nullptr;
-    float f = 0.0f;
-    if (s >= 0) {
-        const float n = static_cast<float>(max(a.tokens[s], 1));
-        f = a.d_loss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n;
-        cnt = a.counts + static_cast<int64_t>(s) * E;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e0 = (32 * i + lane) * V;
-            if (e0 < E)
-#pragma unroll
-                for (int j = 0; j < V; ++j) inner = fmaf(d[i * V + j] * inv, f * static_cast<float>(cnt[e0 + j]), inner);
-        }
-        inner = warp_sum(inner);
-    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e0 = (32 * i + lane) * V;
         if (e0 >= E) continue;
-        float o[V];
+        float o[V], ct[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = i * V + j;
-            float r = 0.0f;
-            if (s >= 0) {
-                r = d[c] * inv * (f * static_cast<float>(cnt[e0 + j]) - inner);
-                if (sigmoid) r *= sigmoid_rest(v[c]);
+        for (int j = 0; j < V; ++j) o[j] = 0.0f;
+        if (gates) {
+            if constexpr (V == 8) {
+                const float4 p = *reinterpret_cast<const float4*>(srow + e0), q = *reinterpret_cast<const float4*>(srow + e0 + 4);
+                o[0] = p.x;
+                o[1] = p.y;
+                o[2] = p.z;
+                o[3] = p.w;
+                o[4] = q.x;
+                o[5] = q.y;
+                o[6] = q.z;
+                o[7] = q.w;
+            } else {
+                o[0] = srow[e0];
             }
-            if (a.d_gates && any) {
-                r += srow[e0 + j];
-                if (all) r -= d[c] * inv * shift;
+        }
+        if (all)
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[j] -= shared ? x[i * V + j] * inv * shift : 0.0f;
+        if (s >= 0) {
+            load_counts<V>(cnt + e0, wide, ct);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = i * V + j;
+                const float d = inv * (f * ct[j] - inner);
+                float r;
+                if (!sigmoid || low) {
+                    r = x[c] * d;
+                } else {
+                    const float u = fabsf(x[c]), q = __fdividef(1.0f, 1.0f + u);
+                    r = u * q * q * d;                   // sigmoid(l) (1 - sigmoid(l)) = u / (1 + u)^2
+                }
+                if (low) {
+                    float z[1];
+                    raw_to_f32(load_raw<1>(a.logits, t * a.ld + e0 + j, a.dt), a.dt, z);
+                    r *= sigmoid_rest(open_logit(z[0]));
+                }
+                o[j] += r;
             }
-            o[j] = r;
         }
         store_vec(a.d_logits, t * a.ld_d + e0, a.dt, o);
     }
@@ -681,7 +804,7 @@ cudaError_t balance_as(const BalanceArgs& a, cudaStream_t s) {
         const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess) return err;
     }
-    return launch_ex_cluster(balance_sum_kernel, dim3(static_cast<unsigned>(a.S) * kBalCtas), dim3(512), 0, s, a.T > 0, kBalCtas, a);
+    return launch_ex_cluster(balance_sum_kernel, dim3(static_cast<unsigned>(a.S) * kBalCtas), dim3(128 * kSumRows), 0, s, a.T > 0, kBalCtas, a);
 }
 
 }  // namespace
@@ -696,7 +819,7 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
     const unsigned blocks = static_cast<unsigned>((a.T + kSelectWarps - 1) / kSelectWarps);
 #define MOE_RUN(V, NI) (select_kernel<V, NI><<<blocks, kSelectWarps * 32, 0, s>>>(a), cudaGetLastError())
-    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E), a.E);
+    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0, a.E);
 #undef MOE_RUN
 }
 
