@@ -31,8 +31,8 @@ constexpr uint32_t kAll = 0xffffffffu;
 __device__ __forceinline__ float open_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
 // A lane's part of a row: value i V + j is that of expert (32 i + lane) V + j;
-// minus infinity behind the last expert.
-template <int V, int NI>
+// minus infinity behind the last expert.  OPEN: as open_logit has them.
+template <bool OPEN, int V, int NI>
 __device__ __forceinline__ void load_row(const void* base, int64_t off, int E, int dt, int lane, float (&v)[NI * V]) {
     RawVec<V> raw[NI];
 #pragma unroll
@@ -46,7 +46,7 @@ __device__ __forceinline__ void load_row(const void* base, int64_t off, int E, i
         float f[V];
         if (e < E) raw_to_f32(raw[i], dt, f);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[i * V + j] = e < E ? open_logit(f[j]) : -INFINITY;
+        for (int j = 0; j < V; ++j) v[i * V + j] = e < E ? (OPEN ? open_logit(f[j]) : f[j]) : -INFINITY;
     }
 }
 
@@ -62,13 +62,29 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// e^x and 1 / x by the instructions for them.  2^(x log2 e) is off by two units in
+// the last place and by |x| of them for the product's rounding: as much as the
+// rounding of an argument l - top, which e^-|x| turns into less than a unit of the
+// largest score.  (expf takes 8 instructions for this one's 2, and the row's
+// exponentials were more than half of these kernels.)
+__device__ __forceinline__ float fast_exp(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
+    return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // ------------------------------------------------------------------ scores
 // Scores of values v[N] as multiples of a common factor that keeps them from
 // underflow, and their sum over the warp.  Softmax: e^(v - max).  Sigmoid:
 // sigmoid(v) = e^min(v, 0) / (1 + e^-|v|), its numerator over the largest one,
 // which is 1 unless every value is negative.  Closed values give 0.
-template <int N>
-__device__ __forceinline__ float scores(float (&v)[N], bool sigmoid) {
+template <bool SIG, int N>
+__device__ __forceinline__ float scores(float (&v)[N]) {
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, v[i]);
@@ -77,29 +93,33 @@ __device__ __forceinline__ float scores(float (&v)[N], bool sigmoid) {
     if (top == -INFINITY) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = 0.0f;
-        return 0.0f;
-    }
-    if (!sigmoid) {
+    } else if (!SIG) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = expf(v[i] - top);
+            v[i] = fast_exp(v[i] - top);
             sum += v[i];
         }
     } else if (top >= 0.0f) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float u = expf(-fabsf(v[i]));
-            v[i] = __fdividef(v[i] >= 0.0f ? 1.0f : u, 1.0f + u);
+            const float u = fast_exp(-fabsf(v[i]));
+            v[i] = (v[i] >= 0.0f ? 1.0f : u) * fast_rcp(1.0f + u);
             sum += v[i];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = __fdividef(expf(v[i] - top), 1.0f + expf(v[i]));
+            v[i] = fast_exp(v[i] - top) * fast_rcp(1.0f + fast_exp(v[i]));
             sum += v[i];
         }
     }
     return warp_sum(sum);
+}
+// The same for one value a lane, which the gates are made of.
+__device__ __forceinline__ float slot_scores(float& v, bool sigmoid) {
+    const float top = warp_max(sigmoid ? fminf(v, 0.0f) : v);
+    v = top == -INFINITY ? 0.0f : expf((sigmoid ? fminf(v, 0.0f) : v) - top) / (sigmoid ? 1.0f + expf(-fabsf(v)) : 1.0f);
+    return warp_sum(v);
 }
 
 __device__ __forceinline__ float sigmoid_of(float v) {
@@ -121,7 +141,7 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 //
 // Keys with a bias are defined in 64 bits, whose exponentials would take some
 // ten times as long as the logits' way from memory.  They are estimated in 32:
-// |estimate - key| <= 1e-6 + 2^-22 |estimate| (__expf is off by 2 + 1.17 |l|
+// |estimate - key| <= 1e-6 + 2^-22 |estimate| (the exponential is off by 2 + |l|
 // units in the last place, which sigmoid(l) (1 - sigmoid(l)) turns into less
 // than 2^-22 at most, sum and quotient add 2^-22, the sum with b its own
 // rounding), candidates are what reaches the bound less twice that, and only
@@ -137,7 +157,7 @@ struct Candidate {
 };
 
 __device__ __forceinline__ float key32(float l, float b) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-l)) + b;
+    const float s = fast_rcp(1.0f + fast_exp(-l)) + b;
     return l == -INFINITY ? -INFINITY : s;
 }
 __device__ __forceinline__ double key64(float l, float b) {
@@ -243,13 +263,14 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
     float v[N];
     if (a.bias) {
         float b[N];
-        load_row<V, NI>(a.bias, 0, E, ELEM_F32, lane, b);
-        load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+        load_row<false, V, NI>(a.bias, 0, E, ELEM_F32, lane, b);
+        load_row<false, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
 #pragma unroll
         for (int c = 0; c < N; ++c) v[c] = key32(v[c], b[c]);
     } else {
-        load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+        load_row<false, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
     }
+    // (a key that is not a number is passed over by maxima and reaches no bound)
     // the bound: the k-th largest of 32 or 64 disjoint sets' largest keys
     float h0 = -INFINITY, h1 = -INFINITY;
 #pragma unroll
@@ -270,6 +291,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
         for (int stride = 16; stride > 0; stride /= 2) least = bitonic_step(least, lane, stride, true);
     }
     least = __shfl_sync(kAll, least, k - 1);
+    least = fminf(least, FLT_MAX);
     if (a.bias) least -= kNear + kNearRel * fabsf(least);
     least = fmaxf(least, -FLT_MAX);      // (fewer than k sets have an open expert: all that are open)
     uint32_t mask = 0;
@@ -393,21 +415,21 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
     }
     float w;
     if (a.normalize) {
-        float x[1] = {l[0]};
-        const float sum = scores(x, a.sigmoid != 0);
-        w = sum > 0.0f ? x[0] / sum : 0.0f;
+        w = l[0];
+        const float sum = slot_scores(w, a.sigmoid != 0);
+        w = sum > 0.0f ? w / sum : 0.0f;
     } else if (a.sigmoid) {
         w = e >= 0 ? sigmoid_of(l[0]) : 0.0f;
     } else {
         float top = -INFINITY, sum = 0.0f;           // (no bias goes with softmax: v are the logits)
 #pragma unroll
-        for (int c = 0; c < N; ++c) top = fmaxf(top, v[c]);
+        for (int c = 0; c < N; ++c) top = fmaxf(top, open_logit(v[c]));
         top = warp_max(top);
         if (top > -INFINITY)
 #pragma unroll
-            for (int c = 0; c < N; ++c) sum += expf(v[c] - top);
+            for (int c = 0; c < N; ++c) sum += fast_exp(open_logit(v[c]) - top);
         sum = warp_sum(sum);
-        w = e >= 0 ? expf(l[0] - top) / sum : 0.0f;
+        w = e >= 0 ? fast_exp(l[0] - top) / sum : 0.0f;
     }
     if (lane < k) {
         a.idx[t * k + lane] = e;
@@ -453,7 +475,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int64_t T,
 constexpr int kBalWarps = 12;
 constexpr int kBalCtas = 8;
 
-template <int V, int NI>
+template <bool SIG, int V, int NI>
 __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const BalanceArgs a) {
     extern __shared__ __align__(16) float s_sum[];       // [kBalWarps][pitch], then int32 [pitch] counts
     __shared__ int s_tokens;
@@ -495,8 +517,8 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const 
             if (kept) atomicAdd(&hist[e], 1);
             ++used;
             float v[N];
-            load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
-            const float sum = scores(v, a.sigmoid != 0);
+            load_row<true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+            const float sum = scores<SIG>(v);
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
             for (int c = 0; c < N; ++c) acc[c] = fmaf(v[c], inv, acc[c]);
@@ -593,8 +615,8 @@ __global__ void __launch_bounds__(128 * kSumRows) balance_sum_kernel(const Balan
 // the gates w over the winners, the gates give w_j r_j (g_j - sum g w); not
 // normalised, g_j s_j r_j, or for the softmax over all p_e ([e won] g_e - sum g p).
 // A lane holds slot j = lane; the slots' values meet their experts' lanes in a row
-// of shared memory.  One exponential a logit: sigmoid(l) and 1 - sigmoid(l) are
-// {1, u} / (1 + u) with u = e^-|l|, and u is kept, with l's sign, for the second pass.
+// of shared memory.  One exponential a logit: with u = e^-|l|, sigmoid(l) is {1, u} /
+// (1 + u) and sigmoid(l) (1 - sigmoid(l)) = u / (1 + u)^2; u is kept for the second pass.
 constexpr int kBackWarps = 4;
 
 // Eight (or one) counts as floats.
@@ -618,7 +640,7 @@ __device__ __forceinline__ void load_counts(const int32_t* p, bool wide, float (
     for (int j = 0; j < V; ++j) c[j] = static_cast<float>(__ldg(p + j));
 }
 
-template <int V, int NI>
+template <bool SIG, int V, int NI>
 __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const RouterBackArgs a) {
     extern __shared__ __align__(16) float s_rows[];      // [kBackWarps][pitch]
     constexpr int N = NI * V;
@@ -626,57 +648,69 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kBackWarps + warp;
     if (t >= a.T) return;
     const int E = a.E, k = a.k;
-    const bool sigmoid = a.sigmoid != 0;
     float* srow = s_rows + warp * a.pitch;
     int e = lane < k ? a.idx[t * k + lane] : -1;
     if (e < 0 || e >= E) e = -1;
     const bool any = __any_sync(kAll, e >= 0);
     const int s = a.d_loss && any ? sequence_of(a.seq, a.S, a.T, t, lane) : -1;
-    const bool all = !a.normalize && !sigmoid && a.d_gates;       // gates by the softmax over all
+    const bool all = !SIG && !a.normalize && a.d_gates;          // gates by the softmax over all
     // x: scores as multiples of p; with sigmoid scores u, negative where the logit is
-    float x[N];
-    float inv = 0.0f, top = -INFINITY, inner = 0.0f, f = 0.0f;
+    float x[N], ac[N];                                   // ac: a_e
+    float inv = 0.0f, top = -INFINITY, inner = 0.0f;
     bool low = false;                                    // sigmoid scores of negative logits only: x are the scores
-    const int32_t* cnt = nullptr;
-    const bool wide = E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.counts) & 15) == 0;
     const bool shared = any && (s >= 0 || all);
     if (shared) {
-        load_row<V, NI>(a.logits, t * a.ld, E, a.dt, lane, x);
+        load_row<true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, x);
+        if (s >= 0) {
+            const bool wide = E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.counts) & 15) == 0;
+            const float n = static_cast<float>(max(a.tokens[s], 1));
+            const float f = a.d_loss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n;
+            const int32_t* cnt = a.counts + static_cast<int64_t>(s) * E;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e0 = (32 * i + lane) * V;
+                float ct[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) ct[j] = 0.0f;
+                if (e0 < E) load_counts<V>(cnt + e0, wide, ct);
+#pragma unroll
+                for (int j = 0; j < V; ++j) ac[i * V + j] = f * ct[j];
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; ++c) ac[c] = 0.0f;
+        }
 #pragma unroll
         for (int c = 0; c < N; ++c) top = fmaxf(top, x[c]);
         top = warp_max(top);
-        if (s >= 0) {
-            const float n = static_cast<float>(max(a.tokens[s], 1));
-            f = a.d_loss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n;
-            cnt = a.counts + static_cast<int64_t>(s) * E;
-        }
-        low = sigmoid && top < 0.0f;
+        low = SIG && top < 0.0f;
         float sum = 0.0f;
+        if (top == -INFINITY) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e0 = (32 * i + lane) * V;
-            float ct[V];
+            for (int c = 0; c < N; ++c) x[c] = 0.0f;
+        } else if (!SIG) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) ct[j] = 0.0f;
-            if (cnt && e0 < E) load_counts<V>(cnt + e0, wide, ct);
+            for (int c = 0; c < N; ++c) {
+                x[c] = fast_exp(x[c] - top);
+                sum += x[c];
+                inner = fmaf(x[c], ac[c], inner);
+            }
+        } else if (!low) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = i * V + j;
-                float y;
-                if (top == -INFINITY) {
-                    y = x[c] = 0.0f;
-                } else if (!sigmoid) {
-                    y = x[c] = expf(x[c] - top);
-                } else if (!low) {
-                    const float u = expf(-fabsf(x[c]));
-                    y = __fdividef(x[c] >= 0.0f ? 1.0f : u, 1.0f + u);
-                    x[c] = copysignf(u, x[c]);
-                } else {
-                    y = __fdividef(expf(x[c] - top), 1.0f + expf(x[c]));
-                    x[c] = y;
-                }
+            for (int c = 0; c < N; ++c) {
+                const float u = fast_exp(-fabsf(x[c])), y = (x[c] >= 0.0f ? 1.0f : u) * fast_rcp(1.0f + u);
+                x[c] = u;                                // s (1 - s) is the same for l and -l
                 sum += y;
-                inner = fmaf(y, f * ct[j], inner);
+                inner = fmaf(y, ac[c], inner);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                const float q = fast_rcp(1.0f + fast_exp(x[c]));
+                const float y = fast_exp(x[c] - top) * q;
+                x[c] = y * q;                            // with 1 - s = q
+                sum += y;
+                inner = fmaf(y, ac[c], inner);
             }
         }
         sum = warp_sum(sum);
@@ -695,15 +729,15 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
         }
         float val;
         if (a.normalize) {
-            float w[1] = {l};
-            const float sum = scores(w, sigmoid);
-            w[0] = sum > 0.0f ? w[0] / sum : 0.0f;
-            val = w[0] * (g - warp_sum(w[0] * g));
-            if (sigmoid) val *= sigmoid_rest(l);
-        } else if (sigmoid) {
+            float w = l;
+            const float sum = slot_scores(w, SIG);
+            w = sum > 0.0f ? w / sum : 0.0f;
+            val = w * (g - warp_sum(w * g));
+            if (SIG) val *= sigmoid_rest(l);
+        } else if (SIG) {
             val = g * sigmoid_of(l) * sigmoid_rest(l);
         } else {
-            val = l > -INFINITY ? g * expf(l - top) * inv : 0.0f;
+            val = l > -INFINITY ? g * fast_exp(l - top) * inv : 0.0f;
             shift = warp_sum(val);
         }
         if (l == -INFINITY) val = 0.0f;
@@ -724,7 +758,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
     for (int i = 0; i < NI; ++i) {
         const int e0 = (32 * i + lane) * V;
         if (e0 >= E) continue;
-        float o[V], ct[V];
+        float o[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = 0.0f;
         if (gates) {
@@ -742,28 +776,18 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
                 o[0] = srow[e0];
             }
         }
-        if (all)
-#pragma unroll
-            for (int j = 0; j < V; ++j) o[j] -= shared ? x[i * V + j] * inv * shift : 0.0f;
-        if (s >= 0) {
-            load_counts<V>(cnt + e0, wide, ct);
+        if (shared) {
+            // p r (a - inner), and for gates by the softmax over all -p shift
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = i * V + j;
-                const float d = inv * (f * ct[j] - inner);
-                float r;
-                if (!sigmoid || low) {
-                    r = x[c] * d;
+                const float d = inv * (ac[c] - inner - shift);
+                if (SIG && !low) {
+                    const float q = fast_rcp(1.0f + x[c]);
+                    o[j] = fmaf(x[c] * q * q, d, o[j]);  // s (1 - s) = u / (1 + u)^2
                 } else {
-                    const float u = fabsf(x[c]), q = __fdividef(1.0f, 1.0f + u);
-                    r = u * q * q * d;                   // sigmoid(l) (1 - sigmoid(l)) = u / (1 + u)^2
+                    o[j] = fmaf(x[c], d, o[j]);
                 }
-                if (low) {
-                    float z[1];
-                    raw_to_f32(load_raw<1>(a.logits, t * a.ld + e0 + j, a.dt), a.dt, z);
-                    r *= sigmoid_rest(open_logit(z[0]));
-                }
-                o[j] += r;
             }
         }
         store_vec(a.d_logits, t * a.ld_d + e0, a.dt, o);
@@ -775,32 +799,37 @@ bool rows_wide(const void* p, int64_t ld, int dt, int E) {
     return E % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
 }
 
-// f<V, NI> with the fewest registers that hold E values a warp.
-#define MOE_ROW_FORMS(RUN, wide, E)              \
-    if (wide) {                                  \
-        if ((E) <= 256) return RUN(8, 1);        \
-        if ((E) <= 512) return RUN(8, 2);        \
-        return RUN(8, 4);                        \
-    }                                            \
-    if ((E) <= 256) return RUN(1, 8);            \
-    return RUN(1, 32)
+// RUN(SIG, V, NI) with the fewest registers that hold E values a warp.
+#define MOE_ROW_FORMS_OF(RUN, SIG, wide, E)      \
+    do {                                         \
+        if (wide) {                              \
+            if ((E) <= 256) return RUN(SIG, 8, 1); \
+            if ((E) <= 512) return RUN(SIG, 8, 2); \
+            return RUN(SIG, 8, 4);               \
+        }                                        \
+        if ((E) <= 256) return RUN(SIG, 1, 8);   \
+        return RUN(SIG, 1, 32);                  \
+    } while (0)
+#define MOE_ROW_FORMS(RUN, sigmoid, wide, E)     \
+    if (sigmoid) MOE_ROW_FORMS_OF(RUN, true, wide, E); \
+    MOE_ROW_FORMS_OF(RUN, false, wide, E)
 
 int64_t balance_per(int64_t T) {
     const int64_t per = (T + 151) / 152;
     return std::max<int64_t>(per, 1);
 }
 
-template <int V, int NI>
+template <bool SIG, int V, int NI>
 cudaError_t balance_as(const BalanceArgs& a, cudaStream_t s) {
     if (a.T > 0) {
         const unsigned blocks = static_cast<unsigned>((a.T + a.per - 1) / a.per);
         const size_t smem = sizeof(float) * static_cast<size_t>(kBalWarps + 1) * a.pitch;
         if (smem > 48 * 1024 - 256) {
-            const cudaError_t err = cudaFuncSetAttribute(balance_parts_kernel<V, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            const cudaError_t err = cudaFuncSetAttribute(balance_parts_kernel<SIG, V, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                          static_cast<int>(sizeof(float) * (kBalWarps + 1) * 1024));
             if (err != cudaSuccess) return err;
         }
-        balance_parts_kernel<V, NI><<<blocks, kBalWarps * 32, smem, s>>>(a);
+        balance_parts_kernel<SIG, V, NI><<<blocks, kBalWarps * 32, smem, s>>>(a);
         const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess) return err;
     }
@@ -818,16 +847,16 @@ size_t balance_workspace_bytes(int64_t T, int E, int S) {
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
     const unsigned blocks = static_cast<unsigned>((a.T + kSelectWarps - 1) / kSelectWarps);
-#define MOE_RUN(V, NI) (select_kernel<V, NI><<<blocks, kSelectWarps * 32, 0, s>>>(a), cudaGetLastError())
-    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0, a.E);
+#define MOE_RUN(SIG, V, NI) (select_kernel<V, NI><<<blocks, kSelectWarps * 32, 0, s>>>(a), cudaGetLastError())
+    MOE_ROW_FORMS_OF(MOE_RUN, , rows_wide(a.logits, a.ld, a.dt, a.E) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0, a.E);
 #undef MOE_RUN
 }
 
 cudaError_t launch_balance(BalanceArgs a, cudaStream_t s) {
     a.per = balance_per(a.T);
     a.pitch = (a.E + 3) & ~3;
-#define MOE_RUN(V, NI) balance_as<V, NI>(a, s)
-    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E), a.E);
+#define MOE_RUN(SIG, V, NI) balance_as<SIG, V, NI>(a, s)
+    MOE_ROW_FORMS(MOE_RUN, a.sigmoid, rows_wide(a.logits, a.ld, a.dt, a.E), a.E);
 #undef MOE_RUN
 }
 
@@ -836,8 +865,8 @@ cudaError_t launch_router_backward(RouterBackArgs a, cudaStream_t s) {
     a.pitch = (a.E + 3) & ~3;
     const unsigned blocks = static_cast<unsigned>((a.T + kBackWarps - 1) / kBackWarps);
     const size_t smem = a.d_gates ? sizeof(float) * kBackWarps * static_cast<size_t>(a.pitch) : 0;
-#define MOE_RUN(V, NI) (router_backward_kernel<V, NI><<<blocks, kBackWarps * 32, smem, s>>>(a), cudaGetLastError())
-    MOE_ROW_FORMS(MOE_RUN, rows_wide(a.logits, a.ld, a.dt, a.E) && rows_wide(a.d_logits, a.ld_d, a.dt, a.E), a.E);
+#define MOE_RUN(SIG, V, NI) (router_backward_kernel<SIG, V, NI><<<blocks, kBackWarps * 32, smem, s>>>(a), cudaGetLastError())
+    MOE_ROW_FORMS(MOE_RUN, a.sigmoid, rows_wide(a.logits, a.ld, a.dt, a.E) && rows_wide(a.d_logits, a.ld_d, a.dt, a.E), a.E);
 #undef MOE_RUN
 }
 
