@@ -17,6 +17,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "norm.cuh"
 #include "vec.cuh"
 
 namespace moe {
@@ -30,16 +31,8 @@ constexpr uint32_t kAll = 0xffffffffu;
 // (fmaxf and fminf go past NaN.)
 __device__ __forceinline__ float open_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
-// A lane's part of a row: value i V + j is that of expert (32 i + lane) V + j;
-// minus infinity behind the last expert.  OPEN: as open_logit has them.
 template <bool OPEN, int V, int NI>
-__device__ __forceinline__ void load_row(const void* base, int64_t off, int E, int dt, int lane, float (&v)[NI * V]) {
-    RawVec<V> raw[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = (32 * i + lane) * V;
-        if (e < E) raw[i] = load_raw<V>(base, off + e, dt);
-    }
+__device__ __forceinline__ void open_row(const RawVec<V> (&raw)[NI], int E, int dt, int lane, float (&v)[NI * V]) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e = (32 * i + lane) * V;
@@ -48,6 +41,21 @@ __device__ __forceinline__ void load_row(const void* base, int64_t off, int E, i
 #pragma unroll
         for (int j = 0; j < V; ++j) v[i * V + j] = e < E ? (OPEN ? open_logit(f[j]) : f[j]) : -INFINITY;
     }
+}
+
+// A lane's part of a row: value i V + j is that of expert (32 i + lane) V + j;
+// minus infinity behind the last expert.  DT: the type, or -1 where dt has it
+// (rows that are read by single elements).  OPEN: as open_logit has them.
+template <int DT, bool OPEN, int V, int NI>
+__device__ __forceinline__ void load_row(const void* base, int64_t off, int E, int dt, int lane, float (&v)[NI * V]) {
+    if (DT >= 0) dt = DT;
+    RawVec<V> raw[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = (32 * i + lane) * V;
+        if (e < E) raw[i] = load_raw<V>(base, off + e, dt);
+    }
+    open_row<OPEN, V, NI>(raw, E, dt, lane, v);
 }
 
 // ------------------------------------------------------------------ reductions over a warp
@@ -235,8 +243,8 @@ __device__ __noinline__ void select_rounds(const SelectArgs& a, int64_t t, int l
     }
 }
 
-template <int V, int NI>
-__global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectArgs a) {
+template <int DT, int V, int NI>
+__global__ void __launch_bounds__(kSelectWarps * 32, 7) select_kernel(const SelectArgs a) {
     __shared__ __align__(16) Candidate s_cand[kSelectWarps][kCand];
     __shared__ double s_key[kSelectWarps][kCand];
     __shared__ int s_win[kSelectWarps][32];
@@ -256,19 +264,23 @@ __global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const SelectA
     Candidate* cand = s_cand[warp];
     auto logit = [&](int e) {
         float f[1];
-        raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, a.dt), a.dt, f);
+        raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, DT >= 0 ? DT : a.dt), ELEM_F32, f);
         return open_logit(f[0]);
     };
     // keys; without a bias these are the logits
     float v[N];
+    load_row<DT, false, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
     if (a.bias) {
-        float b[N];
-        load_row<false, V, NI>(a.bias, 0, E, ELEM_F32, lane, b);
-        load_row<false, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
 #pragma unroll
-        for (int c = 0; c < N; ++c) v[c] = key32(v[c], b[c]);
-    } else {
-        load_row<false, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+        for (int i = 0; i < NI; ++i) {
+            const int e0 = (32 * i + lane) * V;
+            float b[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) b[j] = 0.0f;
+            if (e0 < E) raw_to_f32(load_raw<V>(a.bias, e0, ELEM_F32), ELEM_F32, b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i * V + j] = key32(v[i * V + j], b[j]);
+        }
     }
     // (a key that is not a number is passed over by maxima and reaches no bound)
     // the bound: the k-th largest of 32 or 64 disjoint sets' largest keys
@@ -472,18 +484,28 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int64_t T,
 // goes to row b + s of the workspace: both numbers only grow along the tokens,
 // so that no two parts share a row.  A cluster of eight CTAs for each sequence
 // then adds its parts, each CTA an eighth of the experts.
-constexpr int kBalWarps = 12;
+//
+// A warp's rows come through a ring in shared memory, of which a lane copies and
+// reads its own words: with a warp's loads and its arithmetic in turn, 32,768
+// rows of 256 took 31 us for 14, 8,192 of 896 23 us for 17.
 constexpr int kBalCtas = 8;
+__host__ __device__ constexpr int bal_warps(int n) { return n <= 8 ? 24 : n <= 16 ? 16 : 12; }       // of n values a lane: what the registers hold
+__host__ __device__ constexpr int bal_depth(int n) { return n <= 8 ? 4 : n <= 16 ? 3 : 2; }
+template <int DT, int V, int NI>
+__host__ __device__ constexpr int bal_slot() { return V == 8 ? 512 * NI * (DT == ELEM_F32 ? 2 : 1) : 0; }
 
-template <bool SIG, int V, int NI>
-__global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const BalanceArgs a) {
-    extern __shared__ __align__(16) float s_sum[];       // [kBalWarps][pitch], then int32 [pitch] counts
+template <bool SIG, int DT, int V, int NI>
+__global__ void __launch_bounds__(bal_warps(NI * V) * 32, 1) balance_parts_kernel(const BalanceArgs a) {
+    constexpr int kBalWarps = bal_warps(NI * V), D = bal_depth(NI * V), kSlot = bal_slot<DT, V, NI>();
+    extern __shared__ __align__(16) float s_sum[];       // [kBalWarps][pitch], int32 [pitch] counts, rings [kBalWarps][D][kSlot]
     __shared__ int s_tokens;
     constexpr int N = NI * V;
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = a.E, k = a.k, P = a.pitch;
     int32_t* hist = reinterpret_cast<int32_t*>(s_sum + kBalWarps * P);
+    const uint8_t* rings = reinterpret_cast<const uint8_t*>(hist + P) + warp * (D * kSlot);
+    const uint32_t ring = smem_u32(rings);
     const int64_t t0 = blockIdx.x * a.per, t1 = min(t0 + a.per, a.T);
     // the first sequence that ends behind t0 (every warp finds the same)
     int s = 0;
@@ -509,15 +531,51 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const 
         float acc[N];
 #pragma unroll
         for (int c = 0; c < N; ++c) acc[c] = 0.0f;
-        int used = 0;
+        int used = 0, slot = 0;
+        auto fetch = [&](int64_t t, int to) {
+            if constexpr (V == 8) {
+                if (t < l) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int e0 = (32 * i + lane) * V;
+                        if (e0 >= E) continue;
+                        const uint8_t* src = static_cast<const uint8_t*>(a.logits) + (t * a.ld + e0) * (DT == ELEM_F32 ? 4 : 2);
+                        const uint32_t dst = ring + static_cast<uint32_t>(to * kSlot + i * (kSlot / NI) + lane * 16);
+                        cp_async16(dst, src);
+                        if (DT == ELEM_F32) cp_async16(dst + 512, src + 16);
+                    }
+                }
+                cp_async_commit();
+            }
+        };
+        int e_next = f + warp < l && lane < k ? a.idx[(f + warp) * k + lane] : -1;
+#pragma unroll
+        for (int d = 0; d < D - 1; ++d) fetch(f + warp + d * kBalWarps, d);
+#pragma unroll 1
         for (int64_t t = f + warp; t < l; t += kBalWarps) {
-            const int e = lane < k ? a.idx[t * k + lane] : -1;
+            const int e = e_next;
+            if (t + kBalWarps < l && lane < k) e_next = a.idx[(t + kBalWarps) * k + lane];
+            fetch(t + (D - 1) * kBalWarps, slot == 0 ? D - 1 : slot - 1);
+            const int from = slot;
+            slot = slot + 1 == D ? 0 : slot + 1;
             const bool kept = e >= 0 && e < E;
             if (!__any_sync(kAll, kept)) continue;
             if (kept) atomicAdd(&hist[e], 1);
             ++used;
             float v[N];
-            load_row<true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+            if constexpr (V == 8) {
+                cp_async_wait(D - 1);
+                RawVec<V> raw[NI];
+                const uint8_t* p = rings + from * kSlot + lane * 16;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    raw[i].a = ld16(p + i * (kSlot / NI));
+                    if (DT == ELEM_F32) raw[i].b = ld16(p + i * (kSlot / NI) + 512);
+                }
+                open_row<true, V, NI>(raw, E, DT, lane, v);
+            } else {
+                load_row<DT, true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+            }
             const float sum = scores<SIG>(v);
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
@@ -545,48 +603,67 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_parts_kernel(const 
     }
 }
 
-// The parts are written by the launch that this one overlaps: plain loads.
-constexpr int kSumRows = 8;              // threads that share an expert's parts
-__global__ void __launch_bounds__(128 * kSumRows) balance_sum_kernel(const BalanceArgs a) {
-    __shared__ float s_sum[kSumRows][128];
-    __shared__ int s_cnt[kSumRows][128];
-    __shared__ int s_tok[4 * kSumRows];
+// Experts that a CTA of the sums takes, a multiple of four.
+__device__ __forceinline__ int sum_cols(int E) { return ((E + kBalCtas - 1) / kBalCtas + 3) & ~3; }
+
+// The parts are written by the launch that this one overlaps: plain loads.  A warp
+// takes four experts a lane of every 32nd part and has its loads of five parts,
+// which are those of 152 blocks, in flight at once: the kernel is one latency long.
+constexpr int kSumRows = 32, kSumAhead = 5;
+__global__ void __launch_bounds__(32 * kSumRows) balance_sum_kernel(const BalanceArgs a) {
+    __shared__ __align__(16) float s_sum[kSumRows][128];
+    __shared__ __align__(16) int s_cnt[kSumRows][128];
+    __shared__ int s_tok[kSumRows];
     __shared__ float s_loss[kBalCtas];
     const int rank = blockIdx.x % kBalCtas, s = blockIdx.x / kBalCtas;
-    const int col = threadIdx.x & 127, row = threadIdx.x >> 7;
-    const int per = (a.E + kBalCtas - 1) / kBalCtas;
-    const int e = rank * per + col;
-    const bool mine = col < per && e < a.E;
+    const int col = (threadIdx.x & 31) * 4, row = threadIdx.x >> 5;
+    const int per = sum_cols(a.E);
+    const int e0 = rank * per + col;
     const int64_t stride = 2 * a.pitch + 4;
     const int64_t first = border(a.seq, s, a.S, a.T), last = border(a.seq, s + 1, a.S, a.T);
     const int64_t b0 = last > first ? first / a.per : 0, b1 = last > first ? (last - 1) / a.per + 1 : 0;
     cluster_sync_all();                // every CTA runs before its shared memory is written to
     pdl_wait();
-    float sum = 0.0f;
-    int cnt = 0, tok = 0;
-    if (mine) {
-#pragma unroll 8
-        for (int64_t b = b0 + row; b < b1; b += kSumRows) {
-            const float* part = a.part + (b + s) * stride;
-            sum += part[e];
-            cnt += reinterpret_cast<const int32_t*>(part)[a.pitch + e];
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int4 cnt = make_int4(0, 0, 0, 0);
+    int tok = 0;
+    if (col < per && e0 < a.pitch) {   // (experts between E and the pitch, a multiple of four, count for nothing)
+        for (int64_t b = b0 + row; b < b1; b += kSumRows * kSumAhead) {
+            float4 x[kSumAhead];
+            int4 c[kSumAhead];
+#pragma unroll
+            for (int u = 0; u < kSumAhead; ++u) {
+                const float* part = a.part + (b + u * kSumRows + s) * stride + e0;
+                const bool in = b + u * kSumRows < b1;
+                x[u] = in ? *reinterpret_cast<const float4*>(part) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                c[u] = in ? *reinterpret_cast<const int4*>(part + a.pitch) : make_int4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < kSumAhead; ++u) {
+                sum = make_float4(sum.x + x[u].x, sum.y + x[u].y, sum.z + x[u].z, sum.w + x[u].w);
+                cnt = make_int4(cnt.x + c[u].x, cnt.y + c[u].y, cnt.z + c[u].z, cnt.w + c[u].w);
+            }
         }
     }
     for (int64_t b = b0 + threadIdx.x; b < b1; b += blockDim.x)
         tok += reinterpret_cast<const int32_t*>(a.part + (b + s) * stride)[2 * a.pitch];
     tok = __reduce_add_sync(kAll, tok);
     if ((threadIdx.x & 31) == 0) s_tok[threadIdx.x >> 5] = tok;
-    s_sum[row][col] = sum;
-    s_cnt[row][col] = cnt;
+    *reinterpret_cast<float4*>(&s_sum[row][col]) = sum;
+    *reinterpret_cast<int4*>(&s_cnt[row][col]) = cnt;
     __syncthreads();
     if (threadIdx.x < 128) {
+        const int c = threadIdx.x, e = rank * per + c;
+        float x = 0.0f;
+        int n = 0;
 #pragma unroll
-        for (int r = 1; r < kSumRows; ++r) {
-            sum += s_sum[r][col];
-            cnt += s_cnt[r][col];
+        for (int r = 0; r < kSumRows; ++r) {
+            x += s_sum[r][c];
+            n += s_cnt[r][c];
         }
-        if (mine) a.counts[static_cast<int64_t>(s) * a.E + e] = cnt;
-        s_sum[0][col] = mine ? static_cast<float>(cnt) * sum : 0.0f;
+        const bool mine = c < per && e < a.E;
+        if (mine) a.counts[static_cast<int64_t>(s) * a.E + e] = n;
+        s_sum[0][c] = mine ? static_cast<float>(n) * x : 0.0f;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -600,7 +677,7 @@ __global__ void __launch_bounds__(128 * kSumRows) balance_sum_kernel(const Balan
     cluster_sync_all();
     if (rank == 0 && threadIdx.x == 0) {
         int n = 0;
-        for (int w = 0; w < 4 * kSumRows; ++w) n += s_tok[w];
+        for (int w = 0; w < kSumRows; ++w) n += s_tok[w];
         float x = 0.0f;
         for (int r = 0; r < kBalCtas; ++r) x += s_loss[r];
         const float m = static_cast<float>(max(n, 1));
@@ -640,8 +717,8 @@ __device__ __forceinline__ void load_counts(const int32_t* p, bool wide, float (
     for (int j = 0; j < V; ++j) c[j] = static_cast<float>(__ldg(p + j));
 }
 
-template <bool SIG, int V, int NI>
-__global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const RouterBackArgs a) {
+template <bool SIG, int DT, int V, int NI>
+__global__ void __launch_bounds__(kBackWarps * 32, 5) router_backward_kernel(const RouterBackArgs a) {
     extern __shared__ __align__(16) float s_rows[];      // [kBackWarps][pitch]
     constexpr int N = NI * V;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -660,7 +737,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
     bool low = false;                                    // sigmoid scores of negative logits only: x are the scores
     const bool shared = any && (s >= 0 || all);
     if (shared) {
-        load_row<true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, x);
+        load_row<DT, true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, x);
         if (s >= 0) {
             const bool wide = E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.counts) & 15) == 0;
             const float n = static_cast<float>(max(a.tokens[s], 1));
@@ -757,11 +834,10 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e0 = (32 * i + lane) * V;
-        if (e0 >= E) continue;
         float o[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) o[j] = 0.0f;
-        if (gates) {
+        if (gates && e0 < E) {
             if constexpr (V == 8) {
                 const float4 p = *reinterpret_cast<const float4*>(srow + e0), q = *reinterpret_cast<const float4*>(srow + e0 + 4);
                 o[0] = p.x;
@@ -790,7 +866,7 @@ __global__ void __launch_bounds__(kBackWarps * 32) router_backward_kernel(const 
                 }
             }
         }
-        store_vec(a.d_logits, t * a.ld_d + e0, a.dt, o);
+        if (e0 < E) store_vec(a.d_logits, t * a.ld_d + e0, DT >= 0 ? DT : a.dt, o);
     }
 }
 
@@ -799,41 +875,48 @@ bool rows_wide(const void* p, int64_t ld, int dt, int E) {
     return E % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elem_bytes(dt)) % 16 == 0;
 }
 
-// RUN(SIG, V, NI) with the fewest registers that hold E values a warp.
-#define MOE_ROW_FORMS_OF(RUN, SIG, wide, E)      \
-    do {                                         \
-        if (wide) {                              \
-            if ((E) <= 256) return RUN(SIG, 8, 1); \
-            if ((E) <= 512) return RUN(SIG, 8, 2); \
-            return RUN(SIG, 8, 4);               \
-        }                                        \
-        if ((E) <= 256) return RUN(SIG, 1, 8);   \
-        return RUN(SIG, 1, 32);                  \
+// RUN(SIG, DT, V, NI) with the type and the fewest registers that hold E values a warp.
+#define MOE_ROW_FORMS_OF(RUN, SIG, wide, dt, E)            \
+    do {                                                   \
+        if (!(wide)) {                                     \
+            if ((E) <= 256) return RUN(SIG, -1, 1, 8);     \
+            return RUN(SIG, -1, 1, 32);                    \
+        }                                                  \
+        if ((dt) == ELEM_F32) MOE_ROW_WIDE(RUN, SIG, ELEM_F32, E);   \
+        if ((dt) == ELEM_BF16) MOE_ROW_WIDE(RUN, SIG, ELEM_BF16, E); \
+        MOE_ROW_WIDE(RUN, SIG, ELEM_F16, E);               \
     } while (0)
-#define MOE_ROW_FORMS(RUN, sigmoid, wide, E)     \
-    if (sigmoid) MOE_ROW_FORMS_OF(RUN, true, wide, E); \
-    MOE_ROW_FORMS_OF(RUN, false, wide, E)
+#define MOE_ROW_WIDE(RUN, SIG, DT, E)                      \
+    do {                                                   \
+        if ((E) <= 256) return RUN(SIG, DT, 8, 1);         \
+        if ((E) <= 512) return RUN(SIG, DT, 8, 2);         \
+        return RUN(SIG, DT, 8, 4);                         \
+    } while (0)
+#define MOE_ROW_FORMS(RUN, sigmoid, wide, dt, E)           \
+    if (sigmoid) MOE_ROW_FORMS_OF(RUN, true, wide, dt, E); \
+    MOE_ROW_FORMS_OF(RUN, false, wide, dt, E)
 
 int64_t balance_per(int64_t T) {
     const int64_t per = (T + 151) / 152;
     return std::max<int64_t>(per, 1);
 }
 
-template <bool SIG, int V, int NI>
+template <bool SIG, int DT, int V, int NI>
 cudaError_t balance_as(const BalanceArgs& a, cudaStream_t s) {
     if (a.T > 0) {
         const unsigned blocks = static_cast<unsigned>((a.T + a.per - 1) / a.per);
-        const size_t smem = sizeof(float) * static_cast<size_t>(kBalWarps + 1) * a.pitch;
+        constexpr int kBalWarps = bal_warps(NI * V), kRings = kBalWarps * bal_depth(NI * V) * bal_slot<DT, V, NI>();
+        const size_t smem = sizeof(float) * static_cast<size_t>(kBalWarps + 1) * a.pitch + kRings;
         if (smem > 48 * 1024 - 256) {
-            const cudaError_t err = cudaFuncSetAttribute(balance_parts_kernel<SIG, V, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                         static_cast<int>(sizeof(float) * (kBalWarps + 1) * 1024));
+            const cudaError_t err = cudaFuncSetAttribute(balance_parts_kernel<SIG, DT, V, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                         static_cast<int>(sizeof(float) * (kBalWarps + 1) * 32 * V * NI) + kRings);
             if (err != cudaSuccess) return err;
         }
-        balance_parts_kernel<SIG, V, NI><<<blocks, kBalWarps * 32, smem, s>>>(a);
+        balance_parts_kernel<SIG, DT, V, NI><<<blocks, kBalWarps * 32, smem, s>>>(a);
         const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess) return err;
     }
-    return launch_ex_cluster(balance_sum_kernel, dim3(static_cast<unsigned>(a.S) * kBalCtas), dim3(128 * kSumRows), 0, s, a.T > 0, kBalCtas, a);
+    return launch_ex_cluster(balance_sum_kernel, dim3(static_cast<unsigned>(a.S) * kBalCtas), dim3(32 * kSumRows), 0, s, a.T > 0, kBalCtas, a);
 }
 
 }  // namespace
@@ -847,16 +930,16 @@ size_t balance_workspace_bytes(int64_t T, int E, int S) {
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
     const unsigned blocks = static_cast<unsigned>((a.T + kSelectWarps - 1) / kSelectWarps);
-#define MOE_RUN(SIG, V, NI) (select_kernel<V, NI><<<blocks, kSelectWarps * 32, 0, s>>>(a), cudaGetLastError())
-    MOE_ROW_FORMS_OF(MOE_RUN, , rows_wide(a.logits, a.ld, a.dt, a.E) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0, a.E);
+#define MOE_RUN(SIG, DT, V, NI) (select_kernel<DT, V, NI><<<blocks, kSelectWarps * 32, 7, s>>>(a), cudaGetLastError())
+    MOE_ROW_FORMS_OF(MOE_RUN, , rows_wide(a.logits, a.ld, a.dt, a.E) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0, a.dt, a.E);
 #undef MOE_RUN
 }
 
 cudaError_t launch_balance(BalanceArgs a, cudaStream_t s) {
     a.per = balance_per(a.T);
     a.pitch = (a.E + 3) & ~3;
-#define MOE_RUN(SIG, V, NI) balance_as<SIG, V, NI>(a, s)
-    MOE_ROW_FORMS(MOE_RUN, a.sigmoid, rows_wide(a.logits, a.ld, a.dt, a.E), a.E);
+#define MOE_RUN(SIG, DT, V, NI) balance_as<SIG, DT, V, NI>(a, s)
+    MOE_ROW_FORMS(MOE_RUN, a.sigmoid, rows_wide(a.logits, a.ld, a.dt, a.E), a.dt, a.E);
 #undef MOE_RUN
 }
 
@@ -865,8 +948,8 @@ cudaError_t launch_router_backward(RouterBackArgs a, cudaStream_t s) {
     a.pitch = (a.E + 3) & ~3;
     const unsigned blocks = static_cast<unsigned>((a.T + kBackWarps - 1) / kBackWarps);
     const size_t smem = a.d_gates ? sizeof(float) * kBackWarps * static_cast<size_t>(a.pitch) : 0;
-#define MOE_RUN(SIG, V, NI) (router_backward_kernel<SIG, V, NI><<<blocks, kBackWarps * 32, smem, s>>>(a), cudaGetLastError())
-    MOE_ROW_FORMS(MOE_RUN, a.sigmoid, rows_wide(a.logits, a.ld, a.dt, a.E) && rows_wide(a.d_logits, a.ld_d, a.dt, a.E), a.E);
+#define MOE_RUN(SIG, DT, V, NI) (router_backward_kernel<SIG, DT, V, NI><<<blocks, kBackWarps * 32, smem, s>>>(a), cudaGetLastError())
+    MOE_ROW_FORMS(MOE_RUN, a.sigmoid, rows_wide(a.logits, a.ld, a.dt, a.E) && rows_wide(a.d_logits, a.ld_d, a.dt, a.E), a.dt, a.E);
 #undef MOE_RUN
 }
 
