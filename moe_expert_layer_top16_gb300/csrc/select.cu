@@ -86,6 +86,18 @@ __device__ __forceinline__ float fast_rcp(float x) {
     return r;
 }
 
+// 1 / d of four values from 1 to 2^30 by one reciprocal: the special functions
+// take four of a warp's lanes a clock, and with two for each logit they were what
+// a row took longest for.  Off by five roundings at most.
+__device__ __forceinline__ void rcp4(const float (&d)[4], float (&q)[4]) {
+    const float a = d[0] * d[1], b = d[2] * d[3], r = fast_rcp(a * b);
+    const float ra = r * b, rb = r * a;
+    q[0] = ra * d[1];
+    q[1] = ra * d[0];
+    q[2] = rb * d[3];
+    q[3] = rb * d[2];
+}
+
 // ------------------------------------------------------------------ scores
 // Scores of values v[N] as multiples of a common factor that keeps them from
 // underflow, and their sum over the warp.  Softmax: e^(v - max).  Sigmoid:
@@ -109,10 +121,19 @@ __device__ __forceinline__ float scores(float (&v)[N]) {
         }
     } else if (top >= 0.0f) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float u = fast_exp(-fabsf(v[i]));
-            v[i] = (v[i] >= 0.0f ? 1.0f : u) * fast_rcp(1.0f + u);
-            sum += v[i];
+        for (int i = 0; i < N; i += 4) {
+            float u[4], d[4], q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u[j] = fast_exp(-fabsf(v[i + j]));
+                d[j] = 1.0f + u[j];
+            }
+            rcp4(d, q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[i + j] = (v[i + j] >= 0.0f ? 1.0f : u[j]) * q[j];
+                sum += v[i + j];
+            }
         }
     } else {
 #pragma unroll
@@ -149,15 +170,17 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 //
 // Keys with a bias are defined in 64 bits, whose exponentials would take some
 // ten times as long as the logits' way from memory.  They are estimated in 32:
-// |estimate - key| <= 1e-6 + 2^-22 |estimate| (the exponential is off by 2 + |l|
-// units in the last place, which sigmoid(l) (1 - sigmoid(l)) turns into less
-// than 2^-22 at most, sum and quotient add 2^-22, the sum with b its own
-// rounding), candidates are what reaches the bound less twice that, and only
-// where two neighbours in the order are nearer than that and not equal in logit
-// and bias are the candidates ranked by keys of 64 bits.
+// |estimate - key| <= 4e-7 + 2^-24 |estimate|.  (With u = e^-l and s = 1 / (1 + u),
+// u is off by (2^-22 + 1.3 |l| 2^-24) u, of which s (1 - s) <= 1/4 and |l| s (1 - s)
+// <= 0.23 leave 1.3 2^-24; sum, reciprocal and the products of rcp4 add 2^-22 and
+// the u kept below 2^30 1e-9, together less than 4e-7; the last term is the sum
+// with b.)  Candidates are what reaches the bound less twice that, and only where
+// two neighbours in the order are nearer than that and not equal in logit and
+// bias are the candidates ranked by keys of 64 bits: a row in some hundreds, which
+// takes 10 us longer than the others.
 constexpr int kCand = 64;
 constexpr int kSelectWarps = 4;
-constexpr float kNear = 4e-6f, kNearRel = 0x1p-20f;
+constexpr float kNear = 8e-7f, kNearRel = 0x1p-22f;
 
 struct Candidate {
     float key, l, b;
@@ -165,8 +188,16 @@ struct Candidate {
 };
 
 __device__ __forceinline__ float key32(float l, float b) {
-    const float s = fast_rcp(1.0f + fast_exp(-l)) + b;
-    return l == -INFINITY ? -INFINITY : s;
+    const float s = fast_rcp(1.0f + fminf(fast_exp(-l), 0x1p30f)) + b;
+    return l > -INFINITY ? s : -INFINITY;
+}
+__device__ __forceinline__ void keys32(float* l, const float* b) {
+    float d[4], q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = 1.0f + fminf(fast_exp(-l[j]), 0x1p30f);
+    rcp4(d, q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) l[j] = l[j] > -INFINITY ? q[j] + b[j] : -INFINITY;
 }
 __device__ __forceinline__ double key64(float l, float b) {
     return 1.0 / (1.0 + exp(-static_cast<double>(l))) + static_cast<double>(b);
@@ -271,15 +302,22 @@ __global__ void __launch_bounds__(kSelectWarps * 32, 7) select_kernel(const Sele
     float v[N];
     load_row<DT, false, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
     if (a.bias) {
+        constexpr int W = V == 8 ? 8 : 4;                // keys at a time
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e0 = (32 * i + lane) * V;
-            float b[V];
+        for (int i = 0; i < N; i += W) {
+            float b[W];
 #pragma unroll
-            for (int j = 0; j < V; ++j) b[j] = 0.0f;
-            if (e0 < E) raw_to_f32(load_raw<V>(a.bias, e0, ELEM_F32), ELEM_F32, b);
+            for (int j = 0; j < W; j += V) {
+                const int e0 = (32 * ((i + j) / V) + lane) * V;
+                float f[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[i * V + j] = key32(v[i * V + j], b[j]);
+                for (int c = 0; c < V; ++c) f[c] = 0.0f;
+                if (e0 < E) raw_to_f32(load_raw<V>(a.bias, e0, ELEM_F32), ELEM_F32, f);
+#pragma unroll
+                for (int c = 0; c < V; ++c) b[j + c] = f[c];
+            }
+#pragma unroll
+            for (int j = 0; j < W; j += 4) keys32(v + i + j, b + j);
         }
     }
     // (a key that is not a number is passed over by maxima and reaches no bound)
@@ -329,16 +367,22 @@ __global__ void __launch_bounds__(kSelectWarps * 32, 7) select_kernel(const Sele
         __syncwarp();
     }
     if (n <= 32) {
-        e = lane < n ? cand[lane].e : 0x7fffffff;
-        float key = -INFINITY;
-        if (lane < n) key = a.bias ? key32(logit(e), open_bias(a.bias[e])) : logit(e);
-        sort_keys(key, e, lane);
-        float bias = 0.0f;
+        float key = -INFINITY, bias = 0.0f;
+        int at = 0x7fffffff;             // the expert and the lane that has its logit and bias
         if (lane < n) {
-            l[0] = logit(e);
-            if (a.bias) bias = open_bias(a.bias[e]);
+            e = cand[lane].e;
+            l[0] = key = logit(e);
+            if (a.bias) {
+                bias = open_bias(a.bias[e]);
+                key = key32(key, bias);
+            }
+            at = e * 32 + lane;
         }
+        sort_keys(key, at, lane);
+        e = at >> 5;
+        l[0] = __shfl_sync(kAll, l[0], at & 31);
         if (a.bias) {
+            bias = __shfl_sync(kAll, bias, at & 31);
             const float key2 = __shfl_down_sync(kAll, key, 1), l2 = __shfl_down_sync(kAll, l[0], 1), b2 = __shfl_down_sync(kAll, bias, 1);
             const bool near = lane < k && lane + 1 < n && key - key2 <= kNear + kNearRel * fabsf(key) && !(l2 == l[0] && b2 == bias);
             if (__any_sync(kAll, near)) {
@@ -693,7 +737,7 @@ __global__ void __launch_bounds__(32 * kSumRows) balance_sum_kernel(const Balanc
 // normalised, g_j s_j r_j, or for the softmax over all p_e ([e won] g_e - sum g p).
 // A lane holds slot j = lane; the slots' values meet their experts' lanes in a row
 // of shared memory.  One exponential a logit: with u = e^-|l|, sigmoid(l) is {1, u} /
-// (1 + u) and sigmoid(l) (1 - sigmoid(l)) = u / (1 + u)^2; u is kept for the second pass.
+// (1 + u) and sigmoid(l) (1 - sigmoid(l)) = u / (1 + u)^2, which is kept for the second pass.
 constexpr int kBackWarps = 4;
 
 // Eight (or one) counts as floats.
@@ -726,18 +770,25 @@ __global__ void __launch_bounds__(kBackWarps * 32, 5) router_backward_kernel(con
     if (t >= a.T) return;
     const int E = a.E, k = a.k;
     float* srow = s_rows + warp * a.pitch;
+    const bool all = !SIG && !a.normalize && a.d_gates;          // gates by the softmax over all
+    // (all that has no need of another load's value is asked for first)
+    RawVec<V> raw[NI];
+    if (a.d_loss || all) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e0 = (32 * i + lane) * V;
+            if (e0 < E) raw[i] = load_raw<V>(a.logits, t * a.ld + e0, DT >= 0 ? DT : a.dt);
+        }
+    }
     int e = lane < k ? a.idx[t * k + lane] : -1;
+    int s = a.d_loss ? sequence_of(a.seq, a.S, a.T, t, lane) : -1;
     if (e < 0 || e >= E) e = -1;
     const bool any = __any_sync(kAll, e >= 0);
-    const int s = a.d_loss && any ? sequence_of(a.seq, a.S, a.T, t, lane) : -1;
-    const bool all = !SIG && !a.normalize && a.d_gates;          // gates by the softmax over all
-    // x: scores as multiples of p; with sigmoid scores u, negative where the logit is
-    float x[N], ac[N];                                   // ac: a_e
+    if (!any) s = -1;
+    float x[N], ac[N];                                   // x: p r as multiples of 1 / inv; ac: a_e
     float inv = 0.0f, top = -INFINITY, inner = 0.0f;
-    bool low = false;                                    // sigmoid scores of negative logits only: x are the scores
     const bool shared = any && (s >= 0 || all);
     if (shared) {
-        load_row<DT, true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, x);
         if (s >= 0) {
             const bool wide = E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.counts) & 15) == 0;
             const float n = static_cast<float>(max(a.tokens[s], 1));
@@ -757,10 +808,10 @@ __global__ void __launch_bounds__(kBackWarps * 32, 5) router_backward_kernel(con
 #pragma unroll
             for (int c = 0; c < N; ++c) ac[c] = 0.0f;
         }
+        open_row<true, V, NI>(raw, E, DT >= 0 ? DT : a.dt, lane, x);
 #pragma unroll
         for (int c = 0; c < N; ++c) top = fmaxf(top, x[c]);
         top = warp_max(top);
-        low = SIG && top < 0.0f;
         float sum = 0.0f;
         if (top == -INFINITY) {
 #pragma unroll
@@ -772,13 +823,23 @@ __global__ void __launch_bounds__(kBackWarps * 32, 5) router_backward_kernel(con
                 sum += x[c];
                 inner = fmaf(x[c], ac[c], inner);
             }
-        } else if (!low) {
+        } else if (top >= 0.0f) {
 #pragma unroll
-            for (int c = 0; c < N; ++c) {
-                const float u = fast_exp(-fabsf(x[c])), y = (x[c] >= 0.0f ? 1.0f : u) * fast_rcp(1.0f + u);
-                x[c] = u;                                // s (1 - s) is the same for l and -l
-                sum += y;
-                inner = fmaf(y, ac[c], inner);
+            for (int c = 0; c < N; c += 4) {
+                float u[4], d[4], q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[j] = fast_exp(-fabsf(x[c + j]));
+                    d[j] = 1.0f + u[j];
+                }
+                rcp4(d, q);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float z = u[j] * q[j], y = x[c + j] >= 0.0f ? q[j] : z;
+                    x[c + j] = z * q[j];
+                    sum += y;
+                    inner = fmaf(y, ac[c + j], inner);
+                }
             }
         } else {
 #pragma unroll
@@ -857,13 +918,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, 5) router_backward_kernel(con
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = i * V + j;
-                const float d = inv * (ac[c] - inner - shift);
-                if (SIG && !low) {
-                    const float q = fast_rcp(1.0f + x[c]);
-                    o[j] = fmaf(x[c] * q * q, d, o[j]);  // s (1 - s) = u / (1 + u)^2
-                } else {
-                    o[j] = fmaf(x[c], d, o[j]);
-                }
+                o[j] = fmaf(x[c] * inv, ac[c] - (inner + shift), o[j]);
             }
         }
         if (e0 < E) store_vec(a.d_logits, t * a.ld_d + e0, DT >= 0 ? DT : a.dt, o);
