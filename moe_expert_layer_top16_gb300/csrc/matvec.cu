@@ -45,6 +45,7 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRows = 16;                // rows of a team's tile
+constexpr int D = 2;                     // units in a warp's ring
 constexpr int kUK = 256;                 // k of a unit
 constexpr int kUnitGroups = kUK / 32;
 constexpr int kMvMaxThreads = 512;
@@ -98,8 +99,8 @@ __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&h)[4], uint32_
     }
 }
 
-// Kinds of scale: E8M0 (with E2M1 codes), two bytes or four (with integers).
-enum ScaleKind : int { SCALE_E8M0 = 0, SCALE_16 = 1, SCALE_32 = 2 };
+// Kinds of scale: E8M0 (with E2M1 codes), fp16, bf16 or fp32 (with integers).
+enum ScaleKind : int { SCALE_E8M0 = 0, SCALE_F16 = 1, SCALE_BF16 = 2, SCALE_F32 = 3 };
 
 template <int N>
 __device__ __forceinline__ void ld_words(uint32_t (&b)[N], const uint8_t* p) {
@@ -126,17 +127,18 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" 
 
 // Two scales as they lie in a word.
 template <int SK>
-__device__ __forceinline__ float2 two_scales(uint32_t v, bool bf16) {
+__device__ __forceinline__ float2 two_scales(uint32_t v) {
     if constexpr (SK == SCALE_E8M0) {
         uint32_t r;                      // 2^-127 for code 0, NaN for 255
         asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
-        return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
-    } else {
-        if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+        v = r;
+    }
+    if constexpr (SK == SCALE_F16) {
         __half2 h;
         memcpy(&h, &v, 4);
         return __half22float2(h);
     }
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 // A row's scales of a unit, W words as they lie in memory: `bytes` of them, in pieces of 16, 8 or 4 bytes.
 __device__ __forceinline__ void ld_global(uint32_t& a, const uint8_t* p) { asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(a) : "l"(p)); }
@@ -167,37 +169,43 @@ template <int SK, int W>
 __device__ __forceinline__ void load_row_scales_one(uint32_t (&w)[W], const uint8_t* p, int n, int left) {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0;
-    constexpr int size = SK == SCALE_E8M0 ? 1 : SK == SCALE_16 ? 2 : 4;
+    constexpr int size = SK == SCALE_E8M0 ? 1 : SK == SCALE_F32 ? 4 : 2;
 #pragma unroll
     for (int i = 0; i < kUnitGroups; ++i) {
         if (i >= n || i * size >= left) break;
         if constexpr (SK == SCALE_E8M0) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
-        if constexpr (SK == SCALE_16) w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
-        if constexpr (SK == SCALE_32) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        if constexpr (SK == SCALE_F16 || SK == SCALE_BF16) w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
+        if constexpr (SK == SCALE_F32) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    }
+}
+// Scales as loaded, each for 2^shift groups of 32, as one for each of the unit's groups.
+template <int SK, int W>
+__device__ __forceinline__ void spread_scales(uint32_t (&to)[W], const uint32_t (&w)[W], int shift) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) to[i] = w[i];
+    if constexpr (SK == SCALE_F32) {
+        if (shift > 0)
+#pragma unroll
+            for (int i = 0; i < W; ++i) to[i] = shift == 1 ? w[i / 2] : w[i / 4];
+    } else if constexpr (SK != SCALE_E8M0) {
+        if (shift > 0)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const int n = shift == 1 ? i : i / 2;
+                to[i] = __byte_perm(shift == 1 ? w[i / 2] : w[0], 0, n & 1 ? 0x3232 : 0x1010);
+            }
     }
 }
 // The scales of groups 2 q and 2 q + 1, or with `odd` (q even then) of the two behind them.
 template <int SK, int W>
-__device__ __forceinline__ void pair_of_scales(const uint32_t (&w)[W], int q, int odd, int shift, bool bf16, float (&s)[2]) {
-    if constexpr (SK == SCALE_E8M0) {
-        const float2 v = two_scales<SK>(w[q / 2] >> (16 * (q % 2) + 16 * odd), false);
+__device__ __forceinline__ void pair_of_scales(const uint32_t (&w)[W], int q, int odd, float (&s)[2]) {
+    if constexpr (SK == SCALE_F32) {
+        s[0] = __uint_as_float(odd ? w[(2 * q + 2) % W] : w[2 * q]);
+        s[1] = __uint_as_float(odd ? w[(2 * q + 3) % W] : w[2 * q + 1]);
+    } else {
+        const float2 v = two_scales<SK>(SK == SCALE_E8M0 ? w[q / 2] >> (16 * (q % 2) + 16 * odd) : odd ? w[(q + 1) % W] : w[q]);
         s[0] = v.x;
         s[1] = v.y;
-    } else if constexpr (SK == SCALE_16) {
-        if (shift == 0) {
-            const float2 v = two_scales<SK>(odd ? w[(q + 1) % W] : w[q], bf16);
-            s[0] = v.x;
-            s[1] = v.y;
-        } else {
-            s[0] = s[1] = two_scales<SK>(shift == 1 ? w[q / 2] >> (16 * (q % 2) + 16 * odd) : w[0] >> (16 * (q / 2)), bf16).x;
-        }
-    } else {
-        if (shift == 0) {
-            s[0] = __uint_as_float(odd ? w[(2 * q + 2) % W] : w[2 * q]);
-            s[1] = __uint_as_float(odd ? w[(2 * q + 3) % W] : w[2 * q + 1]);
-        } else {
-            s[0] = s[1] = __uint_as_float(shift == 1 ? (odd ? w[(q + 1) % W] : w[q]) : w[q / 2]);
-        }
     }
 }
 
@@ -223,14 +231,14 @@ __device__ __forceinline__ int row_of(int g) { return (g >> 2) | (g & 2) | ((g &
 // rings' codes, [warp][slot][matrix]; x as fp16 [unit][half][part of GP groups][word of 8][vector][lane of the row], 16
 // bytes each; as many zero bytes as a unit has (read by the lanes off the diagonal); factors of the groups in fp32; the
 // warps' sums [team][matrix][warp][vector][row].
-template <int SK, int GP, int NT, bool DUAL, int D>
+template <int SK, int GP, int NT, bool DUAL>
 struct Layout {
     static constexpr int VT = 8 / GP;            // vectors of a tile
     static constexpr int VS = NT * VT;           // vectors there is room for
     static constexpr int NM = DUAL ? 2 : 1;
     static constexpr int kUnitX = kUK * VS * 2, kUnitF = VS * kUnitGroups * 4;
     static constexpr int kZero = GP == 1 ? 0 : kUnitX;
-    static constexpr int W = SK == SCALE_E8M0 ? 2 : SK == SCALE_16 ? 4 : 8;             // words of a row's scales in a unit
+    static constexpr int W = SK == SCALE_E8M0 ? 2 : SK == SCALE_E8M0 ? 2 : SK == SCALE_F32 ? 8 : 4;            // words of a row's scales in a unit
     static constexpr int kWarp = NM * kRows * VS * 4 + D * NM * kCodeBytes;             // of a warp: sums and ring
 };
 
@@ -244,9 +252,9 @@ __device__ __noinline__ void matvec_drain(uint64_t* bar, uint32_t parity, int* s
         }
 }
 
-template <int SK, int GP, int NT, bool DUAL, int D>
+template <int SK, int GP, int NT, bool DUAL>
 __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_constant__ MatvecArgs a) {
-    using L = Layout<SK, GP, NT, DUAL, D>;
+    using L = Layout<SK, GP, NT, DUAL>;
     constexpr int VT = L::VT, VS = L::VS, NM = L::NM, PARTS = 4 / GP;
     constexpr int AC = GP == 1 ? 4 : 2;  // sums of a lane and tile: two rows, and two vectors where a column is one
     extern __shared__ uint8_t smem_raw[];
@@ -403,7 +411,6 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
     };
 
     // this lane's places
-    const bool bf16 = a.dt_scale == ELEM_BF16;
     // B fragments: the lane's column is that of vector vb in group gb of a part; values in the rows of that group's
     // lanes, zeros elsewhere
     const int vb = g / GP;
@@ -527,8 +534,8 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
             for (int m = 0; m < NM; ++m) {
                 if constexpr (GP == 1) {
                     float s[2], r[2];
-                    pair_of_scales<SK>(now[m][0], pair, 0, a.shift, bf16, s);
-                    pair_of_scales<SK>(now[m][1], pair, 0, a.shift, bf16, r);
+                    pair_of_scales<SK>(now[m][0], pair, 0, s);
+                    pair_of_scales<SK>(now[m][1], pair, 0, r);
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -543,8 +550,8 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float s[2], r[2];
-                        pair_of_scales<SK>(now[m][0], (2 * pair + h) * GP / 2, odd, a.shift, bf16, s);
-                        pair_of_scales<SK>(now[m][1], (2 * pair + h) * GP / 2, odd, a.shift, bf16, r);
+                        pair_of_scales<SK>(now[m][0], (2 * pair + h) * GP / 2, odd, s);
+                        pair_of_scales<SK>(now[m][1], (2 * pair + h) * GP / 2, odd, r);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const float2 f = *reinterpret_cast<const float2*>(f_at + n * VT * kUnitGroups + gi + h * GP);
@@ -603,11 +610,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
                     if (i >= run || !live || !ok) break;
 #pragma unroll
                     for (int m = 0; m < NM; ++m)
-#pragma unroll
-                        for (int w = 0; w < L::W; ++w) {
-                            now[m][0][w] = next[m][0][w];
-                            now[m][1][w] = next[m][1][w];
-                        }
+                        for (int r = 0; r < 2; ++r) spread_scales<SK>(now[m][r], next[m][r], a.shift);
                     if (i + 1 < run) {
                         if (segs > 1 && s_left <= 0) aim_scales(tile, first + i + 1);
                         load_scales();
@@ -697,9 +700,9 @@ int ilog2(int n) { return n > 1 ? 1 + ilog2(n / 2) : 0; }
 // Warps of a block and of a team, and blocks of a set.  16 warps an SM, in one block or, where both fit, in two.  A
 // block's time, in halves of a unit: its share of x, and rounds of tiles, each as long as a warp's run and its start and
 // end; the split that makes the waves of blocks shortest.
-template <int SK, int GP, int NT, bool DUAL, int D>
+template <int SK, int GP, int NT, bool DUAL>
 cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
-    using L = Layout<SK, GP, NT, DUAL, D>;
+    using L = Layout<SK, GP, NT, DUAL>;
     const int tiles = a.tiles;
     const int64_t units = static_cast<int64_t>(a.weights ? a.k : 1) * a.cps;
     const size_t unit_bytes = L::kUnitX + L::kUnitF;
@@ -725,10 +728,10 @@ cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
     a.cap = static_cast<int>(std::min<int64_t>(units, (kMvSmem - L::kZero - warps * L::kWarp) / unit_bytes));
     const size_t smem = 1024 + a.cap * unit_bytes + L::kZero + warps * L::kWarp;
     // (also gives a host thread its context, which the tensor maps' encoder, a driver call, wants)
-    const cudaError_t err = cudaFuncSetAttribute(matvec_kernel<SK, GP, NT, DUAL, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMvSmem + 1024);
+    const cudaError_t err = cudaFuncSetAttribute(matvec_kernel<SK, GP, NT, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMvSmem + 1024);
     if (err != cudaSuccess) return err;
     if (!a.make_maps(a)) return cudaErrorInvalidValue;
-    matvec_kernel<SK, GP, NT, DUAL, D><<<static_cast<unsigned>(a.sets * a.blocks), warps * 32, smem, s>>>(a);
+    matvec_kernel<SK, GP, NT, DUAL><<<static_cast<unsigned>(a.sets * a.blocks), warps * 32, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -737,10 +740,10 @@ cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
 template <int SK, bool DUAL>
 cudaError_t matvec_of(const MatvecArgs& a, cudaStream_t s) {
     const int vv = a.nv * a.parts;
-    if (vv <= 2) return matvec_as<SK, 4, 1, DUAL, DUAL ? 2 : 4>(a, s);
-    if (vv <= 4) return matvec_as<SK, 2, 1, DUAL, DUAL ? 2 : 4>(a, s);
-    if (vv <= 8) return matvec_as<SK, 1, 1, DUAL, 2>(a, s);
-    return matvec_as<SK, 1, 2, DUAL, 2>(a, s);
+    if (vv <= 2) return matvec_as<SK, 4, 1, DUAL>(a, s);
+    if (vv <= 4) return matvec_as<SK, 2, 1, DUAL>(a, s);
+    if (vv <= 8) return matvec_as<SK, 1, 1, DUAL>(a, s);
+    return matvec_as<SK, 1, 2, DUAL>(a, s);
 }
 
 }  // namespace
@@ -767,8 +770,9 @@ cudaError_t launch_matvec(MatvecArgs a, cudaStream_t s) {
     a.cps = (a.K + kUK - 1) / kUK;
     a.tiles = static_cast<int>((static_cast<int64_t>(a.M) + kRows - 1) / kRows);
     if (a.format == 0) return a.up_codes ? matvec_of<SCALE_E8M0, true>(a, s) : matvec_of<SCALE_E8M0, false>(a, s);
-    if (a.dt_scale == ELEM_F32) return a.up_codes ? matvec_of<SCALE_32, true>(a, s) : matvec_of<SCALE_32, false>(a, s);
-    return a.up_codes ? matvec_of<SCALE_16, true>(a, s) : matvec_of<SCALE_16, false>(a, s);
+    if (a.dt_scale == ELEM_F32) return a.up_codes ? matvec_of<SCALE_F32, true>(a, s) : matvec_of<SCALE_F32, false>(a, s);
+    if (a.dt_scale == ELEM_BF16) return a.up_codes ? matvec_of<SCALE_BF16, true>(a, s) : matvec_of<SCALE_BF16, false>(a, s);
+    return a.up_codes ? matvec_of<SCALE_F16, true>(a, s) : matvec_of<SCALE_F16, false>(a, s);
 }
 
 }  // namespace moe

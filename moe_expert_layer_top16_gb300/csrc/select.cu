@@ -745,7 +745,7 @@ template <int V>
 __device__ __forceinline__ void load_counts(const int32_t* p, bool wide, float (&c)[V]) {
     if constexpr (V == 8) {
         if (wide) {
-            const int4 a = __ldg(reinterpret_cast<const int4*>(p)), b = __ldg(reinterpret_cast<const int4*>(p) + 1);
+            const int4 a = *reinterpret_cast<const int4*>(p), b = *(reinterpret_cast<const int4*>(p) + 1);
             c[0] = static_cast<float>(a.x);
             c[1] = static_cast<float>(a.y);
             c[2] = static_cast<float>(a.z);
@@ -758,7 +758,7 @@ __device__ __forceinline__ void load_counts(const int32_t* p, bool wide, float (
         }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) c[j] = static_cast<float>(__ldg(p + j));
+    for (int j = 0; j < V; ++j) c[j] = static_cast<float>(p[j]);
 }
 
 template <bool SIG, int DT, int V, int NI>
@@ -985,7 +985,7 @@ size_t balance_workspace_bytes(int64_t T, int E, int S) {
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     if (a.T == 0) return cudaSuccess;
     const unsigned blocks = static_cast<unsigned>((a.T + kSelectWarps - 1) / kSelectWarps);
-#define MOE_RUN(SIG, DT, V, NI) (select_kernel<DT, V, NI><<<blocks, kSelectWarps * 32, 7, s>>>(a), cudaGetLastError())
+#define MOE_RUN(SIG, DT, V, NI) (select_kernel<DT, V, NI><<<blocks, kSelectWarps * 32, 0, s>>>(a), cudaGetLastError())
     MOE_ROW_FORMS_OF(MOE_RUN, , rows_wide(a.logits, a.ld, a.dt, a.E) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0, a.dt, a.E);
 #undef MOE_RUN
 }
