@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
     constexpr int VT = L::VT, VS = L::VS, NM = L::NM, PARTS = 4 / GP;
     constexpr int AC = GP == 1 ? 4 : 2;  // sums of a lane and tile: two rows, and two vectors where a column is one
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* const sm = smem_raw + (-smem_u32(smem_raw) & 1023u);        // (by an offset: it stays known as shared memory)
     __shared__ int s_expert[kMaxSegs], s_row[kMaxSegs], s_segs, s_abort;
     __shared__ __align__(8) uint64_t s_full[kMvMaxThreads / 32][D];
     __shared__ float s_gate[kMaxSegs];
