@@ -218,7 +218,10 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
 }
 
 // A unit is 256 k of a team's 16 rows: 128 bytes of a row.  Each warp has a ring of D units for itself: the codes come
-// by TMA, a box of 16 rows of 128 bytes in the 128-byte swizzle (piece i of 16 bytes of row r lies at piece i ^ (r % 8)),
+// by TMA, a box of 16 rows of 128 bytes in the 128-byte swizzle (piece i of 16 bytes of row r lies at piece i ^ (r % 8)).
+// Two units in the ring do as well as more in long runs and better at the start, where x comes behind them: 8,192 rows of
+// 7,168 and one token 14.6 us, with four 15.8.  (Tiles of 32 rows, with x read once for two MMAs, are no faster: shared
+// memory is at a fifth of its rate, and 256 tiles leave 24 of 152 SMs idle.)
 // The scales go to registers, a unit ahead: four lanes read the same 8 bytes of an MXFP4 row.  (By cp.async or by TMA to
 // shared memory and from there they cost more instructions than all else but the conversion of the codes: 155,648 rows
 // of 7,168 120 us, without scales 100.)  The MMA's row g is row `row_of(g)` of the tile and g + 8 eight behind it: with the three
@@ -238,7 +241,7 @@ struct Layout {
     static constexpr int NM = DUAL ? 2 : 1;
     static constexpr int kUnitX = kUK * VS * 2, kUnitF = VS * kUnitGroups * 4;
     static constexpr int kZero = GP == 1 ? 0 : kUnitX;
-    static constexpr int W = SK == SCALE_E8M0 ? 2 : SK == SCALE_E8M0 ? 2 : SK == SCALE_F32 ? 8 : 4;            // words of a row's scales in a unit
+    static constexpr int W = SK == SCALE_E8M0 ? 2 : SK == SCALE_F32 ? 8 : 4;     // words of a row's scales in a unit
     static constexpr int kWarp = NM * kRows * VS * 4 + D * NM * kCodeBytes;             // of a warp: sums and ring
 };
 
@@ -698,8 +701,10 @@ __global__ void __launch_bounds__(kMvMaxThreads) matvec_kernel(const __grid_cons
 int ilog2(int n) { return n > 1 ? 1 + ilog2(n / 2) : 0; }
 
 // Warps of a block and of a team, and blocks of a set.  16 warps an SM, in one block or, where both fit, in two.  A
-// block's time, in halves of a unit: its share of x, and rounds of tiles, each as long as a warp's run and its start and
-// end; the split that makes the waves of blocks shortest.
+// block's time, in halves of a unit (0.35 us): its start, some 6 us of first instructions and first loads; its share of
+// x; rounds of tiles, each as long as a warp's run and an end.  Taken is what makes the waves of blocks shortest.  (With
+// no start counted and half the waves, four tokens of 16 slots, down, took 25 us for 12; twelve of 16 slots kept by
+// nobody, or all kept, within 2%.)
 template <int SK, int GP, int NT, bool DUAL>
 cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
     using L = Layout<SK, GP, NT, DUAL>;
@@ -710,13 +715,13 @@ cudaError_t matvec_as(MatvecArgs a, cudaStream_t s) {
     int64_t best = INT64_MAX;
     int warps = 16;
     for (int w = two ? 8 : 16; w <= 16; w *= 2) {
-        // a set of its own for each slot: some four waves of blocks, as many of them may have nothing to do
-        const int64_t resident = 152 * 16 / w, most = std::max<int64_t>(1, a.idx ? (4 * resident + a.sets - 1) / a.sets : resident / a.sets);
+        // a set of its own for each slot: up to eight waves of blocks, as many of them may have nothing to do
+        const int64_t resident = 152 * 16 / w, most = std::max<int64_t>(1, a.idx ? (8 * resident + a.sets - 1) / a.sets : resident / a.sets);
         for (int kw = 1; kw <= w; kw *= 2) {
             const int teams = w / kw;
             const int64_t blocks = std::min<int64_t>((tiles + teams - 1) / teams, most);
             const int64_t rounds = (tiles + blocks * teams - 1) / (blocks * teams), waves = (a.sets * blocks + resident - 1) / resident;
-            const int64_t cost = waves * (units * a.nv / w + rounds * (2 * ((units + kw - 1) / kw) + 1));
+            const int64_t cost = waves * (18 + units * a.nv / w + rounds * (2 * ((units + kw - 1) / kw) + 1));
             if (cost < best) {
                 best = cost;
                 warps = w;
