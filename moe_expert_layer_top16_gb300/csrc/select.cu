@@ -88,7 +88,7 @@ __device__ __forceinline__ float fast_rcp(float x) {
 
 // 1 / d of four values from 1 to 2^30 by one reciprocal: the special functions
 // take four of a warp's lanes a clock, and with two for each logit they were what
-// a row took longest for.  Off by five roundings at most.
+// a row took longest for.  Off by 6 x 2^-24 at most.
 __device__ __forceinline__ void rcp4(const float (&d)[4], float (&q)[4]) {
     const float a = d[0] * d[1], b = d[2] * d[3], r = fast_rcp(a * b);
     const float ra = r * b, rb = r * a;
@@ -170,17 +170,17 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 //
 // Keys with a bias are defined in 64 bits, whose exponentials would take some
 // ten times as long as the logits' way from memory.  They are estimated in 32:
-// |estimate - key| <= 4e-7 + 2^-24 |estimate|.  (With u = e^-l and s = 1 / (1 + u),
+// |estimate - key| <= 5e-7 + 2^-24 |estimate|.  (With u = e^-l and s = 1 / (1 + u),
 // u is off by (2^-22 + 1.3 |l| 2^-24) u, of which s (1 - s) <= 1/4 and |l| s (1 - s)
-// <= 0.23 leave 1.3 2^-24; sum, reciprocal and the products of rcp4 add 2^-22 and
-// the u kept below 2^30 1e-9, together less than 4e-7; the last term is the sum
-// with b.)  Candidates are what reaches the bound less twice that, and only where
-// two neighbours in the order are nearer than that and not equal in logit and
-// bias are the candidates ranked by keys of 64 bits: a row in some hundreds, which
-// takes 10 us longer than the others.
+// <= 0.23 leave 1.3 x 2^-24; the sum 1 + u and rcp4 add 7 x 2^-24, the u kept below
+// 2^30 1e-9, together less than 5e-7; the last term is the sum with b.)  Candidates
+// are what reaches the bound less twice that, and only where two neighbours in the
+// order are nearer than that and not equal in logit and bias are the candidates
+// ranked by keys of 64 bits: a row in some hundreds, at which a launch's last rows
+// wait longest.  8,192 rows of 896, k = 16: 22 us with a bias, 16 without.
 constexpr int kCand = 64;
 constexpr int kSelectWarps = 4;
-constexpr float kNear = 8e-7f, kNearRel = 0x1p-22f;
+constexpr float kNear = 1e-6f, kNearRel = 0x1p-22f;
 
 struct Candidate {
     float key, l, b;
@@ -530,8 +530,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int64_t T,
 // then adds its parts, each CTA an eighth of the experts.
 //
 // A warp's rows come through a ring in shared memory, of which a lane copies and
-// reads its own words: with a warp's loads and its arithmetic in turn, 32,768
-// rows of 256 took 31 us for 14, 8,192 of 896 23 us for 17.
+// reads its own words: with a warp's loads and its arithmetic in turn, the loss
+// of 16,384 rows of 896 in bf16 took 34 us for 21.
 constexpr int kBalCtas = 8;
 __host__ __device__ constexpr int bal_warps(int n) { return n <= 8 ? 24 : n <= 16 ? 16 : 12; }       // of n values a lane: what the registers hold
 __host__ __device__ constexpr int bal_depth(int n) { return n <= 8 ? 4 : n <= 16 ? 3 : 2; }
