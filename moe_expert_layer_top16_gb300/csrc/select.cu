@@ -533,10 +533,77 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int64_t T,
 // reads its own words: with a warp's loads and its arithmetic in turn, the loss
 // of 16,384 rows of 896 in bf16 took 34 us for 21.
 constexpr int kBalCtas = 8;
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __host__ __device__ constexpr int bal_warps(int n) { return n <= 8 ? 24 : n <= 16 ? 16 : 12; }       // of n values a lane: what the registers hold
 __host__ __device__ constexpr int bal_depth(int n) { return n <= 8 ? 4 : n <= 16 ? 3 : 2; }
 template <int DT, int V, int NI>
 __host__ __device__ constexpr int bal_slot() { return V == 8 ? 512 * NI * (DT == ELEM_F32 ? 2 : 1) : 0; }
+
+// A warp's rows t0, t0 + step, ... before `end`: their shares to acc, their slots to hist; the rows that have one.
+template <bool SIG, int DT, int V, int NI>
+__device__ __forceinline__ int balance_rows(const BalanceArgs& a, int64_t t0, int64_t end, int step, int lane, int32_t* hist,
+                                            const uint8_t* rings, float (&acc)[NI * V]) {
+    constexpr int N = NI * V, D = bal_depth(NI * V), kSlot = bal_slot<DT, V, NI>();
+    const uint32_t ring = smem_u32(rings);
+    const int E = a.E, k = a.k;
+#pragma unroll
+    for (int c = 0; c < N; ++c) acc[c] = 0.0f;
+    int used = 0, slot = 0;
+    auto fetch = [&](int64_t t, int to) {
+        if constexpr (V == 8) {
+            if (t < end) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int e0 = (32 * i + lane) * V;
+                    if (e0 >= E) continue;
+                    const uint8_t* src = static_cast<const uint8_t*>(a.logits) + (t * a.ld + e0) * (DT == ELEM_F32 ? 4 : 2);
+                    const uint32_t dst = ring + static_cast<uint32_t>(to * kSlot + i * (kSlot / NI) + lane * 16);
+                    cp_async16(dst, src);
+                    if (DT == ELEM_F32) cp_async16(dst + 512, src + 16);
+                }
+            }
+            cp_async_commit();
+        }
+    };
+    int e_next = t0 < end && lane < k ? a.idx[t0 * k + lane] : -1;
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) fetch(t0 + d * step, d);
+#pragma unroll 1
+    for (int64_t t = t0; t < end; t += step) {
+        const int e = e_next;
+        if (t + step < end && lane < k) e_next = a.idx[(t + step) * k + lane];
+        fetch(t + (D - 1) * step, slot == 0 ? D - 1 : slot - 1);
+        if constexpr (V == 8) cp_async_wait(D - 1);      // (of rows without a slot too: their words of the ring are copied to again)
+        const int from = slot;
+        slot = slot + 1 == D ? 0 : slot + 1;
+        const bool kept = e >= 0 && e < E;
+        if (!__any_sync(kAll, kept)) continue;
+        if (kept) atomicAdd(&hist[e], 1);
+        ++used;
+        float v[N];
+        if constexpr (V == 8) {
+            RawVec<V> raw[NI];
+            const uint8_t* p = rings + from * kSlot + lane * 16;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                raw[i].a = ld16(p + i * (kSlot / NI));
+                if (DT == ELEM_F32) raw[i].b = ld16(p + i * (kSlot / NI) + 512);
+            }
+            open_row<true, V, NI>(raw, E, DT, lane, v);
+        } else {
+            load_row<DT, true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
+        }
+        const float sum = scores<SIG>(v);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] = fmaf(v[c], inv, acc[c]);
+    }
+    return used;
+}
 
 template <bool SIG, int DT, int V, int NI>
 __global__ void __launch_bounds__(bal_warps(NI * V) * 32, 1) balance_parts_kernel(const BalanceArgs a) {
@@ -546,10 +613,9 @@ __global__ void __launch_bounds__(bal_warps(NI * V) * 32, 1) balance_parts_kerne
     constexpr int N = NI * V;
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int E = a.E, k = a.k, P = a.pitch;
+    const int E = a.E, P = a.pitch;
     int32_t* hist = reinterpret_cast<int32_t*>(s_sum + kBalWarps * P);
     const uint8_t* rings = reinterpret_cast<const uint8_t*>(hist + P) + warp * (D * kSlot);
-    const uint32_t ring = smem_u32(rings);
     const int64_t t0 = blockIdx.x * a.per, t1 = min(t0 + a.per, a.T);
     // the first sequence that ends behind t0 (every warp finds the same)
     int s = 0;
@@ -573,58 +639,7 @@ __global__ void __launch_bounds__(bal_warps(NI * V) * 32, 1) balance_parts_kerne
         if (threadIdx.x == 0) s_tokens = 0;
         __syncthreads();
         float acc[N];
-#pragma unroll
-        for (int c = 0; c < N; ++c) acc[c] = 0.0f;
-        int used = 0, slot = 0;
-        auto fetch = [&](int64_t t, int to) {
-            if constexpr (V == 8) {
-                if (t < l) {
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        const int e0 = (32 * i + lane) * V;
-                        if (e0 >= E) continue;
-                        const uint8_t* src = static_cast<const uint8_t*>(a.logits) + (t * a.ld + e0) * (DT == ELEM_F32 ? 4 : 2);
-                        const uint32_t dst = ring + static_cast<uint32_t>(to * kSlot + i * (kSlot / NI) + lane * 16);
-                        cp_async16(dst, src);
-                        if (DT == ELEM_F32) cp_async16(dst + 512, src + 16);
-                    }
-                }
-                cp_async_commit();
-            }
-        };
-        int e_next = f + warp < l && lane < k ? a.idx[(f + warp) * k + lane] : -1;
-#pragma unroll
-        for (int d = 0; d < D - 1; ++d) fetch(f + warp + d * kBalWarps, d);
-#pragma unroll 1
-        for (int64_t t = f + warp; t < l; t += kBalWarps) {
-            const int e = e_next;
-            if (t + kBalWarps < l && lane < k) e_next = a.idx[(t + kBalWarps) * k + lane];
-            fetch(t + (D - 1) * kBalWarps, slot == 0 ? D - 1 : slot - 1);
-            const int from = slot;
-            slot = slot + 1 == D ? 0 : slot + 1;
-            const bool kept = e >= 0 && e < E;
-            if (!__any_sync(kAll, kept)) continue;
-            if (kept) atomicAdd(&hist[e], 1);
-            ++used;
-            float v[N];
-            if constexpr (V == 8) {
-                cp_async_wait(D - 1);
-                RawVec<V> raw[NI];
-                const uint8_t* p = rings + from * kSlot + lane * 16;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    raw[i].a = ld16(p + i * (kSlot / NI));
-                    if (DT == ELEM_F32) raw[i].b = ld16(p + i * (kSlot / NI) + 512);
-                }
-                open_row<true, V, NI>(raw, E, DT, lane, v);
-            } else {
-                load_row<DT, true, V, NI>(a.logits, t * a.ld, E, a.dt, lane, v);
-            }
-            const float sum = scores<SIG>(v);
-            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-            for (int c = 0; c < N; ++c) acc[c] = fmaf(v[c], inv, acc[c]);
-        }
+        const int used = balance_rows<SIG, DT, V, NI>(a, f + warp, l, kBalWarps, lane, hist, rings, acc);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int e0 = (32 * i + lane) * V;
@@ -644,6 +659,81 @@ __global__ void __launch_bounds__(bal_warps(NI * V) * 32, 1) balance_parts_kerne
         }
         if (threadIdx.x == 0) reinterpret_cast<int32_t*>(part)[2 * P] = s_tokens;
         __syncthreads();
+    }
+}
+
+// Few rows in one launch: a cluster for each sequence, whose CTAs take every eighth row and exchange their sums
+// through each other's shared memory.  (A second launch costs a small call's host more than the rows cost the device:
+// loss and gradient of 64 rows of 32 experts 35 us a call among others with two launches for the loss, 31 with one; 1,001
+// rows of 131 in 13 sequences 7.8 us on the device with two, 4.9 with one.)
+constexpr int kSmallRounds = 6;          // rows of a warp at most
+constexpr int kSmallSequences = 38;      // two waves of clusters
+template <bool SIG, int DT, int V, int NI>
+__global__ void __launch_bounds__(bal_warps(NI * V) * 32, 1) balance_small_kernel(const BalanceArgs a) {
+    constexpr int kBalWarps = bal_warps(NI * V), D = bal_depth(NI * V), kSlot = bal_slot<DT, V, NI>();
+    extern __shared__ __align__(16) float s_sum[];       // as in balance_parts_kernel
+    __shared__ int s_tokens;
+    __shared__ float s_part[kBalWarps], s_loss[kBalCtas];
+    constexpr int N = NI * V;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = a.E, P = a.pitch;
+    const int rank = blockIdx.x % kBalCtas, s = blockIdx.x / kBalCtas;
+    int32_t* hist = reinterpret_cast<int32_t*>(s_sum + kBalWarps * P);
+    const uint8_t* rings = reinterpret_cast<const uint8_t*>(hist + P) + warp * (D * kSlot);
+    const int64_t first = border(a.seq, s, a.S, a.T), last = border(a.seq, s + 1, a.S, a.T);
+    for (int e = threadIdx.x; e < P; e += blockDim.x) hist[e] = 0;
+    if (threadIdx.x == 0) s_tokens = 0;
+    __syncthreads();
+    float acc[N];
+    const int used = balance_rows<SIG, DT, V, NI>(a, first + rank + kBalCtas * warp, last, kBalCtas * kBalWarps, lane, hist, rings, acc);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e0 = (32 * i + lane) * V;
+        if (e0 < E)
+#pragma unroll
+            for (int j = 0; j < V; ++j) s_sum[warp * P + e0 + j] = acc[i * V + j];
+    }
+    if (lane == 0) atomicAdd(&s_tokens, used);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kBalWarps; ++w) sum += s_sum[w * P + e];
+        s_sum[e] = sum;
+    }
+    cluster_sync_all();
+    const int per = (E + kBalCtas - 1) / kBalCtas, end = min((rank + 1) * per, E);
+    float mine = 0.0f;
+    for (int e = rank * per + threadIdx.x; e < end; e += blockDim.x) {
+        float x = 0.0f;
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < kBalCtas; ++r) {
+            x += __uint_as_float(ld_cluster(mapa_shared(smem_u32(&s_sum[e]), r)));
+            n += static_cast<int>(ld_cluster(mapa_shared(smem_u32(&hist[e]), r)));
+        }
+        a.counts[static_cast<int64_t>(s) * E + e] = n;
+        mine = fmaf(static_cast<float>(n), x, mine);
+    }
+    mine = warp_sum(mine);
+    if (lane == 0) s_part[warp] = mine;
+    __syncthreads();
+    int n = 0;
+    if (threadIdx.x == 0) {
+        float x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kBalWarps; ++w) x += s_part[w];
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&s_loss[rank]), 0)), "f"(x) : "memory");
+        if (rank == 0)
+            for (int r = 0; r < kBalCtas; ++r) n += static_cast<int>(ld_cluster(mapa_shared(smem_u32(&s_tokens), r)));
+    }
+    cluster_sync_all();
+    if (rank == 0 && threadIdx.x == 0) {
+        float x = 0.0f;
+        for (int r = 0; r < kBalCtas; ++r) x += s_loss[r];
+        const float m = static_cast<float>(max(n, 1));
+        a.loss[s] = (static_cast<float>(E) / static_cast<float>(a.k)) * (x / m) / m;
+        a.tokens[s] = n;
     }
 }
 
@@ -962,6 +1052,15 @@ cudaError_t balance_as(const BalanceArgs& a, cudaStream_t s) {
         const unsigned blocks = static_cast<unsigned>((a.T + a.per - 1) / a.per);
         constexpr int kBalWarps = bal_warps(NI * V), kRings = kBalWarps * bal_depth(NI * V) * bal_slot<DT, V, NI>();
         const size_t smem = sizeof(float) * static_cast<size_t>(kBalWarps + 1) * a.pitch + kRings;
+        if (a.T <= kSmallRounds * kBalCtas * kBalWarps && a.S <= kSmallSequences) {
+            if (smem > 48 * 1024 - 256) {
+                const cudaError_t err = cudaFuncSetAttribute(balance_small_kernel<SIG, DT, V, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                             static_cast<int>(sizeof(float) * (kBalWarps + 1) * 32 * V * NI) + kRings);
+                if (err != cudaSuccess) return err;
+            }
+            return launch_ex_cluster(balance_small_kernel<SIG, DT, V, NI>, dim3(static_cast<unsigned>(a.S) * kBalCtas), dim3(kBalWarps * 32), smem, s,
+                                     false, kBalCtas, a);
+        }
         if (smem > 48 * 1024 - 256) {
             const cudaError_t err = cudaFuncSetAttribute(balance_parts_kernel<SIG, DT, V, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                          static_cast<int>(sizeof(float) * (kBalWarps + 1) * 32 * V * NI) + kRings);

@@ -292,3 +292,17 @@ def test_losses_in_one_workspace():
         kept.append([t.clone() for t in out])
     for i, got in zip(idx, kept):
         assert all(torch.equal(p, q) for p, q in zip(got, moe.balance_loss(s["logits"], i, sequences=s["sequences"])))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E,S", [(500, 896, 3), (20_000, 896, 40), (20_000, 256, 5), (9000, 512, 1), (1000, 32, 12)])
+def test_losses_of_rows_mostly_without_slots(T, E, S, dtype):
+    """Runs of rows whose tokens are routed nowhere, which a warp passes in no time while their copies are on the way."""
+    s = batch(T, E, 8, 4, S, T + E, dtype)
+    s["logits"] = s["logits"] + torch.arange(T, device=DEV).to(dtype)[:, None] % 7         # rows of different size
+    idx, _ = moe.select_experts(s["logits"], 4)
+    routed = torch.rand(T, generator=ops.gen(T), device=DEV) < 0.03
+    idx = torch.where(routed[:, None], idx, -1).contiguous()
+    for _ in range(3):
+        for score in ("sigmoid", "softmax"):
+            ops.check_loss(s["logits"], idx, score, s["sequences"])
