@@ -28,6 +28,14 @@
 //   An fp32 value is three such parts, 12 bits apart, in three vectors.
 // - Products and their sums over 32 (MMA) and over all groups are fp32.
 //
+// Measured, K = 7,168: MXFP4 and one bf16 vector, 8,192 rows 13.9 us (31 MB: 2.2 TB/s),
+// 65,536 rows 60 us (4.2 TB/s).  A block's start takes some 6 us of that (first
+// instructions, x from memory to its fp16 form), a unit of 16 x 256 weights 350
+// instructions, at which 16 warps an SM keep up with two thirds of HBM.  Integers in
+// groups of 128 and eight fp16 vectors, 65,536 rows 86 us: 576 instructions a unit,
+// which the schedulers issue in 65% of the cycles (the tensor pipe is at 12%, shared
+// memory at a fifth).
+//
 // A team of warps takes 16 rows of the matrix, its warps take the units of K (what
 // the MMAs of one load cover) in turn and add their sums in shared memory in a fixed
 // order.

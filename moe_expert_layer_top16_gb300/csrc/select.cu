@@ -11,7 +11,15 @@
 //              both in one pass over them
 //
 // A token's logits are one warp's: a lane holds them in registers, eight
-// neighbours at a time where rows allow it.  Every sum runs in a fixed order.
+// neighbours at a time where rows allow it (one at a time the loads are eight
+// times as many).  Every sum runs in a fixed order.
+//
+// Large batches should be bound by the logits' way from HBM, 4.4 us for 8,192 rows
+// of 896 in fp32; they take 22 us (selection), 21 (loss) and 24 (gradient): a row
+// is 650 (loss) to some 1,200 instructions of one warp, most of them in chains
+// (sorts and sums over the lanes, 25 to 35 cycles a step), which 17 to 28 warps
+// an SM hide in part.  Small calls are the host's: 11 to 15 us a call for 3 to 5 us
+// on the device.
 #include <algorithm>
 #include <cfloat>
 
