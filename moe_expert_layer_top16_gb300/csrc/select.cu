@@ -185,7 +185,10 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 // are what reaches the bound less twice that, and only where two neighbours in the
 // order are nearer than that and not equal in logit and bias are the candidates
 // ranked by keys of 64 bits: a row in some hundreds, at which a launch's last rows
-// wait longest.  8,192 rows of 896, k = 16: 22 us with a bias, 16 without.
+// wait longest.  The neighbours looked at are those up to the end of the run of
+// equals that holds the last slot: of two candidates in the wrong order, the better
+// one behind, those from the first to the last are all near, and the first two of
+// them that differ stand at the end of a run that begins before or at the last slot.  8,192 rows of 896, k = 16: 22 us with a bias, 16 without.
 constexpr int kCand = 64;
 constexpr int kSelectWarps = 4;
 constexpr float kNear = 1e-6f, kNearRel = 0x1p-22f;
@@ -392,8 +395,12 @@ __global__ void __launch_bounds__(kSelectWarps * 32, 7) select_kernel(const Sele
         if (a.bias) {
             bias = __shfl_sync(kAll, bias, at & 31);
             const float key2 = __shfl_down_sync(kAll, key, 1), l2 = __shfl_down_sync(kAll, l[0], 1), b2 = __shfl_down_sync(kAll, bias, 1);
-            const bool near = lane < k && lane + 1 < n && key - key2 <= kNear + kNearRel * fabsf(key) && !(l2 == l[0] && b2 == bias);
-            if (__any_sync(kAll, near)) {
+            const bool differ = lane + 1 >= n || l2 != l[0] || b2 != bias;
+            const uint32_t ends = __ballot_sync(kAll, differ);           // of runs of equals; lane 31 is always one
+            const uint32_t near = __ballot_sync(kAll, lane + 1 < n && differ && key - key2 <= kNear + kNearRel * fabsf(key));
+            // as far as the run that has the last slot: what is behind its end may be better than its equals
+            const int last = k - 1 + __ffs(ends >> (k - 1)) - 1;
+            if (near & (0xffffffffu >> (31 - last))) {
                 const double exact = lane < n ? key64(l[0], bias) : -INFINITY;
                 int rank = 0;
                 for (int p = 0; p < n; ++p) {
