@@ -648,7 +648,8 @@ MOE_API moe_status moe_balance_loss(const moe_balance_loss_args *args, void *str
  *   gates   normalize != 0   w_j r_j (g_j - sum_i g_i w_i)   w: gates / scale
  *           normalize == 0   g_j s_j r_j; softmax p_e (g_e - sum_i g_i p_i)
  *   losses  p_e r_e (a_e - sum_i p_i a_i)   a_e = d_loss E counts[e] / (k n^2)
- * The selection itself has no gradient, nor has the bias.  d_logits [T][E] of
+ * The selection itself has no gradient, nor has the bias.  What stands in d_gates
+ * at dropped slots and at slots of closed experts is not used.  d_logits [T][E] of
  * the logits' type, all of it written (0 for tokens that nothing counts); it
  * may be logits itself (same address and stride).  An expert that two slots of
  * a token name gets both. */

@@ -968,7 +968,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, 5) router_backward_kernel(con
             float q[1];
             raw_to_f32(load_raw<1>(a.logits, t * a.ld + e, a.dt), a.dt, q);
             l = open_logit(q[0]);
-            g = a.scale * a.d_gates[t * k + lane];
+            if (l > -INFINITY) g = a.scale * a.d_gates[t * k + lane];     // (0 times what stands there could be NaN)
         }
         float val;
         if (a.normalize) {

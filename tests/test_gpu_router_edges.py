@@ -74,3 +74,27 @@ def test_logits_in_steps(E, k, steps):
         bias = torch.randint(-2, 3, (E,), generator=g, device=DEV) * 2.0 ** -20
     for dtype in (BF16, F16):
         ops.check_selection((x * 4).round().div(4).to(dtype), k, bias=bias)
+
+
+# ------------------------------------------------------------------ gradients that nothing may be made of
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("E", [61, 64, 896])
+@pytest.mark.parametrize("score,normalize", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+def test_gate_gradients_of_closed_experts_are_not_read(score, normalize, E, dtype):
+    """A slot that is dropped, or whose expert the logits close, has no gradient whatever stands in d_gates: a value there
+    that is no number changes nothing, in its token's other slots neither."""
+    T, k = 40, 6
+    x = ops.data(T, E, dtype, 31)
+    idx, _ = moe.select_experts(x, k, score=score)
+    rows = torch.arange(T, device=DEV)
+    for j, closed in ((1, -INF), (4, NAN)):
+        x[rows[::2], idx[::2, j].long()] = closed            # behind the selection: its slot stays
+    idx[::3, 0], idx[1::3, 2] = -1, E + 1
+    l = ops.opened(x).gather(1, idx.long().clamp(0, E - 1))
+    off = (idx < 0) | (idx >= E) | (l == -INF)
+    dg = torch.randn(T, k, generator=ops.gen(32), device=DEV)
+    want = moe.router_backward(x, idx, d_gates=torch.where(off, 0.0, dg), score=score, normalize=normalize, scale=2.5)
+    assert want.isfinite().all() and off.any(1).sum() > T / 2
+    for junk in (NAN, INF, -INF):
+        got = moe.router_backward(x, idx, d_gates=torch.where(off, junk, dg), score=score, normalize=normalize, scale=2.5)
+        assert torch.equal(got, want)
