@@ -175,7 +175,7 @@ def _slots(slot_pos, dev, what):
 def _weights_of(weights, slot_pos, what):
     if weights is None:
         return None
-    if weights.dtype != torch.float32 or weights.shape != slot_pos.shape or weights.get_device() != slot_pos.get_device():
+    if not isinstance(weights, torch.Tensor) or weights.dtype != torch.float32 or weights.shape != slot_pos.shape or weights.get_device() != slot_pos.get_device():
         _bad(what + ": weights are float32 [T][k] on the same device")
     return weights.contiguous()
 
@@ -627,7 +627,7 @@ def w4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, up=
         lead = tuple(x.shape[:-1])
         T = lead[0] if lead else 1
     else:
-        if idx.dtype != torch.int32 or idx.dim() != 2 or idx.get_device() != dev:
+        if not isinstance(idx, torch.Tensor) or idx.dtype != torch.int32 or idx.dim() != 2 or idx.get_device() != dev:
             _bad(what + ": idx is int32 [T][k] on the same device")
         G, (T, k) = codes.shape[0], idx.shape
         _int32(idx.numel(), what)
@@ -641,10 +641,12 @@ def w4_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, up=
             _bad(what + ": up and weights do not go together")
     xr, ld = _rows(x, what)
     _int32(max(T, K, G * M), what)
+    if out is not None and not isinstance(out, torch.Tensor):
+        _bad(what + ": out is a tensor")
     dtype = out_dtype or (x.dtype if out is None else out.dtype)
-    if dtype not in DTYPES:
+    if not isinstance(dtype, torch.dtype) or dtype not in DTYPES:
         _bad(what + ": output type")
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev):
+    if status is not None and (not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev):
         _bad(what + ": status is int32 on x's device")
     shape = lead + (M,)
     n = T if len(lead) < 2 else T * k

@@ -52,7 +52,7 @@ def declare(L):
 
 
 def _score(score, what):
-    if score not in SCORES:
+    if not isinstance(score, str) or score not in SCORES:
         _bad(what + ": score is 'sigmoid' or 'softmax'")
     return SCORES[score]
 
@@ -117,7 +117,7 @@ def select_experts(logits: torch.Tensor, k: int, *, bias: Optional[torch.Tensor]
             _bad(what + ": a bias goes with sigmoid scores")
         bias = _floats(bias, (E,), dev, "bias is float32 [E] on the same device", what)
     if mask is not None:
-        if mask.dtype != torch.bool or tuple(mask.shape) != (T,) or mask.get_device() != dev:
+        if not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool or tuple(mask.shape) != (T,) or mask.get_device() != dev:
             _bad(what + ": mask is bool [T] on the same device")
         mask = mask.contiguous()
     idx = _empty((T, k), dtype=torch.int32, device=logits.device)
