@@ -549,7 +549,12 @@ MOE_API moe_status moe_mx4_gemm(const uint8_t *a_codes, const uint8_t *a_scales,
  *
  * The values of x are split into 32s along K and held to 2^-39 of the largest in
  * their 32 (fp32: 2^-63), so that bf16 and fp16 values are exact down to 2^-28 of
- * it; products and sums are fp32.  x's rows go by 16 bytes where address and
+ * it; products and sums are fp32.  A weight of a slot multiplies x's part before the
+ * sum: with x, scales and weights below 2^63 in magnitude nothing on the way
+ * overflows that the sum itself does not, and with weights and the largest x of a 32
+ * at 2^-40 or above (or 0) nothing is lost below; beyond that, and with infinite
+ * weights or scales, a product on the way may be infinite, 0 or NaN where the sum is
+ * not.  Rows and weights of dropped slots are not read.  x's rows go by 16 bytes where address and
  * stride are multiples of 16 bytes, else element by element.  T >= 0, T k <
  * 2^31, 1 <= k <= 32, M >= 1, G M <= 2^31 - 256, K a multiple of the group up
  * to 2^24.  dev_status receives a non-zero code if a bounded wait inside the
@@ -586,6 +591,12 @@ MOE_API moe_status moe_w4_matvec(const moe_w4_matvec_args *args, void *stream);
  * 1 <= k <= 32, k <= E <= 1024, T >= 0.  score_fn is a moe_score_fn.  A logit
  * of minus infinity or NaN closes the expert for the token (no score, no
  * gradient); plus infinity counts as the largest finite number.
+ *
+ * Scores, sums and gradients are fp32, with the hardware's approximations of
+ * exponentials and reciprocals (2^-22) where a whole row is gone through.  In units
+ * of 2^-24, gates are off by 24 of their value at most (64 if not normalised) and one
+ * of `scale`, losses by 160 of their value and one more for each 1,824 rows, gradients
+ * before their rounding by 160 of the magnitudes that their sums add.
  *
  * Selection: the k experts with the largest keys in descending order, equal
  * keys by the lower expert.  The key is the logit; with a bias (sigmoid only)

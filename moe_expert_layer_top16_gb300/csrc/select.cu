@@ -15,7 +15,7 @@
 // times as many).  Every sum runs in a fixed order.
 //
 // Large batches should be bound by the logits' way from HBM, 4.4 us for 8,192 rows
-// of 896 in fp32; they take 22 us (selection), 21 (loss) and 24 (gradient): a row
+// of 896 in fp32, k = 16; they take 22 us (selection), 21 (loss) and 24 (gradient): a row
 // is 650 (loss) to some 1,200 instructions of one warp, most of them in chains
 // (sorts and sums over the lanes, 25 to 35 cycles a step), which 17 to 28 warps
 // an SM hide in part.  Small calls are the host's: 11 to 15 us a call for 3 to 5 us
@@ -170,11 +170,22 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 }
 
 // ------------------------------------------------------------------ select
-// The k-th largest of the lanes' largest keys is at most the k-th largest key:
-// what reaches it, some 1.4 k of the keys, are the candidates, whose numbers go
-// to shared memory.  Up to 32 of them are sorted over the lanes, up to kCand
-// ranked by counting the better ones; rows with more (many equal keys) take k
-// rounds of a maximum over the row.
+// The k-th largest of the lanes' largest keys (for k > 16: of the lanes' halves')
+// is at most the k-th largest key: what reaches it are the candidates, whose
+// numbers go to shared memory.  Up to 32 of them are sorted over the lanes, up to
+// kCand ranked by counting the better ones; rows with more take k rounds of a
+// maximum over the row.
+//
+// How many there are depends on how many of those sets hold an expert: 1.1 to 1.4 k
+// where all do and k is at most half of them (896 or 256 experts, k = 16: 21; element
+// by element from 61 up).  Rows that go by eight values fill E / 8 lanes, and with
+// fewer sets than k every expert is a candidate; for k > 16 element by element one
+// half of each lane is empty up to E = 512 (and for E <= 256 up to 128).  Ordinary
+// rows then take the slow ways too.  8,192 rows in fp32, with a bias and without:
+//   k = 16   256 experts 15, 12 us   128: 149, 46   96: 775, 191   64: 50, 26
+//   k = 32   896: 664, 141   512: 45, 26   256: 42, 24   128: 1,954, 431   384, not
+//            aligned: 5,643, 971
+//   k = 8    64 to 256: 12 to 21, 10 to 15
 //
 // Keys with a bias are defined in 64 bits, whose exponentials would take some
 // ten times as long as the logits' way from memory.  They are estimated in 32:
@@ -542,7 +553,9 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq, int S, int64_t T,
 // warps' sums are added in shared memory, and the block's part of the sequence
 // goes to row b + s of the workspace: both numbers only grow along the tokens,
 // so that no two parts share a row.  A cluster of eight CTAs for each sequence
-// then adds its parts, each CTA an eighth of the experts.
+// then adds its parts, each CTA an eighth of the experts, however short the sequence
+// is: 16,384 rows of 896 in bf16 take 19 us in one sequence, 21 in 9, 40 in 64, 279 in
+// 1,000.
 //
 // A warp's rows come through a ring in shared memory, of which a lane copies and
 // reads its own words: with a warp's loads and its arithmetic in turn, the loss
@@ -843,6 +856,8 @@ __global__ void __launch_bounds__(32 * kSumRows) balance_sum_kernel(const Balanc
 // A lane holds slot j = lane; the slots' values meet their experts' lanes in a row
 // of shared memory.  One exponential a logit: with u = e^-|l|, sigmoid(l) is {1, u} /
 // (1 + u) and sigmoid(l) (1 - sigmoid(l)) = u / (1 + u)^2, which is kept for the second pass.
+// (Rows of more than 512 experts by eight values: 96 registers, of which a thread stores 56 to
+// 124 bytes to local memory.)
 constexpr int kBackWarps = 4;
 
 // Eight (or one) counts as floats.

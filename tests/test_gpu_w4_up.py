@@ -44,7 +44,7 @@ def test_one_matrix_and_up(N, M, K, form):
 @pytest.mark.parametrize("form", ["mxfp4", (32, F32), (64, BF16), (128, F16)], ids=str)
 @pytest.mark.parametrize("N", [1, 3, 4, 5, 8, 9])
 def test_the_hidden_width(N, form):
-    """K = 7,168: x of five rows, or of three in fp32, goes to shared memory in parts, for each tile of rows anew; more
+    """K = 7,168: x of five rows, or of two in fp32, goes to shared memory in parts, for each round of tiles anew; more
     tiles than blocks take at once."""
     for dtype in (F32, BF16):
         x = mv.rows(N, 7168, dtype, N)
