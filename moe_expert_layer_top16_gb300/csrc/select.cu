@@ -183,9 +183,11 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 // half of each lane is empty up to E = 512 (and for E <= 256 up to 128).  Ordinary
 // rows then take the slow ways too.  8,192 rows in fp32, with a bias and without:
 //   k = 16   256 experts 15, 12 us   128: 149, 46   96: 775, 191   64: 50, 26
-//   k = 32   896: 664, 141   512: 45, 26   256: 42, 24   128: 1,954, 431   384, not
-//            aligned: 5,643, 971
+//   k = 32   896: 55, 30   512: 47, 27   256: 42, 24   384: 455, 134   128: 1,954, 431
+//            384, not aligned: 5,643, 971
 //   k = 8    64 to 256: 12 to 21, 10 to 15
+// One row that takes rounds is enough for most of it: 501 experts and k = 32, 560 and 150
+// us for a single token, and up to 1,115 and 283 us where a few rows of 896 or 1,024 do.
 //
 // Keys with a bias are defined in 64 bits, whose exponentials would take some
 // ten times as long as the logits' way from memory.  They are estimated in 32:
@@ -199,7 +201,8 @@ __device__ __forceinline__ float sigmoid_rest(float v) {
 // wait longest.  The neighbours looked at are those up to the end of the run of
 // equals that holds the last slot: of two candidates in the wrong order, the better
 // one behind, those from the first to the last are all near, and the first two of
-// them that differ stand at the end of a run that begins before or at the last slot.  8,192 rows of 896, k = 16: 22 us with a bias, 16 without.
+// them that differ stand at the end of a run that begins before or at the last slot.
+// 8,192 rows of 896, k = 16: 22 us with a bias, 16 without.
 constexpr int kCand = 64;
 constexpr int kSelectWarps = 4;
 constexpr float kNear = 1e-6f, kNearRel = 0x1p-22f;
